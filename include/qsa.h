@@ -329,6 +329,137 @@ qsa_status qsa_get_device_error(uint32_t *code, cudaStream_t stream);
  */
 qsa_status qsa_debug_inject(uint32_t faults, uint64_t wait_limit_ns);
 
+/* ---- A cache kept within a budget: prompt attention, paged decode attention, eviction ---- */
+
+/* Element types of the calls below. */
+typedef enum {
+    QSA_F32 = 0,
+    QSA_F16 = 1,
+    QSA_BF16 = 2,
+    QSA_I8 = 3
+} qsa_dtype;
+
+/*
+ * A pool of key and value pages. Cell `slot` of page `p` holds, for each of
+ * the nkv KV heads, 128 key and 128 value elements at
+ *   k[p * page_stride + slot * cell_stride + head * head_stride + d]
+ * (v likewise; the strides are in elements and shared by k and v, so cells
+ * outside heads, heads outside cells, and keys and values side by side in one
+ * allocation are all pools). dtype: QSA_BF16, QSA_F16, or QSA_I8 with one
+ * binary16 scale per cell and KV head (element = code * scale) at
+ *   k_scale_f16[p * scale_page_stride + slot * scale_cell_stride + head * scale_head_stride]
+ * (v_scale_f16 likewise; both NULL for the 16-bit types).
+ * k and v are 16-byte aligned and the strides are multiples of 16 bytes and
+ * not negative; scales are 2-byte aligned. npages >= 0, page_size >= 1 (any,
+ * not only powers of two), nkv >= 1.
+ */
+typedef struct {
+    void *k, *v;
+    uint16_t *k_scale_f16, *v_scale_f16;
+    int32_t dtype, npages, page_size, nkv;
+    int64_t page_stride, cell_stride, head_stride;
+    int64_t scale_page_stride, scale_cell_stride, scale_head_stride;
+} qsa_kv_pages;
+
+/*
+ * Attention of one new token per sequence over its paged cache.
+ * Sequence s has n = lens[s] cells (its newest cell, n - 1, is the query's
+ * own token); cell j is slot j % page_size of page page_table[s][j / page_size].
+ * Head h attends KV head h / (nheads / nkv). Visible cells: j < n and
+ * (window < 0 or j >= n - window or j < sinks).
+ *   logit[h][j] = scale * sum_d q[s][h][d] * key[j][d]
+ *   lse[s][h]   = log sum_j exp(logit[h][j])
+ *   out[s][h]   = sum_j exp(logit[h][j] - lse[s][h]) * value[j]
+ * With no visible cell out = 0 and lse = -infinity. Cells that are not
+ * visible are never used, whatever they hold. lens is clamped to
+ * [0, table_cols * page_size]; a visible cell whose page id is outside
+ * [0, npages) is skipped (as if it were not visible).
+ * mass, mass_out (both or neither NULL; may be equal):
+ *   mass_out[s][j] = mass[s][j] + sum over all heads of exp(logit[h][j] - lse[s][h])
+ * for j < n (the sum is 0 for cells that are not visible); columns >= n are
+ * not written. Each element is summed in a fixed order.
+ * q         [nseq][nheads][128] of q_dtype, element strides q_seq_stride and
+ *           q_head_stride (multiples of 16 bytes, not negative). q_dtype is the
+ *           pages' dtype for 16-bit pages; QSA_F32, QSA_F16 or QSA_BF16 for int8.
+ * page_table int32, row stride table_stride >= table_cols. lens int32 [nseq].
+ * out       [nseq][nheads][128] of q_dtype, contiguous. lse fp32
+ *           [nseq][nheads] or NULL. mass, mass_out fp32 with row stride
+ *           mass_stride >= table_cols * page_size.
+ * scale     positive and finite.
+ * scratch   at least qsa_paged_attn_scratch_bytes(...) bytes, 16-byte aligned
+ *           (may be NULL when that is 0); no contents need survive.
+ * Sums and softmax statistics are fp32. q, out and the page pool are 16-byte
+ * aligned, the others 4-byte.
+ * nseq, nheads or nkv out of range, nheads % nkv != 0, a bad type, scale,
+ * pointer or stride returns QSA_ERR_INVALID; nseq or nheads above 65,535,
+ * nseq * nheads or table_cols * page_size above 2^30 returns
+ * QSA_ERR_UNSUPPORTED.
+ */
+size_t qsa_paged_attn_scratch_bytes(int nseq, int nheads, int nkv, int table_cols, int page_size, int with_mass);
+qsa_status qsa_paged_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride, int64_t q_head_stride, int nseq,
+                          int nheads, const qsa_kv_pages *kv, const int32_t *page_table, int table_cols,
+                          int64_t table_stride, const int32_t *lens, int window, int sinks, float scale, void *out,
+                          float *lse, const float *mass, float *mass_out, int64_t mass_stride, void *scratch,
+                          size_t scratch_bytes, cudaStream_t stream);
+
+/*
+ * Attention of ragged sequences of new tokens over their keys: causal,
+ * within a sliding window, with the first `sinks` tokens always visible.
+ * Sequence s has queries cu_q[s] .. cu_q[s+1]-1 and keys cu_k[s] ..
+ * cu_k[s+1]-1; its nq queries are the last of its nk tokens: query i stands
+ * at pos = nk - nq + i. Visible keys: 0 <= j <= pos, j < nk and
+ * (window < 0 or j > pos - window or j < sinks). logit, lse and out as
+ * qsa_paged_attn; a query with no visible key (nq > nk, or window 0 without
+ * sinks) gets out = 0 and lse = -infinity.
+ * q         [total_q][nheads][128], k, v [total_k][nkv][128], all of dtype
+ *           (QSA_F16 or QSA_BF16), 16-byte aligned, element strides per token
+ *           and head (multiples of 16 bytes, not negative).
+ * cu_q, cu_k int32 [nseq + 1], ascending from 0 (device memory; values are
+ *           clamped to [0, total_q] and [0, total_k]).
+ * max_q     at least the longest sequence's query count (queries past it are
+ *           not computed).
+ * out       [total_q][nheads][128] of dtype, contiguous, 16-byte aligned; lse
+ *           fp32 [total_q][nheads] or NULL.
+ * scratch   at least qsa_window_attn_scratch_bytes(...) bytes, 16-byte aligned
+ *           (may be NULL when that is 0).
+ * Softmax statistics and sums are fp32; the weights are rounded once to dtype
+ * for the product with the values. The values of keys that are not visible
+ * never reach a result, whatever they hold.
+ * Errors as qsa_paged_attn; nheads / nkv above 128, nseq above 65,535 or
+ * total_q * nheads above 2^31 - 1 returns QSA_ERR_UNSUPPORTED.
+ */
+size_t qsa_window_attn_scratch_bytes(int nseq, int total_q, int max_q, int nheads, int nkv);
+qsa_status qsa_window_attn(const void *q, const void *k, const void *v, qsa_dtype dtype, const int64_t *strides,
+                           const int32_t *cu_q, const int32_t *cu_k, int nseq, int total_q, int total_k, int max_q,
+                           int nheads, int nkv, int window, int sinks, float scale, void *out, float *lse,
+                           void *scratch, size_t scratch_bytes, cudaStream_t stream);
+
+/*
+ * Eviction by accumulated attention weight: each sequence of n = lens[s]
+ * cells (clamped as in qsa_paged_attn) keeps min(n, budget) of them: all when
+ * n <= budget, else the first `sinks`, the last `recent`, and of the cells
+ * between them the budget - sinks - recent with the largest mass (equal
+ * masses: the lower cell first; NaN counts as -infinity, -0 as +0). The kept
+ * cells keep their order: cell i of the new cache is a copy of cell kept[s][i]
+ * (keys, values and int8 scales, bit for bit) in slot i % page_size of page
+ * new_table[s][i / page_size] of the same pool.
+ * kept      int32 [nseq][budget], written, ascending, -1 past the kept cells.
+ * new_lens  int32 [nseq], written: min(n, budget).
+ * new_mass  fp32, row stride new_mass_stride, new_mass_cols columns written:
+ *           the kept cells' masses, then zeros.
+ * Pages of new_table must not be pages that any row of page_table uses for a
+ * cell below its length, nor appear twice (else the copied cells are
+ * undefined). A page id outside [0, npages) on either side skips the copy of
+ * that cell. budget >= 1, sinks + recent <= budget <= new_cols * page_size,
+ * budget <= new_mass_cols; mass_stride >= table_cols * page_size. Size limits
+ * as qsa_paged_attn. Allocates nothing.
+ */
+qsa_status qsa_cache_evict(const qsa_kv_pages *kv, int nseq, const int32_t *page_table, int table_cols,
+                           int64_t table_stride, const int32_t *lens, const float *mass, int64_t mass_stride,
+                           const int32_t *new_table, int new_cols, int64_t new_table_stride, int budget, int sinks,
+                           int recent, int32_t *kept, int32_t *new_lens, float *new_mass, int64_t new_mass_stride,
+                           int new_mass_cols, cudaStream_t stream);
+
 /* Static description of a status code. */
 const char *qsa_status_string(qsa_status status);
 

@@ -1,5 +1,7 @@
 """Exact QSA block selection on GB300: block scoring, per-query top-k,
-attention over the selected blocks, and block summary keys on append.
+attention over the selected blocks, and block summary keys on append; and a
+cache kept within a budget: prompt attention with a sliding window and sinks,
+paged decode attention, and eviction by accumulated attention weight.
 
 The computation lives in ``libqsa.so`` (CUDA kernels for sm_103a behind the C
 ABI of ``include/qsa.h``); ``qsa`` is its Python binding and ``workloads``
@@ -21,10 +23,15 @@ from .qsa import (  # noqa: F401
     block_summary,
     block_topk,
     block_topk_gmax,
+    cache_evict,
     groups,
+    paged_attn,
+    paged_attn_scratch_bytes,
     select_scratch_bytes,
     debug_inject,
     default_scorer_kernel,
     device_error,
     sparse_attn,
+    window_attn,
+    window_attn_scratch_bytes,
 )

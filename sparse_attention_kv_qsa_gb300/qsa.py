@@ -21,13 +21,29 @@ GROUP_BLOCKS = 32   # blocks per group of the group-maximum side output
 TOPK_MAX_ACTIVE = 393216
 SELECT_STATIC_GROUPS_MAX = 262144   # scratch bound of qsa_block_select_static
 
+SOFTMAX_SCALE = D ** -0.5   # default temperature of the attention calls
+
 QSA_OK, QSA_ERR_INVALID, QSA_ERR_UNSUPPORTED, QSA_ERR_CUDA = 0, 1, 2, 3
 
 EXPORTED = ("qsa_block_scores", "qsa_block_scores_q8", "qsa_block_scores_ffma", "qsa_block_topk",
             "qsa_block_scores_gmax", "qsa_block_scores_q8_gmax", "qsa_block_group_max", "qsa_block_topk_gmax",
             "qsa_block_select_static", "qsa_block_select_small", "qsa_sparse_attn", "qsa_block_summary",
             "qsa_get_device_error", "qsa_debug_inject", "qsa_status_string", "qsa_block_select",
-            "qsa_block_select_scratch_bytes")
+            "qsa_block_select_scratch_bytes", "qsa_paged_attn", "qsa_paged_attn_scratch_bytes", "qsa_window_attn",
+            "qsa_window_attn_scratch_bytes", "qsa_cache_evict")
+
+
+F32, F16, BF16, I8 = 0, 1, 2, 3   # qsa_dtype
+
+
+class KVPages(ctypes.Structure):
+    """``qsa_kv_pages``: a pool of key and value pages (pointers and element strides)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale_f16", ctypes.c_void_p),
+                ("v_scale_f16", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("npages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("nkv", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("cell_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_cell_stride", ctypes.c_int64),
+                ("scale_head_stride", ctypes.c_int64)]
 
 
 class QSAError(RuntimeError):
@@ -70,6 +86,19 @@ def lib() -> ctypes.CDLL:
         L.qsa_block_select.restype = i
         L.qsa_block_select_scratch_bytes.argtypes = [i]
         L.qsa_block_select_scratch_bytes.restype = ctypes.c_size_t
+        ll, f, kv = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(KVPages)
+        L.qsa_paged_attn_scratch_bytes.argtypes = [i, i, i, i, i, i]
+        L.qsa_paged_attn_scratch_bytes.restype = ctypes.c_size_t
+        L.qsa_paged_attn.argtypes = [vp, i, ll, ll, i, i, kv, vp, i, ll, vp, i, i, f, vp, vp, vp, vp, ll, vp,
+                                     ctypes.c_size_t, vp]
+        L.qsa_paged_attn.restype = i
+        L.qsa_window_attn_scratch_bytes.argtypes = [i, i, i, i, i]
+        L.qsa_window_attn_scratch_bytes.restype = ctypes.c_size_t
+        L.qsa_window_attn.argtypes = [vp, vp, vp, i, ctypes.POINTER(ll), vp, vp, i, i, i, i, i, i, i, i, f, vp, vp, vp,
+                                      ctypes.c_size_t, vp]
+        L.qsa_window_attn.restype = i
+        L.qsa_cache_evict.argtypes = [kv, i, vp, i, ll, vp, vp, ll, vp, i, ll, i, i, i, vp, vp, vp, ll, i, vp]
+        L.qsa_cache_evict.restype = i
         L.qsa_debug_inject.argtypes = [ctypes.c_uint32, ctypes.c_uint64]
         L.qsa_debug_inject.restype = i
         L.qsa_status_string.argtypes = [i]
@@ -427,6 +456,225 @@ def block_summary(k_cells: torch.Tensor, k_scale_f16: torch.Tensor, block_begin:
             raise ValueError(f"kblk_scale_f16 must be a 1-d CUDA tensor of >= {block_end} binary16 values")
     _check(lib().qsa_block_summary(_ptr(k_cells), _ptr(k_scale_f16), ncells, block_begin, block_end, _ptr(kblk),
                                    _ptr(kblk_q8), _ptr(kblk_scale_f16), _stream(k_cells)), "qsa_block_summary")
+
+
+_DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.int8: I8}
+
+
+def _tensor(t: torch.Tensor, name: str, dtypes: tuple, ndim: int, device: torch.device) -> None:
+    """A CUDA tensor on `device` of one of `dtypes` and `ndim` dimensions, unit stride in the last."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a {ndim}-d tensor, contiguous in its last dimension")
+
+
+def _strides(t: torch.Tensor, n: int) -> tuple[int, ...]:
+    """The first n strides; 0 for a dimension of one element (torch leaves that one arbitrary)."""
+    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(n))
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16) -> KVPages:
+    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
+        raise ValueError("k_pages must be a CUDA tensor")
+    kinds = (torch.bfloat16, torch.float16, torch.int8)
+    _tensor(k_pages, "k_pages", kinds, 4, k_pages.device)
+    _tensor(v_pages, "v_pages", (k_pages.dtype,), 4, k_pages.device)
+    if k_pages.shape[3] != D or v_pages.shape != k_pages.shape or _strides(v_pages, 3) != _strides(k_pages, 3):
+        raise ValueError("k_pages and v_pages must both be [npages, page_size, nkv, 128], of the same strides")
+    st = _strides(k_pages, 3)
+    kv = KVPages(_ptr(k_pages), _ptr(v_pages), None, None, _DTYPE[k_pages.dtype], k_pages.shape[0], k_pages.shape[1],
+                 k_pages.shape[2], st[0], st[1], st[2], 0, 0, 0)
+    if k_pages.dtype == torch.int8:
+        for name, t in (("k_scale_f16", k_scale_f16), ("v_scale_f16", v_scale_f16)):
+            if (not isinstance(t, torch.Tensor) or t.device != k_pages.device or t.element_size() != 2
+                    or t.shape != k_pages.shape[:3]):
+                raise ValueError(f"{name} must be [npages, page_size, nkv] binary16 values beside int8 pages")
+        st = _strides(k_scale_f16, 3)
+        if _strides(v_scale_f16, 3) != st:
+            raise ValueError("k_scale_f16 and v_scale_f16 must have the same strides")
+        kv.k_scale_f16, kv.v_scale_f16 = _ptr(k_scale_f16), _ptr(v_scale_f16)
+        kv.scale_page_stride, kv.scale_cell_stride, kv.scale_head_stride = st
+    elif k_scale_f16 is not None or v_scale_f16 is not None:
+        raise ValueError("scales are for int8 pages only")
+    return kv
+
+
+def _table(table, lens, device) -> int:
+    _tensor(table, "page_table", (torch.int32,), 2, device)
+    _tensor(lens, "lens", (torch.int32,), 1, device)
+    if lens.shape[0] != table.shape[0]:
+        raise ValueError("page_table and lens must have one row per sequence")
+    return _row_stride(table)
+
+
+def _made(t, name, shape, dtype, device):
+    """`t` checked as a contiguous output of that shape and type, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _tensor(t, name, (dtype,), len(shape), device)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}")
+    return t
+
+
+def _scratch(t, need, device):
+    if t is None:
+        return torch.empty((need,), dtype=torch.uint8, device=device) if need else None
+    _tensor(t, "scratch", (torch.uint8,), 1, device)
+    if t.numel() < need:
+        raise ValueError(f"scratch must have at least {need} bytes")
+    return t
+
+
+def paged_attn_scratch_bytes(nseq: int, nheads: int, nkv: int, table_cols: int, page_size: int,
+                             with_mass: bool = False) -> int:
+    """``qsa_paged_attn_scratch_bytes``: scratch bytes paged_attn needs."""
+    return int(lib().qsa_paged_attn_scratch_bytes(nseq, nheads, nkv, table_cols, page_size, int(with_mass)))
+
+
+def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+               lens: torch.Tensor, *, k_scale_f16: torch.Tensor | None = None,
+               v_scale_f16: torch.Tensor | None = None, window: int = -1, sinks: int = 0,
+               scale: float | None = None, mass: torch.Tensor | None = None, mass_out: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               scratch: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """``qsa_paged_attn``: ``(out, lse)`` of one new token per sequence,
+    ``q [nseq, nheads, 128]``, over its paged cache: cell ``j`` of sequence
+    ``s`` is slot ``j % page_size`` of page ``page_table[s, j // page_size]``
+    of ``k_pages``/``v_pages [npages, page_size, nkv, 128]`` (bfloat16,
+    float16, or int8 with binary16 scales ``[npages, page_size, nkv]``; any
+    strides that are multiples of 16 bytes). Cells ``j < lens[s]`` within the
+    last ``window`` (all when negative) or among the first ``sinks`` are
+    visible. ``scale`` defaults to ``1/sqrt(128)``. With ``mass`` (fp32,
+    ``[nseq, >= page_table.shape[1] * page_size]``) the weight that each cell
+    received, summed over the heads, is added into ``mass_out`` (default:
+    ``mass`` itself). ``scratch``: a uint8 tensor of
+    ``paged_attn_scratch_bytes`` bytes, allocated when not given."""
+    kv = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16)
+    dev = k_pages.device
+    _tensor(q, "q", (torch.float32, torch.float16, torch.bfloat16) if kv.dtype == I8 else (k_pages.dtype,), 3, dev)
+    nseq, nheads = q.shape[:2]
+    if q.shape[2] != D or nheads < 1 or nheads % kv.nkv:
+        raise ValueError(f"q must be [nseq, a multiple of {kv.nkv}, {D}]")
+    tstride = _table(page_table, lens, dev)
+    if page_table.shape[0] != nseq:
+        raise ValueError("page_table must have one row per query")
+    cols = page_table.shape[1]
+    out = _made(out, "out", (nseq, nheads, D), q.dtype, dev)
+    lse = _made(lse, "lse", (nseq, nheads), torch.float32, dev)
+    mstride = 0
+    if mass is not None:
+        mass_out = mass if mass_out is None else mass_out
+        for name, t in (("mass", mass), ("mass_out", mass_out)):
+            _tensor(t, name, (torch.float32,), 2, dev)
+            if t.shape[0] != nseq or t.shape[1] < cols * kv.page_size:
+                raise ValueError(f"{name} must be [{nseq}, >= {cols * kv.page_size}]")
+        mstride = _row_stride(mass)
+        if _strides(mass_out, 1) != _strides(mass, 1):
+            raise ValueError("mass and mass_out must have the same strides")
+    elif mass_out is not None:
+        raise ValueError("mass_out needs mass")
+    scratch = _scratch(scratch, paged_attn_scratch_bytes(nseq, nheads, kv.nkv, cols, kv.page_size, mass is not None), dev)
+    _check(lib().qsa_paged_attn(_ptr(q), _DTYPE[q.dtype], *_strides(q, 2), nseq, nheads, ctypes.byref(kv),
+                                _ptr(page_table), cols, tstride, _ptr(lens), window, sinks,
+                                SOFTMAX_SCALE if scale is None else scale, _ptr(out), _ptr(lse), _ptr(mass),
+                                _ptr(mass_out), mstride, _ptr(scratch), 0 if scratch is None else scratch.numel(),
+                                _stream(q)), "qsa_paged_attn")
+    return out, lse
+
+
+def window_attn_scratch_bytes(nseq: int, total_q: int, max_q: int, nheads: int, nkv: int) -> int:
+    """``qsa_window_attn_scratch_bytes``: scratch bytes window_attn needs."""
+    return int(lib().qsa_window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv))
+
+
+def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor, max_q: int,
+                *, window: int = -1, sinks: int = 0, scale: float | None = None, out: torch.Tensor | None = None,
+                lse: torch.Tensor | None = None,
+                scratch: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """``qsa_window_attn``: ``(out, lse)`` of ragged sequences of new tokens,
+    ``q [total_q, nheads, 128]`` over ``k, v [total_k, nkv, 128]`` (bfloat16 or
+    float16; token and head strides of multiples of 16 bytes). Sequence ``s``
+    has queries ``cu_q[s] .. cu_q[s+1]-1``, the last of its keys ``cu_k[s] ..
+    cu_k[s+1]-1``; a query sees the keys up to its own place that lie within
+    the last ``window`` (all when negative) or among the first ``sinks``.
+    ``max_q`` is at least the longest sequence's query count."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dev = q.device
+    _tensor(q, "q", (torch.bfloat16, torch.float16), 3, dev)
+    _tensor(k, "k", (q.dtype,), 3, dev)
+    _tensor(v, "v", (q.dtype,), 3, dev)
+    total_q, nheads = q.shape[:2]
+    total_k, nkv = k.shape[:2]
+    if q.shape[2] != D or k.shape[2] != D or v.shape != k.shape or nkv < 1 or nheads < 1 or nheads % nkv:
+        raise ValueError("q must be [total_q, nheads, 128] and k, v [total_k, nkv, 128] with nheads a multiple of nkv")
+    _tensor(cu_q, "cu_q", (torch.int32,), 1, dev)
+    _tensor(cu_k, "cu_k", (torch.int32,), 1, dev)
+    if cu_q.shape != cu_k.shape or cu_q.shape[0] < 1:
+        raise ValueError("cu_q and cu_k must both have one more element than there are sequences")
+    nseq = cu_q.shape[0] - 1
+    if max_q < 0:
+        raise ValueError("max_q must not be negative")
+    max_q = min(max_q, total_q)
+    out = _made(out, "out", (total_q, nheads, D), q.dtype, dev)
+    lse = _made(lse, "lse", (total_q, nheads), torch.float32, dev)
+    scratch = _scratch(scratch, window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv), dev)
+    strides = (ctypes.c_int64 * 6)(*_strides(q, 2), *_strides(k, 2), *_strides(v, 2))
+    _check(lib().qsa_window_attn(_ptr(q), _ptr(k), _ptr(v), _DTYPE[q.dtype], strides, _ptr(cu_q), _ptr(cu_k), nseq,
+                                 total_q, total_k, max_q, nheads, nkv, window, sinks,
+                                 SOFTMAX_SCALE if scale is None else scale, _ptr(out), _ptr(lse), _ptr(scratch),
+                                 0 if scratch is None else scratch.numel(), _stream(q)), "qsa_window_attn")
+    return out, lse
+
+
+def cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                mass: torch.Tensor, new_table: torch.Tensor, budget: int, *, sinks: int = 0, recent: int = 0,
+                k_scale_f16: torch.Tensor | None = None, v_scale_f16: torch.Tensor | None = None,
+                kept: torch.Tensor | None = None, new_lens: torch.Tensor | None = None,
+                new_mass: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """``qsa_cache_evict``: ``(kept, new_lens, new_mass)``. Each sequence keeps
+    at most ``budget`` cells: the first ``sinks``, the last ``recent`` and the
+    cells of largest ``mass`` between (ties to the lower cell), in order; cell
+    ``i`` of the new cache (slot ``i % page_size`` of page ``new_table[s, i //
+    page_size]`` of the same pool) is a copy of cell ``kept[s, i]``. ``kept``
+    int32 ``[nseq, budget]`` (-1 past the kept cells), ``new_lens`` int32,
+    ``new_mass`` fp32 ``[nseq, >= budget]`` (default ``new_table.shape[1] *
+    page_size`` columns): the kept masses, then zeros. Pages of ``new_table``
+    must be none that ``page_table`` still uses."""
+    kv = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16)
+    dev = k_pages.device
+    tstride = _table(page_table, lens, dev)
+    nseq, cols = page_table.shape
+    _tensor(new_table, "new_table", (torch.int32,), 2, dev)
+    _tensor(mass, "mass", (torch.float32,), 2, dev)
+    if new_table.shape[0] != nseq:
+        raise ValueError("new_table must have one row per sequence")
+    if mass.shape[0] != nseq or mass.shape[1] < cols * kv.page_size:
+        raise ValueError(f"mass must be [{nseq}, >= {cols * kv.page_size}]")
+    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget or budget > new_table.shape[1] * kv.page_size:
+        raise ValueError("budget must be at least 1 and sinks + recent, and fit the new table's pages")
+    kept = _made(kept, "kept", (nseq, budget), torch.int32, dev)
+    new_lens = _made(new_lens, "new_lens", (nseq,), torch.int32, dev)
+    if new_mass is None:
+        new_mass = torch.empty((nseq, new_table.shape[1] * kv.page_size), dtype=torch.float32, device=dev)
+    _tensor(new_mass, "new_mass", (torch.float32,), 2, dev)
+    if new_mass.shape[0] != nseq or new_mass.shape[1] < budget:
+        raise ValueError(f"new_mass must be [{nseq}, >= {budget}]")
+    _check(lib().qsa_cache_evict(ctypes.byref(kv), nseq, _ptr(page_table), cols, tstride, _ptr(lens), _ptr(mass),
+                                 _row_stride(mass), _ptr(new_table), new_table.shape[1], _row_stride(new_table),
+                                 budget, sinks, recent, _ptr(kept), _ptr(new_lens), _ptr(new_mass),
+                                 _row_stride(new_mass), new_mass.shape[1], _stream(k_pages)), "qsa_cache_evict")
+    return kept, new_lens, new_mass
 
 
 def device_error(device: torch.device | None = None) -> int:
