@@ -2,108 +2,767 @@
 // sliding window, always-visible first cells, and the weight each cell
 // received added to a running mass.
 //
-//   s_hj = scale q_h . k_j;  lse_h = log sum_j exp(s_hj);  out_h = sum_j exp(s_hj - lse_h) v_j
-//   mass_out_j = mass_j + sum_h exp(s_hj - lse_h)
+//   x_hj = log2(e) scale q_h . k_j;  lse_h = ln 2 log2 sum_j 2^x_hj
+//   out_h = sum_j 2^(x_hj - log2 sum) v_j;  mass_out_j = mass_j + sum_h 2^(x_hj - log2 sum)
 //
-// One warp per sequence and head in fp32 on CUDA cores, one cell at a time.
+// What bounds it: every visible cell of every KV head is read once and used
+// by the few query heads that share it, so HBM.
+//
+// Work. The visible cells of a sequence, sinks first, are numbered without
+// gaps and cut into tiles of 64; (sequence, KV head, up to 16 query heads) is
+// a unit, and all tiles of all units in order are cut into one equal range
+// per CTA, two CTAs per SM. Lengths live on the device only: every CTA sums
+// the tile counts of all sequences itself, so ragged batches are balanced,
+// a captured graph follows the lengths, and a single long sequence fills the
+// GPU. A unit that falls into several ranges leaves partial results (outputs,
+// maximum, sum per head) in scratch, which join_kernel adds in range order;
+// the result does not depend on scheduling.
+//
+// A tile. Each of the 4 warps takes 16 of the 64 cells and runs alone: its
+// rows arrive in a ring of its own by 16-byte asynchronous copies (rows past
+// the end are filled with zeros), and the page numbers (and int8 scales) of a
+// step are fetched one step ahead of its copies. Both products run on
+// mma.sync m16n8k16 with the heads as rows: x = Q K^T with rows 0-7 the heads
+// and rows 8-15 the remainder of q where it has one, then P V with rows 0-7
+// the weights rounded to the operand type and rows 8-15 what that rounding
+// left, so the weights carry 17 (bfloat16) or 22 (binary16) bits. The
+// fragments of x are the fragments of P. tcgen05 would need 64 rows at least
+// for the 1 to 16 heads that share a cell; the arithmetic is far from the
+// bound as it is.
+//
+// int8 cells become binary16 exactly (a byte in the low bits of 1024 + u), q
+// is scaled by a power of two per head into binary16's range, and the key
+// scale multiplies x. The value scale vs_j joins the weight, and the running
+// reference M of the exponent follows x_j + log2 vs_j, so that p_j vs_j =
+// 2^(x_j - M) vs_j stays within binary16 whatever the scales' range.
+// M moves only when it would have to grow by more than 2^8: the sums are
+// scaled by whatever M they started from, and rescaling is rare.
+#include <algorithm>
+#include <cmath>
+
 #include "attn_row.cuh"
 #include "cache_internal.cuh"
+#include "qsa_internal.cuh"
 
 namespace qsa {
 namespace {
 
-struct Cell {
-    const void *k, *v;
-    float ks, vs;
-    bool ok;
+constexpr int WARPS = 4, THREADS = 32 * WARPS;
+constexpr int STEP = 16;               // cells of one warp's step
+constexpr int TILE = STEP * WARPS;
+constexpr int CTAS_PER_SM = 2;
+constexpr float LAZY = 8.0f;           // log2 of how far the sums may run above their reference
+constexpr int SLOT_ROW = 132;          // 128 outputs, maximum, sum, padding
+
+// floor(n / d) for 0 <= n < 2^31, by multiplication.
+struct Divider {
+    uint32_t d, mul, shift;
+};
+Divider make_divider(uint32_t d) {
+    if (d == 1) return {1, 0, 0};
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return {d, static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), l - 1};
+}
+__device__ __forceinline__ uint32_t divide(Divider v, uint32_t n) { return v.d == 1 ? n : __umulhi(n, v.mul) >> v.shift; }
+
+struct Params {
+    PagedAttnArgs a;
+    Divider page;
+    int group;        // query heads per KV head
+    int parts;        // units per KV head
+    int units;        // units per sequence
+    int capacity, stride;   // cells of a table row; columns of a row of kept logits
+    float *slots;     // [2 grid][heads of a unit][SLOT_ROW]
+    int4 *meta;       // [grid]: sequence, unit, first range, last range of the unit to join
+    float *lse2;      // [nseq][nheads], or null
+    float *logits;    // [nseq][nheads][stride], or null
 };
 
-template <typename KT>
-__device__ __forceinline__ Cell find_cell(const PagedAttnArgs &a, int s, int j, int head) {
-    const int page = __ldcg(a.table + s * a.table_stride + j / a.kv.page_size), slot = j % a.kv.page_size;
-    Cell c{nullptr, nullptr, 1.0f, 1.0f, page >= 0 && page < a.kv.npages};
-    if (!c.ok) return c;
-    const int64_t at = page * a.kv.page_stride + slot * a.kv.cell_stride + head * a.kv.head_stride;
-    c.k = static_cast<const KT *>(a.kv.k) + at;
-    c.v = static_cast<const KT *>(a.kv.v) + at;
-    if constexpr (sizeof(KT) == 1) {
-        const int64_t sc = page * a.kv.scale_page_stride + slot * a.kv.scale_cell_stride + head * a.kv.scale_head_stride;
-        c.ks = __half2float(__ushort_as_half(ld_in_u16(a.kv.k_scale_f16 + sc)));
-        c.vs = __half2float(__ushort_as_half(ld_in_u16(a.kv.v_scale_f16 + sc)));
-    }
-    return c;
+// The visible cells of a sequence, numbered without gaps.
+struct Span {
+    int n, sinks, shift;
+    __device__ __forceinline__ int cell(int i) const { return i < sinks ? i : i + shift; }
+};
+__device__ __forceinline__ Span visible(const Params &p, int s) {
+    const int len = min(max(ld_in(p.a.lens + s), 0), p.capacity);
+    const int lo = p.a.window < 0 ? 0 : max(0, len - p.a.window);
+    const int k = min(p.a.sinks, lo);
+    return {k + len - lo, k, lo - k};
+}
+__device__ __forceinline__ int tiles_of(const Span &v) { return (v.n + TILE - 1) / TILE; }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-template <typename KT, typename QT>
-__global__ void __launch_bounds__(128) paged_rows_kernel(const PagedAttnArgs a, float *lse2) {
-    const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (w >= static_cast<long long>(a.nseq) * a.nheads) return;
-    const int s = static_cast<int>(w / a.nheads), h = static_cast<int>(w % a.nheads), kvh = h / (a.nheads / a.kv.nkv);
-    const int n = min(max(a.lens[s], 0), a.table_cols * a.kv.page_size);
-    const int lo = a.window < 0 ? 0 : max(0, n - a.window);
-    const float4 q = load4(static_cast<const QT *>(a.q) + s * a.q_seq_stride + h * a.q_head_stride + 4 * lane);
-    RowState r;
-    auto span = [&](int j0, int j1) {
-        for (int j = j0; j < j1; ++j) {
-            const Cell c = find_cell<KT>(a, s, j, kvh);
-            if (!c.ok) continue;
-            const float x = warp_sum(dot4(q, load4(static_cast<const KT *>(c.k) + 4 * lane))) * c.ks * a.scale * LOG2E;
-            float4 v = load4(static_cast<const KT *>(c.v) + 4 * lane);
-            r.add(x, make_float4(v.x * c.vs, v.y * c.vs, v.z * c.vs, v.w * c.vs));
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+// Operand type: bfloat16 for bfloat16 cells, binary16 for the others.
+template <bool kBf16>
+struct Op {
+    static constexpr float LO = kBf16 ? 1.0f : 2048.0f;   // what remainders are multiplied by
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        if constexpr (kBf16) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+            return *reinterpret_cast<const uint32_t *>(&v);
+        } else {
+            const __half2 v = __floats2half2_rn(a, b);
+            return *reinterpret_cast<const uint32_t *>(&v);
         }
-    };
-    span(0, min(a.sinks, lo));
-    span(lo, n);
-    store4(static_cast<QT *>(a.out) + w * 128 + 4 * lane, r.result());
-    if (lane == 0) {
-        if (a.lse != nullptr) a.lse[w] = (r.m + log2f(r.l)) * LN2;
-        if (lse2 != nullptr) lse2[w] = r.m + log2f(r.l);
     }
+    static __device__ __forceinline__ float2 unpack(uint32_t w) {
+        if constexpr (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+    // a, b rounded to the type, and the (scaled) remainders of that.
+    static __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
+        hi = pack(a, b);
+        const float2 h = unpack(hi);
+        lo = pack((a - h.x) * LO, (b - h.y) * LO);
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        if constexpr (kBf16)
+            asm volatile(
+                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                "{%0, %1, %2, %3};"
+                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        else
+            asm volatile(
+                "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                "{%0, %1, %2, %3};"
+                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+
+// Bytes kSel picks from {lo word, hi word} (0x64 bytes come from the second operand), minus 1152: int8 -> binary16.
+__device__ __forceinline__ uint32_t biased_to_half2(uint32_t w, uint32_t sel) {
+    const uint32_t x = __byte_perm(w, 0x64646464u, sel);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <typename KT, typename QT>
-__global__ void __launch_bounds__(256) paged_mass_kernel(const PagedAttnArgs a, const float *lse2) {
-    const int lane = threadIdx.x & 31, s = blockIdx.y;
-    const int n = min(max(a.lens[s], 0), a.table_cols * a.kv.page_size);
-    const int lo = a.window < 0 ? 0 : max(0, n - a.window);
-    for (int j = blockIdx.x * 8 + (threadIdx.x >> 5); j < n; j += gridDim.x * 8) {
-        float got = 0.0f;
-        if (j >= lo || j < a.sinks) {
-            for (int h = 0; h < a.nheads; ++h) {
-                const Cell c = find_cell<KT>(a, s, j, h / (a.nheads / a.kv.nkv));
-                if (!c.ok) continue;
-                const float4 q = load4(static_cast<const QT *>(a.q) + s * a.q_seq_stride + h * a.q_head_stride + 4 * lane);
-                const float x = warp_sum(dot4(q, load4(static_cast<const KT *>(c.k) + 4 * lane))) * c.ks * a.scale * LOG2E;
-                got += exp2f(x - lse2[static_cast<size_t>(s) * a.nheads + h]);
+template <int kKv>   // QSA_BF16, QSA_F16 or QSA_I8
+struct Form {
+    static constexpr bool kInt8 = kKv == QSA_I8;
+    using O = Op<kKv == QSA_BF16>;
+    static constexpr int ROW = kInt8 ? 128 : 256;          // bytes of a cell's row
+    // Rows 16 bytes apart from a multiple of 128: the fragment loads of both
+    // products (ldmatrix, or 16-byte loads for int8) meet no bank twice.
+    static constexpr int PITCH = ROW + 16;
+    static constexpr int STAGES = kInt8 ? 6 : 3;
+    static constexpr int STAGE = 2 * STEP * PITCH;
+    static constexpr int RING = STAGES * STAGE;            // one warp's ring
+    static constexpr int SIDE = 8 * STEP + 16;             // a stage's scales (float ks, vs per cell) and cell mask
+};
+
+template <int kKv, int kMT>
+constexpr int smem_bytes() {
+    using F = Form<kKv>;
+    return std::max(WARPS * F::RING, WARPS * 8 * kMT * 128 * 4) + WARPS * F::STAGES * F::SIDE + 2 * WARPS * 8 * kMT * 4;
+}
+
+template <int kKv, typename QT, int kMT>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __grid_constant__ Params p) {
+    using F = Form<kKv>;
+    using O = typename F::O;
+    constexpr bool kInt8 = F::kInt8;
+    constexpr int HEADS_PER_UNIT = 8 * kMT;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long sh_scan[WARPS], sh_first;
+    __shared__ int sh_seq;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r = lane >> 2, t = lane & 3;
+    const PagedAttnArgs &a = p.a;
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ---- this CTA's range of tiles -------------------------------------------------
+    const int each = (a.nseq + THREADS - 1) / THREADS;
+    const int s0 = min(tid * each, a.nseq), s1 = min(s0 + each, a.nseq);
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) mine += tiles_of(visible(p, s));
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(FULL_MASK, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) sh_scan[warp] = before;
+    if (tid == 0) sh_seq = -1;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += sh_scan[w];
+        total += sh_scan[w];
+    }
+    before -= mine;
+    // Below 2^63: at most 65,535 sequences of 2^24 tiles times 65,535 units.
+    const long long all = total * p.units;
+    const long long per = (all + gridDim.x - 1) / gridDim.x;
+    const long long x0 = per * blockIdx.x, x1 = min(x0 + per, all);
+    if (tid == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    // The sequence that x0 falls into, and the number of its first tile.
+    if (x0 < x1 && x0 >= before * p.units && x0 < (before + mine) * p.units) {
+        int s = s0;
+        long long b = before;
+        for (; s < s1 - 1; ++s) {
+            const int n = tiles_of(visible(p, s));
+            if (x0 < (b + n) * p.units) break;
+            b += n;
+        }
+        sh_seq = s;
+        sh_first = b * p.units;
+    }
+    // Sequences without a visible cell have no tile: their rows are written here.
+    for (int s = blockIdx.x; s < a.nseq; s += gridDim.x) {
+        if (visible(p, s).n > 0) continue;
+        for (int e = tid; e < a.nheads * 32; e += THREADS)
+            store4(static_cast<QT *>(a.out) + static_cast<size_t>(s) * a.nheads * 128 + 4 * e, make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int h = tid; h < a.nheads; h += THREADS) {
+            if (a.lse != nullptr) a.lse[static_cast<size_t>(s) * a.nheads + h] = -INFINITY;
+            if (p.lse2 != nullptr) p.lse2[static_cast<size_t>(s) * a.nheads + h] = -INFINITY;
+        }
+    }
+    __syncthreads();
+    int s = sh_seq;
+    if (s < 0) return;
+    long long first = sh_first;
+
+    unsigned char *side_base = smem + std::max(WARPS * F::RING, WARPS * HEADS_PER_UNIT * 128 * 4);
+    float *merge_m = reinterpret_cast<float *>(side_base + WARPS * F::STAGES * F::SIDE);
+    float *merge_l = merge_m + WARPS * HEADS_PER_UNIT;
+    float *merge_o = reinterpret_cast<float *>(smem);
+    const uint32_t ring = smem_u32(smem + warp * F::RING);
+    unsigned char *side = side_base + warp * F::STAGES * F::SIDE;
+    const int elem = kInt8 ? 1 : 2;
+    const float c = a.scale * LOG2E;
+
+    for (long long x = x0; x < x1;) {
+        const Span v = visible(p, s);
+        const int nt = tiles_of(v);
+        if (x >= first + static_cast<long long>(nt) * p.units) {   // on to the next sequence
+            first += static_cast<long long>(nt) * p.units;
+            ++s;
+            continue;
+        }
+        const int u = static_cast<int>((x - first) / nt), t0 = static_cast<int>((x - first) % nt);
+        const int t1 = static_cast<int>(min(static_cast<long long>(nt), t0 + (x1 - x)));
+        const int kvh = u / p.parts, h0 = kvh * p.group + (u % p.parts) * HEADS_PER_UNIT;
+        const int nh = min(HEADS_PER_UNIT, (kvh + 1) * p.group - h0);
+
+        // ---- query fragments: head r of each 8 in rows 0-7, remainders in rows 8-15 ----
+        uint32_t qa[kMT][8][kInt8 ? 4 : 2];
+        float qc[kMT];   // what a product is multiplied by to become x
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+            const bool have = 8 * m + r < nh;
+            const QT *qp = static_cast<const QT *>(a.q) + s * a.q_seq_stride + (h0 + (have ? 8 * m + r : 0)) * a.q_head_stride;
+            qc[m] = c;
+            if constexpr (kInt8) {
+                // This thread's elements: d = 32 t + 4 k + {0, 1, 2, 3} of step k.
+                float4 e[8];
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    e[k] = have ? load4(qp + 32 * t + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(e[k].x), fabsf(e[k].y)), fmaxf(fabsf(e[k].z), fabsf(e[k].w))));
+                }
+                top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
+                int ex = 0;
+                if (top > 0.0f && top < INFINITY) frexpf(top, &ex);
+                ex = max(-100, min(100, ex));
+                const float down = ldexpf(1.0f, -ex);
+                qc[m] = c * ldexpf(1.0f, ex);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    O::split(e[k].x * down, e[k].y * down, qa[m][k][0], qa[m][k][1]);
+                    O::split(e[k].z * down, e[k].w * down, qa[m][k][2], qa[m][k][3]);
+                }
+            } else {
+                // d = 16 k + 2 t + {0, 1} and + 8
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    qa[m][k][0] = have ? ld_in(reinterpret_cast<const uint32_t *>(qp + 16 * k + 2 * t)) : 0u;
+                    qa[m][k][1] = have ? ld_in(reinterpret_cast<const uint32_t *>(qp + 16 * k + 2 * t + 8)) : 0u;
+                }
             }
         }
-        if (lane == 0) a.mass_out[s * a.mass_stride + j] = a.mass[s * a.mass_stride + j] + got;
+
+        float o[kMT][16][4];
+        float ref[kMT], sum[kMT];
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+            ref[m] = -INFINITY;
+            sum[m] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[m][n][e] = 0.0f;
+        }
+
+        // ---- this warp's steps: visible cells 64 tile + 16 warp + 0..15 ----------------
+        const int32_t *table = a.table + s * a.table_stride;
+        const int row = lane & 15;                   // the row whose address this lane finds
+        auto index = [&](int step) { return (t0 + step) * TILE + warp * STEP; };
+        auto find_page = [&](int step) {             // page of this lane's row, -1 without one
+            const int i = index(step) + row;
+            return step < t1 - t0 && i < v.n ? ld_in(table + divide(p.page, v.cell(i))) : -1;
+        };
+        uint16_t pend = 0;                           // this lane's scale of the newest step
+        auto issue = [&](int step, int page) {
+            if (step < t1 - t0) {
+                const int slot_at = step % F::STAGES;
+                const int i = index(step) + row;
+                const bool ok = page >= 0 && page < a.kv.npages;
+                const int j = v.cell(i);
+                const int in_page = j - static_cast<int>(divide(p.page, j)) * a.kv.page_size;
+                const long long off = ok ? (page * a.kv.page_stride + in_page * a.kv.cell_stride + kvh * a.kv.head_stride) * elem : 0;
+                const uint32_t mask = __ballot_sync(FULL_MASK, ok) & 0xFFFFu;
+                unsigned char *sd = side + slot_at * F::SIDE;
+                if (lane == 0) *reinterpret_cast<uint32_t *>(sd + 8 * STEP) = mask;
+                if constexpr (kInt8) {
+                    const long long so = page * a.kv.scale_page_stride + in_page * a.kv.scale_cell_stride + kvh * a.kv.scale_head_stride;
+                    pend = ok ? ld_in_u16((lane < 16 ? a.kv.k_scale_f16 : a.kv.v_scale_f16) + so) : 0;
+                }
+                const uint32_t dst = ring + slot_at * F::STAGE;
+                constexpr int LANES = F::ROW / 16, ROWS = 32 / LANES;
+                const int chunk = 16 * (lane % LANES);
+#pragma unroll
+                for (int b = 0; b < STEP / ROWS; ++b) {
+                    const int rr = b * ROWS + lane / LANES;
+                    const long long ro = __shfl_sync(FULL_MASK, off, rr) + chunk;
+                    const bool rok = (mask >> rr) & 1u;
+                    cp_async_16_or_zero(dst + rr * F::PITCH + chunk, static_cast<const char *>(a.kv.k) + (rok ? ro : 0), rok);
+                    cp_async_16_or_zero(dst + (STEP + rr) * F::PITCH + chunk, static_cast<const char *>(a.kv.v) + (rok ? ro : 0), rok);
+                }
+            }
+            cp_async_commit();
+        };
+        auto put_scale = [&](int step) {
+            if constexpr (kInt8)
+                if (step < t1 - t0)
+                    reinterpret_cast<float *>(side + (step % F::STAGES) * F::SIDE)[2 * row + (lane >> 4)] =
+                        __half2float(__ushort_as_half(pend));
+        };
+
+        const int nsteps = t1 - t0;
+        int page = find_page(0);
+#pragma unroll 1
+        for (int i = 0; i < F::STAGES - 1; ++i) {
+            const int next = find_page(i + 1);
+            issue(i, page);
+            if (i < F::STAGES - 2) put_scale(i);
+            page = next;
+        }
+#pragma unroll 1
+        for (int step = 0; step < nsteps; ++step) {
+            put_scale(step + F::STAGES - 2);
+            cp_async_wait<F::STAGES - 2>();
+            __syncwarp();
+            const int next = find_page(step + F::STAGES);
+            issue(step + F::STAGES - 1, page);
+            page = next;
+            if (index(step) >= v.n) continue;
+
+            const uint32_t kb = ring + (step % F::STAGES) * F::STAGE, vb = kb + STEP * F::PITCH;
+            const unsigned char *sd = side + (step % F::STAGES) * F::SIDE;
+            const uint32_t mask = *reinterpret_cast<const uint32_t *>(sd + 8 * STEP);
+            // x of heads (row r) by cells 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+            float sc[kMT][2][4];
+#pragma unroll
+            for (int m = 0; m < kMT; ++m)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[m][n][e] = 0.0f;
+            float ks[4], vs[4];
+            if constexpr (kInt8) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float4 f = *reinterpret_cast<const float4 *>(sd + 8 * (2 * t + 8 * n));
+                    ks[2 * n] = f.x;
+                    vs[2 * n] = f.y;
+                    ks[2 * n + 1] = f.z;
+                    vs[2 * n + 1] = f.w;
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const uint32_t at = kb + (8 * n + r) * F::PITCH + 32 * t;
+                    const uint4 w0 = ld_shared_v4(at), w1 = ld_shared_v4(at + 16);
+                    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t z = w[k] ^ 0x80808080u;
+                        const uint32_t b0 = biased_to_half2(z, 0x4140), b1 = biased_to_half2(z, 0x4342);
+#pragma unroll
+                        for (int m = 0; m < kMT; ++m) O::mma(sc[m][n], qa[m][k], b0, b1);
+                    }
+                }
+            } else {
+                // matrices: cells 0-7 and 8-15 by d 0-7 and 8-15 of step k
+                const uint32_t at = kb + ((lane & 7) + 8 * (lane >> 4)) * F::PITCH + 16 * ((lane >> 3) & 1);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t b[4];
+                    ldmatrix4(b, at + 32 * k);
+#pragma unroll
+                    for (int m = 0; m < kMT; ++m) {
+                        const uint32_t qf[4] = {qa[m][k][0], 0u, qa[m][k][1], 0u};
+                        O::mma(sc[m][0], qf, b[0], b[1]);
+                        O::mma(sc[m][1], qf, b[2], b[3]);
+                    }
+                }
+            }
+            uint32_t pa[kMT][4];
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) {
+                float xx[4], top = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y = sc[m][n][e];
+                        if constexpr (kInt8) y = fmaf(sc[m][n][2 + e], 1.0f / O::LO, y) * ks[2 * n + e];
+                        y *= qc[m];
+                        if (!((mask >> (2 * t + 8 * n + e)) & 1u)) y = -INFINITY;
+                        xx[2 * n + e] = y;
+                        float z = y;
+                        if constexpr (kInt8) z += __log2f(fmaxf(fabsf(vs[2 * n + e]), 5.9604645e-8f));
+                        top = fmaxf(top, z);
+                    }
+                if (p.logits != nullptr && 8 * m + r < nh) {
+                    float *lp = p.logits + (static_cast<size_t>(s) * a.nheads + h0 + 8 * m + r) * p.stride + index(step) + 2 * t;
+                    *reinterpret_cast<float2 *>(lp) = make_float2(xx[0], xx[1]);
+                    *reinterpret_cast<float2 *>(lp + 8) = make_float2(xx[2], xx[3]);
+                }
+                top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
+                const bool move = top > ref[m] + LAZY || (ref[m] == -INFINITY && top > -INFINITY);
+                if (__any_sync(FULL_MASK, move)) {
+                    const float f = move ? ex2(ref[m] - top) : 1.0f;
+                    if (move) ref[m] = top;
+                    sum[m] *= f;
+#pragma unroll
+                    for (int n = 0; n < 16; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[m][n][e] *= f;
+                }
+                const float base = ref[m] == -INFINITY ? 0.0f : ref[m];
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = ex2(xx[e] - base);
+                    sum[m] += w[e];
+                    if constexpr (kInt8) w[e] *= vs[e];
+                }
+                O::split(w[0], w[1], pa[m][0], pa[m][1]);
+                O::split(w[2], w[3], pa[m][2], pa[m][3]);
+            }
+            if constexpr (kInt8) {
+                // This thread's cells 2 t, 2 t + 1, 2 t + 8, 2 t + 9; column r of product n is d = 16 r + n.
+                uint4 cw[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) cw[e] = ld_shared_v4(vb + (2 * t + (e & 1) + 8 * (e >> 1)) * F::PITCH + 16 * r);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t lo[2], hi[2];   // cells (2t, 2t+1) and (2t+8, 2t+9): d 0, 1 and d 2, 3 of the word
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t w0 = reinterpret_cast<const uint32_t *>(&cw[2 * e])[g] ^ 0x80808080u;
+                        const uint32_t w1 = reinterpret_cast<const uint32_t *>(&cw[2 * e + 1])[g] ^ 0x80808080u;
+                        lo[e] = __byte_perm(w0, w1, 0x5140);
+                        hi[e] = __byte_perm(w0, w1, 0x7362);
+                    }
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const uint32_t sel = (d & 1) ? 0x4342 : 0x4140;
+                        const uint32_t b0 = biased_to_half2(d < 2 ? lo[0] : hi[0], sel);
+                        const uint32_t b1 = biased_to_half2(d < 2 ? lo[1] : hi[1], sel);
+#pragma unroll
+                        for (int m = 0; m < kMT; ++m) O::mma(o[m][4 * g + d], pa[m], b0, b1);
+                    }
+                }
+            } else {
+                // matrices: cells 0-7, 8-15 by d 16 n .. + 7, then d 16 n + 8 .. + 15
+                const uint32_t at = vb + (lane & 15) * F::PITCH + 16 * (lane >> 4);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    uint32_t b[4];
+                    ldmatrix4_t(b, at + 32 * n);
+#pragma unroll
+                    for (int m = 0; m < kMT; ++m) {
+                        O::mma(o[m][2 * n], pa[m], b[0], b[1]);
+                        O::mma(o[m][2 * n + 1], pa[m], b[2], b[3]);
+                    }
+                }
+            }
+        }
+        cp_async_wait<0>();
+
+        // ---- join the warps, in warp order ----------------------------------------------
+        __syncthreads();   // every warp is done with its ring
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+            sum[m] += __shfl_xor_sync(FULL_MASK, sum[m], 1);
+            sum[m] += __shfl_xor_sync(FULL_MASK, sum[m], 2);
+            const int h = warp * HEADS_PER_UNIT + 8 * m + r;
+            if (t == 0) {
+                merge_m[h] = ref[m];
+                merge_l[h] = sum[m];
+            }
+            float *mo = merge_o + h * 128;
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+                const float y0 = fmaf(o[m][n][2], 1.0f / O::LO, o[m][n][0]), y1 = fmaf(o[m][n][3], 1.0f / O::LO, o[m][n][1]);
+                if constexpr (kInt8) {
+                    mo[32 * t + n] = y0;
+                    mo[32 * t + 16 + n] = y1;
+                } else {
+                    *reinterpret_cast<float2 *>(mo + 8 * n + 2 * t) = make_float2(y0, y1);
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == nt;
+        const int slot = 2 * blockIdx.x + (x == x0 ? 0 : 1);
+        for (int h = warp; h < nh; h += WARPS) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) top = fmaxf(top, merge_m[w * HEADS_PER_UNIT + h]);
+            const float base = top == -INFINITY ? 0.0f : top;
+            float l = 0.0f;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                const int hw = w * HEADS_PER_UNIT + h;
+                const float f = ex2(merge_m[hw] - base);
+                l = fmaf(merge_l[hw], f, l);
+                const float4 z = *reinterpret_cast<const float4 *>(merge_o + hw * 128 + 4 * lane);
+                y.x = fmaf(z.x, f, y.x);
+                y.y = fmaf(z.y, f, y.y);
+                y.z = fmaf(z.z, f, y.z);
+                y.w = fmaf(z.w, f, y.w);
+            }
+            if (whole) {
+                const size_t out_row = static_cast<size_t>(s) * a.nheads + h0 + h;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                store4(static_cast<QT *>(a.out) + out_row * 128 + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+                if (lane == 0) {
+                    const float e = l == 0.0f ? -INFINITY : top + log2f(l);
+                    if (a.lse != nullptr) a.lse[out_row] = e * LN2;
+                    if (p.lse2 != nullptr) p.lse2[out_row] = e;
+                }
+            } else {
+                float *sp = p.slots + (static_cast<size_t>(slot) * HEADS_PER_UNIT + h) * SLOT_ROW;
+                *reinterpret_cast<float4 *>(sp + 4 * lane) = y;
+                if (lane == 0) {
+                    sp[128] = top;
+                    sp[129] = l;
+                }
+            }
+        }
+        // The unit is joined by the block of the second range that it falls into.
+        const long long unit0 = first + static_cast<long long>(u) * nt;
+        if (tid == 0 && !whole && x == x0 && x0 > unit0 && unit0 / per == blockIdx.x - 1)
+            p.meta[blockIdx.x] = make_int4(s, u, static_cast<int>(unit0 / per) * 2 + (unit0 % per == 0 ? 0 : 1),
+                                           static_cast<int>((unit0 + nt - 1) / per));
+        x += t1 - t0;
+        __syncthreads();   // the rings are free again
     }
 }
 
-template <typename KT, typename QT>
-cudaError_t launch(const PagedAttnArgs &a, cudaStream_t stream) {
-    const long long warps = static_cast<long long>(a.nseq) * a.nheads;
-    float *lse2 = a.mass != nullptr ? static_cast<float *>(a.scratch) : nullptr;
-    paged_rows_kernel<KT, QT><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(a, lse2);
-    if (a.mass != nullptr && a.table_cols > 0)
-        paged_mass_kernel<KT, QT><<<dim3(256, a.nseq), 256, 0, stream>>>(a, lse2);
-    return cudaGetLastError();
+// Adds the partial results of one unit's ranges for one head, in range order.
+template <typename QT>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p, int heads_per_unit) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int4 w = __ldcg(p.meta + blockIdx.x);
+    if (w.x < 0) return;
+    const PagedAttnArgs &a = p.a;
+    const int s = w.x, kvh = w.y / p.parts, h0 = kvh * p.group + (w.y % p.parts) * heads_per_unit;
+    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    if (h0 + h >= (kvh + 1) * p.group) return;
+    const int c0 = w.z >> 1, n = w.w - c0 + 1;
+    auto slot = [&](int i) {   // the unit's first range may be its CTA's second segment
+        return p.slots + (static_cast<size_t>(i == 0 ? w.z : 2 * (c0 + i)) * heads_per_unit + h) * SLOT_ROW;
+    };
+    __shared__ float red[4];
+    float top = -INFINITY;
+    for (int i = tid; i < n; i += 128) top = fmaxf(top, __ldcg(slot(i) + 128));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+    if (lane == 0) red[tid >> 5] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float l = 0.0f, y = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float *sp = slot(i);
+        const float f = ex2(__ldcg(sp + 128) - base);
+        l = fmaf(__ldcg(sp + 129), f, l);
+        y = fmaf(__ldcg(sp + tid), f, y);
+    }
+    const size_t row = static_cast<size_t>(s) * a.nheads + h0 + h;
+    y *= l == 0.0f ? 0.0f : 1.0f / l;
+    if constexpr (sizeof(QT) == 4)
+        static_cast<float *>(a.out)[row * 128 + tid] = y;
+    else
+        static_cast<QT *>(a.out)[row * 128 + tid] = static_cast<QT>(y);
+    if (tid == 0) {
+        const float e = l == 0.0f ? -INFINITY : top + log2f(l);
+        if (a.lse != nullptr) a.lse[row] = e * LN2;
+        if (p.lse2 != nullptr) p.lse2[row] = e;
+    }
+}
+
+// mass_out = mass + sum over the heads, in head order, of the weights of the
+// kept logits. One thread per 4 cells, so a row of logits is read in 512-byte
+// pieces per warp; cells that are not visible keep their mass.
+__global__ void __launch_bounds__(256) mass_kernel(const __grid_constant__ Params p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const PagedAttnArgs &a = p.a;
+    const int s = blockIdx.y;
+    const Span v = visible(p, s);
+    const int len = v.n + v.shift;                  // sinks + window + what lies between
+    const float *mass = a.mass + s * a.mass_stride;
+    float *out = a.mass_out + s * a.mass_stride;
+    const float *lse = p.lse2 + static_cast<size_t>(s) * a.nheads;
+    for (int i = (blockIdx.x * 256 + threadIdx.x) * 4; i < v.n; i += gridDim.x * 1024) {
+        float got[4] = {0.f, 0.f, 0.f, 0.f};
+        const float *lp = p.logits + static_cast<size_t>(s) * a.nheads * p.stride + i;
+#pragma unroll 8
+        for (int h = 0; h < a.nheads; ++h) {
+            const float e = __ldcg(lse + h);
+            const float4 x = ld_in(reinterpret_cast<const float4 *>(lp + static_cast<size_t>(h) * p.stride));
+            if (e == -INFINITY) continue;
+            got[0] += ex2(x.x - e);
+            got[1] += ex2(x.y - e);
+            got[2] += ex2(x.z - e);
+            got[3] += ex2(x.w - e);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < v.n) out[v.cell(i + k)] = __ldcg(mass + v.cell(i + k)) + got[k];
+    }
+    if (out != mass && v.shift > 0)
+        for (int j = v.sinks + blockIdx.x * 256 + threadIdx.x; j < v.sinks + v.shift; j += gridDim.x * 256)
+            if (j < len) out[j] = __ldcg(mass + j);
+}
+
+struct Layout {
+    size_t meta, slots, lse2, logits, bytes;
+    int heads_per_unit, grid, stride;
+};
+Layout layout(int nseq, int nheads, int nkv, int capacity, bool with_mass) {
+    Layout y;
+    const int group = nheads / nkv;
+    y.heads_per_unit = group <= 8 ? 8 : 16;
+    const long long parts = (group + y.heads_per_unit - 1) / y.heads_per_unit;
+    const long long tiles = (static_cast<long long>(capacity) + TILE - 1) / TILE * nkv * parts * nseq;
+    y.grid = static_cast<int>(std::max(1LL, std::min<long long>(static_cast<long long>(CTAS_PER_SM) * device_sm_count(), tiles)));
+    y.stride = (capacity + TILE - 1) / TILE * TILE;
+    size_t at = 0;
+    y.meta = at;
+    at += sizeof(int4) * y.grid;
+    y.slots = at;
+    at += sizeof(float) * 2 * y.grid * y.heads_per_unit * SLOT_ROW;
+    y.lse2 = at;
+    if (with_mass) at += (sizeof(float) * nseq * static_cast<size_t>(nheads) + 15) / 16 * 16;
+    y.logits = at;
+    if (with_mass) at += sizeof(float) * nseq * static_cast<size_t>(nheads) * y.stride;
+    y.bytes = at;
+    return y;
+}
+
+// Launches as a programmatic dependent of the previous grid on the stream.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int kKv, typename QT, int kMT>
+cudaError_t run(const Params &p, int grid, cudaStream_t stream) {
+    constexpr int smem = smem_bytes<kKv, kMT>();
+    auto kernel = paged_kernel<kKv, QT, kMT>;
+    static thread_local int configured_device = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && configured_device != dev) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) configured_device = dev;
+    }
+    if (e == cudaSuccess) e = launch(kernel, dim3(grid), THREADS, smem, stream, p);
+    if (e == cudaSuccess) e = launch(join_kernel<QT>, dim3(grid, std::min(p.group, 8 * kMT)), 128, 0, stream, p, 8 * kMT);
+    if (e == cudaSuccess && p.logits != nullptr)
+        e = launch(mass_kernel, dim3(std::min((p.stride + 1023) / 1024, 64), p.a.nseq), 256, 0, stream, p);
+    return e;
+}
+
+template <int kKv, typename QT>
+cudaError_t run_heads(const Params &p, const Layout &y, cudaStream_t stream) {
+    return y.heads_per_unit == 8 ? run<kKv, QT, 1>(p, y.grid, stream) : run<kKv, QT, 2>(p, y.grid, stream);
 }
 
 }  // namespace
 
-size_t paged_attn_scratch_bytes(int nseq, int nheads, int, int, bool) {
-    return static_cast<size_t>(nseq) * nheads * sizeof(float);
+size_t paged_attn_scratch_bytes(int nseq, int nheads, int nkv, int capacity, bool with_mass) {
+    return layout(nseq, nheads, nkv, capacity, with_mass).bytes;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t stream) {
-    if (a.kv.dtype == QSA_BF16) return launch<__nv_bfloat16, __nv_bfloat16>(a, stream);
-    if (a.kv.dtype == QSA_F16) return launch<__half, __half>(a, stream);
-    if (a.q_dtype == QSA_F32) return launch<int8_t, float>(a, stream);
-    if (a.q_dtype == QSA_F16) return launch<int8_t, __half>(a, stream);
-    return launch<int8_t, __nv_bfloat16>(a, stream);
+    Params p;
+    p.a = a;
+    p.capacity = a.table_cols * a.kv.page_size;
+    const Layout y = layout(a.nseq, a.nheads, a.kv.nkv, p.capacity, a.mass != nullptr);
+    p.page = make_divider(a.kv.page_size);
+    p.group = a.nheads / a.kv.nkv;
+    p.parts = (p.group + y.heads_per_unit - 1) / y.heads_per_unit;
+    p.units = a.kv.nkv * p.parts;
+    p.stride = y.stride;
+    char *b = static_cast<char *>(a.scratch);
+    p.meta = reinterpret_cast<int4 *>(b + y.meta);
+    p.slots = reinterpret_cast<float *>(b + y.slots);
+    p.lse2 = a.mass != nullptr ? reinterpret_cast<float *>(b + y.lse2) : nullptr;
+    p.logits = a.mass != nullptr && p.capacity > 0 ? reinterpret_cast<float *>(b + y.logits) : nullptr;
+    if (a.kv.dtype == QSA_BF16) return run_heads<QSA_BF16, __nv_bfloat16>(p, y, stream);
+    if (a.kv.dtype == QSA_F16) return run_heads<QSA_F16, __half>(p, y, stream);
+    if (a.q_dtype == QSA_F32) return run_heads<QSA_I8, float>(p, y, stream);
+    if (a.q_dtype == QSA_F16) return run_heads<QSA_I8, __half>(p, y, stream);
+    return run_heads<QSA_I8, __nv_bfloat16>(p, y, stream);
 }
 
 }  // namespace qsa
