@@ -308,7 +308,8 @@ qsa_status qsa_block_select(const float *q, const float *kblk, int nq, int max_b
  * Bit 0x100: a wait of the tensor-core scorer's pipeline ran out (the CTA
  * then abandons its remaining waits at once, lets its own copies and MMAs
  * in flight finish, and exits); bit 0x2: the fused decode select's grid
- * barrier ran out. Synchronises `stream`. *code receives the word.
+ * barrier ran out; bit 0x10000: a wait of the prompt attention's pipeline ran
+ * out. Synchronises `stream`. *code receives the word.
  */
 qsa_status qsa_get_device_error(uint32_t *code, cudaStream_t stream);
 

@@ -263,6 +263,18 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr) {
            | (static_cast<uint64_t>(2) << 61);                  // swizzle: 128 B
 }
 
+// Shared-memory matrix descriptor of an operand stored with its M/N dimension
+// contiguous (K rows of 64 elements, 128 bytes, in 8-row swizzled atoms 1,024 B
+// apart); the next 64 elements of M/N lie `group_bytes` further. Advancing K
+// by 16 rows adds 2,048 bytes to the start address.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t group_bytes) {
+    return static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4)        // start address >> 4
+           | (static_cast<uint64_t>(group_bytes >> 4) << 16)         // leading byte offset: 64-element groups of M/N
+           | (static_cast<uint64_t>(1024 >> 4) << 32)                // stride byte offset: 8-row groups of K
+           | (static_cast<uint64_t>(1) << 46)                        // descriptor version
+           | (static_cast<uint64_t>(2) << 61);                       // swizzle: 128 B
+}
+
 // Instruction descriptor, kind::f16: fp32 D, bf16 A and B, both K-major.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
     return (1u << 4)                                   // D format: f32
@@ -294,6 +306,18 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
                  "r"(c), "r"(d)
                  : "memory");
 }
+// 32 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 1-D bulk async copy shared -> global, tracked by this thread's bulk group.
@@ -318,6 +342,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst_smem, const void *map, 
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
         "[%4];" ::"r"(dst_smem),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+// 3-D form of tma_load_2d (coordinates innermost first).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst_smem, const void *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst_smem),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
 // Named barrier `id` over `count` threads (a multiple of 32).

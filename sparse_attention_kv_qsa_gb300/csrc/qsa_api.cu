@@ -339,10 +339,11 @@ qsa_status qsa_block_summary(const int8_t *k_cells, const uint16_t *k_scale_f16,
 qsa_status qsa_get_device_error(uint32_t *code, cudaStream_t stream) {
     if (code == nullptr) return QSA_ERR_INVALID;
     *code = 0;
-    uint32_t a = 0, b = 0;
+    uint32_t a = 0, b = 0, c = 0;
     cudaError_t e = qsa::topk_error_read_clear(&a, stream);
     if (e == cudaSuccess) e = qsa::tc_error_read_clear(&b, stream);
-    *code = a | (b << 8);
+    if (e == cudaSuccess) e = qsa::window_error_read_clear(&c, stream);
+    *code = a | (b << 8) | (c << 16);
     return from_cuda(e);
 }
 

@@ -108,5 +108,6 @@ uint64_t wait_limit_ns();
 // qsa_debug_inject's fault bits for the kernels launched from now on (0 in use).
 uint32_t debug_inject();
 cudaError_t tc_error_read_clear(uint32_t *word, cudaStream_t stream);
+cudaError_t window_error_read_clear(uint32_t *word, cudaStream_t stream);
 
 }  // namespace qsa
