@@ -161,6 +161,25 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two fp32 values in one 64-bit register, worked on by one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 template <typename T>
 __device__ __forceinline__ uint32_t pack2_rn(float a, float b);
 template <>
@@ -364,11 +383,20 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                         if (!((bits >> e) & 1u)) sr[g][e] = 0xFF800000u;
                 }
             }
-            float top = -INFINITY;
+            // 8 chains, so that the maximum of 128 is not a chain of 128.
+            float tops[8];
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
+            for (int e = 0; e < 8; ++e) tops[e] = __uint_as_float(sr[0][e]);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(sr[g][e]));
+            for (int e = 8; e < 128; e += 16)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float y = __uint_as_float(sr[e >> 5][(e & 31) + k]);
+                    tops[k] = e + 8 < 128 ? fmaxf(fmaxf(tops[k], y), __uint_as_float(sr[(e + 8) >> 5][((e + 8) & 31) + k]))
+                                          : fmaxf(tops[k], y);
+                }
+            const float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                                    fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
             const bool move = (top - m) * c > LAZY;   // also true from -infinity to a finite maximum
             if (__any_sync(FULL_MASK, move)) {
                 const float f = move ? exp2_approx((m - top) * c) : 1.0f;
@@ -387,17 +415,27 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                 }
             }
             const float mc = m == -INFINITY ? 0.0f : m * c;
+            const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+            uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 uint32_t pw[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    const float x0 = exp2_approx(fmaf(__uint_as_float(sr[2 * g + (e >> 4)][(2 * e) & 31]), c, -mc));
-                    const float x1 = exp2_approx(fmaf(__uint_as_float(sr[2 * g + (e >> 4)][(2 * e + 1) & 31]), c, -mc));
-                    l += x0 + x1;
+                    float x0, x1;
+                    unpair(fma_pair(pair(__uint_as_float(sr[2 * g + (e >> 4)][(2 * e) & 31]),
+                                         __uint_as_float(sr[2 * g + (e >> 4)][(2 * e + 1) & 31])), c2, mc2), x0, x1);
+                    x0 = exp2_approx(x0);
+                    x1 = exp2_approx(x1);
+                    sums[e & 3] = add_pair(sums[e & 3], pair(x0, x1));
                     pw[e] = pack2_rn<T>(x0, x1);
                 }
                 tmem_st32(s_at + 32 * g, pw);
+            }
+            {
+                float y0, y1;
+                unpair(add_pair(add_pair(sums[0], sums[1]), add_pair(sums[2], sums[3])), y0, y1);
+                l += y0 + y1;
             }
             tmem_st_wait();
             tc_fence_before_sync();
