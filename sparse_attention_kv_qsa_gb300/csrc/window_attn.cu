@@ -31,6 +31,7 @@
 // such a row's values would reach the sums. A row whose sums are not finite
 // is therefore computed again from its visible keys alone (attend_row, also
 // the whole path for strides that a tensor map cannot express).
+#include <algorithm>
 #include <cstring>
 #include <type_traits>
 
@@ -49,7 +50,11 @@ constexpr int HALF = ROWS * 128;            // bytes of 128 rows x 64 elements
 constexpr int TILE_BYTES = 2 * HALF;
 constexpr int STAGES = 5;                   // key and value tiles in flight
 constexpr int PIECE = 16;                   // rows of a copy in the tile where sinks and window meet
-constexpr int MMA_WARP = 8, COPY_WARP = 9, WTHREADS = 320;
+constexpr int MMA_WARP = 8, COPY_WARP = 9, WTHREADS = 384;
+// 168 registers a thread at launch: 8 softmax warps x 208 + 4 x 88 = 12 x 168.
+constexpr int MORE_REGISTERS = 208, FEW_REGISTERS = 88;
+constexpr int PART_TILES = 4;               // key tiles of a part at least
+constexpr int SLOT_ROW = 132;               // 128 sums, reference, weight sum, padding
 constexpr float LAZY = 8.0f;
 constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 
@@ -58,11 +63,22 @@ struct WindowParams {
     WindowAttnArgs a;
     int group, tokens;      // query heads per KV head; tokens of a query tile
     int k_has_heads, v_has_heads;   // 0: all KV heads at one address
+    int pairs, splits;      // pairs of query tiles of the batch; parts that an item's keys are split into at most
+    float *slots;           // [pairs][nkv][splits][2 x 128 rows][SLOT_ROW]
     uint64_t wait_ns;
 };
 
+// A work item: two query tiles of one sequence and KV head, and (when items
+// are split over their keys) one part of their key tiles.
+struct Item {
+    int q0, nq, k0, nk, t0, kvh, part, slot;   // t0: first token; slot: of the partial results
+};
+
 struct WindowBarriers {
-    uint64_t q_full[2], kv_full[STAGES], kv_empty[STAGES], s_full[2], p_full[2], o_full[2], drain;
+    uint4 next;             // the answer about the next item
+    Item item[2];
+    uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t item_full[2], item_empty[2], next_full, drain;
     uint32_t tmem, abort;
 };
 constexpr size_t WINDOW_SMEM = 1024 + (2 + STAGES) * static_cast<size_t>(TILE_BYTES) + sizeof(WindowBarriers);
@@ -149,11 +165,6 @@ struct ItemKeys {
     // Row at pos sees number i iff i <= last(pos) and (i < sink_end or i >= first(pos)).
     __device__ __forceinline__ int last(int pos) const { return pos < 0 ? -1 : pos - lo + front; }
     __device__ __forceinline__ int first(int pos) const { return max(pos + 1 - window, lo) - lo + front; }
-    // Does any row between these places see a key of tile j?
-    __device__ __forceinline__ bool needed(int j, int pos_a, int pos_b) const {
-        const int i = j * ROWS;
-        return i <= last(pos_b) && (i < sink_end || i + ROWS - 1 >= first(pos_a));
-    }
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -193,6 +204,93 @@ __device__ __forceinline__ uint32_t pack2_rn<__half>(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// The item number `n` of the grid, found by a whole warp; false when there is
+// nothing to do. Query tiles pairs are numbered over the batch without
+// knowing the lengths: sequence s begins at cu_q[s] / (tokens per pair) + s.
+__device__ __forceinline__ bool find_item(const WindowParams &p, uint32_t n, Item &it) {
+    const WindowAttnArgs &a = p.a;
+    const int lane = threadIdx.x & 31, per = 2 * p.tokens;
+    it.kvh = n % a.nkv;
+    n /= a.nkv;
+    it.part = n % p.splits;
+    const int g = static_cast<int>(p.pairs - 1 - n / p.splits);   // the last tokens, which see most, first
+    auto start = [&](int s) { return min(max(ld_in(a.cu_q + s), 0), a.total_q) / per + s; };
+    int lo = 0, hi = a.nseq;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, s = lo + (lane + 1) * step;
+        const int below = __popc(__ballot_sync(FULL_MASK, s < hi && start(s) <= g));
+        lo += below * step;
+        hi = min(hi, lo + step);
+    }
+    const Sequence x = sequence(a, lo);
+    it.q0 = x.q0;
+    it.nq = x.nq;
+    it.k0 = x.k0;
+    it.nk = x.nk;
+    const long long t0 = static_cast<long long>(g - (x.q0 / per + lo)) * per;
+    if (t0 < 0 || t0 >= x.nq) return false;
+    it.t0 = static_cast<int>(t0);
+    it.slot = (g * a.nkv + it.kvh) * p.splits + it.part;
+    return true;
+}
+
+// What all roles derive from an item.
+struct Work {
+    int tokens0, tokens1, pos0, pos1;   // tokens and first row of the two tiles
+    ItemKeys keys;
+    int last0, first0, last1, first1;   // limits of the tiles' last and first rows
+    int parts, j0, j1;                  // parts that have key tiles (at least 1), this part's tiles
+    __device__ __forceinline__ Work(const WindowParams &p, const Item &it)
+        : tokens0(min(p.tokens, it.nq - it.t0)), tokens1(min(p.tokens, max(0, it.nq - it.t0 - p.tokens))),
+          pos0(it.nk - it.nq + it.t0), pos1(pos0 + p.tokens), keys(p.a, it.nk, pos0, pos0 + tokens0 + tokens1 - 1) {
+        last0 = keys.last(pos0 + tokens0 - 1);
+        first0 = keys.first(pos0);
+        last1 = tokens1 > 0 ? keys.last(pos1 + tokens1 - 1) : -1;
+        first1 = keys.first(pos1);
+        const int n = keys.tiles(), each = max((n + p.splits - 1) / p.splits, PART_TILES);
+        parts = max(1, (n + each - 1) / each);
+        j0 = min(it.part * each, n);
+        j1 = min(j0 + each, n);
+    }
+    // Does any row of query tile i see a key of key tile j?
+    __device__ __forceinline__ bool needed(int i, int j) const {
+        const int n = j * ROWS;
+        return n <= (i == 0 ? last0 : last1) && (n < keys.sink_end || n + ROWS - 1 >= (i == 0 ? first0 : first1));
+    }
+};
+
+// Asks for the index of a CTA of this grid that has not started, which then
+// never starts: the 16-byte answer completes on `bar`.
+__device__ __forceinline__ void ask_next(uint32_t answer, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// The answer: false when every CTA has started.
+__device__ __forceinline__ bool read_next(uint32_t answer, uint32_t &x) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    return ok != 0;
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <typename T>
 __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_constant__ WindowParams p) {
     extern __shared__ unsigned char raw[];
@@ -202,37 +300,25 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
     const uint32_t ring = base + 2 * TILE_BYTES;
     WindowBarriers *bars = reinterpret_cast<WindowBarriers *>(raw + (base - smem_u32(raw)) + (2 + STAGES) * TILE_BYTES);
 
-    grid_dependency_wait();
-    grid_launch_dependents();
-
-    const int kvh = blockIdx.x % a.nkv, h0 = kvh * p.group;
-    const Sequence x = sequence(a, blockIdx.y);
-    const int t0 = static_cast<int>((gridDim.x - 1 - blockIdx.x) / a.nkv) * 2 * p.tokens;   // longest rows first
-    if (t0 >= x.nq) return;
-    const int shift = x.nk - x.nq;                                // pos = shift + token
-    const int tokens0 = min(p.tokens, x.nq - t0), tokens1 = min(p.tokens, max(0, x.nq - t0 - p.tokens));
-    const int pos0 = shift + t0, pos1 = pos0 + p.tokens;          // first rows of the two tiles
-    const ItemKeys keys(a, x.nk, pos0, pos0 + tokens0 + tokens1 - 1);
-    const int ntiles = keys.tiles();
-    auto needed = [&](int i, int j) {
-        return i == 0 ? keys.needed(j, pos0, pos0 + tokens0 - 1)
-                      : tokens1 > 0 && keys.needed(j, pos1, pos1 + tokens1 - 1);
-    };
-
     if (warp == MMA_WARP) {
         tmem_alloc(&bars->tmem, TMEM_COLS);
         tmem_relinquish();
     } else if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 1);
+            mbar_init(&bars->q_empty[i], 1);
             mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->p_full[i], 4);
             mbar_init(&bars->o_full[i], 1);
+            mbar_init(&bars->o_empty[i], 4);
+            mbar_init(&bars->item_full[i], 1);
+            mbar_init(&bars->item_empty[i], 1 + 8);
         }
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&bars->kv_full[i], 1);
             mbar_init(&bars->kv_empty[i], 1);
         }
+        mbar_init(&bars->next_full, 1);
         mbar_init(&bars->drain, 1);
         bars->abort = 0;
         fence_mbar_init();
@@ -241,6 +327,8 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = bars->tmem;
+    grid_dependency_wait();
+    grid_launch_dependents();
 
     // A wait of the pipeline: the first that runs out sets the error word, and
     // all later ones return at once.
@@ -254,226 +342,343 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
         }
         return false;
     };
+    auto wait_warp = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL_MASK, wait(bar, parity)); };
 
     if (warp == COPY_WARP) {
-        if (lane == 0) {
-            const uint32_t q_bytes = 2u * 128u * p.group * p.tokens;
-            for (int i = 0; i < (tokens1 > 0 ? 2 : 1); ++i) {
-                mbar_arrive_expect_tx(&bars->q_full[i], q_bytes);
-                for (int half = 0; half < 2; ++half)
-                    tma_load_3d(base + i * TILE_BYTES + half * HALF, &p.q, 64 * half, h0, x.q0 + t0 + i * p.tokens,
-                                &bars->q_full[i]);
+        fewer_registers<FEW_REGISTERS>();
+        // ---- items, queries, keys and values in ------------------------------------------
+        uint32_t n = blockIdx.x;             // the item's number
+        uint32_t asked = 0, kv = 0, nq[2] = {0, 0};
+        bool ok = true, more = true, open = false;   // open: an answer is under way
+        const uint32_t answer = smem_u32(&bars->next);
+        auto ask = [&]() {
+            if (lane == 0) {
+                fence_proxy_async_smem();    // the last answer has been read
+                mbar_arrive_expect_tx(&bars->next_full, 16);
+                ask_next(answer, &bars->next_full);
             }
-            int n = 0;   // copies begun: tile n / 2, keys then values
-            for (; n < 2 * ntiles; ++n) {
-                const int slot = n % STAGES, j = n >> 1, i0 = j * ROWS;
-                if (!wait(&bars->kv_empty[slot], ((n / STAGES) & 1) ^ 1)) break;
-                uint64_t *bar = &bars->kv_full[slot];
-                const uint32_t dst = ring + slot * TILE_BYTES;
-                const int head = (n & 1) ? (p.v_has_heads ? kvh : 0) : (p.k_has_heads ? kvh : 0);
-                mbar_arrive_expect_tx(bar, TILE_BYTES);
-                if (i0 < keys.front && i0 + ROWS > keys.front) {
-                    const CUtensorMap *map = (n & 1) ? &p.v_piece : &p.k_piece;
-                    for (int r = 0; r < ROWS; r += PIECE) {
-                        const int key = i0 + r < keys.front ? i0 + r : i0 + r - keys.front + keys.lo;
-                        for (int half = 0; half < 2; ++half)
-                            tma_load_3d(dst + half * HALF + r * 128, map, 64 * half, head, x.k0 + key, bar);
-                    }
-                } else {
-                    const CUtensorMap *map = (n & 1) ? &p.v : &p.k;
-                    const int key = i0 < keys.front ? i0 : i0 - keys.front + keys.lo;
-                    for (int half = 0; half < 2; ++half)
-                        tma_load_3d(dst + half * HALF, map, 64 * half, head, x.k0 + key, bar);
+            open = true;
+            __syncwarp();
+        };
+        auto get = [&]() {
+            ok = wait_warp(&bars->next_full, asked & 1);
+            if (!ok) return;
+            open = false;
+            ++asked;
+            more = read_next(answer, n);
+            __syncwarp();
+        };
+        for (uint32_t k = 0; ok; ++k) {
+            Item it;
+            bool found = false;
+            while (ok && more && !found) {
+                found = find_item(p, n, it);
+                if (found) {
+                    const Work w(p, it);
+                    found = it.part < w.parts;
+                }
+                if (!found) {
+                    ask();
+                    get();
                 }
             }
-            // Copies begun here land before the CTA leaves (at once without an abort).
-            for (int d = max(0, n - STAGES); d < n; ++d) mbar_wait(&bars->kv_full[d % STAGES], (d / STAGES) & 1, p.wait_ns);
-            for (int i = 0; i < (tokens1 > 0 ? 2 : 1); ++i) mbar_wait(&bars->q_full[i], 0, p.wait_ns);
+            if (!ok || !wait_warp(&bars->item_empty[k & 1], ((k >> 1) & 1) ^ 1)) break;
+            if (lane == 0) {
+                if (!found) it.nq = 0;       // the end
+                bars->item[k & 1] = it;
+                mbar_arrive(&bars->item_full[k & 1]);
+            }
+            __syncwarp();
+            if (!found) break;
+            ask();
+            const Work w(p, it);
+            for (int i = 0; ok && i < (w.tokens1 > 0 ? 2 : 1); ++i, __syncwarp()) {
+                ok = wait_warp(&bars->q_empty[i], (nq[i] & 1) ^ 1);
+                if (ok && nq[i] > 0) ok = wait_warp(&bars->q_full[i], (nq[i] - 1) & 1);   // landed, needed or not
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars->q_full[i], 2u * 128u * p.group * p.tokens);
+                    for (int half = 0; half < 2; ++half)
+                        tma_load_3d(base + i * TILE_BYTES + half * HALF, &p.q, 64 * half, it.kvh * p.group,
+                                    it.q0 + it.t0 + i * p.tokens, &bars->q_full[i]);
+                }
+                ++nq[i];
+            }
+            const ItemKeys &keys = w.keys;
+            for (int j2 = 2 * w.j0; ok && j2 < 2 * w.j1; ++j2, ++kv) {   // keys, then values of tile j2 / 2
+                const int slot = kv % STAGES, i0 = (j2 >> 1) * ROWS;
+                ok = wait_warp(&bars->kv_empty[slot], ((kv / STAGES) & 1) ^ 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    uint64_t *bar = &bars->kv_full[slot];
+                    const uint32_t dst = ring + slot * TILE_BYTES;
+                    const bool values = j2 & 1;
+                    const int head = (values ? p.v_has_heads : p.k_has_heads) ? it.kvh : 0;
+                    mbar_arrive_expect_tx(bar, TILE_BYTES);
+                    if (i0 < keys.front && i0 + ROWS > keys.front) {
+                        for (int r = 0; r < ROWS; r += PIECE) {
+                            const int key = i0 + r < keys.front ? i0 + r : i0 + r - keys.front + keys.lo;
+                            for (int half = 0; half < 2; ++half)
+                                tma_load_3d(dst + half * HALF + r * 128, values ? &p.v_piece : &p.k_piece, 64 * half, head,
+                                            it.k0 + key, bar);
+                        }
+                    } else {
+                        const int key = i0 < keys.front ? i0 : i0 - keys.front + keys.lo;
+                        for (int half = 0; half < 2; ++half)
+                            tma_load_3d(dst + half * HALF, values ? &p.v : &p.k, 64 * half, head, it.k0 + key, bar);
+                    }
+                }
+                __syncwarp();
+            }
+            if (ok) get();
         }
+        // What was begun here lands before the CTA leaves (at once without an abort).
+        if (open) mbar_wait(&bars->next_full, asked & 1, p.wait_ns);
+        for (uint32_t d = kv > STAGES ? kv - STAGES : 0; d < kv; ++d)
+            mbar_wait(&bars->kv_full[d % STAGES], (d / STAGES) & 1, p.wait_ns);
+        for (int i = 0; i < 2; ++i)
+            if (nq[i] > 0) mbar_wait(&bars->q_full[i], (nq[i] - 1) & 1, p.wait_ns);
         __syncwarp();
     } else if (warp == MMA_WARP) {
+        fewer_registers<FEW_REGISTERS>();
         if (lane == 0) {
             constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
             constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t idesc_v = idesc | (1u << 16);   // second operand contiguous in N
+            // Per query tile, in registers: every index below is a constant.
+            struct Tile {
+                uint32_t ns = 0, nq = 0;   // products S and query tiles so far
+                bool pending, any, free_o;
+            } tile0, tile1;
             bool ok = true;
-            bool pending[2] = {false, false};
-            int np[2] = {0, 0};
-            // Step j: each tile's P V of its last S, then its S of key tile j.
-            for (int j = 0; ok && j <= ntiles; ++j) {
-                const int kn = 2 * j;
-                // Every copy is waited for, also one that no row needs: its slot is reused after this step.
-                if (j < ntiles) ok = wait(&bars->kv_full[kn % STAGES], (kn / STAGES) & 1);
-                if (ok && j > 0) ok = wait(&bars->kv_full[(kn - 1) % STAGES], ((kn - 1) / STAGES) & 1);
-                for (int i = 0; ok && i < 2; ++i) {
+            uint32_t kv = 0;               // copies so far
+            for (uint32_t k = 0; ok; ++k) {
+                ok = wait(&bars->item_full[k & 1], (k >> 1) & 1);
+                if (!ok) break;
+                const Item it = bars->item[k & 1];
+                mbar_arrive(&bars->item_empty[k & 1]);
+                if (it.nq == 0) break;
+                const Work w(p, it);
+                tile0.pending = tile0.any = tile0.free_o = false;
+                tile1.pending = tile1.any = tile1.free_o = false;
+                // A tile's P V of its last S, then its S of key tile j.
+                auto advance = [&](auto which, Tile &t, int j, uint32_t kn) {
+                    constexpr int i = decltype(which)::value;
                     const uint32_t s_col = tmem + S_COL + 128 * i, o_col = tmem + O_COL + 128 * i;
-                    if (pending[i]) {
-                        const int vn = kn - 1;
-                        ok = wait(&bars->p_full[i], (np[i] - 1) & 1);
-                        if (!ok) break;
+                    if (t.pending) {
+                        const uint64_t vd = sw128_mnmajor_desc(ring + ((kn - 1) % STAGES) * TILE_BYTES, HALF);
+                        ok = wait(&bars->p_full[i], (t.ns - 1) & 1);
+                        if (ok && !t.free_o) ok = t.free_o = wait(&bars->o_empty[i], (k & 1) ^ 1);
+                        if (!ok) return;
                         tc_fence_after_sync();
-                        const uint64_t vd = sw128_mnmajor_desc(ring + (vn % STAGES) * TILE_BYTES, HALF);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            tc_mma_bf16_ta(o_col, s_col + 8 * kk, vd + 128 * kk, idesc_v, (np[i] > 1 || kk > 0) ? 1u : 0u);
-                        pending[i] = false;
+                            tc_mma_bf16_ta(o_col, s_col + 8 * kk, vd + 128 * kk, idesc_v, (t.any || kk > 0) ? 1u : 0u);
+                        t.pending = false;
+                        t.any = true;
                     }
-                    if (j < ntiles && needed(i, j)) {
-                        if (np[i] == 0) ok = wait(&bars->q_full[i], 0);
-                        if (!ok) break;
-                        tc_fence_after_sync();
+                    if (j < w.j1 && w.needed(i, j)) {
                         const uint64_t qd = sw128_kmajor_desc(base + i * TILE_BYTES);
                         const uint64_t kd = sw128_kmajor_desc(ring + (kn % STAGES) * TILE_BYTES);
+                        if (!t.any) ok = wait(&bars->q_full[i], t.nq & 1);
+                        if (!ok) return;
+                        tc_fence_after_sync();
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {
                             const uint64_t step = (kk >> 2) * (HALF >> 4) + 2 * (kk & 3);
                             tc_mma_bf16(s_col, qd + step, kd + step, idesc, kk > 0 ? 1u : 0u);
                         }
                         tc_commit(&bars->s_full[i]);
-                        pending[i] = true;
-                        ++np[i];
+                        t.pending = true;
+                        ++t.ns;
+                    }
+                };
+                for (int j = w.j0; ok && j <= w.j1; ++j) {
+                    const uint32_t kn = kv + 2 * (j - w.j0);
+                    // Every copy is waited for, also one that no row needs: its slot is reused after this step.
+                    if (j < w.j1) ok = wait(&bars->kv_full[kn % STAGES], (kn / STAGES) & 1);
+                    if (ok && j > w.j0) ok = wait(&bars->kv_full[(kn - 1) % STAGES], ((kn - 1) / STAGES) & 1);
+                    if (ok) advance(std::integral_constant<int, 0>(), tile0, j, kn);
+                    if (ok) advance(std::integral_constant<int, 1>(), tile1, j, kn);
+                    if (!ok) break;
+                    // Tile j's keys and tile j-1's values are free when all of this is done.
+                    if (j > w.j0) tc_commit(&bars->kv_empty[(kn - 1) % STAGES]);
+                    if (j < w.j1) tc_commit(&bars->kv_empty[kn % STAGES]);
+                    if (j == w.j1 - 1 || w.j0 == w.j1) {
+                        tc_commit(&bars->q_empty[0]);
+                        if (w.tokens1 > 0) tc_commit(&bars->q_empty[1]);
                     }
                 }
-                if (!ok) break;
-                // Tile j's keys and tile j-1's values are free when all of this is done.
-                if (j > 0) tc_commit(&bars->kv_empty[(kn - 1) % STAGES]);
-                if (j < ntiles) tc_commit(&bars->kv_empty[kn % STAGES]);
+                kv += 2 * (w.j1 - w.j0);
+                ++tile0.nq;
+                if (w.tokens1 > 0) ++tile1.nq;
+                // One item ahead of the results at most.
+                if (ok && !tile0.free_o) ok = wait(&bars->o_empty[0], (k & 1) ^ 1);
+                if (ok && !tile1.free_o) ok = wait(&bars->o_empty[1], (k & 1) ^ 1);
+                if (ok) {
+                    tc_commit(&bars->o_full[0]);
+                    tc_commit(&bars->o_full[1]);
+                }
             }
-            if (ok)
-                for (int i = 0; i < 2; ++i) tc_commit(&bars->o_full[i]);
             tc_commit(&bars->drain);
             mbar_wait(&bars->drain, 0, p.wait_ns);
         }
         __syncwarp();
+    } else if (warp > COPY_WARP) {
+        fewer_registers<FEW_REGISTERS>();   // completes the group of four whose registers the softmax takes
     } else {
+        more_registers<MORE_REGISTERS>();
         // ---- softmax of one query tile, one row per thread -----------------------------
         const int i = warp >> 2, row = 32 * (warp & 3) + lane;
         const int tok = row / p.group, head = row - tok * p.group;
-        const int ntok = i == 0 ? tokens0 : tokens1;
-        const bool valid = tok < ntok;
-        const int pos = (i == 0 ? pos0 : pos1) + min(tok, max(ntok - 1, 0));
-        const int last = keys.last(pos), first = keys.first(pos);
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t s_at = tmem + lanes + S_COL + 128 * i, o_at = tmem + lanes + O_COL + 128 * i;
         const float c = a.scale * LOG2E;
-        float m = -INFINITY, l = 0.0f;   // m: of the products, before c
-        int n = 0;
-        bool ok = true;
-        for (int j = 0; j < ntiles; ++j) {
-            if (!needed(i, j)) continue;
-            ok = __all_sync(FULL_MASK, wait(&bars->s_full[i], n & 1));
-            if (!ok) break;
-            tc_fence_after_sync();
-            uint32_t sr[4][32];
+        uint32_t ns = 0;
+        for (uint32_t k = 0;; ++k) {
+            if (!wait_warp(&bars->item_full[k & 1], (k >> 1) & 1)) break;
+            const Item it = bars->item[k & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->item_empty[k & 1]);
+            if (it.nq == 0) break;
+            const Work w(p, it);
+            const int ntok = i == 0 ? w.tokens0 : w.tokens1;
+            const bool valid = tok < ntok;
+            const int pos = (i == 0 ? w.pos0 : w.pos1) + min(tok, max(ntok - 1, 0));
+            const int last = w.keys.last(pos), first = w.keys.first(pos);
+            float m = -INFINITY, l = 0.0f;   // m: of the products, before c
+            bool any = false, ok = true;
+            for (int j = w.j0; j < w.j1; ++j) {
+                if (!w.needed(i, j)) continue;
+                ok = wait_warp(&bars->s_full[i], ns & 1);
+                if (!ok) break;
+                ++ns;
+                tc_fence_after_sync();
+                uint32_t sr[4][32];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) tmem_ld32(s_at + 32 * g, sr[g]);
-            tmem_ld_wait();
-            const int i0 = j * ROWS;
-            const bool open = i0 + ROWS - 1 <= last && (i0 >= first || i0 + ROWS <= keys.sink_end);
-            if (!__all_sync(FULL_MASK, open)) {
+                for (int g = 0; g < 4; ++g) tmem_ld32(s_at + 32 * g, sr[g]);
+                tmem_ld_wait();
+                const int i0 = j * ROWS;
+                const bool open = i0 + ROWS - 1 <= last && (i0 >= first || i0 + ROWS <= w.keys.sink_end);
+                if (!__all_sync(FULL_MASK, open)) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    auto below = [&](int limit) {   // bits of the numbers i0 + 32 g + bit < limit
-                        const int k = limit - (i0 + 32 * g);
-                        return k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u;
-                    };
-                    const uint32_t bits = below(last + 1) & (below(keys.sink_end) | ~below(first));
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!((bits >> e) & 1u)) sr[g][e] = 0xFF800000u;
-                }
-            }
-            // 8 chains, so that the maximum of 128 is not a chain of 128.
-            float tops[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) tops[e] = __uint_as_float(sr[0][e]);
-#pragma unroll
-            for (int e = 8; e < 128; e += 16)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float y = __uint_as_float(sr[e >> 5][(e & 31) + k]);
-                    tops[k] = e + 8 < 128 ? fmaxf(fmaxf(tops[k], y), __uint_as_float(sr[(e + 8) >> 5][((e + 8) & 31) + k]))
-                                          : fmaxf(tops[k], y);
-                }
-            const float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
-                                    fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
-            const bool move = (top - m) * c > LAZY;   // also true from -infinity to a finite maximum
-            if (__any_sync(FULL_MASK, move)) {
-                const float f = move ? exp2_approx((m - top) * c) : 1.0f;
-                if (move) m = top;
-                l *= f;
-                if (n > 0) {
-#pragma unroll 1
                     for (int g = 0; g < 4; ++g) {
-                        uint32_t o[32];
-                        tmem_ld32(o_at + 32 * g, o);
-                        tmem_ld_wait();
+                        auto below = [&](int limit) {   // bits of the numbers i0 + 32 g + bit < limit
+                            const int k = limit - (i0 + 32 * g);
+                            return k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u;
+                        };
+                        const uint32_t bits = below(last + 1) & (below(w.keys.sink_end) | ~below(first));
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(o_at + 32 * g, o);
+                        for (int e = 0; e < 32; ++e)
+                            if (!((bits >> e) & 1u)) sr[g][e] = 0xFF800000u;
                     }
                 }
-            }
-            const float mc = m == -INFINITY ? 0.0f : m * c;
-            const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
-            uint64_t sums[4] = {0, 0, 0, 0};
+                // 8 chains, so that the maximum of 128 is not a chain of 128.
+                float tops[8];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t pw[32];
+                for (int e = 0; e < 8; ++e) tops[e] = __uint_as_float(sr[0][e]);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float x0, x1;
-                    unpair(fma_pair(pair(__uint_as_float(sr[2 * g + (e >> 4)][(2 * e) & 31]),
-                                         __uint_as_float(sr[2 * g + (e >> 4)][(2 * e + 1) & 31])), c2, mc2), x0, x1);
-                    x0 = exp2_approx(x0);
-                    x1 = exp2_approx(x1);
-                    sums[e & 3] = add_pair(sums[e & 3], pair(x0, x1));
-                    pw[e] = pack2_rn<T>(x0, x1);
+                for (int e = 8; e < 128; e += 16)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float y = __uint_as_float(sr[e >> 5][(e & 31) + k]);
+                        tops[k] = e + 8 < 128 ? fmaxf(fmaxf(tops[k], y), __uint_as_float(sr[(e + 8) >> 5][((e + 8) & 31) + k]))
+                                              : fmaxf(tops[k], y);
+                    }
+                const float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                                        fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
+                const bool move = (top - m) * c > LAZY;   // also true from -infinity to a finite maximum
+                if (__any_sync(FULL_MASK, move)) {
+                    const float f = move ? exp2_approx((m - top) * c) : 1.0f;
+                    if (move) m = top;
+                    l *= f;
+                    if (any) {
+#pragma unroll 1
+                        for (int g = 0; g < 4; ++g) {
+                            uint32_t o[32];
+                            tmem_ld32(o_at + 32 * g, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(o_at + 32 * g, o);
+                        }
+                    }
                 }
-                tmem_st32(s_at + 32 * g, pw);
+                const float mc = m == -INFINITY ? 0.0f : m * c;
+                const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+                uint64_t sums[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t pw[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float x0, x1;
+                        unpair(fma_pair(pair(__uint_as_float(sr[2 * g + (e >> 4)][(2 * e) & 31]),
+                                             __uint_as_float(sr[2 * g + (e >> 4)][(2 * e + 1) & 31])), c2, mc2), x0, x1);
+                        x0 = exp2_approx(x0);
+                        x1 = exp2_approx(x1);
+                        sums[e & 3] = add_pair(sums[e & 3], pair(x0, x1));
+                        pw[e] = pack2_rn<T>(x0, x1);
+                    }
+                    tmem_st32(s_at + 32 * g, pw);
+                }
+                {
+                    float y0, y1;
+                    unpair(add_pair(add_pair(sums[0], sums[1]), add_pair(sums[2], sums[3])), y0, y1);
+                    l += y0 + y1;
+                }
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_full[i]);
+                any = true;
             }
-            {
-                float y0, y1;
-                unpair(add_pair(add_pair(sums[0], sums[1]), add_pair(sums[2], sums[3])), y0, y1);
-                l += y0 + y1;
-            }
-            tmem_st_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[i]);
-            ++n;
-        }
-        // ---- results -------------------------------------------------------------------
-        if (ok) ok = __all_sync(FULL_MASK, wait(&bars->o_full[i], 0));
-        if (ok && ntok > 0) {
+            // ---- results -------------------------------------------------------------------
+            if (!ok || !wait_warp(&bars->o_full[i], k & 1)) break;
             tc_fence_after_sync();
-            const int q_row = x.q0 + t0 + i * p.tokens + tok, h = h0 + head;
+            const int q_row = it.q0 + it.t0 + i * p.tokens + tok, h = it.kvh * p.group + head;
             const size_t out_row = static_cast<size_t>(q_row) * a.nheads + h;
             uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + out_row * 128);
+            float *slot = p.slots + (static_cast<size_t>(it.slot) * 2 * ROWS + i * ROWS + row) * SLOT_ROW;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             float odd = 0.0f;   // stays 0 while everything is finite
 #pragma unroll 1
             for (int g = 0; g < 4; ++g) {
                 uint32_t o[32];
-                if (n > 0) {
+                if (any) {
                     tmem_ld32(o_at + 32 * g, o);
                     tmem_ld_wait();
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0u;
                 }
+                if (valid && w.parts > 1) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
-                if (valid) {
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4 *>(slot + 32 * g + 4 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                } else if (valid) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        uint32_t w[4];
+                        uint32_t y[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = pack2_rn<T>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-                        out[4 * g + e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int q = 0; q < 4; ++q)
+                            y[q] = pack2_rn<T>(__uint_as_float(o[8 * e + 2 * q]) * inv, __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
+                        out[4 * g + e] = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
+                __syncwarp();
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->o_empty[i]);
+            if (w.parts > 1) {
+                if (valid) {
+                    slot[128] = m == -INFINITY ? -INFINITY : m * c;
+                    slot[129] = l;
+                }
+                continue;
             }
             if (valid && a.lse != nullptr) a.lse[out_row] = l == 0.0f ? -INFINITY : (m * c + log2f(l)) * LN2;
             uint32_t again = __ballot_sync(FULL_MASK, valid && !(odd * l == 0.0f));
@@ -481,7 +686,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                 const int from = __ffs(again) - 1;
                 again &= again - 1;
                 __syncwarp();
-                attend_row<T>(a, __shfl_sync(FULL_MASK, q_row, from), __shfl_sync(FULL_MASK, h, from), x.k0, x.nk,
+                attend_row<T>(a, __shfl_sync(FULL_MASK, q_row, from), __shfl_sync(FULL_MASK, h, from), it.k0, it.nk,
                               __shfl_sync(FULL_MASK, pos, from));
             }
         }
@@ -491,6 +696,53 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
     if (warp == MMA_WARP) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// Adds the parts of an item that was split over its keys: one warp per row.
+template <typename T>
+__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WindowParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const WindowAttnArgs &a = p.a;
+    const int lane = threadIdx.x & 31;
+    Item it;
+    if (!find_item(p, (blockIdx.x / a.nkv * p.splits) * a.nkv + blockIdx.x % a.nkv, it)) return;   // its part 0
+    const Work w(p, it);
+    if (w.parts < 2) return;
+    const int per = p.group * p.tokens;                  // rows of a tile
+    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < 2 * per; r += gridDim.y * 8) {
+        const int i = r / per, row = r - i * per, tok = row / p.group, h = it.kvh * p.group + row - tok * p.group;
+        if (tok >= (i == 0 ? w.tokens0 : w.tokens1)) continue;
+        const float *slot = p.slots + (static_cast<size_t>(it.slot) * 2 * ROWS + i * ROWS + row) * SLOT_ROW;
+        constexpr size_t NEXT = static_cast<size_t>(2 * ROWS) * SLOT_ROW;
+        float top = -INFINITY;
+        for (int z = lane; z < w.parts; z += 32) top = fmaxf(top, __ldcg(slot + z * NEXT + 128));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float l = 0.0f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int z = 0; z < w.parts; ++z) {
+            const float f = exp2_approx(__ldcg(slot + z * NEXT + 128) - ref);
+            const float4 v = ld_in(reinterpret_cast<const float4 *>(slot + z * NEXT) + lane);
+            l = fmaf(__ldcg(slot + z * NEXT + 129), f, l);
+            y.x = fmaf(v.x, f, y.x);
+            y.y = fmaf(v.y, f, y.y);
+            y.z = fmaf(v.z, f, y.z);
+            y.w = fmaf(v.w, f, y.w);
+        }
+        const int q_row = it.q0 + it.t0 + i * p.tokens + tok;
+        const size_t out_row = static_cast<size_t>(q_row) * a.nheads + h;
+        const float odd = (y.x * 0.0f + y.y * 0.0f) + (y.z * 0.0f + y.w * 0.0f);
+        if (!__all_sync(FULL_MASK, odd * l == 0.0f)) {   // the row's visible keys alone
+            attend_row<T>(a, q_row, h, it.k0, it.nk, (i == 0 ? w.pos0 : w.pos1) + tok);
+            continue;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        store4(static_cast<T *>(a.out) + out_row * 128 + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+        if (a.lse != nullptr && lane == 0) a.lse[out_row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * LN2;
     }
 }
 
@@ -512,6 +764,25 @@ bool encode_map(CUtensorMap *map, bool bf16, const void *p, int64_t heads, int64
 
 // A stride a tensor map takes (a multiple of 16 bytes below 2^40, not 0).
 bool map_stride(int64_t n, int64_t elements) { return n <= 1 || (elements > 0 && elements < (1LL << 38)); }
+
+// How the batch is cut, from what the host knows. Items are split over their
+// keys when there are fewer than two per SM, into about three per SM.
+struct Split {
+    int pairs, splits;
+};
+Split split(int nseq, int total_q, int nheads, int nkv) {
+    const int per = 2 * (ROWS / (nheads / nkv)), sms = device_sm_count();
+    const long long least = static_cast<long long>(std::max(total_q / per, std::min(nseq, total_q))) * nkv;
+    const long long parts = least >= 2LL * sms ? 1 : (3LL * sms + least - 1) / least;
+    return {total_q / per + nseq, static_cast<int>(std::min(parts, 64LL))};
+}
+// Parts of at least PART_TILES tiles that the longest item can have.
+int most_parts(const WindowAttnArgs &a, int tokens) {
+    long long keys = a.total_k;
+    if (a.window >= 0) keys = std::min(keys, static_cast<long long>(a.window) + std::min(a.sinks, a.total_k) + PIECE + 2 * tokens);
+    const long long tiles = (keys + ROWS - 1) / ROWS;
+    return static_cast<int>(std::max(1LL, std::min(64LL, (tiles + PART_TILES - 1) / PART_TILES)));
+}
 
 template <typename T>
 cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
@@ -556,17 +827,30 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
     if (a.sinks > 0 && (!encode_map(&p.k_piece, bf16, a.k, k_heads ? a.nkv : 1, a.total_k, a.k_head, a.k_tok, 1, PIECE) ||
                         !encode_map(&p.v_piece, bf16, a.v, v_heads ? a.nkv : 1, a.total_k, a.v_head, a.v_tok, 1, PIECE)))
         return cudaErrorNotSupported;
-    const long long items = (static_cast<long long>(a.max_q) + 2 * p.tokens - 1) / (2 * p.tokens) * a.nkv;
+    const Split x = split(a.nseq, a.total_q, a.nheads, a.nkv);
+    p.pairs = x.pairs;
+    p.splits = std::min(x.splits, most_parts(a, p.tokens));
+    p.slots = static_cast<float *>(a.scratch);
+    const long long items = static_cast<long long>(p.pairs) * a.nkv * p.splits;
     if (items > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3(static_cast<unsigned>(items), a.nseq);
+    cfg.gridDim = dim3(static_cast<unsigned>(items));
     cfg.blockDim = dim3(WTHREADS);
     cfg.dynamicSmemBytes = WINDOW_SMEM;
-    return cudaLaunchKernelEx(&cfg, window_kernel<T>, p);
+    e = cudaLaunchKernelEx(&cfg, window_kernel<T>, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.pairs * a.nkv), 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, window_join_kernel<T>, p);
 }
 
 }  // namespace
 
-size_t window_attn_scratch_bytes(int, int, int, int, int) { return 0; }
+size_t window_attn_scratch_bytes(int nseq, int total_q, int, int nheads, int nkv) {
+    if (nheads / nkv > ROWS) return 0;
+    const Split x = split(nseq, total_q, nheads, nkv);
+    return x.splits > 1 ? sizeof(float) * x.pairs * nkv * x.splits * 2 * ROWS * SLOT_ROW : 0;
+}
 
 cudaError_t launch_window_attn(const WindowAttnArgs &a, cudaStream_t stream) {
     return a.dtype == QSA_BF16 ? launch<__nv_bfloat16>(a, stream) : launch<__half>(a, stream);
