@@ -48,11 +48,12 @@ __device__ uint32_t g_window_error;
 constexpr int ROWS = 128;                   // rows of a query tile, keys of a key tile
 constexpr int HALF = ROWS * 128;            // bytes of 128 rows x 64 elements
 constexpr int TILE_BYTES = 2 * HALF;
-constexpr int STAGES = 5;                   // key and value tiles in flight
+constexpr int STAGES = 4;                   // key and value tiles in flight
 constexpr int PIECE = 16;                   // rows of a copy in the tile where sinks and window meet
-constexpr int MMA_WARP = 8, COPY_WARP = 9, WTHREADS = 384;
-// 168 registers a thread at launch: 8 softmax warps x 208 + 4 x 88 = 12 x 168.
-constexpr int MORE_REGISTERS = 208, FEW_REGISTERS = 88;
+constexpr int MMA_WARP = 8, COPY_WARP = 9, OUT_WARP = 12, WTHREADS = 512;
+// 128 registers a thread at launch: 8 softmax warps x 168 + 8 x 88 = 16 x 128.
+constexpr int MORE_REGISTERS = 168, FEW_REGISTERS = 88;
+constexpr int STAGING = 32 * 128;           // bytes of an output warp's staging: 128 bytes of each of its rows
 constexpr int PART_TILES = 4;               // key tiles of a part at least
 constexpr int SLOT_ROW = 132;               // 128 sums, reference, weight sum, padding
 constexpr float LAZY = 8.0f;
@@ -77,11 +78,13 @@ struct Item {
 struct WindowBarriers {
     uint4 next;             // the answer about the next item
     Item item[2];
-    uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[2], p_full[2], o_full[2], o_empty[2];
-    uint64_t item_full[2], item_empty[2], next_full, drain;
+    uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[2], p_half[2], p_full[2];
+    uint64_t o_full[2], o_empty[2], sum_full[2], sum_empty[2], item_full[2], item_empty[2], next_full, drain;
     uint32_t tmem, abort;
+    uint32_t any[2];        // whether the tile's O was written
+    float2 sum[2][ROWS];    // reference (base 2) and weight sum of each row
 };
-constexpr size_t WINDOW_SMEM = 1024 + (2 + STAGES) * static_cast<size_t>(TILE_BYTES) + sizeof(WindowBarriers);
+constexpr size_t WINDOW_SMEM = 1024 + (2 + STAGES) * static_cast<size_t>(TILE_BYTES) + 4 * STAGING + sizeof(WindowBarriers);
 static_assert(WINDOW_SMEM <= 232448, "shared memory per CTA");
 
 // The keys one query row sees: [0, sinks) and [lo, end).
@@ -298,7 +301,8 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t ring = base + 2 * TILE_BYTES;
-    WindowBarriers *bars = reinterpret_cast<WindowBarriers *>(raw + (base - smem_u32(raw)) + (2 + STAGES) * TILE_BYTES);
+    const uint32_t staging = ring + STAGES * TILE_BYTES;
+    WindowBarriers *bars = reinterpret_cast<WindowBarriers *>(raw + (staging + 4 * STAGING - smem_u32(raw)));
 
     if (warp == MMA_WARP) {
         tmem_alloc(&bars->tmem, TMEM_COLS);
@@ -308,11 +312,14 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             mbar_init(&bars->q_full[i], 1);
             mbar_init(&bars->q_empty[i], 1);
             mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_half[i], 4);
             mbar_init(&bars->p_full[i], 4);
             mbar_init(&bars->o_full[i], 1);
             mbar_init(&bars->o_empty[i], 4);
+            mbar_init(&bars->sum_full[i], 4);
+            mbar_init(&bars->sum_empty[i], 4);
             mbar_init(&bars->item_full[i], 1);
-            mbar_init(&bars->item_empty[i], 1 + 8);
+            mbar_init(&bars->item_empty[i], 1 + 8 + 4);
         }
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&bars->kv_full[i], 1);
@@ -441,7 +448,8 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
         __syncwarp();
     } else if (warp == MMA_WARP) {
         fewer_registers<FEW_REGISTERS>();
-        if (lane == 0) {
+        {
+            const bool one = elect_one();   // the warp runs as one, one lane issues
             constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
             constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t idesc_v = idesc | (1u << 16);   // second operand contiguous in N
@@ -453,10 +461,11 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             bool ok = true;
             uint32_t kv = 0;               // copies so far
             for (uint32_t k = 0; ok; ++k) {
-                ok = wait(&bars->item_full[k & 1], (k >> 1) & 1);
+                ok = wait_warp(&bars->item_full[k & 1], (k >> 1) & 1);
                 if (!ok) break;
                 const Item it = bars->item[k & 1];
-                mbar_arrive(&bars->item_empty[k & 1]);
+                __syncwarp();
+                if (one) mbar_arrive(&bars->item_empty[k & 1]);
                 if (it.nq == 0) break;
                 const Work w(p, it);
                 tile0.pending = tile0.any = tile0.free_o = false;
@@ -467,28 +476,34 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                     const uint32_t s_col = tmem + S_COL + 128 * i, o_col = tmem + O_COL + 128 * i;
                     if (t.pending) {
                         const uint64_t vd = sw128_mnmajor_desc(ring + ((kn - 1) % STAGES) * TILE_BYTES, HALF);
-                        ok = wait(&bars->p_full[i], (t.ns - 1) & 1);
-                        if (ok && !t.free_o) ok = t.free_o = wait(&bars->o_empty[i], (k & 1) ^ 1);
+                        if (!t.free_o) ok = t.free_o = wait_warp(&bars->o_empty[i], (k & 1) ^ 1);
+                        if (ok) ok = wait_warp(&bars->p_half[i], (t.ns - 1) & 1);
                         if (!ok) return;
                         tc_fence_after_sync();
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            tc_mma_bf16_ta(o_col, s_col + 8 * kk, vd + 128 * kk, idesc_v, (t.any || kk > 0) ? 1u : 0u);
+                        for (int kk = 0; kk < 4; ++kk)
+                            if (one) tc_mma_bf16_ta(o_col, s_col + 8 * kk, vd + 128 * kk, idesc_v, (t.any || kk > 0) ? 1u : 0u);
+                        ok = wait_warp(&bars->p_full[i], (t.ns - 1) & 1);
+                        if (!ok) return;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int kk = 4; kk < 8; ++kk)
+                            if (one) tc_mma_bf16_ta(o_col, s_col + 8 * kk, vd + 128 * kk, idesc_v, 1u);
                         t.pending = false;
                         t.any = true;
                     }
                     if (j < w.j1 && w.needed(i, j)) {
                         const uint64_t qd = sw128_kmajor_desc(base + i * TILE_BYTES);
                         const uint64_t kd = sw128_kmajor_desc(ring + (kn % STAGES) * TILE_BYTES);
-                        if (!t.any) ok = wait(&bars->q_full[i], t.nq & 1);
+                        if (!t.any) ok = wait_warp(&bars->q_full[i], t.nq & 1);
                         if (!ok) return;
                         tc_fence_after_sync();
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {
                             const uint64_t step = (kk >> 2) * (HALF >> 4) + 2 * (kk & 3);
-                            tc_mma_bf16(s_col, qd + step, kd + step, idesc, kk > 0 ? 1u : 0u);
+                            if (one) tc_mma_bf16(s_col, qd + step, kd + step, idesc, kk > 0 ? 1u : 0u);
                         }
-                        tc_commit(&bars->s_full[i]);
+                        if (one) tc_commit(&bars->s_full[i]);
                         t.pending = true;
                         ++t.ns;
                     }
@@ -496,41 +511,141 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                 for (int j = w.j0; ok && j <= w.j1; ++j) {
                     const uint32_t kn = kv + 2 * (j - w.j0);
                     // Every copy is waited for, also one that no row needs: its slot is reused after this step.
-                    if (j < w.j1) ok = wait(&bars->kv_full[kn % STAGES], (kn / STAGES) & 1);
-                    if (ok && j > w.j0) ok = wait(&bars->kv_full[(kn - 1) % STAGES], ((kn - 1) / STAGES) & 1);
+                    if (j < w.j1) ok = wait_warp(&bars->kv_full[kn % STAGES], (kn / STAGES) & 1);
+                    if (ok && j > w.j0) ok = wait_warp(&bars->kv_full[(kn - 1) % STAGES], ((kn - 1) / STAGES) & 1);
                     if (ok) advance(std::integral_constant<int, 0>(), tile0, j, kn);
                     if (ok) advance(std::integral_constant<int, 1>(), tile1, j, kn);
                     if (!ok) break;
                     // Tile j's keys and tile j-1's values are free when all of this is done.
-                    if (j > w.j0) tc_commit(&bars->kv_empty[(kn - 1) % STAGES]);
-                    if (j < w.j1) tc_commit(&bars->kv_empty[kn % STAGES]);
+                    if (one && j > w.j0) tc_commit(&bars->kv_empty[(kn - 1) % STAGES]);
+                    if (one && j < w.j1) tc_commit(&bars->kv_empty[kn % STAGES]);
                     if (j == w.j1 - 1 || w.j0 == w.j1) {
-                        tc_commit(&bars->q_empty[0]);
-                        if (w.tokens1 > 0) tc_commit(&bars->q_empty[1]);
+                        if (one) tc_commit(&bars->q_empty[0]);
+                        if (one && w.tokens1 > 0) tc_commit(&bars->q_empty[1]);
                     }
                 }
                 kv += 2 * (w.j1 - w.j0);
                 ++tile0.nq;
                 if (w.tokens1 > 0) ++tile1.nq;
                 // One item ahead of the results at most.
-                if (ok && !tile0.free_o) ok = wait(&bars->o_empty[0], (k & 1) ^ 1);
-                if (ok && !tile1.free_o) ok = wait(&bars->o_empty[1], (k & 1) ^ 1);
+                if (ok && !tile0.free_o) ok = wait_warp(&bars->o_empty[0], (k & 1) ^ 1);
+                if (ok && !tile1.free_o) ok = wait_warp(&bars->o_empty[1], (k & 1) ^ 1);
                 if (ok) {
-                    tc_commit(&bars->o_full[0]);
-                    tc_commit(&bars->o_full[1]);
+                    if (one) tc_commit(&bars->o_full[0]);
+                    if (one) tc_commit(&bars->o_full[1]);
                 }
             }
-            tc_commit(&bars->drain);
+            if (one) tc_commit(&bars->drain);
             mbar_wait(&bars->drain, 0, p.wait_ns);
         }
         __syncwarp();
+    } else if (warp >= OUT_WARP) {
+        fewer_registers<FEW_REGISTERS>();
+        // ---- results: rows 32 quarter .. + 31 of both tiles --------------------------------
+        const int quarter = warp & 3;
+        const uint32_t stage = staging + quarter * STAGING;
+        for (uint32_t k = 0;; ++k) {
+            if (!wait_warp(&bars->item_full[k & 1], (k >> 1) & 1)) break;
+            const Item it = bars->item[k & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->item_empty[k & 1]);
+            if (it.nq == 0) break;
+            const Work w(p, it);
+            bool ok = true;
+            for (int i = 0; i < 2; ++i) {
+                ok = wait_warp(&bars->sum_full[i], k & 1) && wait_warp(&bars->o_full[i], k & 1);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const int row = 32 * quarter + lane, tok = row / p.group, head = row - tok * p.group;
+                const int ntok = i == 0 ? w.tokens0 : w.tokens1;
+                const bool valid = tok < ntok;
+                const float2 sum = bars->sum[i][row];
+                const bool any = bars->any[i] != 0u, split = w.parts > 1;
+                const int q_row = it.q0 + it.t0 + i * p.tokens + tok, h = it.kvh * p.group + head;
+                const long long out_row = static_cast<long long>(q_row) * a.nheads + h;
+                const uint32_t rows = __ballot_sync(FULL_MASK, valid);
+                // Where this lane's row goes: 4 pieces of 128 bytes of partial sums, or 2 of results.
+                char *to = split ? reinterpret_cast<char *>(p.slots + (static_cast<size_t>(it.slot) * 2 * ROWS + i * ROWS + row) * SLOT_ROW)
+                                 : reinterpret_cast<char *>(static_cast<T *>(a.out) + out_row * 128);
+                const float inv = sum.y == 0.0f ? 0.0f : 1.0f / sum.y;
+                float odd = 0.0f;   // stays 0 while everything is finite
+                const uint32_t o_at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + O_COL + 128 * i;
+                // A piece is staged with its 16-byte chunks at chunk ^ (row % 8) and leaves as whole 128-byte rows.
+                auto leave = [&](int piece) {
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = 4 * e + (lane >> 3), chunk = lane & 7;
+                        const uint4 v = ld_shared_v4(stage + r * 128 + ((chunk ^ (r & 7)) << 4));
+                        char *dst = reinterpret_cast<char *>(__shfl_sync(FULL_MASK, reinterpret_cast<unsigned long long>(to), r));
+                        if ((rows >> r) & 1u) *reinterpret_cast<uint4 *>(dst + 128 * piece + 16 * chunk) = v;
+                    }
+                    __syncwarp();
+                };
+                auto put = [&](int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
+                    st_shared_v4(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4), x, y, z, u);
+                };
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    if (any) {
+                        tmem_ld32(o_at + 32 * g, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    }
+                    if (g == 3) {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bars->o_empty[i]);
+                            mbar_arrive(&bars->sum_empty[i]);
+                        }
+                    }
+                    if (split) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) put(e, o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        leave(g);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                y[q] = pack2_rn<T>(__uint_as_float(o[8 * e + 2 * q]) * inv, __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
+                            put(4 * (g & 1) + e, y[0], y[1], y[2], y[3]);
+                        }
+                        if (g & 1) leave(g >> 1);
+                    }
+                }
+                if (split) {
+                    if (valid) *reinterpret_cast<float2 *>(to + 512) = sum;
+                    continue;
+                }
+                if (valid && a.lse != nullptr) a.lse[out_row] = sum.y == 0.0f ? -INFINITY : (sum.x + log2f(sum.y)) * LN2;
+                uint32_t again = __ballot_sync(FULL_MASK, valid && !(odd * sum.y == 0.0f));
+                const int pos = (i == 0 ? w.pos0 : w.pos1) + tok;
+                while (again != 0u) {   // the row's visible keys alone
+                    const int from = __ffs(again) - 1;
+                    again &= again - 1;
+                    __syncwarp();
+                    attend_row<T>(a, __shfl_sync(FULL_MASK, q_row, from), __shfl_sync(FULL_MASK, h, from), it.k0, it.nk,
+                                  __shfl_sync(FULL_MASK, pos, from));
+                }
+            }
+            if (!ok) break;
+        }
     } else if (warp > COPY_WARP) {
         fewer_registers<FEW_REGISTERS>();   // completes the group of four whose registers the softmax takes
     } else {
         more_registers<MORE_REGISTERS>();
         // ---- softmax of one query tile, one row per thread -----------------------------
         const int i = warp >> 2, row = 32 * (warp & 3) + lane;
-        const int tok = row / p.group, head = row - tok * p.group;
+        const int tok = row / p.group;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t s_at = tmem + lanes + S_COL + 128 * i, o_at = tmem + lanes + O_COL + 128 * i;
         const float c = a.scale * LOG2E;
@@ -543,13 +658,13 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             if (it.nq == 0) break;
             const Work w(p, it);
             const int ntok = i == 0 ? w.tokens0 : w.tokens1;
-            const bool valid = tok < ntok;
             const int pos = (i == 0 ? w.pos0 : w.pos1) + min(tok, max(ntok - 1, 0));
-            const int last = w.keys.last(pos), first = w.keys.first(pos);
+            const int last = w.keys.last(pos), first = w.keys.first(pos), sink_end = w.keys.sink_end, j1 = w.j1;
+            const int tile_last = i == 0 ? w.last0 : w.last1, tile_first = i == 0 ? w.first0 : w.first1;
             float m = -INFINITY, l = 0.0f;   // m: of the products, before c
             bool any = false, ok = true;
-            for (int j = w.j0; j < w.j1; ++j) {
-                if (!w.needed(i, j)) continue;
+            for (int i0 = w.j0 * ROWS; i0 < j1 * ROWS; i0 += ROWS) {
+                if (!(i0 <= tile_last && (i0 < sink_end || i0 + ROWS - 1 >= tile_first))) continue;
                 ok = wait_warp(&bars->s_full[i], ns & 1);
                 if (!ok) break;
                 ++ns;
@@ -558,8 +673,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
 #pragma unroll
                 for (int g = 0; g < 4; ++g) tmem_ld32(s_at + 32 * g, sr[g]);
                 tmem_ld_wait();
-                const int i0 = j * ROWS;
-                const bool open = i0 + ROWS - 1 <= last && (i0 >= first || i0 + ROWS <= w.keys.sink_end);
+                const bool open = i0 + ROWS - 1 <= last && (i0 >= first || i0 + ROWS <= sink_end);
                 if (!__all_sync(FULL_MASK, open)) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
@@ -567,12 +681,30 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                             const int k = limit - (i0 + 32 * g);
                             return k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u;
                         };
-                        const uint32_t bits = below(last + 1) & (below(w.keys.sink_end) | ~below(first));
+                        const uint32_t bits = below(last + 1) & (below(sink_end) | ~below(first));
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!((bits >> e) & 1u)) sr[g][e] = 0xFF800000u;
                     }
                 }
+                // Weights of 32 columns against the reference as it stands, so that they need not
+                // wait for the maximum of this tile, which rarely moves it.
+                uint64_t sums[2];
+                uint32_t pw[16];
+                auto weights = [&](int g) {
+                    const float mc = m == -INFINITY ? 0.0f : m * c;
+                    const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float x0, x1;
+                        unpair(fma_pair(pair(__uint_as_float(sr[g][2 * e]), __uint_as_float(sr[g][2 * e + 1])), c2, mc2), x0, x1);
+                        x0 = exp2_approx(x0);
+                        x1 = exp2_approx(x1);
+                        sums[e & 1] = g == 0 && e < 2 ? pair(x0, x1) : add_pair(sums[e & 1], pair(x0, x1));
+                        pw[e] = pack2_rn<T>(x0, x1);
+                    }
+                };
+                weights(0);
                 // 8 chains, so that the maximum of 128 is not a chain of 128.
                 float tops[8];
 #pragma unroll
@@ -594,101 +726,41 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                     l *= f;
                     if (any) {
 #pragma unroll 1
-                        for (int g = 0; g < 4; ++g) {
-                            uint32_t o[32];
-                            tmem_ld32(o_at + 32 * g, o);
+                        for (int g = 0; g < 8; ++g) {
+                            uint32_t o[16];
+                            tmem_ld16(o_at + 16 * g, o);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st32(o_at + 32 * g, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(o_at + 16 * g, o);
                         }
                     }
+                    weights(0);
                 }
-                const float mc = m == -INFINITY ? 0.0f : m * c;
-                const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
-                uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t pw[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float x0, x1;
-                        unpair(fma_pair(pair(__uint_as_float(sr[2 * g + (e >> 4)][(2 * e) & 31]),
-                                             __uint_as_float(sr[2 * g + (e >> 4)][(2 * e + 1) & 31])), c2, mc2), x0, x1);
-                        x0 = exp2_approx(x0);
-                        x1 = exp2_approx(x1);
-                        sums[e & 3] = add_pair(sums[e & 3], pair(x0, x1));
-                        pw[e] = pack2_rn<T>(x0, x1);
+                for (int g = 0; g < 4; ++g) {
+                    if (g > 0) weights(g);
+                    tmem_st16(s_at + 16 * g, pw);
+                    if (g & 1) {   // the products with half of the values can begin
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(g == 1 ? &bars->p_half[i] : &bars->p_full[i]);
                     }
-                    tmem_st32(s_at + 32 * g, pw);
                 }
                 {
                     float y0, y1;
-                    unpair(add_pair(add_pair(sums[0], sums[1]), add_pair(sums[2], sums[3])), y0, y1);
+                    unpair(add_pair(sums[0], sums[1]), y0, y1);
                     l += y0 + y1;
                 }
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_full[i]);
                 any = true;
             }
-            // ---- results -------------------------------------------------------------------
-            if (!ok || !wait_warp(&bars->o_full[i], k & 1)) break;
-            tc_fence_after_sync();
-            const int q_row = it.q0 + it.t0 + i * p.tokens + tok, h = it.kvh * p.group + head;
-            const size_t out_row = static_cast<size_t>(q_row) * a.nheads + h;
-            uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + out_row * 128);
-            float *slot = p.slots + (static_cast<size_t>(it.slot) * 2 * ROWS + i * ROWS + row) * SLOT_ROW;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            float odd = 0.0f;   // stays 0 while everything is finite
-#pragma unroll 1
-            for (int g = 0; g < 4; ++g) {
-                uint32_t o[32];
-                if (any) {
-                    tmem_ld32(o_at + 32 * g, o);
-                    tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
-                }
-                if (valid && w.parts > 1) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        *reinterpret_cast<uint4 *>(slot + 32 * g + 4 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else if (valid) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            y[q] = pack2_rn<T>(__uint_as_float(o[8 * e + 2 * q]) * inv, __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
-                        out[4 * g + e] = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
-                }
-                __syncwarp();
-            }
-            tc_fence_before_sync();
+            // The output warps take over; they are done with the last item's sums long since.
+            if (!ok || !wait_warp(&bars->sum_empty[i], (k & 1) ^ 1)) break;
+            bars->sum[i][row] = make_float2(m == -INFINITY ? -INFINITY : m * c, l);
+            if (row == 0) bars->any[i] = any;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->o_empty[i]);
-            if (w.parts > 1) {
-                if (valid) {
-                    slot[128] = m == -INFINITY ? -INFINITY : m * c;
-                    slot[129] = l;
-                }
-                continue;
-            }
-            if (valid && a.lse != nullptr) a.lse[out_row] = l == 0.0f ? -INFINITY : (m * c + log2f(l)) * LN2;
-            uint32_t again = __ballot_sync(FULL_MASK, valid && !(odd * l == 0.0f));
-            while (again != 0u) {   // the row's visible keys alone
-                const int from = __ffs(again) - 1;
-                again &= again - 1;
-                __syncwarp();
-                attend_row<T>(a, __shfl_sync(FULL_MASK, q_row, from), __shfl_sync(FULL_MASK, h, from), it.k0, it.nk,
-                              __shfl_sync(FULL_MASK, pos, from));
-            }
+            if (lane == 0) mbar_arrive(&bars->sum_full[i]);
         }
     }
     tc_fence_before_sync();
