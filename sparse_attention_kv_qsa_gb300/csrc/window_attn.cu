@@ -69,24 +69,6 @@ struct WindowParams {
     uint64_t wait_ns;
 };
 
-// A work item: two query tiles of one sequence and KV head, and (when items
-// are split over their keys) one part of their key tiles.
-struct Item {
-    int q0, nq, k0, nk, t0, kvh, part, slot;   // t0: first token; slot: of the partial results
-};
-
-struct WindowBarriers {
-    uint4 next;             // the answer about the next item
-    Item item[2];
-    uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[2], p_half[2], p_full[2];
-    uint64_t o_full[2], o_empty[2], sum_full[2], sum_empty[2], item_full[2], item_empty[2], next_full, drain;
-    uint32_t tmem, abort;
-    uint32_t any[2];        // whether the tile's O was written
-    float2 sum[2][ROWS];    // reference (base 2) and weight sum of each row
-};
-constexpr size_t WINDOW_SMEM = 1024 + (2 + STAGES) * static_cast<size_t>(TILE_BYTES) + 4 * STAGING + sizeof(WindowBarriers);
-static_assert(WINDOW_SMEM <= 232448, "shared memory per CTA");
-
 // The keys one query row sees: [0, sinks) and [lo, end).
 struct RowKeys {
     int sinks, lo, end;
@@ -146,9 +128,9 @@ __global__ void __launch_bounds__(256) window_rows_kernel(const WindowAttnArgs a
 struct ItemKeys {
     int front, lo, count;
     int sink_end;            // numbers below it are sinks of every row
-    int window, nk;
-    __device__ __forceinline__ ItemKeys(const WindowAttnArgs &a, int nk_, int pos_first, int pos_last) {
-        nk = nk_;
+    int window;
+    ItemKeys() = default;
+    __device__ __forceinline__ ItemKeys(const WindowAttnArgs &a, int nk, int pos_first, int pos_last) {
         window = a.window < 0 || a.window > nk ? nk : a.window;
         lo = max(0, pos_first + 1 - window);
         const int sinks = min(a.sinks, nk);
@@ -207,6 +189,51 @@ __device__ __forceinline__ uint32_t pack2_rn<__half>(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// A work item: two query tiles of one sequence and KV head, and (when items
+// are split over their keys) one part of their key tiles.
+struct Item {
+    int q0, nq, k0, nk, t0, kvh, part, slot;   // t0: first token; slot: of the partial results
+};
+
+// What all roles need of an item, worked out once by the copying warp.
+struct Work {
+    Item it;
+    int tokens0, tokens1, pos0, pos1;   // tokens and first row of the two tiles
+    ItemKeys keys;
+    int last0, first0, last1, first1;   // limits of the tiles' last and first rows
+    int parts, j0, j1;                  // parts that have key tiles (at least 1), this part's tiles
+    Work() = default;
+    __device__ __forceinline__ Work(const WindowParams &p, const Item &it)
+        : it(it), tokens0(min(p.tokens, it.nq - it.t0)), tokens1(min(p.tokens, max(0, it.nq - it.t0 - p.tokens))),
+          pos0(it.nk - it.nq + it.t0), pos1(pos0 + p.tokens), keys(p.a, it.nk, pos0, pos0 + tokens0 + tokens1 - 1) {
+        last0 = keys.last(pos0 + tokens0 - 1);
+        first0 = keys.first(pos0);
+        last1 = tokens1 > 0 ? keys.last(pos1 + tokens1 - 1) : -1;
+        first1 = keys.first(pos1);
+        const int n = keys.tiles(), each = max((n + p.splits - 1) / p.splits, PART_TILES);
+        parts = max(1, (n + each - 1) / each);
+        j0 = min(it.part * each, n);
+        j1 = min(j0 + each, n);
+    }
+    // Does any row of query tile i see a key of key tile j?
+    __device__ __forceinline__ bool needed(int i, int j) const {
+        const int n = j * ROWS;
+        return n <= (i == 0 ? last0 : last1) && (n < keys.sink_end || n + ROWS - 1 >= (i == 0 ? first0 : first1));
+    }
+};
+
+struct WindowBarriers {
+    uint4 next;             // the answer about the next item
+    Work work[2];
+    uint64_t q_full[2], q_empty[2], kv_full[STAGES], kv_empty[STAGES], s_full[2], p_half[2], p_full[2];
+    uint64_t o_full[2], o_empty[2], sum_full[2], sum_empty[2], item_full[2], item_empty[2], next_full, drain;
+    uint32_t tmem, abort;
+    uint32_t any[2];        // whether the tile's O was written
+    float2 sum[2][ROWS];    // reference (base 2) and weight sum of each row
+};
+constexpr size_t WINDOW_SMEM = 1024 + (2 + STAGES) * static_cast<size_t>(TILE_BYTES) + 4 * STAGING + sizeof(WindowBarriers);
+static_assert(WINDOW_SMEM <= 232448, "shared memory per CTA");
+
 // The item number `n` of the grid, found by a whole warp; false when there is
 // nothing to do. Query tiles pairs are numbered over the batch without
 // knowing the lengths: sequence s begins at cu_q[s] / (tokens per pair) + s.
@@ -236,31 +263,6 @@ __device__ __forceinline__ bool find_item(const WindowParams &p, uint32_t n, Ite
     it.slot = (g * a.nkv + it.kvh) * p.splits + it.part;
     return true;
 }
-
-// What all roles derive from an item.
-struct Work {
-    int tokens0, tokens1, pos0, pos1;   // tokens and first row of the two tiles
-    ItemKeys keys;
-    int last0, first0, last1, first1;   // limits of the tiles' last and first rows
-    int parts, j0, j1;                  // parts that have key tiles (at least 1), this part's tiles
-    __device__ __forceinline__ Work(const WindowParams &p, const Item &it)
-        : tokens0(min(p.tokens, it.nq - it.t0)), tokens1(min(p.tokens, max(0, it.nq - it.t0 - p.tokens))),
-          pos0(it.nk - it.nq + it.t0), pos1(pos0 + p.tokens), keys(p.a, it.nk, pos0, pos0 + tokens0 + tokens1 - 1) {
-        last0 = keys.last(pos0 + tokens0 - 1);
-        first0 = keys.first(pos0);
-        last1 = tokens1 > 0 ? keys.last(pos1 + tokens1 - 1) : -1;
-        first1 = keys.first(pos1);
-        const int n = keys.tiles(), each = max((n + p.splits - 1) / p.splits, PART_TILES);
-        parts = max(1, (n + each - 1) / each);
-        j0 = min(it.part * each, n);
-        j1 = min(j0 + each, n);
-    }
-    // Does any row of query tile i see a key of key tile j?
-    __device__ __forceinline__ bool needed(int i, int j) const {
-        const int n = j * ROWS;
-        return n <= (i == 0 ? last0 : last1) && (n < keys.sink_end || n + ROWS - 1 >= (i == 0 ? first0 : first1));
-    }
-};
 
 // Asks for the index of a CTA of this grid that has not started, which then
 // never starts: the 16-byte answer completes on `bar`.
@@ -376,12 +378,13 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             __syncwarp();
         };
         for (uint32_t k = 0; ok; ++k) {
-            Item it;
+            Work w;
             bool found = false;
             while (ok && more && !found) {
+                Item it;
                 found = find_item(p, n, it);
                 if (found) {
-                    const Work w(p, it);
+                    w = Work(p, it);
                     found = it.part < w.parts;
                 }
                 if (!found) {
@@ -391,14 +394,14 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             }
             if (!ok || !wait_warp(&bars->item_empty[k & 1], ((k >> 1) & 1) ^ 1)) break;
             if (lane == 0) {
-                if (!found) it.nq = 0;       // the end
-                bars->item[k & 1] = it;
+                if (!found) w.tokens0 = 0;   // the end
+                bars->work[k & 1] = w;
                 mbar_arrive(&bars->item_full[k & 1]);
             }
             __syncwarp();
             if (!found) break;
             ask();
-            const Work w(p, it);
+            const Item &it = w.it;
             for (int i = 0; ok && i < (w.tokens1 > 0 ? 2 : 1); ++i, __syncwarp()) {
                 ok = wait_warp(&bars->q_empty[i], (nq[i] & 1) ^ 1);
                 if (ok && nq[i] > 0) ok = wait_warp(&bars->q_full[i], (nq[i] - 1) & 1);   // landed, needed or not
@@ -463,11 +466,10 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             for (uint32_t k = 0; ok; ++k) {
                 ok = wait_warp(&bars->item_full[k & 1], (k >> 1) & 1);
                 if (!ok) break;
-                const Item it = bars->item[k & 1];
+                const Work w = bars->work[k & 1];
                 __syncwarp();
                 if (one) mbar_arrive(&bars->item_empty[k & 1]);
-                if (it.nq == 0) break;
-                const Work w(p, it);
+                if (w.tokens0 == 0) break;
                 tile0.pending = tile0.any = tile0.free_o = false;
                 tile1.pending = tile1.any = tile1.free_o = false;
                 // A tile's P V of its last S, then its S of key tile j.
@@ -546,11 +548,11 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
         const uint32_t stage = staging + quarter * STAGING;
         for (uint32_t k = 0;; ++k) {
             if (!wait_warp(&bars->item_full[k & 1], (k >> 1) & 1)) break;
-            const Item it = bars->item[k & 1];
+            const Work w = bars->work[k & 1];
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->item_empty[k & 1]);
-            if (it.nq == 0) break;
-            const Work w(p, it);
+            if (w.tokens0 == 0) break;
+            const Item &it = w.it;
             bool ok = true;
             for (int i = 0; i < 2; ++i) {
                 ok = wait_warp(&bars->sum_full[i], k & 1) && wait_warp(&bars->o_full[i], k & 1);
@@ -652,15 +654,16 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
         uint32_t ns = 0;
         for (uint32_t k = 0;; ++k) {
             if (!wait_warp(&bars->item_full[k & 1], (k >> 1) & 1)) break;
-            const Item it = bars->item[k & 1];
+            const Work w = bars->work[k & 1];
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->item_empty[k & 1]);
-            if (it.nq == 0) break;
-            const Work w(p, it);
+            if (w.tokens0 == 0) break;
             const int ntok = i == 0 ? w.tokens0 : w.tokens1;
             const int pos = (i == 0 ? w.pos0 : w.pos1) + min(tok, max(ntok - 1, 0));
             const int last = w.keys.last(pos), first = w.keys.first(pos), sink_end = w.keys.sink_end, j1 = w.j1;
             const int tile_last = i == 0 ? w.last0 : w.last1, tile_first = i == 0 ? w.first0 : w.first1;
+            // The warp's rows stand in order, so lane 0 sees the least far and lane 31 begins last.
+            const int last_min = __shfl_sync(FULL_MASK, last, 0), first_max = __shfl_sync(FULL_MASK, first, 31);
             float m = -INFINITY, l = 0.0f;   // m: of the products, before c
             bool any = false, ok = true;
             for (int i0 = w.j0 * ROWS; i0 < j1 * ROWS; i0 += ROWS) {
@@ -673,12 +676,14 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
 #pragma unroll
                 for (int g = 0; g < 4; ++g) tmem_ld32(s_at + 32 * g, sr[g]);
                 tmem_ld_wait();
-                const bool open = i0 + ROWS - 1 <= last && (i0 >= first || i0 + ROWS <= sink_end);
-                if (!__all_sync(FULL_MASK, open)) {
+                if (i0 + ROWS - 1 > last_min || (i0 < first_max && i0 + ROWS > sink_end)) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        auto below = [&](int limit) {   // bits of the numbers i0 + 32 g + bit < limit
-                            const int k = limit - (i0 + 32 * g);
+                        // Numbers n0 .. n0 + 31: mostly all of them are visible to the warp's rows, or none.
+                        const int n0 = i0 + 32 * g;
+                        if (n0 + 31 <= last_min && (n0 >= first_max || n0 + 32 <= sink_end)) continue;
+                        auto below = [&](int limit) {   // bits of the numbers below the limit
+                            const int k = limit - n0;
                             return k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u;
                         };
                         const uint32_t bits = below(last + 1) & (below(sink_end) | ~below(first));
@@ -704,7 +709,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                         pw[e] = pack2_rn<T>(x0, x1);
                     }
                 };
-                weights(0);
+                if (any) weights(0);
                 // 8 chains, so that the maximum of 128 is not a chain of 128.
                 float tops[8];
 #pragma unroll
@@ -720,7 +725,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                 const float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
                                         fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
                 const bool move = (top - m) * c > LAZY;   // also true from -infinity to a finite maximum
-                if (__any_sync(FULL_MASK, move)) {
+                if (__any_sync(FULL_MASK, move) || !any) {
                     const float f = move ? exp2_approx((m - top) * c) : 1.0f;
                     if (move) m = top;
                     l *= f;
