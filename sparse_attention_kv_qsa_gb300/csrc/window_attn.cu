@@ -66,6 +66,7 @@ struct WindowParams {
     int k_has_heads, v_has_heads;   // 0: all KV heads at one address
     int pairs, splits;      // pairs of query tiles of the batch; parts that an item's keys are split into at most
     float *slots;           // [pairs][nkv][splits][2 x 128 rows][SLOT_ROW]
+    struct Work *split_work;   // [pairs][nkv]: for the join, when splits > 1
     uint64_t wait_ns;
 };
 
@@ -258,10 +259,9 @@ __device__ __forceinline__ bool find_item(const WindowParams &p, uint32_t n, Ite
     it.k0 = x.k0;
     it.nk = x.nk;
     const long long t0 = static_cast<long long>(g - (x.q0 / per + lo)) * per;
-    if (t0 < 0 || t0 >= x.nq) return false;
-    it.t0 = static_cast<int>(t0);
+    it.t0 = static_cast<int>(max(0LL, min(t0, static_cast<long long>(x.nq))));
     it.slot = (g * a.nkv + it.kvh) * p.splits + it.part;
-    return true;
+    return t0 >= 0 && t0 < x.nq;
 }
 
 // Asks for the index of a CTA of this grid that has not started, which then
@@ -383,10 +383,11 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             while (ok && more && !found) {
                 Item it;
                 found = find_item(p, n, it);
-                if (found) {
-                    w = Work(p, it);
-                    found = it.part < w.parts;
-                }
+                w = Work(p, it);
+                if (!found) w.parts = 0;
+                if (p.splits > 1 && it.part == 0 && lane == 0)   // tell the join
+                    p.split_work[n / (a.nkv * p.splits) * a.nkv + it.kvh] = w;
+                found = found && it.part < w.parts;
                 if (!found) {
                     ask();
                     get();
@@ -776,50 +777,70 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
     }
 }
 
-// Adds the parts of an item that was split over its keys: one warp per row.
+// Adds the parts of an item that was split over its keys, in their order: a
+// warp takes JOIN_ROWS rows at once, whose loads are under way together.
+constexpr int JOIN_ROWS = 4, JOIN_BLOCKS = 2 * ROWS / (8 * JOIN_ROWS);
 template <typename T>
 __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WindowParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
     const WindowAttnArgs &a = p.a;
     const int lane = threadIdx.x & 31;
-    Item it;
-    if (!find_item(p, (blockIdx.x / a.nkv * p.splits) * a.nkv + blockIdx.x % a.nkv, it)) return;   // its part 0
-    const Work w(p, it);
+    __shared__ Work w;
+    if (threadIdx.x < sizeof(Work) / 4)
+        reinterpret_cast<int *>(&w)[threadIdx.x] = ld_in(reinterpret_cast<const int *>(p.split_work + blockIdx.x) + threadIdx.x);
+    __syncthreads();
     if (w.parts < 2) return;
-    const int per = p.group * p.tokens;                  // rows of a tile
-    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < 2 * per; r += gridDim.y * 8) {
-        const int i = r / per, row = r - i * per, tok = row / p.group, h = it.kvh * p.group + row - tok * p.group;
-        if (tok >= (i == 0 ? w.tokens0 : w.tokens1)) continue;
-        const float *slot = p.slots + (static_cast<size_t>(it.slot) * 2 * ROWS + i * ROWS + row) * SLOT_ROW;
-        constexpr size_t NEXT = static_cast<size_t>(2 * ROWS) * SLOT_ROW;
-        float top = -INFINITY;
-        for (int z = lane; z < w.parts; z += 32) top = fmaxf(top, __ldcg(slot + z * NEXT + 128));
+    constexpr size_t NEXT = static_cast<size_t>(2 * ROWS) * SLOT_ROW;
+    const int first = (blockIdx.y * 8 + (threadIdx.x >> 5)) * JOIN_ROWS;   // of the 256 rows of both tiles
+    const float *slot = p.slots + (static_cast<size_t>(w.it.slot) * 2 * ROWS + first) * SLOT_ROW;
+    float ref[JOIN_ROWS], l[JOIN_ROWS];
+    float4 y[JOIN_ROWS];
+    bool valid[JOIN_ROWS];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
-        const float ref = top == -INFINITY ? 0.0f : top;
-        float l = 0.0f;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int z = 0; z < w.parts; ++z) {
-            const float f = exp2_approx(__ldcg(slot + z * NEXT + 128) - ref);
-            const float4 v = ld_in(reinterpret_cast<const float4 *>(slot + z * NEXT) + lane);
-            l = fmaf(__ldcg(slot + z * NEXT + 129), f, l);
-            y.x = fmaf(v.x, f, y.x);
-            y.y = fmaf(v.y, f, y.y);
-            y.z = fmaf(v.z, f, y.z);
-            y.w = fmaf(v.w, f, y.w);
+    for (int r = 0; r < JOIN_ROWS; ++r) {
+        const int i = (first + r) / ROWS;
+        valid[r] = (first + r) % ROWS / p.group < (i == 0 ? w.tokens0 : w.tokens1);
+        ref[r] = -INFINITY;
+        l[r] = 0.0f;
+        y[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int z = lane; valid[r] && z < w.parts; z += 32) ref[r] = fmaxf(ref[r], __ldcg(slot + z * NEXT + r * SLOT_ROW + 128));
+    }
+#pragma unroll
+    for (int r = 0; r < JOIN_ROWS; ++r)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ref[r] = fmaxf(ref[r], __shfl_xor_sync(FULL_MASK, ref[r], o));
+#pragma unroll 2
+    for (int z = 0; z < w.parts; ++z) {
+#pragma unroll
+        for (int r = 0; r < JOIN_ROWS; ++r) {
+            if (!valid[r]) continue;
+            const float *sp = slot + z * NEXT + r * SLOT_ROW;
+            const float2 m = __ldcg(reinterpret_cast<const float2 *>(sp + 128));
+            const float4 v = ld_in(reinterpret_cast<const float4 *>(sp) + lane);
+            const float f = exp2_approx(m.x - (ref[r] == -INFINITY ? 0.0f : ref[r]));
+            l[r] = fmaf(m.y, f, l[r]);
+            y[r].x = fmaf(v.x, f, y[r].x);
+            y[r].y = fmaf(v.y, f, y[r].y);
+            y[r].z = fmaf(v.z, f, y[r].z);
+            y[r].w = fmaf(v.w, f, y[r].w);
         }
-        const int q_row = it.q0 + it.t0 + i * p.tokens + tok;
-        const size_t out_row = static_cast<size_t>(q_row) * a.nheads + h;
-        const float odd = (y.x * 0.0f + y.y * 0.0f) + (y.z * 0.0f + y.w * 0.0f);
-        if (!__all_sync(FULL_MASK, odd * l == 0.0f)) {   // the row's visible keys alone
-            attend_row<T>(a, q_row, h, it.k0, it.nk, (i == 0 ? w.pos0 : w.pos1) + tok);
+    }
+#pragma unroll
+    for (int r = 0; r < JOIN_ROWS; ++r) {
+        if (!valid[r]) continue;
+        const int i = (first + r) / ROWS, row = (first + r) % ROWS, tok = row / p.group;
+        const int h = w.it.kvh * p.group + row - tok * p.group, q_row = w.it.q0 + w.it.t0 + i * p.tokens + tok;
+        const float odd = (y[r].x * 0.0f + y[r].y * 0.0f) + (y[r].z * 0.0f + y[r].w * 0.0f);
+        if (!__all_sync(FULL_MASK, odd * l[r] == 0.0f)) {   // the row's visible keys alone
+            attend_row<T>(a, q_row, h, w.it.k0, w.it.nk, (i == 0 ? w.pos0 : w.pos1) + tok);
             continue;
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        store4(static_cast<T *>(a.out) + out_row * 128 + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-        if (a.lse != nullptr && lane == 0) a.lse[out_row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * LN2;
+        const size_t out_row = static_cast<size_t>(q_row) * a.nheads + h;
+        const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
+        store4(static_cast<T *>(a.out) + out_row * 128 + 4 * lane,
+               make_float4(y[r].x * inv, y[r].y * inv, y[r].z * inv, y[r].w * inv));
+        if (a.lse != nullptr && lane == 0) a.lse[out_row] = l[r] == 0.0f ? -INFINITY : (ref[r] + log2f(l[r])) * LN2;
     }
 }
 
@@ -853,6 +874,7 @@ Split split(int nseq, int total_q, int nheads, int nkv) {
     const long long parts = least >= 2LL * sms ? 1 : (3LL * sms + least - 1) / least;
     return {total_q / per + nseq, static_cast<int>(std::min(parts, 64LL))};
 }
+size_t work_bytes(int pairs, int nkv) { return (sizeof(Work) * static_cast<size_t>(pairs) * nkv + 15) / 16 * 16; }
 // Parts of at least PART_TILES tiles that the longest item can have.
 int most_parts(const WindowAttnArgs &a, int tokens) {
     long long keys = a.total_k;
@@ -907,7 +929,8 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
     const Split x = split(a.nseq, a.total_q, a.nheads, a.nkv);
     p.pairs = x.pairs;
     p.splits = std::min(x.splits, most_parts(a, p.tokens));
-    p.slots = static_cast<float *>(a.scratch);
+    p.split_work = static_cast<Work *>(a.scratch);
+    p.slots = reinterpret_cast<float *>(static_cast<char *>(a.scratch) + work_bytes(p.pairs, a.nkv));
     const long long items = static_cast<long long>(p.pairs) * a.nkv * p.splits;
     if (items > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     cfg.gridDim = dim3(static_cast<unsigned>(items));
@@ -915,7 +938,7 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
     cfg.dynamicSmemBytes = WINDOW_SMEM;
     e = cudaLaunchKernelEx(&cfg, window_kernel<T>, p);
     if (e != cudaSuccess || p.splits == 1) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(p.pairs * a.nkv), 8);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.pairs * a.nkv), JOIN_BLOCKS);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, window_join_kernel<T>, p);
@@ -926,7 +949,7 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
 size_t window_attn_scratch_bytes(int nseq, int total_q, int, int nheads, int nkv) {
     if (nheads / nkv > ROWS) return 0;
     const Split x = split(nseq, total_q, nheads, nkv);
-    return x.splits > 1 ? sizeof(float) * x.pairs * nkv * x.splits * 2 * ROWS * SLOT_ROW : 0;
+    return x.splits > 1 ? work_bytes(x.pairs, nkv) + sizeof(float) * x.pairs * nkv * x.splits * 2 * ROWS * SLOT_ROW : 0;
 }
 
 cudaError_t launch_window_attn(const WindowAttnArgs &a, cudaStream_t stream) {
