@@ -459,80 +459,100 @@ def block_summary(k_cells: torch.Tensor, k_scale_f16: torch.Tensor, block_begin:
 
 
 _DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.int8: I8}
+_PAGE_TYPES = (torch.bfloat16, torch.float16, torch.int8)
+_Q_TYPES = (torch.bfloat16, torch.float16, torch.float32)
+_FLOAT, _INT, _BYTE = (torch.float32,), (torch.int32,), (torch.uint8,)
+_Strides6 = ctypes.c_int64 * 6
+# The current stream's handle by device index (torch.cuda.current_stream builds a Stream object around it).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _tensor(t: torch.Tensor, name: str, dtypes: tuple, ndim: int, device: torch.device) -> None:
-    """A CUDA tensor on `device` of one of `dtypes` and `ndim` dimensions, unit stride in the last."""
+def _tensor(t: torch.Tensor, name: str, dtypes: tuple, ndim: int, index: int) -> tuple[int, ...]:
+    """Checks for a CUDA tensor on device `index` of one of `dtypes` and `ndim` dimensions, contiguous in the
+    last; returns its strides."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    st = t.stride()
+    if len(st) != ndim or (st[-1] != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be a {ndim}-d tensor, contiguous in its last dimension")
+    return st
 
 
-def _strides(t: torch.Tensor, n: int) -> tuple[int, ...]:
-    """The first n strides; 0 for a dimension of one element (torch leaves that one arbitrary)."""
-    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(n))
+def _rows(t: torch.Tensor, st: tuple[int, ...]) -> int:
+    """Row stride of a 2-d tensor (the stride of a dimension of one element is arbitrary in torch)."""
+    n = t.shape
+    return st[0] if n[0] > 1 else n[1]
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _outer2(t: torch.Tensor, st: tuple[int, ...]) -> tuple[int, int]:
+    n = t.shape
+    return (st[0] if n[0] > 1 else 0), (st[1] if n[1] > 1 else 0)
 
 
-def _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16) -> KVPages:
+def _outer3(t: torch.Tensor, st: tuple[int, ...]) -> tuple[int, int, int]:
+    n = t.shape
+    return (st[0] if n[0] > 1 else 0), (st[1] if n[1] > 1 else 0), (st[2] if n[2] > 1 else 0)
+
+
+def _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16) -> tuple[KVPages, int]:
+    """The pool's description and its device's index."""
     if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
         raise ValueError("k_pages must be a CUDA tensor")
-    kinds = (torch.bfloat16, torch.float16, torch.int8)
-    _tensor(k_pages, "k_pages", kinds, 4, k_pages.device)
-    _tensor(v_pages, "v_pages", (k_pages.dtype,), 4, k_pages.device)
-    if k_pages.shape[3] != D or v_pages.shape != k_pages.shape or _strides(v_pages, 3) != _strides(k_pages, 3):
+    index, dtype, shape = k_pages.get_device(), k_pages.dtype, k_pages.shape
+    st = _outer3(k_pages, _tensor(k_pages, "k_pages", _PAGE_TYPES, 4, index))
+    vst = _tensor(v_pages, "v_pages", (dtype,), 4, index)
+    if shape[3] != D or v_pages.shape != shape or _outer3(v_pages, vst) != st:
         raise ValueError("k_pages and v_pages must both be [npages, page_size, nkv, 128], of the same strides")
-    st = _strides(k_pages, 3)
-    kv = KVPages(_ptr(k_pages), _ptr(v_pages), None, None, _DTYPE[k_pages.dtype], k_pages.shape[0], k_pages.shape[1],
-                 k_pages.shape[2], st[0], st[1], st[2], 0, 0, 0)
-    if k_pages.dtype == torch.int8:
+    if dtype == torch.int8:
         for name, t in (("k_scale_f16", k_scale_f16), ("v_scale_f16", v_scale_f16)):
-            if (not isinstance(t, torch.Tensor) or t.device != k_pages.device or t.element_size() != 2
-                    or t.shape != k_pages.shape[:3]):
+            if (not isinstance(t, torch.Tensor) or t.get_device() != index or t.element_size() != 2
+                    or t.shape != shape[:3]):
                 raise ValueError(f"{name} must be [npages, page_size, nkv] binary16 values beside int8 pages")
-        st = _strides(k_scale_f16, 3)
-        if _strides(v_scale_f16, 3) != st:
+        sst = _outer3(k_scale_f16, k_scale_f16.stride())
+        if _outer3(v_scale_f16, v_scale_f16.stride()) != sst:
             raise ValueError("k_scale_f16 and v_scale_f16 must have the same strides")
-        kv.k_scale_f16, kv.v_scale_f16 = _ptr(k_scale_f16), _ptr(v_scale_f16)
-        kv.scale_page_stride, kv.scale_cell_stride, kv.scale_head_stride = st
-    elif k_scale_f16 is not None or v_scale_f16 is not None:
+        return KVPages(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale_f16), _ptr(v_scale_f16), I8, shape[0], shape[1],
+                       shape[2], *st, *sst), index
+    if k_scale_f16 is not None or v_scale_f16 is not None:
         raise ValueError("scales are for int8 pages only")
-    return kv
+    return KVPages(_ptr(k_pages), _ptr(v_pages), None, None, _DTYPE[dtype], shape[0], shape[1], shape[2], *st,
+                   0, 0, 0), index
 
 
-def _table(table, lens, device) -> int:
-    _tensor(table, "page_table", (torch.int32,), 2, device)
-    _tensor(lens, "lens", (torch.int32,), 1, device)
+def _table(table, lens, index) -> int:
+    st = _tensor(table, "page_table", _INT, 2, index)
+    _tensor(lens, "lens", _INT, 1, index)
     if lens.shape[0] != table.shape[0]:
         raise ValueError("page_table and lens must have one row per sequence")
-    return _row_stride(table)
+    return _rows(table, st)
 
 
 def _made(t, name, shape, dtype, device):
     """`t` checked as a contiguous output of that shape and type, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _tensor(t, name, (dtype,), len(shape), device)
+    _tensor(t, name, (dtype,), len(shape), device.index)
     if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}")
     return t
 
 
 def _scratch(t, need, device):
+    """(pointer, bytes, tensor to keep until the call is made)"""
     if t is None:
-        return torch.empty((need,), dtype=torch.uint8, device=device) if need else None
-    _tensor(t, "scratch", (torch.uint8,), 1, device)
+        if need == 0:
+            return None, 0, None
+        t = torch.empty((need,), dtype=torch.uint8, device=device)
+        return t.data_ptr(), need, t
+    _tensor(t, "scratch", _BYTE, 1, device.index)
     if t.numel() < need:
         raise ValueError(f"scratch must have at least {need} bytes")
-    return t
+    return _ptr(t), t.numel(), t
 
 
 def paged_attn_scratch_bytes(nseq: int, nheads: int, nkv: int, table_cols: int, page_size: int,
@@ -559,36 +579,39 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, pa
     received, summed over the heads, is added into ``mass_out`` (default:
     ``mass`` itself). ``scratch``: a uint8 tensor of
     ``paged_attn_scratch_bytes`` bytes, allocated when not given."""
-    kv = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16)
-    dev = k_pages.device
-    _tensor(q, "q", (torch.float32, torch.float16, torch.bfloat16) if kv.dtype == I8 else (k_pages.dtype,), 3, dev)
-    nseq, nheads = q.shape[:2]
-    if q.shape[2] != D or nheads < 1 or nheads % kv.nkv:
+    kv, index = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16)
+    dev, dtype = k_pages.device, q.dtype
+    qst = _tensor(q, "q", _Q_TYPES if kv.dtype == I8 else (k_pages.dtype,), 3, index)
+    nseq, nheads, d = q.shape
+    if d != D or nheads < 1 or nheads % kv.nkv:
         raise ValueError(f"q must be [nseq, a multiple of {kv.nkv}, {D}]")
-    tstride = _table(page_table, lens, dev)
-    if page_table.shape[0] != nseq:
+    tstride = _table(page_table, lens, index)
+    rows, cols = page_table.shape
+    if rows != nseq:
         raise ValueError("page_table must have one row per query")
-    cols = page_table.shape[1]
-    out = _made(out, "out", (nseq, nheads, D), q.dtype, dev)
+    out = _made(out, "out", (nseq, nheads, D), dtype, dev)
     lse = _made(lse, "lse", (nseq, nheads), torch.float32, dev)
     mstride = 0
     if mass is not None:
         mass_out = mass if mass_out is None else mass_out
         for name, t in (("mass", mass), ("mass_out", mass_out)):
-            _tensor(t, name, (torch.float32,), 2, dev)
+            st = _tensor(t, name, _FLOAT, 2, index)
             if t.shape[0] != nseq or t.shape[1] < cols * kv.page_size:
                 raise ValueError(f"{name} must be [{nseq}, >= {cols * kv.page_size}]")
-        mstride = _row_stride(mass)
-        if _strides(mass_out, 1) != _strides(mass, 1):
-            raise ValueError("mass and mass_out must have the same strides")
+            # of one row any stride will do
+            if t is mass:
+                mstride = st[0] if nseq > 1 else max(t.shape[1], mass_out.shape[1])
+            elif nseq > 1 and st[0] != mstride:
+                raise ValueError("mass and mass_out must have the same strides")
     elif mass_out is not None:
         raise ValueError("mass_out needs mass")
-    scratch = _scratch(scratch, paged_attn_scratch_bytes(nseq, nheads, kv.nkv, cols, kv.page_size, mass is not None), dev)
-    _check(lib().qsa_paged_attn(_ptr(q), _DTYPE[q.dtype], *_strides(q, 2), nseq, nheads, ctypes.byref(kv),
-                                _ptr(page_table), cols, tstride, _ptr(lens), window, sinks,
-                                SOFTMAX_SCALE if scale is None else scale, _ptr(out), _ptr(lse), _ptr(mass),
-                                _ptr(mass_out), mstride, _ptr(scratch), 0 if scratch is None else scratch.numel(),
-                                _stream(q)), "qsa_paged_attn")
+    need = lib().qsa_paged_attn_scratch_bytes(nseq, nheads, kv.nkv, cols, kv.page_size, mass is not None)
+    sp, sbytes, scratch = _scratch(scratch, need, dev)
+    q0, q1 = _outer2(q, qst)
+    _check(lib().qsa_paged_attn(_ptr(q), _DTYPE[dtype], q0, q1, nseq, nheads, kv, _ptr(page_table), cols, tstride,
+                                _ptr(lens), window, sinks, SOFTMAX_SCALE if scale is None else scale, _ptr(out),
+                                _ptr(lse), _ptr(mass), _ptr(mass_out), mstride, sp, sbytes, _raw_stream(index)),
+           "qsa_paged_attn")
     return out, lse
 
 
@@ -610,30 +633,31 @@ def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     ``max_q`` is at least the longest sequence's query count."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    dev = q.device
-    _tensor(q, "q", (torch.bfloat16, torch.float16), 3, dev)
-    _tensor(k, "k", (q.dtype,), 3, dev)
-    _tensor(v, "v", (q.dtype,), 3, dev)
-    total_q, nheads = q.shape[:2]
-    total_k, nkv = k.shape[:2]
-    if q.shape[2] != D or k.shape[2] != D or v.shape != k.shape or nkv < 1 or nheads < 1 or nheads % nkv:
+    dev, index, dtype = q.device, q.get_device(), q.dtype
+    qst = _tensor(q, "q", _PAGE_TYPES[:2], 3, index)
+    kst = _tensor(k, "k", (dtype,), 3, index)
+    vst = _tensor(v, "v", (dtype,), 3, index)
+    total_q, nheads, d = q.shape
+    total_k, nkv, kd = k.shape
+    if d != D or kd != D or v.shape != k.shape or nkv < 1 or nheads < 1 or nheads % nkv:
         raise ValueError("q must be [total_q, nheads, 128] and k, v [total_k, nkv, 128] with nheads a multiple of nkv")
-    _tensor(cu_q, "cu_q", (torch.int32,), 1, dev)
-    _tensor(cu_k, "cu_k", (torch.int32,), 1, dev)
-    if cu_q.shape != cu_k.shape or cu_q.shape[0] < 1:
-        raise ValueError("cu_q and cu_k must both have one more element than there are sequences")
+    _tensor(cu_q, "cu_q", _INT, 1, index)
+    _tensor(cu_k, "cu_k", _INT, 1, index)
     nseq = cu_q.shape[0] - 1
+    if cu_k.shape[0] - 1 != nseq or nseq < 0:
+        raise ValueError("cu_q and cu_k must both have one more element than there are sequences")
     if max_q < 0:
         raise ValueError("max_q must not be negative")
     max_q = min(max_q, total_q)
-    out = _made(out, "out", (total_q, nheads, D), q.dtype, dev)
+    out = _made(out, "out", (total_q, nheads, D), dtype, dev)
     lse = _made(lse, "lse", (total_q, nheads), torch.float32, dev)
-    scratch = _scratch(scratch, window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv), dev)
-    strides = (ctypes.c_int64 * 6)(*_strides(q, 2), *_strides(k, 2), *_strides(v, 2))
-    _check(lib().qsa_window_attn(_ptr(q), _ptr(k), _ptr(v), _DTYPE[q.dtype], strides, _ptr(cu_q), _ptr(cu_k), nseq,
+    need = lib().qsa_window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv)
+    sp, sbytes, scratch = _scratch(scratch, need, dev)
+    strides = _Strides6(*_outer2(q, qst), *_outer2(k, kst), *_outer2(v, vst))
+    _check(lib().qsa_window_attn(_ptr(q), _ptr(k), _ptr(v), _DTYPE[dtype], strides, _ptr(cu_q), _ptr(cu_k), nseq,
                                  total_q, total_k, max_q, nheads, nkv, window, sinks,
-                                 SOFTMAX_SCALE if scale is None else scale, _ptr(out), _ptr(lse), _ptr(scratch),
-                                 0 if scratch is None else scratch.numel(), _stream(q)), "qsa_window_attn")
+                                 SOFTMAX_SCALE if scale is None else scale, _ptr(out), _ptr(lse), sp, sbytes,
+                                 _raw_stream(index)), "qsa_window_attn")
     return out, lse
 
 
@@ -651,29 +675,30 @@ def cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.
     ``new_mass`` fp32 ``[nseq, >= budget]`` (default ``new_table.shape[1] *
     page_size`` columns): the kept masses, then zeros. Pages of ``new_table``
     must be none that ``page_table`` still uses."""
-    kv = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16)
+    kv, index = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16)
     dev = k_pages.device
-    tstride = _table(page_table, lens, dev)
+    tstride = _table(page_table, lens, index)
     nseq, cols = page_table.shape
-    _tensor(new_table, "new_table", (torch.int32,), 2, dev)
-    _tensor(mass, "mass", (torch.float32,), 2, dev)
-    if new_table.shape[0] != nseq:
+    nst = _tensor(new_table, "new_table", _INT, 2, index)
+    mst = _tensor(mass, "mass", _FLOAT, 2, index)
+    new_rows, new_cols = new_table.shape
+    if new_rows != nseq:
         raise ValueError("new_table must have one row per sequence")
     if mass.shape[0] != nseq or mass.shape[1] < cols * kv.page_size:
         raise ValueError(f"mass must be [{nseq}, >= {cols * kv.page_size}]")
-    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget or budget > new_table.shape[1] * kv.page_size:
+    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget or budget > new_cols * kv.page_size:
         raise ValueError("budget must be at least 1 and sinks + recent, and fit the new table's pages")
     kept = _made(kept, "kept", (nseq, budget), torch.int32, dev)
     new_lens = _made(new_lens, "new_lens", (nseq,), torch.int32, dev)
     if new_mass is None:
-        new_mass = torch.empty((nseq, new_table.shape[1] * kv.page_size), dtype=torch.float32, device=dev)
-    _tensor(new_mass, "new_mass", (torch.float32,), 2, dev)
+        new_mass = torch.empty((nseq, new_cols * kv.page_size), dtype=torch.float32, device=dev)
+    nmst = _tensor(new_mass, "new_mass", _FLOAT, 2, index)
     if new_mass.shape[0] != nseq or new_mass.shape[1] < budget:
         raise ValueError(f"new_mass must be [{nseq}, >= {budget}]")
-    _check(lib().qsa_cache_evict(ctypes.byref(kv), nseq, _ptr(page_table), cols, tstride, _ptr(lens), _ptr(mass),
-                                 _row_stride(mass), _ptr(new_table), new_table.shape[1], _row_stride(new_table),
-                                 budget, sinks, recent, _ptr(kept), _ptr(new_lens), _ptr(new_mass),
-                                 _row_stride(new_mass), new_mass.shape[1], _stream(k_pages)), "qsa_cache_evict")
+    _check(lib().qsa_cache_evict(kv, nseq, _ptr(page_table), cols, tstride, _ptr(lens), _ptr(mass), _rows(mass, mst),
+                                 _ptr(new_table), new_cols, _rows(new_table, nst), budget, sinks, recent, _ptr(kept),
+                                 _ptr(new_lens), _ptr(new_mass), _rows(new_mass, nmst), new_mass.shape[1],
+                                 _raw_stream(index)), "qsa_cache_evict")
     return kept, new_lens, new_mass
 
 
