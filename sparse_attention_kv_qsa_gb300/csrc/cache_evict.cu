@@ -2,12 +2,21 @@
 // cells, the last `recent` cells and, of the cells between, those of largest
 // mass are kept in order and copied to new pages.
 //
-// Two launches. evict_select_kernel: one CTA per sequence finds the mass of
-// the last cell to keep by a radix search on the order-preserving key of
-// csrc/qsa_internal.cuh, 8 bits per pass over shared-memory histograms (the
-// search is exact: it ends with the 32-bit key of that cell and how many of
-// the cells with that very key are kept, lowest first), then lists the kept
-// cells in order by block scans. evict_copy_kernel: one thread per 16 bytes.
+// select_kernel: a cluster of CTAs per sequence finds the mass of the last
+// cell to keep by a radix search on the order-preserving key of
+// csrc/qsa_internal.cuh, 11, 11 and 10 bits at a time. Each CTA holds a run of
+// the candidates' keys in shared memory, so the masses are read once, and
+// counts its digits there; after one cluster barrier every CTA adds all CTAs'
+// counts of a digit through distributed shared memory and finds the same
+// digit. The search ends with the exact 32-bit key of that cell and how many
+// cells with that very key are kept, the lowest first. The cells are then
+// listed in order: warps take consecutive runs, count, scan, and write.
+// Latency bounds it: four cluster barriers and the scans between them.
+//
+// copy_kernel: bandwidth. A warp takes a kept cell, finds both addresses once
+// and moves the cell's heads in 16-byte pieces, all loads before the stores.
+#include <algorithm>
+
 #include "cache_internal.cuh"
 #include "ptx.cuh"
 #include "qsa_internal.cuh"
@@ -15,118 +24,222 @@
 namespace qsa {
 namespace {
 
-constexpr int SEL_THREADS = 1024;
+constexpr int SEL_THREADS = 1024, SEL_WARPS = SEL_THREADS / 32;
+constexpr int MAX_CLUSTER = 8;
+constexpr int BINS = 2048;
+constexpr int MAX_KEYS = 40960;   // keys a CTA holds; longer runs are read again in every pass
 
-// Inclusive scan over the CTA of one int per thread; the total in *total.
-__device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int v = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(FULL_MASK, v, o);
-        if (lane >= o) v += y;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-        int w = warp_sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(FULL_MASK, w, o);
-            if (lane >= o) w += y;
-        }
-        warp_sums[lane] = w;
-    }
-    __syncthreads();
-    *total = warp_sums[31];
-    return v + (warp > 0 ? warp_sums[warp - 1] : 0);
+struct SelectShared {
+    int hist[3][BINS];
+    int warp_sums[SEL_WARPS];
+    unsigned long long warp_pairs[SEL_WARPS];
+    int digit, left;
+    int above, ties;   // of this CTA's run, for the others
+};
+
+__device__ __forceinline__ int ld_shared_rank(const int *p, uint32_t rank) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_shared_rank(smem_u32(p), rank)) : "memory");
+    return v;
 }
 
-__global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const CacheEvictArgs a) {
-    __shared__ int hist[256], warp_sums[32], sh_digit, sh_left;
-    const int s = blockIdx.x, tid = threadIdx.x;
-    const int n = min(max(a.lens[s], 0), a.table_cols * a.kv.page_size), m = min(n, a.budget);
+__global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArgs a, int cluster, int max_keys) {
+    extern __shared__ uint32_t keys[];
+    __shared__ SelectShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+    for (int i = tid; i < 3 * BINS; i += SEL_THREADS) (&sh.hist[0][0])[i] = 0;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int n = min(max(ld_in(a.lens + s), 0), a.table_cols * a.kv.page_size), m = min(n, a.budget);
     const float *mass = a.mass + s * a.mass_stride;
     int32_t *kept = a.kept + static_cast<size_t>(s) * a.budget;
     float *nm = a.new_mass + s * a.new_mass_stride;
-    if (tid == 0) a.new_lens[s] = m;
-    if (n <= a.budget) {
-        for (int i = tid; i < a.budget; i += SEL_THREADS) kept[i] = i < m ? i : -1;
-        for (int i = tid; i < a.new_mass_cols; i += SEL_THREADS) nm[i] = i < m ? mass[i] : 0.0f;
+    const int all_tid = rank * SEL_THREADS + tid, all_threads = cluster * SEL_THREADS;
+    if (all_tid == 0) a.new_lens[s] = m;
+    for (int i = m + all_tid; i < a.new_mass_cols; i += all_threads) nm[i] = 0.0f;
+    if (n <= a.budget) {   // the whole cluster leaves here
+        for (int i = all_tid; i < a.budget; i += all_threads) {
+            kept[i] = i < m ? i : -1;
+            if (i < m) nm[i] = ld_in(mass + i);
+        }
         return;
     }
-    // Candidates: [c0, c1); `left` of them are kept.
-    const int c0 = a.sinks, c1 = n - a.recent;
-    int left = a.budget - a.sinks - a.recent;
+    // Sinks and recent cells; the candidates between them are [c0, c1).
+    const int c0 = a.sinks, c1 = n - a.recent, recent_at = a.budget - a.recent;
+    for (int i = all_tid; i < a.sinks; i += all_threads) {
+        kept[i] = i;
+        nm[i] = ld_in(mass + i);
+    }
+    for (int i = all_tid; i < a.recent; i += all_threads) {
+        kept[recent_at + i] = c1 + i;
+        nm[recent_at + i] = ld_in(mass + c1 + i);
+    }
+    int left = recent_at - a.sinks;   // candidates to keep
+    if (left == 0) return;
+    const int per = (c1 - c0 + cluster - 1) / cluster;
+    const int j0 = min(c0 + rank * per, c1), count = min(per, c1 - j0);
+    const bool held = per <= max_keys;
+    auto key_at = [&](int i) { return held ? keys[i] : score_key(ld_in(mass + j0 + i)); };
+    auto barrier = [&]() {
+        if (cluster > 1)
+            cluster_sync_all();
+        else
+            __syncthreads();
+    };
+
     uint32_t prefix = 0;
-    if (left > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += SEL_THREADS) hist[i] = 0;
-            __syncthreads();
-            for (int j = c0 + tid; j < c1; j += SEL_THREADS) {
-                const uint32_t key = score_key(mass[j]);
-                if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1);
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? 2048 : 1024;
+        int *hist = sh.hist[pass];
+        __syncthreads();   // the counts are cleared
+        for (int i = tid; i < count; i += SEL_THREADS) {
+            uint32_t key;
+            if (pass == 0) {
+                key = score_key(ld_in(mass + j0 + i));
+                if (held) keys[i] = key;
+            } else {
+                key = key_at(i);
+                if ((key ^ prefix) >> (pass == 1 ? 21 : 10)) continue;
             }
-            __syncthreads();
-            if (tid == 0) {
-                int d = 255, need = left;
-                for (; d > 0 && hist[d] < need; --d) need -= hist[d];
-                sh_digit = d;
-                sh_left = need;
+            atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+        }
+        barrier();
+        // Two digits per thread, from the highest down, over all CTAs.
+        const int top = bins - 1 - 2 * tid;
+        int hi = 0, lo = 0;
+        if (top > 0)
+            for (int r = 0; r < cluster; ++r) {
+                hi += cluster > 1 ? ld_shared_rank(hist + top, r) : hist[top];
+                lo += cluster > 1 ? ld_shared_rank(hist + top - 1, r) : hist[top - 1];
             }
-            __syncthreads();
-            prefix |= static_cast<uint32_t>(sh_digit) << shift;
-            left = sh_left;
-            __syncthreads();
+        int sum = hi + lo;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL_MASK, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (lane == 31) sh.warp_sums[warp] = sum;
+        __syncthreads();
+        int before = sum - hi - lo;
+        for (int w = 0; w < SEL_WARPS; ++w)
+            if (w < warp) before += sh.warp_sums[w];
+        if (before < left && left <= before + hi + lo) {
+            const bool upper = left <= before + hi;
+            sh.digit = upper ? top : top - 1;
+            sh.left = left - before - (upper ? 0 : hi);
+        }
+        __syncthreads();
+        prefix |= static_cast<uint32_t>(sh.digit) << shift;
+        left = sh.left;
+    }
+
+    // Keys above `prefix` are kept, and the first `left` that equal it. Each warp
+    // takes a run of whole 32s, so that the lists stay in order.
+    const int run = (count + SEL_THREADS - 1) / SEL_THREADS * 32;
+    const int r0 = min(warp * run, count), r1 = min(r0 + run, count);
+    int above = 0, ties = 0;
+    for (int i = r0 + lane; i < r1; i += 32) {
+        const uint32_t key = key_at(i);
+        above += key > prefix;
+        ties += key == prefix;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        above += __shfl_xor_sync(FULL_MASK, above, o);
+        ties += __shfl_xor_sync(FULL_MASK, ties, o);
+    }
+    if (lane == 0) sh.warp_pairs[warp] = (static_cast<unsigned long long>(above) << 32) | static_cast<unsigned>(ties);
+    __syncthreads();
+    int above_before = 0, ties_before = 0, above_all = 0, ties_all = 0;
+    for (int w = 0; w < SEL_WARPS; ++w) {
+        const int u = static_cast<int>(sh.warp_pairs[w] >> 32), v = static_cast<int>(sh.warp_pairs[w] & 0xFFFFFFFFu);
+        above_all += u;
+        ties_all += v;
+        above_before += w < warp ? u : 0;
+        ties_before += w < warp ? v : 0;
+    }
+    if (cluster > 1) {
+        if (tid == 0) {
+            sh.above = above_all;
+            sh.ties = ties_all;
+        }
+        cluster_sync_all();
+        for (int r = 0; r < rank; ++r) {
+            above_before += ld_shared_rank(&sh.above, r);
+            ties_before += ld_shared_rank(&sh.ties, r);
         }
     }
-    // Keys above `prefix` are kept, and the first `left` equal to it. In order:
-    int out = 0, ties = 0;
-    const bool none = a.budget == a.sinks + a.recent;
-    for (int base = 0; base < n; base += SEL_THREADS) {
-        const int j = base + tid;
-        const bool mid = j >= c0 && j < c1;
-        const uint32_t key = mid ? score_key(mass[j]) : 0u;
-        const bool tie = mid && !none && key == prefix;
-        int nties, ntaken;
-        const int trank = block_scan(tie, warp_sums, &nties) + ties;
-        const bool take = j < n && (!mid || (!none && (key > prefix || (tie && trank <= left))));
-        const int at = block_scan(take, warp_sums, &ntaken) + out - 1;
+    for (int i0 = r0; i0 < r1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t key = i < r1 ? key_at(i) : 0u;
+        const uint32_t up = __ballot_sync(FULL_MASK, i < r1 && key > prefix);
+        const uint32_t eq = __ballot_sync(FULL_MASK, i < r1 && key == prefix);
+        const uint32_t lower = lanemask_lt();
+        const int tie_rank = ties_before + __popc(eq & lower);
+        const bool take = ((up >> lane) & 1u) || (((eq >> lane) & 1u) && tie_rank < left);
         if (take) {
-            kept[at] = j;
-            nm[at] = mass[j];
+            const int at = a.sinks + above_before + __popc(up & lower) + min(tie_rank, left);
+            kept[at] = j0 + i;
+            nm[at] = ld_in(mass + j0 + i);
         }
-        ties += nties;
-        out += ntaken;
+        above_before += __popc(up);
+        ties_before += __popc(eq);
     }
-    for (int i = a.budget + tid; i < a.new_mass_cols; i += SEL_THREADS) nm[i] = 0.0f;
+    if (cluster > 1) cluster_sync_all();   // no CTA leaves while another may read its counts
 }
 
-// Copies cell i of sequence s, 16 bytes of one head's K and V per thread.
-__global__ void __launch_bounds__(256) evict_copy_kernel(const CacheEvictArgs a) {
-    const int s = blockIdx.y;
-    const int elem = a.kv.dtype == QSA_I8 ? 1 : 2, vecs = 128 * elem / 16, per = a.kv.nkv * vecs;
-    const int m = a.new_lens[s];
-    for (long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; t < static_cast<long long>(m) * per;
-         t += static_cast<long long>(gridDim.x) * 256) {
-        const int i = static_cast<int>(t / per), r = static_cast<int>(t % per), h = r / vecs, c = r % vecs;
-        const int j = a.kept[static_cast<size_t>(s) * a.budget + i];
-        const int src = a.table[s * a.table_stride + j / a.kv.page_size];
-        const int dst = a.new_table[s * a.new_table_stride + i / a.kv.page_size];
+constexpr int COPY_THREADS = 256;
+
+// kVecs: 16-byte pieces of one head's row. Each warp moves one cell at a time.
+template <int kVecs>
+__global__ void __launch_bounds__(COPY_THREADS) copy_kernel(const CacheEvictArgs a, Divider page) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    constexpr int ELEM = kVecs == 8 ? 1 : 2, BATCH = 4;
+    const int lane = threadIdx.x & 31, s = blockIdx.y;
+    const int m = ld_in(a.new_lens + s), pieces = a.kv.nkv * kVecs;
+    char *k = static_cast<char *>(a.kv.k), *v = static_cast<char *>(a.kv.v);
+    const int64_t head_bytes = a.kv.head_stride * ELEM;
+    for (int i = blockIdx.x * (COPY_THREADS / 32) + (threadIdx.x >> 5); i < m; i += gridDim.x * (COPY_THREADS / 32)) {
+        const int j = ld_in(a.kept + static_cast<size_t>(s) * a.budget + i);
+        const int jp = divide(page, j), ip = divide(page, i);
+        const int src = ld_in(a.table + s * a.table_stride + jp), dst = ld_in(a.new_table + s * a.new_table_stride + ip);
         if (src < 0 || src >= a.kv.npages || dst < 0 || dst >= a.kv.npages) continue;
-        const int js = j % a.kv.page_size, is = i % a.kv.page_size;
-        const int64_t from = (src * a.kv.page_stride + js * a.kv.cell_stride + h * a.kv.head_stride) * elem + 16 * c;
-        const int64_t to = (dst * a.kv.page_stride + is * a.kv.cell_stride + h * a.kv.head_stride) * elem + 16 * c;
-        char *k = static_cast<char *>(a.kv.k), *v = static_cast<char *>(a.kv.v);
-        const uint4 x = ld_in(reinterpret_cast<const uint4 *>(k + from)), y = ld_in(reinterpret_cast<const uint4 *>(v + from));
-        *reinterpret_cast<uint4 *>(k + to) = x;
-        *reinterpret_cast<uint4 *>(v + to) = y;
-        if (a.kv.dtype == QSA_I8 && c == 0) {
-            const int64_t f = src * a.kv.scale_page_stride + js * a.kv.scale_cell_stride + h * a.kv.scale_head_stride;
-            const int64_t g = dst * a.kv.scale_page_stride + is * a.kv.scale_cell_stride + h * a.kv.scale_head_stride;
-            a.kv.k_scale_f16[g] = a.kv.k_scale_f16[f];
-            a.kv.v_scale_f16[g] = a.kv.v_scale_f16[f];
+        const int js = j - jp * a.kv.page_size, is = i - ip * a.kv.page_size;
+        const int64_t from = (src * a.kv.page_stride + js * a.kv.cell_stride) * ELEM;
+        const int64_t to = (dst * a.kv.page_stride + is * a.kv.cell_stride) * ELEM;
+        for (int c0 = 0; c0 < pieces; c0 += 32 * BATCH) {
+            uint4 x[BATCH], y[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int c = c0 + 32 * b + lane;
+                const int64_t off = from + (c / kVecs) * head_bytes + 16 * (c % kVecs);
+                if (c < pieces) {
+                    x[b] = ld_in(reinterpret_cast<const uint4 *>(k + off));
+                    y[b] = ld_in(reinterpret_cast<const uint4 *>(v + off));
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int c = c0 + 32 * b + lane;
+                const int64_t off = to + (c / kVecs) * head_bytes + 16 * (c % kVecs);
+                if (c < pieces) {
+                    *reinterpret_cast<uint4 *>(k + off) = x[b];
+                    *reinterpret_cast<uint4 *>(v + off) = y[b];
+                }
+            }
+        }
+        if constexpr (ELEM == 1) {
+            const int64_t f = src * a.kv.scale_page_stride + js * a.kv.scale_cell_stride;
+            const int64_t g = dst * a.kv.scale_page_stride + is * a.kv.scale_cell_stride;
+            for (int h = lane; h < a.kv.nkv; h += 32) {
+                const uint16_t x = ld_in_u16(a.kv.k_scale_f16 + f + h * a.kv.scale_head_stride);
+                const uint16_t y = ld_in_u16(a.kv.v_scale_f16 + f + h * a.kv.scale_head_stride);
+                a.kv.k_scale_f16[g + h * a.kv.scale_head_stride] = x;
+                a.kv.v_scale_f16[g + h * a.kv.scale_head_stride] = y;
+            }
         }
     }
 }
@@ -134,9 +247,45 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const CacheEvictArgs a)
 }  // namespace
 
 cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
-    evict_select_kernel<<<a.nseq, SEL_THREADS, 0, stream>>>(a);
-    evict_copy_kernel<<<dim3(512, a.nseq), 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    const int capacity = a.table_cols * a.kv.page_size;
+    // One CTA searches what a few rounds of its threads cover.
+    const int cluster = capacity <= 4 * SEL_THREADS ? 1 : MAX_CLUSTER;
+    const int max_keys = std::min((capacity + cluster - 1) / cluster, MAX_KEYS);
+    static thread_local int configured_device = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (configured_device != dev) {
+        e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_KEYS * 4);
+        if (e != cudaSuccess) return e;
+        configured_device = dev;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.stream = stream;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.nseq * cluster));
+    cfg.blockDim = dim3(SEL_THREADS);
+    cfg.dynamicSmemBytes = 4 * max_keys;
+    e = cudaLaunchKernelEx(&cfg, select_kernel, a, cluster, max_keys);
+    if (e != cudaSuccess) return e;
+    // Cells in one warp each, up to the CTAs that the GPU holds.
+    const long long blocks = std::min<long long>((a.budget + COPY_THREADS / 32 - 1) / (COPY_THREADS / 32),
+                                                 std::max(1LL, 8LL * device_sm_count() / a.nseq));
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), a.nseq);
+    cfg.blockDim = dim3(COPY_THREADS);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    const Divider page = make_divider(a.kv.page_size);
+    return a.kv.dtype == QSA_I8 ? cudaLaunchKernelEx(&cfg, copy_kernel<8>, a, page)
+                                : cudaLaunchKernelEx(&cfg, copy_kernel<16>, a, page);
 }
 
 }  // namespace qsa

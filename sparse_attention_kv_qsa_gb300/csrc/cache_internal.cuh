@@ -13,6 +13,18 @@ namespace qsa {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
+// floor(n / d) for 0 <= n < 2^31, by multiplication.
+struct Divider {
+    uint32_t d, mul, shift;
+};
+inline Divider make_divider(uint32_t d) {
+    if (d == 1) return {1, 0, 0};
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return {d, static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), l - 1};
+}
+__device__ __forceinline__ uint32_t divide(Divider v, uint32_t n) { return v.d == 1 ? n : __umulhi(n, v.mul) >> v.shift; }
+
 struct PagedAttnArgs {
     const void *q;
     qsa_dtype q_dtype;

@@ -54,18 +54,6 @@ constexpr int CTAS_PER_SM = 2;
 constexpr float LAZY = 8.0f;           // log2 of how far the sums may run above their reference
 constexpr int SLOT_ROW = 132;          // 128 outputs, maximum, sum, padding
 
-// floor(n / d) for 0 <= n < 2^31, by multiplication.
-struct Divider {
-    uint32_t d, mul, shift;
-};
-Divider make_divider(uint32_t d) {
-    if (d == 1) return {1, 0, 0};
-    uint32_t l = 0;
-    while ((1ull << l) < d) ++l;
-    return {d, static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), l - 1};
-}
-__device__ __forceinline__ uint32_t divide(Divider v, uint32_t n) { return v.d == 1 ? n : __umulhi(n, v.mul) >> v.shift; }
-
 struct Params {
     PagedAttnArgs a;
     Divider page;
