@@ -25,25 +25,47 @@ namespace qsa {
 namespace {
 
 constexpr int SEL_THREADS = 1024, SEL_WARPS = SEL_THREADS / 32;
-constexpr int MAX_CLUSTER = 8;
+// CTAs of a long sequence. 16 (not portable, but within a GB300 GPC) against 8: 131,072 cells 22 against 26 us.
+constexpr int MAX_CLUSTER = 16;
 constexpr int BINS = 2048;
 constexpr int MAX_KEYS = 40960;   // keys a CTA holds; longer runs are read again in every pass
 
-struct SelectShared {
+struct alignas(16) SelectShared {
     int hist[3][BINS];
-    int warp_sums[SEL_WARPS];
-    unsigned long long warp_pairs[SEL_WARPS];
+    int coarse[3][32];
+    int run[2];   // kept for their key, and equal to the last key, of this CTA's run: for the others
+    int warp_sums[SEL_WARPS], warp_ties[SEL_WARPS];
     int digit, left;
-    int above, ties;   // of this CTA's run, for the others
 };
 
+// A count, or two, of CTA `rank` of the cluster.
 __device__ __forceinline__ int ld_shared_rank(const int *p, uint32_t rank) {
     int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_shared_rank(smem_u32(p), rank)) : "memory");
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_shared_rank(smem_u32(p), rank)));
+    return v;
+}
+__device__ __forceinline__ int2 ld_shared_rank2(const int *p, uint32_t rank) {
+    int2 v;
+    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+                 : "=r"(v.x), "=r"(v.y)
+                 : "r"(map_shared_rank(smem_u32(p), rank)));
     return v;
 }
 
-__global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArgs a, int cluster, int max_keys) {
+// Inclusive prefix sum over the warp.
+__device__ __forceinline__ int warp_scan(int x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(FULL_MASK, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+template <int kCluster>
+__global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArgs a, int max_keys) {
+    constexpr int cluster = kCluster;
     extern __shared__ uint32_t keys[];
     __shared__ SelectShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,41 +116,67 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? 2048 : 1024;
         int *hist = sh.hist[pass];
         __syncthreads();   // the counts are cleared
-        for (int i = tid; i < count; i += SEL_THREADS) {
-            uint32_t key;
-            if (pass == 0) {
-                key = score_key(ld_in(mass + j0 + i));
-                if (held) keys[i] = key;
-            } else {
-                key = key_at(i);
-                if ((key ^ prefix) >> (pass == 1 ? 21 : 10)) continue;
+        constexpr int BATCH = 8;   // masses under way at once
+        for (int i0 = warp * 32; i0 < count; i0 += BATCH * SEL_THREADS) {
+            uint32_t key[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int i = i0 + b * SEL_THREADS + lane;
+                if (i < count) key[b] = pass == 0 || !held ? __float_as_uint(ld_in(mass + j0 + i)) : keys[i];
             }
-            atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int i = i0 + b * SEL_THREADS + lane;
+                if (i0 + b * SEL_THREADS >= count) break;
+                bool in = i < count;
+                if (pass == 0 || !held) key[b] = score_key(__uint_as_float(key[b]));
+                if (pass == 0 && held && in) keys[i] = key[b];
+                if (pass > 0) in = in && (key[b] ^ prefix) >> (pass == 1 ? 21 : 10) == 0;
+                if (in) atomicAdd(hist + ((key[b] >> shift) & (bins - 1)), 1);
+            }
+        }
+        __syncthreads();
+        {   // 32 coarse digits, a warp each
+            const int each = bins / 32;
+            int sum = hist[warp * each + lane] + (each > 32 ? hist[warp * each + 32 + lane] : 0);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
+            if (lane == 0) sh.coarse[pass][warp] = sum;
         }
         barrier();
-        // Two digits per thread, from the highest down, over all CTAs.
-        const int top = bins - 1 - 2 * tid;
-        int hi = 0, lo = 0;
-        if (top > 0)
-            for (int r = 0; r < cluster; ++r) {
-                hi += cluster > 1 ? ld_shared_rank(hist + top, r) : hist[top];
-                lo += cluster > 1 ? ld_shared_rank(hist + top - 1, r) : hist[top - 1];
-            }
-        int sum = hi + lo;
+        if (warp == 0) {
+            // From the highest digit down: the coarse digit of all CTAs' counts that the
+            // `left`-th key falls into, then the digit within it.
+            auto find = [&](const int *counts, int n, int &before) {
+                int mine = 0;
+                const int at = n - 1 - lane;
+                if (at >= 0) {
+                    int x[cluster];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(FULL_MASK, sum, o);
-            if (lane >= o) sum += y;
-        }
-        if (lane == 31) sh.warp_sums[warp] = sum;
-        __syncthreads();
-        int before = sum - hi - lo;
-        for (int w = 0; w < SEL_WARPS; ++w)
-            if (w < warp) before += sh.warp_sums[w];
-        if (before < left && left <= before + hi + lo) {
-            const bool upper = left <= before + hi;
-            sh.digit = upper ? top : top - 1;
-            sh.left = left - before - (upper ? 0 : hi);
+                    for (int r = 0; r < cluster; ++r) x[r] = cluster > 1 ? ld_shared_rank(counts + at, r) : counts[at];
+#pragma unroll
+                    for (int r = 0; r < cluster; ++r) mine += x[r];
+                }
+                const int upto = warp_scan(mine);
+                const uint32_t reach = __ballot_sync(FULL_MASK, upto + before >= left);
+                if (reach == 0u) {   // not among these 32
+                    before += __shfl_sync(FULL_MASK, upto, 31);
+                    return -1;
+                }
+                const int l = __ffs(reach) - 1;
+                before += __shfl_sync(FULL_MASK, upto - mine, l);
+                return n - 1 - l;
+            };
+            const int each = bins / 32;
+            int before = 0;
+            const int c = find(sh.coarse[pass], 32, before);
+            int d = -1;
+            if (each > 32) d = find(hist + c * each + 32, 32, before);
+            d = d >= 0 ? c * each + 32 + d : c * each + find(hist + c * each, 32, before);
+            if (lane == 0) {
+                sh.digit = d;
+                sh.left = left - before;
+            }
         }
         __syncthreads();
         prefix |= static_cast<uint32_t>(sh.digit) << shift;
@@ -150,25 +198,28 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
         above += __shfl_xor_sync(FULL_MASK, above, o);
         ties += __shfl_xor_sync(FULL_MASK, ties, o);
     }
-    if (lane == 0) sh.warp_pairs[warp] = (static_cast<unsigned long long>(above) << 32) | static_cast<unsigned>(ties);
-    __syncthreads();
-    int above_before = 0, ties_before = 0, above_all = 0, ties_all = 0;
-    for (int w = 0; w < SEL_WARPS; ++w) {
-        const int u = static_cast<int>(sh.warp_pairs[w] >> 32), v = static_cast<int>(sh.warp_pairs[w] & 0xFFFFFFFFu);
-        above_all += u;
-        ties_all += v;
-        above_before += w < warp ? u : 0;
-        ties_before += w < warp ? v : 0;
+    if (lane == 0) {
+        sh.warp_sums[warp] = above;
+        sh.warp_ties[warp] = ties;
     }
+    __syncthreads();
+    const int upto_above = warp_scan(sh.warp_sums[lane]), upto_ties = warp_scan(sh.warp_ties[lane]);
+    int above_before = __shfl_sync(FULL_MASK, upto_above, warp) - above;
+    int ties_before = __shfl_sync(FULL_MASK, upto_ties, warp) - ties;
+    const int above_all = __shfl_sync(FULL_MASK, upto_above, 31), ties_all = __shfl_sync(FULL_MASK, upto_ties, 31);
     if (cluster > 1) {
         if (tid == 0) {
-            sh.above = above_all;
-            sh.ties = ties_all;
+            sh.run[0] = above_all;
+            sh.run[1] = ties_all;
         }
         cluster_sync_all();
-        for (int r = 0; r < rank; ++r) {
-            above_before += ld_shared_rank(&sh.above, r);
-            ties_before += ld_shared_rank(&sh.ties, r);
+        int2 x[cluster];
+#pragma unroll
+        for (int r = 0; r < cluster; ++r) x[r] = ld_shared_rank2(sh.run, r);
+#pragma unroll
+        for (int r = 0; r < cluster; ++r) {
+            above_before += r < rank ? x[r].x : 0;
+            ties_before += r < rank ? x[r].y : 0;
         }
     }
     for (int i0 = r0; i0 < r1; i0 += 32) {
@@ -182,7 +233,9 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
         if (take) {
             const int at = a.sinks + above_before + __popc(up & lower) + min(tie_rank, left);
             kept[at] = j0 + i;
-            nm[at] = ld_in(mass + j0 + i);
+            // The mass is its key backwards, except that the key of -0 is +0's and NaN's is -infinity's.
+            const bool lost = key == 0x80000000u || key == 0x007FFFFFu;
+            nm[at] = lost ? ld_in(mass + j0 + i) : __uint_as_float((key >> 31) ? key ^ 0x80000000u : ~key);
         }
         above_before += __popc(up);
         ties_before += __popc(eq);
@@ -256,7 +309,11 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (configured_device != dev) {
-        e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_KEYS * 4);
+        e = cudaFuncSetAttribute(select_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_KEYS * 4);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(select_kernel<MAX_CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_KEYS * 4);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(select_kernel<MAX_CLUSTER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
@@ -274,7 +331,8 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
     cfg.gridDim = dim3(static_cast<unsigned>(a.nseq * cluster));
     cfg.blockDim = dim3(SEL_THREADS);
     cfg.dynamicSmemBytes = 4 * max_keys;
-    e = cudaLaunchKernelEx(&cfg, select_kernel, a, cluster, max_keys);
+    e = cluster == 1 ? cudaLaunchKernelEx(&cfg, select_kernel<1>, a, max_keys)
+                     : cudaLaunchKernelEx(&cfg, select_kernel<MAX_CLUSTER>, a, max_keys);
     if (e != cudaSuccess) return e;
     // Cells in one warp each, up to the CTAs that the GPU holds.
     const long long blocks = std::min<long long>((a.budget + COPY_THREADS / 32 - 1) / (COPY_THREADS / 32),
