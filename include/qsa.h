@@ -393,8 +393,8 @@ typedef struct {
  * aligned, the others 4-byte.
  * nseq, nheads or nkv out of range, nheads % nkv != 0, a bad type, scale,
  * pointer or stride returns QSA_ERR_INVALID; nseq or nheads above 65,535,
- * nseq * nheads or table_cols * page_size above 2^30 returns
- * QSA_ERR_UNSUPPORTED.
+ * nseq * nheads or table_cols * page_size above 2^30, or nseq * nheads *
+ * ceil(table_cols * page_size / 64) above 2^38 returns QSA_ERR_UNSUPPORTED.
  */
 size_t qsa_paged_attn_scratch_bytes(int nseq, int nheads, int nkv, int table_cols, int page_size, int with_mass);
 qsa_status qsa_paged_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride, int64_t q_head_stride, int nseq,

@@ -7,7 +7,7 @@
 
 namespace {
 
-constexpr long long MAX_SEQS = 65535, MAX_HEADS = 65535, MAX_CELLS = 1LL << 30;
+constexpr long long MAX_SEQS = 65535, MAX_HEADS = 65535, MAX_CELLS = 1LL << 30, MAX_TILES = 1LL << 38;
 
 bool aligned(const void *p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -71,7 +71,8 @@ qsa_status qsa_paged_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride
     const long long capacity = static_cast<long long>(table_cols) * kv->page_size;
     if (mass != nullptr && mass_stride < capacity) return QSA_ERR_INVALID;
     if (nseq == 0) return QSA_OK;
-    if (nseq > MAX_SEQS || nheads > MAX_HEADS || static_cast<long long>(nseq) * nheads > MAX_CELLS)
+    if (nseq > MAX_SEQS || nheads > MAX_HEADS || static_cast<long long>(nseq) * nheads > MAX_CELLS ||
+        static_cast<long long>(nseq) * nheads * ((capacity + 63) / 64) > MAX_TILES)
         return QSA_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lens, 4)) return QSA_ERR_INVALID;
     if (lse != nullptr && !aligned(lse, 4)) return QSA_ERR_INVALID;

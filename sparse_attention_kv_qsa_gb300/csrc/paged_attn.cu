@@ -48,8 +48,7 @@ namespace qsa {
 namespace {
 
 constexpr int WARPS = 4, THREADS = 32 * WARPS;
-constexpr int STEP = 16;               // cells of one warp's step
-constexpr int TILE = STEP * WARPS;
+constexpr int TILE_16BIT = 64, TILE_INT8 = 128;   // cells of a tile
 constexpr int CTAS_PER_SM = 2;
 constexpr float LAZY = 8.0f;           // log2 of how far the sums may run above their reference
 constexpr int SLOT_ROW = 132;          // 128 outputs, maximum, sum, padding
@@ -78,7 +77,6 @@ __device__ __forceinline__ Span visible(const Params &p, int s) {
     const int k = min(p.a.sinks, lo);
     return {k + len - lo, k, lo - k};
 }
-__device__ __forceinline__ int tiles_of(const Span &v) { return (v.n + TILE - 1) / TILE; }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -127,14 +125,12 @@ struct Op {
     }
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         if constexpr (kBf16)
-            asm volatile(
-                "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                 "{%0, %1, %2, %3};"
                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
         else
-            asm volatile(
-                "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                 "{%0, %1, %2, %3};"
                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -152,31 +148,64 @@ template <int kKv>   // QSA_BF16, QSA_F16 or QSA_I8
 struct Form {
     static constexpr bool kInt8 = kKv == QSA_I8;
     using O = Op<kKv == QSA_BF16>;
+    static constexpr int STEP = kInt8 ? 32 : 16;           // cells of one warp's step: 8 KiB of keys and values
+    static constexpr int TILE = STEP * WARPS;
+    static_assert(TILE == (kInt8 ? TILE_INT8 : TILE_16BIT), "tile sizes");
     static constexpr int ROW = kInt8 ? 128 : 256;          // bytes of a cell's row
     // Rows 16 bytes apart from a multiple of 128: the fragment loads of both
     // products (ldmatrix, or 16-byte loads for int8) meet no bank twice.
     static constexpr int PITCH = ROW + 16;
-    static constexpr int STAGES = kInt8 ? 6 : 3;
+    static constexpr int STAGES = 3;
     static constexpr int STAGE = 2 * STEP * PITCH;
     static constexpr int RING = STAGES * STAGE;            // one warp's ring
     static constexpr int SIDE = 8 * STEP + 16;             // a stage's scales (float ks, vs per cell) and cell mask
+    static_assert(STAGE >= 16 * 128 * 4, "a stage holds a warp's outputs");
 };
 
 template <int kKv, int kMT>
 constexpr int smem_bytes() {
     using F = Form<kKv>;
-    return std::max(WARPS * F::RING, WARPS * 8 * kMT * 128 * 4) + WARPS * F::STAGES * F::SIDE + 2 * WARPS * 8 * kMT * 4;
+    return WARPS * F::RING + WARPS * F::STAGES * F::SIDE + 2 * WARPS * 8 * kMT * 4;
 }
+
+template <int kTile>
+__device__ __forceinline__ int tiles_of(const Span &v) {
+    return (v.n + kTile - 1) / kTile;
+}
+
+// A place in the CTA's range of tiles: tile t of unit u of sequence s.
+template <int kTile>
+struct Cursor {
+    int s, u, t, nt;
+    Span v;
+    __device__ __forceinline__ void enter(const Params &p, int seq) {
+        s = seq;
+        v = visible(p, s);
+        nt = tiles_of<kTile>(v);
+    }
+    // The next tile, which exists.
+    __device__ __forceinline__ void next(const Params &p) {
+        if (++t < nt) return;
+        t = 0;
+        if (++u < p.units) return;
+        u = 0;
+        do enter(p, s + 1);
+        while (nt == 0);
+    }
+};
 
 template <int kKv, typename QT, int kMT>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __grid_constant__ Params p) {
     using F = Form<kKv>;
     using O = typename F::O;
     constexpr bool kInt8 = F::kInt8;
+    constexpr int STEP = F::STEP, TILE = F::TILE, STAGES = F::STAGES, ELEM = kInt8 ? 1 : 2;
     constexpr int HEADS_PER_UNIT = 8 * kMT;
+    // Cells whose weights are found together, in 16s; with 16 heads their registers allow 16 only.
+    constexpr int GROUPS = kMT == 1 ? STEP / 16 : 1;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long sh_scan[WARPS], sh_first;
-    __shared__ int sh_seq;
+    __shared__ long long sh_scan[WARPS];
+    __shared__ int sh_seq, sh_unit, sh_tile;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, t = lane & 3;
     const PagedAttnArgs &a = p.a;
@@ -188,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     const int each = (a.nseq + THREADS - 1) / THREADS;
     const int s0 = min(tid * each, a.nseq), s1 = min(s0 + each, a.nseq);
     long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += tiles_of(visible(p, s));
+    for (int s = s0; s < s1; ++s) mine += tiles_of<TILE>(visible(p, s));
     long long before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -196,7 +225,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
         if (lane >= o) before += y;
     }
     if (lane == 31) sh_scan[warp] = before;
-    if (tid == 0) sh_seq = -1;
+    if (tid == 0) {
+        sh_seq = -1;
+        p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
     __syncthreads();
     long long total = 0;
 #pragma unroll
@@ -209,18 +241,19 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     const long long all = total * p.units;
     const long long per = (all + gridDim.x - 1) / gridDim.x;
     const long long x0 = per * blockIdx.x, x1 = min(x0 + per, all);
-    if (tid == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    // The sequence that x0 falls into, and the number of its first tile.
+    // The tile that x0 is.
     if (x0 < x1 && x0 >= before * p.units && x0 < (before + mine) * p.units) {
         int s = s0;
         long long b = before;
-        for (; s < s1 - 1; ++s) {
-            const int n = tiles_of(visible(p, s));
-            if (x0 < (b + n) * p.units) break;
+        int n = tiles_of<TILE>(visible(p, s));
+        while (x0 >= (b + n) * p.units) {
             b += n;
+            n = tiles_of<TILE>(visible(p, ++s));
         }
+        const long long in_seq = x0 - b * p.units;
         sh_seq = s;
-        sh_first = b * p.units;
+        sh_unit = static_cast<int>(in_seq / n);
+        sh_tile = static_cast<int>(in_seq % n);
     }
     // Sequences without a visible cell have no tile: their rows are written here.
     for (int s = blockIdx.x; s < a.nseq; s += gridDim.x) {
@@ -233,33 +266,87 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
         }
     }
     __syncthreads();
-    int s = sh_seq;
-    if (s < 0) return;
-    long long first = sh_first;
+    if (sh_seq < 0) return;
 
-    unsigned char *side_base = smem + std::max(WARPS * F::RING, WARPS * HEADS_PER_UNIT * 128 * 4);
+    unsigned char *side_base = smem + WARPS * F::RING;
     float *merge_m = reinterpret_cast<float *>(side_base + WARPS * F::STAGES * F::SIDE);
     float *merge_l = merge_m + WARPS * HEADS_PER_UNIT;
-    float *merge_o = reinterpret_cast<float *>(smem);
     const uint32_t ring = smem_u32(smem + warp * F::RING);
     unsigned char *side = side_base + warp * F::STAGES * F::SIDE;
-    const int elem = kInt8 ? 1 : 2;
     const float c = a.scale * LOG2E;
+    const int steps = static_cast<int>(x1 - x0);   // of every warp: 16 or 32 cells of each tile
 
-    for (long long x = x0; x < x1;) {
-        const Span v = visible(p, s);
-        const int nt = tiles_of(v);
-        if (x >= first + static_cast<long long>(nt) * p.units) {   // on to the next sequence
-            first += static_cast<long long>(nt) * p.units;
-            ++s;
-            continue;
+    // ---- copies, which run ahead over the units without a stop ----------------------
+    const int row = lane & (STEP - 1);             // the row whose address this lane finds
+    Cursor<TILE> at;                               // the step whose page is fetched next
+    at.enter(p, sh_seq);
+    at.u = sh_unit;
+    at.t = sh_tile;
+    Cursor<TILE> here = at;                        // the step that is computed
+    int page = -1;                                 // of this lane's row of the step to copy next, and the rest of its address
+    long long rest = 0, scale_rest = 0;
+    auto fetch = [&](int step) {
+        if (step >= steps) return;
+        if (step > 0) at.next(p);
+        const int i = at.t * TILE + warp * STEP + row;
+        page = -1;
+        if (i < at.v.n) {
+            const int j = at.v.cell(i), pg = static_cast<int>(divide(p.page, j)), in_page = j - pg * a.kv.page_size;
+            page = ld_in(a.table + at.s * a.table_stride + pg);
+            const int kvh = p.parts == 1 ? at.u : at.u / p.parts;
+            rest = in_page * a.kv.cell_stride + kvh * a.kv.head_stride;
+            if constexpr (kInt8) scale_rest = in_page * a.kv.scale_cell_stride + kvh * a.kv.scale_head_stride;
         }
-        const int u = static_cast<int>((x - first) / nt), t0 = static_cast<int>((x - first) % nt);
-        const int t1 = static_cast<int>(min(static_cast<long long>(nt), t0 + (x1 - x)));
+    };
+    uint16_t key_scale = 0, value_scale = 0;       // this lane's row's of the newest step
+    auto issue = [&](int step) {
+        if (step < steps) {
+            const int slot_at = step % STAGES;
+            const bool ok = page >= 0 && page < a.kv.npages;
+            const long long off = ok ? (page * a.kv.page_stride + rest) * ELEM : 0;
+            const uint32_t mask = __ballot_sync(FULL_MASK, ok);
+            if (lane == 0) *reinterpret_cast<uint32_t *>(side + slot_at * F::SIDE + 8 * STEP) = mask;
+            if constexpr (kInt8) {
+                const long long so = ok ? page * a.kv.scale_page_stride + scale_rest : 0;
+                key_scale = ok ? ld_in_u16(a.kv.k_scale_f16 + so) : 0;
+                value_scale = ok ? ld_in_u16(a.kv.v_scale_f16 + so) : 0;
+            }
+            constexpr int LANES = F::ROW / 16, ROWS = 32 / LANES;
+            const int chunk = 16 * (lane % LANES), first = lane / LANES;
+            const uint32_t dst = ring + slot_at * F::STAGE + first * F::PITCH + chunk;
+            const char *k = static_cast<const char *>(a.kv.k) + chunk, *v = static_cast<const char *>(a.kv.v) + chunk;
+#pragma unroll
+            for (int b = 0; b < STEP / ROWS; ++b) {
+                const long long ro = __shfl_sync(FULL_MASK, off, b * ROWS + first);
+                const bool rok = (mask >> (b * ROWS + first)) & 1u;
+                cp_async_16_or_zero(dst + b * ROWS * F::PITCH, k + ro, rok);
+                cp_async_16_or_zero(dst + (STEP + b * ROWS) * F::PITCH, v + ro, rok);
+            }
+        }
+        cp_async_commit();
+    };
+    auto put_scale = [&](int step) {
+        if constexpr (kInt8)
+            if (step < steps)
+                *reinterpret_cast<float2 *>(side + (step % STAGES) * F::SIDE + 8 * row) =
+                    make_float2(__half2float(__ushort_as_half(key_scale)), __half2float(__ushort_as_half(value_scale)));
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int i = 0; i < STAGES - 1; ++i) {
+        issue(i);
+        fetch(i + 1);
+        if (i < STAGES - 2) put_scale(i);
+    }
+
+    // ---- units ------------------------------------------------------------------------
+    for (int step = 0; step < steps;) {
+        const int s = here.s, u = here.u, t0 = here.t, t1 = min(here.nt, t0 + steps - step), nt = here.nt;
         const int kvh = u / p.parts, h0 = kvh * p.group + (u % p.parts) * HEADS_PER_UNIT;
         const int nh = min(HEADS_PER_UNIT, (kvh + 1) * p.group - h0);
+        const bool begins = step == 0;
 
-        // ---- query fragments: head r of each 8 in rows 0-7, remainders in rows 8-15 ----
+        // Query fragments: head r of each 8 in rows 0-7, remainders in rows 8-15.
         uint32_t qa[kMT][8][kInt8 ? 4 : 2];
         float qc[kMT];   // what a product is multiplied by to become x
 #pragma unroll
@@ -310,217 +397,172 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 for (int e = 0; e < 4; ++e) o[m][n][e] = 0.0f;
         }
 
-        // ---- this warp's steps: visible cells 64 tile + 16 warp + 0..15 ----------------
-        const int32_t *table = a.table + s * a.table_stride;
-        const int row = lane & 15;                   // the row whose address this lane finds
-        auto index = [&](int step) { return (t0 + step) * TILE + warp * STEP; };
-        auto find_page = [&](int step) {             // page of this lane's row, -1 without one
-            const int i = index(step) + row;
-            return step < t1 - t0 && i < v.n ? ld_in(table + divide(p.page, v.cell(i))) : -1;
-        };
-        uint16_t pend = 0;                           // this lane's scale of the newest step
-        auto issue = [&](int step, int page) {
-            if (step < t1 - t0) {
-                const int slot_at = step % F::STAGES;
-                const int i = index(step) + row;
-                const bool ok = page >= 0 && page < a.kv.npages;
-                const int j = v.cell(i);
-                const int in_page = j - static_cast<int>(divide(p.page, j)) * a.kv.page_size;
-                const long long off = ok ? (page * a.kv.page_stride + in_page * a.kv.cell_stride + kvh * a.kv.head_stride) * elem : 0;
-                const uint32_t mask = __ballot_sync(FULL_MASK, ok) & 0xFFFFu;
-                unsigned char *sd = side + slot_at * F::SIDE;
-                if (lane == 0) *reinterpret_cast<uint32_t *>(sd + 8 * STEP) = mask;
-                if constexpr (kInt8) {
-                    const long long so = page * a.kv.scale_page_stride + in_page * a.kv.scale_cell_stride + kvh * a.kv.scale_head_stride;
-                    pend = ok ? ld_in_u16((lane < 16 ? a.kv.k_scale_f16 : a.kv.v_scale_f16) + so) : 0;
-                }
-                const uint32_t dst = ring + slot_at * F::STAGE;
-                constexpr int LANES = F::ROW / 16, ROWS = 32 / LANES;
-                const int chunk = 16 * (lane % LANES);
-#pragma unroll
-                for (int b = 0; b < STEP / ROWS; ++b) {
-                    const int rr = b * ROWS + lane / LANES;
-                    const long long ro = __shfl_sync(FULL_MASK, off, rr) + chunk;
-                    const bool rok = (mask >> rr) & 1u;
-                    cp_async_16_or_zero(dst + rr * F::PITCH + chunk, static_cast<const char *>(a.kv.k) + (rok ? ro : 0), rok);
-                    cp_async_16_or_zero(dst + (STEP + rr) * F::PITCH + chunk, static_cast<const char *>(a.kv.v) + (rok ? ro : 0), rok);
-                }
-            }
-            cp_async_commit();
-        };
-        auto put_scale = [&](int step) {
-            if constexpr (kInt8)
-                if (step < t1 - t0)
-                    reinterpret_cast<float *>(side + (step % F::STAGES) * F::SIDE)[2 * row + (lane >> 4)] =
-                        __half2float(__ushort_as_half(pend));
-        };
-
-        const int nsteps = t1 - t0;
-        int page = find_page(0);
 #pragma unroll 1
-        for (int i = 0; i < F::STAGES - 1; ++i) {
-            const int next = find_page(i + 1);
-            issue(i, page);
-            if (i < F::STAGES - 2) put_scale(i);
-            page = next;
-        }
-#pragma unroll 1
-        for (int step = 0; step < nsteps; ++step) {
-            put_scale(step + F::STAGES - 2);
-            cp_async_wait<F::STAGES - 2>();
+        for (int tile = t0; tile < t1; ++tile, ++step) {
+            put_scale(step + STAGES - 2);
+            cp_async_wait<STAGES - 2>();
             __syncwarp();
-            const int next = find_page(step + F::STAGES);
-            issue(step + F::STAGES - 1, page);
-            page = next;
-            if (index(step) >= v.n) continue;
-
-            const uint32_t kb = ring + (step % F::STAGES) * F::STAGE, vb = kb + STEP * F::PITCH;
-            const unsigned char *sd = side + (step % F::STAGES) * F::SIDE;
+            issue(step + STAGES - 1);
+            fetch(step + STAGES);
+            const unsigned char *sd = side + (step % STAGES) * F::SIDE;
             const uint32_t mask = *reinterpret_cast<const uint32_t *>(sd + 8 * STEP);
-            // x of heads (row r) by cells 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-            float sc[kMT][2][4];
+            if (mask == 0u && p.logits == nullptr) continue;
+            const uint32_t kb = ring + (step % STAGES) * F::STAGE, vb = kb + STEP * F::PITCH;
 #pragma unroll
-            for (int m = 0; m < kMT; ++m)
+            for (int g0 = 0; g0 < STEP / 16; g0 += GROUPS) {
+                // x of heads (row r) by cells 16 g + 2 t, + 1, + 8, + 9
+                float sc[kMT][2 * GROUPS][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int m = 0; m < kMT; ++m)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[m][n][e] = 0.0f;
-            float ks[4], vs[4];
-            if constexpr (kInt8) {
+                    for (int n = 0; n < 2 * GROUPS; ++n)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float4 f = *reinterpret_cast<const float4 *>(sd + 8 * (2 * t + 8 * n));
-                    ks[2 * n] = f.x;
-                    vs[2 * n] = f.y;
-                    ks[2 * n + 1] = f.z;
-                    vs[2 * n + 1] = f.w;
-                }
+                        for (int e = 0; e < 4; ++e) sc[m][n][e] = 0.0f;
+                float ks[4 * GROUPS], vs[4 * GROUPS];
+                if constexpr (kInt8) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const uint32_t at = kb + (8 * n + r) * F::PITCH + 32 * t;
-                    const uint4 w0 = ld_shared_v4(at), w1 = ld_shared_v4(at + 16);
-                    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                    for (int n = 0; n < 2 * GROUPS; ++n) {
+                        const float4 f = *reinterpret_cast<const float4 *>(sd + 8 * (16 * g0 + 8 * n + 2 * t));
+                        ks[2 * n] = f.x;
+                        vs[2 * n] = f.y;
+                        ks[2 * n + 1] = f.z;
+                        vs[2 * n + 1] = f.w;
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2 * GROUPS; ++n) {
+                        const uint32_t at_k = kb + (16 * g0 + 8 * n + r) * F::PITCH + 32 * t;
+                        const uint4 w0 = ld_shared_v4(at_k), w1 = ld_shared_v4(at_k + 16);
+                        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t z = w[k] ^ 0x80808080u;
+                            const uint32_t b0 = biased_to_half2(z, 0x4140), b1 = biased_to_half2(z, 0x4342);
+#pragma unroll
+                            for (int m = 0; m < kMT; ++m) O::mma(sc[m][n], qa[m][k], b0, b1);
+                        }
+                    }
+                } else {
+                    // matrices: cells 0-7 and 8-15 by d 0-7 and 8-15 of step k
+                    const uint32_t at_k = kb + ((lane & 7) + 8 * (lane >> 4)) * F::PITCH + 16 * ((lane >> 3) & 1);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const uint32_t z = w[k] ^ 0x80808080u;
-                        const uint32_t b0 = biased_to_half2(z, 0x4140), b1 = biased_to_half2(z, 0x4342);
+                        uint32_t b[4];
+                        ldmatrix4(b, at_k + 32 * k);
 #pragma unroll
-                        for (int m = 0; m < kMT; ++m) O::mma(sc[m][n], qa[m][k], b0, b1);
+                        for (int m = 0; m < kMT; ++m) {
+                            const uint32_t qf[4] = {qa[m][k][0], 0u, qa[m][k][1], 0u};
+                            O::mma(sc[m][0], qf, b[0], b[1]);
+                            O::mma(sc[m][1], qf, b[2], b[3]);
+                        }
                     }
                 }
-            } else {
-                // matrices: cells 0-7 and 8-15 by d 0-7 and 8-15 of step k
-                const uint32_t at = kb + ((lane & 7) + 8 * (lane >> 4)) * F::PITCH + 16 * ((lane >> 3) & 1);
+                uint32_t pa[kMT][GROUPS][4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    uint32_t b[4];
-                    ldmatrix4(b, at + 32 * k);
+                for (int m = 0; m < kMT; ++m) {
+                    float xx[4 * GROUPS], top = -INFINITY;
 #pragma unroll
-                    for (int m = 0; m < kMT; ++m) {
-                        const uint32_t qf[4] = {qa[m][k][0], 0u, qa[m][k][1], 0u};
-                        O::mma(sc[m][0], qf, b[0], b[1]);
-                        O::mma(sc[m][1], qf, b[2], b[3]);
+                    for (int n = 0; n < 2 * GROUPS; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float y = sc[m][n][e];
+                            if constexpr (kInt8) y = fmaf(sc[m][n][2 + e], 1.0f / O::LO, y) * ks[2 * n + e];
+                            y *= qc[m];
+                            if (!((mask >> (16 * g0 + 8 * n + 2 * t + e)) & 1u)) y = -INFINITY;
+                            xx[2 * n + e] = y;
+                            float z = y;
+                            if constexpr (kInt8) z += __log2f(fmaxf(fabsf(vs[2 * n + e]), 5.9604645e-8f));
+                            top = fmaxf(top, z);
+                        }
+                    if (p.logits != nullptr && 8 * m + r < nh) {
+                        float *lp = p.logits + (static_cast<size_t>(s) * a.nheads + h0 + 8 * m + r) * p.stride +
+                                    tile * TILE + warp * STEP + 16 * g0 + 2 * t;
+#pragma unroll
+                        for (int n = 0; n < 2 * GROUPS; ++n)
+                            *reinterpret_cast<float2 *>(lp + 8 * n) = make_float2(xx[2 * n], xx[2 * n + 1]);
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
+                    const bool move = top > ref[m] + LAZY || (ref[m] == -INFINITY && top > -INFINITY);
+                    if (__any_sync(FULL_MASK, move)) {
+                        const float f = move ? ex2(ref[m] - top) : 1.0f;
+                        if (move) ref[m] = top;
+                        sum[m] *= f;
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[m][n][e] *= f;
+                    }
+                    const float base = ref[m] == -INFINITY ? 0.0f : ref[m];
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) {
+                        float w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            w[e] = ex2(xx[4 * g + e] - base);
+                            sum[m] += w[e];
+                            if constexpr (kInt8) w[e] *= vs[4 * g + e];
+                        }
+                        O::split(w[0], w[1], pa[m][g][0], pa[m][g][1]);
+                        O::split(w[2], w[3], pa[m][g][2], pa[m][g][3]);
                     }
                 }
-            }
-            uint32_t pa[kMT][4];
 #pragma unroll
-            for (int m = 0; m < kMT; ++m) {
-                float xx[4], top = -INFINITY;
+                for (int gg = 0; gg < GROUPS; ++gg) {
+                    const uint32_t vg = vb + 16 * (g0 + gg) * F::PITCH;
+                    if constexpr (kInt8) {
+                        // This thread's cells 2 t, 2 t + 1, 2 t + 8, 2 t + 9; column r of product n is d = 16 r + n.
+                        uint4 cw[4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                        for (int e = 0; e < 4; ++e) cw[e] = ld_shared_v4(vg + (2 * t + (e & 1) + 8 * (e >> 1)) * F::PITCH + 16 * r);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float y = sc[m][n][e];
-                        if constexpr (kInt8) y = fmaf(sc[m][n][2 + e], 1.0f / O::LO, y) * ks[2 * n + e];
-                        y *= qc[m];
-                        if (!((mask >> (2 * t + 8 * n + e)) & 1u)) y = -INFINITY;
-                        xx[2 * n + e] = y;
-                        float z = y;
-                        if constexpr (kInt8) z += __log2f(fmaxf(fabsf(vs[2 * n + e]), 5.9604645e-8f));
-                        top = fmaxf(top, z);
-                    }
-                if (p.logits != nullptr && 8 * m + r < nh) {
-                    float *lp = p.logits + (static_cast<size_t>(s) * a.nheads + h0 + 8 * m + r) * p.stride + index(step) + 2 * t;
-                    *reinterpret_cast<float2 *>(lp) = make_float2(xx[0], xx[1]);
-                    *reinterpret_cast<float2 *>(lp + 8) = make_float2(xx[2], xx[3]);
-                }
-                top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
-                const bool move = top > ref[m] + LAZY || (ref[m] == -INFINITY && top > -INFINITY);
-                if (__any_sync(FULL_MASK, move)) {
-                    const float f = move ? ex2(ref[m] - top) : 1.0f;
-                    if (move) ref[m] = top;
-                    sum[m] *= f;
+                        for (int g = 0; g < 4; ++g) {
+                            uint32_t lo[2], hi[2];   // cells (2t, 2t+1) and (2t+8, 2t+9): d 0, 1 and d 2, 3 of the word
 #pragma unroll
-                    for (int n = 0; n < 16; ++n)
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t w0 = reinterpret_cast<const uint32_t *>(&cw[2 * e])[g] ^ 0x80808080u;
+                                const uint32_t w1 = reinterpret_cast<const uint32_t *>(&cw[2 * e + 1])[g] ^ 0x80808080u;
+                                lo[e] = __byte_perm(w0, w1, 0x5140);
+                                hi[e] = __byte_perm(w0, w1, 0x7362);
+                            }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[m][n][e] *= f;
-                }
-                const float base = ref[m] == -INFINITY ? 0.0f : ref[m];
-                float w[4];
+                            for (int d = 0; d < 4; ++d) {
+                                const uint32_t sel = (d & 1) ? 0x4342 : 0x4140;
+                                const uint32_t b0 = biased_to_half2(d < 2 ? lo[0] : hi[0], sel);
+                                const uint32_t b1 = biased_to_half2(d < 2 ? lo[1] : hi[1], sel);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[e] = ex2(xx[e] - base);
-                    sum[m] += w[e];
-                    if constexpr (kInt8) w[e] *= vs[e];
-                }
-                O::split(w[0], w[1], pa[m][0], pa[m][1]);
-                O::split(w[2], w[3], pa[m][2], pa[m][3]);
-            }
-            if constexpr (kInt8) {
-                // This thread's cells 2 t, 2 t + 1, 2 t + 8, 2 t + 9; column r of product n is d = 16 r + n.
-                uint4 cw[4];
+                                for (int m = 0; m < kMT; ++m) O::mma(o[m][4 * g + d], pa[m][gg], b0, b1);
+                            }
+                        }
+                    } else {
+                        // matrices: cells 0-7, 8-15 by d 16 n .. + 7, then d 16 n + 8 .. + 15
+                        const uint32_t at_v = vg + (lane & 15) * F::PITCH + 16 * (lane >> 4);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) cw[e] = ld_shared_v4(vb + (2 * t + (e & 1) + 8 * (e >> 1)) * F::PITCH + 16 * r);
+                        for (int n = 0; n < 8; ++n) {
+                            uint32_t b[4];
+                            ldmatrix4_t(b, at_v + 32 * n);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t lo[2], hi[2];   // cells (2t, 2t+1) and (2t+8, 2t+9): d 0, 1 and d 2, 3 of the word
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t w0 = reinterpret_cast<const uint32_t *>(&cw[2 * e])[g] ^ 0x80808080u;
-                        const uint32_t w1 = reinterpret_cast<const uint32_t *>(&cw[2 * e + 1])[g] ^ 0x80808080u;
-                        lo[e] = __byte_perm(w0, w1, 0x5140);
-                        hi[e] = __byte_perm(w0, w1, 0x7362);
-                    }
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        const uint32_t sel = (d & 1) ? 0x4342 : 0x4140;
-                        const uint32_t b0 = biased_to_half2(d < 2 ? lo[0] : hi[0], sel);
-                        const uint32_t b1 = biased_to_half2(d < 2 ? lo[1] : hi[1], sel);
-#pragma unroll
-                        for (int m = 0; m < kMT; ++m) O::mma(o[m][4 * g + d], pa[m], b0, b1);
-                    }
-                }
-            } else {
-                // matrices: cells 0-7, 8-15 by d 16 n .. + 7, then d 16 n + 8 .. + 15
-                const uint32_t at = vb + (lane & 15) * F::PITCH + 16 * (lane >> 4);
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    uint32_t b[4];
-                    ldmatrix4_t(b, at + 32 * n);
-#pragma unroll
-                    for (int m = 0; m < kMT; ++m) {
-                        O::mma(o[m][2 * n], pa[m], b[0], b[1]);
-                        O::mma(o[m][2 * n + 1], pa[m], b[2], b[3]);
+                            for (int m = 0; m < kMT; ++m) {
+                                O::mma(o[m][2 * n], pa[m][gg], b[0], b[1]);
+                                O::mma(o[m][2 * n + 1], pa[m][gg], b[2], b[3]);
+                            }
+                        }
                     }
                 }
             }
         }
-        cp_async_wait<0>();
 
-        // ---- join the warps, in warp order ----------------------------------------------
-        __syncthreads();   // every warp is done with its ring
+        // ---- join the warps, in warp order, through the stage each has just used ----------
+        __syncwarp();
+        const int used = (step - 1) % STAGES;
 #pragma unroll
         for (int m = 0; m < kMT; ++m) {
             sum[m] += __shfl_xor_sync(FULL_MASK, sum[m], 1);
             sum[m] += __shfl_xor_sync(FULL_MASK, sum[m], 2);
-            const int h = warp * HEADS_PER_UNIT + 8 * m + r;
             if (t == 0) {
-                merge_m[h] = ref[m];
-                merge_l[h] = sum[m];
+                merge_m[warp * HEADS_PER_UNIT + 8 * m + r] = ref[m];
+                merge_l[warp * HEADS_PER_UNIT + 8 * m + r] = sum[m];
             }
-            float *mo = merge_o + h * 128;
+            float *mo = reinterpret_cast<float *>(smem + warp * F::RING + used * F::STAGE) + (8 * m + r) * 128;
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
                 const float y0 = fmaf(o[m][n][2], 1.0f / O::LO, o[m][n][0]), y1 = fmaf(o[m][n][3], 1.0f / O::LO, o[m][n][1]);
@@ -534,7 +576,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
         }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == nt;
-        const int slot = 2 * blockIdx.x + (x == x0 ? 0 : 1);
+        const int slot = 2 * blockIdx.x + (begins ? 0 : 1);
         for (int h = warp; h < nh; h += WARPS) {
             float top = -INFINITY;
 #pragma unroll
@@ -547,7 +589,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 const int hw = w * HEADS_PER_UNIT + h;
                 const float f = ex2(merge_m[hw] - base);
                 l = fmaf(merge_l[hw], f, l);
-                const float4 z = *reinterpret_cast<const float4 *>(merge_o + hw * 128 + 4 * lane);
+                const float4 z = *reinterpret_cast<const float4 *>(smem + w * F::RING + used * F::STAGE + (h * 128 + 4 * lane) * 4);
                 y.x = fmaf(z.x, f, y.x);
                 y.y = fmaf(z.y, f, y.y);
                 y.z = fmaf(z.z, f, y.z);
@@ -572,12 +614,17 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
             }
         }
         // The unit is joined by the block of the second range that it falls into.
-        const long long unit0 = first + static_cast<long long>(u) * nt;
-        if (tid == 0 && !whole && x == x0 && x0 > unit0 && unit0 / per == blockIdx.x - 1)
-            p.meta[blockIdx.x] = make_int4(s, u, static_cast<int>(unit0 / per) * 2 + (unit0 % per == 0 ? 0 : 1),
-                                           static_cast<int>((unit0 + nt - 1) / per));
-        x += t1 - t0;
-        __syncthreads();   // the rings are free again
+        if (tid == 0 && !whole && begins) {
+            const long long unit0 = x0 - t0;
+            if (t0 > 0 && unit0 / per == blockIdx.x - 1)
+                p.meta[blockIdx.x] = make_int4(s, u, static_cast<int>(unit0 / per) * 2 + (unit0 % per == 0 ? 0 : 1),
+                                               static_cast<int>((unit0 + nt - 1) / per));
+        }
+        if (step < steps) {
+            here.t = here.nt - 1;
+            here.next(p);
+        }
+        __syncthreads();   // the stages are free again
     }
 }
 
@@ -670,9 +717,9 @@ Layout layout(int nseq, int nheads, int nkv, int capacity, bool with_mass) {
     const int group = nheads / nkv;
     y.heads_per_unit = group <= 8 ? 8 : 16;
     const long long parts = (group + y.heads_per_unit - 1) / y.heads_per_unit;
-    const long long tiles = (static_cast<long long>(capacity) + TILE - 1) / TILE * nkv * parts * nseq;
+    const long long tiles = (static_cast<long long>(capacity) + TILE_16BIT - 1) / TILE_16BIT * nkv * parts * nseq;
     y.grid = static_cast<int>(std::max(1LL, std::min<long long>(static_cast<long long>(CTAS_PER_SM) * device_sm_count(), tiles)));
-    y.stride = (capacity + TILE - 1) / TILE * TILE;
+    y.stride = (capacity + TILE_INT8 - 1) / TILE_INT8 * TILE_INT8;
     size_t at = 0;
     y.meta = at;
     at += sizeof(int4) * y.grid;

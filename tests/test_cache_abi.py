@@ -73,6 +73,7 @@ def test_paged_attn_limits(lib):
     assert paged(lib, nheads=65536) == UNSUPPORTED
     assert paged(lib, nseq=65535, nheads=32768) == UNSUPPORTED
     assert paged(lib, cols=1 << 27, tstride=1 << 27) == UNSUPPORTED
+    assert paged(lib, nseq=65535, nheads=16000, cols=1 << 20, tstride=1 << 20) == UNSUPPORTED
     assert paged(lib, pages(dtype=qsa.I8, k_scale_f16=A, v_scale_f16=A), q_dtype=qsa.I8) == INVALID
     n = qsa.paged_attn_scratch_bytes
     assert n(0, 8, 2, 4, 16) == 0 and n(2, 7, 2, 4, 16) == 0
