@@ -39,6 +39,7 @@
 // scaled by whatever M they started from, and rescaling is rare.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "attn_row.cuh"
 #include "cache_internal.cuh"
@@ -340,7 +341,32 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     }
 
     // ---- units ------------------------------------------------------------------------
+    // The queries of unit `here`, as they lie: d = 32 t + 4 k + {0, 1, 2, 3} of step k for int8
+    // cells, else d = 16 k + 2 t + {0, 1} and + 8.
+    using Raw = typename std::conditional<kInt8, float4, uint2>::type;
+    Raw raw_q[kMT][8];
+    auto load_q = [&]() {
+        const int kvh = here.u / p.parts, h0 = kvh * p.group + (here.u % p.parts) * HEADS_PER_UNIT;
+        const int nh = (kvh + 1) * p.group - h0;
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+            const bool have = 8 * m + r < nh;
+            const QT *qp = static_cast<const QT *>(a.q) + here.s * a.q_seq_stride + (h0 + (have ? 8 * m + r : 0)) * a.q_head_stride;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if constexpr (kInt8) {
+                    raw_q[m][k] = have ? load4(qp + 32 * t + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                } else {
+                    raw_q[m][k].x = have ? ld_in(reinterpret_cast<const uint32_t *>(qp + 16 * k + 2 * t)) : 0u;
+                    raw_q[m][k].y = have ? ld_in(reinterpret_cast<const uint32_t *>(qp + 16 * k + 2 * t + 8)) : 0u;
+                }
+            }
+        }
+    };
+    constexpr bool AHEAD = kMT == 1;   // the registers for 16 heads' queries are not there
+    if (AHEAD) load_q();
     for (int step = 0; step < steps;) {
+        if (!AHEAD) load_q();
         const int s = here.s, u = here.u, t0 = here.t, t1 = min(here.nt, t0 + steps - step), nt = here.nt;
         const int kvh = u / p.parts, h0 = kvh * p.group + (u % p.parts) * HEADS_PER_UNIT;
         const int nh = min(HEADS_PER_UNIT, (kvh + 1) * p.group - h0);
@@ -351,18 +377,13 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
         float qc[kMT];   // what a product is multiplied by to become x
 #pragma unroll
         for (int m = 0; m < kMT; ++m) {
-            const bool have = 8 * m + r < nh;
-            const QT *qp = static_cast<const QT *>(a.q) + s * a.q_seq_stride + (h0 + (have ? 8 * m + r : 0)) * a.q_head_stride;
             qc[m] = c;
             if constexpr (kInt8) {
-                // This thread's elements: d = 32 t + 4 k + {0, 1, 2, 3} of step k.
-                float4 e[8];
                 float top = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    e[k] = have ? load4(qp + 32 * t + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    top = fmaxf(top, fmaxf(fmaxf(fabsf(e[k].x), fabsf(e[k].y)), fmaxf(fabsf(e[k].z), fabsf(e[k].w))));
-                }
+                for (int k = 0; k < 8; ++k)
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(raw_q[m][k].x), fabsf(raw_q[m][k].y)),
+                                           fmaxf(fabsf(raw_q[m][k].z), fabsf(raw_q[m][k].w))));
                 top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
                 int ex = 0;
@@ -372,15 +393,14 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 qc[m] = c * ldexpf(1.0f, ex);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    O::split(e[k].x * down, e[k].y * down, qa[m][k][0], qa[m][k][1]);
-                    O::split(e[k].z * down, e[k].w * down, qa[m][k][2], qa[m][k][3]);
+                    O::split(raw_q[m][k].x * down, raw_q[m][k].y * down, qa[m][k][0], qa[m][k][1]);
+                    O::split(raw_q[m][k].z * down, raw_q[m][k].w * down, qa[m][k][2], qa[m][k][3]);
                 }
             } else {
-                // d = 16 k + 2 t + {0, 1} and + 8
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    qa[m][k][0] = have ? ld_in(reinterpret_cast<const uint32_t *>(qp + 16 * k + 2 * t)) : 0u;
-                    qa[m][k][1] = have ? ld_in(reinterpret_cast<const uint32_t *>(qp + 16 * k + 2 * t + 8)) : 0u;
+                    qa[m][k][0] = raw_q[m][k].x;
+                    qa[m][k][1] = raw_q[m][k].y;
                 }
             }
         }
@@ -574,6 +594,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 }
             }
         }
+        if (step < steps) {   // the next unit's queries come while this one's results leave
+            here.t = here.nt - 1;
+            here.next(p);
+            if (AHEAD) load_q();
+        }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == nt;
         const int slot = 2 * blockIdx.x + (begins ? 0 : 1);
@@ -620,92 +645,122 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 p.meta[blockIdx.x] = make_int4(s, u, static_cast<int>(unit0 / per) * 2 + (unit0 % per == 0 ? 0 : 1),
                                                static_cast<int>((unit0 + nt - 1) / per));
         }
-        if (step < steps) {
-            here.t = here.nt - 1;
-            here.next(p);
-        }
         __syncthreads();   // the stages are free again
     }
 }
 
-// Adds the partial results of one unit's ranges for one head, in range order.
+// Adds the partial results of one unit's ranges for one head: warp w takes
+// every 4th range from w on, then the warps are added in order.
+constexpr int JOIN_WARPS = 4;
 template <typename QT>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p, int heads_per_unit) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_constant__ Params p, int heads_per_unit) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int4 w = __ldcg(p.meta + blockIdx.x);
     if (w.x < 0) return;
     const PagedAttnArgs &a = p.a;
     const int s = w.x, kvh = w.y / p.parts, h0 = kvh * p.group + (w.y % p.parts) * heads_per_unit;
-    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (h0 + h >= (kvh + 1) * p.group) return;
     const int c0 = w.z >> 1, n = w.w - c0 + 1;
     auto slot = [&](int i) {   // the unit's first range may be its CTA's second segment
         return p.slots + (static_cast<size_t>(i == 0 ? w.z : 2 * (c0 + i)) * heads_per_unit + h) * SLOT_ROW;
     };
-    __shared__ float red[4];
+    __shared__ float4 sum[JOIN_WARPS][32];
+    __shared__ float weight[JOIN_WARPS];
     float top = -INFINITY;
-    for (int i = tid; i < n; i += 128) top = fmaxf(top, __ldcg(slot(i) + 128));
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(slot(i) + 128));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
-    if (lane == 0) red[tid >> 5] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     const float base = top == -INFINITY ? 0.0f : top;
-    float l = 0.0f, y = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
+    float l = 0.0f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = warp; i < n; i += JOIN_WARPS) {
         const float *sp = slot(i);
-        const float f = ex2(__ldcg(sp + 128) - base);
-        l = fmaf(__ldcg(sp + 129), f, l);
-        y = fmaf(__ldcg(sp + tid), f, y);
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(sp + 128));
+        const float4 v = ld_in(reinterpret_cast<const float4 *>(sp) + lane);
+        const float f = ex2(ml.x - base);
+        l = fmaf(ml.y, f, l);
+        y.x = fmaf(v.x, f, y.x);
+        y.y = fmaf(v.y, f, y.y);
+        y.z = fmaf(v.z, f, y.z);
+        y.w = fmaf(v.w, f, y.w);
+    }
+    sum[warp][lane] = y;
+    if (lane == 0) weight[warp] = l;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int v = 1; v < JOIN_WARPS; ++v) {
+        const float4 z = sum[v][lane];
+        y.x += z.x;
+        y.y += z.y;
+        y.z += z.z;
+        y.w += z.w;
+        l += weight[v];
     }
     const size_t row = static_cast<size_t>(s) * a.nheads + h0 + h;
-    y *= l == 0.0f ? 0.0f : 1.0f / l;
-    if constexpr (sizeof(QT) == 4)
-        static_cast<float *>(a.out)[row * 128 + tid] = y;
-    else
-        static_cast<QT *>(a.out)[row * 128 + tid] = static_cast<QT>(y);
-    if (tid == 0) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    store4(static_cast<QT *>(a.out) + row * 128 + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+    if (lane == 0) {
         const float e = l == 0.0f ? -INFINITY : top + log2f(l);
         if (a.lse != nullptr) a.lse[row] = e * LN2;
         if (p.lse2 != nullptr) p.lse2[row] = e;
     }
 }
 
-// mass_out = mass + sum over the heads, in head order, of the weights of the
-// kept logits. One thread per 4 cells, so a row of logits is read in 512-byte
-// pieces per warp; cells that are not visible keep their mass.
-__global__ void __launch_bounds__(256) mass_kernel(const __grid_constant__ Params p) {
+// mass_out = mass + sum over the heads of the weights of the kept logits. A
+// block takes 256 cells, 4 per thread, and 4 groups of threads every fourth
+// head each, added in order. Cells that are not visible keep their mass.
+constexpr int MASS_CELLS = 256, MASS_GROUPS = 4;
+__global__ void __launch_bounds__(MASS_CELLS) mass_kernel(const __grid_constant__ Params p) {
     grid_dependency_wait();
     grid_launch_dependents();
+    __shared__ float4 part[MASS_GROUPS - 1][MASS_CELLS / 4];
     const PagedAttnArgs &a = p.a;
-    const int s = blockIdx.y;
+    const int s = blockIdx.y, quad = threadIdx.x % (MASS_CELLS / 4), group = threadIdx.x / (MASS_CELLS / 4);
     const Span v = visible(p, s);
-    const int len = v.n + v.shift;                  // sinks + window + what lies between
     const float *mass = a.mass + s * a.mass_stride;
     float *out = a.mass_out + s * a.mass_stride;
     const float *lse = p.lse2 + static_cast<size_t>(s) * a.nheads;
-    for (int i = (blockIdx.x * 256 + threadIdx.x) * 4; i < v.n; i += gridDim.x * 1024) {
-        float got[4] = {0.f, 0.f, 0.f, 0.f};
-        const float *lp = p.logits + static_cast<size_t>(s) * a.nheads * p.stride + i;
+    for (int i0 = blockIdx.x * MASS_CELLS; i0 < v.n; i0 += gridDim.x * MASS_CELLS) {
+        const int i = i0 + 4 * quad;
+        float4 got = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < v.n) {
+            const float *lp = p.logits + static_cast<size_t>(s) * a.nheads * p.stride + i;
 #pragma unroll 8
-        for (int h = 0; h < a.nheads; ++h) {
-            const float e = __ldcg(lse + h);
-            const float4 x = ld_in(reinterpret_cast<const float4 *>(lp + static_cast<size_t>(h) * p.stride));
-            if (e == -INFINITY) continue;
-            got[0] += ex2(x.x - e);
-            got[1] += ex2(x.y - e);
-            got[2] += ex2(x.z - e);
-            got[3] += ex2(x.w - e);
+            for (int h = group; h < a.nheads; h += MASS_GROUPS) {
+                const float e = __ldcg(lse + h);
+                const float4 x = ld_in(reinterpret_cast<const float4 *>(lp + static_cast<size_t>(h) * p.stride));
+                const float base = e == -INFINITY ? INFINITY : e;   // no visible cell: weight 0
+                got.x += ex2(x.x - base);
+                got.y += ex2(x.y - base);
+                got.z += ex2(x.z - base);
+                got.w += ex2(x.w - base);
+            }
         }
+        if (group > 0) part[group - 1][quad] = got;
+        __syncthreads();
+        if (group == 0 && i < v.n) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i + k < v.n) out[v.cell(i + k)] = __ldcg(mass + v.cell(i + k)) + got[k];
+            for (int g = 0; g < MASS_GROUPS - 1; ++g) {
+                const float4 z = part[g][quad];
+                got.x += z.x;
+                got.y += z.y;
+                got.z += z.z;
+                got.w += z.w;
+            }
+            const float add[4] = {got.x, got.y, got.z, got.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k < v.n) out[v.cell(i + k)] = __ldcg(mass + v.cell(i + k)) + add[k];
+        }
+        __syncthreads();
     }
-    if (out != mass && v.shift > 0)
-        for (int j = v.sinks + blockIdx.x * 256 + threadIdx.x; j < v.sinks + v.shift; j += gridDim.x * 256)
-            if (j < len) out[j] = __ldcg(mass + j);
+    if (out != mass)
+        for (int j = v.sinks + blockIdx.x * MASS_CELLS + threadIdx.x; j < v.sinks + v.shift; j += gridDim.x * MASS_CELLS)
+            out[j] = __ldcg(mass + j);
 }
 
 struct Layout {
@@ -761,9 +816,9 @@ cudaError_t run(const Params &p, int grid, cudaStream_t stream) {
         if (e == cudaSuccess) configured_device = dev;
     }
     if (e == cudaSuccess) e = launch(kernel, dim3(grid), THREADS, smem, stream, p);
-    if (e == cudaSuccess) e = launch(join_kernel<QT>, dim3(grid, std::min(p.group, 8 * kMT)), 128, 0, stream, p, 8 * kMT);
+    if (e == cudaSuccess) e = launch(join_kernel<QT>, dim3(grid, std::min(p.group, 8 * kMT)), 32 * JOIN_WARPS, 0, stream, p, 8 * kMT);
     if (e == cudaSuccess && p.logits != nullptr)
-        e = launch(mass_kernel, dim3(std::min((p.stride + 1023) / 1024, 64), p.a.nseq), 256, 0, stream, p);
+        e = launch(mass_kernel, dim3(std::min((p.stride + MASS_CELLS - 1) / MASS_CELLS, 512), p.a.nseq), MASS_CELLS, 0, stream, p);
     return e;
 }
 
