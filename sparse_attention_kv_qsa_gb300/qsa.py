@@ -9,6 +9,7 @@ if the library is missing, importing the functions raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -470,17 +471,27 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _tensor(t: torch.Tensor, name: str, dtypes: tuple, ndim: int, index: int) -> tuple[int, ...]:
     """Checks for a CUDA tensor on device `index` of one of `dtypes` and `ndim` dimensions, contiguous in the
-    last; returns its strides."""
+    last; returns its strides. (These calls are short on the GPU: the checks are kept to a few attribute reads.)"""
+    try:
+        if t.get_device() == index and t.dtype in dtypes:
+            st = t.stride()
+            if len(st) == ndim and (st[-1] == 1 or t.shape[-1] <= 1):
+                return st
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    st = t.stride()
-    if len(st) != ndim or (st[-1] != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name} must be a {ndim}-d tensor, contiguous in its last dimension")
-    return st
+    raise ValueError(f"{name} must be a {ndim}-d tensor, contiguous in its last dimension")
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
 def _rows(t: torch.Tensor, st: tuple[int, ...]) -> int:
@@ -499,14 +510,13 @@ def _outer3(t: torch.Tensor, st: tuple[int, ...]) -> tuple[int, int, int]:
     return (st[0] if n[0] > 1 else 0), (st[1] if n[1] > 1 else 0), (st[2] if n[2] > 1 else 0)
 
 
-def _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16) -> tuple[KVPages, int]:
-    """The pool's description and its device's index."""
-    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
-        raise ValueError("k_pages must be a CUDA tensor")
-    index, dtype, shape = k_pages.get_device(), k_pages.dtype, k_pages.shape
-    st = _outer3(k_pages, _tensor(k_pages, "k_pages", _PAGE_TYPES, 4, index))
+def _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16, index: int) -> KVPages:
+    """The pool's description."""
+    dtype, shape = k_pages.dtype, k_pages.shape
+    kst = _tensor(k_pages, "k_pages", _PAGE_TYPES, 4, index)
     vst = _tensor(v_pages, "v_pages", (dtype,), 4, index)
-    if shape[3] != D or v_pages.shape != shape or _outer3(v_pages, vst) != st:
+    st = _outer3(k_pages, kst)
+    if shape[3] != D or v_pages.shape != shape or (vst != kst and _outer3(v_pages, vst) != st):
         raise ValueError("k_pages and v_pages must both be [npages, page_size, nkv, 128], of the same strides")
     if dtype == torch.int8:
         for name, t in (("k_scale_f16", k_scale_f16), ("v_scale_f16", v_scale_f16)):
@@ -516,20 +526,22 @@ def _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16) -> tuple[KVPages, int]
         sst = _outer3(k_scale_f16, k_scale_f16.stride())
         if _outer3(v_scale_f16, v_scale_f16.stride()) != sst:
             raise ValueError("k_scale_f16 and v_scale_f16 must have the same strides")
-        return KVPages(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale_f16), _ptr(v_scale_f16), I8, shape[0], shape[1],
-                       shape[2], *st, *sst), index
+        return KVPages(k_pages.data_ptr(), v_pages.data_ptr(), k_scale_f16.data_ptr(), v_scale_f16.data_ptr(), I8,
+                       shape[0], shape[1], shape[2], *st, *sst)
     if k_scale_f16 is not None or v_scale_f16 is not None:
         raise ValueError("scales are for int8 pages only")
-    return KVPages(_ptr(k_pages), _ptr(v_pages), None, None, _DTYPE[dtype], shape[0], shape[1], shape[2], *st,
-                   0, 0, 0), index
+    return KVPages(k_pages.data_ptr(), v_pages.data_ptr(), None, None, _DTYPE[dtype], shape[0], shape[1], shape[2],
+                   *st)
 
 
-def _table(table, lens, index) -> int:
+def _table(table, lens, index) -> tuple[int, int, int]:
+    """(rows, columns, row stride)"""
     st = _tensor(table, "page_table", _INT, 2, index)
     _tensor(lens, "lens", _INT, 1, index)
-    if lens.shape[0] != table.shape[0]:
+    rows, cols = table.shape
+    if lens.shape[0] != rows:
         raise ValueError("page_table and lens must have one row per sequence")
-    return _rows(table, st)
+    return rows, cols, st[0] if rows > 1 else cols
 
 
 def _made(t, name, shape, dtype, device):
@@ -547,14 +559,15 @@ def _scratch(t, need, device):
     if t is None:
         if need == 0:
             return None, 0, None
-        t = torch.empty((need,), dtype=torch.uint8, device=device)
+        t = torch.empty(need, dtype=torch.uint8, device=device)
         return t.data_ptr(), need, t
     _tensor(t, "scratch", _BYTE, 1, device.index)
     if t.numel() < need:
         raise ValueError(f"scratch must have at least {need} bytes")
-    return _ptr(t), t.numel(), t
+    return t.data_ptr(), t.numel(), t
 
 
+@functools.lru_cache(maxsize=4096)
 def paged_attn_scratch_bytes(nseq: int, nheads: int, nkv: int, table_cols: int, page_size: int,
                              with_mass: bool = False) -> int:
     """``qsa_paged_attn_scratch_bytes``: scratch bytes paged_attn needs."""
@@ -579,42 +592,47 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, pa
     received, summed over the heads, is added into ``mass_out`` (default:
     ``mass`` itself). ``scratch``: a uint8 tensor of
     ``paged_attn_scratch_bytes`` bytes, allocated when not given."""
-    kv, index = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16)
+    index = _device_of(k_pages, "k_pages")
+    kv = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16, index)
+    kind, page_size, nkv = kv.dtype, kv.page_size, kv.nkv
+    qst = _tensor(q, "q", _Q_TYPES if kind == I8 else (k_pages.dtype,), 3, index)
     dev, dtype = k_pages.device, q.dtype
-    qst = _tensor(q, "q", _Q_TYPES if kv.dtype == I8 else (k_pages.dtype,), 3, index)
     nseq, nheads, d = q.shape
-    if d != D or nheads < 1 or nheads % kv.nkv:
-        raise ValueError(f"q must be [nseq, a multiple of {kv.nkv}, {D}]")
-    tstride = _table(page_table, lens, index)
-    rows, cols = page_table.shape
+    if d != D or nheads < 1 or nkv < 1 or nheads % nkv:
+        raise ValueError(f"q must be [nseq, a multiple of {nkv}, {D}]")
+    rows, cols, tstride = _table(page_table, lens, index)
     if rows != nseq:
         raise ValueError("page_table must have one row per query")
     out = _made(out, "out", (nseq, nheads, D), dtype, dev)
     lse = _made(lse, "lse", (nseq, nheads), torch.float32, dev)
-    mstride = 0
+    mstride, mp, mop = 0, None, None
     if mass is not None:
         mass_out = mass if mass_out is None else mass_out
         for name, t in (("mass", mass), ("mass_out", mass_out)):
             st = _tensor(t, name, _FLOAT, 2, index)
-            if t.shape[0] != nseq or t.shape[1] < cols * kv.page_size:
-                raise ValueError(f"{name} must be [{nseq}, >= {cols * kv.page_size}]")
+            if t.shape[0] != nseq or t.shape[1] < cols * page_size:
+                raise ValueError(f"{name} must be [{nseq}, >= {cols * page_size}]")
             # of one row any stride will do
             if t is mass:
                 mstride = st[0] if nseq > 1 else max(t.shape[1], mass_out.shape[1])
             elif nseq > 1 and st[0] != mstride:
                 raise ValueError("mass and mass_out must have the same strides")
+        mp, mop = mass.data_ptr(), mass_out.data_ptr()
     elif mass_out is not None:
         raise ValueError("mass_out needs mass")
-    need = lib().qsa_paged_attn_scratch_bytes(nseq, nheads, kv.nkv, cols, kv.page_size, mass is not None)
-    sp, sbytes, scratch = _scratch(scratch, need, dev)
-    q0, q1 = _outer2(q, qst)
-    _check(lib().qsa_paged_attn(_ptr(q), _DTYPE[dtype], q0, q1, nseq, nheads, kv, _ptr(page_table), cols, tstride,
-                                _ptr(lens), window, sinks, SOFTMAX_SCALE if scale is None else scale, _ptr(out),
-                                _ptr(lse), _ptr(mass), _ptr(mass_out), mstride, sp, sbytes, _raw_stream(index)),
-           "qsa_paged_attn")
+    sp, sbytes, scratch = _scratch(
+        scratch, paged_attn_scratch_bytes(nseq, nheads, nkv, cols, page_size, mass is not None), dev)
+    status = (_lib or lib()).qsa_paged_attn(
+        q.data_ptr(), _DTYPE[dtype], qst[0] if nseq > 1 else 0, qst[1] if nheads > 1 else 0, nseq, nheads, kv,
+        page_table.data_ptr(), cols, tstride, lens.data_ptr(), window, sinks,
+        SOFTMAX_SCALE if scale is None else scale, out.data_ptr(), lse.data_ptr(), mp, mop, mstride, sp, sbytes,
+        _raw_stream(index))
+    if status != QSA_OK:
+        raise QSAError(status, "qsa_paged_attn")
     return out, lse
 
 
+@functools.lru_cache(maxsize=4096)
 def window_attn_scratch_bytes(nseq: int, total_q: int, max_q: int, nheads: int, nkv: int) -> int:
     """``qsa_window_attn_scratch_bytes``: scratch bytes window_attn needs."""
     return int(lib().qsa_window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv))
@@ -631,10 +649,9 @@ def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     cu_k[s+1]-1``; a query sees the keys up to its own place that lie within
     the last ``window`` (all when negative) or among the first ``sinks``.
     ``max_q`` is at least the longest sequence's query count."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
-    dev, index, dtype = q.device, q.get_device(), q.dtype
+    index = _device_of(q, "q")
     qst = _tensor(q, "q", _PAGE_TYPES[:2], 3, index)
+    dev, dtype = q.device, q.dtype
     kst = _tensor(k, "k", (dtype,), 3, index)
     vst = _tensor(v, "v", (dtype,), 3, index)
     total_q, nheads, d = q.shape
@@ -651,13 +668,14 @@ def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     max_q = min(max_q, total_q)
     out = _made(out, "out", (total_q, nheads, D), dtype, dev)
     lse = _made(lse, "lse", (total_q, nheads), torch.float32, dev)
-    need = lib().qsa_window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv)
-    sp, sbytes, scratch = _scratch(scratch, need, dev)
+    sp, sbytes, scratch = _scratch(scratch, window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv), dev)
     strides = _Strides6(*_outer2(q, qst), *_outer2(k, kst), *_outer2(v, vst))
-    _check(lib().qsa_window_attn(_ptr(q), _ptr(k), _ptr(v), _DTYPE[dtype], strides, _ptr(cu_q), _ptr(cu_k), nseq,
-                                 total_q, total_k, max_q, nheads, nkv, window, sinks,
-                                 SOFTMAX_SCALE if scale is None else scale, _ptr(out), _ptr(lse), sp, sbytes,
-                                 _raw_stream(index)), "qsa_window_attn")
+    status = (_lib or lib()).qsa_window_attn(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPE[dtype], strides, cu_q.data_ptr(), cu_k.data_ptr(), nseq,
+        total_q, total_k, max_q, nheads, nkv, window, sinks, SOFTMAX_SCALE if scale is None else scale,
+        out.data_ptr(), lse.data_ptr(), sp, sbytes, _raw_stream(index))
+    if status != QSA_OK:
+        raise QSAError(status, "qsa_window_attn")
     return out, lse
 
 
@@ -675,30 +693,32 @@ def cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.
     ``new_mass`` fp32 ``[nseq, >= budget]`` (default ``new_table.shape[1] *
     page_size`` columns): the kept masses, then zeros. Pages of ``new_table``
     must be none that ``page_table`` still uses."""
-    kv, index = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16)
-    dev = k_pages.device
-    tstride = _table(page_table, lens, index)
-    nseq, cols = page_table.shape
+    index = _device_of(k_pages, "k_pages")
+    kv = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16, index)
+    dev, page_size = k_pages.device, kv.page_size
+    nseq, cols, tstride = _table(page_table, lens, index)
     nst = _tensor(new_table, "new_table", _INT, 2, index)
     mst = _tensor(mass, "mass", _FLOAT, 2, index)
     new_rows, new_cols = new_table.shape
     if new_rows != nseq:
         raise ValueError("new_table must have one row per sequence")
-    if mass.shape[0] != nseq or mass.shape[1] < cols * kv.page_size:
-        raise ValueError(f"mass must be [{nseq}, >= {cols * kv.page_size}]")
-    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget or budget > new_cols * kv.page_size:
+    if mass.shape[0] != nseq or mass.shape[1] < cols * page_size:
+        raise ValueError(f"mass must be [{nseq}, >= {cols * page_size}]")
+    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget or budget > new_cols * page_size:
         raise ValueError("budget must be at least 1 and sinks + recent, and fit the new table's pages")
     kept = _made(kept, "kept", (nseq, budget), torch.int32, dev)
     new_lens = _made(new_lens, "new_lens", (nseq,), torch.int32, dev)
     if new_mass is None:
-        new_mass = torch.empty((nseq, new_cols * kv.page_size), dtype=torch.float32, device=dev)
+        new_mass = torch.empty((nseq, new_cols * page_size), dtype=torch.float32, device=dev)
     nmst = _tensor(new_mass, "new_mass", _FLOAT, 2, index)
     if new_mass.shape[0] != nseq or new_mass.shape[1] < budget:
         raise ValueError(f"new_mass must be [{nseq}, >= {budget}]")
-    _check(lib().qsa_cache_evict(kv, nseq, _ptr(page_table), cols, tstride, _ptr(lens), _ptr(mass), _rows(mass, mst),
-                                 _ptr(new_table), new_cols, _rows(new_table, nst), budget, sinks, recent, _ptr(kept),
-                                 _ptr(new_lens), _ptr(new_mass), _rows(new_mass, nmst), new_mass.shape[1],
-                                 _raw_stream(index)), "qsa_cache_evict")
+    status = (_lib or lib()).qsa_cache_evict(
+        kv, nseq, page_table.data_ptr(), cols, tstride, lens.data_ptr(), mass.data_ptr(), _rows(mass, mst),
+        new_table.data_ptr(), new_cols, nst[0] if nseq > 1 else new_cols, budget, sinks, recent, kept.data_ptr(),
+        new_lens.data_ptr(), new_mass.data_ptr(), _rows(new_mass, nmst), new_mass.shape[1], _raw_stream(index))
+    if status != QSA_OK:
+        raise QSAError(status, "qsa_cache_evict")
     return kept, new_lens, new_mass
 
 
