@@ -804,26 +804,27 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
         ref[r] = -INFINITY;
         l[r] = 0.0f;
         y[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int z = lane; valid[r] && z < w.parts; z += 32) ref[r] = fmaxf(ref[r], __ldcg(slot + z * NEXT + r * SLOT_ROW + 128));
     }
-#pragma unroll
-    for (int r = 0; r < JOIN_ROWS; ++r)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ref[r] = fmaxf(ref[r], __shfl_xor_sync(FULL_MASK, ref[r], o));
 #pragma unroll 2
     for (int z = 0; z < w.parts; ++z) {
+        float2 m[JOIN_ROWS];
+        float4 v[JOIN_ROWS];
 #pragma unroll
         for (int r = 0; r < JOIN_ROWS; ++r) {
-            if (!valid[r]) continue;
             const float *sp = slot + z * NEXT + r * SLOT_ROW;
-            const float2 m = __ldcg(reinterpret_cast<const float2 *>(sp + 128));
-            const float4 v = ld_in(reinterpret_cast<const float4 *>(sp) + lane);
-            const float f = exp2_approx(m.x - (ref[r] == -INFINITY ? 0.0f : ref[r]));
-            l[r] = fmaf(m.y, f, l[r]);
-            y[r].x = fmaf(v.x, f, y[r].x);
-            y[r].y = fmaf(v.y, f, y[r].y);
-            y[r].z = fmaf(v.z, f, y[r].z);
-            y[r].w = fmaf(v.w, f, y[r].w);
+            m[r] = valid[r] ? __ldcg(reinterpret_cast<const float2 *>(sp + 128)) : make_float2(-INFINITY, 0.0f);
+            v[r] = valid[r] ? ld_in(reinterpret_cast<const float4 *>(sp) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int r = 0; r < JOIN_ROWS; ++r) {
+            const float top = fmaxf(ref[r], m[r].x), base = top == -INFINITY ? 0.0f : top;
+            const float e = exp2_approx(ref[r] - base), f = exp2_approx(m[r].x - base);
+            ref[r] = top;
+            l[r] = fmaf(m[r].y, f, l[r] * e);
+            y[r].x = fmaf(v[r].x, f, y[r].x * e);
+            y[r].y = fmaf(v[r].y, f, y[r].y * e);
+            y[r].z = fmaf(v[r].z, f, y[r].z * e);
+            y[r].w = fmaf(v[r].w, f, y[r].w * e);
         }
     }
 #pragma unroll
