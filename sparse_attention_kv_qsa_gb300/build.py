@@ -1,8 +1,11 @@
-"""Builds ``libqsa.so`` (the C ABI of include/qsa.h) for sm_103a with nvcc.
+"""Builds ``libqsa.so`` (the C ABI of include/qsa.h) for sm_103a with nvcc, and
+``qsa_ops.so``, the Python module that binds the bounded-cache calls to torch.
 
-Each CUDA source compiles to an object in parallel, then one link step makes
-the shared library in ``_build/``. The CUDA runtime is linked statically, so
-the library needs only the driver at run time.
+Each CUDA source compiles to an object in parallel (the module's one C++ source
+beside them), then one link step makes the shared library in ``_build/`` and
+another the module, which links to it. The CUDA runtime is linked statically
+into ``libqsa.so``, so the library needs only the driver at run time; the module
+needs the torch that it was built against.
 """
 
 from __future__ import annotations
@@ -11,6 +14,7 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libqsa.so")
 INCLUDE = os.path.join(ROOT, "include")
+BINDING = os.path.join(HERE, "binding", "qsa_ops.cpp")
+OPS = os.path.join(BUILD, "qsa_ops.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -54,8 +60,43 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_binding(force: bool) -> str:
+    """qsa_ops.o; rebuilt when its source, the header or the torch version changed."""
+    import torch
+    tag = torch.__version__.replace("+", "_")
+    obj = os.path.join(BUILD, f"qsa_ops.{tag}.obj")
+    newest = max(os.path.getmtime(BINDING), os.path.getmtime(os.path.join(INCLUDE, "qsa.h")))
+    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= newest:
+        return obj
+    t = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", t,
+           "-I", os.path.join(t, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"], "-I", cuda,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-c", BINDING, "-o", obj + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING}:\n{r.stdout}\n{r.stderr}")
+    os.replace(obj + ".tmp", obj)
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    lib = os.path.join(_torch_dir(), "lib")
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", OPS + ".tmp", obj, "-L", BUILD, "-l:libqsa.so", "-L", lib,
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {OPS} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(OPS + ".tmp", OPS)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every CUDA source and link libqsa.so; returns its path."""
+    """Compile every CUDA source and link libqsa.so, then qsa_ops.so; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     if force:
@@ -63,14 +104,18 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             if f.endswith(".o"):
                 os.remove(os.path.join(BUILD, f))
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1 + min(8, len(srcs))) as ex:
+        binding = ex.submit(_compile_binding, force)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        ops = binding.result()
     if force or extra or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         cmd = [nvcc(), *ARCH, "-shared", "-o", LIB + ".tmp", *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(LIB + ".tmp", LIB)
+    if force or not os.path.exists(OPS) or os.path.getmtime(OPS) < max(os.path.getmtime(ops), os.path.getmtime(LIB)):
+        _link_binding(ops)
     return LIB
 
 

@@ -2,14 +2,16 @@
 
 Every step of the selection runs in ``libqsa.so``'s CUDA kernels; this module
 checks tensor shapes, dtypes and devices, allocates outputs with torch, and
-passes raw device pointers and the current CUDA stream. There is no fallback:
-if the library is missing, importing the functions raises.
+passes raw device pointers and the current CUDA stream. The bounded-cache calls
+(``window_attn``, ``paged_attn``, ``cache_evict``) do the same in the compiled
+module ``qsa_ops.so``, whose checks take a few microseconds less of each call.
+There is no fallback: if a library is missing, calling the functions raises.
 """
 
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 
 import torch
@@ -459,115 +461,23 @@ def block_summary(k_cells: torch.Tensor, k_scale_f16: torch.Tensor, block_begin:
                                    _ptr(kblk_q8), _ptr(kblk_scale_f16), _stream(k_cells)), "qsa_block_summary")
 
 
-_DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.int8: I8}
-_PAGE_TYPES = (torch.bfloat16, torch.float16, torch.int8)
-_Q_TYPES = (torch.bfloat16, torch.float16, torch.float32)
-_FLOAT, _INT, _BYTE = (torch.float32,), (torch.int32,), (torch.uint8,)
-_Strides6 = ctypes.c_int64 * 6
-# The current stream's handle by device index (torch.cuda.current_stream builds a Stream object around it).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_ops_module = None
 
 
-def _tensor(t: torch.Tensor, name: str, dtypes: tuple, ndim: int, index: int) -> tuple[int, ...]:
-    """Checks for a CUDA tensor on device `index` of one of `dtypes` and `ndim` dimensions, contiguous in the
-    last; returns its strides. (These calls are short on the GPU: the checks are kept to a few attribute reads.)"""
-    try:
-        if t.get_device() == index and t.dtype in dtypes:
-            st = t.stride()
-            if len(st) == ndim and (st[-1] == 1 or t.shape[-1] <= 1):
-                return st
-    except AttributeError:
-        pass
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    raise ValueError(f"{name} must be a {ndim}-d tensor, contiguous in its last dimension")
+def _ops():
+    """``qsa_ops.so``, the compiled binding of the bounded-cache calls (raises if it has not been built)."""
+    global _ops_module
+    if _ops_module is None:
+        lib()
+        if not os.path.exists(_build.OPS):
+            raise RuntimeError(f"{_build.OPS} is missing: build it with __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("qsa_ops", _build.OPS)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _ops_module = module
+    return _ops_module
 
 
-def _device_of(t: torch.Tensor, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
-
-
-def _rows(t: torch.Tensor, st: tuple[int, ...]) -> int:
-    """Row stride of a 2-d tensor (the stride of a dimension of one element is arbitrary in torch)."""
-    n = t.shape
-    return st[0] if n[0] > 1 else n[1]
-
-
-def _outer2(t: torch.Tensor, st: tuple[int, ...]) -> tuple[int, int]:
-    n = t.shape
-    return (st[0] if n[0] > 1 else 0), (st[1] if n[1] > 1 else 0)
-
-
-def _outer3(t: torch.Tensor, st: tuple[int, ...]) -> tuple[int, int, int]:
-    n = t.shape
-    return (st[0] if n[0] > 1 else 0), (st[1] if n[1] > 1 else 0), (st[2] if n[2] > 1 else 0)
-
-
-def _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16, index: int) -> KVPages:
-    """The pool's description."""
-    dtype, shape = k_pages.dtype, k_pages.shape
-    kst = _tensor(k_pages, "k_pages", _PAGE_TYPES, 4, index)
-    vst = _tensor(v_pages, "v_pages", (dtype,), 4, index)
-    st = _outer3(k_pages, kst)
-    if shape[3] != D or v_pages.shape != shape or (vst != kst and _outer3(v_pages, vst) != st):
-        raise ValueError("k_pages and v_pages must both be [npages, page_size, nkv, 128], of the same strides")
-    if dtype == torch.int8:
-        for name, t in (("k_scale_f16", k_scale_f16), ("v_scale_f16", v_scale_f16)):
-            if (not isinstance(t, torch.Tensor) or t.get_device() != index or t.element_size() != 2
-                    or t.shape != shape[:3]):
-                raise ValueError(f"{name} must be [npages, page_size, nkv] binary16 values beside int8 pages")
-        sst = _outer3(k_scale_f16, k_scale_f16.stride())
-        if _outer3(v_scale_f16, v_scale_f16.stride()) != sst:
-            raise ValueError("k_scale_f16 and v_scale_f16 must have the same strides")
-        return KVPages(k_pages.data_ptr(), v_pages.data_ptr(), k_scale_f16.data_ptr(), v_scale_f16.data_ptr(), I8,
-                       shape[0], shape[1], shape[2], *st, *sst)
-    if k_scale_f16 is not None or v_scale_f16 is not None:
-        raise ValueError("scales are for int8 pages only")
-    return KVPages(k_pages.data_ptr(), v_pages.data_ptr(), None, None, _DTYPE[dtype], shape[0], shape[1], shape[2],
-                   *st)
-
-
-def _table(table, lens, index) -> tuple[int, int, int]:
-    """(rows, columns, row stride)"""
-    st = _tensor(table, "page_table", _INT, 2, index)
-    _tensor(lens, "lens", _INT, 1, index)
-    rows, cols = table.shape
-    if lens.shape[0] != rows:
-        raise ValueError("page_table and lens must have one row per sequence")
-    return rows, cols, st[0] if rows > 1 else cols
-
-
-def _made(t, name, shape, dtype, device):
-    """`t` checked as a contiguous output of that shape and type, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _tensor(t, name, (dtype,), len(shape), device.index)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}")
-    return t
-
-
-def _scratch(t, need, device):
-    """(pointer, bytes, tensor to keep until the call is made)"""
-    if t is None:
-        if need == 0:
-            return None, 0, None
-        t = torch.empty(need, dtype=torch.uint8, device=device)
-        return t.data_ptr(), need, t
-    _tensor(t, "scratch", _BYTE, 1, device.index)
-    if t.numel() < need:
-        raise ValueError(f"scratch must have at least {need} bytes")
-    return t.data_ptr(), t.numel(), t
-
-
-@functools.lru_cache(maxsize=4096)
 def paged_attn_scratch_bytes(nseq: int, nheads: int, nkv: int, table_cols: int, page_size: int,
                              with_mass: bool = False) -> int:
     """``qsa_paged_attn_scratch_bytes``: scratch bytes paged_attn needs."""
@@ -592,47 +502,14 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, pa
     received, summed over the heads, is added into ``mass_out`` (default:
     ``mass`` itself). ``scratch``: a uint8 tensor of
     ``paged_attn_scratch_bytes`` bytes, allocated when not given."""
-    index = _device_of(k_pages, "k_pages")
-    kv = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16, index)
-    kind, page_size, nkv = kv.dtype, kv.page_size, kv.nkv
-    qst = _tensor(q, "q", _Q_TYPES if kind == I8 else (k_pages.dtype,), 3, index)
-    dev, dtype = k_pages.device, q.dtype
-    nseq, nheads, d = q.shape
-    if d != D or nheads < 1 or nkv < 1 or nheads % nkv:
-        raise ValueError(f"q must be [nseq, a multiple of {nkv}, {D}]")
-    rows, cols, tstride = _table(page_table, lens, index)
-    if rows != nseq:
-        raise ValueError("page_table must have one row per query")
-    out = _made(out, "out", (nseq, nheads, D), dtype, dev)
-    lse = _made(lse, "lse", (nseq, nheads), torch.float32, dev)
-    mstride, mp, mop = 0, None, None
-    if mass is not None:
-        mass_out = mass if mass_out is None else mass_out
-        for name, t in (("mass", mass), ("mass_out", mass_out)):
-            st = _tensor(t, name, _FLOAT, 2, index)
-            if t.shape[0] != nseq or t.shape[1] < cols * page_size:
-                raise ValueError(f"{name} must be [{nseq}, >= {cols * page_size}]")
-            # of one row any stride will do
-            if t is mass:
-                mstride = st[0] if nseq > 1 else max(t.shape[1], mass_out.shape[1])
-            elif nseq > 1 and st[0] != mstride:
-                raise ValueError("mass and mass_out must have the same strides")
-        mp, mop = mass.data_ptr(), mass_out.data_ptr()
-    elif mass_out is not None:
-        raise ValueError("mass_out needs mass")
-    sp, sbytes, scratch = _scratch(
-        scratch, paged_attn_scratch_bytes(nseq, nheads, nkv, cols, page_size, mass is not None), dev)
-    status = (_lib or lib()).qsa_paged_attn(
-        q.data_ptr(), _DTYPE[dtype], qst[0] if nseq > 1 else 0, qst[1] if nheads > 1 else 0, nseq, nheads, kv,
-        page_table.data_ptr(), cols, tstride, lens.data_ptr(), window, sinks,
-        SOFTMAX_SCALE if scale is None else scale, out.data_ptr(), lse.data_ptr(), mp, mop, mstride, sp, sbytes,
-        _raw_stream(index))
-    if status != QSA_OK:
-        raise QSAError(status, "qsa_paged_attn")
-    return out, lse
+    r = (_ops_module or _ops()).paged_attn(
+        q, k_pages, v_pages, page_table, lens, k_scale_f16, v_scale_f16, window, sinks,
+        SOFTMAX_SCALE if scale is None else scale, mass, mass_out, out, lse, scratch)
+    if r.__class__ is int:
+        raise QSAError(r, "qsa_paged_attn")
+    return r
 
 
-@functools.lru_cache(maxsize=4096)
 def window_attn_scratch_bytes(nseq: int, total_q: int, max_q: int, nheads: int, nkv: int) -> int:
     """``qsa_window_attn_scratch_bytes``: scratch bytes window_attn needs."""
     return int(lib().qsa_window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv))
@@ -649,34 +526,11 @@ def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     cu_k[s+1]-1``; a query sees the keys up to its own place that lie within
     the last ``window`` (all when negative) or among the first ``sinks``.
     ``max_q`` is at least the longest sequence's query count."""
-    index = _device_of(q, "q")
-    qst = _tensor(q, "q", _PAGE_TYPES[:2], 3, index)
-    dev, dtype = q.device, q.dtype
-    kst = _tensor(k, "k", (dtype,), 3, index)
-    vst = _tensor(v, "v", (dtype,), 3, index)
-    total_q, nheads, d = q.shape
-    total_k, nkv, kd = k.shape
-    if d != D or kd != D or v.shape != k.shape or nkv < 1 or nheads < 1 or nheads % nkv:
-        raise ValueError("q must be [total_q, nheads, 128] and k, v [total_k, nkv, 128] with nheads a multiple of nkv")
-    _tensor(cu_q, "cu_q", _INT, 1, index)
-    _tensor(cu_k, "cu_k", _INT, 1, index)
-    nseq = cu_q.shape[0] - 1
-    if cu_k.shape[0] - 1 != nseq or nseq < 0:
-        raise ValueError("cu_q and cu_k must both have one more element than there are sequences")
-    if max_q < 0:
-        raise ValueError("max_q must not be negative")
-    max_q = min(max_q, total_q)
-    out = _made(out, "out", (total_q, nheads, D), dtype, dev)
-    lse = _made(lse, "lse", (total_q, nheads), torch.float32, dev)
-    sp, sbytes, scratch = _scratch(scratch, window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv), dev)
-    strides = _Strides6(*_outer2(q, qst), *_outer2(k, kst), *_outer2(v, vst))
-    status = (_lib or lib()).qsa_window_attn(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPE[dtype], strides, cu_q.data_ptr(), cu_k.data_ptr(), nseq,
-        total_q, total_k, max_q, nheads, nkv, window, sinks, SOFTMAX_SCALE if scale is None else scale,
-        out.data_ptr(), lse.data_ptr(), sp, sbytes, _raw_stream(index))
-    if status != QSA_OK:
-        raise QSAError(status, "qsa_window_attn")
-    return out, lse
+    r = (_ops_module or _ops()).window_attn(
+        q, k, v, cu_q, cu_k, max_q, window, sinks, SOFTMAX_SCALE if scale is None else scale, out, lse, scratch)
+    if r.__class__ is int:
+        raise QSAError(r, "qsa_window_attn")
+    return r
 
 
 def cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
@@ -693,33 +547,11 @@ def cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.
     ``new_mass`` fp32 ``[nseq, >= budget]`` (default ``new_table.shape[1] *
     page_size`` columns): the kept masses, then zeros. Pages of ``new_table``
     must be none that ``page_table`` still uses."""
-    index = _device_of(k_pages, "k_pages")
-    kv = _kv_pages(k_pages, v_pages, k_scale_f16, v_scale_f16, index)
-    dev, page_size = k_pages.device, kv.page_size
-    nseq, cols, tstride = _table(page_table, lens, index)
-    nst = _tensor(new_table, "new_table", _INT, 2, index)
-    mst = _tensor(mass, "mass", _FLOAT, 2, index)
-    new_rows, new_cols = new_table.shape
-    if new_rows != nseq:
-        raise ValueError("new_table must have one row per sequence")
-    if mass.shape[0] != nseq or mass.shape[1] < cols * page_size:
-        raise ValueError(f"mass must be [{nseq}, >= {cols * page_size}]")
-    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget or budget > new_cols * page_size:
-        raise ValueError("budget must be at least 1 and sinks + recent, and fit the new table's pages")
-    kept = _made(kept, "kept", (nseq, budget), torch.int32, dev)
-    new_lens = _made(new_lens, "new_lens", (nseq,), torch.int32, dev)
-    if new_mass is None:
-        new_mass = torch.empty((nseq, new_cols * page_size), dtype=torch.float32, device=dev)
-    nmst = _tensor(new_mass, "new_mass", _FLOAT, 2, index)
-    if new_mass.shape[0] != nseq or new_mass.shape[1] < budget:
-        raise ValueError(f"new_mass must be [{nseq}, >= {budget}]")
-    status = (_lib or lib()).qsa_cache_evict(
-        kv, nseq, page_table.data_ptr(), cols, tstride, lens.data_ptr(), mass.data_ptr(), _rows(mass, mst),
-        new_table.data_ptr(), new_cols, nst[0] if nseq > 1 else new_cols, budget, sinks, recent, kept.data_ptr(),
-        new_lens.data_ptr(), new_mass.data_ptr(), _rows(new_mass, nmst), new_mass.shape[1], _raw_stream(index))
-    if status != QSA_OK:
-        raise QSAError(status, "qsa_cache_evict")
-    return kept, new_lens, new_mass
+    r = (_ops_module or _ops()).cache_evict(k_pages, v_pages, page_table, lens, mass, new_table, budget, sinks, recent,
+                                           k_scale_f16, v_scale_f16, kept, new_lens, new_mass)
+    if r.__class__ is int:
+        raise QSAError(r, "qsa_cache_evict")
+    return r
 
 
 def device_error(device: torch.device | None = None) -> int:
