@@ -13,8 +13,8 @@
 // listed in order: warps take consecutive runs, count, scan, and write.
 // Latency bounds it: four cluster barriers and the scans between them.
 //
-// copy_kernel: bandwidth. A warp takes a kept cell, finds both addresses once
-// and moves the cell's heads in 16-byte pieces, all loads before the stores.
+// copy_cells_kernel, copy_pieces_kernel: bandwidth. 16-byte pieces of keys and
+// values, a batch of loads before its stores.
 #include <algorithm>
 
 #include "cache_internal.cuh"
@@ -243,14 +243,15 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
     if (cluster > 1) cluster_sync_all();   // no CTA leaves while another may read its counts
 }
 
-constexpr int COPY_THREADS = 256;
+constexpr int COPY_THREADS = 256, COPY_BATCH = 4;
 
-// kVecs: 16-byte pieces of one head's row. Each warp moves one cell at a time.
+// kVecs: 16-byte pieces of one head's row. A warp moves one cell at a time, its
+// addresses found once, up to BATCH pieces of keys and of values per lane.
 template <int kVecs>
-__global__ void __launch_bounds__(COPY_THREADS) copy_kernel(const CacheEvictArgs a, Divider page) {
+__global__ void __launch_bounds__(COPY_THREADS) copy_cells_kernel(const CacheEvictArgs a, Divider page) {
     grid_dependency_wait();
     grid_launch_dependents();
-    constexpr int ELEM = kVecs == 8 ? 1 : 2, BATCH = 4;
+    constexpr int ELEM = kVecs == 8 ? 1 : 2, BATCH = COPY_BATCH;
     const int lane = threadIdx.x & 31, s = blockIdx.y;
     const int m = ld_in(a.new_lens + s), pieces = a.kv.nkv * kVecs;
     char *k = static_cast<char *>(a.kv.k), *v = static_cast<char *>(a.kv.v);
@@ -297,6 +298,77 @@ __global__ void __launch_bounds__(COPY_THREADS) copy_kernel(const CacheEvictArgs
     }
 }
 
+// The same for cells of few pieces: a thread moves COPY_BATCH pieces of keys
+// and of values at a time, consecutive threads consecutive pieces of a
+// cell and then the next cells, so a warp is full whatever the heads' number.
+template <int kVecs>
+__global__ void __launch_bounds__(COPY_THREADS) copy_pieces_kernel(const CacheEvictArgs a, Divider page, Divider per_cell) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    constexpr int ELEM = kVecs == 8 ? 1 : 2;
+    const int s = blockIdx.y, m = ld_in(a.new_lens + s);
+    const char *k = static_cast<const char *>(a.kv.k), *v = static_cast<const char *>(a.kv.v);
+    const int32_t *kept = a.kept + static_cast<size_t>(s) * a.budget;
+    const int32_t *table = a.table + s * a.table_stride, *new_table = a.new_table + s * a.new_table_stride;
+    const long long pieces = static_cast<long long>(m) * per_cell.d, step = static_cast<long long>(gridDim.x) * COPY_THREADS;
+    // Cells and pieces in 32 bits: a thread's pieces are told apart by whole cells first.
+    for (long long t0 = static_cast<long long>(blockIdx.x) * COPY_THREADS + threadIdx.x; t0 < pieces; t0 += COPY_BATCH * step) {
+        int64_t from[COPY_BATCH], to[COPY_BATCH], scale_from[COPY_BATCH], scale_to[COPY_BATCH];
+        uint4 x[COPY_BATCH], y[COPY_BATCH];
+        int cell[COPY_BATCH], piece[COPY_BATCH], j[COPY_BATCH];
+        bool ok[COPY_BATCH];
+#pragma unroll
+        for (int b = 0; b < COPY_BATCH; ++b) {
+            const long long t = t0 + b * step;
+            ok[b] = t < pieces;
+            cell[b] = ok[b] ? (t < 0x7FFFFFFFLL ? static_cast<int>(divide(per_cell, static_cast<uint32_t>(t))) : static_cast<int>(t / per_cell.d)) : 0;
+            piece[b] = ok[b] ? static_cast<int>(t - static_cast<long long>(cell[b]) * per_cell.d) : 0;
+            j[b] = ok[b] ? ld_in(kept + cell[b]) : 0;
+        }
+#pragma unroll
+        for (int b = 0; b < COPY_BATCH; ++b) {
+            const int jp = divide(page, j[b]), ip = divide(page, cell[b]);
+            const int src = ok[b] ? ld_in(table + jp) : -1, dst = ok[b] ? ld_in(new_table + ip) : -1;
+            ok[b] = src >= 0 && src < a.kv.npages && dst >= 0 && dst < a.kv.npages;
+            const int js = j[b] - jp * a.kv.page_size, is = cell[b] - ip * a.kv.page_size, h = piece[b] / kVecs;
+            const int64_t off = h * a.kv.head_stride * ELEM + 16 * (piece[b] % kVecs);
+            from[b] = (src * a.kv.page_stride + js * a.kv.cell_stride) * ELEM + off;
+            to[b] = (dst * a.kv.page_stride + is * a.kv.cell_stride) * ELEM + off;
+            if constexpr (ELEM == 1) {
+                scale_from[b] = src * a.kv.scale_page_stride + js * a.kv.scale_cell_stride + h * a.kv.scale_head_stride;
+                scale_to[b] = dst * a.kv.scale_page_stride + is * a.kv.scale_cell_stride + h * a.kv.scale_head_stride;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < COPY_BATCH; ++b)
+            if (ok[b]) {
+                x[b] = ld_in(reinterpret_cast<const uint4 *>(k + from[b]));
+                y[b] = ld_in(reinterpret_cast<const uint4 *>(v + from[b]));
+            }
+        if constexpr (ELEM == 1) {   // the scales with each head's first piece
+            uint16_t ks[COPY_BATCH], vs[COPY_BATCH];
+#pragma unroll
+            for (int b = 0; b < COPY_BATCH; ++b)
+                if (ok[b] && piece[b] % kVecs == 0) {
+                    ks[b] = ld_in_u16(a.kv.k_scale_f16 + scale_from[b]);
+                    vs[b] = ld_in_u16(a.kv.v_scale_f16 + scale_from[b]);
+                }
+#pragma unroll
+            for (int b = 0; b < COPY_BATCH; ++b)
+                if (ok[b] && piece[b] % kVecs == 0) {
+                    a.kv.k_scale_f16[scale_to[b]] = ks[b];
+                    a.kv.v_scale_f16[scale_to[b]] = vs[b];
+                }
+        }
+#pragma unroll
+        for (int b = 0; b < COPY_BATCH; ++b)
+            if (ok[b]) {
+                *reinterpret_cast<uint4 *>(static_cast<char *>(a.kv.k) + to[b]) = x[b];
+                *reinterpret_cast<uint4 *>(static_cast<char *>(a.kv.v) + to[b]) = y[b];
+            }
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
@@ -334,16 +406,25 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
     e = cluster == 1 ? cudaLaunchKernelEx(&cfg, select_kernel<1>, a, max_keys)
                      : cudaLaunchKernelEx(&cfg, select_kernel<MAX_CLUSTER>, a, max_keys);
     if (e != cudaSuccess) return e;
-    // Cells in one warp each, up to the CTAs that the GPU holds.
-    const long long blocks = std::min<long long>((a.budget + COPY_THREADS / 32 - 1) / (COPY_THREADS / 32),
-                                                 std::max(1LL, 8LL * device_sm_count() / a.nseq));
+    // Cells of at least two pieces per lane go to whole warps (8 heads of int8, 64 pieces: 26
+    // sequences of 527 cells 12.5 us against 14.4 by pieces; 2 x 131,072 cells 46 against 52);
+    // smaller ones by pieces (1 head of int8, 8 pieces: 16 x 13,337 cells 36 us against 72).
+    const int per_cell = a.kv.nkv * (a.kv.dtype == QSA_I8 ? 8 : 16);
+    const bool cells = per_cell >= 64;
+    const long long wanted = cells ? (a.budget + COPY_THREADS / 32 - 1) / (COPY_THREADS / 32)
+                                   : (static_cast<long long>(a.budget) * per_cell + COPY_THREADS * COPY_BATCH - 1) / (COPY_THREADS * COPY_BATCH);
+    // As many CTAs as the GPU holds.
+    const long long blocks = std::min(wanted, std::max(1LL, 8LL * device_sm_count() / a.nseq));
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), a.nseq);
     cfg.blockDim = dim3(COPY_THREADS);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    const Divider page = make_divider(a.kv.page_size);
-    return a.kv.dtype == QSA_I8 ? cudaLaunchKernelEx(&cfg, copy_kernel<8>, a, page)
-                                : cudaLaunchKernelEx(&cfg, copy_kernel<16>, a, page);
+    const Divider page = make_divider(a.kv.page_size), cell = make_divider(per_cell);
+    const bool int8 = a.kv.dtype == QSA_I8;
+    if (cells)
+        return int8 ? cudaLaunchKernelEx(&cfg, copy_cells_kernel<8>, a, page) : cudaLaunchKernelEx(&cfg, copy_cells_kernel<16>, a, page);
+    return int8 ? cudaLaunchKernelEx(&cfg, copy_pieces_kernel<8>, a, page, cell)
+                : cudaLaunchKernelEx(&cfg, copy_pieces_kernel<16>, a, page, cell);
 }
 
 }  // namespace qsa

@@ -367,6 +367,10 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst_smem, const void *map, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
+// Brings a tensor map into the descriptor cache ahead of its first copy.
+__device__ __forceinline__ void prefetch_tensor_map(const void *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // 3-D form of tma_load_2d (coordinates innermost first).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst_smem, const void *map, int x, int y, int z, uint64_t *bar) {
     asm volatile(

@@ -66,7 +66,7 @@ struct WindowParams {
     int k_has_heads, v_has_heads;   // 0: all KV heads at one address
     int pairs, splits;      // pairs of query tiles of the batch; parts that an item's keys are split into at most
     float *slots;           // [pairs][nkv][splits][2 x 128 rows][SLOT_ROW]
-    struct Work *split_work;   // [pairs][nkv]: for the join, when splits > 1
+    struct Work *split_work;   // [pairs x nkv], by item number: for the join, when splits > 1
     uint64_t wait_ns;
 };
 
@@ -241,10 +241,12 @@ static_assert(WINDOW_SMEM <= 232448, "shared memory per CTA");
 __device__ __forceinline__ bool find_item(const WindowParams &p, uint32_t n, Item &it) {
     const WindowAttnArgs &a = p.a;
     const int lane = threadIdx.x & 31, per = 2 * p.tokens;
+    // Head fastest, then the pairs, the last tokens (which see most) first, then the parts:
+    // what runs together reads the same keys.
     it.kvh = n % a.nkv;
     n /= a.nkv;
-    it.part = n % p.splits;
-    const int g = static_cast<int>(p.pairs - 1 - n / p.splits);   // the last tokens, which see most, first
+    it.part = n / p.pairs;
+    const int g = static_cast<int>(p.pairs - 1 - n % p.pairs);
     auto start = [&](int s) { return min(max(ld_in(a.cu_q + s), 0), a.total_q) / per + s; };
     int lo = 0, hi = a.nseq;
     while (hi - lo > 1) {
@@ -306,9 +308,20 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
     const uint32_t staging = ring + STAGES * TILE_BYTES;
     WindowBarriers *bars = reinterpret_cast<WindowBarriers *>(raw + (staging + 4 * STAGING - smem_u32(raw)));
 
+    Item first_item;
+    bool first_found = false;
     if (warp == MMA_WARP) {
         tmem_alloc(&bars->tmem, TMEM_COLS);
         tmem_relinquish();
+    } else if (warp == COPY_WARP) {
+        if (lane == 0) {
+            prefetch_tensor_map(&p.q);
+            prefetch_tensor_map(&p.k);
+            prefetch_tensor_map(&p.v);
+        }
+        __syncwarp();
+        grid_dependency_wait();
+        first_found = find_item(p, blockIdx.x, first_item);
     } else if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 1);
@@ -381,12 +394,12 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             Work w;
             bool found = false;
             while (ok && more && !found) {
-                Item it;
-                found = find_item(p, n, it);
+                Item it = first_item;
+                found = asked == 0 ? first_found : find_item(p, n, it);
                 w = Work(p, it);
                 if (!found) w.parts = 0;
                 if (p.splits > 1 && it.part == 0 && lane == 0)   // tell the join
-                    p.split_work[n / (a.nkv * p.splits) * a.nkv + it.kvh] = w;
+                    p.split_work[n] = w;
                 found = found && it.part < w.parts;
                 if (!found) {
                     ask();
@@ -401,7 +414,6 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             }
             __syncwarp();
             if (!found) break;
-            ask();
             const Item &it = w.it;
             for (int i = 0; ok && i < (w.tokens1 > 0 ? 2 : 1); ++i, __syncwarp()) {
                 ok = wait_warp(&bars->q_empty[i], (nq[i] & 1) ^ 1);
@@ -417,6 +429,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             }
             const ItemKeys &keys = w.keys;
             for (int j2 = 2 * w.j0; ok && j2 < 2 * w.j1; ++j2, ++kv) {   // keys, then values of tile j2 / 2
+                if (j2 == 2 * w.j0 + 2) ask();   // the first copies do not wait for it
                 const int slot = kv % STAGES, i0 = (j2 >> 1) * ROWS;
                 ok = wait_warp(&bars->kv_empty[slot], ((kv / STAGES) & 1) ^ 1);
                 if (!ok) break;
@@ -441,6 +454,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                 }
                 __syncwarp();
             }
+            if (ok && !open) ask();
             if (ok) get();
         }
         // What was begun here lands before the CTA leaves (at once without an abort).
@@ -571,18 +585,26 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                 char *to = split ? reinterpret_cast<char *>(p.slots + (static_cast<size_t>(it.slot) * 2 * ROWS + i * ROWS + row) * SLOT_ROW)
                                  : reinterpret_cast<char *>(static_cast<T *>(a.out) + out_row * 128);
                 const float inv = sum.y == 0.0f ? 0.0f : 1.0f / sum.y;
-                float odd = 0.0f;   // stays 0 while everything is finite
+                float odds[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // stay 0 while everything is finite
                 const uint32_t o_at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + O_COL + 128 * i;
-                // A piece is staged with its 16-byte chunks at chunk ^ (row % 8) and leaves as whole 128-byte rows.
+                // A piece is staged with its 16-byte chunks at chunk ^ (row % 8) and leaves as whole
+                // 128-byte rows: this lane stores chunk lane % 8 of rows lane / 8 + 0, 4, .. 28.
+                char *row_to[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    row_to[e] = reinterpret_cast<char *>(__shfl_sync(FULL_MASK, reinterpret_cast<unsigned long long>(to), 4 * e + (lane >> 3))) +
+                                16 * (lane & 7);
                 auto leave = [&](int piece) {
                     __syncwarp();
+                    uint4 v[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int r = 4 * e + (lane >> 3), chunk = lane & 7;
-                        const uint4 v = ld_shared_v4(stage + r * 128 + ((chunk ^ (r & 7)) << 4));
-                        char *dst = reinterpret_cast<char *>(__shfl_sync(FULL_MASK, reinterpret_cast<unsigned long long>(to), r));
-                        if ((rows >> r) & 1u) *reinterpret_cast<uint4 *>(dst + 128 * piece + 16 * chunk) = v;
+                        const int r = 4 * e + (lane >> 3);
+                        v[e] = ld_shared_v4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
                     }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if ((rows >> (4 * e + (lane >> 3))) & 1u) *reinterpret_cast<uint4 *>(row_to[e] + 128 * piece) = v[e];
                     __syncwarp();
                 };
                 auto put = [&](int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
@@ -613,7 +635,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                         leave(g);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+                        for (int e = 0; e < 32; ++e) odds[e & 3] = fmaf(__uint_as_float(o[e]), 0.0f, odds[e & 3]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t y[4];
@@ -630,6 +652,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                     continue;
                 }
                 if (valid && a.lse != nullptr) a.lse[out_row] = sum.y == 0.0f ? -INFINITY : (sum.x + log2f(sum.y)) * LN2;
+                const float odd = (odds[0] + odds[1]) + (odds[2] + odds[3]);
                 uint32_t again = __ballot_sync(FULL_MASK, valid && !(odd * sum.y == 0.0f));
                 const int pos = (i == 0 ? w.pos0 : w.pos1) + tok;
                 while (again != 0u) {   // the row's visible keys alone
@@ -876,9 +899,10 @@ Split split(int nseq, int total_q, int nheads, int nkv) {
     return {total_q / per + nseq, static_cast<int>(std::min(parts, 64LL))};
 }
 size_t work_bytes(int pairs, int nkv) { return (sizeof(Work) * static_cast<size_t>(pairs) * nkv + 15) / 16 * 16; }
-// Parts of at least PART_TILES tiles that the longest item can have.
+// Parts of at least PART_TILES tiles that a long item has.
 int most_parts(const WindowAttnArgs &a, int tokens) {
-    long long keys = a.total_k;
+    // Lengths are not known here: twice the mean stands for the longest (a part may then be longer).
+    long long keys = std::min<long long>(a.total_k, 2LL * ((static_cast<long long>(a.total_k) + a.nseq - 1) / a.nseq));
     if (a.window >= 0) keys = std::min(keys, static_cast<long long>(a.window) + std::min(a.sinks, a.total_k) + PIECE + 2 * tokens);
     const long long tiles = (keys + ROWS - 1) / ROWS;
     return static_cast<int>(std::max(1LL, std::min(64LL, (tiles + PART_TILES - 1) / PART_TILES)));
