@@ -576,6 +576,14 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                 const int row = 32 * quarter + lane, tok = row / p.group, head = row - tok * p.group;
                 const int ntok = i == 0 ? w.tokens0 : w.tokens1;
                 const bool valid = tok < ntok;
+                if (ntok == 0) {   // the second tile of a short item
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bars->o_empty[i]);
+                        mbar_arrive(&bars->sum_empty[i]);
+                    }
+                    continue;
+                }
                 const float2 sum = bars->sum[i][row];
                 const bool any = bars->any[i] != 0u, split = w.parts > 1;
                 const int q_row = it.q0 + it.t0 + i * p.tokens + tok, h = it.kvh * p.group + head;
