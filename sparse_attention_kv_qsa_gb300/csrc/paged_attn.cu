@@ -202,8 +202,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     constexpr bool kInt8 = F::kInt8;
     constexpr int STEP = F::STEP, TILE = F::TILE, STAGES = F::STAGES, ELEM = kInt8 ? 1 : 2;
     constexpr int HEADS_PER_UNIT = 8 * kMT;
-    // Cells whose weights are found together, in 16s; with 16 heads their registers allow 16 only.
-    constexpr int GROUPS = kMT == 1 ? STEP / 16 : 1;
+    constexpr int GROUPS = STEP / 16;              // of 16 cells, whose weights are found together
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long sh_scan[WARPS];
     __shared__ int sh_seq, sh_unit, sh_tile;
@@ -428,143 +427,140 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
             const uint32_t mask = *reinterpret_cast<const uint32_t *>(sd + 8 * STEP);
             if (mask == 0u && p.logits == nullptr) continue;
             const uint32_t kb = ring + (step % STAGES) * F::STAGE, vb = kb + STEP * F::PITCH;
+            // x of heads (row r) by cells 16 g + 2 t, + 1, + 8, + 9
+            float sc[kMT][2 * GROUPS][4];
 #pragma unroll
-            for (int g0 = 0; g0 < STEP / 16; g0 += GROUPS) {
-                // x of heads (row r) by cells 16 g + 2 t, + 1, + 8, + 9
-                float sc[kMT][2 * GROUPS][4];
+            for (int m = 0; m < kMT; ++m)
 #pragma unroll
-                for (int m = 0; m < kMT; ++m)
+                for (int n = 0; n < 2 * GROUPS; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[m][n][e] = 0.0f;
+            float ks[4 * GROUPS], vs[4 * GROUPS];
+            if constexpr (kInt8) {
+#pragma unroll
+                for (int n = 0; n < 2 * GROUPS; ++n) {
+                    const float4 f = *reinterpret_cast<const float4 *>(sd + 8 * (8 * n + 2 * t));
+                    ks[2 * n] = f.x;
+                    vs[2 * n] = f.y;
+                    ks[2 * n + 1] = f.z;
+                    vs[2 * n + 1] = f.w;
+                }
+#pragma unroll
+                for (int n = 0; n < 2 * GROUPS; ++n) {
+                    const uint32_t at_k = kb + (8 * n + r) * F::PITCH + 32 * t;
+                    const uint4 w0 = ld_shared_v4(at_k), w1 = ld_shared_v4(at_k + 16);
+                    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t z = w[k] ^ 0x80808080u;
+                        const uint32_t b0 = biased_to_half2(z, 0x4140), b1 = biased_to_half2(z, 0x4342);
+#pragma unroll
+                        for (int m = 0; m < kMT; ++m) O::mma(sc[m][n], qa[m][k], b0, b1);
+                    }
+                }
+            } else {
+                // matrices: cells 0-7 and 8-15 by d 0-7 and 8-15 of step k
+                const uint32_t at_k = kb + ((lane & 7) + 8 * (lane >> 4)) * F::PITCH + 16 * ((lane >> 3) & 1);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t b[4];
+                    ldmatrix4(b, at_k + 32 * k);
+#pragma unroll
+                    for (int m = 0; m < kMT; ++m) {
+                        const uint32_t qf[4] = {qa[m][k][0], 0u, qa[m][k][1], 0u};
+                        O::mma(sc[m][0], qf, b[0], b[1]);
+                        O::mma(sc[m][1], qf, b[2], b[3]);
+                    }
+                }
+            }
+            uint32_t pa[kMT][GROUPS][4];
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) {
+                float xx[4 * GROUPS], top = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 2 * GROUPS; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y = sc[m][n][e];
+                        if constexpr (kInt8) y = fmaf(sc[m][n][2 + e], 1.0f / O::LO, y) * ks[2 * n + e];
+                        y *= qc[m];
+                        if (!((mask >> (8 * n + 2 * t + e)) & 1u)) y = -INFINITY;
+                        xx[2 * n + e] = y;
+                        float z = y;
+                        if constexpr (kInt8) z += __log2f(fmaxf(fabsf(vs[2 * n + e]), 5.9604645e-8f));
+                        top = fmaxf(top, z);
+                    }
+                if (p.logits != nullptr && 8 * m + r < nh) {
+                    float *lp = p.logits + (static_cast<size_t>(s) * a.nheads + h0 + 8 * m + r) * p.stride +
+                                tile * TILE + warp * STEP + 2 * t;
 #pragma unroll
                     for (int n = 0; n < 2 * GROUPS; ++n)
+                        *reinterpret_cast<float2 *>(lp + 8 * n) = make_float2(xx[2 * n], xx[2 * n + 1]);
+                }
+                top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
+                const bool move = top > ref[m] + LAZY || (ref[m] == -INFINITY && top > -INFINITY);
+                if (__any_sync(FULL_MASK, move)) {
+                    const float f = move ? ex2(ref[m] - top) : 1.0f;
+                    if (move) ref[m] = top;
+                    sum[m] *= f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[m][n][e] = 0.0f;
-                float ks[4 * GROUPS], vs[4 * GROUPS];
-                if constexpr (kInt8) {
+                    for (int n = 0; n < 16; ++n)
 #pragma unroll
-                    for (int n = 0; n < 2 * GROUPS; ++n) {
-                        const float4 f = *reinterpret_cast<const float4 *>(sd + 8 * (16 * g0 + 8 * n + 2 * t));
-                        ks[2 * n] = f.x;
-                        vs[2 * n] = f.y;
-                        ks[2 * n + 1] = f.z;
-                        vs[2 * n + 1] = f.w;
+                        for (int e = 0; e < 4; ++e) o[m][n][e] *= f;
+                }
+                const float base = ref[m] == -INFINITY ? 0.0f : ref[m];
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = ex2(xx[4 * g + e] - base);
+                        sum[m] += w[e];
+                        if constexpr (kInt8) w[e] *= vs[4 * g + e];
                     }
+                    O::split(w[0], w[1], pa[m][g][0], pa[m][g][1]);
+                    O::split(w[2], w[3], pa[m][g][2], pa[m][g][3]);
+                }
+            }
 #pragma unroll
-                    for (int n = 0; n < 2 * GROUPS; ++n) {
-                        const uint32_t at_k = kb + (16 * g0 + 8 * n + r) * F::PITCH + 32 * t;
-                        const uint4 w0 = ld_shared_v4(at_k), w1 = ld_shared_v4(at_k + 16);
-                        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            for (int gg = 0; gg < GROUPS; ++gg) {
+                const uint32_t vg = vb + 16 * gg * F::PITCH;
+                if constexpr (kInt8) {
+                    // This thread's cells 2 t, 2 t + 1, 2 t + 8, 2 t + 9; column r of product n is d = 16 r + n.
+                    uint4 cw[4];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t z = w[k] ^ 0x80808080u;
-                            const uint32_t b0 = biased_to_half2(z, 0x4140), b1 = biased_to_half2(z, 0x4342);
+                    for (int e = 0; e < 4; ++e) cw[e] = ld_shared_v4(vg + (2 * t + (e & 1) + 8 * (e >> 1)) * F::PITCH + 16 * r);
 #pragma unroll
-                            for (int m = 0; m < kMT; ++m) O::mma(sc[m][n], qa[m][k], b0, b1);
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t lo[2], hi[2];   // cells (2t, 2t+1) and (2t+8, 2t+9): d 0, 1 and d 2, 3 of the word
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t w0 = reinterpret_cast<const uint32_t *>(&cw[2 * e])[g] ^ 0x80808080u;
+                            const uint32_t w1 = reinterpret_cast<const uint32_t *>(&cw[2 * e + 1])[g] ^ 0x80808080u;
+                            lo[e] = __byte_perm(w0, w1, 0x5140);
+                            hi[e] = __byte_perm(w0, w1, 0x7362);
+                        }
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            const uint32_t sel = (d & 1) ? 0x4342 : 0x4140;
+                            const uint32_t b0 = biased_to_half2(d < 2 ? lo[0] : hi[0], sel);
+                            const uint32_t b1 = biased_to_half2(d < 2 ? lo[1] : hi[1], sel);
+#pragma unroll
+                            for (int m = 0; m < kMT; ++m) O::mma(o[m][4 * g + d], pa[m][gg], b0, b1);
                         }
                     }
                 } else {
-                    // matrices: cells 0-7 and 8-15 by d 0-7 and 8-15 of step k
-                    const uint32_t at_k = kb + ((lane & 7) + 8 * (lane >> 4)) * F::PITCH + 16 * ((lane >> 3) & 1);
+                    // matrices: cells 0-7, 8-15 by d 16 n .. + 7, then d 16 n + 8 .. + 15
+                    const uint32_t at_v = vg + (lane & 15) * F::PITCH + 16 * (lane >> 4);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int n = 0; n < 8; ++n) {
                         uint32_t b[4];
-                        ldmatrix4(b, at_k + 32 * k);
+                        ldmatrix4_t(b, at_v + 32 * n);
 #pragma unroll
                         for (int m = 0; m < kMT; ++m) {
-                            const uint32_t qf[4] = {qa[m][k][0], 0u, qa[m][k][1], 0u};
-                            O::mma(sc[m][0], qf, b[0], b[1]);
-                            O::mma(sc[m][1], qf, b[2], b[3]);
-                        }
-                    }
-                }
-                uint32_t pa[kMT][GROUPS][4];
-#pragma unroll
-                for (int m = 0; m < kMT; ++m) {
-                    float xx[4 * GROUPS], top = -INFINITY;
-#pragma unroll
-                    for (int n = 0; n < 2 * GROUPS; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float y = sc[m][n][e];
-                            if constexpr (kInt8) y = fmaf(sc[m][n][2 + e], 1.0f / O::LO, y) * ks[2 * n + e];
-                            y *= qc[m];
-                            if (!((mask >> (16 * g0 + 8 * n + 2 * t + e)) & 1u)) y = -INFINITY;
-                            xx[2 * n + e] = y;
-                            float z = y;
-                            if constexpr (kInt8) z += __log2f(fmaxf(fabsf(vs[2 * n + e]), 5.9604645e-8f));
-                            top = fmaxf(top, z);
-                        }
-                    if (p.logits != nullptr && 8 * m + r < nh) {
-                        float *lp = p.logits + (static_cast<size_t>(s) * a.nheads + h0 + 8 * m + r) * p.stride +
-                                    tile * TILE + warp * STEP + 16 * g0 + 2 * t;
-#pragma unroll
-                        for (int n = 0; n < 2 * GROUPS; ++n)
-                            *reinterpret_cast<float2 *>(lp + 8 * n) = make_float2(xx[2 * n], xx[2 * n + 1]);
-                    }
-                    top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
-                    const bool move = top > ref[m] + LAZY || (ref[m] == -INFINITY && top > -INFINITY);
-                    if (__any_sync(FULL_MASK, move)) {
-                        const float f = move ? ex2(ref[m] - top) : 1.0f;
-                        if (move) ref[m] = top;
-                        sum[m] *= f;
-#pragma unroll
-                        for (int n = 0; n < 16; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[m][n][e] *= f;
-                    }
-                    const float base = ref[m] == -INFINITY ? 0.0f : ref[m];
-#pragma unroll
-                    for (int g = 0; g < GROUPS; ++g) {
-                        float w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            w[e] = ex2(xx[4 * g + e] - base);
-                            sum[m] += w[e];
-                            if constexpr (kInt8) w[e] *= vs[4 * g + e];
-                        }
-                        O::split(w[0], w[1], pa[m][g][0], pa[m][g][1]);
-                        O::split(w[2], w[3], pa[m][g][2], pa[m][g][3]);
-                    }
-                }
-#pragma unroll
-                for (int gg = 0; gg < GROUPS; ++gg) {
-                    const uint32_t vg = vb + 16 * (g0 + gg) * F::PITCH;
-                    if constexpr (kInt8) {
-                        // This thread's cells 2 t, 2 t + 1, 2 t + 8, 2 t + 9; column r of product n is d = 16 r + n.
-                        uint4 cw[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) cw[e] = ld_shared_v4(vg + (2 * t + (e & 1) + 8 * (e >> 1)) * F::PITCH + 16 * r);
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            uint32_t lo[2], hi[2];   // cells (2t, 2t+1) and (2t+8, 2t+9): d 0, 1 and d 2, 3 of the word
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t w0 = reinterpret_cast<const uint32_t *>(&cw[2 * e])[g] ^ 0x80808080u;
-                                const uint32_t w1 = reinterpret_cast<const uint32_t *>(&cw[2 * e + 1])[g] ^ 0x80808080u;
-                                lo[e] = __byte_perm(w0, w1, 0x5140);
-                                hi[e] = __byte_perm(w0, w1, 0x7362);
-                            }
-#pragma unroll
-                            for (int d = 0; d < 4; ++d) {
-                                const uint32_t sel = (d & 1) ? 0x4342 : 0x4140;
-                                const uint32_t b0 = biased_to_half2(d < 2 ? lo[0] : hi[0], sel);
-                                const uint32_t b1 = biased_to_half2(d < 2 ? lo[1] : hi[1], sel);
-#pragma unroll
-                                for (int m = 0; m < kMT; ++m) O::mma(o[m][4 * g + d], pa[m][gg], b0, b1);
-                            }
-                        }
-                    } else {
-                        // matrices: cells 0-7, 8-15 by d 16 n .. + 7, then d 16 n + 8 .. + 15
-                        const uint32_t at_v = vg + (lane & 15) * F::PITCH + 16 * (lane >> 4);
-#pragma unroll
-                        for (int n = 0; n < 8; ++n) {
-                            uint32_t b[4];
-                            ldmatrix4_t(b, at_v + 32 * n);
-#pragma unroll
-                            for (int m = 0; m < kMT; ++m) {
-                                O::mma(o[m][2 * n], pa[m][gg], b[0], b[1]);
-                                O::mma(o[m][2 * n + 1], pa[m][gg], b[2], b[3]);
-                            }
+                            O::mma(o[m][2 * n], pa[m][gg], b[0], b[1]);
+                            O::mma(o[m][2 * n + 1], pa[m][gg], b[2], b[3]);
                         }
                     }
                 }
@@ -767,11 +763,21 @@ struct Layout {
     size_t meta, slots, lse2, logits, bytes;
     int heads_per_unit, grid, stride;
 };
+// A unit of 16 heads reads its cells once where two of 8 read them twice, but its
+// steps are slower (registers: no queries ahead, and the 16 outputs' merges). It pays for
+// 16-bit cells that do not stay in L2 for the second reading: 16 heads on a KV head, bfloat16, 8 x
+// 16,384 cells of 8 KV heads 93 us against 115, 16 x 8,192 cells of one 24.7 against 20.3. int8
+// units of 16 lose throughout (2 x 100,000 cells 51 us against 40).
+constexpr long long L2_BYTES = 128LL << 20;
+int heads_per_unit(int nseq, int group, int nkv, int capacity, bool int8) {
+    return group > 8 && !int8 && 512LL * nseq * capacity * nkv > L2_BYTES ? 16 : 8;
+}
+// The scratch is laid out for 16 heads whenever there are as many, whatever the cells' type.
 Layout layout(int nseq, int nheads, int nkv, int capacity, bool with_mass) {
     Layout y;
     const int group = nheads / nkv;
     y.heads_per_unit = group <= 8 ? 8 : 16;
-    const long long parts = (group + y.heads_per_unit - 1) / y.heads_per_unit;
+    const long long parts = (group + 7) / 8;
     const long long tiles = (static_cast<long long>(capacity) + TILE_16BIT - 1) / TILE_16BIT * nkv * parts * nseq;
     y.grid = static_cast<int>(std::max(1LL, std::min<long long>(static_cast<long long>(CTAS_PER_SM) * device_sm_count(), tiles)));
     y.stride = (capacity + TILE_INT8 - 1) / TILE_INT8 * TILE_INT8;
@@ -822,11 +828,6 @@ cudaError_t run(const Params &p, int grid, cudaStream_t stream) {
     return e;
 }
 
-template <int kKv, typename QT>
-cudaError_t run_heads(const Params &p, const Layout &y, cudaStream_t stream) {
-    return y.heads_per_unit == 8 ? run<kKv, QT, 1>(p, y.grid, stream) : run<kKv, QT, 2>(p, y.grid, stream);
-}
-
 }  // namespace
 
 size_t paged_attn_scratch_bytes(int nseq, int nheads, int nkv, int capacity, bool with_mass) {
@@ -840,7 +841,9 @@ cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t stream) {
     const Layout y = layout(a.nseq, a.nheads, a.kv.nkv, p.capacity, a.mass != nullptr);
     p.page = make_divider(a.kv.page_size);
     p.group = a.nheads / a.kv.nkv;
-    p.parts = (p.group + y.heads_per_unit - 1) / y.heads_per_unit;
+    const bool int8 = a.kv.dtype == QSA_I8;
+    const int heads = heads_per_unit(a.nseq, p.group, a.kv.nkv, p.capacity, int8);
+    p.parts = (p.group + heads - 1) / heads;
     p.units = a.kv.nkv * p.parts;
     p.stride = y.stride;
     char *b = static_cast<char *>(a.scratch);
@@ -848,11 +851,12 @@ cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t stream) {
     p.slots = reinterpret_cast<float *>(b + y.slots);
     p.lse2 = a.mass != nullptr ? reinterpret_cast<float *>(b + y.lse2) : nullptr;
     p.logits = a.mass != nullptr && p.capacity > 0 ? reinterpret_cast<float *>(b + y.logits) : nullptr;
-    if (a.kv.dtype == QSA_BF16) return run_heads<QSA_BF16, __nv_bfloat16>(p, y, stream);
-    if (a.kv.dtype == QSA_F16) return run_heads<QSA_F16, __half>(p, y, stream);
-    if (a.q_dtype == QSA_F32) return run_heads<QSA_I8, float>(p, y, stream);
-    if (a.q_dtype == QSA_F16) return run_heads<QSA_I8, __half>(p, y, stream);
-    return run_heads<QSA_I8, __nv_bfloat16>(p, y, stream);
+    if (a.kv.dtype == QSA_BF16)
+        return heads == 8 ? run<QSA_BF16, __nv_bfloat16, 1>(p, y.grid, stream) : run<QSA_BF16, __nv_bfloat16, 2>(p, y.grid, stream);
+    if (a.kv.dtype == QSA_F16) return heads == 8 ? run<QSA_F16, __half, 1>(p, y.grid, stream) : run<QSA_F16, __half, 2>(p, y.grid, stream);
+    if (a.q_dtype == QSA_F32) return run<QSA_I8, float, 1>(p, y.grid, stream);
+    if (a.q_dtype == QSA_F16) return run<QSA_I8, __half, 1>(p, y.grid, stream);
+    return run<QSA_I8, __nv_bfloat16, 1>(p, y.grid, stream);
 }
 
 }  // namespace qsa

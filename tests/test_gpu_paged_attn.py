@@ -122,6 +122,23 @@ def test_every_length(dev, kv, qt, nkv, group, page, layout):
     assert torch.equal(out, again) and torch.equal(lse, lse2)      # a fixed order of sums
 
 
+@pytest.mark.parametrize("kv,qt", [(BF16, BF16), (F16, F16), (I8, F32)])
+@pytest.mark.parametrize("nkv,group,page", [(1, 9, 16), (2, 16, 48), (1, 12, 64), (1, 40, 16)])
+def test_many_heads_on_wide_tables(dev, kv, qt, nkv, group, page):
+    """Tables for more cells than stay in L2: 9 to 16 heads of 16-bit cells share one reading."""
+    lens = LENS + [9000, 20000]
+    cols = max(20000 // page + 2, 1 + (128 << 20) // (512 * nkv * page * len(lens)))
+    c = Cache(dev, lens, nkv, page, kv, cols=cols)
+    q = queries(dev, len(lens), nkv * group, qt)
+    out, lse = c.call(q)
+    c.check(q, out, lse)
+    again, lse2 = c.call(q)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    mass = torch.zeros((len(lens), c.cols * page), device=dev)
+    out, lse = c.poison(700, 9).call(q, window=700, sinks=9, mass=mass)
+    c.check(q, out, lse, 700, 9, mass=torch.zeros_like(mass), mass_out=mass)
+
+
 @pytest.mark.parametrize("kv,qt", [(BF16, BF16), (I8, F32)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (0, 3), (1, 0), (1, 1), (16, 4), (100, 70), (511, 0), (512, 1),
                                           (4096, 5), (64, 5000), (0, 2 ** 31 - 1), (2 ** 31 - 1, 4)])
