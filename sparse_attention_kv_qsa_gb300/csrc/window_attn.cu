@@ -302,7 +302,8 @@ template <typename T>
 __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_constant__ WindowParams p) {
     extern __shared__ unsigned char raw[];
     const WindowAttnArgs &a = p.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(FULL_MASK, tid >> 5, 0);   // the same for the warp, as the compiler now knows
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t ring = base + 2 * TILE_BYTES;
     const uint32_t staging = ring + STAGES * TILE_BYTES;
