@@ -15,6 +15,12 @@
 //
 // copy_cells_kernel, copy_pieces_kernel: bandwidth. 16-byte pieces of keys and
 // values, a batch of loads before its stores.
+//
+// Measured (GB300): 2 sequences of up to 131,072 int8 cells of 8 heads cut to
+// 16,384, 46 us: 22 to choose, 24 to copy 136 MB (0.83 of the measured copy rate);
+// one sequence of 576 cells cut to 512, 9.2 us, launches and latencies. Masses
+// crowd into a few digits of the first pass, yet plain shared-memory atomics beat
+// one atomic per different digit of a warp (choosing 40 us against 48).
 #include <algorithm>
 
 #include "cache_internal.cuh"

@@ -9,26 +9,25 @@
 // by the few query heads that share it, so HBM.
 //
 // Work. The visible cells of a sequence, sinks first, are numbered without
-// gaps and cut into tiles of 64; (sequence, KV head, up to 16 query heads) is
-// a unit, and all tiles of all units in order are cut into one equal range
-// per CTA, two CTAs per SM. Lengths live on the device only: every CTA sums
-// the tile counts of all sequences itself, so ragged batches are balanced,
-// a captured graph follows the lengths, and a single long sequence fills the
-// GPU. A unit that falls into several ranges leaves partial results (outputs,
-// maximum, sum per head) in scratch, which join_kernel adds in range order;
-// the result does not depend on scheduling.
+// gaps and cut into tiles of 64 (int8: 128); (sequence, KV head, up to 8 or 16
+// query heads) is a unit, and all tiles of all units in order are cut into one
+// equal range per CTA, two CTAs per SM. Lengths live on the device only: every
+// CTA sums the tile counts of all sequences itself, so ragged batches are
+// balanced, a captured graph follows the lengths, and a single long sequence
+// fills the GPU. A unit that falls into several ranges leaves partial results
+// (outputs, maximum, sum per head) in scratch, which join_kernel adds in range
+// order; the result does not depend on scheduling.
 //
-// A tile. Each of the 4 warps takes 16 of the 64 cells and runs alone: its
-// rows arrive in a ring of its own by 16-byte asynchronous copies (rows past
-// the end are filled with zeros), and the page numbers (and int8 scales) of a
-// step are fetched one step ahead of its copies. Both products run on
-// mma.sync m16n8k16 with the heads as rows: x = Q K^T with rows 0-7 the heads
-// and rows 8-15 the remainder of q where it has one, then P V with rows 0-7
-// the weights rounded to the operand type and rows 8-15 what that rounding
-// left, so the weights carry 17 (bfloat16) or 22 (binary16) bits. The
-// fragments of x are the fragments of P. tcgen05 would need 64 rows at least
-// for the 1 to 16 heads that share a cell; the arithmetic is far from the
-// bound as it is.
+// A tile. Each of the 4 warps takes a quarter of the cells (8 KiB) and runs
+// alone: its rows arrive in a ring of its own by 16-byte asynchronous copies
+// (rows that do not exist are filled with zeros), two steps ahead and on over
+// the units' boundaries; the page numbers are fetched one step before that.
+// Both products run on mma.sync m16n8k16 with the heads as rows: x = Q K^T with
+// rows 0-7 the heads and rows 8-15 the remainder of q where it has one, then
+// P V with rows 0-7 the weights rounded to the operand type and rows 8-15 what
+// that rounding left, so the weights carry 17 (bfloat16) or 22 (binary16) bits.
+// The fragments of x are the fragments of P. tcgen05 would need 64 rows at
+// least for the 1 to 16 heads that share a cell.
 //
 // int8 cells become binary16 exactly (a byte in the low bits of 1024 + u), q
 // is scaled by a power of two per head into binary16's range, and the key
@@ -37,6 +36,15 @@
 // 2^(x_j - M) vs_j stays within binary16 whatever the scales' range.
 // M moves only when it would have to grow by more than 2^8: the sums are
 // scaled by whatever M they started from, and rescaling is rare.
+//
+// Measured (GB300): 64 ragged sequences of up to 8,192 bfloat16 cells, 8 KV heads
+// of 4, 207 us, 6.1 TB/s (0.90 of the measured copy rate); 48 sequences of which
+// 1,028 binary16 cells are visible, 48 us, 4.2 TB/s (launches, first copies and the
+// join are 9 of them); 4 sequences of up to 131,072 int8 cells, 2 KV heads, 56 us,
+// 3.4 TB/s: about 850 instructions per warp and 32 cells, the conversions to
+// binary16 360 of them, at 43 % of the issue slots with the 8 warps per SM that
+// 239 registers leave (12 warps of 168 registers: 69 us against 66 then). One
+// sequence of 700 cells 8.8 us, launches and latencies.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
