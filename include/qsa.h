@@ -383,7 +383,7 @@ typedef struct {
  *           q_head_stride (multiples of 16 bytes, not negative). q_dtype is the
  *           pages' dtype for 16-bit pages; QSA_F32, QSA_F16 or QSA_BF16 for int8.
  * page_table int32, row stride table_stride >= table_cols. lens int32 [nseq].
- * out       [nseq][nheads][128] of q_dtype, contiguous. lse fp32
+ * out       [nseq][nheads][128] of q_dtype, contiguous, not over an input. lse fp32
  *           [nseq][nheads] or NULL. mass, mass_out fp32 with row stride
  *           mass_stride >= table_cols * page_size.
  * scale     positive and finite.
@@ -417,10 +417,10 @@ qsa_status qsa_paged_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride
  *           and head (multiples of 16 bytes, not negative).
  * cu_q, cu_k int32 [nseq + 1], ascending from 0 (device memory; values are
  *           clamped to [0, total_q] and [0, total_k]).
- * max_q     at least the longest sequence's query count (queries past it are
- *           not computed).
+ * max_q     at least the longest sequence's query count (queries past it may
+ *           not be computed). Rows of no sequence are not written.
  * out       [total_q][nheads][128] of dtype, contiguous, 16-byte aligned; lse
- *           fp32 [total_q][nheads] or NULL.
+ *           fp32 [total_q][nheads] or NULL. They do not overlap the inputs.
  * scratch   at least qsa_window_attn_scratch_bytes(...) bytes, 16-byte aligned
  *           (may be NULL when that is 0).
  * Softmax statistics and sums are fp32; the weights are rounded once to dtype
@@ -448,6 +448,8 @@ qsa_status qsa_window_attn(const void *q, const void *k, const void *v, qsa_dtyp
  * new_lens  int32 [nseq], written: min(n, budget).
  * new_mass  fp32, row stride new_mass_stride, new_mass_cols columns written:
  *           the kept cells' masses, then zeros.
+ * The outputs overlap neither one another nor the inputs (new_lens == lens or
+ * new_mass == mass returns QSA_ERR_INVALID).
  * Pages of new_table must not be pages that any row of page_table uses for a
  * cell below its length, nor appear twice (else the copied cells are
  * undefined). A page id outside [0, npages) on either side skips the copy of

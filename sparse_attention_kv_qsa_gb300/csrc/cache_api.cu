@@ -138,6 +138,7 @@ qsa_status qsa_cache_evict(const qsa_kv_pages *kv, int nseq, const int32_t *page
         !aligned(new_mass, 4))
         return QSA_ERR_INVALID;
     if (table_cols > 0 && (!aligned(page_table, 4) || !aligned(mass, 4))) return QSA_ERR_INVALID;
+    if (new_lens == lens || new_mass == mass) return QSA_ERR_INVALID;   // read while they are written
     const qsa::CacheEvictArgs a{*kv,  nseq,   page_table, table_cols, table_stride, lens, mass, mass_stride,
                                 new_table, new_cols, new_table_stride, budget, sinks, recent, kept, new_lens,
                                 new_mass, new_mass_stride, new_mass_cols};

@@ -929,9 +929,12 @@ struct Split {
 };
 Split split(int nseq, int total_q, int nheads, int nkv) {
     const int per = 2 * (ROWS / (nheads / nkv)), sms = device_sm_count();
+    const int pairs = total_q / per + nseq;
     const long long least = static_cast<long long>(std::max(total_q / per, std::min(nseq, total_q))) * nkv;
+    // The partial results are laid out for empty sequences too: no more than 8 parts per SM in all.
+    const long long room = std::max(1LL, 8LL * sms / (static_cast<long long>(pairs) * nkv));
     const long long parts = least >= 2LL * sms ? 1 : (3LL * sms + least - 1) / least;
-    return {total_q / per + nseq, static_cast<int>(std::min(parts, 64LL))};
+    return {pairs, static_cast<int>(std::min(std::min(parts, room), 64LL))};
 }
 size_t work_bytes(int pairs, int nkv) { return (sizeof(Work) * static_cast<size_t>(pairs) * nkv + 15) / 16 * 16; }
 // Parts of at least PART_TILES tiles that a long item has.

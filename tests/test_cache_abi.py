@@ -100,6 +100,14 @@ def test_window_attn_argument_errors(lib, bad):
     assert window(lib, **bad) == INVALID
 
 
+def test_window_attn_scratch_stays_bounded(lib):
+    """Partial results are kept for few items only, however many empty sequences are named."""
+    n = qsa.window_attn_scratch_bytes
+    for nseq, total_q, nheads, nkv in ((1, 1, 8, 8), (65535, 10, 32, 8), (76, 1, 8, 8), (300, 300, 1, 1), (1, 100000, 8, 1),
+                                       (4, 2000, 32, 8), (1, 2 ** 30, 1, 1)):
+        assert n(nseq, total_q, total_q, nheads, nkv) <= 256 << 20
+
+
 def test_window_attn_limits(lib):
     assert window(lib, nseq=0, q=None, out=None) == OK
     assert window(lib, total_q=0, max_q=0, q=None, out=None, cu_q=None) == OK
@@ -110,7 +118,7 @@ def test_window_attn_limits(lib):
 
 def evict(lib, kv=None, **kw):
     d = dict(nseq=2, table=A, cols=8, tstride=8, lens=A, mass=A, mstride=128, new=A, new_cols=4, nstride=4, budget=64,
-             sinks=4, recent=16, kept=A, new_lens=A, new_mass=A, nmstride=64, nmcols=64)
+             sinks=4, recent=16, kept=B, new_lens=B, new_mass=B, nmstride=64, nmcols=64)
     d.update(kw)
     return lib.qsa_cache_evict(kv or pages(), d["nseq"], d["table"], d["cols"], d["tstride"], d["lens"], d["mass"],
                                d["mstride"], d["new"], d["new_cols"], d["nstride"], d["budget"], d["sinks"], d["recent"],
@@ -121,7 +129,8 @@ def evict(lib, kv=None, **kw):
                                  dict(sinks=40, recent=25), dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1),
                                  dict(budget=65), dict(nmcols=63), dict(nmstride=63), dict(mstride=127),
                                  dict(tstride=7), dict(nstride=3), dict(lens=None), dict(table=None), dict(mass=MIS),
-                                 dict(new=None), dict(kept=MIS), dict(new_lens=None), dict(new_mass=MIS)])
+                                 dict(new=None), dict(kept=MIS), dict(new_lens=None), dict(new_mass=MIS),
+                                 dict(new_lens=A), dict(new_mass=A)])
 def test_cache_evict_argument_errors(lib, bad):
     assert evict(lib, **bad) == INVALID
 

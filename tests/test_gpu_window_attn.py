@@ -99,6 +99,21 @@ def test_many_sequences(dev):
     both(dev, n, n, 1, 2, window=9, sinks=2)
 
 
+def test_empty_sequences(dev):
+    """No keys at all, and a few tokens among thousands of empty sequences."""
+    both(dev, [5, 70], [0, 0])
+    n = [0] * 3000
+    n[17], n[2999] = 3, 200
+    both(dev, n, n, 2, 4)
+
+
+@pytest.mark.parametrize("nseq,total_q,nheads,nkv", [(1, 1, 8, 8), (65535, 10, 32, 8), (76, 1, 8, 8), (300, 300, 1, 1),
+                                                     (1, 100000, 8, 1), (4, 2000, 32, 8)])
+def test_scratch_stays_bounded(dev, nseq, total_q, nheads, nkv):
+    """However many empty sequences are named; on the device's own SM count."""
+    assert qsa.window_attn_scratch_bytes(nseq, total_q, total_q, nheads, nkv) <= 256 << 20
+
+
 def test_strided_arguments(dev):
     """Slices of a fused projection, and tensors with heads outside tokens."""
     n, cu = [150, 70], starts([150, 70], dev)
