@@ -44,11 +44,12 @@
 // Every mbarrier wait is bounded; a timeout sets the error word.
 #include <cstring>
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include "ptx.cuh"
 #include "qsa_internal.cuh"
-#include "tensor_map.cuh"
 
 namespace qsa {
 namespace {
@@ -719,6 +720,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         tc_fence_after_sync();
         tmem_dealloc(tmem, TMEM_COLS);
     }
+}
+
+// cuTensorMapEncodeTiled from the driver, looked up once (no link-time
+// dependency on the driver library).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
 }
 
 // Tensor map of the scores [nq][active] fp32 for 32 x 128 boxes, 128-byte
