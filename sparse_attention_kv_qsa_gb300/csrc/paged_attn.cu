@@ -39,12 +39,13 @@
 //
 // Measured (GB300): 64 ragged sequences of up to 8,192 bfloat16 cells, 8 KV heads
 // of 4, 207 us, 6.1 TB/s (0.90 of the measured copy rate); 48 sequences of which
-// 1,028 binary16 cells are visible, 48 us, 4.2 TB/s (launches, first copies and the
-// join are 9 of them); 4 sequences of up to 131,072 int8 cells, 2 KV heads, 56 us,
-// 3.4 TB/s: about 850 instructions per warp and 32 cells, the conversions to
+// 1,028 binary16 cells are visible, 46.5 us, 4.4 TB/s (the first 5 us bring the
+// first cells, the ranges end within 4 us of one another, the join takes 2); 4
+// sequences of up to 131,072 int8 cells, 2 KV heads, 53 us, 3.6 TB/s: about 850 instructions per warp and 32 cells, the conversions to
 // binary16 360 of them, at 43 % of the issue slots with the 8 warps per SM that
-// 239 registers leave (12 warps of 168 registers: 69 us against 66 then). One
-// sequence of 700 cells 8.8 us, launches and latencies.
+// 243 registers leave (12 warps of 168 registers: 69 us against 66 then). One
+// sequence of 700 cells 7.9 us, launches and latencies: 0.7 us to find the range,
+// 1.5 for the page and the cells, 1 for the products and the merge, the join.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long sh_scan[WARPS];
     __shared__ int sh_seq, sh_unit, sh_tile;
+    __shared__ Span sh_span;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, t = lane & 3;
     const PagedAttnArgs &a = p.a;
@@ -225,7 +227,13 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     const int each = (a.nseq + THREADS - 1) / THREADS;
     const int s0 = min(tid * each, a.nseq), s1 = min(s0 + each, a.nseq);
     long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += tiles_of<TILE>(visible(p, s));
+    Span first_span = {0, 0, 0};   // of s0: its length is read once
+    for (int s = s0; s < s1; ++s) {
+        const Span v = visible(p, s);
+        if (s == s0) first_span = v;
+        mine += tiles_of<TILE>(v);
+    }
+    const int own_n = blockIdx.x < a.nseq ? visible(p, blockIdx.x).n : 1;   // for the rows without a cell, below
     long long before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -253,19 +261,22 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     if (x0 < x1 && x0 >= before * p.units && x0 < (before + mine) * p.units) {
         int s = s0;
         long long b = before;
-        int n = tiles_of<TILE>(visible(p, s));
+        Span v = first_span;
+        int n = tiles_of<TILE>(v);
         while (x0 >= (b + n) * p.units) {
             b += n;
-            n = tiles_of<TILE>(visible(p, ++s));
+            v = visible(p, ++s);
+            n = tiles_of<TILE>(v);
         }
         const long long in_seq = x0 - b * p.units;
         sh_seq = s;
+        sh_span = v;
         sh_unit = static_cast<int>(in_seq / n);
         sh_tile = static_cast<int>(in_seq % n);
     }
     // Sequences without a visible cell have no tile: their rows are written here.
     for (int s = blockIdx.x; s < a.nseq; s += gridDim.x) {
-        if (visible(p, s).n > 0) continue;
+        if ((s == blockIdx.x ? own_n : visible(p, s).n) > 0) continue;
         for (int e = tid; e < a.nheads * 32; e += THREADS)
             store4(static_cast<QT *>(a.out) + static_cast<size_t>(s) * a.nheads * 128 + 4 * e, make_float4(0.f, 0.f, 0.f, 0.f));
         for (int h = tid; h < a.nheads; h += THREADS) {
@@ -287,35 +298,40 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     // ---- copies, which run ahead over the units without a stop ----------------------
     const int row = lane & (STEP - 1);             // the row whose address this lane finds
     Cursor<TILE> at;                               // the step whose page is fetched next
-    at.enter(p, sh_seq);
+    at.s = sh_seq;
+    at.v = sh_span;
+    at.nt = tiles_of<TILE>(at.v);
     at.u = sh_unit;
     at.t = sh_tile;
     Cursor<TILE> here = at;                        // the step that is computed
-    int page = -1;                                 // of this lane's row of the step to copy next, and the rest of its address
-    long long rest = 0, scale_rest = 0;
+    struct Place {                                 // of this lane's row: the page, and the rest of its address
+        int page;
+        long long rest, scale_rest;
+    } place = {-1, 0, 0};                          // for the step to copy next
     auto fetch = [&](int step) {
         if (step >= steps) return;
         if (step > 0) at.next(p);
         const int i = at.t * TILE + warp * STEP + row;
-        page = -1;
+        place.page = -1;
         if (i < at.v.n) {
             const int j = at.v.cell(i), pg = static_cast<int>(divide(p.page, j)), in_page = j - pg * a.kv.page_size;
-            page = ld_in(a.table + at.s * a.table_stride + pg);
+            place.page = ld_in(a.table + at.s * a.table_stride + pg);
             const int kvh = p.parts == 1 ? at.u : at.u / p.parts;
-            rest = in_page * a.kv.cell_stride + kvh * a.kv.head_stride;
-            if constexpr (kInt8) scale_rest = in_page * a.kv.scale_cell_stride + kvh * a.kv.scale_head_stride;
+            place.rest = in_page * a.kv.cell_stride + kvh * a.kv.head_stride;
+            if constexpr (kInt8) place.scale_rest = in_page * a.kv.scale_cell_stride + kvh * a.kv.scale_head_stride;
         }
     };
     uint16_t key_scale = 0, value_scale = 0;       // this lane's row's of the newest step
     auto issue = [&](int step) {
         if (step < steps) {
             const int slot_at = step % STAGES;
+            const int page = place.page;
             const bool ok = page >= 0 && page < a.kv.npages;
-            const long long off = ok ? (page * a.kv.page_stride + rest) * ELEM : 0;
+            const long long off = ok ? (page * a.kv.page_stride + place.rest) * ELEM : 0;
             const uint32_t mask = __ballot_sync(FULL_MASK, ok);
             if (lane == 0) *reinterpret_cast<uint32_t *>(side + slot_at * F::SIDE + 8 * STEP) = mask;
             if constexpr (kInt8) {
-                const long long so = ok ? page * a.kv.scale_page_stride + scale_rest : 0;
+                const long long so = ok ? page * a.kv.scale_page_stride + place.scale_rest : 0;
                 key_scale = ok ? ld_in_u16(a.kv.k_scale_f16 + so) : 0;
                 value_scale = ok ? ld_in_u16(a.kv.v_scale_f16 + so) : 0;
             }
@@ -339,12 +355,24 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 *reinterpret_cast<float2 *>(side + (step % STAGES) * F::SIDE + 8 * row) =
                     make_float2(__half2float(__ushort_as_half(key_scale)), __half2float(__ushort_as_half(value_scale)));
     };
-    fetch(0);
-#pragma unroll 1
-    for (int i = 0; i < STAGES - 1; ++i) {
-        issue(i);
-        fetch(i + 1);
-        if (i < STAGES - 2) put_scale(i);
+    {   // Both pages, both steps' cells and scales: no load waits for the other step's.
+        static_assert(STAGES == 3, "two steps ahead");
+        fetch(0);
+        const Place first = place;
+        fetch(1);
+        const Place second = place;
+        place = first;
+        issue(0);
+        const uint16_t first_key_scale = key_scale, first_value_scale = value_scale;
+        place = second;
+        issue(1);
+        fetch(2);
+        const uint16_t second_key_scale = key_scale, second_value_scale = value_scale;
+        key_scale = first_key_scale;
+        value_scale = first_value_scale;
+        put_scale(0);
+        key_scale = second_key_scale;
+        value_scale = second_value_scale;
     }
 
     // ---- units ------------------------------------------------------------------------
@@ -653,9 +681,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     }
 }
 
-// Adds the partial results of one unit's ranges for one head: warp w takes
-// every 4th range from w on, then the warps are added in order.
-constexpr int JOIN_WARPS = 4;
+// Adds the partial results of one unit's ranges for one head: of W warps, warp w
+// takes every W-th range from w on, then the warps are added in order. W is 1
+// where a unit has about as many ranges as a warp loads at once, else 4 (measured,
+// whole call: 2 ranges a unit 46.4 us with 1 warp, 48.0 with 4, 51.0 with 8; 39
+// ranges 58.3, 54.1 and 54.5; 12 ranges 8.5, 7.9 and 8.2).
+constexpr int JOIN_WARPS = 4, JOIN_BATCH = 4;
 template <typename QT>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_constant__ Params p, int heads_per_unit) {
     grid_dependency_wait();
@@ -664,7 +695,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
     if (w.x < 0) return;
     const PagedAttnArgs &a = p.a;
     const int s = w.x, kvh = w.y / p.parts, h0 = kvh * p.group + (w.y % p.parts) * heads_per_unit;
-    const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     if (h0 + h >= (kvh + 1) * p.group) return;
     const int c0 = w.z >> 1, n = w.w - c0 + 1;
     auto slot = [&](int i) {   // the unit's first range may be its CTA's second segment
@@ -672,6 +703,22 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
     };
     __shared__ float4 sum[JOIN_WARPS][32];
     __shared__ float weight[JOIN_WARPS];
+    // The warp's first ranges come along with all ranges' maxima.
+    float2 ml[JOIN_BATCH];
+    float4 v[JOIN_BATCH];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int b = 0; b < JOIN_BATCH; ++b) {
+            const int i = i0 + warps * b;
+            ml[b] = make_float2(-INFINITY, 0.0f);
+            v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < n) {
+                ml[b] = __ldcg(reinterpret_cast<const float2 *>(slot(i) + 128));
+                v[b] = ld_in(reinterpret_cast<const float4 *>(slot(i)) + lane);
+            }
+        }
+    };
+    load(warp);
     float top = -INFINITY;
     for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(slot(i) + 128));
 #pragma unroll
@@ -679,30 +726,29 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
     const float base = top == -INFINITY ? 0.0f : top;
     float l = 0.0f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = warp; i < n; i += JOIN_WARPS) {
-        const float *sp = slot(i);
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(sp + 128));
-        const float4 v = ld_in(reinterpret_cast<const float4 *>(sp) + lane);
-        const float f = ex2(ml.x - base);
-        l = fmaf(ml.y, f, l);
-        y.x = fmaf(v.x, f, y.x);
-        y.y = fmaf(v.y, f, y.y);
-        y.z = fmaf(v.z, f, y.z);
-        y.w = fmaf(v.w, f, y.w);
+    for (int i0 = warp; i0 < n; i0 += warps * JOIN_BATCH) {
+        if (i0 != warp) load(i0);
+#pragma unroll
+        for (int b = 0; b < JOIN_BATCH; ++b) {
+            const float f = ex2(ml[b].x - base);
+            l = fmaf(ml[b].y, f, l);
+            y.x = fmaf(v[b].x, f, y.x);
+            y.y = fmaf(v[b].y, f, y.y);
+            y.z = fmaf(v[b].z, f, y.z);
+            y.w = fmaf(v[b].w, f, y.w);
+        }
     }
     sum[warp][lane] = y;
     if (lane == 0) weight[warp] = l;
     __syncthreads();
     if (warp > 0) return;
-#pragma unroll
-    for (int v = 1; v < JOIN_WARPS; ++v) {
-        const float4 z = sum[v][lane];
+    for (int o = 1; o < warps; ++o) {
+        const float4 z = sum[o][lane];
         y.x += z.x;
         y.y += z.y;
         y.z += z.z;
         y.w += z.w;
-        l += weight[v];
+        l += weight[o];
     }
     const size_t row = static_cast<size_t>(s) * a.nheads + h0 + h;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -830,7 +876,9 @@ cudaError_t run(const Params &p, int grid, cudaStream_t stream) {
         if (e == cudaSuccess) configured_device = dev;
     }
     if (e == cudaSuccess) e = launch(kernel, dim3(grid), THREADS, smem, stream, p);
-    if (e == cudaSuccess) e = launch(join_kernel<QT>, dim3(grid, std::min(p.group, 8 * kMT)), 32 * JOIN_WARPS, 0, stream, p, 8 * kMT);
+    const int ranges = static_cast<int>(grid / (static_cast<long long>(p.a.nseq) * p.units)) + 1;   // of a unit, on average
+    const int join_threads = ranges <= JOIN_BATCH ? 32 : 32 * JOIN_WARPS;
+    if (e == cudaSuccess) e = launch(join_kernel<QT>, dim3(grid, std::min(p.group, 8 * kMT)), join_threads, 0, stream, p, 8 * kMT);
     if (e == cudaSuccess && p.logits != nullptr)
         e = launch(mass_kernel, dim3(std::min((p.stride + MASS_CELLS - 1) / MASS_CELLS, 512), p.a.nseq), MASS_CELLS, 0, stream, p);
     return e;
