@@ -36,9 +36,10 @@
 // first weights of a tile are taken before its maximum is known.
 //
 // CTAs that have finished an item take the next from those of the grid that
-// have not started (cluster launch control): longest rows first, balanced
-// whatever the lengths, and the next item's copies and first products run
-// while the last one's results leave. With few items per SM each item's keys
+// have not started (cluster launch control, asked with the copies of the last tile:
+// the chunks below 214 us, and 231 asked with those of the second): longest rows
+// first, balanced whatever the lengths, and the next item's copies and first
+// products run while the last one's results leave. With few items per SM each item's keys
 // are split into parts whose partial sums window_join_kernel adds.
 //
 // The keys that an item's rows see are the sinks and one contiguous range.
@@ -51,12 +52,12 @@
 // is therefore computed again from its visible keys alone (attend_row, also
 // the whole path for strides that a tensor map cannot express).
 //
-// Measured (GB300, 32 heads on 8 KV heads): 8,192 tokens causal 338 us, 1.63
+// Measured (GB300, 32 heads on 8 KV heads): 8,192 tokens causal 337 us, 1.63
 // PFLOP/s of the visible pairs, 0.85 of the measured cuBLAS burst; 8,192 tokens
-// in a window of 1,024 113 us, 0.61 (masked edges, and about 2.5 us per item
+// in a window of 1,024 111 us, 0.61 (masked edges, and about 2.5 us per item
 // that its 9 key tiles do not hide); 8 ragged prompts of up to 2,048 tokens in a
-// window of 512 79 us; chunks of up to 512 tokens over 7,000 to 16,000 keys 240
-// us, of which the join takes 20.
+// window of 512 78 us; chunks of up to 512 tokens over 7,000 to 16,000 keys 214
+// us, of which the join takes 18.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -80,7 +81,6 @@ constexpr int MMA_WARP = 8, COPY_WARP = 9, OUT_WARP = 12, WTHREADS = 512;
 // 128 registers a thread at launch: 8 softmax warps x 168 + 8 x 88 = 16 x 128.
 constexpr int MORE_REGISTERS = 168, FEW_REGISTERS = 88;
 constexpr int STAGING = 32 * 128;           // bytes of an output warp's staging: 128 bytes of each of its rows
-constexpr int PART_TILES = 4;               // key tiles of a part at least
 constexpr int SLOT_ROW = 132;               // 128 sums, reference, weight sum, padding
 constexpr float LAZY = 8.0f;
 constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
@@ -91,6 +91,9 @@ struct WindowParams {
     int group, tokens;      // query heads per KV head; tokens of a query tile
     int k_has_heads, v_has_heads;   // 0: all KV heads at one address
     int pairs, splits;      // pairs of query tiles of the batch; parts that an item's keys are split into at most
+    int part_tiles;         // key tiles of a part, at least on average
+    int falling;            // parts fall in size
+    Divider per_split, per_part;   // by splits, by part_tiles
     float *slots;           // [pairs][nkv][splits][2 x 128 rows][SLOT_ROW]
     struct Work *split_work;   // [pairs x nkv], by item number: for the join, when splits > 1
     uint64_t wait_ns;
@@ -237,10 +240,32 @@ struct Work {
         first0 = keys.first(pos0);
         last1 = tokens1 > 0 ? keys.last(pos1 + tokens1 - 1) : -1;
         first1 = keys.first(pos1);
-        const int n = keys.tiles(), each = max((n + p.splits - 1) / p.splits, PART_TILES);
-        parts = max(1, (n + each - 1) / each);
-        j0 = min(it.part * each, n);
-        j1 = min(j0 + each, n);
+        const int n = keys.tiles();
+        parts = 1;
+        j0 = 0;
+        j1 = n;
+        if (p.splits > 1 && n > 0) {
+            if (p.falling) {
+                parts = min(p.splits, divide(p.per_part, n - 1) + 1);
+                j0 = falling_begin(it.part, n);
+                j1 = falling_begin(it.part + 1, n);
+            } else {
+                const int each = max(divide(p.per_split, n - 1) + 1, p.part_tiles);
+                parts = (n + each - 1) / each;
+                j0 = min(it.part * each, n);
+                j1 = min(j0 + each, n);
+            }
+        }
+    }
+    // First key tile of part k of parts that fall in size, in the ratio m - 0.3, m - 1.3, .. 0.7 of m
+    // parts (each has a tile), so that all items' large parts run first and the small ones fill
+    // the ends.
+    __device__ __forceinline__ int falling_begin(int k, int n) const {
+        if (k == 0) return 0;
+        if (k >= parts) return n;
+        const uint32_t of = parts * (5 * parts + 2), at = k * (10 * parts - 5 * k + 2);
+        const uint32_t whole = n / of, left = n - whole * of;   // n x at / of, where n x at might not fit
+        return static_cast<int>(whole * at + left * at / of);
     }
     // Does any row of query tile i see a key of key tile j?
     __device__ __forceinline__ bool needed(int i, int j) const {
@@ -456,7 +481,9 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
             }
             const ItemKeys &keys = w.keys;
             for (int j2 = 2 * w.j0; ok && j2 < 2 * w.j1; ++j2, ++kv) {   // keys, then values of tile j2 / 2
-                if (j2 == 2 * w.j0 + 2) ask();   // the first copies do not wait for it
+                // The next item is claimed with the last tile's copies: earlier, items would be dealt
+                // out by when CTAs start one and not by when they end one.
+                if (j2 == 2 * w.j1 - 2 && j2 > 2 * w.j0) ask();
                 const int slot = kv % STAGES, i0 = (j2 >> 1) * ROWS;
                 ok = wait_warp(&bars->kv_empty[slot], ((kv / STAGES) & 1) ^ 1);
                 if (!ok) break;
@@ -923,9 +950,17 @@ bool encode_map(CUtensorMap *map, bool bf16, const void *p, int64_t heads, int64
 bool map_stride(int64_t n, int64_t elements) { return n <= 1 || (elements > 0 && elements < (1LL << 38)); }
 
 // How the batch is cut, from what the host knows. Items are split over their
-// keys when there are fewer than two per SM, into about three per SM.
+// keys when there are fewer than two per SM, into about two parts per SM (three:
+// 16 items of 170 tiles 80 us against 63). Items that fill less than a quarter of
+// the SMs: into equal parts of 4 key tiles at least, which mostly run at once. More
+// items: into parts that fall in size, the longer the more items there are, as what
+// a split saves falls and the partial sums it moves grow with the items. Measured:
+// 200 items of 55 to 128 tiles 215 us, in equal parts 233; 250 items of 5 tiles
+// 27 us whole and 52 in two parts; 28 items of 12 tiles 21 us in equal parts of 4
+// tiles and 25 in falling ones of 6.
 struct Split {
-    int pairs, splits;
+    int pairs, splits, part_tiles;
+    bool falling;
 };
 Split split(int nseq, int total_q, int nheads, int nkv) {
     const int per = 2 * (ROWS / (nheads / nkv)), sms = device_sm_count();
@@ -933,17 +968,19 @@ Split split(int nseq, int total_q, int nheads, int nkv) {
     const long long least = static_cast<long long>(std::max(total_q / per, std::min(nseq, total_q))) * nkv;
     // The partial results are laid out for empty sequences too: no more than 8 parts per SM in all.
     const long long room = std::max(1LL, 8LL * sms / (static_cast<long long>(pairs) * nkv));
-    const long long parts = least >= 2LL * sms ? 1 : (3LL * sms + least - 1) / least;
-    return {pairs, static_cast<int>(std::min(std::min(parts, room), 64LL))};
+    const bool falling = 4 * least >= sms;
+    const long long wanted = (2LL * sms + least - 1) / std::max(1LL, least);
+    const int part_tiles = falling ? 4 + static_cast<int>(std::min(28LL, 16 * least / sms)) : 4;
+    return {pairs, static_cast<int>(least >= 2LL * sms ? 1LL : std::min(std::min(wanted, room), 64LL)), part_tiles, falling};
 }
 size_t work_bytes(int pairs, int nkv) { return (sizeof(Work) * static_cast<size_t>(pairs) * nkv + 15) / 16 * 16; }
-// Parts of at least PART_TILES tiles that a long item has.
-int most_parts(const WindowAttnArgs &a, int tokens) {
+// Parts of at least part_tiles tiles that a long item has.
+int most_parts(const WindowAttnArgs &a, int tokens, int part_tiles) {
     // Lengths are not known here: twice the mean stands for the longest (a part may then be longer).
     long long keys = std::min<long long>(a.total_k, 2LL * ((static_cast<long long>(a.total_k) + a.nseq - 1) / a.nseq));
     if (a.window >= 0) keys = std::min(keys, static_cast<long long>(a.window) + std::min(a.sinks, a.total_k) + PIECE + 2 * tokens);
     const long long tiles = (keys + ROWS - 1) / ROWS;
-    return static_cast<int>(std::max(1LL, std::min(64LL, (tiles + PART_TILES - 1) / PART_TILES)));
+    return static_cast<int>(std::max(1LL, std::min(64LL, (tiles + part_tiles - 1) / part_tiles)));
 }
 
 template <typename T>
@@ -991,7 +1028,11 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
         return cudaErrorNotSupported;
     const Split x = split(a.nseq, a.total_q, a.nheads, a.nkv);
     p.pairs = x.pairs;
-    p.splits = std::min(x.splits, most_parts(a, p.tokens));
+    p.part_tiles = x.part_tiles;
+    p.falling = x.falling;
+    p.splits = std::min(x.splits, most_parts(a, p.tokens, x.part_tiles));
+    p.per_split = make_divider(p.splits);
+    p.per_part = make_divider(p.part_tiles);
     p.split_work = static_cast<Work *>(a.scratch);
     p.slots = reinterpret_cast<float *>(static_cast<char *>(a.scratch) + work_bytes(p.pairs, a.nkv));
     const long long items = static_cast<long long>(p.pairs) * a.nkv * p.splits;

@@ -94,6 +94,15 @@ def test_long(dev, dtype, nq, nk, kw):
     both(dev, nq, nk, 2, 4, dtype, **kw)
 
 
+@pytest.mark.parametrize("nq,nk,kw", [([320], [1537], {}), ([320], [8200], dict(window=5000, sinks=20)),
+                                      ([300, 150], [2600, 1200], {}), ([640], [2050], dict(window=1500, sinks=3)),
+                                      ([100, 1, 540], [700, 3000, 5000], {}), ([1216], [4100], {}),
+                                      ([2000, 301], [7000, 1000], dict(window=6000, sinks=1))])
+def test_parts_of_every_size(dev, nq, nk, kw):
+    """A quarter to two items per SM: keys split into 2 to 8 parts that fall in size, some rows' all masked."""
+    both(dev, nq, nk, 8, 4, **kw)
+
+
 def test_many_sequences(dev):
     n = [(7 * i) % 23 for i in range(600)]
     both(dev, n, n, 1, 2, window=9, sinks=2)
