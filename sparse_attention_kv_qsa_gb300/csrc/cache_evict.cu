@@ -38,25 +38,33 @@ constexpr int MAX_KEYS = 40960;   // keys a CTA holds; longer runs are read agai
 
 struct alignas(16) SelectShared {
     int hist[3][BINS];
-    int coarse[3][32];
-    int run[2];   // kept for their key, and equal to the last key, of this CTA's run: for the others
+    int4 own[8];                         // this CTA's coarse counts
+    int4 coarse[3][MAX_CLUSTER][8];      // each CTA's, which it puts into every CTA's (adding them there by atomics: 2 us a pass)
+    int2 run[MAX_CLUSTER];   // kept for their key, and equal to the last key, of each CTA's run
     int warp_sums[SEL_WARPS], warp_ties[SEL_WARPS];
-    int digit, left;
+    int digit, left, same;
 };
 
-// A count, or two, of CTA `rank` of the cluster.
-__device__ __forceinline__ int ld_shared_rank(const int *p, uint32_t rank) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_shared_rank(smem_u32(p), rank)));
-    return v;
+// Shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ void st_shared_rank4(int4 *p, uint32_t rank, int4 v) {
+    asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(map_shared_rank(smem_u32(p), rank)), "r"(v.x),
+                 "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void st_shared_rank2(int2 *p, uint32_t rank, int2 v) {
+    asm volatile("st.shared::cluster.v2.s32 [%0], {%1, %2};" ::"r"(map_shared_rank(smem_u32(p), rank)), "r"(v.x), "r"(v.y)
+                 : "memory");
 }
 __device__ __forceinline__ int2 ld_shared_rank2(const int *p, uint32_t rank) {
     int2 v;
     asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
                  : "=r"(v.x), "=r"(v.y)
-                 : "r"(map_shared_rank(smem_u32(p), rank)));
+                 : "r"(map_shared_rank(smem_u32(p), rank))
+                 : "memory");
     return v;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Inclusive prefix sum over the warp.
 __device__ __forceinline__ int warp_scan(int x) {
@@ -83,10 +91,10 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
     const float *mass = a.mass + s * a.mass_stride;
     int32_t *kept = a.kept + static_cast<size_t>(s) * a.budget;
     float *nm = a.new_mass + s * a.new_mass_stride;
-    const int all_tid = rank * SEL_THREADS + tid, all_threads = cluster * SEL_THREADS;
-    if (all_tid == 0) a.new_lens[s] = m;
-    for (int i = m + all_tid; i < a.new_mass_cols; i += all_threads) nm[i] = 0.0f;
+    if (rank == 0 && tid == 0) a.new_lens[s] = m;
     if (n <= a.budget) {   // the whole cluster leaves here
+        const int all_tid = rank * SEL_THREADS + tid, all_threads = cluster * SEL_THREADS;
+        for (int i = m + all_tid; i < a.new_mass_cols; i += all_threads) nm[i] = 0.0f;
         for (int i = all_tid; i < a.budget; i += all_threads) {
             kept[i] = i < m ? i : -1;
             if (i < m) nm[i] = ld_in(mass + i);
@@ -95,26 +103,28 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
     }
     // Sinks and recent cells; the candidates between them are [c0, c1).
     const int c0 = a.sinks, c1 = n - a.recent, recent_at = a.budget - a.recent;
-    for (int i = all_tid; i < a.sinks; i += all_threads) {
-        kept[i] = i;
-        nm[i] = ld_in(mass + i);
-    }
-    for (int i = all_tid; i < a.recent; i += all_threads) {
-        kept[recent_at + i] = c1 + i;
-        nm[recent_at + i] = ld_in(mass + c1 + i);
-    }
+    auto edges = [&](int thread, int threads) {   // of each CTA
+        const int first = rank * threads + thread, step = cluster * threads;
+        for (int i = first; i < a.sinks; i += step) {
+            kept[i] = i;
+            nm[i] = ld_in(mass + i);
+        }
+        for (int i = first; i < a.recent; i += step) {
+            kept[recent_at + i] = c1 + i;
+            nm[recent_at + i] = ld_in(mass + c1 + i);
+        }
+        for (int i = m + first; i < a.new_mass_cols; i += step) nm[i] = 0.0f;
+    };
     int left = recent_at - a.sinks;   // candidates to keep
-    if (left == 0) return;
+    if (left == 0) {
+        edges(tid, SEL_THREADS);
+        return;
+    }
+    if (cluster > 1) cluster_arrive();   // all CTAs have begun
     const int per = (c1 - c0 + cluster - 1) / cluster;
     const int j0 = min(c0 + rank * per, c1), count = min(per, c1 - j0);
     const bool held = per <= max_keys;
     auto key_at = [&](int i) { return held ? keys[i] : score_key(ld_in(mass + j0 + i)); };
-    auto barrier = [&]() {
-        if (cluster > 1)
-            cluster_sync_all();
-        else
-            __syncthreads();
-    };
 
     uint32_t prefix = 0;
 #pragma unroll 1
@@ -142,51 +152,58 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
             }
         }
         __syncthreads();
-        {   // 32 coarse digits, a warp each
-            const int each = bins / 32;
-            int sum = hist[warp * each + lane] + (each > 32 ? hist[warp * each + 32 + lane] : 0);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
-            if (lane == 0) sh.coarse[pass][warp] = sum;
+        const int each = bins / 32;   // of a coarse digit, one a warp
+        const int sum = __reduce_add_sync(FULL_MASK, hist[warp * each + lane] + (each > 32 ? hist[warp * each + 32 + lane] : 0));
+        if (lane == 0) reinterpret_cast<int *>(sh.own)[warp] = sum;
+        __syncthreads();
+        if (cluster > 1) {
+            if (pass == 0) cluster_wait();
+            if (tid < 8 * cluster) st_shared_rank4(&sh.coarse[pass][rank][tid & 7], tid >> 3, sh.own[tid & 7]);
+            cluster_sync_all();
         }
-        barrier();
         if (warp == 0) {
-            // From the highest digit down: the coarse digit of all CTAs' counts that the
-            // `left`-th key falls into, then the digit within it.
-            auto find = [&](const int *counts, int n, int &before) {
-                int mine = 0;
-                const int at = n - 1 - lane;
-                if (at >= 0) {
-                    int x[cluster];
+            // From the highest digit down: the coarse digit that the `left`-th key falls into, then the
+            // digit within it, two per lane, for which all CTAs' counts are fetched.
+            int mine = 0;
 #pragma unroll
-                    for (int r = 0; r < cluster; ++r) x[r] = cluster > 1 ? ld_shared_rank(counts + at, r) : counts[at];
+            for (int r = 0; r < cluster; ++r)
+                mine += reinterpret_cast<const int *>(cluster > 1 ? sh.coarse[pass][r] : sh.own)[31 - lane];
+            const int upto = warp_scan(mine);
+            const int l = __ffs(__ballot_sync(FULL_MASK, upto >= left)) - 1, c = 31 - l;
+            int before = __shfl_sync(FULL_MASK, upto - mine, l);
+            const int at = each - 2 - 2 * lane;
+            int low = 0, high = 0;
+            if (at >= 0) {
+                const int *counts = hist + c * each + at;
+                int2 x[cluster];
 #pragma unroll
-                    for (int r = 0; r < cluster; ++r) mine += x[r];
+                for (int r = 0; r < cluster; ++r) x[r] = cluster > 1 ? ld_shared_rank2(counts, r) : *reinterpret_cast<const int2 *>(counts);
+#pragma unroll
+                for (int r = 0; r < cluster; ++r) {
+                    low += x[r].x;
+                    high += x[r].y;
                 }
-                const int upto = warp_scan(mine);
-                const uint32_t reach = __ballot_sync(FULL_MASK, upto + before >= left);
-                if (reach == 0u) {   // not among these 32
-                    before += __shfl_sync(FULL_MASK, upto, 31);
-                    return -1;
-                }
-                const int l = __ffs(reach) - 1;
-                before += __shfl_sync(FULL_MASK, upto - mine, l);
-                return n - 1 - l;
-            };
-            const int each = bins / 32;
-            int before = 0;
-            const int c = find(sh.coarse[pass], 32, before);
-            int d = -1;
-            if (each > 32) d = find(hist + c * each + 32, 32, before);
-            d = d >= 0 ? c * each + 32 + d : c * each + find(hist + c * each, 32, before);
-            if (lane == 0) {
-                sh.digit = d;
-                sh.left = left - before;
             }
+            const int upto2 = warp_scan(low + high);
+            const int l2 = __ffs(__ballot_sync(FULL_MASK, before + upto2 >= left)) - 1;
+            if (lane == l2) {
+                before += upto2 - low - high;
+                const bool upper = before + high >= left;
+                sh.digit = c * each + at + upper;
+                sh.left = left - before - (upper ? 0 : high);
+                sh.same = upper ? high : low;
+            }
+        } else if (pass == 0) {
+            edges(tid - 32, SEL_THREADS - 32);   // while the first warp searches
         }
         __syncthreads();
         prefix |= static_cast<uint32_t>(sh.digit) << shift;
         left = sh.left;
+        if (left == sh.same) {   // all keys of the digit are kept: those above its lowest less one (not 0: no key is)
+            --prefix;
+            left = 0;
+            break;
+        }
     }
 
     // Keys above `prefix` are kept, and the first `left` that equal it. Each warp
@@ -199,34 +216,26 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
         above += key > prefix;
         ties += key == prefix;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        above += __shfl_xor_sync(FULL_MASK, above, o);
-        ties += __shfl_xor_sync(FULL_MASK, ties, o);
-    }
+    above = __reduce_add_sync(FULL_MASK, above);
+    ties = __reduce_add_sync(FULL_MASK, ties);
     if (lane == 0) {
         sh.warp_sums[warp] = above;
         sh.warp_ties[warp] = ties;
     }
     __syncthreads();
-    const int upto_above = warp_scan(sh.warp_sums[lane]), upto_ties = warp_scan(sh.warp_ties[lane]);
-    int above_before = __shfl_sync(FULL_MASK, upto_above, warp) - above;
-    int ties_before = __shfl_sync(FULL_MASK, upto_ties, warp) - ties;
-    const int above_all = __shfl_sync(FULL_MASK, upto_above, 31), ties_all = __shfl_sync(FULL_MASK, upto_ties, 31);
+    const int warp_above = sh.warp_sums[lane], warp_ties = sh.warp_ties[lane];
+    int above_before = __reduce_add_sync(FULL_MASK, lane < warp ? warp_above : 0);
+    int ties_before = __reduce_add_sync(FULL_MASK, lane < warp ? warp_ties : 0);
     if (cluster > 1) {
-        if (tid == 0) {
-            sh.run[0] = above_all;
-            sh.run[1] = ties_all;
+        if (warp == 0) {
+            const int2 all = make_int2(__reduce_add_sync(FULL_MASK, warp_above), __reduce_add_sync(FULL_MASK, warp_ties));
+            if (lane < cluster) st_shared_rank2(&sh.run[rank], lane, all);
         }
+        // The last that a CTA does with another's memory is before this barrier: any may leave after it.
         cluster_sync_all();
-        int2 x[cluster];
-#pragma unroll
-        for (int r = 0; r < cluster; ++r) x[r] = ld_shared_rank2(sh.run, r);
-#pragma unroll
-        for (int r = 0; r < cluster; ++r) {
-            above_before += r < rank ? x[r].x : 0;
-            ties_before += r < rank ? x[r].y : 0;
-        }
+        const int2 x = lane < rank ? sh.run[lane] : make_int2(0, 0);
+        above_before += __reduce_add_sync(FULL_MASK, x.x);
+        ties_before += __reduce_add_sync(FULL_MASK, x.y);
     }
     for (int i0 = r0; i0 < r1; i0 += 32) {
         const int i = i0 + lane;
@@ -246,7 +255,6 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
         above_before += __popc(up);
         ties_before += __popc(eq);
     }
-    if (cluster > 1) cluster_sync_all();   // no CTA leaves while another may read its counts
 }
 
 constexpr int COPY_THREADS = 256, COPY_BATCH = 4;
