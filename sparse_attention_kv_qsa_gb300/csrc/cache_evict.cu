@@ -6,21 +6,23 @@
 // cell to keep by a radix search on the order-preserving key of
 // csrc/qsa_internal.cuh, 11, 11 and 10 bits at a time. Each CTA holds a run of
 // the candidates' keys in shared memory, so the masses are read once, and
-// counts its digits there; after one cluster barrier every CTA adds all CTAs'
-// counts of a digit through distributed shared memory and finds the same
-// digit. The search ends with the exact 32-bit key of that cell and how many
-// cells with that very key are kept, the lowest first. The cells are then
-// listed in order: warps take consecutive runs, count, scan, and write.
-// Latency bounds it: four cluster barriers and the scans between them.
+// counts its digits there. Its counts of 32 coarse digits go into every CTA's
+// shared memory; after a cluster barrier each CTA finds the same coarse digit
+// and fetches all CTAs' counts of the fine ones within it. The search ends with
+// the exact 32-bit key of that cell and how many cells with that very key are
+// kept, the lowest first, or earlier where a digit's cells are all kept. The
+// cells are then listed in order: warps take consecutive runs, count, scan, and
+// write. Latency bounds it: per pass a count, a barrier (1,200 cycles) and a
+// fetch of the others' counts (2,000).
 //
 // copy_cells_kernel, copy_pieces_kernel: bandwidth. 16-byte pieces of keys and
 // values, a batch of loads before its stores.
 //
 // Measured (GB300): 2 sequences of up to 131,072 int8 cells of 8 heads cut to
-// 16,384, 46 us: 22 to choose, 24 to copy 136 MB (0.83 of the measured copy rate);
-// one sequence of 576 cells cut to 512, 9.2 us, launches and latencies. Masses
+// 16,384, 41 us: 16 to choose, 24 to copy 136 MB (0.83 of the measured copy rate);
+// one sequence of 576 cells cut to 512, 7.1 us, launches and latencies. Masses
 // crowd into a few digits of the first pass, yet plain shared-memory atomics beat
-// one atomic per different digit of a warp (choosing 40 us against 48).
+// one atomic per different digit of a warp (choosing 40 us against 48 then).
 #include <algorithm>
 
 #include "cache_internal.cuh"
@@ -31,7 +33,7 @@ namespace qsa {
 namespace {
 
 constexpr int SEL_THREADS = 1024, SEL_WARPS = SEL_THREADS / 32;
-// CTAs of a long sequence. 16 (not portable, but within a GB300 GPC) against 8: 131,072 cells 22 against 26 us.
+// CTAs of a long sequence. 16 (not portable, but within a GB300 GPC) against 8: 131,072 cells chosen in 22 against 26 us then.
 constexpr int MAX_CLUSTER = 16;
 constexpr int BINS = 2048;
 constexpr int MAX_KEYS = 40960;   // keys a CTA holds; longer runs are read again in every pass
@@ -80,7 +82,7 @@ __device__ __forceinline__ int warp_scan(int x) {
 template <int kCluster>
 __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArgs a, int max_keys) {
     constexpr int cluster = kCluster;
-    extern __shared__ uint32_t keys[];
+    extern __shared__ __align__(16) uint32_t keys[];
     __shared__ SelectShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster;
@@ -123,8 +125,21 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
     if (cluster > 1) cluster_arrive();   // all CTAs have begun
     const int per = (c1 - c0 + cluster - 1) / cluster;
     const int j0 = min(c0 + rank * per, c1), count = min(per, c1 - j0);
-    const bool held = per <= max_keys;
-    auto key_at = [&](int i) { return held ? keys[i] : score_key(ld_in(mass + j0 + i)); };
+    const bool held = per <= max_keys;   // a run's last quad fits too: max_keys is a multiple of 4
+    // Keys i .. i + 3; 0, which is no cell's key, past the end.
+    auto quad_at = [&](int i, uint32_t (&key)[4]) {
+        if (held) {
+            const uint4 k = *reinterpret_cast<const uint4 *>(keys + i);
+            key[0] = k.x;
+            key[1] = k.y;
+            key[2] = k.z;
+            key[3] = k.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) key[e] = i + e < count ? score_key(ld_in(mass + j0 + i + e)) : 0u;
+        }
+    };
+    if (held && tid < 4 && count + tid < max_keys) keys[count + tid] = 0u;
 
     uint32_t prefix = 0;
 #pragma unroll 1
@@ -132,23 +147,34 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? 2048 : 1024;
         int *hist = sh.hist[pass];
         __syncthreads();   // the counts are cleared
-        constexpr int BATCH = 8;   // masses under way at once
-        for (int i0 = warp * 32; i0 < count; i0 += BATCH * SEL_THREADS) {
-            uint32_t key[BATCH];
+        if (pass == 0) {
+            constexpr int BATCH = 8;   // masses under way at once
+            for (int i0 = warp * 32; i0 < count; i0 += BATCH * SEL_THREADS) {
+                float x[BATCH];
 #pragma unroll
-            for (int b = 0; b < BATCH; ++b) {
-                const int i = i0 + b * SEL_THREADS + lane;
-                if (i < count) key[b] = pass == 0 || !held ? __float_as_uint(ld_in(mass + j0 + i)) : keys[i];
+                for (int b = 0; b < BATCH; ++b) {
+                    const int i = i0 + b * SEL_THREADS + lane;
+                    if (i < count) x[b] = ld_in(mass + j0 + i);
+                }
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) {
+                    const int i = i0 + b * SEL_THREADS + lane;
+                    if (i0 + b * SEL_THREADS >= count) break;
+                    if (i < count) {
+                        const uint32_t key = score_key(x[b]);
+                        if (held) keys[i] = key;
+                        atomicAdd(hist + (key >> shift), 1);
+                    }
+                }
             }
+        } else {
+            const int known = pass == 1 ? 21 : 10;   // bits above it are those of `prefix`
+            for (int i = 4 * tid; i < count; i += 4 * SEL_THREADS) {
+                uint32_t key[4];
+                quad_at(i, key);
 #pragma unroll
-            for (int b = 0; b < BATCH; ++b) {
-                const int i = i0 + b * SEL_THREADS + lane;
-                if (i0 + b * SEL_THREADS >= count) break;
-                bool in = i < count;
-                if (pass == 0 || !held) key[b] = score_key(__uint_as_float(key[b]));
-                if (pass == 0 && held && in) keys[i] = key[b];
-                if (pass > 0) in = in && (key[b] ^ prefix) >> (pass == 1 ? 21 : 10) == 0;
-                if (in) atomicAdd(hist + ((key[b] >> shift) & (bins - 1)), 1);
+                for (int e = 0; e < 4; ++e)
+                    if ((key[e] ^ prefix) >> known == 0) atomicAdd(hist + ((key[e] >> shift) & (bins - 1)), 1);
             }
         }
         __syncthreads();
@@ -207,14 +233,18 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
     }
 
     // Keys above `prefix` are kept, and the first `left` that equal it. Each warp
-    // takes a run of whole 32s, so that the lists stay in order.
-    const int run = (count + SEL_THREADS - 1) / SEL_THREADS * 32;
+    // takes a run of whole 128s, so that the lists stay in order.
+    const int run = (count + 4 * SEL_THREADS - 1) / (4 * SEL_THREADS) * 128;
     const int r0 = min(warp * run, count), r1 = min(r0 + run, count);
     int above = 0, ties = 0;
-    for (int i = r0 + lane; i < r1; i += 32) {
-        const uint32_t key = key_at(i);
-        above += key > prefix;
-        ties += key == prefix;
+    for (int i = r0 + 4 * lane; i < r1; i += 128) {
+        uint32_t key[4];
+        quad_at(i, key);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            above += key[e] > prefix;
+            ties += key[e] == prefix;
+        }
     }
     above = __reduce_add_sync(FULL_MASK, above);
     ties = __reduce_add_sync(FULL_MASK, ties);
@@ -237,23 +267,30 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const CacheEvictArg
         above_before += __reduce_add_sync(FULL_MASK, x.x);
         ties_before += __reduce_add_sync(FULL_MASK, x.y);
     }
-    for (int i0 = r0; i0 < r1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t key = i < r1 ? key_at(i) : 0u;
-        const uint32_t up = __ballot_sync(FULL_MASK, i < r1 && key > prefix);
-        const uint32_t eq = __ballot_sync(FULL_MASK, i < r1 && key == prefix);
-        const uint32_t lower = lanemask_lt();
-        const int tie_rank = ties_before + __popc(eq & lower);
-        const bool take = ((up >> lane) & 1u) || (((eq >> lane) & 1u) && tie_rank < left);
-        if (take) {
-            const int at = a.sinks + above_before + __popc(up & lower) + min(tie_rank, left);
-            kept[at] = j0 + i;
-            // The mass is its key backwards, except that the key of -0 is +0's and NaN's is -infinity's.
-            const bool lost = key == 0x80000000u || key == 0x007FFFFFu;
-            nm[at] = lost ? ld_in(mass + j0 + i) : __uint_as_float((key >> 31) ? key ^ 0x80000000u : ~key);
+    for (int i0 = r0; i0 < r1; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        uint32_t key[4] = {0u, 0u, 0u, 0u};
+        if (i < r1) quad_at(i, key);
+        int own = 0;   // kept for the key, and equal keys x 2^16
+#pragma unroll
+        for (int e = 0; e < 4; ++e) own += key[e] > prefix ? 1 : key[e] == prefix ? 0x10000 : 0;
+        const int upto = warp_scan(own), before = upto - own, all = __shfl_sync(FULL_MASK, upto, 31);
+        int at = above_before + (before & 0xFFFF), tie = ties_before + (before >> 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool up = key[e] > prefix, eq = key[e] == prefix;
+            if (up || (eq && tie < left)) {
+                const int to = a.sinks + at + min(tie, left);
+                kept[to] = j0 + i + e;
+                // The mass is its key backwards, except that the key of -0 is +0's and NaN's is -infinity's.
+                const bool lost = key[e] == 0x80000000u || key[e] == 0x007FFFFFu;
+                nm[to] = lost ? ld_in(mass + j0 + i + e) : __uint_as_float((key[e] >> 31) ? key[e] ^ 0x80000000u : ~key[e]);
+            }
+            at += up;
+            tie += eq;
         }
-        above_before += __popc(up);
-        ties_before += __popc(eq);
+        above_before += all & 0xFFFF;
+        ties_before += all >> 16;
     }
 }
 
@@ -389,7 +426,7 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
     const int capacity = a.table_cols * a.kv.page_size;
     // One CTA searches what a few rounds of its threads cover.
     const int cluster = capacity <= 4 * SEL_THREADS ? 1 : MAX_CLUSTER;
-    const int max_keys = std::min((capacity + cluster - 1) / cluster, MAX_KEYS);
+    const int max_keys = std::min((capacity + cluster - 1) / cluster + 3, MAX_KEYS) & ~3;   // whole quads
     static thread_local int configured_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -77,6 +77,21 @@ def test_ties_keep_the_lower_cells(dev):
         run(dev, [n, n - 1], 500, 3, 30, mass=[values, values[:n - 1]])
 
 
+@pytest.mark.parametrize("n,budget", [(700, 200), (30000, 5000)])
+@pytest.mark.parametrize("high,low", [(2.0, 0.5), (1.0625, 1.0), (1.0000001192092896, 1.0), (-0.5, -math.inf), (1e-45, 0.0)])
+def test_exactly_the_larger_masses_fit(dev, n, budget, high, low):
+    """The cells to keep are all those of one mass, told apart by the first, second or last bits; and one more, one less."""
+    for more in (-1, 0, 1):
+        mass = [low] * n
+        for i in range(budget - 4 - 20 + more):
+            mass[4 + (i * 7919) % (n - 24)] = high             # 7919 is prime: other cells every time
+        run(dev, [n], budget, 4, 20, 1, 16, I8, mass=[mass])
+
+
+def test_more_cells_than_shared_memory_holds(dev):
+    run(dev, [700001], 9001, 4, 100, 1, 64, I8)
+
+
 def test_masses_of_every_kind(dev):
     """NaN counts as the lowest, infinities and tiny differences are told apart."""
     n = 2000
