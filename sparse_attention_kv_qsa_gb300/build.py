@@ -88,7 +88,7 @@ def _compile_binding(force: bool) -> str:
 def _link_binding(obj: str) -> None:
     lib = os.path.join(_torch_dir(), "lib")
     cmd = [shutil.which("g++") or "g++", "-shared", "-o", OPS + ".tmp", obj, "-L", BUILD, "-l:libqsa.so", "-L", lib,
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of {OPS} failed:\n{r.stdout}\n{r.stderr}")
