@@ -33,8 +33,7 @@ namespace qsa {
 namespace {
 
 constexpr int SEL_THREADS = 1024, SEL_WARPS = SEL_THREADS / 32;
-// CTAs of a long sequence. 16 (not portable, but within a GB300 GPC) against 8: 131,072 cells chosen in 22 against 26 us then.
-constexpr int MAX_CLUSTER = 16;
+constexpr int MAX_CLUSTER = 16;   // not portable, but within a GB300 GPC
 constexpr int BINS = 2048;
 constexpr int MAX_KEYS = 40960;   // keys a CTA holds; longer runs are read again in every pass
 
@@ -422,24 +421,40 @@ __global__ void __launch_bounds__(COPY_THREADS) copy_pieces_kernel(const CacheEv
 
 }  // namespace
 
-cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
-    const int capacity = a.table_cols * a.kv.page_size;
-    // One CTA searches what a few rounds of its threads cover.
-    const int cluster = capacity <= 4 * SEL_THREADS ? 1 : MAX_CLUSTER;
-    const int max_keys = std::min((capacity + cluster - 1) / cluster + 3, MAX_KEYS) & ~3;   // whole quads
+// CTAs of a sequence. One searches what a few rounds of its threads cover; the
+// longer the cache, the more, as long as all sequences' clusters run at once (the
+// GPU holds one of 16 CTAs per GPC, two of 8). Measured, whole call: 9 x 9,607
+// cells 20.5 us with 16, 12.8 with 8, 12.3 with 4, 13.4 with 2; 4 x 20,000 cells 14.3,
+// 13.3, 14.3 and 16.4; 1 x 30,000 cells 12.8, 12.7, 14.0 and 17.0; 2 x 60,000 cells
+// 16.4, 16.5, 20.0 and 26.8; 16 x 13,337 cells 30.3, 21.1, 15.4 and 16.3.
+static int cluster_size(int capacity, int nseq) {
+    int cluster = capacity <= 4 * SEL_THREADS ? 1 : capacity <= 16 * SEL_THREADS ? 4 : capacity <= 48 * SEL_THREADS ? 8 : MAX_CLUSTER;
+    while (cluster > 4 && static_cast<long long>(cluster) * nseq > device_sm_count() && 2LL * capacity <= static_cast<long long>(cluster) * MAX_KEYS)
+        cluster /= 2;
+    return cluster;
+}
+
+template <int kCluster>
+static cudaError_t launch_select(const CacheEvictArgs &a, int capacity, cudaLaunchConfig_t cfg) {
     static thread_local int configured_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (configured_device != dev) {
-        e = cudaFuncSetAttribute(select_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_KEYS * 4);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(select_kernel<MAX_CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_KEYS * 4);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(select_kernel<MAX_CLUSTER>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        configured_device = dev;
+    if (e == cudaSuccess && configured_device != dev) {
+        e = cudaFuncSetAttribute(select_kernel<kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_KEYS * 4);
+        if (e == cudaSuccess && kCluster > 8)
+            e = cudaFuncSetAttribute(select_kernel<kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) configured_device = dev;
     }
+    if (e != cudaSuccess) return e;
+    const int max_keys = std::min((capacity + kCluster - 1) / kCluster + 3, MAX_KEYS) & ~3;   // whole quads
+    cfg.gridDim = dim3(static_cast<unsigned>(a.nseq * kCluster));
+    cfg.blockDim = dim3(SEL_THREADS);
+    cfg.dynamicSmemBytes = 4 * max_keys;
+    return cudaLaunchKernelEx(&cfg, select_kernel<kCluster>, a, max_keys);
+}
+
+cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
+    const int capacity = a.table_cols * a.kv.page_size, cluster = cluster_size(capacity, a.nseq);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attrs[2];
     attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -451,11 +466,10 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attrs;
     cfg.numAttrs = 2;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.nseq * cluster));
-    cfg.blockDim = dim3(SEL_THREADS);
-    cfg.dynamicSmemBytes = 4 * max_keys;
-    e = cluster == 1 ? cudaLaunchKernelEx(&cfg, select_kernel<1>, a, max_keys)
-                     : cudaLaunchKernelEx(&cfg, select_kernel<MAX_CLUSTER>, a, max_keys);
+    const cudaError_t e = cluster == 1   ? launch_select<1>(a, capacity, cfg)
+                          : cluster == 4 ? launch_select<4>(a, capacity, cfg)
+                          : cluster == 8 ? launch_select<8>(a, capacity, cfg)
+                                         : launch_select<MAX_CLUSTER>(a, capacity, cfg);
     if (e != cudaSuccess) return e;
     // Cells of at least two pieces per lane go to whole warps (8 heads of int8, 64 pieces: 26
     // sequences of 527 cells 12.5 us against 14.4 by pieces; 2 x 131,072 cells 46 against 52);

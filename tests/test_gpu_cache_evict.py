@@ -88,6 +88,11 @@ def test_exactly_the_larger_masses_fit(dev, n, budget, high, low):
         run(dev, [n], budget, 4, 20, 1, 16, I8, mass=[mass])
 
 
+@pytest.mark.parametrize("lens", [[9000, 16000, 0, 4097, 15999], [20000, 33333, 6], [20000 - 700 * i for i in range(21)]])
+def test_several_middle_sized_caches(dev, lens):
+    run(dev, lens, 3000, 4, 100, 1, 16, I8)
+
+
 def test_more_cells_than_shared_memory_holds(dev):
     run(dev, [700001], 9001, 4, 100, 1, 64, I8)
 
