@@ -41,9 +41,9 @@
 // of 4, 207 us, 6.1 TB/s (0.90 of the measured copy rate); 48 sequences of which
 // 1,028 binary16 cells are visible, 46.5 us, 4.4 TB/s (the first 5 us bring the
 // first cells, the ranges end within 4 us of one another, the join takes 2); 4
-// sequences of up to 131,072 int8 cells, 2 KV heads, 53 us, 3.6 TB/s: about 850 instructions per warp and 32 cells, the conversions to
+// sequences of up to 131,072 int8 cells, 2 KV heads, 52 us, 3.7 TB/s: about 850 instructions per warp and 32 cells, the conversions to
 // binary16 360 of them, at 43 % of the issue slots with the 8 warps per SM that
-// 243 registers leave (12 warps of 168 registers: 69 us against 66 then). One
+// 245 registers leave (12 warps of 168 registers: 69 us against 66 then). One
 // sequence of 700 cells 7.9 us, launches and latencies: 0.7 us to find the range,
 // 1.5 for the page and the cells, 1 for the products and the merge, the join.
 #include <algorithm>
@@ -71,7 +71,8 @@ struct Params {
     int units;        // units per sequence
     int capacity, stride;   // cells of a table row; columns of a row of kept logits
     float *slots;     // [2 grid][heads of a unit][SLOT_ROW]
-    int4 *meta;       // [grid]: sequence, unit, first range, last range of the unit to join
+    int by_unit;      // no more units than ranges: a place in meta is a unit, else a range
+    int4 *meta;       // sequence, unit, first range, last range of the unit to join there, or -1
     float *lse2;      // [nseq][nheads], or null
     float *logits;    // [nseq][nheads][stride], or null
 };
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     if (lane == 31) sh_scan[warp] = before;
     if (tid == 0) {
         sh_seq = -1;
-        p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        if (!p.by_unit) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
     long long total = 0;
@@ -283,6 +284,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
             if (a.lse != nullptr) a.lse[static_cast<size_t>(s) * a.nheads + h] = -INFINITY;
             if (p.lse2 != nullptr) p.lse2[static_cast<size_t>(s) * a.nheads + h] = -INFINITY;
         }
+        if (p.by_unit)
+            for (int u = tid; u < p.units; u += THREADS) p.meta[s * p.units + u] = make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
     if (sh_seq < 0) return;
@@ -670,12 +673,17 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 }
             }
         }
-        // The unit is joined by the block of the second range that it falls into.
-        if (tid == 0 && !whole && begins) {
+        // A unit of several ranges is written down for the join by the second of them (by_unit: the
+        // place is the unit's own, and every unit has one writer).
+        if (tid == 0) {
+            int4 *at_unit = p.meta + (p.by_unit ? s * p.units + u : blockIdx.x);
             const long long unit0 = x0 - t0;
-            if (t0 > 0 && unit0 / per == blockIdx.x - 1)
-                p.meta[blockIdx.x] = make_int4(s, u, static_cast<int>(unit0 / per) * 2 + (unit0 % per == 0 ? 0 : 1),
-                                               static_cast<int>((unit0 + nt - 1) / per));
+            if (whole) {
+                if (p.by_unit) *at_unit = make_int4(-1, 0, 0, 0);
+            } else if (begins && t0 > 0 && unit0 / per == blockIdx.x - 1) {
+                *at_unit = make_int4(s, u, static_cast<int>(unit0 / per) * 2 + (unit0 % per == 0 ? 0 : 1),
+                                     static_cast<int>((unit0 + nt - 1) / per));
+            }
         }
         __syncthreads();   // the stages are free again
     }
@@ -683,10 +691,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
 
 // Adds the partial results of one unit's ranges for one head: of W warps, warp w
 // takes every W-th range from w on, then the warps are added in order. W is 1
-// where a unit has about as many ranges as a warp loads at once, else 4 (measured,
-// whole call: 2 ranges a unit 46.4 us with 1 warp, 48.0 with 4, 51.0 with 8; 39
-// ranges 58.3, 54.1 and 54.5; 12 ranges 8.5, 7.9 and 8.2).
-constexpr int JOIN_WARPS = 4, JOIN_BATCH = 4;
+// where a unit has about as many ranges as a warp loads at once, 4 up to 16
+// ranges, else 16 (measured, whole call: 2 ranges a unit 46.4 us with 1 warp, 48.0 with
+// 4; 12 ranges 8.5 and 7.9; 39 ranges 54.3 with 4, 52.3 with 16; about 250 ranges 38.9
+// and 33.7).
+constexpr int JOIN_WARPS = 16, JOIN_BATCH = 8;
 template <typename QT>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_constant__ Params p, int heads_per_unit) {
     grid_dependency_wait();
@@ -720,9 +729,17 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_cons
     };
     load(warp);
     float top = -INFINITY;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(slot(i) + 128));
+    for (int i = threadIdx.x; i < n; i += blockDim.x) top = fmaxf(top, __ldcg(slot(i) + 128));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+    if (warps > 1) {
+        if (lane == 0) weight[warp] = top;
+        __syncthreads();
+        top = lane < warps ? weight[lane] : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+        __syncthreads();   // the place takes the warps' sums next
+    }
     const float base = top == -INFINITY ? 0.0f : top;
     float l = 0.0f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -877,8 +894,9 @@ cudaError_t run(const Params &p, int grid, cudaStream_t stream) {
     }
     if (e == cudaSuccess) e = launch(kernel, dim3(grid), THREADS, smem, stream, p);
     const int ranges = static_cast<int>(grid / (static_cast<long long>(p.a.nseq) * p.units)) + 1;   // of a unit, on average
-    const int join_threads = ranges <= JOIN_BATCH ? 32 : 32 * JOIN_WARPS;
-    if (e == cudaSuccess) e = launch(join_kernel<QT>, dim3(grid, std::min(p.group, 8 * kMT)), join_threads, 0, stream, p, 8 * kMT);
+    const int join_threads = 32 * (ranges <= 4 ? 1 : ranges <= 16 ? 4 : JOIN_WARPS);
+    const int places = p.by_unit ? p.a.nseq * p.units : grid;
+    if (e == cudaSuccess) e = launch(join_kernel<QT>, dim3(places, std::min(p.group, 8 * kMT)), join_threads, 0, stream, p, 8 * kMT);
     if (e == cudaSuccess && p.logits != nullptr)
         e = launch(mass_kernel, dim3(std::min((p.stride + MASS_CELLS - 1) / MASS_CELLS, 512), p.a.nseq), MASS_CELLS, 0, stream, p);
     return e;
@@ -902,6 +920,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t stream) {
     p.parts = (p.group + heads - 1) / heads;
     p.units = a.kv.nkv * p.parts;
     p.stride = y.stride;
+    p.by_unit = static_cast<long long>(a.nseq) * p.units <= y.grid;
     char *b = static_cast<char *>(a.scratch);
     p.meta = reinterpret_cast<int4 *>(b + y.meta);
     p.slots = reinterpret_cast<float *>(b + y.slots);
