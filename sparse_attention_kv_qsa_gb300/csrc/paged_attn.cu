@@ -794,6 +794,11 @@ __global__ void __launch_bounds__(MASS_CELLS) mass_kernel(const __grid_constant_
     for (int i0 = blockIdx.x * MASS_CELLS; i0 < v.n; i0 += gridDim.x * MASS_CELLS) {
         const int i = i0 + 4 * quad;
         float4 got = make_float4(0.f, 0.f, 0.f, 0.f);
+        float old[4];   // on its way with the logits
+        if (group == 0)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k < v.n) old[k] = __ldcg(mass + v.cell(i + k));
         if (i < v.n) {
             const float *lp = p.logits + static_cast<size_t>(s) * a.nheads * p.stride + i;
 #pragma unroll 8
@@ -821,7 +826,7 @@ __global__ void __launch_bounds__(MASS_CELLS) mass_kernel(const __grid_constant_
             const float add[4] = {got.x, got.y, got.z, got.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (i + k < v.n) out[v.cell(i + k)] = __ldcg(mass + v.cell(i + k)) + add[k];
+                if (i + k < v.n) out[v.cell(i + k)] = old[k] + add[k];
         }
         __syncthreads();
     }
