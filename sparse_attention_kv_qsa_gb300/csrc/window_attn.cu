@@ -950,14 +950,14 @@ bool encode_map(CUtensorMap *map, bool bf16, const void *p, int64_t heads, int64
 bool map_stride(int64_t n, int64_t elements) { return n <= 1 || (elements > 0 && elements < (1LL << 38)); }
 
 // How the batch is cut, from what the host knows. Items are split over their
-// keys when there are fewer than two per SM, into about two parts per SM (three:
-// 16 items of 170 tiles 80 us against 63). Items that fill less than a quarter of
-// the SMs: into equal parts of 4 key tiles at least, which mostly run at once. More
-// items: into parts that fall in size, the longer the more items there are, as what
-// a split saves falls and the partial sums it moves grow with the items. Measured:
-// 200 items of 55 to 128 tiles 215 us, in equal parts 233; 250 items of 5 tiles
-// 27 us whole and 52 in two parts; 28 items of 12 tiles 21 us in equal parts of 4
-// tiles and 25 in falling ones of 6.
+// keys when there are fewer than two per SM. Items that fill less than a quarter
+// of the SMs: into equal parts of 4 key tiles at least, no more than run at once
+// however the lengths fall. More items: into about two parts per SM that fall in
+// size, the longer the more items there are, as what a split saves falls and the
+// partial sums it moves grow with the items. Measured: 8 items of 123 tiles 31.3 us in
+// parts for one per SM, 40.5 for two, 41.0 for three; 200 items of 55 to 128 tiles 215
+// us, in equal parts 233; 250 items of 5 tiles 27 us whole and 52 in two parts; 28
+// items of 12 tiles 21 us in equal parts of 4 tiles and 25 in falling ones of 6.
 struct Split {
     int pairs, splits, part_tiles;
     bool falling;
@@ -969,7 +969,8 @@ Split split(int nseq, int total_q, int nheads, int nkv) {
     // The partial results are laid out for empty sequences too: no more than 8 parts per SM in all.
     const long long room = std::max(1LL, 8LL * sms / (static_cast<long long>(pairs) * nkv));
     const bool falling = 4 * least >= sms;
-    const long long wanted = (2LL * sms + least - 1) / std::max(1LL, least);
+    const long long wanted = falling ? (2LL * sms + least - 1) / least
+                                     : std::max(1LL, sms / (static_cast<long long>(pairs) * nkv));
     const int part_tiles = falling ? 4 + static_cast<int>(std::min(28LL, 16 * least / sms)) : 4;
     return {pairs, static_cast<int>(least >= 2LL * sms ? 1LL : std::min(std::min(wanted, room), 64LL)), part_tiles, falling};
 }
