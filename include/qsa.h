@@ -387,8 +387,9 @@ typedef struct {
  *           [nseq][nheads] or NULL. mass, mass_out fp32 with row stride
  *           mass_stride >= table_cols * page_size.
  * scale     positive and finite.
- * scratch   at least qsa_paged_attn_scratch_bytes(...) bytes, 16-byte aligned
- *           (may be NULL when that is 0); no contents need survive.
+ * scratch   at least qsa_paged_attn_scratch_bytes(...) bytes, 16-byte aligned;
+ *           no contents need survive. Some is needed for a table of no columns
+ *           too (it is 0 for nseq = 0 and for arguments that are refused).
  * Sums and softmax statistics are fp32. q, out and the page pool are 16-byte
  * aligned, the others 4-byte.
  * nseq, nheads or nkv out of range, nheads % nkv != 0, a bad type, scale,

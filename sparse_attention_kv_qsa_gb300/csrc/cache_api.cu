@@ -47,7 +47,8 @@ qsa_status check_table(int cols, int64_t stride, int page_size) {
 extern "C" {
 
 size_t qsa_paged_attn_scratch_bytes(int nseq, int nheads, int nkv, int table_cols, int page_size, int with_mass) {
-    if (nseq < 1 || nheads < 1 || nkv < 1 || nheads % nkv != 0 || table_cols < 1 || page_size < 1 ||
+    // A table without columns is a call like any other: every sequence is empty, and the kernels say so in scratch.
+    if (nseq < 1 || nheads < 1 || nkv < 1 || nheads % nkv != 0 || table_cols < 0 || page_size < 1 ||
         nseq > MAX_SEQS || nheads > MAX_HEADS || static_cast<long long>(table_cols) * page_size > MAX_CELLS)
         return 0;
     return qsa::paged_attn_scratch_bytes(nseq, nheads, nkv, table_cols * page_size, with_mass != 0);
@@ -79,7 +80,7 @@ qsa_status qsa_paged_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride
     if (table_cols > 0 && !aligned(page_table, 4)) return QSA_ERR_INVALID;
     if (mass != nullptr && (!aligned(mass, 4) || !aligned(mass_out, 4))) return QSA_ERR_INVALID;
     const size_t need = qsa_paged_attn_scratch_bytes(nseq, nheads, kv->nkv, table_cols, kv->page_size, mass != nullptr);
-    if (need > 0 && (!aligned(scratch, 16) || scratch_bytes < need)) return QSA_ERR_INVALID;
+    if (need == 0 || !aligned(scratch, 16) || scratch_bytes < need) return QSA_ERR_INVALID;
     const qsa::PagedAttnArgs a{q,     q_dtype, q_seq_stride, q_head_stride, nseq, nheads, *kv,  page_table,
                                table_cols, table_stride, lens, window, sinks, scale, out, lse, mass, mass_out,
                                mass_stride, scratch};
