@@ -321,7 +321,9 @@ qsa_status qsa_get_device_error(uint32_t *code, cudaStream_t stream);
  *   bit 0: the tensor-core scorer's CTA 0 never loads its first key piece
  *          (qsa_block_scores, _q8, _gmax and _select_static with nq > 4);
  *   bit 1: the fused decode select's grid barrier waits for one arrival
- *          more than its grid has (qsa_block_select_small).
+ *          more than its grid has (qsa_block_select_small);
+ *   bit 3: the prompt attention's CTA 0 never copies its first key tile
+ *          (qsa_window_attn, where the strides suit a tensor map).
  * The outputs of such calls are invalid and qsa_get_device_error reports
  * them; the device stays usable. Call qsa_debug_inject(0, 2000000000) to
  * restore normal operation. Process-wide; not thread-safe against

@@ -348,7 +348,7 @@ qsa_status qsa_get_device_error(uint32_t *code, cudaStream_t stream) {
 }
 
 qsa_status qsa_debug_inject(uint32_t faults, uint64_t wait_limit_ns) {
-    if ((faults & ~3u) != 0u || wait_limit_ns == 0 || wait_limit_ns > 60000000000ull) return QSA_ERR_INVALID;
+    if ((faults & ~11u) != 0u || wait_limit_ns == 0 || wait_limit_ns > 60000000000ull) return QSA_ERR_INVALID;
     qsa::g_inject.store(faults, std::memory_order_relaxed);
     qsa::g_wait_limit_ns.store(wait_limit_ns, std::memory_order_relaxed);
     return QSA_OK;

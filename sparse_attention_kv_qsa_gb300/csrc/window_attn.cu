@@ -95,8 +95,8 @@ struct WindowParams {
     int falling;            // parts fall in size
     Divider per_split, per_part;   // by splits, by part_tiles
     float *slots;           // [pairs][nkv][splits][2 x 128 rows][SLOT_ROW]
-    struct Work *split_work;   // [pairs x nkv], by item number: for the join, when splits > 1
     uint64_t wait_ns;
+    int stall;              // diagnostics only: CTA 0 never copies its first key tile
 };
 
 // The keys one query row sees: [0, sinks) and [lo, end).
@@ -449,9 +449,6 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                 Item it = first_item;
                 found = asked == 0 ? first_found : find_item(p, n, it);
                 w = Work(p, it);
-                if (!found) w.parts = 0;
-                if (p.splits > 1 && it.part == 0 && lane == 0)   // tell the join
-                    p.split_work[n] = w;
                 found = found && it.part < w.parts;
                 if (!found) {
                     ask();
@@ -487,7 +484,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
                 const int slot = kv % STAGES, i0 = (j2 >> 1) * ROWS;
                 ok = wait_warp(&bars->kv_empty[slot], ((kv / STAGES) & 1) ^ 1);
                 if (!ok) break;
-                if (lane == 0) {
+                if (lane == 0 && !(p.stall != 0 && blockIdx.x == 0 && kv == 0)) {
                     uint64_t *bar = &bars->kv_full[slot];
                     const uint32_t dst = ring + slot * TILE_BYTES;
                     const bool values = j2 & 1;
@@ -863,17 +860,26 @@ __global__ void __launch_bounds__(WTHREADS, 1) window_kernel(const __grid_consta
 }
 
 // Adds the parts of an item that was split over its keys, in their order: a
-// warp takes JOIN_ROWS rows at once, whose loads are under way together.
+// warp takes JOIN_ROWS rows at once, whose loads are under way together. What the
+// item is it works out itself: a CTA of window_kernel that gave up on a wait may have
+// claimed items that it never reached, so nothing but numbers is taken from scratch.
 constexpr int JOIN_ROWS = 4, JOIN_BLOCKS = 2 * ROWS / (8 * JOIN_ROWS);
 template <typename T>
 __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WindowParams p) {
-    grid_dependency_wait();
-    grid_launch_dependents();
     const WindowAttnArgs &a = p.a;
     const int lane = threadIdx.x & 31;
     __shared__ Work w;
-    if (threadIdx.x < sizeof(Work) / 4)
-        reinterpret_cast<int *>(&w)[threadIdx.x] = ld_in(reinterpret_cast<const int *>(p.split_work + blockIdx.x) + threadIdx.x);
+    // Before the wait: window_kernel let this grid start only after it had waited for its own
+    // predecessors, so the sequences' starts are final (2 us of 216 for the chunks above).
+    if (threadIdx.x < 32) {
+        Item it;
+        const bool found = find_item(p, blockIdx.x, it);   // its first part
+        Work mine(p, it);
+        if (!found) mine.parts = 0;
+        if (lane == 0) w = mine;
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
     __syncthreads();
     if (w.parts < 2) return;
     constexpr size_t NEXT = static_cast<size_t>(2 * ROWS) * SLOT_ROW;
@@ -974,7 +980,6 @@ Split split(int nseq, int total_q, int nheads, int nkv) {
     const int part_tiles = falling ? 4 + static_cast<int>(std::min(28LL, 16 * least / sms)) : 4;
     return {pairs, static_cast<int>(least >= 2LL * sms ? 1LL : std::min(std::min(wanted, room), 64LL)), part_tiles, falling};
 }
-size_t work_bytes(int pairs, int nkv) { return (sizeof(Work) * static_cast<size_t>(pairs) * nkv + 15) / 16 * 16; }
 // Parts of at least part_tiles tiles that a long item has.
 int most_parts(const WindowAttnArgs &a, int tokens, int part_tiles) {
     // Lengths are not known here: twice the mean stands for the longest (a part may then be longer).
@@ -1020,6 +1025,7 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
     p.k_has_heads = k_heads;
     p.v_has_heads = v_heads;
     p.wait_ns = wait_limit_ns();
+    p.stall = (debug_inject() & 8u) != 0u;
     if (!encode_map(&p.q, bf16, a.q, a.nheads, a.total_q, a.q_head, a.q_tok, p.group, p.tokens) ||
         !encode_map(&p.k, bf16, a.k, k_heads ? a.nkv : 1, a.total_k, a.k_head, a.k_tok, 1, ROWS) ||
         !encode_map(&p.v, bf16, a.v, v_heads ? a.nkv : 1, a.total_k, a.v_head, a.v_tok, 1, ROWS))
@@ -1034,8 +1040,7 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
     p.splits = std::min(x.splits, most_parts(a, p.tokens, x.part_tiles));
     p.per_split = make_divider(p.splits);
     p.per_part = make_divider(p.part_tiles);
-    p.split_work = static_cast<Work *>(a.scratch);
-    p.slots = reinterpret_cast<float *>(static_cast<char *>(a.scratch) + work_bytes(p.pairs, a.nkv));
+    p.slots = static_cast<float *>(a.scratch);
     const long long items = static_cast<long long>(p.pairs) * a.nkv * p.splits;
     if (items > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     cfg.gridDim = dim3(static_cast<unsigned>(items));
@@ -1054,7 +1059,7 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
 size_t window_attn_scratch_bytes(int nseq, int total_q, int, int nheads, int nkv) {
     if (nheads / nkv > ROWS) return 0;
     const Split x = split(nseq, total_q, nheads, nkv);
-    return x.splits > 1 ? work_bytes(x.pairs, nkv) + sizeof(float) * x.pairs * nkv * x.splits * 2 * ROWS * SLOT_ROW : 0;
+    return x.splits > 1 ? sizeof(float) * x.pairs * nkv * x.splits * 2 * ROWS * SLOT_ROW : 0;
 }
 
 cudaError_t launch_window_attn(const WindowAttnArgs &a, cudaStream_t stream) {

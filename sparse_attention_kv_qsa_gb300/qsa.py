@@ -565,6 +565,7 @@ def device_error(device: torch.device | None = None) -> int:
 WAIT_LIMIT_DEFAULT_NS = 2_000_000_000
 INJECT_SCORER_STALL = 1    # the tensor-core scorer's CTA 0 never loads its first key piece
 INJECT_DECODE_BARRIER = 2  # the fused decode select's grid barrier waits for one arrival too many
+INJECT_WINDOW_STALL = 8    # the prompt attention's CTA 0 never copies its first key tile
 
 
 def debug_inject(faults: int, wait_limit_ns: int = WAIT_LIMIT_DEFAULT_NS) -> None:

@@ -23,3 +23,9 @@ def test_a_table_without_columns_is_refused_without_scratch(lib, kw):  # noqa: F
     need = qsa.paged_attn_scratch_bytes(2, 8, 2, 0, 16, "mass" in kw)
     for bad in (dict(scratch=None, bytes=0), dict(scratch=None), dict(bytes=need - 1), dict(scratch=A + 4)):
         assert paged(lib, cols=0, tstride=0, table=None, **bad, **kw) == INVALID
+
+
+def test_prompt_attention_has_a_fault_bit(lib):  # noqa: F811
+    assert lib.qsa_debug_inject(qsa.INJECT_WINDOW_STALL, 10 ** 6) == qsa.QSA_OK      # nothing is launched
+    assert lib.qsa_debug_inject(16, 10 ** 6) == INVALID
+    assert lib.qsa_debug_inject(0, qsa.WAIT_LIMIT_DEFAULT_NS) == qsa.QSA_OK
