@@ -35,3 +35,78 @@ def test_a_table_without_columns(dev, nseq, heads, nkv, kv, qt, mass):
     assert torch.count_nonzero(out) == 0 and bool((lse == -math.inf).all())
     if mass:
         assert bool((kw["mass"] == 2.0).all()) and bool((kw["mass_out"] == -5.0).all())
+
+
+def prompt(dev, n, nkv, group, dtype, seed=0):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    r = lambda h: torch.randn((n, h, 128), generator=g, device=dev, dtype=dtype)  # noqa: E731
+    return r(nkv * group), r(nkv), r(nkv), torch.tensor([0, n], dtype=torch.int32, device=dev)
+
+
+def test_rows_summed_again_take_longer_than_a_wait_may(dev):
+    """NaN in the values of the last token, which all rows of its key tile but its own read as hidden: thousands of
+    keys are summed again for each while the pipeline's waits, cut to 1 ms, stand. Nothing gives up, all rows come."""
+    n = 6000
+    q, k, v, cu = prompt(dev, n, 8, 4, BF16)
+    want, want_lse = qsa.window_attn(q, k, v, cu, cu, n)
+    v[n - 1] = math.nan
+    out, lse = torch.full_like(q, math.nan), torch.full(q.shape[:2], math.nan, device=dev)
+    torch.cuda.synchronize()
+    assert qsa.device_error(dev) == 0
+    qsa.debug_inject(0, 1_000_000)
+    try:
+        qsa.window_attn(q, k, v, cu, cu, n, out=out, lse=lse)
+        torch.cuda.synchronize()
+    finally:
+        qsa.debug_inject(0)
+    assert qsa.device_error(dev) == 0
+    assert torch.isnan(out[n - 1]).all() and torch.equal(lse, want_lse)
+    # both forms are within half a step of bfloat16 (2^-8 of the weights, 2^-8 of the result) of the formula
+    err = (out[:-1].float() - want[:-1].float()).abs().max()
+    assert float(err) <= 2 * (2.0 ** -8 + 2.0 ** -8) * float(v[:-1].abs().max())
+
+
+@pytest.mark.parametrize("n", [130, 600, 5000])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_visible_infinities_and_nan_reach_their_columns_alone(dev, n, dtype):
+    """Columns 0 to 3: an infinity, a negative one, both, NaN in values that the later rows see. The weights'
+    sum does not depend on them, nor does any other column of a row."""
+    q, k, v, cu = prompt(dev, n, 2, 4, dtype)
+    want, want_lse = qsa.window_attn(q, k, v, cu, cu, n)
+    at = 70
+    v[at, 0, 0] = math.inf
+    v[at, 0, 1] = -math.inf
+    v[at, 0, 2], v[at + 1, 0, 2] = math.inf, -math.inf
+    v[at, 0, 3] = math.nan
+    out, lse = qsa.window_attn(q, k, v, cu, cu, n)
+    assert torch.equal(lse, want_lse)
+    sees = out[at + 1:, :4]
+    assert bool((sees[..., 0] == math.inf).all()) and bool((sees[..., 1] == -math.inf).all())
+    assert torch.isnan(sees[..., 2:4]).all()
+    assert torch.equal(out[at:, :4, 4:], want[at:, :4, 4:]) and torch.equal(out[:, 4:], want[:, 4:])
+    tol = 2 * (2 * torch.finfo(dtype).eps) * float(v[:at].abs().max())   # two forms, each half a step for weights and result
+    assert float((out[:at].float() - want[:at].float()).abs().max()) <= tol
+
+
+def test_a_visible_nan_costs_little(dev):
+    """Every row sees a NaN in token 0's values: no row is summed again (each is found NaN at its first key)."""
+    n = 4096
+    q, k, v, cu = prompt(dev, n, 8, 4, BF16)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=dev)
+
+    def least():
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        times = []
+        for _ in range(5):
+            a.record()
+            qsa.window_attn(q, k, v, cu, cu, n, out=out, lse=lse)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    fine = least()
+    v[0] = math.nan
+    slow = least()
+    assert torch.isnan(out).all() and torch.isfinite(lse).all()
+    assert slow < 20 * fine, (slow, fine)    # a thousand times when every row's keys were gone through again
