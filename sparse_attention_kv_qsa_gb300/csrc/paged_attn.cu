@@ -538,8 +538,20 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 }
                 top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
-                const bool move = top > ref[m] + LAZY || (ref[m] == -INFINITY && top > -INFINITY);
+                bool move = top > ref[m] + LAZY || (ref[m] == -INFINITY && top > -INFINITY);
                 if (__any_sync(FULL_MASK, move)) {
+                    if constexpr (kInt8)
+                        // An infinite value scale must not become the reference, which the sum of weights needs finite:
+                        // it counts as binary16's largest number.
+                        if (__any_sync(FULL_MASK, top == INFINITY)) {
+                            top = -INFINITY;
+#pragma unroll
+                            for (int n = 0; n < 4 * GROUPS; ++n)
+                                top = fmaxf(top, xx[n] + __log2f(fminf(fmaxf(fabsf(vs[n]), 5.9604645e-8f), 65504.0f)));
+                            top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
+                            top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
+                            move = top > ref[m] + LAZY || (ref[m] == -INFINITY && top > -INFINITY);
+                        }
                     const float f = move ? ex2(ref[m] - top) : 1.0f;
                     if (move) ref[m] = top;
                     sum[m] *= f;

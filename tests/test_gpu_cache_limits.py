@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import sparse_attention_kv_qsa_gb300 as qsa
+from test_gpu_paged_attn import Cache, queries
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32, I8 = torch.bfloat16, torch.float16, torch.float32, torch.int8
@@ -110,3 +111,23 @@ def test_a_visible_nan_costs_little(dev):
     slow = least()
     assert torch.isnan(out).all() and torch.isfinite(lse).all()
     assert slow < 20 * fine, (slow, fine)    # a thousand times when every row's keys were gone through again
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("qt", [F32, BF16])
+@pytest.mark.parametrize("at", [0, 77, 299])
+def test_value_scales_do_not_reach_the_weights(dev, qt, at, bad):
+    """An infinite or NaN scale of an int8 cell's values spoils the results of its KV head, not lse and mass."""
+    c = Cache(dev, [300, 20000], 2, 16, I8)
+    q = queries(dev, 2, 8, qt)
+    mass = torch.zeros((2, c.cols * 16), device=dev)
+    want, _ = c.call(q, mass=torch.zeros_like(mass))
+    places = [(c.table[s, at // 16].long(), at % 16, 1) for s in (0, 1)]
+    kept = [c.vs[p].clone() for p in places]
+    for p in places:
+        c.vs[p] = bad
+    out, lse = c.call(q, mass=mass)
+    assert not torch.isfinite(out[:, 4:]).any() and torch.equal(out[:, :4], want[:, :4])
+    for p, x in zip(places, kept):
+        c.vs[p] = x
+    c.check(q, want, lse, mass=torch.zeros_like(mass), mass_out=mass)
