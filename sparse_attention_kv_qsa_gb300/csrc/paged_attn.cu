@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
                 int ex = 0;
                 if (top > 0.0f && top < INFINITY) frexpf(top, &ex);
-                ex = max(-100, min(100, ex));
+                ex = max(-126, min(127, ex));   // both powers are fp32 numbers
                 const float down = ldexpf(1.0f, -ex);
                 qc[m] = c * ldexpf(1.0f, ex);
 #pragma unroll

@@ -131,3 +131,13 @@ def test_value_scales_do_not_reach_the_weights(dev, qt, at, bad):
     for p, x in zip(places, kept):
         c.vs[p] = x
     c.check(q, want, lse, mass=torch.zeros_like(mass), mass_out=mass)
+
+
+@pytest.mark.parametrize("qmul,scale", [(1e36, 1e-37), (3e37, 3e-38), (1e-36, 1e35), (1e-37, 1e36)])
+def test_queries_of_the_whole_range_over_int8_cells(dev, qmul, scale):
+    """fp32 queries near both ends of their range whose logits are ordinary numbers."""
+    c = Cache(dev, [300, 5000], 2, 16, I8)
+    q = (queries(dev, 2, 8, F32).clamp(-4, 4) * qmul)
+    assert torch.isfinite(q).all()
+    out, lse = c.call(q, scale=scale)
+    c.check(q, out, lse, scale=scale)
