@@ -1,6 +1,6 @@
 """Generating with a key-value cache that is kept within a budget.
 
-    python examples/bounded_cache.py [--sequences 4] [--prompt 900] [--steps 200] [--budget 512]
+    python examples/bounded_cache.py [--sequences 4] [--prompt 900] [--steps 200] [--budget 512] [--observe 32]
 
 One attention layer with random projections stands for a model. The prompts'
 tokens attend with a sliding window and the first tokens always visible
@@ -9,6 +9,11 @@ attends its sequence's pages (``paged_attn``), which also adds the weight that
 every cell received to a running mass. When a cache has grown past its budget
 by a few pages, ``cache_evict`` keeps the first cells, the most recent ones and
 those of largest mass, in new pages, and the old pages are free again.
+
+``window_attn`` gives no masses. What the prompt's cells are worth is learnt from
+its last tokens (``--observe``), which attend the pages once more, each as a row of
+``paged_attn`` with a length of its own, and from the steps: a cache is cut only
+after a step has attended it.
 """
 
 from __future__ import annotations
@@ -60,6 +65,14 @@ class PagedCache:
         out, _ = qsa.paged_attn(q, self.k, self.v, self.table, self.lens, window=window, sinks=sinks, mass=self.mass)
         return out
 
+    def observe(self, s: int, q: torch.Tensor, window: int = -1, sinks: int = 0) -> None:
+        """Adds the weights that the last tokens ``q [n, heads, 128]`` of sequence ``s`` give its cells to its mass."""
+        n = q.shape[0]
+        lens = torch.arange(self.length[s] - n + 1, self.length[s] + 1, dtype=torch.int32, device=self.device)
+        mass = torch.zeros((n, self.mass.shape[1]), device=self.device)
+        qsa.paged_attn(q, self.k, self.v, self.table[s].repeat(n, 1), lens, window=window, sinks=sinks, mass=mass)
+        self.mass[s] += mass.sum(0)
+
     def evict(self, budget: int, sinks: int, recent: int) -> torch.Tensor:
         """Every sequence down to ``budget`` cells, in new pages; returns the kept cells' old places."""
         each = -(-budget // self.page)
@@ -79,9 +92,9 @@ class PagedCache:
 
 
 def generate(sequences: int = 4, prompt: int = 900, steps: int = 200, budget: int = 512, sinks: int = 4, recent: int = 64,
-             window: int = 256, heads: int = 8, nkv: int = 2, page: int = 16, seed: int = 0, report=None):
+             window: int = 256, heads: int = 8, nkv: int = 2, page: int = 16, seed: int = 0, report=None, observe: int = 0):
     """Runs prompts and steps; returns ``(outputs of the prompts, outputs of every step, cache)``. ``report`` is
-    called with a text now and then."""
+    called with a text now and then. ``observe``: how many of a prompt's last tokens tell what its cells are worth."""
     dev = torch.device("cuda")
     g = torch.Generator(device=dev).manual_seed(seed)
     width = heads * D
@@ -105,6 +118,8 @@ def generate(sequences: int = 4, prompt: int = 900, steps: int = 200, budget: in
     for s in range(sequences):
         a, b = sum(lengths[:s]), sum(lengths[:s + 1])
         cache.append(s, k[a:b], v[a:b])
+        if observe > 0:
+            cache.observe(s, q[max(a, b - observe):b])
     if report:
         report(f"prompts of {lengths} tokens, {len(cache.free)} of {pages} pages free")
 
@@ -113,26 +128,26 @@ def generate(sequences: int = 4, prompt: int = 900, steps: int = 200, budget: in
     x = prompts[ends].reshape(sequences, width)
     made = []
     for step in range(steps):
-        if max(cache.length) >= budget + slack:
-            before = list(cache.length)
-            cache.evict(budget, sinks, recent)
-            if report:
-                report(f"step {step}: {before} -> {cache.length} cells, {len(cache.free)} pages free")
         q, k, v = qkv(torch.nn.functional.normalize(x.float(), dim=1).to(torch.bfloat16) * width ** 0.5)
         for s in range(sequences):
             cache.append(s, k[s:s + 1], v[s:s + 1])
         out = cache.attend(q)
         made.append(out)
+        if max(cache.length) >= budget + slack:   # with this step's weights in the masses
+            before = list(cache.length)
+            cache.evict(budget, sinks, recent)
+            if report:
+                report(f"step {step}: {before} -> {cache.length} cells, {len(cache.free)} pages free")
         x = out.reshape(sequences, width)
     return prompts, made, cache
 
 
 def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    for name, default in (("sequences", 4), ("prompt", 900), ("steps", 200), ("budget", 512)):
+    for name, default in (("sequences", 4), ("prompt", 900), ("steps", 200), ("budget", 512), ("observe", 32)):
         ap.add_argument("--" + name, type=int, default=default)
     a = ap.parse_args()
-    _, made, cache = generate(a.sequences, a.prompt, a.steps, a.budget, report=print)
+    _, made, cache = generate(a.sequences, a.prompt, a.steps, a.budget, report=print, observe=a.observe)
     torch.cuda.synchronize()
     print(f"{len(made)} steps of {a.sequences} sequences; caches of {cache.length} cells")
 
