@@ -11,6 +11,7 @@ needs the torch that it was built against.
 from __future__ import annotations
 
 import concurrent.futures
+import hashlib
 import os
 import shutil
 import subprocess
@@ -24,6 +25,7 @@ LIB = os.path.join(BUILD, "libqsa.so")
 INCLUDE = os.path.join(ROOT, "include")
 BINDING = os.path.join(HERE, "binding", "qsa_ops.cpp")
 OPS = os.path.join(BUILD, "qsa_ops.so")
+OPS_KEY = OPS + ".key"   # what the module was linked against: binding_key()
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -65,11 +67,24 @@ def _torch_dir() -> str:
     return os.path.dirname(torch.__file__)
 
 
-def _compile_binding(force: bool) -> str:
-    """qsa_ops.o; rebuilt when its source, the header or the torch version changed."""
+def binding_key() -> str:
+    """The torch and the Python that a built module belongs to: it uses both their C++ and C interfaces."""
     import torch
-    tag = torch.__version__.replace("+", "_")
-    obj = os.path.join(BUILD, f"qsa_ops.{tag}.obj")
+    return f"torch {torch.__version__} {_torch_dir()}, {sysconfig.get_config_var('SOABI')}"
+
+
+def linked_for() -> str | None:
+    """The ``binding_key()`` that ``qsa_ops.so`` was linked for; None where there is no module, or it does not say."""
+    if not os.path.exists(OPS) or not os.path.exists(OPS_KEY):
+        return None
+    with open(OPS_KEY) as f:
+        return f.read()
+
+
+def _compile_binding(force: bool) -> str:
+    """The module's object; one for each binding_key(), rebuilt when its source or the header changed."""
+    import torch
+    obj = os.path.join(BUILD, f"qsa_ops.{hashlib.sha256(binding_key().encode()).hexdigest()[:16]}.obj")
     newest = max(os.path.getmtime(BINDING), os.path.getmtime(os.path.join(INCLUDE, "qsa.h")))
     if not force and os.path.exists(obj) and os.path.getmtime(obj) >= newest:
         return obj
@@ -85,6 +100,11 @@ def _compile_binding(force: bool) -> str:
     return obj
 
 
+def _binding_is_current(obj: str) -> bool:
+    # By the key and not by times alone: another torch's object may be the older one and yet not the one linked.
+    return linked_for() == binding_key() and os.path.getmtime(OPS) >= max(os.path.getmtime(obj), os.path.getmtime(LIB))
+
+
 def _link_binding(obj: str) -> None:
     lib = os.path.join(_torch_dir(), "lib")
     cmd = [shutil.which("g++") or "g++", "-shared", "-o", OPS + ".tmp", obj, "-L", BUILD, "-l:libqsa.so", "-L", lib,
@@ -92,7 +112,12 @@ def _link_binding(obj: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of {OPS} failed:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(OPS_KEY):
+        os.remove(OPS_KEY)   # a module without a key is linked again
     os.replace(OPS + ".tmp", OPS)
+    with open(OPS_KEY + ".tmp", "w") as f:
+        f.write(binding_key())
+    os.replace(OPS_KEY + ".tmp", OPS_KEY)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -114,7 +139,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(LIB + ".tmp", LIB)
-    if force or not os.path.exists(OPS) or os.path.getmtime(OPS) < max(os.path.getmtime(ops), os.path.getmtime(LIB)):
+    if force or not _binding_is_current(ops):
         _link_binding(ops)
     return LIB
 

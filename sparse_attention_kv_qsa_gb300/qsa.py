@@ -471,6 +471,9 @@ def _ops():
         lib()
         if not os.path.exists(_build.OPS):
             raise RuntimeError(f"{_build.OPS} is missing: build it with __graft_entry__.build()")
+        if _build.linked_for() != _build.binding_key():
+            raise RuntimeError(f"{_build.OPS} was built for {_build.linked_for() or 'another torch'}, this is "
+                               f"{_build.binding_key()}: build it with __graft_entry__.build()")
         spec = importlib.util.spec_from_file_location("qsa_ops", _build.OPS)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
