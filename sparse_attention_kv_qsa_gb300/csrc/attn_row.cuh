@@ -1,5 +1,6 @@
-// One query row attended by one warp in fp32: the plain CUDA-core form of the
-// bounded-cache attention kernels. Lane l holds elements 4l .. 4l+3.
+// Rows of 128 elements by one warp in fp32, lane l with elements 4l .. 4l+3: the
+// loads and stores of the bounded-cache attention kernels, and the running softmax of
+// the rows that prompt attention computes on CUDA cores.
 #pragma once
 
 #include <cmath>
@@ -36,11 +37,6 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
     const uint2 w = __ldcg(reinterpret_cast<const uint2 *>(p));
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
                        __uint_as_float(w.y & 0xFFFF0000u));
-}
-template <>
-__device__ __forceinline__ float4 load4<int8_t>(const int8_t *p) {
-    const char4 c = __ldcg(reinterpret_cast<const char4 *>(p));
-    return make_float4(c.x, c.y, c.z, c.w);
 }
 
 template <typename T>

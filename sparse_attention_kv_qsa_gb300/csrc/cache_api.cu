@@ -89,7 +89,7 @@ qsa_status qsa_paged_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride
 
 size_t qsa_window_attn_scratch_bytes(int nseq, int total_q, int max_q, int nheads, int nkv) {
     if (nseq < 1 || total_q < 1 || max_q < 1 || nheads < 1 || nkv < 1 || nheads % nkv != 0) return 0;
-    return qsa::window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv);
+    return qsa::window_attn_scratch_bytes(nseq, total_q, nheads, nkv);   // the longest sequence does not matter
 }
 
 qsa_status qsa_window_attn(const void *q, const void *k, const void *v, qsa_dtype dtype, const int64_t *strides,

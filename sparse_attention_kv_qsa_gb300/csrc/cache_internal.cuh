@@ -60,7 +60,7 @@ struct WindowAttnArgs {
     void *scratch;
 };
 
-size_t window_attn_scratch_bytes(int nseq, int total_q, int max_q, int nheads, int nkv);
+size_t window_attn_scratch_bytes(int nseq, int total_q, int nheads, int nkv);
 cudaError_t launch_window_attn(const WindowAttnArgs &a, cudaStream_t stream);
 
 struct CacheEvictArgs {

@@ -1166,7 +1166,7 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t window_attn_scratch_bytes(int nseq, int total_q, int, int nheads, int nkv) {
+size_t window_attn_scratch_bytes(int nseq, int total_q, int nheads, int nkv) {
     if (nheads / nkv > ROWS) return 0;
     const Split x = split(nseq, total_q, nheads, nkv);
     return odd_bytes(x.pairs, nkv, x.splits) + (x.splits > 1 ? sizeof(float) * x.pairs * nkv * x.splits * 2 * ROWS * SLOT_ROW : 0);
