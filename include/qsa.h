@@ -427,11 +427,12 @@ qsa_status qsa_paged_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride
  * scratch   at least qsa_window_attn_scratch_bytes(...) bytes, 16-byte aligned
  *           (0 without sequences or queries); no contents need survive.
  * Softmax statistics and sums are fp32; the weights are rounded once to dtype
- * for the product with the values. The values of keys that are not visible
- * never reach a result, whatever they hold; but where an infinity or NaN lies
- * among the values of a row's key tiles (128 keys, also past a sequence's
- * end), that row is gone through again by one warp, which is slow (about 0.25
- * us per key and row): keep memory that is not a token's finite.
+ * for the product with the values. An infinity in a visible value makes its
+ * column that infinity, NaN (or infinities of both signs) NaN. The values of
+ * keys that are not visible never reach a result, whatever they hold; but where
+ * an infinity or NaN lies among the values of a row's key tiles (128 keys, also
+ * past a sequence's end), that row is gone through again by one warp, which is
+ * slow (about 0.25 us per key and row): keep memory that is not a token's finite.
  * Errors as qsa_paged_attn; nheads / nkv above 128, nseq above 65,535 or
  * total_q * nheads above 2^31 - 1 returns QSA_ERR_UNSUPPORTED.
  */

@@ -120,9 +120,9 @@ __device__ __forceinline__ RowKeys row_keys(const WindowAttnArgs &a, int nk, int
     return r;
 }
 
-// One row by one warp in fp32.
+// One row by one warp in fp32. True: the weights' sum is finite, a result is not.
 template <typename T>
-__device__ void attend_row(const WindowAttnArgs &a, int q_row, int h, int k0, int nk, int pos) {
+__device__ bool attend_row(const WindowAttnArgs &a, int q_row, int h, int k0, int nk, int pos) {
     const int lane = threadIdx.x & 31, kvh = h / (a.nheads / a.nkv);
     const float4 q = load4(static_cast<const T *>(a.q) + q_row * a.q_tok + h * a.q_head + 4 * lane);
     const T *kp = static_cast<const T *>(a.k) + k0 * a.k_tok + kvh * a.k_head + 4 * lane;
@@ -136,8 +136,11 @@ __device__ void attend_row(const WindowAttnArgs &a, int q_row, int h, int k0, in
             r.add(c * warp_sum(dot4(q, load4(kp + j * a.k_tok))), load4(vp + j * a.v_tok));
     }
     const size_t row = static_cast<size_t>(q_row) * a.nheads + h;
-    store4(static_cast<T *>(a.out) + row * 128 + 4 * lane, r.result());
+    const float4 y = r.result();
+    store4(static_cast<T *>(a.out) + row * 128 + 4 * lane, y);
     if (a.lse != nullptr && lane == 0) a.lse[row] = (r.m + log2f(r.l)) * LN2;
+    const float odd = (y.x * 0.0f + y.y * 0.0f) + (y.z * 0.0f + y.w * 0.0f);
+    return r.l - r.l == 0.0f && __any_sync(FULL_MASK, !(odd == 0.0f));
 }
 
 // A row in `out` whose weights have a finite sum but whose results are not all
@@ -226,7 +229,10 @@ __global__ void __launch_bounds__(256) window_rows_kernel(const WindowAttnArgs a
     grid_dependency_wait();
     const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
     const Sequence x = sequence(a, blockIdx.z);
-    if (i < x.nq) attend_row<T>(a, x.q0 + i, blockIdx.y, x.k0, x.nk, x.nk - x.nq + i);
+    if (i >= x.nq) return;
+    const int pos = x.nk - x.nq + i;
+    // An infinity whose weight has since underflowed has become NaN.
+    if (attend_row<T>(a, x.q0 + i, blockIdx.y, x.k0, x.nk, pos)) mend_row<T, 8, 4>(a, x.q0 + i, blockIdx.y, x.k0, x.nk, pos);
 }
 
 // An item's keys, numbered without gaps: numbers below `front` are keys

@@ -141,3 +141,24 @@ def test_queries_of_the_whole_range_over_int8_cells(dev, qmul, scale):
     assert torch.isfinite(q).all()
     out, lse = c.call(q, scale=scale)
     c.check(q, out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("expanded", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_infinities_whose_weights_vanish(dev, dtype, expanded):
+    """Each key outweighs the one before it, so that an infinity among the first values has a weight below fp32's
+    range in later rows: by the formula it is positive still. Both by tensor copies and row by row (a token stride of 0)."""
+    n = 300
+    _, _, v, cu = prompt(dev, n, 1, 4, dtype)
+    q = torch.zeros((1, 4, 128), device=dev, dtype=dtype)
+    q[..., 0] = 1.0
+    q = q.expand(n, 4, 128) if expanded else q.repeat(n, 1, 1)
+    k = torch.zeros((n, 1, 128), device=dev, dtype=dtype)
+    k[:, 0, 0] = 4.0 * torch.arange(n, device=dev)
+    k[40:, 0, 0] += 400.0                                   # there all weights so far vanish at once
+    v[2, 0, 5], v[3, 0, 6], v[4, 0, 7] = math.inf, -math.inf, math.nan
+    out, lse = qsa.window_attn(q, k, v, cu, cu, n, scale=1.0)
+    assert bool((out[2:, :, 5] == math.inf).all()) and bool((out[3:, :, 6] == -math.inf).all())
+    assert torch.isnan(out[4:, :, 7]).all() and torch.isfinite(lse).all()
+    rest = [c for c in range(128) if c not in (5, 6, 7)]
+    assert torch.isfinite(out[..., rest]).all() and torch.isfinite(out[:2]).all()
