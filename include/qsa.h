@@ -374,7 +374,8 @@ typedef struct {
  *   lse[s][h]   = log sum_j exp(logit[h][j])
  *   out[s][h]   = sum_j exp(logit[h][j] - lse[s][h]) * value[j]
  * With no visible cell out = 0 and lse = -infinity. Cells that are not
- * visible are never used, whatever they hold. lens is clamped to
+ * visible are never used, whatever they hold; an infinity or NaN in a visible
+ * value (or its scale) makes the results that use it infinite or NaN. lens is clamped to
  * [0, table_cols * page_size]; a visible cell whose page id is outside
  * [0, npages) is skipped (as if it were not visible).
  * mass, mass_out (both or neither NULL; may be equal):

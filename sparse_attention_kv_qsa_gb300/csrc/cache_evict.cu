@@ -22,7 +22,7 @@
 // 16,384, 41 us: 16 to choose, 24 to copy 136 MB (0.83 of the measured copy rate);
 // one sequence of 576 cells cut to 512, 7.1 us, launches and latencies. Masses
 // crowd into a few digits of the first pass, yet plain shared-memory atomics beat
-// one atomic per different digit of a warp (choosing 40 us against 48 then).
+// one atomic per different digit of a warp (by a sixth of the choice when both were tried).
 #include <algorithm>
 
 #include "cache_internal.cuh"
@@ -423,10 +423,12 @@ __global__ void __launch_bounds__(COPY_THREADS) copy_pieces_kernel(const CacheEv
 
 // CTAs of a sequence. One searches what a few rounds of its threads cover; the
 // longer the cache, the more, as long as all sequences' clusters run at once (the
-// GPU holds one of 16 CTAs per GPC, two of 8). Measured, whole call: 9 x 9,607
-// cells 20.5 us with 16, 12.8 with 8, 12.3 with 4, 13.4 with 2; 4 x 20,000 cells 14.3,
-// 13.3, 14.3 and 16.4; 1 x 30,000 cells 12.8, 12.7, 14.0 and 17.0; 2 x 60,000 cells
-// 16.4, 16.5, 20.0 and 26.8; 16 x 13,337 cells 30.3, 21.1, 15.4 and 16.3.
+// GPU holds one of 16 CTAs per GPC, two of 8). Measured, whole call with 16, 8, 4 and 1
+// CTAs, a quarter of the cells kept: 9 x 9,607 cells 35.9, 28.2, 28.1 and 29.6 us; 4 x
+// 20,000 cells 28.4, 27.7, 29.0 and 33.7; 1 x 30,000 cells 18.5, 18.2, 19.9 and 29.0; 2 x
+// 60,000 cells 28.6, 29.4, 33.2 and 64.3; 16 x 13,337 cells of one head 34.8, 25.4, 20.1
+// and 22.6; 1 x 2,000 cells 10.2, 9.3, 9.0 and 7.2. The length is the table's width, as the
+// sequences' own are on the device alone.
 static int cluster_size(int capacity, int nseq) {
     int cluster = capacity <= 4 * SEL_THREADS ? 1 : capacity <= 16 * SEL_THREADS ? 4 : capacity <= 48 * SEL_THREADS ? 8 : MAX_CLUSTER;
     while (cluster > 4 && static_cast<long long>(cluster) * nseq > device_sm_count() && 2LL * capacity <= static_cast<long long>(cluster) * MAX_KEYS)
@@ -472,8 +474,9 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
                                          : launch_select<MAX_CLUSTER>(a, capacity, cfg);
     if (e != cudaSuccess) return e;
     // Cells of at least two pieces per lane go to whole warps (8 heads of int8, 64 pieces: 26
-    // sequences of 527 cells 12.5 us against 14.4 by pieces; 2 x 131,072 cells 46 against 52);
-    // smaller ones by pieces (1 head of int8, 8 pieces: 16 x 13,337 cells 36 us against 72).
+    // sequences of 527 cells 14.1 us against 14.9 by pieces; 2 x 131,072 cells 40.3 against 47.4);
+    // smaller ones by pieces (4 heads, 32 pieces: 8 x 20,000 cells 40.3 us against 42.8; 1 head, 8
+    // pieces: 16 x 13,337 cells 22.9 against 47.9).
     const int per_cell = a.kv.nkv * (a.kv.dtype == QSA_I8 ? 8 : 16);
     const bool cells = per_cell >= 64;
     const long long wanted = cells ? (a.budget + COPY_THREADS / 32 - 1) / (COPY_THREADS / 32)

@@ -38,14 +38,15 @@
 // scaled by whatever M they started from, and rescaling is rare.
 //
 // Measured (GB300): 64 ragged sequences of up to 8,192 bfloat16 cells, 8 KV heads
-// of 4, 207 us, 6.1 TB/s (0.90 of the measured copy rate); 48 sequences of which
-// 1,028 binary16 cells are visible, 46.5 us, 4.4 TB/s (the first 5 us bring the
+// of 4, 208 us, 6.1 TB/s (0.90 of the measured copy rate); 48 sequences of which
+// 1,028 binary16 cells are visible, 46 us, 4.4 TB/s (the first 5 us bring the
 // first cells, the ranges end within 4 us of one another, the join takes 2); 4
-// sequences of up to 131,072 int8 cells, 2 KV heads, 52 us, 3.7 TB/s: about 850 instructions per warp and 32 cells, the conversions to
-// binary16 360 of them, at 43 % of the issue slots with the 8 warps per SM that
-// 245 registers leave (12 warps of 168 registers: 69 us against 66 then). One
-// sequence of 700 cells 7.9 us, launches and latencies: 0.7 us to find the range,
-// 1.5 for the page and the cells, 1 for the products and the merge, the join.
+// sequences of up to 131,072 int8 cells, 2 KV heads, 52 us, 3.7 TB/s: about 850
+// instructions per warp and 32 cells, the conversions to binary16 360 of them, at 43
+// % of the issue slots with the 8 warps per SM that 245 registers leave (an earlier
+// form with 12 warps of 168 registers was 4 % slower than its own with 8). One
+// sequence of 700 cells 7.3 us on the device, launches and latencies: 0.7 us to find the
+// range, 1.5 for the page and the cells, 1 for the products and the merge, the join.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -704,9 +705,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
 // Adds the partial results of one unit's ranges for one head: of W warps, warp w
 // takes every W-th range from w on, then the warps are added in order. W is 1
 // where a unit has about as many ranges as a warp loads at once, 4 up to 16
-// ranges, else 16 (measured, whole call: 2 ranges a unit 46.4 us with 1 warp, 48.0 with
-// 4; 12 ranges 8.5 and 7.9; 39 ranges 54.3 with 4, 52.3 with 16; about 250 ranges 38.9
-// and 33.7).
+// ranges, else 16 (measured, whole call: 2 ranges a unit 45.9 us with 1 warp, 49.8 with
+// 4; 11 ranges 7.6 and 7.25; 39 ranges 54.1 with 4, 51.4 with 16; about 300 ranges 15.9
+// and 14.0). The ranges are taken from the grid, which goes by the table's width: lengths
+// are on the device alone. Short caches on a wide table have fewer ranges than it says.
 constexpr int JOIN_WARPS = 16, JOIN_BATCH = 8;
 template <typename QT>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const __grid_constant__ Params p, int heads_per_unit) {
@@ -852,10 +854,13 @@ struct Layout {
     int heads_per_unit, grid, stride;
 };
 // A unit of 16 heads reads its cells once where two of 8 read them twice, but its
-// steps are slower (registers: no queries ahead, and the 16 outputs' merges). It pays for
-// 16-bit cells that do not stay in L2 for the second reading: 16 heads on a KV head, bfloat16, 8 x
-// 16,384 cells of 8 KV heads 93 us against 115, 16 x 8,192 cells of one 24.7 against 20.3. int8
-// units of 16 lose throughout (2 x 100,000 cells 51 us against 40).
+// steps are slower (255 registers, 116 bytes of them spilled to local memory; no queries ahead,
+// and the 16 outputs' merges). It pays for 16-bit cells that do not stay in L2 for the second
+// reading: 16 heads on a KV head, bfloat16, 8 x 16,384 cells of 8 KV heads 122 us against 174,
+// 64 x 8,192 cells of one 73 against 94, but 16 x 8,192 cells of one 32.8 against 28.5. The rule has only
+// the table's width to go by: where the sequences fill less of it, it can choose 16 for
+// cells that would stay (87 of 100 to 800 cells, 4 KV heads of 12: 45 us against 40). There is no
+// unit of 16 for int8 cells, whose 8 heads' registers leave no room (one that was tried lost a quarter).
 constexpr long long L2_BYTES = 128LL << 20;
 int heads_per_unit(int nseq, int group, int nkv, int capacity, bool int8) {
     return group > 8 && !int8 && 512LL * nseq * capacity * nkv > L2_BYTES ? 16 : 8;

@@ -17,7 +17,7 @@
 //   1 MMA warp        all tcgen05.mma; the warp runs as one with one lane
 //                     elected per instruction: with the whole loop inside one
 //                     lane's branch the operands of every MMA had to be moved to
-//                     uniform registers first (prompt_full 426 -> 350 us)
+//                     uniform registers first (a fifth slower when it was changed)
 //   1 copy warp       items, and the tensor copies of queries, keys and values
 //   4 output warps    O out of TMEM, normalised, staged and stored in 128-byte rows
 //
@@ -29,15 +29,15 @@
 //               d-contiguous operand form), into TMEM
 //
 // The two query tiles alternate: while one tile's softmax runs, the tensor
-// cores run the other's P V and the next S. (An MMA warp per tile was slower,
-// 475 us against 410: the two then fall into step.) The running maximum m is a
+// cores run the other's P V and the next S. (An MMA warp per tile was a sixth
+// slower when it was tried: the two then fall into step.) The running maximum m is a
 // lazy reference: O is rescaled only when a row's maximum grew by more than
 // 2^8 (weights then reach 2^8, whose relative rounding is the same), and the
 // first weights of a tile are taken before its maximum is known.
 //
 // CTAs that have finished an item take the next from those of the grid that
-// have not started (cluster launch control, asked with the copies of the last tile:
-// the chunks below 214 us, and 231 asked with those of the second): longest rows
+// have not started (cluster launch control, asked with the copies of the last tile: the
+// chunks below were 8 % slower when it was asked with those of the second): longest rows
 // first, balanced whatever the lengths, and the next item's copies and first
 // products run while the last one's results leave. With few items per SM each item's keys
 // are split into parts whose partial sums window_join_kernel adds.
@@ -54,12 +54,14 @@
 // the pipeline's waits have a limit. Strides that a tensor map cannot express go
 // row by row altogether (attend_row).
 //
-// Measured (GB300, 32 heads on 8 KV heads): 8,192 tokens causal 337 us, 1.63
-// PFLOP/s of the visible pairs, 0.85 of the measured cuBLAS burst; 8,192 tokens
-// in a window of 1,024 111 us, 0.61 (masked edges, and about 2.5 us per item
-// that its 9 key tiles do not hide); 8 ragged prompts of up to 2,048 tokens in a
-// window of 512 78 us; chunks of up to 512 tokens over 7,000 to 16,000 keys 214
-// us, of which the join takes 18.
+// Measured (GB300, 32 heads on 8 KV heads): 8,192 tokens causal 333 us in a short
+// CUDA graph, 1.65 PFLOP/s of the visible pairs, 0.86 of the measured cuBLAS burst, and
+// 375 us in a long loop of calls under the power limit, 0.77; in a window of 1,024 110
+// us, 0.62 (masked edges, and about 2.5 us per item that its 9 key tiles do not hide);
+// 8 ragged prompts of up to 2,048 tokens in a window of 512 76 us; chunks of up to 512
+// tokens over 7,000 to 16,000 keys 215 us, of which the join takes 18. Code that the
+// warps' loops do not need costs all of them: values past a sequence's end made zeros in
+// shared memory, by the MMA, the copy or a spare warp, took 2 to 4 % of every prompt.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -1070,10 +1072,10 @@ bool map_stride(int64_t n, int64_t elements) { return n <= 1 || (elements > 0 &&
 // of the SMs: into equal parts of 4 key tiles at least, no more than run at once
 // however the lengths fall. More items: into about two parts per SM that fall in
 // size, the longer the more items there are, as what a split saves falls and the
-// partial sums it moves grow with the items. Measured: 8 items of 123 tiles 31.3 us in
-// parts for one per SM, 40.5 for two, 41.0 for three; 200 items of 55 to 128 tiles 215
-// us, in equal parts 233; 250 items of 5 tiles 27 us whole and 52 in two parts; 28
-// items of 12 tiles 21 us in equal parts of 4 tiles and 25 in falling ones of 6.
+// partial sums it moves grow with the items. Measured: 8 items of 123 tiles 32.0 us in
+// parts for one per SM, 41.7 for two or three; 200 items of 55 to 128 tiles 216 us, in
+// equal parts 234, whole 226; 250 items of 5 tiles 26 us whole and 50 in two parts; 28
+// items of 12 tiles 20 us in equal parts of 4 tiles and 23 in falling ones of 6.
 struct Split {
     int pairs, splits, part_tiles;
     bool falling;
@@ -1160,9 +1162,9 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
     cfg.dynamicSmemBytes = WINDOW_SMEM;
     e = cudaLaunchKernelEx(&cfg, window_kernel<T>, p);
     if (e != cudaSuccess || p.splits == 1) return e;
-    // Many parts are a long chain for a row, so a warp takes fewer rows and more parts of each at once: 38
-    // parts of one item per KV head 22.9 us against 35.1, 19 parts 32.8 against 40.4; few parts move more
-    // rows: 2 to 8 parts of 200 to 250 items 214 us against 218 and 68.5 against 71.9.
+    // Many parts are a long chain for a row, so a warp takes fewer rows and more parts of each at once
+    // (38 parts an item 23.2 us against 34.8, 19 parts 32.6 against 40.3); few parts are many rows
+    // (2 to 8 parts of 200 to 250 items 216 us against 220, 68.6 against 71.4; 3 parts 25.6 against 26.4).
     const bool many = p.splits > 8;
     cfg.gridDim = dim3(static_cast<unsigned>(p.pairs * a.nkv), many ? join_blocks(2) : join_blocks(4));
     cfg.blockDim = dim3(32 * JOIN_WARPS);
