@@ -316,8 +316,9 @@ qsa_status qsa_get_device_error(uint32_t *code, cudaStream_t stream);
 /*
  * Diagnostics for the bounded waits (not for production use; the pages have
  * no counterpart). For the kernels launched after the call: every spin-wait
- * gives up after wait_limit_ns (default 2,000,000,000), and `faults` plants
- * a wait that cannot complete so that the time-out path runs:
+ * gives up after wait_limit_ns (default 2,000,000,000; in the prompt attention
+ * 8 us more for every 128 keys of the call, as items take that long), and
+ * `faults` plants a wait that cannot complete so that the time-out path runs:
  *   bit 0: the tensor-core scorer's CTA 0 never loads its first key piece
  *          (qsa_block_scores, _q8, _gmax and _select_static with nq > 4);
  *   bit 1: the fused decode select's grid barrier waits for one arrival

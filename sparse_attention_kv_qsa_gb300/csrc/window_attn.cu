@@ -1137,7 +1137,8 @@ cudaError_t launch(const WindowAttnArgs &a, cudaStream_t stream) {
     p.tokens = ROWS / p.group;
     p.k_has_heads = k_heads;
     p.v_has_heads = v_heads;
-    p.wait_ns = wait_limit_ns();
+    // The output warps wait for a whole item, 2 to 3.5 us a key tile: the limit is beside the work.
+    p.wait_ns = wait_limit_ns() + 8192ull * ((a.total_k + static_cast<uint64_t>(ROWS) - 1) / ROWS);
     p.stall = (debug_inject() & 8u) != 0u;
     if (!encode_map(&p.q, bf16, a.q, a.nheads, a.total_q, a.q_head, a.q_tok, p.group, p.tokens) ||
         !encode_map(&p.k, bf16, a.k, k_heads ? a.nkv : 1, a.total_k, a.k_head, a.k_tok, 1, ROWS) ||

@@ -162,3 +162,24 @@ def test_infinities_whose_weights_vanish(dev, dtype, expanded):
     assert torch.isnan(out[4:, :, 7]).all() and torch.isfinite(lse).all()
     rest = [c for c in range(128) if c not in (5, 6, 7)]
     assert torch.isfinite(out[..., rest]).all() and torch.isfinite(out[:2]).all()
+
+
+def test_items_that_take_longer_than_a_wait_may(dev):
+    """Whole items of 800 to 860 key tiles, some milliseconds each, under a limit of 1 ms for every wait."""
+    nq, nk = 10000, 110000
+    g = torch.Generator(device=dev).manual_seed(4)
+    q = torch.randn((nq, 8, 128), generator=g, device=dev, dtype=BF16)
+    k, v = (torch.randn((nk, 8, 128), generator=g, device=dev, dtype=BF16) for _ in range(2))
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32, device=dev) for n in (nq, nk))
+    want, want_lse = qsa.window_attn(q, k, v, cu_q, cu_k, nq)
+    out, lse = torch.full_like(q, math.nan), torch.full_like(want_lse, math.nan)
+    torch.cuda.synchronize()
+    assert qsa.device_error(dev) == 0
+    qsa.debug_inject(0, 1_000_000)
+    try:
+        qsa.window_attn(q, k, v, cu_q, cu_k, nq, out=out, lse=lse)
+        torch.cuda.synchronize()
+    finally:
+        qsa.debug_inject(0)
+    assert qsa.device_error(dev) == 0
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
