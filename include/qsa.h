@@ -390,7 +390,7 @@ typedef struct {
  * out       [nseq][nheads][128] of q_dtype, contiguous, not over an input. lse fp32
  *           [nseq][nheads] or NULL. mass, mass_out fp32 with row stride
  *           mass_stride >= table_cols * page_size.
- * scale     positive and finite.
+ * scale     positive, and finite in fp32 times log2(e) (up to 2.3e38).
  * scratch   at least qsa_paged_attn_scratch_bytes(...) bytes, 16-byte aligned;
  *           no contents need survive. Some is needed for a table of no columns
  *           too (it is 0 for nseq = 0 and for arguments that are refused).

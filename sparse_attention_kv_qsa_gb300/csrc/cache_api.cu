@@ -16,7 +16,8 @@ int element_size(int dtype) { return dtype == QSA_F32 ? 4 : dtype == QSA_I8 ? 1 
 // A stride that 16-byte accesses can use.
 bool good_stride(int64_t elements, int dtype) { return elements >= 0 && elements * element_size(dtype) % 16 == 0; }
 
-bool good_scale(float scale) { return std::isfinite(scale) && scale > 0.0f; }
+// The kernels work in base 2, with scale log2(e) in fp32.
+bool good_scale(float scale) { return scale > 0.0f && std::isfinite(scale * qsa::LOG2E); }
 
 qsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA; }
 

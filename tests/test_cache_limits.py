@@ -4,7 +4,7 @@ checks finds no device)."""
 import pytest
 
 from sparse_attention_kv_qsa_gb300 import qsa
-from test_cache_abi import A, lib, paged  # noqa: F401 (lib is a fixture)
+from test_cache_abi import A, lib, paged, window  # noqa: F401 (lib is a fixture)
 
 INVALID = qsa.QSA_ERR_INVALID
 
@@ -29,3 +29,8 @@ def test_prompt_attention_has_a_fault_bit(lib):  # noqa: F811
     assert lib.qsa_debug_inject(qsa.INJECT_WINDOW_STALL, 10 ** 6) == qsa.QSA_OK      # nothing is launched
     assert lib.qsa_debug_inject(16, 10 ** 6) == INVALID
     assert lib.qsa_debug_inject(0, qsa.WAIT_LIMIT_DEFAULT_NS) == qsa.QSA_OK
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38])
+def test_a_scale_that_overflows_in_base_2_is_refused(lib, scale):  # noqa: F811
+    assert paged(lib, scale=scale) == INVALID and window(lib, scale=scale) == INVALID
