@@ -472,6 +472,77 @@ qsa_status qsa_cache_evict(const qsa_kv_pages *kv, int nseq, const int32_t *page
                            int recent, int32_t *kept, int32_t *new_lens, float *new_mass, int64_t new_mass_stride,
                            int new_mass_cols, cudaStream_t stream);
 
+/* ---- New tokens in the paged cache: rotation by position, append, attention over a shared prefix ---- */
+
+/*
+ * Rotation by position of the first 2 * npairs elements of a head's 128
+ * (the others stay as they are). Pair p is elements (p, p + npairs), or
+ * (2 p, 2 p + 1) where `interleaved`; it is turned by
+ *   angle = position * freqs[p]:  (a, b) -> (a cos - b sin, b cos + a sin),
+ * by -angle where `inverse` (which undoes it, and is its gradient). The
+ * position of token t for pair p is positions[axis[p] * position_stride + t]:
+ * one axis for text, several (time, height, width) for images and video, an
+ * axis for each pair. A pair whose axis is outside [0, naxes) is not turned.
+ * The angle is reduced exactly (fixed point, 2^-32 turns), whatever the
+ * position; sine, cosine and products are fp32, the result is rounded once.
+ * A frequency that is not finite gives NaN.
+ * freqs     fp32 [npairs]; npairs a multiple of 8, 8 .. 64.
+ * axis      int32 [npairs], or NULL: axis 0 for every pair.
+ * positions int32 [naxes] rows of one element per token, row stride
+ *           position_stride (elements, not negative), 4-byte aligned.
+ */
+typedef struct {
+    const float *freqs;
+    const int32_t *axis, *positions;
+    int64_t position_stride;
+    int32_t npairs, naxes, interleaved, inverse;
+} qsa_rotation;
+
+/*
+ * out[t][h] = x[t][h] rotated by token t's position (see qsa_rotation).
+ * x, out    [ntok][nheads][128] of dtype (QSA_F32, QSA_F16 or QSA_BF16),
+ *           16-byte aligned; strides: element strides of x per token and head,
+ *           then of out, multiples of 16 bytes, not negative, those of out at
+ *           least 128 (a dimension of one element: any). out is x itself (same
+ *           address and strides) or does not overlap it.
+ * A missing rotation, frequency or position, a bad type, size, pointer or
+ * stride returns QSA_ERR_INVALID; nheads or naxes above 65,535 QSA_ERR_UNSUPPORTED.
+ */
+qsa_status qsa_rotate(const void *x, qsa_dtype dtype, const int64_t *strides, int ntok, int nheads,
+                      const qsa_rotation *rotation, void *out, cudaStream_t stream);
+
+/*
+ * Appends new tokens to a paged cache. Tokens cu[s] .. cu[s+1]-1 are the new
+ * tokens of sequence s, the last of its lens[s] cells (lens counts them
+ * already, as the attention calls that follow want it): token t's cell is
+ * lens[s] - (cu[s+1] - t), in the pages as qsa_paged_attn reads them.
+ *   key cell = rotated k[t], value cell = v[t]; q_out[t] = rotated q[t], k_out[t] = rotated k[t]
+ * Without a rotation keys are copied and there is no q. Without positions
+ * (naxes 1) a token's position is its cell's number; `inverse` has to be 0.
+ * int8 pages: scale = binary16(max_d |x_d| / 127) (to nearest even, 65504 at
+ * most), codes rint(x_d / scale), at most 127 in size (0 where the scale is 0),
+ * in fp32; a cell with an infinity or NaN gets scale NaN and codes 0.
+ * Tokens of no sequence (below cu[0], from cu[nseq] on) are left out: nothing
+ * of theirs is written. A cell below 0, at or past table_cols * page_size, or
+ * whose page number is outside [0, npages) is not written (q_out and k_out are).
+ * Two tokens with the same cell leave it undefined.
+ * k, v      [ntok][nkv][128], q [ntok][nheads][128] (or NULL, with nheads 0),
+ *           of dtype: QSA_F32, or the pages' type; any of the three 16- and
+ *           32-bit types for int8 pages. q_out and k_out (or NULL) of dtype.
+ *           q_out with q; k_out only with a rotation.
+ * strides   of k, v, q, q_out, k_out per token and head (10 numbers, elements;
+ *           rules as qsa_rotate's; those of missing tensors are not read).
+ *           q_out may be q itself, k_out k itself; no other overlaps.
+ * The pages' strides are at least 128 here (a dimension of one element: any).
+ * cu        int32 [nseq + 1], ascending (values are clamped to [0, ntok]), or
+ *           NULL: one token per sequence, ntok == nseq.
+ * page_table, lens as qsa_paged_attn. Errors and limits as qsa_paged_attn.
+ */
+qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dtype dtype, const int64_t *strides,
+                            int ntok, int nheads, const qsa_kv_pages *kv, const int32_t *page_table, int table_cols,
+                            int64_t table_stride, const int32_t *lens, const int32_t *cu, int nseq,
+                            const qsa_rotation *rotation, void *q_out, void *k_out, cudaStream_t stream);
+
 /* Static description of a status code. */
 const char *qsa_status_string(qsa_status status);
 

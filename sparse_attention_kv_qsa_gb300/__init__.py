@@ -1,7 +1,8 @@
 """Exact QSA block selection on GB300: block scoring, per-query top-k,
 attention over the selected blocks, and block summary keys on append; and a
 cache kept within a budget: prompt attention with a sliding window and sinks,
-paged decode attention, and eviction by accumulated attention weight.
+paged decode attention, and eviction by accumulated attention weight; and new
+tokens: rotation by position and append to the paged cache.
 
 The computation lives in ``libqsa.so`` (CUDA kernels for sm_103a behind the C
 ABI of ``include/qsa.h``); ``qsa`` is its Python binding and ``workloads``
@@ -23,10 +24,12 @@ from .qsa import (  # noqa: F401
     block_summary,
     block_topk,
     block_topk_gmax,
+    cache_append,
     cache_evict,
     groups,
     paged_attn,
     paged_attn_scratch_bytes,
+    rotate,
     select_scratch_bytes,
     debug_inject,
     default_scorer_kernel,

@@ -1,4 +1,4 @@
-// Python binding of the bounded-cache calls of include/qsa.h (argument checks,
+// Python binding of the paged-cache calls of include/qsa.h (argument checks,
 // outputs, pointers and the current stream; no computation). These calls take
 // 10 to 20 us on the GPU at serving sizes, so what the host does before each of
 // them counts: measured on the GB300's Arm host, a call of decode attention
@@ -319,7 +319,138 @@ PyObject *cache_evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// positions (None where `own_positions`), freqs, axis, interleaved, inverse of `ntok` tokens
+qsa_rotation rotation_of(PyObject *positions, PyObject *freqs, PyObject *axis, PyObject *interleaved, PyObject *inverse,
+                         bool own_positions, int ntok, int index) {
+    qsa_rotation r = {};
+    const Tensor &f = checked(freqs, "freqs", {at::kFloat}, 1, index);
+    if (f.size(0) < 8 || f.size(0) > 64 || f.size(0) % 8 != 0) refuse("freqs must have 8, 16, .. 64 elements");
+    r.npairs = static_cast<int>(f.size(0));
+    r.freqs = f.data_ptr<float>();
+    if (axis != Py_None) {
+        const Tensor &a = checked(axis, "axis", {at::kInt}, 1, index);
+        if (a.size(0) != f.size(0)) refuse("axis must have one element per frequency");
+        r.axis = a.data_ptr<int32_t>();
+    }
+    if (positions == Py_None) {
+        if (!own_positions) refuse("positions must be a CUDA tensor");
+        if (r.axis != nullptr) refuse("axis needs positions");
+        r.naxes = 1;
+    } else {
+        const Tensor &p = cuda_tensor(positions, "positions");
+        checked(positions, "positions", {at::kInt}, p.dim() == 1 ? 1 : 2, index);
+        if (p.size(p.dim() - 1) != ntok || p.numel() == 0) refuse("positions must be [%d] or [axes, %d]", ntok, ntok);
+        r.positions = p.data_ptr<int32_t>();
+        r.naxes = p.dim() == 1 ? 1 : size32(p.size(0), "axes");
+        r.position_stride = p.dim() == 1 ? 0 : stride(p, 0);
+    }
+    r.interleaved = PyObject_IsTrue(interleaved) > 0;
+    r.inverse = PyObject_IsTrue(inverse) > 0;
+    return r;
+}
+
+// An output of that shape and type with strides of its own, or a new one.
+Tensor made_rows(PyObject *o, const char *name, at::IntArrayRef shape, ScalarType type, int index) {
+    if (o == Py_None) return made(o, name, shape, type, index);
+    const Tensor &t = checked(o, name, {type}, 3, index);
+    if (t.sizes() != shape) refuse("%s must have the result's shape", name);
+    return t;
+}
+
+// x, positions, freqs, axis, interleaved, inverse, out
+PyObject *rotate(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject * {
+        const int index = static_cast<int>(cuda_tensor(a[0], "x").get_device());
+        const c10::cuda::CUDAGuard device(static_cast<c10::DeviceIndex>(index));
+        const Tensor &x = checked(a[0], "x", {at::kFloat, at::kHalf, at::kBFloat16}, 3, index);
+        const int ntok = size32(x.size(0), "ntok"), nheads = size32(x.size(1), "nheads");
+        if (x.size(2) != QSA_D || nheads < 1) refuse("x must be [ntok, nheads, %d]", QSA_D);
+        const Tensor out = made_rows(a[6], "out", {ntok, nheads, QSA_D}, x.scalar_type(), index);
+        if (ntok == 0) return tuple({out});
+        const qsa_rotation r = rotation_of(a[1], a[2], a[3], a[4], a[5], false, ntok, index);
+        const int64_t strides[4] = {stride(x, 0), stride(x, 1), stride(out, 0), stride(out, 1)};
+        const qsa_status status =
+            qsa_rotate(x.data_ptr(), kind(x), strides, ntok, nheads, &r, out.data_ptr(), current_stream(index));
+        return status == QSA_OK ? tuple({out}) : PyLong_FromLong(status);
+    });
+}
+
+// k, v, k_pages, v_pages, page_table, lens, cu, k_scale, v_scale, q, positions, freqs, axis, interleaved, q_out, k_out
+PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 16, [&]() -> PyObject * {
+        const int index = static_cast<int>(cuda_tensor(a[2], "k_pages").get_device());
+        const c10::cuda::CUDAGuard device(static_cast<c10::DeviceIndex>(index));
+        const qsa_kv_pages kv = pages(a[2], a[3], a[7], a[8], index);
+        const ScalarType cells = THPVariable_Unpack(a[2]).scalar_type();
+        const Tensor &k = cells == at::kChar ? checked(a[0], "k", {at::kFloat, at::kHalf, at::kBFloat16}, 3, index)
+                                             : checked(a[0], "k", {cells, at::kFloat}, 3, index);
+        const Tensor &v = checked(a[1], "v", {k.scalar_type()}, 3, index);
+        const int ntok = size32(k.size(0), "ntok");
+        if (k.size(1) != kv.nkv || k.size(2) != QSA_D || v.sizes() != k.sizes())
+            refuse("k and v must be [ntok, %d, %d]", kv.nkv, QSA_D);
+        const Tensor &table = checked(a[4], "page_table", {at::kInt}, 2, index), &lens = checked(a[5], "lens", {at::kInt}, 1, index);
+        if (lens.size(0) != table.size(0)) refuse("page_table and lens must have one row per sequence");
+        const int nseq = size32(table.size(0), "nseq"), cols = size32(table.size(1), "page_table's width");
+        const int32_t *cu = nullptr;
+        if (a[6] != Py_None) {
+            const Tensor &c = checked(a[6], "cu", {at::kInt}, 1, index);
+            if (c.size(0) != static_cast<int64_t>(nseq) + 1) refuse("cu must have one more element than there are sequences");
+            cu = c.data_ptr<int32_t>();
+        } else if (ntok != nseq) {
+            refuse("without cu there is one token per sequence");
+        }
+        int64_t strides[10] = {stride(k, 0), stride(k, 1), stride(v, 0), stride(v, 1)};
+        const void *q = nullptr;
+        Tensor q_out, k_out;
+        int nheads = 0;
+        if (a[9] != Py_None) {
+            const Tensor &t = checked(a[9], "q", {k.scalar_type()}, 3, index);
+            nheads = size32(t.size(1), "nheads");
+            if (t.size(0) != ntok || t.size(2) != QSA_D || nheads < 1) refuse("q must be [%d, nheads, %d]", ntok, QSA_D);
+            if (a[11] == Py_None) refuse("q needs freqs");
+            q = t.data_ptr();
+            q_out = made_rows(a[14], "q_out", {ntok, nheads, QSA_D}, k.scalar_type(), index);
+            strides[4] = stride(t, 0);
+            strides[5] = stride(t, 1);
+            strides[6] = stride(q_out, 0);
+            strides[7] = stride(q_out, 1);
+        } else if (a[14] != Py_None) {
+            refuse("q_out needs q");
+        }
+        if (a[15] != Py_None) {
+            if (a[11] == Py_None) refuse("k_out needs freqs");
+            k_out = made_rows(a[15], "k_out", {ntok, kv.nkv, QSA_D}, k.scalar_type(), index);
+            strides[8] = stride(k_out, 0);
+            strides[9] = stride(k_out, 1);
+        }
+        if (a[11] == Py_None && (a[10] != Py_None || a[12] != Py_None)) refuse("positions and axis need freqs");
+        qsa_rotation r = {};
+        if (a[11] != Py_None && ntok > 0) r = rotation_of(a[10], a[11], a[12], a[13], Py_False, true, ntok, index);
+        if (ntok > 0) {
+            const qsa_status status = qsa_cache_append(
+                k.data_ptr(), v.data_ptr(), q, kind(k), strides, ntok, nheads, &kv, table.data_ptr<int32_t>(), cols,
+                row_stride(table), lens.data_ptr<int32_t>(), cu, nseq, a[11] == Py_None ? nullptr : &r,
+                q == nullptr ? nullptr : q_out.data_ptr(), a[15] == Py_None ? nullptr : k_out.data_ptr(), current_stream(index));
+            if (status != QSA_OK) return PyLong_FromLong(status);
+        }
+        PyObject *pair = PyTuple_New(2);
+        if (pair == nullptr) throw PythonError();
+        for (int i = 0; i < 2; ++i) {
+            const Tensor &t = i == 0 ? q_out : k_out;
+            PyObject *o = t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);
+            if (o == nullptr) {
+                Py_DECREF(pair);
+                throw PythonError();
+            }
+            PyTuple_SET_ITEM(pair, i, o);
+        }
+        return pair;
+    });
+}
+
 PyMethodDef methods[] = {
+    {"rotate", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rotate)), METH_FASTCALL, nullptr},
+    {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
     {"paged_attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attn)), METH_FASTCALL, nullptr},
     {"window_attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(window_attn)), METH_FASTCALL, nullptr},
     {"cache_evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_evict)), METH_FASTCALL, nullptr},

@@ -43,9 +43,77 @@ qsa_status check_table(int cols, int64_t stride, int page_size) {
     return static_cast<long long>(cols) * page_size > MAX_CELLS ? QSA_ERR_UNSUPPORTED : QSA_OK;
 }
 
+// A rotation; positions may be missing where `own_positions`.
+qsa_status check_rotation(const qsa_rotation *r, bool own_positions) {
+    if (r->npairs < 8 || r->npairs > 64 || r->npairs % 8 != 0 || r->naxes < 1 || !aligned(r->freqs, 4)) return QSA_ERR_INVALID;
+    if (r->axis != nullptr && !aligned(r->axis, 4)) return QSA_ERR_INVALID;
+    if (r->positions == nullptr) {
+        if (!own_positions || r->naxes != 1) return QSA_ERR_INVALID;
+    } else if (!aligned(r->positions, 4) || r->position_stride < 0) {
+        return QSA_ERR_INVALID;
+    }
+    return r->naxes > MAX_HEADS ? QSA_ERR_UNSUPPORTED : QSA_OK;
+}
+
+// Strides per token and head of [ntok][nheads][128] elements, which rows written must not share.
+bool good_rows(const int64_t *strides, int dtype, int ntok, int nheads, bool written) {
+    if (!good_stride(strides[0], dtype) || !good_stride(strides[1], dtype)) return false;
+    return !written || ((ntok == 1 || strides[0] >= 128) && (nheads == 1 || strides[1] >= 128));
+}
+
+bool row_type(int dtype) { return dtype == QSA_F32 || dtype == QSA_F16 || dtype == QSA_BF16; }
+
 }  // namespace
 
 extern "C" {
+
+qsa_status qsa_rotate(const void *x, qsa_dtype dtype, const int64_t *strides, int ntok, int nheads,
+                      const qsa_rotation *rotation, void *out, cudaStream_t stream) {
+    if (!row_type(dtype) || ntok < 0 || nheads < 1 || strides == nullptr || rotation == nullptr) return QSA_ERR_INVALID;
+    const qsa_status s = check_rotation(rotation, ntok == 0);
+    if (s != QSA_OK) return s;
+    if (!good_rows(strides, dtype, ntok, nheads, false) || !good_rows(strides + 2, dtype, ntok, nheads, true)) return QSA_ERR_INVALID;
+    if (ntok == 0) return QSA_OK;
+    if (nheads > MAX_HEADS) return QSA_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(out, 16)) return QSA_ERR_INVALID;
+    return from_cuda(qsa::launch_rotate(x, dtype, strides, ntok, nheads, *rotation, out, stream));
+}
+
+qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dtype dtype, const int64_t *strides,
+                            int ntok, int nheads, const qsa_kv_pages *kv, const int32_t *page_table, int table_cols,
+                            int64_t table_stride, const int32_t *lens, const int32_t *cu, int nseq,
+                            const qsa_rotation *rotation, void *q_out, void *k_out, cudaStream_t stream) {
+    qsa_status s = check_pages(kv);
+    if (s != QSA_OK) return s;
+    s = check_table(table_cols, table_stride, kv->page_size);
+    if (s != QSA_OK) return s;
+    if (!row_type(dtype) || (kv->dtype != QSA_I8 && dtype != QSA_F32 && static_cast<int>(dtype) != kv->dtype)) return QSA_ERR_INVALID;
+    if (ntok < 0 || nseq < 0 || nheads < 0 || strides == nullptr || (cu == nullptr && ntok != nseq)) return QSA_ERR_INVALID;
+    if (rotation == nullptr ? nheads != 0 || k_out != nullptr : rotation->inverse != 0) return QSA_ERR_INVALID;
+    if (rotation != nullptr && (s = check_rotation(rotation, true)) != QSA_OK) return s;
+    const int nkv = kv->nkv;
+    if (!good_rows(strides, dtype, ntok, nkv, false) || !good_rows(strides + 2, dtype, ntok, nkv, false)) return QSA_ERR_INVALID;
+    if (nheads > 0 && (!good_rows(strides + 4, dtype, ntok, nheads, false) || !good_rows(strides + 6, dtype, ntok, nheads, true)))
+        return QSA_ERR_INVALID;
+    if (k_out != nullptr && !good_rows(strides + 8, dtype, ntok, nkv, true)) return QSA_ERR_INVALID;
+    // Cells are written: none may share its memory with another.
+    if ((kv->npages > 1 && kv->page_stride < 128) || (kv->page_size > 1 && kv->cell_stride < 128) ||
+        (nkv > 1 && kv->head_stride < 128))
+        return QSA_ERR_INVALID;
+    if (kv->dtype == QSA_I8 && ((kv->npages > 1 && kv->scale_page_stride < 1) || (kv->page_size > 1 && kv->scale_cell_stride < 1) ||
+                                (nkv > 1 && kv->scale_head_stride < 1)))
+        return QSA_ERR_INVALID;
+    if (ntok == 0 || nseq == 0) return QSA_OK;
+    if (nseq > MAX_SEQS || nheads > MAX_HEADS || nkv > MAX_HEADS) return QSA_ERR_UNSUPPORTED;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(lens, 4)) return QSA_ERR_INVALID;
+    if (nheads > 0 && (!aligned(q, 16) || !aligned(q_out, 16))) return QSA_ERR_INVALID;
+    if (k_out != nullptr && !aligned(k_out, 16)) return QSA_ERR_INVALID;
+    if (cu != nullptr && !aligned(cu, 4)) return QSA_ERR_INVALID;
+    if (table_cols > 0 && !aligned(page_table, 4)) return QSA_ERR_INVALID;
+    const qsa::CacheAppendArgs a{k, v, q, dtype, strides, ntok, nheads, *kv, page_table, table_cols, table_stride,
+                                 lens, cu, nseq, rotation, q_out, k_out};
+    return from_cuda(qsa::launch_cache_append(a, stream));
+}
 
 size_t qsa_paged_attn_scratch_bytes(int nseq, int nheads, int nkv, int table_cols, int page_size, int with_mass) {
     // A table without columns is a call like any other: every sequence is empty, and the kernels say so in scratch.

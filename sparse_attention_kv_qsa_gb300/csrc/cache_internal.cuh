@@ -84,4 +84,24 @@ struct CacheEvictArgs {
 
 cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream);
 
+cudaError_t launch_rotate(const void *x, int dtype, const int64_t *strides, int ntok, int nheads, const qsa_rotation &rot,
+                          void *out, cudaStream_t stream);
+
+struct CacheAppendArgs {
+    const void *k, *v, *q;
+    int dtype;
+    const int64_t *strides;   // of k, v, q, q_out, k_out per token and head
+    int ntok, nheads;
+    qsa_kv_pages kv;
+    const int32_t *table;
+    int table_cols;
+    int64_t table_stride;
+    const int32_t *lens, *cu;
+    int nseq;
+    const qsa_rotation *rotation;
+    void *q_out, *k_out;
+};
+
+cudaError_t launch_cache_append(const CacheAppendArgs &a, cudaStream_t stream);
+
 }  // namespace qsa

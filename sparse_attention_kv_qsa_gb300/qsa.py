@@ -2,9 +2,9 @@
 
 Every step of the selection runs in ``libqsa.so``'s CUDA kernels; this module
 checks tensor shapes, dtypes and devices, allocates outputs with torch, and
-passes raw device pointers and the current CUDA stream. The bounded-cache calls
-(``window_attn``, ``paged_attn``, ``cache_evict``) do the same in the compiled
-module ``qsa_ops.so``, whose checks take a few microseconds less of each call.
+passes raw device pointers and the current CUDA stream. The paged-cache calls
+(``window_attn``, ``paged_attn``, ``cache_evict``, ``rotate``, ``cache_append``)
+do the same in the compiled module ``qsa_ops.so``, whose checks take a few microseconds less of each call.
 There is no fallback: if a library is missing, calling the functions raises.
 """
 
@@ -33,7 +33,7 @@ EXPORTED = ("qsa_block_scores", "qsa_block_scores_q8", "qsa_block_scores_ffma", 
             "qsa_block_select_static", "qsa_block_select_small", "qsa_sparse_attn", "qsa_block_summary",
             "qsa_get_device_error", "qsa_debug_inject", "qsa_status_string", "qsa_block_select",
             "qsa_block_select_scratch_bytes", "qsa_paged_attn", "qsa_paged_attn_scratch_bytes", "qsa_window_attn",
-            "qsa_window_attn_scratch_bytes", "qsa_cache_evict")
+            "qsa_window_attn_scratch_bytes", "qsa_cache_evict", "qsa_rotate", "qsa_cache_append")
 
 
 F32, F16, BF16, I8 = 0, 1, 2, 3   # qsa_dtype
@@ -47,6 +47,13 @@ class KVPages(ctypes.Structure):
                 ("cell_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("scale_page_stride", ctypes.c_int64), ("scale_cell_stride", ctypes.c_int64),
                 ("scale_head_stride", ctypes.c_int64)]
+
+
+class Rotation(ctypes.Structure):
+    """``qsa_rotation``: frequencies, axes and positions of a rotation."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("position_stride", ctypes.c_int64), ("npairs", ctypes.c_int32), ("naxes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32)]
 
 
 class QSAError(RuntimeError):
@@ -102,6 +109,11 @@ def lib() -> ctypes.CDLL:
         L.qsa_window_attn.restype = i
         L.qsa_cache_evict.argtypes = [kv, i, vp, i, ll, vp, vp, ll, vp, i, ll, i, i, i, vp, vp, vp, ll, i, vp]
         L.qsa_cache_evict.restype = i
+        rot = ctypes.POINTER(Rotation)
+        L.qsa_rotate.argtypes = [vp, i, ctypes.POINTER(ll), i, i, rot, vp, vp]
+        L.qsa_rotate.restype = i
+        L.qsa_cache_append.argtypes = [vp, vp, vp, i, ctypes.POINTER(ll), i, i, kv, vp, i, ll, vp, vp, i, rot, vp, vp, vp]
+        L.qsa_cache_append.restype = i
         L.qsa_debug_inject.argtypes = [ctypes.c_uint32, ctypes.c_uint64]
         L.qsa_debug_inject.restype = i
         L.qsa_status_string.argtypes = [i]
@@ -465,7 +477,7 @@ _ops_module = None
 
 
 def _ops():
-    """``qsa_ops.so``, the compiled binding of the bounded-cache calls (raises if it has not been built)."""
+    """``qsa_ops.so``, the compiled binding of the paged-cache calls (raises if it has not been built)."""
     global _ops_module
     if _ops_module is None:
         lib()
@@ -554,6 +566,47 @@ def cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.
                                            k_scale_f16, v_scale_f16, kept, new_lens, new_mass)
     if r.__class__ is int:
         raise QSAError(r, "qsa_cache_evict")
+    return r
+
+
+def rotate(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, axis: torch.Tensor | None = None,
+           interleaved: bool = False, inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """``qsa_rotate``: ``x [ntok, nheads, 128]`` (float32, bfloat16 or float16;
+    token and head strides of multiples of 16 bytes) with the first ``2 *
+    len(freqs)`` elements of every head turned in pairs ``(p, p + len(freqs))``,
+    or ``(2p, 2p + 1)`` where ``interleaved``, by the angle ``position *
+    freqs[p]`` (by its negative where ``inverse``: the way back, and the
+    gradient). ``positions`` int32 ``[ntok]``, or ``[axes, ntok]`` with the axis
+    of each pair in ``axis`` int32 ``[len(freqs)]`` (time, height, width);
+    ``freqs`` float32, 8, 16, .. 64 of them. ``out`` may be ``x`` itself."""
+    r = (_ops_module or _ops()).rotate(x, positions, freqs, axis, interleaved, inverse, out)
+    if r.__class__ is int:
+        raise QSAError(r, "qsa_rotate")
+    return r[0]
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 page_table: torch.Tensor, lens: torch.Tensor, *, cu: torch.Tensor | None = None,
+                 k_scale_f16: torch.Tensor | None = None, v_scale_f16: torch.Tensor | None = None,
+                 q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                 freqs: torch.Tensor | None = None, axis: torch.Tensor | None = None, interleaved: bool = False,
+                 q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None) -> tuple[torch.Tensor | None, torch.Tensor | None]:
+    """``qsa_cache_append``: writes new tokens' keys and values ``k, v [ntok,
+    nkv, 128]`` to their cells of the paged cache (``k_pages``, ``v_pages``,
+    ``page_table`` as in ``paged_attn``). Sequence ``s`` has tokens ``cu[s] ..
+    cu[s+1]-1``, the last of its ``lens[s]`` cells, which count them already;
+    without ``cu`` one token each. With ``freqs`` keys are rotated on the way as
+    ``rotate`` does, by ``positions`` or, without them, by the number of the
+    cell; ``q [ntok, nheads, 128]`` is rotated beside them. Rows are float32 or
+    the pages' type (for int8 pages, which get a binary16 scale per cell and
+    head, any of the three). Returns ``(q_out, k_out)``: the rotated queries
+    (None without ``q``; ``q_out`` may be ``q``), and the rotated keys where a
+    tensor is given to take them."""
+    r = (_ops_module or _ops()).cache_append(k, v, k_pages, v_pages, page_table, lens, cu, k_scale_f16, v_scale_f16, q,
+                                            positions, freqs, axis, interleaved, q_out, k_out)
+    if r.__class__ is int:
+        raise QSAError(r, "qsa_cache_append")
     return r
 
 

@@ -1,0 +1,142 @@
+"""The new-token calls refuse bad arguments before anything is launched (CPU only: fake device addresses, no call here
+reaches a kernel), and the 64-bit forms that the GPU tests compare with are right where they can be written down by hand."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import token_ref
+from sparse_attention_kv_qsa_gb300 import build as qsa_build
+from sparse_attention_kv_qsa_gb300 import qsa
+from test_cache_abi import A, B, BAD_PAGES, MIS, pages
+
+OK, INVALID, UNSUPPORTED = qsa.QSA_OK, qsa.QSA_ERR_INVALID, qsa.QSA_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def lib():
+    qsa_build.build()
+    return qsa.lib()
+
+
+def rotation(**kw):
+    d = dict(freqs=A, axis=None, positions=A, position_stride=100, npairs=64, naxes=1, interleaved=0, inverse=0)
+    d.update(kw)
+    return ctypes.byref(qsa.Rotation(**d))
+
+
+BAD_ROTATIONS = [dict(freqs=None), dict(freqs=MIS), dict(axis=MIS), dict(positions=MIS), dict(position_stride=-1), dict(npairs=0),
+                 dict(npairs=12), dict(npairs=72), dict(npairs=-8), dict(naxes=0), dict(naxes=-1)]
+
+
+def rotate(lib, rot=None, **kw):
+    d = dict(x=A, dtype=qsa.BF16, strides=(1024, 128, 1024, 128), ntok=5, nheads=8, out=B)
+    d.update(kw)
+    st = None if d["strides"] is None else (ctypes.c_int64 * 4)(*d["strides"])
+    return lib.qsa_rotate(d["x"], d["dtype"], st, d["ntok"], d["nheads"], None if rot == "none" else rot or rotation(), d["out"], None)
+
+
+@pytest.mark.parametrize("bad", BAD_ROTATIONS + [dict(positions=None)])
+def test_rotate_bad_rotations(lib, bad):
+    assert rotate(lib, rotation(**bad)) == INVALID
+
+
+@pytest.mark.parametrize("bad", [dict(x=None), dict(x=MIS), dict(out=None), dict(out=MIS), dict(dtype=qsa.I8), dict(dtype=9),
+                                 dict(strides=None), dict(ntok=-1), dict(nheads=0), dict(strides=(1024, 4, 1024, 128)),
+                                 dict(strides=(-1024, 128, 1024, 128)), dict(strides=(0, 0, 0, 128)),
+                                 dict(strides=(0, 0, 1024, 0)), dict(strides=(0, 0, 64, 128)), dict(rot="none")])
+def test_rotate_argument_errors(lib, bad):
+    assert rotate(lib, **bad) == INVALID
+
+
+def test_rotate_limits(lib):
+    assert rotate(lib, ntok=0, x=None, out=None) == OK
+    assert rotate(lib, nheads=65536) == UNSUPPORTED
+    assert rotate(lib, rotation(naxes=65536)) == UNSUPPORTED
+
+
+def append(lib, kv=None, rot=None, **kw):
+    d = dict(k=A, v=A, q=A, dtype=qsa.BF16, strides=(256, 128, 256, 128, 1024, 128, 1024, 128, 256, 128), ntok=5, nheads=8, table=A,
+             cols=4, tstride=4, lens=A, cu=A, nseq=2, q_out=B, k_out=B)
+    d.update(kw)
+    st = None if d["strides"] is None else (ctypes.c_int64 * 10)(*d["strides"])
+    return lib.qsa_cache_append(d["k"], d["v"], d["q"], d["dtype"], st, d["ntok"], d["nheads"], kv or pages(), d["table"], d["cols"],
+                                d["tstride"], d["lens"], d["cu"], d["nseq"], None if rot == "none" else rot or rotation(), d["q_out"],
+                                d["k_out"], None)
+
+
+INT8 = dict(dtype=qsa.I8, k_scale_f16=A, v_scale_f16=A, scale_page_stride=32, scale_cell_stride=2, scale_head_stride=1)
+
+
+@pytest.mark.parametrize("bad", BAD_PAGES + [dict(page_stride=0), dict(cell_stride=0), dict(head_stride=64),
+                                             dict(INT8, scale_page_stride=0), dict(INT8, scale_cell_stride=0),
+                                             dict(INT8, scale_head_stride=0)])
+def test_append_bad_pages(lib, bad):
+    assert append(lib, pages(**bad)) == INVALID
+
+
+@pytest.mark.parametrize("bad", BAD_ROTATIONS + [dict(inverse=1), dict(positions=None, naxes=2)])
+def test_append_bad_rotations(lib, bad):
+    assert append(lib, rot=rotation(**bad)) == INVALID
+
+
+def strides(i, n):
+    s = [256, 128, 256, 128, 1024, 128, 1024, 128, 256, 128]
+    s[i] = n
+    return tuple(s)
+
+
+@pytest.mark.parametrize("bad", [dict(k=None), dict(k=MIS), dict(v=None), dict(q=None), dict(q_out=None), dict(q_out=MIS), dict(k_out=MIS),
+                                 dict(dtype=qsa.F16), dict(dtype=qsa.I8), dict(strides=None), dict(ntok=-1), dict(nheads=-1),
+                                 dict(nseq=-1), dict(cu=None), dict(cu=MIS), dict(lens=None), dict(table=None), dict(cols=-1),
+                                 dict(tstride=3), dict(rot="none"), dict(rot="none", nheads=0, q=None, q_out=None)]
+                         + [dict(strides=strides(i, -128)) for i in range(10)] + [dict(strides=strides(i, 4)) for i in range(10)]
+                         + [dict(strides=strides(i, 0)) for i in range(6, 10)])
+def test_append_argument_errors(lib, bad):
+    assert append(lib, **bad) == INVALID
+
+
+def test_append_limits(lib):
+    assert append(lib, ntok=0, k=None, v=None, q=None, q_out=None, lens=None) == OK
+    assert append(lib, nseq=0) == OK
+    assert append(lib, nseq=65536) == UNSUPPORTED
+    assert append(lib, nheads=65536) == UNSUPPORTED
+    assert append(lib, rot=rotation(naxes=65536)) == UNSUPPORTED
+    assert append(lib, cols=1 << 27, tstride=1 << 27) == UNSUPPORTED
+
+
+def test_binding_refuses_what_is_not_on_the_gpu():
+    x, p = torch.zeros((1, 1, 128)), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        qsa.rotate(x, p, torch.ones(64))
+    t = torch.zeros((1, 16, 1, 128))
+    with pytest.raises(ValueError):
+        qsa.cache_append(x, x, t, t, torch.zeros((1, 1), dtype=torch.int32), p)
+
+
+def test_reference_rotation_by_hand():
+    x = torch.zeros((2, 1, 128)); x[..., 0], x[..., 8], x[..., 1] = 3.0, 4.0, 5.0
+    f = torch.zeros(8); f[0] = 0.5
+    p = torch.tensor([0, 7], dtype=torch.int32)
+    y = token_ref.rotate(x, p, f)
+    assert torch.equal(y[0], x[0].double())
+    # below, 7 times some 4 roundings of 2^-53 (the reduced angle's, cosine's, product's and sum's): 3.2e-15
+    c, s = math.cos(3.5), math.sin(3.5)
+    assert abs(y[1, 0, 0] - (3 * c - 4 * s)) < 4e-15 and abs(y[1, 0, 8] - (4 * c + 3 * s)) < 4e-15 and y[1, 0, 1] == 5
+    y = token_ref.rotate(x, p, f, interleaved=True, inverse=True)
+    assert abs(y[1, 0, 0] - (3 * c + 5 * s)) < 4e-15 and abs(y[1, 0, 1] - (5 * c - 3 * s)) < 4e-15 and y[1, 0, 8] == 4
+    y = token_ref.rotate(x, torch.stack((p, p + 1)), f, torch.tensor([1] + [0] * 7))
+    assert abs(y[0, 0, 0] - (3 * math.cos(0.5) - 4 * math.sin(0.5))) < 4e-15
+    # a whole number of turns of a far position: 2^31 - 1 times 1 radian
+    far = token_ref.rotate(torch.eye(128)[:1, None], torch.tensor([2 ** 31 - 1], dtype=torch.int32), torch.ones(8))
+    assert abs(float(far[0, 0, 0]) - math.cos(2 ** 31 - 1)) < 1e-9
+
+
+def test_reference_codes_by_hand():
+    x = torch.zeros((4, 128)); x[0, 0], x[0, 1], x[0, 2] = 127.0, -63.5, 0.5
+    x[2, 3], x[3, 0] = 1e-9, math.inf
+    q, s = token_ref.codes(x)
+    assert s[0] == 1.0 and q[0, :3].tolist() == [127, -64, 0]           # halves to even
+    assert s[1] == 0.0 and not q[1].any() and s[2] == 0.0 and not q[2].any()
+    assert math.isnan(s[3]) and not q[3].any()
