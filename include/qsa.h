@@ -309,7 +309,7 @@ qsa_status qsa_block_select(const float *q, const float *kblk, int nq, int max_b
  * then abandons its remaining waits at once, lets its own copies and MMAs
  * in flight finish, and exits); bit 0x2: the fused decode select's grid
  * barrier ran out; bit 0x10000: a wait of the prompt attention's pipeline ran
- * out. Synchronises `stream`. *code receives the word.
+ * out; bit 0x20000: one of the shared prefix's attention. Synchronises `stream`. *code receives the word.
  */
 qsa_status qsa_get_device_error(uint32_t *code, cudaStream_t stream);
 
@@ -317,14 +317,17 @@ qsa_status qsa_get_device_error(uint32_t *code, cudaStream_t stream);
  * Diagnostics for the bounded waits (not for production use; the pages have
  * no counterpart). For the kernels launched after the call: every spin-wait
  * gives up after wait_limit_ns (default 2,000,000,000; in the prompt attention
- * 8 us more for every 128 keys of the call, as items take that long), and
+ * 8 us more for every 128 keys of the call, as items take that long, in the shared
+ * prefix's for every 128 cells that a CTA may have), and
  * `faults` plants a wait that cannot complete so that the time-out path runs:
  *   bit 0: the tensor-core scorer's CTA 0 never loads its first key piece
  *          (qsa_block_scores, _q8, _gmax and _select_static with nq > 4);
  *   bit 1: the fused decode select's grid barrier waits for one arrival
  *          more than its grid has (qsa_block_select_small);
  *   bit 3: the prompt attention's CTA 0 never copies its first key tile
- *          (qsa_window_attn, where the strides suit a tensor map).
+ *          (qsa_window_attn, where the strides suit a tensor map);
+ *   bit 5: the shared prefix's attention's CTA 0 never hands over its first
+ *          key tile (qsa_prefix_attn).
  * The outputs of such calls are invalid and qsa_get_device_error reports
  * them; the device stays usable. Call qsa_debug_inject(0, 2000000000) to
  * restore normal operation. Process-wide; not thread-safe against
@@ -542,6 +545,43 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
                             int ntok, int nheads, const qsa_kv_pages *kv, const int32_t *page_table, int table_cols,
                             int64_t table_stride, const int32_t *lens, const int32_t *cu, int nseq,
                             const qsa_rotation *rotation, void *q_out, void *k_out, cudaStream_t stream);
+
+/*
+ * Attention of one new token per sequence where groups of sequences share a
+ * long prefix: the result of qsa_paged_attn (without window and mass) over the
+ * prefix's cells and then the sequence's own, with the prefix read once for
+ * all sequences of its group.
+ * Group g is sequences cu_seqs[g] .. cu_seqs[g+1]-1; its prefix is the first
+ * prefix_lens[g] cells of the pages of row g of prefix_table. Sequence s has
+ * lens[s] cells of its own in the pages of row s of page_table (its own token
+ * among them). A sequence of no group (before cu_seqs[0], from cu_seqs[ngroups] on) has
+ * no prefix. logit, lse and out as qsa_paged_attn, over both; without any cell
+ * out = 0 and lse = -infinity. Lengths are clamped to their tables' capacity;
+ * a cell whose page number is outside [0, npages) is skipped. Cells that are
+ * not there are never used, whatever they hold; an infinity or NaN in a cell's value
+ * (or its scale) makes results of all sequences that see it infinite or NaN.
+ * cu_seqs   int32 [ngroups + 1], ascending (values are clamped to [0, nseq];
+ *           where they are not ascending the results are unspecified).
+ * prefix_table int32, row stride prefix_stride >= prefix_cols; prefix_lens int32
+ *           [ngroups]. The rest as in qsa_paged_attn, q_dtype among it.
+ * scratch   at least qsa_prefix_attn_scratch_bytes(...) bytes, 16-byte aligned
+ *           (0 for nseq = 0 and for arguments that are refused); no contents
+ *           need survive.
+ * Sums and softmax statistics are fp32. The weights of prefix cells are rounded
+ * once to the 16-bit operand type (the pages', binary16 for int8 cells), as in
+ * qsa_window_attn; for fp32 queries they keep 22 bits.
+ * Errors and limits as qsa_paged_attn; nheads / nkv above 128 (64 for fp32
+ * queries), ngroups above 65,535 or prefix_cols * page_size above 2^30 returns
+ * QSA_ERR_UNSUPPORTED.
+ */
+size_t qsa_prefix_attn_scratch_bytes(int nseq, int ngroups, int nheads, int nkv, int prefix_cols, int table_cols,
+                                     int page_size);
+qsa_status qsa_prefix_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride, int64_t q_head_stride, int nseq,
+                           int nheads, const qsa_kv_pages *kv, const int32_t *prefix_table, int prefix_cols,
+                           int64_t prefix_stride, const int32_t *prefix_lens, const int32_t *cu_seqs, int ngroups,
+                           const int32_t *page_table, int table_cols, int64_t table_stride, const int32_t *lens,
+                           float scale, void *out, float *lse, void *scratch, size_t scratch_bytes,
+                           cudaStream_t stream);
 
 /* Static description of a status code. */
 const char *qsa_status_string(qsa_status status);

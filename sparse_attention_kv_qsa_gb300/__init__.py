@@ -2,7 +2,8 @@
 attention over the selected blocks, and block summary keys on append; and a
 cache kept within a budget: prompt attention with a sliding window and sinks,
 paged decode attention, and eviction by accumulated attention weight; and new
-tokens: rotation by position and append to the paged cache.
+tokens: rotation by position, append to the paged cache, and attention of
+sequences that share a prefix.
 
 The computation lives in ``libqsa.so`` (CUDA kernels for sm_103a behind the C
 ABI of ``include/qsa.h``); ``qsa`` is its Python binding and ``workloads``
@@ -29,6 +30,8 @@ from .qsa import (  # noqa: F401
     groups,
     paged_attn,
     paged_attn_scratch_bytes,
+    prefix_attn,
+    prefix_attn_scratch_bytes,
     rotate,
     select_scratch_bytes,
     debug_inject,

@@ -319,6 +319,40 @@ PyObject *cache_evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// q, k_pages, v_pages, prefix_table, prefix_lens, cu_seqs, page_table, lens, k_scale, v_scale, scale, out, lse, scratch
+PyObject *prefix_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 14, [&]() -> PyObject * {
+        const int index = static_cast<int>(cuda_tensor(a[1], "k_pages").get_device());
+        const c10::cuda::CUDAGuard device(static_cast<c10::DeviceIndex>(index));
+        const qsa_kv_pages kv = pages(a[1], a[2], a[8], a[9], index);
+        const ScalarType cells = THPVariable_Unpack(a[1]).scalar_type();
+        const Tensor &q = cells == at::kChar ? checked(a[0], "q", {at::kFloat, at::kHalf, at::kBFloat16}, 3, index)
+                                             : checked(a[0], "q", {cells}, 3, index);
+        const int nseq = size32(q.size(0), "nseq"), nheads = size32(q.size(1), "nheads");
+        if (q.size(2) != QSA_D || nheads < 1 || kv.nkv < 1 || nheads % kv.nkv != 0)
+            refuse("q must be [nseq, a multiple of %d, %d]", kv.nkv, QSA_D);
+        const Tensor &prefix = checked(a[3], "prefix_table", {at::kInt}, 2, index);
+        const Tensor &prefix_lens = checked(a[4], "prefix_lens", {at::kInt}, 1, index), &cu = checked(a[5], "cu_seqs", {at::kInt}, 1, index);
+        const Tensor &table = checked(a[6], "page_table", {at::kInt}, 2, index), &lens = checked(a[7], "lens", {at::kInt}, 1, index);
+        if (prefix_lens.size(0) != prefix.size(0)) refuse("prefix_table and prefix_lens must have one row per group");
+        if (cu.size(0) != prefix.size(0) + 1) refuse("cu_seqs must have one more element than there are groups");
+        if (table.size(0) != nseq || lens.size(0) != nseq) refuse("page_table and lens must have one row per query");
+        const int ngroups = size32(prefix.size(0), "groups"), pcols = size32(prefix.size(1), "prefix_table's width");
+        const int cols = size32(table.size(1), "page_table's width");
+        const float scale = real(a[10]);
+        const Tensor out = made(a[11], "out", {nseq, nheads, QSA_D}, q.scalar_type(), index);
+        const Tensor lse = made(a[12], "lse", {nseq, nheads}, at::kFloat, index);
+        const size_t need = qsa_prefix_attn_scratch_bytes(nseq, ngroups, nheads, kv.nkv, pcols, cols, kv.page_size);
+        const Scratch scratch = scratch_of(a[13], need, index);
+        const qsa_status status = qsa_prefix_attn(
+            q.data_ptr(), kind(q), stride(q, 0), stride(q, 1), nseq, nheads, &kv, prefix.data_ptr<int32_t>(), pcols,
+            row_stride(prefix), prefix_lens.data_ptr<int32_t>(), cu.data_ptr<int32_t>(), ngroups, table.data_ptr<int32_t>(), cols,
+            row_stride(table), lens.data_ptr<int32_t>(), scale, out.data_ptr(), lse.data_ptr<float>(), scratch.ptr, scratch.bytes,
+            current_stream(index));
+        return status == QSA_OK ? tuple({out, lse}) : PyLong_FromLong(status);
+    });
+}
+
 // positions (None where `own_positions`), freqs, axis, interleaved, inverse of `ntok` tokens
 qsa_rotation rotation_of(PyObject *positions, PyObject *freqs, PyObject *axis, PyObject *interleaved, PyObject *inverse,
                          bool own_positions, int ntok, int index) {
@@ -450,6 +484,7 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 PyMethodDef methods[] = {
     {"rotate", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rotate)), METH_FASTCALL, nullptr},
+    {"prefix_attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefix_attn)), METH_FASTCALL, nullptr},
     {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
     {"paged_attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attn)), METH_FASTCALL, nullptr},
     {"window_attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(window_attn)), METH_FASTCALL, nullptr},

@@ -156,6 +156,48 @@ qsa_status qsa_paged_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride
     return from_cuda(qsa::launch_paged_attn(a, stream));
 }
 
+size_t qsa_prefix_attn_scratch_bytes(int nseq, int ngroups, int nheads, int nkv, int prefix_cols, int table_cols,
+                                     int page_size) {
+    if (nseq < 1 || ngroups < 0 || nheads < 1 || nkv < 1 || nheads % nkv != 0 || prefix_cols < 0 || table_cols < 0 ||
+        page_size < 1 || nseq > MAX_SEQS || ngroups > MAX_SEQS || nheads > MAX_HEADS || nheads / nkv > 128 ||
+        static_cast<long long>(prefix_cols) * page_size > MAX_CELLS || static_cast<long long>(table_cols) * page_size > MAX_CELLS)
+        return 0;
+    return qsa::prefix_attn_scratch_bytes({nseq, ngroups, nheads, nkv, prefix_cols * page_size, table_cols * page_size});
+}
+
+qsa_status qsa_prefix_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride, int64_t q_head_stride, int nseq,
+                           int nheads, const qsa_kv_pages *kv, const int32_t *prefix_table, int prefix_cols,
+                           int64_t prefix_stride, const int32_t *prefix_lens, const int32_t *cu_seqs, int ngroups,
+                           const int32_t *page_table, int table_cols, int64_t table_stride, const int32_t *lens,
+                           float scale, void *out, float *lse, void *scratch, size_t scratch_bytes,
+                           cudaStream_t stream) {
+    qsa_status s = check_pages(kv);
+    if (s != QSA_OK) return s;
+    if (nseq < 0 || ngroups < 0 || nheads < 1 || nheads % kv->nkv != 0 || !good_scale(scale)) return QSA_ERR_INVALID;
+    if (kv->dtype == QSA_I8 ? !row_type(q_dtype) : static_cast<int>(q_dtype) != kv->dtype) return QSA_ERR_INVALID;
+    s = check_table(table_cols, table_stride, kv->page_size);
+    if (s != QSA_OK) return s;
+    s = check_table(prefix_cols, prefix_stride, kv->page_size);
+    if (s != QSA_OK) return s;
+    if (!good_stride(q_seq_stride, q_dtype) || !good_stride(q_head_stride, q_dtype)) return QSA_ERR_INVALID;
+    if (nseq == 0) return QSA_OK;
+    const int group = nheads / kv->nkv;
+    if (nseq > MAX_SEQS || ngroups > MAX_SEQS || nheads > MAX_HEADS || group > (q_dtype == QSA_F32 ? 64 : 128) ||
+        static_cast<long long>(nseq) * nheads > MAX_CELLS ||
+        static_cast<long long>(nseq) * nheads * ((static_cast<long long>(table_cols) * kv->page_size + 63) / 64) > MAX_TILES ||
+        static_cast<long long>(nseq + ngroups) * nheads * ((static_cast<long long>(prefix_cols) * kv->page_size + 127) / 128) > MAX_TILES)
+        return QSA_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lens, 4) || !aligned(cu_seqs, 4)) return QSA_ERR_INVALID;
+    if (ngroups > 0 && (!aligned(prefix_lens, 4) || (prefix_cols > 0 && !aligned(prefix_table, 4)))) return QSA_ERR_INVALID;
+    if (lse != nullptr && !aligned(lse, 4)) return QSA_ERR_INVALID;
+    if (table_cols > 0 && !aligned(page_table, 4)) return QSA_ERR_INVALID;
+    const size_t need = qsa_prefix_attn_scratch_bytes(nseq, ngroups, nheads, kv->nkv, prefix_cols, table_cols, kv->page_size);
+    if (need == 0 || !aligned(scratch, 16) || scratch_bytes < need) return QSA_ERR_INVALID;
+    const qsa::PrefixAttnArgs a{q, q_dtype, q_seq_stride, q_head_stride, nseq, nheads, *kv, prefix_table, prefix_cols, prefix_stride,
+                                prefix_lens, cu_seqs, ngroups, page_table, table_cols, table_stride, lens, scale, out, lse, scratch};
+    return from_cuda(qsa::launch_prefix_attn(a, stream));
+}
+
 size_t qsa_window_attn_scratch_bytes(int nseq, int total_q, int max_q, int nheads, int nkv) {
     if (nseq < 1 || total_q < 1 || max_q < 1 || nheads < 1 || nkv < 1 || nheads % nkv != 0) return 0;
     return qsa::window_attn_scratch_bytes(nseq, total_q, nheads, nkv);   // the longest sequence does not matter

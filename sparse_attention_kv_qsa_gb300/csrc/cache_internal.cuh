@@ -48,6 +48,45 @@ struct PagedAttnArgs {
 size_t paged_attn_scratch_bytes(int nseq, int nheads, int nkv, int capacity, bool with_mass);
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t stream);
 
+// Paged attention's partial results, for another kernel to add: of unit `kvh * parts + part` of sequence s, whole in
+// rows [nseq][nheads][132] where meta[s * units + unit].x < 0, else in ranges of slots as its join reads them
+// (128 sums, reference in base 2, weights' sum). Sequences without a cell leave nothing.
+struct PagedPartial {
+    const float *rows, *slots;
+    const int4 *meta;
+    int parts, units, heads_per_unit, grid;
+};
+
+size_t paged_partial_bytes(int nseq, int nheads, int nkv, int capacity);
+cudaError_t launch_paged_partial(const PagedAttnArgs &a, PagedPartial &left, cudaStream_t stream);
+
+struct PrefixAttnArgs {
+    const void *q;
+    qsa_dtype q_dtype;
+    int64_t q_seq_stride, q_head_stride;
+    int nseq, nheads;
+    qsa_kv_pages kv;
+    const int32_t *prefix_table;
+    int prefix_cols;
+    int64_t prefix_stride;
+    const int32_t *prefix_lens, *cu;
+    int ngroups;
+    const int32_t *table;
+    int table_cols;
+    int64_t table_stride;
+    const int32_t *lens;
+    float scale;
+    void *out;
+    float *lse;
+    void *scratch;
+};
+struct PrefixAttnSizes {
+    int nseq, ngroups, nheads, nkv, prefix_capacity, capacity;
+};
+
+size_t prefix_attn_scratch_bytes(const PrefixAttnSizes &z);
+cudaError_t launch_prefix_attn(const PrefixAttnArgs &a, cudaStream_t stream);
+
 struct WindowAttnArgs {
     const void *q, *k, *v;
     qsa_dtype dtype;

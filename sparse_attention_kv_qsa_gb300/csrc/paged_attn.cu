@@ -74,6 +74,7 @@ struct Params {
     float *slots;     // [2 grid][heads of a unit][SLOT_ROW]
     int by_unit;      // no more units than ranges: a place in meta is a unit, else a range
     int4 *meta;       // sequence, unit, first range, last range of the unit to join there, or -1
+    float *rows;      // [nseq][nheads][SLOT_ROW]: partial results of whole units (kPart)
     float *lse2;      // [nseq][nheads], or null
     float *logits;    // [nseq][nheads][stride], or null
 };
@@ -206,7 +207,10 @@ struct Cursor {
     }
 };
 
-template <int kKv, typename QT, int kMT>
+// kPart: the results stay partial sums (rows, slots), and meta has a place for every unit: another
+// kernel adds them to what it has. It is then launched behind a kernel that its results do not depend on, and
+// which let it start only after it had waited for its own predecessors: it waits for that one at its end alone.
+template <int kKv, typename QT, int kMT, bool kPart>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __grid_constant__ Params p) {
     using F = Form<kKv>;
     using O = typename F::O;
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     const int r = lane >> 2, t = lane & 3;
     const PagedAttnArgs &a = p.a;
 
-    grid_dependency_wait();
+    if (!kPart) grid_dependency_wait();
     grid_launch_dependents();
 
     // ---- this CTA's range of tiles -------------------------------------------------
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
         sh_tile = static_cast<int>(in_seq % n);
     }
     // Sequences without a visible cell have no tile: their rows are written here.
-    for (int s = blockIdx.x; s < a.nseq; s += gridDim.x) {
+    for (int s = blockIdx.x; !kPart && s < a.nseq; s += gridDim.x) {
         if ((s == blockIdx.x ? own_n : visible(p, s).n) > 0) continue;
         for (int e = tid; e < a.nheads * 32; e += THREADS)
             store4(static_cast<QT *>(a.out) + static_cast<size_t>(s) * a.nheads * 128 + 4 * e, make_float4(0.f, 0.f, 0.f, 0.f));
@@ -289,7 +293,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
             for (int u = tid; u < p.units; u += THREADS) p.meta[s * p.units + u] = make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
-    if (sh_seq < 0) return;
+    if (sh_seq < 0) {
+        if (kPart) grid_dependency_wait();
+        return;
+    }
 
     unsigned char *side_base = smem + WARPS * F::RING;
     float *merge_m = reinterpret_cast<float *>(side_base + WARPS * F::STAGES * F::SIDE);
@@ -668,7 +675,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 y.z = fmaf(z.z, f, y.z);
                 y.w = fmaf(z.w, f, y.w);
             }
-            if (whole) {
+            if (whole && !kPart) {
                 const size_t out_row = static_cast<size_t>(s) * a.nheads + h0 + h;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 store4(static_cast<QT *>(a.out) + out_row * 128 + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
@@ -678,7 +685,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                     if (p.lse2 != nullptr) p.lse2[out_row] = e;
                 }
             } else {
-                float *sp = p.slots + (static_cast<size_t>(slot) * HEADS_PER_UNIT + h) * SLOT_ROW;
+                float *sp = kPart && whole ? p.rows + (static_cast<size_t>(s) * a.nheads + h0 + h) * SLOT_ROW
+                                           : p.slots + (static_cast<size_t>(slot) * HEADS_PER_UNIT + h) * SLOT_ROW;
                 *reinterpret_cast<float4 *>(sp + 4 * lane) = y;
                 if (lane == 0) {
                     sp[128] = top;
@@ -700,6 +708,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
         }
         __syncthreads();   // the stages are free again
     }
+    if (kPart) grid_dependency_wait();
 }
 
 // Adds the partial results of one unit's ranges for one head: of W warps, warp w
@@ -903,10 +912,10 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaS
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int kKv, typename QT, int kMT>
-cudaError_t run(const Params &p, int grid, cudaStream_t stream) {
+template <int kKv, typename QT, int kMT, bool kPart>
+cudaError_t run_kernel(const Params &p, int grid, cudaStream_t stream) {
     constexpr int smem = smem_bytes<kKv, kMT>();
-    auto kernel = paged_kernel<kKv, QT, kMT>;
+    auto kernel = paged_kernel<kKv, QT, kMT, kPart>;
     static thread_local int configured_device = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -914,7 +923,12 @@ cudaError_t run(const Params &p, int grid, cudaStream_t stream) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess) configured_device = dev;
     }
-    if (e == cudaSuccess) e = launch(kernel, dim3(grid), THREADS, smem, stream, p);
+    return e == cudaSuccess ? launch(kernel, dim3(grid), THREADS, smem, stream, p) : e;
+}
+
+template <int kKv, typename QT, int kMT>
+cudaError_t run(const Params &p, int grid, cudaStream_t stream) {
+    cudaError_t e = run_kernel<kKv, QT, kMT, false>(p, grid, stream);
     const int ranges = static_cast<int>(grid / (static_cast<long long>(p.a.nseq) * p.units)) + 1;   // of a unit, on average
     const int join_threads = 32 * (ranges <= 4 ? 1 : ranges <= 16 ? 4 : JOIN_WARPS);
     const int places = p.by_unit ? p.a.nseq * p.units : grid;
@@ -930,17 +944,57 @@ size_t paged_attn_scratch_bytes(int nseq, int nheads, int nkv, int capacity, boo
     return layout(nseq, nheads, nkv, capacity, with_mass).bytes;
 }
 
-cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t stream) {
-    Params p;
+namespace {
+// What a launch needs but its scratch; returns the heads of a unit.
+int prepare(Params &p, const PagedAttnArgs &a) {
+    p = {};
     p.a = a;
     p.capacity = a.table_cols * a.kv.page_size;
-    const Layout y = layout(a.nseq, a.nheads, a.kv.nkv, p.capacity, a.mass != nullptr);
     p.page = make_divider(a.kv.page_size);
     p.group = a.nheads / a.kv.nkv;
-    const bool int8 = a.kv.dtype == QSA_I8;
-    const int heads = heads_per_unit(a.nseq, p.group, a.kv.nkv, p.capacity, int8);
+    const int heads = heads_per_unit(a.nseq, p.group, a.kv.nkv, p.capacity, a.kv.dtype == QSA_I8);
     p.parts = (p.group + heads - 1) / heads;
     p.units = a.kv.nkv * p.parts;
+    return heads;
+}
+// Partial results: rows, then a place in meta for every unit, then as layout().
+size_t partial_rows_bytes(int nseq, int nheads) { return (sizeof(float) * nseq * static_cast<size_t>(nheads) * SLOT_ROW + 255) / 256 * 256; }
+size_t partial_meta_bytes(int nseq, int nheads, int nkv) {
+    return (sizeof(int4) * nseq * static_cast<size_t>(nkv) * ((nheads / nkv + 7) / 8) + 255) / 256 * 256;
+}
+}  // namespace
+
+size_t paged_partial_bytes(int nseq, int nheads, int nkv, int capacity) {
+    return partial_rows_bytes(nseq, nheads) + partial_meta_bytes(nseq, nheads, nkv) + layout(nseq, nheads, nkv, capacity, false).bytes;
+}
+
+cudaError_t launch_paged_partial(const PagedAttnArgs &a, PagedPartial &left, cudaStream_t stream) {
+    Params p;
+    const int heads = prepare(p, a);
+    const Layout y = layout(a.nseq, a.nheads, a.kv.nkv, p.capacity, false);
+    p.by_unit = 1;
+    char *b = static_cast<char *>(a.scratch);
+    p.rows = reinterpret_cast<float *>(b);
+    b += partial_rows_bytes(a.nseq, a.nheads);
+    p.meta = reinterpret_cast<int4 *>(b);
+    b += partial_meta_bytes(a.nseq, a.nheads, a.kv.nkv);
+    p.slots = reinterpret_cast<float *>(b + y.slots);
+    left = {p.rows, p.slots, p.meta, p.parts, p.units, heads, y.grid};
+    if (p.capacity == 0) return cudaSuccess;   // no sequence has a cell
+    if (a.kv.dtype == QSA_BF16)
+        return heads == 8 ? run_kernel<QSA_BF16, __nv_bfloat16, 1, true>(p, y.grid, stream)
+                          : run_kernel<QSA_BF16, __nv_bfloat16, 2, true>(p, y.grid, stream);
+    if (a.kv.dtype == QSA_F16)
+        return heads == 8 ? run_kernel<QSA_F16, __half, 1, true>(p, y.grid, stream) : run_kernel<QSA_F16, __half, 2, true>(p, y.grid, stream);
+    if (a.q_dtype == QSA_F32) return run_kernel<QSA_I8, float, 1, true>(p, y.grid, stream);
+    if (a.q_dtype == QSA_F16) return run_kernel<QSA_I8, __half, 1, true>(p, y.grid, stream);
+    return run_kernel<QSA_I8, __nv_bfloat16, 1, true>(p, y.grid, stream);
+}
+
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t stream) {
+    Params p;
+    const int heads = prepare(p, a);
+    const Layout y = layout(a.nseq, a.nheads, a.kv.nkv, p.capacity, a.mass != nullptr);
     p.stride = y.stride;
     p.by_unit = static_cast<long long>(a.nseq) * p.units <= y.grid;
     char *b = static_cast<char *>(a.scratch);

@@ -1,0 +1,1203 @@
+// Attention of one new token per sequence where groups of sequences share a
+// long prefix: the prefix's pages are read once for all of a group.
+//
+//   x_hj = log2(e) scale q_h . k_j  over the group's prefix cells, then the sequence's own cells
+//   lse_h = ln 2 log2 sum_j 2^x_hj;  out_h = sum_j 2^(x_hj - log2 sum) v_j
+//
+// What bounds it: the prefix's cells are read once per block of rows, from HBM
+// or L2 (512 bytes a 16-bit cell and KV head), and cost 4 x 128 flops for
+// every row, a row being a sequence times a query head of the KV head. Below some 290
+// rows that is HBM, above it the tensor cores.
+//
+// Three launches: prefix_kernel (this file) leaves each row's partial sums over the
+// prefix, paged attention's kernel those over its own cells (it starts
+// as the first one's CTAs end), and prefix_join_kernel adds them.
+//
+// prefix_kernel (tcgen05). A block is up to two tiles of 128 rows of one group and KV
+// head; block by block, the tiles of 128 prefix cells are numbered over the batch
+// and cut into one equal range per CTA, one CTA per SM, so that any lengths and
+// group sizes fill the GPU. Lengths live on the device: every CTA finds its range
+// itself. 16 warps:
+//
+//   8 softmax warps   two streams of four, a thread owns a row
+//   1 MMA warp        all tcgen05.mma
+//   1 warp            walks the range and publishes its segments (a block's part in this CTA)
+//   4 copy warps      cells by 16-byte asynchronous copies, each row from its own page (any page
+//                     size), into 128-byte-swizzled tiles; int8 cells become binary16 on the way
+//
+// Two streams of softmax keep the tensor cores fed: with more than 128 rows
+// each takes a tile of rows, and both use every tile of cells; with fewer, both have the
+// same rows and take the tiles of cells in turn, and are added at the segment's end.
+// All rows of a block see the same cells, so there are no masks but the last
+// tile's end and pages that are none; those rows arrive as zeros.
+//
+// fp32 queries (int8 cells): a row's query is scaled by a power of two and held as a
+// binary16 number and the remainder times 2^11, in two rows 16 lanes apart of the
+// tile (64 rows a tile), and so are its weights; lanes exchange halves of the
+// products, so that each finds the weights of 64 of the 128 cells.
+#include <algorithm>
+#include <cstring>
+#include <type_traits>
+
+#include "attn_row.cuh"
+#include "cache_internal.cuh"
+#include "qsa_internal.cuh"
+
+namespace qsa {
+namespace {
+
+__device__ uint32_t g_prefix_error;
+
+constexpr int ROWS = 128;                   // rows of a row tile, cells of a cell tile
+constexpr int HALF = ROWS * 128;            // bytes of 128 rows x 64 elements
+constexpr int TILE_BYTES = 2 * HALF;
+constexpr int MMA_WARP = 8, WALK_WARP = 9, COPY_WARP = 12, COPY_WARPS = 4, PTHREADS = 512;
+// 128 registers a thread at launch: 8 softmax warps x 168 + 8 x 88 = 16 x 128.
+constexpr int MORE_REGISTERS = 168, FEW_REGISTERS = 88;
+constexpr int SLOT_ROW = 132;               // 128 sums, reference, weight sum, padding
+constexpr float LAZY = 8.0f;                // log2 of how far the sums may run above their reference
+constexpr int SEGS = 4, SIDES = 4;
+constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
+
+template <int kKv, typename QT>
+struct Form {
+    static constexpr bool kInt8 = kKv == QSA_I8;
+    static constexpr bool kSplit = std::is_same<QT, float>::value;
+    using T = typename std::conditional<kKv == QSA_BF16, __nv_bfloat16, __half>::type;   // operands
+    static constexpr int REAL = kSplit ? 64 : ROWS;      // rows of a tile that are a query head
+    static constexpr int STAGES = kInt8 ? 3 : 5;         // tiles of keys or values
+    static constexpr int RAW = kInt8 ? 3 : 0;            // int8 tiles on their way
+    static constexpr int FLIGHT = kInt8 ? RAW : 4;       // tiles under way per copy warp
+    // Weights are kept 2^7 above their reference where the operand is binary16, whose smallest
+    // numbers they would otherwise reach sooner: 2^(8 + 7) is within its range.
+    static constexpr float LIFT = kKv == QSA_BF16 ? 0.0f : 7.0f;
+};
+
+struct Params {
+    PrefixAttnArgs a;
+    Divider page;
+    int group, seqs;          // query heads per KV head; sequences of a row tile
+    int capacity;             // cells of a row of the prefix table
+    float *slots;             // [2 grid][256][SLOT_ROW]: a segment at a CTA's begin, and its last
+    float *whole;             // [nseq][nheads][SLOT_ROW]: of blocks that fall into one CTA
+    int2 *meta;               // [blocks][nkv]: first slot, last CTA; -1 where whole
+    uint64_t wait_ns;
+    int stall;                // diagnostics only: CTA 0 never signals its first key tile
+};
+
+// A group of sequences.
+struct Group {
+    int first, count, len, tiles, blocks;
+};
+__device__ __forceinline__ Group group_of(const Params &p, int g) {
+    Group x;
+    x.first = min(max(ld_in(p.a.cu + g), 0), p.a.nseq);
+    x.count = min(max(ld_in(p.a.cu + g + 1), x.first), p.a.nseq) - x.first;
+    x.len = min(max(ld_in(p.a.prefix_lens + g), 0), p.capacity);
+    x.tiles = (x.len + ROWS - 1) / ROWS;
+    x.blocks = (x.count + 2 * p.seqs - 1) / (2 * p.seqs);
+    return x;
+}
+
+// A block's part in this CTA.
+struct Segment {
+    int g, kvh, first, count;   // count: sequences of the block, 0 at the range's end
+    int len, t0, t1;            // cells of the prefix; tiles of cells
+    int slot;                   // of the partial results, -1: whole
+};
+
+struct alignas(16) Bars {
+    uint4 mask[SIDES];          // cells of a tile that are there
+    Segment seg[SEGS];
+    uint64_t seg_full[SEGS], seg_empty[SEGS], q_full, q_empty, kv_full[5], kv_empty[5], s_full[2], p_half[2], p_full[2];
+    uint64_t o_full[2], side_full[SIDES], side_empty[SIDES], pair[4], drain;
+    uint32_t tmem, abort;
+};
+struct alignas(16) Scales {                 // of int8 cells
+    float key[SIDES][ROWS], value[SIDES][ROWS], log_value[SIDES][ROWS];
+    float row[2 * ROWS];        // what a row's products are multiplied by
+};
+template <int kKv, typename QT>
+constexpr size_t smem_bytes() {
+    using F = Form<kKv, QT>;
+    return 1024 + (2 + F::STAGES) * static_cast<size_t>(TILE_BYTES) + F::RAW * (TILE_BYTES / 2) + sizeof(Bars) +
+           (F::kInt8 ? sizeof(Scales) : 0);
+}
+static_assert(smem_bytes<QSA_BF16, __nv_bfloat16>() <= 232448 && smem_bytes<QSA_I8, float>() <= 232448, "shared memory per CTA");
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two fp32 values in one 64-bit register, worked on by one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// a, b as binary16 numbers and what that left of them, times 2^11.
+__device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack<__half>(a, b);
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    lo = pack<__half>((a - h.x) * 2048.0f, (b - h.y) * 2048.0f);
+}
+// Bytes `sel` picks of a word of int8 codes xored with 0x80, as binary16: 0x64 above a byte u is 1024 + u.
+__device__ __forceinline__ uint32_t codes_to_half2(uint32_t w, uint32_t sel) {
+    const uint32_t x = __byte_perm(w, 0x64646464u, sel);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+}
+// Waits until at most n (0 to 3) of this thread's most recent groups are pending.
+__device__ __forceinline__ void cp_async_wait_at_most(int n) {
+    if (n <= 0) cp_async_wait<0>();
+    else if (n == 1) cp_async_wait<1>();
+    else if (n == 2) cp_async_wait<2>();
+    else cp_async_wait<3>();
+}
+__device__ __forceinline__ void arrive(uint64_t *bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// 16-byte chunk c (of 16) of row r of a tile: two halves of 64 elements, 128-byte rows, chunks swizzled.
+__device__ __forceinline__ uint32_t tile_at(int r, int c) { return (c >> 3) * HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
+
+template <int kKv, typename QT>
+__global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_constant__ Params p) {
+    using F = Form<kKv, QT>;
+    using T = typename F::T;
+    constexpr bool kInt8 = F::kInt8, kSplit = F::kSplit;
+    constexpr int STAGES = F::STAGES;
+    extern __shared__ unsigned char raw_smem[];
+    __shared__ long long sh_scan[PTHREADS / 32];
+    __shared__ int sh_group;
+    __shared__ long long sh_inside;             // the range's first tile, counted in its group
+    const PrefixAttnArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(FULL_MASK, tid >> 5, 0);   // the same for the warp, as the compiler now knows
+    const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const uint32_t ring = base + 2 * TILE_BYTES, raws = ring + STAGES * TILE_BYTES;
+    Bars *bars = reinterpret_cast<Bars *>(raw_smem + (raws + F::RAW * (TILE_BYTES / 2) - smem_u32(raw_smem)));
+    Scales *scales = reinterpret_cast<Scales *>(bars + 1);   // int8 cells only
+
+    if (warp == MMA_WARP) {
+        tmem_alloc(&bars->tmem, TMEM_COLS);
+        tmem_relinquish();
+    } else if (tid == 0) {
+        for (int i = 0; i < SEGS; ++i) {
+            mbar_init(&bars->seg_full[i], 1);
+            mbar_init(&bars->seg_empty[i], 1 + 8 + COPY_WARPS);
+        }
+        mbar_init(&bars->q_full, COPY_WARPS);
+        mbar_init(&bars->q_empty, 8);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&bars->kv_full[i], COPY_WARPS);
+            mbar_init(&bars->kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_half[i], 4);
+            mbar_init(&bars->p_full[i], 4);
+            mbar_init(&bars->o_full[i], 1);
+        }
+        for (int i = 0; i < SIDES; ++i) {
+            mbar_init(&bars->side_full[i], COPY_WARPS);
+            mbar_init(&bars->side_empty[i], 8);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&bars->pair[i], 2);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        sh_group = -1;
+        fence_mbar_init();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ---- this CTA's range of tiles -------------------------------------------------
+    const int each = (a.ngroups + PTHREADS - 1) / PTHREADS;
+    const int g0 = min(tid * each, a.ngroups), g1 = min(g0 + each, a.ngroups);
+    auto tiles_in = [&](const Group &x) { return static_cast<long long>(x.tiles) * x.blocks * a.kv.nkv; };
+    long long mine = 0;
+    for (int g = g0; g < g1; ++g) mine += tiles_in(group_of(p, g));
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(FULL_MASK, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) sh_scan[warp] = before;
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    long long all = 0;
+#pragma unroll
+    for (int w = 0; w < PTHREADS / 32; ++w) {
+        if (w < warp) before += sh_scan[w];
+        all += sh_scan[w];
+    }
+    before -= mine;
+    const long long per = (all + gridDim.x - 1) / gridDim.x;
+    const long long x0 = per * blockIdx.x, x1 = min(x0 + per, all);
+    if (x0 < x1 && x0 >= before && x0 < before + mine) {
+        long long b = before;
+        int g = g0;
+        for (long long n = tiles_in(group_of(p, g)); x0 >= b + n; n = tiles_in(group_of(p, g))) {
+            b += n;
+            ++g;
+        }
+        sh_group = g;
+        sh_inside = x0 - b;
+    }
+    __syncthreads();
+    const uint32_t tmem = bars->tmem;
+
+    // A wait of the pipeline: the first that runs out sets the error word, and
+    // all later ones return at once.
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
+        volatile uint32_t *ab = &bars->abort;
+        if (*ab == 0u && mbar_wait(bar, parity, p.wait_ns, ab)) return true;
+        if (*ab == 0u) {
+            *ab = 1u;
+            atomicOr(&g_prefix_error, 1u);
+        }
+        return false;
+    };
+    auto wait_warp = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL_MASK, wait(bar, parity)); };
+    auto ready_warp = [&](uint64_t *bar, uint32_t parity) { return __all_sync(FULL_MASK, mbar_try_wait(bar, parity)); };
+
+    if (warp == WALK_WARP) {
+        fewer_registers<FEW_REGISTERS>();
+        // ---- the segments of the range ----------------------------------------------------
+        long long left = sh_group < 0 ? 0 : x1 - x0;
+        int g = max(sh_group, 0);
+        Group x = {};
+        int kvh = 0, b = 0, t = 0;
+        if (left > 0) {
+            x = group_of(p, g);
+            const long long unit = sh_inside / x.tiles;
+            t = static_cast<int>(sh_inside - unit * x.tiles);
+            kvh = static_cast<int>(unit / x.blocks);
+            b = static_cast<int>(unit - static_cast<long long>(kvh) * x.blocks);
+        }
+        for (uint32_t k = 0;; ++k) {
+            Segment s = {};
+            if (left > 0) {
+                const int n = static_cast<int>(min(static_cast<long long>(x.tiles - t), left));
+                s.g = g;
+                s.kvh = kvh;
+                s.first = x.first + b * 2 * p.seqs;
+                s.count = min(2 * p.seqs, x.first + x.count - s.first);
+                s.len = x.len;
+                s.t0 = t;
+                s.t1 = t + n;
+                const bool whole = n == x.tiles;
+                s.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (k == 0 ? 0 : 1);
+                if (t == 0 && lane == 0) {
+                    // Where the join finds the block: its first tile is tile `at` of the batch.
+                    const long long at = x1 - left;
+                    p.meta[static_cast<size_t>(x.first / (2 * p.seqs) + g + b) * a.kv.nkv + kvh] =
+                        whole ? make_int2(-1, 0) : make_int2(s.slot, static_cast<int>((at + x.tiles - 1) / per));
+                }
+                left -= n;
+                t = 0;
+                if (++b == x.blocks) {
+                    b = 0;
+                    if (++kvh == a.kv.nkv) {
+                        kvh = 0;
+                        // The next group that has tiles: 32 at a time.
+                        for (int from = g + 1; left > 0; from += 32) {
+                            const bool have = from + lane < a.ngroups && tiles_in(group_of(p, from + lane)) > 0;
+                            const uint32_t found = __ballot_sync(FULL_MASK, have);
+                            if (found != 0u) {
+                                g = from + __ffs(found) - 1;
+                                x = group_of(p, g);
+                                break;
+                            }
+                            if (from >= a.ngroups) left = 0;   // not reached: what is left lies in some group
+                        }
+                    }
+                }
+            }
+            if (!wait_warp(&bars->seg_empty[k % SEGS], ((k / SEGS) & 1) ^ 1)) break;
+            if (lane == 0) {
+                bars->seg[k % SEGS] = s;
+                mbar_arrive(&bars->seg_full[k % SEGS]);
+            }
+            __syncwarp();
+            if (s.count == 0) break;
+        }
+    } else if (warp >= COPY_WARP) {
+        fewer_registers<FEW_REGISTERS>();
+        // ---- cells and queries in: rows 32 quarter .. + 31 of every tile ---------------------
+        const int quarter = warp - COPY_WARP;
+        uint32_t issued = 0, done = 0;              // tiles of keys or values (even: keys)
+        uint32_t is = 0, fs = 0;                    // segments begun, and finished with
+        int it = 0, in = 0, ft = 0, fn = 0;         // half tiles issued of segment is - 1 and their number; done of fs - 1
+        bool ok = true, ended = false, q_here = false;
+        Segment s = {}, f = {};                     // segments is - 1 and fs - 1
+        int next_page = -1;
+        long long off = 0;                          // of this lane's row, in bytes
+        uint32_t row_mask = 0;                      // rows of the quarter that are there
+        uint32_t masks[2];                          // of tiles on their way
+        uint32_t pair_scale[2];                     // key and value scale of this lane's row
+        int tiles_in_flight = 0;
+        auto page_of = [&](int cell) {
+            return cell < s.len ? ld_in(a.prefix_table + s.g * a.prefix_stride + divide(p.page, cell)) : -1;
+        };
+        // The queries of segment f: 16-byte pieces, zeros where there is no sequence.
+        auto load_queries = [&](const Segment &w) {
+            const int n0 = min(p.seqs, w.count), tiles = w.count > p.seqs ? 2 : 1;
+            if constexpr (!kInt8) {
+                for (int i = 0; i < tiles; ++i) {
+                    const int rows = (i == 0 ? n0 : w.count - n0) * p.group, mine_row = 32 * quarter + lane;
+                    const int seq = mine_row / p.group;
+                    const long long at = 2 * ((w.first + i * p.seqs + seq) * a.q_seq_stride +
+                                              (w.kvh * p.group + mine_row - seq * p.group) * a.q_head_stride);
+                    const long long good = mine_row < rows ? at : -1;
+                    const int c = lane & 15;
+#pragma unroll 4
+                    for (int e = 0; e < 16; ++e) {
+                        const int r = 2 * e + (lane >> 4);
+                        const long long ro = __shfl_sync(FULL_MASK, good, r);
+                        cp_async_16_or_zero(base + i * TILE_BYTES + tile_at(32 * quarter + r, c),
+                                            static_cast<const char *>(a.q) + (ro < 0 ? 0 : ro) + 16 * c, ro >= 0);
+                    }
+                }
+            } else {
+                // 16 lanes a row of 128 elements, 8 each; rounded to binary16 times a power of two.
+                constexpr int STEPS = F::REAL / (2 * COPY_WARPS);
+                const float c = a.scale * LOG2E;
+                for (int i = 0; i < tiles; ++i) {
+                    const int rows = (i == 0 ? n0 : w.count - n0) * p.group;
+                    for (int e = 0; e < STEPS; ++e) {
+                        const int r = STEPS * 2 * quarter + 2 * e + (lane >> 4), l = lane & 15;   // of the tile's real rows
+                        const bool have = r < rows;
+                        const int seq = r / p.group;
+                        const QT *qp = static_cast<const QT *>(a.q) + (have ? (w.first + i * p.seqs + seq) * a.q_seq_stride +
+                                                                                  (w.kvh * p.group + r - seq * p.group) * a.q_head_stride : 0) + 8 * l;
+                        float4 u = load4(qp), v = load4(qp + 4);
+                        if (!have) u = v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        float top = fmaxf(fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))),
+                                          fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+                        int ex = 0;
+                        if (top > 0.0f && top < INFINITY) frexpf(top, &ex);
+                        ex = max(-126, min(127, ex));   // both powers are fp32 numbers
+                        const float down = ldexpf(1.0f, -ex);
+                        uint32_t hi[4], lo[4];
+                        split(u.x * down, u.y * down, hi[0], lo[0]);
+                        split(u.z * down, u.w * down, hi[1], lo[1]);
+                        split(v.x * down, v.y * down, hi[2], lo[2]);
+                        split(v.z * down, v.w * down, hi[3], lo[3]);
+                        // A real row r of 64 is rows 32 (r / 16) + r % 16 and 16 further.
+                        const int at = kSplit ? 32 * (r >> 4) + (r & 15) : r;
+                        st_shared_v4(base + i * TILE_BYTES + tile_at(at, l), hi[0], hi[1], hi[2], hi[3]);
+                        if (kSplit) st_shared_v4(base + i * TILE_BYTES + tile_at(at + 16, l), lo[0], lo[1], lo[2], lo[3]);
+                        if (l == 0) {
+                            scales->row[i * ROWS + at] = c * ldexpf(1.0f, ex);
+                            if (kSplit) scales->row[i * ROWS + at + 16] = c * ldexpf(1.0f, ex);
+                        }
+                    }
+                }
+            }
+        };
+        auto can_issue = [&]() {
+            if (ended || issued - done >= F::FLIGHT) return false;
+            if (it == in) {                          // a new segment
+                if (!ready_warp(&bars->seg_full[is % SEGS], (is / SEGS) & 1)) return false;
+                s = bars->seg[is % SEGS];
+                __syncwarp();
+                ++is;
+                if (s.count == 0) {
+                    ended = true;
+                    return false;
+                }
+                it = 0;
+                in = 2 * (s.t1 - s.t0);
+                next_page = page_of(s.t0 * ROWS + 32 * quarter + lane);
+            }
+            return kInt8 || ready_warp(&bars->kv_empty[issued % STAGES], ((issued / STAGES) & 1) ^ 1);
+        };
+        auto issue = [&]() {
+            const bool values = it & 1;
+            if (!values) {
+                const int cell = (s.t0 + (it >> 1)) * ROWS + 32 * quarter + lane;
+                const int page = next_page;
+                next_page = page_of(it + 2 < in ? cell + ROWS : s.len);
+                const bool good = page >= 0 && page < a.kv.npages;
+                const int slot = cell - divide(p.page, cell) * a.kv.page_size;
+                off = good ? (page * a.kv.page_stride + slot * a.kv.cell_stride + s.kvh * a.kv.head_stride) * (kInt8 ? 1 : 2) : 0;
+                row_mask = __ballot_sync(FULL_MASK, good);
+                uint32_t sc = 0;
+                if constexpr (kInt8) {
+                    if (good) {
+                        const long long so = page * a.kv.scale_page_stride + slot * a.kv.scale_cell_stride + s.kvh * a.kv.scale_head_stride;
+                        sc = ld_in_u16(a.kv.k_scale_f16 + so) | static_cast<uint32_t>(ld_in_u16(a.kv.v_scale_f16 + so)) << 16;
+                    }
+                }
+                if (tiles_in_flight == 0) {
+                    masks[0] = row_mask;
+                    pair_scale[0] = sc;
+                } else {
+                    masks[1] = row_mask;
+                    pair_scale[1] = sc;
+                }
+                ++tiles_in_flight;
+            }
+            const char *from = static_cast<const char *>(values ? a.kv.v : a.kv.k);
+            if constexpr (!kInt8) {
+                // The first queries come along with the first keys.
+                if (is == 1 && it == 0) {
+                    load_queries(s);
+                    q_here = true;
+                }
+                const uint32_t to = ring + (issued % STAGES) * TILE_BYTES;
+                const int c = lane & 15;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int r = 2 * e + (lane >> 4);
+                    const long long ro = __shfl_sync(FULL_MASK, off, r);
+                    cp_async_16_or_zero(to + tile_at(32 * quarter + r, c), from + ro + 16 * c, (row_mask >> r) & 1u);
+                }
+            } else {
+                const uint32_t to = raws + (issued % F::RAW) * (TILE_BYTES / 2) + 16 * (32 * quarter * 8 + lane);
+                const int c = lane & 7;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int r = 4 * e + (lane >> 3);
+                    const long long ro = __shfl_sync(FULL_MASK, off, r);
+                    cp_async_16_or_zero(to + 512 * e, from + ro + 16 * c, (row_mask >> r) & 1u);
+                }
+            }
+            cp_async_commit();
+            ++issued;
+            ++it;
+        };
+        // The oldest tile on its way: waited for, made operands, and signalled.
+        auto finish = [&]() {
+            cp_async_wait_at_most(static_cast<int>(issued - done) - 1);
+            if (ft == fn) {                          // the first of its segment
+                f = bars->seg[fs % SEGS];
+                ++fs;
+                ft = 0;
+                fn = 2 * (f.t1 - f.t0);
+                if (!q_here) {
+                    if (!wait_warp(&bars->q_empty, (fs & 1))) return false;   // of segment fs - 2
+                    load_queries(f);
+                    if (!kInt8) {
+                        cp_async_commit();
+                        cp_async_wait<0>();
+                    }
+                }
+                q_here = false;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->q_full);
+            }
+            const uint32_t tile = done >> 1;
+            if (!(done & 1u)) {
+                if (!wait_warp(&bars->side_empty[tile % SIDES], ((tile / SIDES) & 1) ^ 1)) return false;
+                if (lane == 0) reinterpret_cast<uint32_t *>(&bars->mask[tile % SIDES])[quarter] = masks[0];
+                if constexpr (kInt8) {
+                    const int r = 32 * quarter + lane;
+                    const float vs = __half2float(__ushort_as_half(static_cast<uint16_t>(pair_scale[0] >> 16)));
+                    scales->key[tile % SIDES][r] = __half2float(__ushort_as_half(static_cast<uint16_t>(pair_scale[0] & 0xFFFFu)));
+                    scales->value[tile % SIDES][r] = vs;
+                    // The sums' reference has to be finite, whatever the scale: within binary16's numbers.
+                    scales->log_value[tile % SIDES][r] = __log2f(fminf(fmaxf(fabsf(vs), 5.9604645e-8f), 65504.0f));
+                }
+                masks[0] = masks[1];
+                pair_scale[0] = pair_scale[1];
+                --tiles_in_flight;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->side_full[tile % SIDES]);
+            }
+            if constexpr (kInt8) {
+                if (!wait_warp(&bars->kv_empty[done % STAGES], ((done / STAGES) & 1) ^ 1)) return false;
+                const uint32_t from = raws + (done % F::RAW) * (TILE_BYTES / 2) + 16 * (32 * quarter * 8 + lane);
+                const uint32_t to = ring + (done % STAGES) * TILE_BYTES;
+                const int c = lane & 7;
+#pragma unroll 4
+                for (int e = 0; e < 8; ++e) {
+                    const int r = 32 * quarter + 4 * e + (lane >> 3);
+                    const uint4 v = ld_shared_v4(from + 512 * e);
+                    const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        st_shared_v4(to + tile_at(r, 2 * c + h), codes_to_half2(w[2 * h], 0x4140), codes_to_half2(w[2 * h], 0x4342),
+                                     codes_to_half2(w[2 * h + 1], 0x4140), codes_to_half2(w[2 * h + 1], 0x4342));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && !(p.stall != 0 && blockIdx.x == 0 && done == 0)) mbar_arrive(&bars->kv_full[done % STAGES]);
+            ++done;
+            if (++ft == fn && lane == 0) mbar_arrive(&bars->seg_empty[(fs - 1) % SEGS]);
+            return true;
+        };
+        while (ok) {
+            if (can_issue()) {
+                issue();
+            } else if (issued != done) {
+                ok = finish();
+            } else if (ended) {
+                break;
+            } else if (it == in) {
+                ok = wait_warp(&bars->seg_full[is % SEGS], (is / SEGS) & 1);
+            } else {
+                ok = wait_warp(&bars->kv_empty[issued % STAGES], ((issued / STAGES) & 1) ^ 1);
+            }
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+    } else if (warp == MMA_WARP) {
+        fewer_registers<FEW_REGISTERS>();
+        const bool one = elect_one();   // the warp runs as one, one lane issues
+        constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+        constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+        constexpr uint32_t idesc_v = idesc | (1u << 16);   // second operand contiguous in N
+        bool ok = true;
+        uint32_t kv = 0;                   // tiles of keys or values so far
+        uint32_t ns[2] = {0, 0};           // products S of each stream so far
+        for (uint32_t k = 0; ok; ++k) {
+            if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
+            const Segment s = bars->seg[k % SEGS];
+            __syncwarp();
+            if (one) mbar_arrive(&bars->seg_empty[k % SEGS]);
+            if (s.count == 0) break;
+            const bool two = s.count > p.seqs;
+            const int n = s.t1 - s.t0;
+            if (!wait_warp(&bars->q_full, k & 1)) break;
+            auto scores = [&](auto which, uint32_t q_at, uint32_t slot) {
+                constexpr int i = decltype(which)::value;
+                const uint64_t qd = sw128_kmajor_desc(q_at), kd = sw128_kmajor_desc(ring + slot * TILE_BYTES);
+                tc_fence_after_sync();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint64_t step = (kk >> 2) * (HALF >> 4) + 2 * (kk & 3);
+                    if (one) tc_mma_bf16(tmem + S_COL + 128 * i, qd + step, kd + step, idesc, kk > 0 ? 1u : 0u);
+                }
+                if (one) tc_commit(&bars->s_full[i]);
+                ++ns[i];
+            };
+            auto outputs = [&](auto which, uint32_t slot, bool first) {
+                constexpr int i = decltype(which)::value;
+                const uint32_t p_col = tmem + S_COL + 128 * i, o_col = tmem + O_COL + 128 * i;
+                const uint64_t vd = sw128_mnmajor_desc(ring + slot * TILE_BYTES, HALF);
+                if (!wait_warp(&bars->p_half[i], (ns[i] - 1) & 1)) return false;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    if (one) tc_mma_bf16_ta(o_col, p_col + 8 * kk, vd + 128 * kk, idesc_v, !first || kk > 0 ? 1u : 0u);
+                if (!wait_warp(&bars->p_full[i], (ns[i] - 1) & 1)) return false;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int kk = 4; kk < 8; ++kk)
+                    if (one) tc_mma_bf16_ta(o_col, p_col + 8 * kk, vd + 128 * kk, idesc_v, 1u);
+                return true;
+            };
+            using I0 = std::integral_constant<int, 0>;
+            using I1 = std::integral_constant<int, 1>;
+            for (int j = 0; ok && j <= n; ++j) {
+                const uint32_t kn = kv + 2 * j, vn = kn - 1;        // keys of tile j, values of tile j - 1
+                const uint32_t ks = kn % STAGES, vs = vn % STAGES;
+                if (two) {
+                    if (j > 0) ok = wait_warp(&bars->kv_full[vs], (vn / STAGES) & 1) && outputs(I0(), vs, j == 1);
+                    if (ok && j < n) {
+                        ok = wait_warp(&bars->kv_full[ks], (kn / STAGES) & 1);
+                        if (ok) scores(I0(), base, ks);
+                    }
+                    if (ok && j > 0) ok = outputs(I1(), vs, j == 1);
+                    if (ok && j > 0 && one) tc_commit(&bars->kv_empty[vs]);
+                    if (ok && j < n) {
+                        scores(I1(), base + TILE_BYTES, ks);
+                        if (one) tc_commit(&bars->kv_empty[ks]);
+                    }
+                } else {
+                    // Tile j goes to stream j % 2; the other's last weights are worked out meanwhile.
+                    if (j < n) {
+                        ok = wait_warp(&bars->kv_full[ks], (kn / STAGES) & 1);
+                        if (!ok) break;
+                        if (j & 1) scores(I1(), base, ks);
+                        else scores(I0(), base, ks);
+                        if (one) tc_commit(&bars->kv_empty[ks]);
+                    }
+                    if (j > 0) {
+                        ok = wait_warp(&bars->kv_full[vs], (vn / STAGES) & 1) &&
+                             ((j & 1) ? outputs(I0(), vs, j <= 2) : outputs(I1(), vs, j <= 2));
+                        if (ok && one) tc_commit(&bars->kv_empty[vs]);
+                    }
+                }
+            }
+            kv += 2 * n;
+            if (ok && one) {
+                tc_commit(&bars->o_full[0]);
+                tc_commit(&bars->o_full[1]);
+            }
+        }
+        if (one) tc_commit(&bars->drain);
+        mbar_wait(&bars->drain, 0, p.wait_ns);
+        __syncwarp();
+    } else if (warp > WALK_WARP) {
+        fewer_registers<FEW_REGISTERS>();   // completes the group of four whose registers the softmax takes
+    } else {
+        more_registers<MORE_REGISTERS>();
+        // ---- softmax of one stream, one row per thread --------------------------------------
+        const int i = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+        const uint32_t s_at = tmem + lanes + S_COL + 128 * i;
+        const bool high = lane >= 16;       // fp32 queries: the remainders' rows
+        uint32_t ns = 0, tiles = 0;
+        for (uint32_t k = 0;; ++k) {
+            if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
+            const Segment s = bars->seg[k % SEGS];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->seg_empty[k % SEGS]);
+            if (s.count == 0) break;
+            const bool two = s.count > p.seqs;
+            const int n = s.t1 - s.t0;
+            const int count = !two ? s.count : i == 0 ? p.seqs : s.count - p.seqs;   // sequences of this stream's rows
+            const int real = kSplit ? 16 * quarter + (lane & 15) : row;              // the row among the tile's
+            const int rows = count * p.group;
+            const bool idle = (kSplit ? 16 : 32) * quarter >= rows;                  // a warp without rows
+            float c = a.scale * LOG2E;
+            if constexpr (kInt8) {
+                if (!wait_warp(&bars->q_full, k & 1)) break;
+                c = scales->row[(two ? i : 0) * ROWS + row];
+            }
+            float m = -INFINITY, l = 0.0f;   // m in base 2, LIFT not counted
+            bool any = false, ok = true;
+            for (int j = 0; j < n; ++j) {
+                if (!two && (j & 1) != i) continue;
+                const uint32_t side = (tiles + j) % SIDES;
+                ok = wait_warp(&bars->s_full[i], ns & 1);
+                if (!ok) break;
+                ++ns;
+                if (idle) {
+                    if (lane == 0) {
+                        arrive(&bars->side_empty[side], two ? 1u : 2u);
+                        mbar_arrive(&bars->p_half[i]);
+                        mbar_arrive(&bars->p_full[i]);
+                    }
+                    continue;
+                }
+                ok = wait_warp(&bars->side_full[side], ((tiles + j) / SIDES) & 1);
+                if (!ok) break;
+                tc_fence_after_sync();
+                uint32_t sr[4][32];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) tmem_ld32(s_at + 32 * g, sr[g]);
+                tmem_ld_wait();
+                const uint4 mask = bars->mask[side];
+                const uint32_t bits[4] = {mask.x, mask.y, mask.z, mask.w};
+                constexpr int CHUNKS = kSplit ? 2 : 4;   // of 32 cells that this lane finds the weights of
+                if constexpr (kSplit) {
+                    // Lanes below 16 take cells 0 to 63 of their row, their partners 64 to 127.
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const uint32_t give = high ? sr[g][e] : sr[2 + g][e], keep = high ? sr[2 + g][e] : sr[g][e];
+                            const uint32_t got = __shfl_xor_sync(FULL_MASK, give, 16);
+                            const float hi = __uint_as_float(high ? got : keep), lo = __uint_as_float(high ? keep : got);
+                            sr[g][e] = __float_as_uint(fmaf(lo, 1.0f / 2048.0f, hi));
+                        }
+                }
+                const int from = kSplit && high ? 64 : 0;   // this lane's first cell
+                if constexpr (kInt8) {
+#pragma unroll
+                    for (int g = 0; g < CHUNKS; ++g)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 ks = *reinterpret_cast<const float4 *>(scales->key[side] + from + 32 * g + e);
+                            sr[g][e] = __float_as_uint(__uint_as_float(sr[g][e]) * ks.x);
+                            sr[g][e + 1] = __float_as_uint(__uint_as_float(sr[g][e + 1]) * ks.y);
+                            sr[g][e + 2] = __float_as_uint(__uint_as_float(sr[g][e + 2]) * ks.z);
+                            sr[g][e + 3] = __float_as_uint(__uint_as_float(sr[g][e + 3]) * ks.w);
+                        }
+                }
+                if ((bits[0] & bits[1] & bits[2] & bits[3]) != 0xFFFFFFFFu) {
+#pragma unroll
+                    for (int g = 0; g < CHUNKS; ++g) {
+                        const uint32_t b = kSplit && high ? bits[2 + g % 2] : bits[g];
+                        if (b == 0xFFFFFFFFu) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((b >> e) & 1u)) sr[g][e] = 0xFF800000u;
+                    }
+                }
+                uint64_t sums[2];
+                uint32_t pw[16], pl[16];
+                // Weights of 32 cells against the reference as it stands, so that they need not wait
+                // for the maximum of this tile, which rarely moves it.
+                auto weights = [&](int g) {
+                    const float mc = m == -INFINITY ? 0.0f : m - F::LIFT;
+                    const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float x0, x1;
+                        unpair(fma_pair(pair(__uint_as_float(sr[g][2 * e]), __uint_as_float(sr[g][2 * e + 1])), c2, mc2), x0, x1);
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        sums[e & 1] = g == 0 && e < 2 ? pair(x0, x1) : add_pair(sums[e & 1], pair(x0, x1));
+                        if constexpr (kInt8) {
+                            const float2 vs = *reinterpret_cast<const float2 *>(scales->value[side] + from + 32 * g + 2 * e);
+                            x0 *= vs.x;
+                            x1 *= vs.y;
+                        }
+                        if constexpr (kSplit) split(x0, x1, pw[e], pl[e]);
+                        else pw[e] = pack<T>(x0, x1);
+                    }
+                };
+                if (!kSplit && any) weights(0);
+                float tops[8];
+                if constexpr (kInt8) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) tops[e] = -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < CHUNKS; ++g)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 lv = *reinterpret_cast<const float4 *>(scales->log_value[side] + from + 32 * g + e);
+                            tops[e & 4] = fmaxf(tops[e & 4], fmaf(__uint_as_float(sr[g][e]), c, lv.x));
+                            tops[(e & 4) + 1] = fmaxf(tops[(e & 4) + 1], fmaf(__uint_as_float(sr[g][e + 1]), c, lv.y));
+                            tops[(e & 4) + 2] = fmaxf(tops[(e & 4) + 2], fmaf(__uint_as_float(sr[g][e + 2]), c, lv.z));
+                            tops[(e & 4) + 3] = fmaxf(tops[(e & 4) + 3], fmaf(__uint_as_float(sr[g][e + 3]), c, lv.w));
+                        }
+                } else {
+                    // 8 chains, so that the maximum of 128 is not a chain of 128.
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) tops[e] = __uint_as_float(sr[0][e]);
+#pragma unroll
+                    for (int e = 8; e < 128; e += 16)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float y = __uint_as_float(sr[e >> 5][(e & 31) + q]);
+                            tops[q] = e + 8 < 128 ? fmaxf(fmaxf(tops[q], y), __uint_as_float(sr[(e + 8) >> 5][((e + 8) & 31) + q]))
+                                                  : fmaxf(tops[q], y);
+                        }
+                }
+                float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                                  fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
+                if constexpr (!kInt8) top *= c;
+                if constexpr (kSplit) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 16));
+                const bool move = top - m > LAZY;   // also true from -infinity to a finite maximum
+                if (__any_sync(FULL_MASK, move) || !any) {
+                    const float f = move ? ex2(m - top) : 1.0f;
+                    if (move) m = top;
+                    l *= f;
+                    if (any) {
+                        const uint32_t o_at = tmem + lanes + O_COL + 128 * i;
+#pragma unroll 1
+                        for (int g = 0; g < 8; ++g) {
+                            uint32_t o[16];
+                            tmem_ld16(o_at + 16 * g, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(o_at + 16 * g, o);
+                        }
+                    }
+                    if (!kSplit) weights(0);
+                }
+#pragma unroll
+                for (int g = 0; g < CHUNKS; ++g) {
+                    if (kSplit || g > 0) weights(g);
+                    if constexpr (kSplit) {
+                        // The row of rounded weights gets the partner's for cells 64 on, the row of remainders those below.
+                        uint32_t first[16], second[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint32_t got = __shfl_xor_sync(FULL_MASK, high ? pw[e] : pl[e], 16);
+                            first[e] = high ? got : pw[e];
+                            second[e] = high ? pl[e] : got;
+                        }
+                        tmem_st16(s_at + 16 * g, first);
+                        tmem_st16(s_at + 32 + 16 * g, second);
+                    } else {
+                        tmem_st16(s_at + 16 * g, pw);
+                    }
+                    if (g == CHUNKS - 1 || (!kSplit && g == 1)) {   // the products with half of the values can begin
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (kSplit || g == 1) mbar_arrive(&bars->p_half[i]);
+                            if (g == CHUNKS - 1) {
+                                mbar_arrive(&bars->p_full[i]);
+                                arrive(&bars->side_empty[side], two ? 1u : 2u);
+                            }
+                        }
+                    }
+                }
+                {
+                    float y0, y1;
+                    unpair(add_pair(sums[0], sums[1]), y0, y1);
+                    l += y0 + y1;
+                }
+                any = true;
+            }
+            tiles += n;
+            if (!ok) break;
+            // ---- the segment's results ---------------------------------------------------------
+            if constexpr (kSplit) l += __shfl_xor_sync(FULL_MASK, l, 16);
+            float2 sum = make_float2(m == -INFINITY ? -INFINITY : m - F::LIFT, l);
+            float f0 = 1.0f, f1 = 1.0f;
+            bool any0 = any, any1 = any;
+            if (!(wait_warp(&bars->o_full[0], k & 1) && wait_warp(&bars->o_full[1], k & 1))) break;
+            if (!two) {
+                // Both streams have the same rows: their sums through the second query tile, which nothing uses.
+                float4 *shared = reinterpret_cast<float4 *>(raw_smem + (base + TILE_BYTES - smem_u32(raw_smem)));
+                shared[i * ROWS + row] = make_float4(sum.x, sum.y, any ? 1.0f : 0.0f, 0.0f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->pair[quarter]);
+                if (!wait_warp(&bars->pair[quarter], k & 1)) break;
+                const float4 o0 = shared[row], o1 = shared[ROWS + row];
+                const float top = fmaxf(o0.x, o1.x), ref = top == -INFINITY ? 0.0f : top;
+                f0 = ex2(o0.x - ref);
+                f1 = ex2(o1.x - ref);
+                any0 = o0.z != 0.0f;
+                any1 = o1.z != 0.0f;
+                sum = make_float2(top, fmaf(o0.y, f0, o1.y * f1));
+            } else if (lane == 0) {
+                mbar_arrive(&bars->pair[quarter]);   // a phase of each segment
+            }
+            tc_fence_after_sync();
+            if (!idle) {
+                const int seq = real / p.group, head = real - seq * p.group;
+                const bool valid = real < rows && !(kSplit && high);
+                const long long out_row = static_cast<long long>(s.first + (two ? i * p.seqs : 0) + seq) * a.nheads + s.kvh * p.group + head;
+                float *to = s.slot < 0 ? p.whole + out_row * SLOT_ROW
+                                       : p.slots + (static_cast<size_t>(s.slot) * 2 * ROWS + (two ? i * ROWS : 0) + real) * SLOT_ROW;
+                const uint32_t live = __ballot_sync(FULL_MASK, valid);
+                // A piece of 32 columns is staged in this stream's query tile with its 16-byte chunks at
+                // chunk ^ (row % 8) and leaves as whole 128-byte rows.
+                const uint32_t stage = base + (two ? i * TILE_BYTES : 0) + (two ? quarter : warp) * 4096;
+                char *row_to[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    row_to[e] = reinterpret_cast<char *>(__shfl_sync(FULL_MASK, reinterpret_cast<unsigned long long>(to), 4 * e + (lane >> 3))) + 16 * (lane & 7);
+                const int piece0 = two ? 0 : 2 * i, piece1 = two ? 4 : 2 * i + 2;   // with the same rows, half of the columns each
+#pragma unroll 1
+                for (int piece = piece0; piece < piece1; ++piece) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    if (two) {
+                        tmem_ld32(tmem + lanes + O_COL + 128 * i + 32 * piece, o);
+                        tmem_ld_wait();
+                        if (!any)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    } else {
+                        uint32_t u[32];
+                        tmem_ld32(tmem + lanes + O_COL + 32 * piece, o);
+                        tmem_ld32(tmem + lanes + O_COL + 128 + 32 * piece, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint((any0 ? __uint_as_float(o[e]) * f0 : 0.0f) + (any1 ? __uint_as_float(u[e]) * f1 : 0.0f));
+                    }
+                    if constexpr (kSplit)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(fmaf(__uint_as_float(__shfl_xor_sync(FULL_MASK, o[e], 16)), 1.0f / 2048.0f, __uint_as_float(o[e])));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        st_shared_v4(stage + lane * 128 + ((e ^ (lane & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    __syncwarp();
+                    uint4 v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = 4 * e + (lane >> 3);
+                        v[e] = ld_shared_v4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if ((live >> (4 * e + (lane >> 3))) & 1u) *reinterpret_cast<uint4 *>(row_to[e] + 128 * piece) = v[e];
+                    __syncwarp();
+                }
+                if (valid && (two || i == 0)) *reinterpret_cast<float2 *>(to + 128) = sum;
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->q_empty);
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// Adds a row's partial sums: of the prefix, in the order of the CTAs that hold them, and of the
+// sequence's own cells, as paged attention left them. A CTA takes a sequence and a query head.
+constexpr int JOIN_WARPS = 8, JOIN_BATCH = 4;
+template <typename QT>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __grid_constant__ Params p, const PagedPartial own, int grid) {
+    const PrefixAttnArgs &a = p.a;
+    const int s = blockIdx.x, h = blockIdx.y, kvh = h / p.group, in_group = h - kvh * p.group;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    // The group that sequence s is of: the last that begins at or before it.
+    int lo = -1, hi = a.ngroups + 1;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, g = lo + (lane + 1) * step;
+        const int below = __popc(__ballot_sync(FULL_MASK, g < hi && min(max(ld_in(a.cu + g), 0), a.nseq) <= s));
+        lo += below * step;
+        hi = min(hi, lo + step);
+    }
+    // Ranges of the prefix: slots c0 (and its part), then those of CTAs c0 + 1 .. c1.
+    int first = 0, n = 0;
+    const float *whole = nullptr;
+    int row = 0;
+    if (lo >= 0 && lo < a.ngroups) {
+        const Group x = group_of(p, lo);
+        if (x.tiles > 0 && s < x.first + x.count) {
+            const int b = (s - x.first) / (2 * p.seqs), in_block = s - x.first - b * 2 * p.seqs;
+            row = in_block < p.seqs ? in_block * p.group + in_group : ROWS + (in_block - p.seqs) * p.group + in_group;
+            const int2 at = __ldcg(p.meta + static_cast<size_t>(x.first / (2 * p.seqs) + lo + b) * a.kv.nkv + kvh);
+            if (at.x < 0) {
+                whole = p.whole + (static_cast<size_t>(s) * a.nheads + h) * SLOT_ROW;
+                n = 1;
+            } else {
+                // Nothing but numbers is taken from scratch: a CTA that gave up may have left anything.
+                first = min(at.x, 2 * grid - 1);
+                n = max(0, min(at.y, grid - 1) - (first >> 1) + 1);
+            }
+        }
+    }
+    // Ranges of the sequence's own cells.
+    const int unit = kvh * own.parts + in_group / own.heads_per_unit, unit_head = in_group % own.heads_per_unit;
+    int4 w = make_int4(-1, 0, 0, -1);
+    int own_n = 0;
+    const int own_len = ld_in(a.lens + s);
+    if (own_len > 0 && a.table_cols > 0) {
+        w = __ldcg(own.meta + static_cast<size_t>(s) * own.units + unit);
+        own_n = 1;
+        if (w.x >= 0) {
+            w.z = max(0, min(w.z, 2 * own.grid - 1));
+            own_n = max(0, min(w.w, own.grid - 1) - (w.z >> 1) + 1);
+        }
+    }
+    const int all = n + own_n;
+    // Range i: its sums, reference and weights' sum.
+    auto place = [&](int i) {
+        if (i < n) return whole != nullptr ? whole : p.slots + (static_cast<size_t>(i == 0 ? first : 2 * ((first >> 1) + i)) * 2 * ROWS + row) * SLOT_ROW;
+        const int e = i - n;
+        if (w.x < 0) return own.rows + (static_cast<size_t>(s) * a.nheads + h) * SLOT_ROW;
+        return own.slots + (static_cast<size_t>(e == 0 ? w.z : 2 * ((w.z >> 1) + e)) * own.heads_per_unit + unit_head) * SLOT_ROW;
+    };
+    float top = -INFINITY, l = 0.0f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = warp; i0 < all; i0 += warps * JOIN_BATCH) {
+        float2 ml[JOIN_BATCH];
+        float4 v[JOIN_BATCH];
+#pragma unroll
+        for (int e = 0; e < JOIN_BATCH; ++e) {
+            const int i = i0 + warps * e;
+            ml[e] = make_float2(-INFINITY, 0.0f);
+            v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < all) {
+                const float *at = place(i);
+                ml[e] = __ldcg(reinterpret_cast<const float2 *>(at + 128));
+                v[e] = ld_in(reinterpret_cast<const float4 *>(at) + lane);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < JOIN_BATCH; ++e) {
+            const float t = fmaxf(top, ml[e].x), b = t == -INFINITY ? 0.0f : t;
+            const float f = ex2(top - b), g = ex2(ml[e].x - b);
+            top = t;
+            l = fmaf(ml[e].y, g, l * f);
+            y.x = fmaf(v[e].x, g, y.x * f);
+            y.y = fmaf(v[e].y, g, y.y * f);
+            y.z = fmaf(v[e].z, g, y.z * f);
+            y.w = fmaf(v[e].w, g, y.w * f);
+        }
+    }
+    __shared__ float4 sum[JOIN_WARPS][32];
+    __shared__ float2 weight[JOIN_WARPS];
+    if (warps > 1) {
+        sum[warp][lane] = y;
+        if (lane == 0) weight[warp] = make_float2(top, l);
+        __syncthreads();
+        if (warp > 0) return;
+        for (int o = 1; o < warps; ++o) {
+            const float2 ml = weight[o];
+            const float4 v = sum[o][lane];
+            const float t = fmaxf(top, ml.x), b = t == -INFINITY ? 0.0f : t;
+            const float f = ex2(top - b), g = ex2(ml.x - b);
+            top = t;
+            l = fmaf(ml.y, g, l * f);
+            y.x = fmaf(v.x, g, y.x * f);
+            y.y = fmaf(v.y, g, y.y * f);
+            y.z = fmaf(v.z, g, y.z * f);
+            y.w = fmaf(v.w, g, y.w * f);
+        }
+    }
+    const size_t out_row = static_cast<size_t>(s) * a.nheads + h;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    store4(static_cast<QT *>(a.out) + out_row * 128 + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+    if (lane == 0 && a.lse != nullptr) a.lse[out_row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * LN2;
+}
+
+int seqs_of(int group, bool split) { return (split ? 64 : 128) / group; }
+
+struct Layout {
+    size_t meta, whole, slots, own, bytes;
+    int grid;
+};
+// q_fp32 only changes how many sequences a row tile takes: the scratch is laid out for the smaller number.
+Layout layout(const PrefixAttnSizes &z) {
+    Layout y;
+    const int seqs = std::max(1, seqs_of(z.nheads / z.nkv, true));
+    const long long blocks = z.nseq / (2 * seqs) + z.ngroups + 1;
+    const long long tiles = (static_cast<long long>(z.prefix_capacity) + ROWS - 1) / ROWS * blocks * z.nkv;
+    y.grid = static_cast<int>(std::max(1LL, std::min<long long>(device_sm_count(), tiles)));
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    size_t at = 0;
+    y.meta = at;
+    at += up(sizeof(int2) * blocks * z.nkv);
+    y.whole = at;
+    at += up(sizeof(float) * z.nseq * static_cast<size_t>(z.nheads) * SLOT_ROW);
+    y.slots = at;
+    at += up(sizeof(float) * 2 * y.grid * 2 * ROWS * SLOT_ROW);
+    y.own = at;
+    at += paged_partial_bytes(z.nseq, z.nheads, z.nkv, z.capacity);
+    y.bytes = at;
+    return y;
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int kKv, typename QT>
+cudaError_t run(Params &p, const Layout &y, const PagedAttnArgs &own_args, cudaStream_t stream) {
+    constexpr size_t smem = smem_bytes<kKv, QT>();
+    auto kernel = prefix_kernel<kKv, QT>;
+    static thread_local int configured_device = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && configured_device != dev) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e == cudaSuccess) configured_device = dev;
+    }
+    p.seqs = seqs_of(p.group, Form<kKv, QT>::kSplit);
+    if (e == cudaSuccess) e = launch(kernel, dim3(y.grid), PTHREADS, smem, stream, p);
+    // Ranges of a block, on average.
+    const int ranges = y.grid / (p.a.kv.nkv * std::max(1, std::max(p.a.ngroups, p.a.nseq / (2 * p.seqs)))) + 1;
+    const int join_warps = ranges <= 4 ? 1 : ranges <= 16 ? 4 : JOIN_WARPS;
+    PagedPartial own;
+    if (e == cudaSuccess) e = launch_paged_partial(own_args, own, stream);
+    if (e == cudaSuccess)
+        e = launch(prefix_join_kernel<QT>, dim3(p.a.nseq, p.a.nheads), 32 * join_warps, 0, stream, p, own, y.grid);
+    return e;
+}
+
+}  // namespace
+
+size_t prefix_attn_scratch_bytes(const PrefixAttnSizes &z) { return layout(z).bytes; }
+
+cudaError_t launch_prefix_attn(const PrefixAttnArgs &a, cudaStream_t stream) {
+    Params p = {};
+    p.a = a;
+    p.page = make_divider(a.kv.page_size);
+    p.group = a.nheads / a.kv.nkv;
+    p.capacity = a.prefix_cols * a.kv.page_size;
+    const Layout y = layout({a.nseq, a.ngroups, a.nheads, a.kv.nkv, p.capacity, a.table_cols * a.kv.page_size});
+    char *b = static_cast<char *>(a.scratch);
+    p.meta = reinterpret_cast<int2 *>(b + y.meta);
+    p.whole = reinterpret_cast<float *>(b + y.whole);
+    p.slots = reinterpret_cast<float *>(b + y.slots);
+    // Waits last as long as a CTA's whole range may: some 2 us a tile.
+    const long long tiles = (static_cast<long long>(p.capacity) + ROWS - 1) / ROWS * a.kv.nkv * (a.nseq + a.ngroups);
+    p.wait_ns = wait_limit_ns() + 8192ull * static_cast<uint64_t>(std::min(tiles / y.grid + 1, 1LL << 24));
+    p.stall = (debug_inject() & 32u) != 0u;
+    PagedAttnArgs own = {};
+    own.q = a.q;
+    own.q_dtype = a.q_dtype;
+    own.q_seq_stride = a.q_seq_stride;
+    own.q_head_stride = a.q_head_stride;
+    own.nseq = a.nseq;
+    own.nheads = a.nheads;
+    own.kv = a.kv;
+    own.table = a.table;
+    own.table_cols = a.table_cols;
+    own.table_stride = a.table_stride;
+    own.lens = a.lens;
+    own.window = -1;
+    own.scale = a.scale;
+    own.scratch = b + y.own;
+    if (a.kv.dtype == QSA_BF16) return run<QSA_BF16, __nv_bfloat16>(p, y, own, stream);
+    if (a.kv.dtype == QSA_F16) return run<QSA_F16, __half>(p, y, own, stream);
+    if (a.q_dtype == QSA_F32) return run<QSA_I8, float>(p, y, own, stream);
+    if (a.q_dtype == QSA_F16) return run<QSA_I8, __half>(p, y, own, stream);
+    return run<QSA_I8, __nv_bfloat16>(p, y, own, stream);
+}
+
+cudaError_t prefix_error_read_clear(uint32_t *word, cudaStream_t stream) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_prefix_error, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return e;
+    const uint32_t zero = 0u;
+    e = cudaMemcpyToSymbolAsync(g_prefix_error, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
+    if (e != cudaSuccess) return e;
+    return cudaStreamSynchronize(stream);
+}
+
+}  // namespace qsa

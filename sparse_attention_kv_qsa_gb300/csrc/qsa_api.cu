@@ -339,16 +339,17 @@ qsa_status qsa_block_summary(const int8_t *k_cells, const uint16_t *k_scale_f16,
 qsa_status qsa_get_device_error(uint32_t *code, cudaStream_t stream) {
     if (code == nullptr) return QSA_ERR_INVALID;
     *code = 0;
-    uint32_t a = 0, b = 0, c = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0;
     cudaError_t e = qsa::topk_error_read_clear(&a, stream);
     if (e == cudaSuccess) e = qsa::tc_error_read_clear(&b, stream);
     if (e == cudaSuccess) e = qsa::window_error_read_clear(&c, stream);
-    *code = a | (b << 8) | (c << 16);
+    if (e == cudaSuccess) e = qsa::prefix_error_read_clear(&d, stream);
+    *code = a | (b << 8) | (c << 16) | (d << 17);
     return from_cuda(e);
 }
 
 qsa_status qsa_debug_inject(uint32_t faults, uint64_t wait_limit_ns) {
-    if ((faults & ~11u) != 0u || wait_limit_ns == 0 || wait_limit_ns > 60000000000ull) return QSA_ERR_INVALID;
+    if ((faults & ~43u) != 0u || wait_limit_ns == 0 || wait_limit_ns > 60000000000ull) return QSA_ERR_INVALID;
     qsa::g_inject.store(faults, std::memory_order_relaxed);
     qsa::g_wait_limit_ns.store(wait_limit_ns, std::memory_order_relaxed);
     return QSA_OK;

@@ -109,5 +109,7 @@ uint64_t wait_limit_ns();
 uint32_t debug_inject();
 cudaError_t tc_error_read_clear(uint32_t *word, cudaStream_t stream);
 cudaError_t window_error_read_clear(uint32_t *word, cudaStream_t stream);
+// prefix_attn.cu, likewise.
+cudaError_t prefix_error_read_clear(uint32_t *word, cudaStream_t stream);
 
 }  // namespace qsa

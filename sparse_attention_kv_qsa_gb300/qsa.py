@@ -3,8 +3,8 @@
 Every step of the selection runs in ``libqsa.so``'s CUDA kernels; this module
 checks tensor shapes, dtypes and devices, allocates outputs with torch, and
 passes raw device pointers and the current CUDA stream. The paged-cache calls
-(``window_attn``, ``paged_attn``, ``cache_evict``, ``rotate``, ``cache_append``)
-do the same in the compiled module ``qsa_ops.so``, whose checks take a few microseconds less of each call.
+(``window_attn``, ``paged_attn``, ``prefix_attn``, ``cache_evict``, ``rotate``,
+``cache_append``) do the same in the compiled module ``qsa_ops.so``, whose checks take a few microseconds less of each call.
 There is no fallback: if a library is missing, calling the functions raises.
 """
 
@@ -33,7 +33,8 @@ EXPORTED = ("qsa_block_scores", "qsa_block_scores_q8", "qsa_block_scores_ffma", 
             "qsa_block_select_static", "qsa_block_select_small", "qsa_sparse_attn", "qsa_block_summary",
             "qsa_get_device_error", "qsa_debug_inject", "qsa_status_string", "qsa_block_select",
             "qsa_block_select_scratch_bytes", "qsa_paged_attn", "qsa_paged_attn_scratch_bytes", "qsa_window_attn",
-            "qsa_window_attn_scratch_bytes", "qsa_cache_evict", "qsa_rotate", "qsa_cache_append")
+            "qsa_window_attn_scratch_bytes", "qsa_cache_evict", "qsa_rotate", "qsa_cache_append", "qsa_prefix_attn",
+            "qsa_prefix_attn_scratch_bytes")
 
 
 F32, F16, BF16, I8 = 0, 1, 2, 3   # qsa_dtype
@@ -114,6 +115,11 @@ def lib() -> ctypes.CDLL:
         L.qsa_rotate.restype = i
         L.qsa_cache_append.argtypes = [vp, vp, vp, i, ctypes.POINTER(ll), i, i, kv, vp, i, ll, vp, vp, i, rot, vp, vp, vp]
         L.qsa_cache_append.restype = i
+        L.qsa_prefix_attn_scratch_bytes.argtypes = [i, i, i, i, i, i, i]
+        L.qsa_prefix_attn_scratch_bytes.restype = ctypes.c_size_t
+        L.qsa_prefix_attn.argtypes = [vp, i, ll, ll, i, i, kv, vp, i, ll, vp, vp, i, vp, i, ll, vp, f, vp, vp, vp,
+                                      ctypes.c_size_t, vp]
+        L.qsa_prefix_attn.restype = i
         L.qsa_debug_inject.argtypes = [ctypes.c_uint32, ctypes.c_uint64]
         L.qsa_debug_inject.restype = i
         L.qsa_status_string.argtypes = [i]
@@ -525,6 +531,33 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, pa
     return r
 
 
+def prefix_attn_scratch_bytes(nseq: int, ngroups: int, nheads: int, nkv: int, prefix_cols: int, table_cols: int,
+                              page_size: int) -> int:
+    """``qsa_prefix_attn_scratch_bytes``: scratch bytes prefix_attn needs."""
+    return int(lib().qsa_prefix_attn_scratch_bytes(nseq, ngroups, nheads, nkv, prefix_cols, table_cols, page_size))
+
+
+def prefix_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, prefix_table: torch.Tensor,
+                prefix_lens: torch.Tensor, cu_seqs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, *,
+                k_scale_f16: torch.Tensor | None = None, v_scale_f16: torch.Tensor | None = None,
+                scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                scratch: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """``qsa_prefix_attn``: ``(out, lse)`` of one new token per sequence, ``q
+    [nseq, nheads, 128]``, where sequences ``cu_seqs[g] .. cu_seqs[g+1]-1``
+    (group ``g``) share a prefix, the first ``prefix_lens[g]`` cells of the
+    pages ``prefix_table[g]``, and each has ``lens[s]`` cells of its own in the
+    pages ``page_table[s]``: what ``paged_attn`` gives over both, but the prefix
+    is read once for its group. Pages, types and ``scale`` as in
+    ``paged_attn``. ``scratch``: a uint8 tensor of
+    ``prefix_attn_scratch_bytes`` bytes, allocated when not given."""
+    r = (_ops_module or _ops()).prefix_attn(
+        q, k_pages, v_pages, prefix_table, prefix_lens, cu_seqs, page_table, lens, k_scale_f16, v_scale_f16,
+        SOFTMAX_SCALE if scale is None else scale, out, lse, scratch)
+    if r.__class__ is int:
+        raise QSAError(r, "qsa_prefix_attn")
+    return r
+
+
 def window_attn_scratch_bytes(nseq: int, total_q: int, max_q: int, nheads: int, nkv: int) -> int:
     """``qsa_window_attn_scratch_bytes``: scratch bytes window_attn needs."""
     return int(lib().qsa_window_attn_scratch_bytes(nseq, total_q, max_q, nheads, nkv))
@@ -622,6 +655,7 @@ WAIT_LIMIT_DEFAULT_NS = 2_000_000_000
 INJECT_SCORER_STALL = 1    # the tensor-core scorer's CTA 0 never loads its first key piece
 INJECT_DECODE_BARRIER = 2  # the fused decode select's grid barrier waits for one arrival too many
 INJECT_WINDOW_STALL = 8    # the prompt attention's CTA 0 never copies its first key tile
+INJECT_PREFIX_STALL = 32   # the shared prefix's attention's CTA 0 never hands over its first key tile
 
 
 def debug_inject(faults: int, wait_limit_ns: int = WAIT_LIMIT_DEFAULT_NS) -> None:

@@ -140,3 +140,42 @@ def test_reference_codes_by_hand():
     assert s[0] == 1.0 and q[0, :3].tolist() == [127, -64, 0]           # halves to even
     assert s[1] == 0.0 and not q[1].any() and s[2] == 0.0 and not q[2].any()
     assert math.isnan(s[3]) and not q[3].any()
+
+
+def prefix(lib, kv=None, **kw):
+    d = dict(q=A, q_dtype=qsa.BF16, qs=1024, qh=128, nseq=4, nheads=8, pt=A, pcols=4, pstride=4, pl=A, cu=A, ngroups=2, table=A, cols=4,
+             tstride=4, lens=A, scale=0.1, out=A, lse=A, scratch=A, bytes=1 << 40)
+    d.update(kw)
+    return lib.qsa_prefix_attn(d["q"], d["q_dtype"], d["qs"], d["qh"], d["nseq"], d["nheads"], kv or pages(), d["pt"], d["pcols"],
+                               d["pstride"], d["pl"], d["cu"], d["ngroups"], d["table"], d["cols"], d["tstride"], d["lens"], d["scale"],
+                               d["out"], d["lse"], d["scratch"], d["bytes"], None)
+
+
+@pytest.mark.parametrize("bad", BAD_PAGES)
+def test_prefix_bad_pages(lib, bad):
+    assert prefix(lib, pages(**bad)) == INVALID
+
+
+@pytest.mark.parametrize("bad", [dict(nseq=-1), dict(ngroups=-1), dict(nheads=0), dict(nheads=7), dict(scale=0.0), dict(scale=-1.0),
+                                 dict(scale=math.inf), dict(scale=3e38), dict(q_dtype=qsa.F16), dict(q_dtype=qsa.F32), dict(pcols=-1),
+                                 dict(cols=-1), dict(pstride=3), dict(tstride=3), dict(qs=-128), dict(qh=4), dict(q=None), dict(q=MIS),
+                                 dict(out=None), dict(out=MIS), dict(lse=MIS), dict(pt=None), dict(pl=None), dict(cu=None), dict(cu=MIS),
+                                 dict(table=None), dict(lens=None), dict(scratch=None), dict(scratch=A + 4), dict(bytes=0)])
+def test_prefix_argument_errors(lib, bad):
+    assert prefix(lib, **bad) == INVALID
+
+
+def test_prefix_limits(lib):
+    assert prefix(lib, nseq=0, q=None, out=None, lens=None, cu=None, scratch=None, bytes=0) == OK
+    assert prefix(lib, nseq=65536) == UNSUPPORTED
+    assert prefix(lib, ngroups=65536) == UNSUPPORTED
+    assert prefix(lib, nheads=65536) == UNSUPPORTED
+    assert prefix(lib, nheads=258) == UNSUPPORTED
+    assert prefix(lib, pages(**INT8), q_dtype=qsa.F32, nheads=130) == UNSUPPORTED
+    assert prefix(lib, pcols=1 << 27, pstride=1 << 27) == UNSUPPORTED
+    assert prefix(lib, cols=1 << 27, tstride=1 << 27) == UNSUPPORTED
+    n = qsa.prefix_attn_scratch_bytes
+    assert n(0, 1, 8, 2, 4, 4, 16) == 0 and n(4, 1, 7, 2, 4, 4, 16) == 0 and n(4, -1, 8, 2, 4, 4, 16) == 0
+    assert n(64, 3, 32, 8, 4096, 64, 16) >= n(4, 1, 32, 8, 4096, 64, 16) > 0 and n(4, 0, 8, 2, 0, 0, 16) > 0
+    # partial results do not grow with the lengths: bounded by the GPU, the sequences and the groups
+    assert n(64, 1, 32, 8, 1 << 25, 1 << 25, 16) == n(64, 1, 32, 8, 1 << 20, 1 << 20, 16) <= 128 << 20
