@@ -67,7 +67,8 @@ struct Form {
     static constexpr int REAL = kSplit ? 64 : ROWS;      // rows of a tile that are a query head
     static constexpr int STAGES = kInt8 ? 3 : 5;         // tiles of keys or values
     static constexpr int RAW = kInt8 ? 3 : 0;            // int8 tiles on their way
-    static constexpr int FLIGHT = kInt8 ? RAW : 4;       // tiles under way per copy warp
+    // Arrivals that make a tile complete: of every copying thread's copies, or of the warps that converted it.
+    static constexpr int COPIES = kInt8 ? COPY_WARPS : 32 * COPY_WARPS;
     // Weights are kept 2^7 above their reference where the operand is binary16, whose smallest
     // numbers they would otherwise reach sooner: 2^(8 + 7) is within its range.
     static constexpr float LIFT = kKv == QSA_BF16 ? 0.0f : 7.0f;
@@ -178,12 +179,15 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *sr
                  "r"(ok ? 16 : 0)
                  : "memory");
 }
-// Waits until at most n (0 to 3) of this thread's most recent groups are pending.
+// Arrives once on `bar`, which counts this thread already, when its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Waits until at most n (0 to 2) of this thread's most recent groups are pending.
 __device__ __forceinline__ void cp_async_wait_at_most(int n) {
     if (n <= 0) cp_async_wait<0>();
     else if (n == 1) cp_async_wait<1>();
-    else if (n == 2) cp_async_wait<2>();
-    else cp_async_wait<3>();
+    else cp_async_wait<2>();
 }
 __device__ __forceinline__ void arrive(uint64_t *bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
@@ -198,6 +202,11 @@ __device__ __forceinline__ void fewer_registers() {
 }
 // 16-byte chunk c (of 16) of row r of a tile: two halves of 64 elements, 128-byte rows, chunks swizzled.
 __device__ __forceinline__ uint32_t tile_at(int r, int c) { return (c >> 3) * HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
+
+// Which of a segment's 2 n copies tile j's keys and values are: in the order in which the products use them.
+// int8 tiles and segments of two row tiles: keys and values in turn; else keys 0, keys 1, values 0, keys 2, values 1, ..
+__device__ __forceinline__ int key_item(bool turn, int j) { return turn ? 2 * j : max(0, 2 * j - 1); }
+__device__ __forceinline__ int value_item(bool turn, int j, int n) { return turn ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1); }
 
 template <int kKv, typename QT>
 __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_constant__ Params p) {
@@ -225,10 +234,10 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             mbar_init(&bars->seg_full[i], 1);
             mbar_init(&bars->seg_empty[i], 1 + 8 + COPY_WARPS);
         }
-        mbar_init(&bars->q_full, COPY_WARPS);
+        mbar_init(&bars->q_full, F::COPIES);
         mbar_init(&bars->q_empty, 8);
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&bars->kv_full[i], COPY_WARPS);
+            mbar_init(&bars->kv_full[i], F::COPIES);
             mbar_init(&bars->kv_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -367,43 +376,123 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
     } else if (warp >= COPY_WARP) {
         fewer_registers<FEW_REGISTERS>();
         // ---- cells and queries in: rows 32 quarter .. + 31 of every tile ---------------------
+        // No fence here: one that orders these writes before the tensor cores' reads would wait for all
+        // copies under way. The MMA warp has it, behind its wait.
         const int quarter = warp - COPY_WARP;
-        uint32_t issued = 0, done = 0;              // tiles of keys or values (even: keys)
-        uint32_t is = 0, fs = 0;                    // segments begun, and finished with
-        int it = 0, in = 0, ft = 0, fn = 0;         // half tiles issued of segment is - 1 and their number; done of fs - 1
-        bool ok = true, ended = false, q_here = false;
-        Segment s = {}, f = {};                     // segments is - 1 and fs - 1
-        int next_page = -1;
+        bool ok = true;
         long long off = 0;                          // of this lane's row, in bytes
         uint32_t row_mask = 0;                      // rows of the quarter that are there
-        uint32_t masks[2];                          // of tiles on their way
-        uint32_t pair_scale[2];                     // key and value scale of this lane's row
-        int tiles_in_flight = 0;
-        auto page_of = [&](int cell) {
+        uint32_t sc = 0;                            // key and value scale of this lane's row
+        auto page_of = [&](const Segment &s, int cell) {
             return cell < s.len ? ld_in(a.prefix_table + s.g * a.prefix_stride + divide(p.page, cell)) : -1;
         };
-        // The queries of segment f: 16-byte pieces, zeros where there is no sequence.
-        auto load_queries = [&](const Segment &w) {
-            const int n0 = min(p.seqs, w.count), tiles = w.count > p.seqs ? 2 : 1;
-            if constexpr (!kInt8) {
+        // This lane's row of a tile is `cell`, in page `page`.
+        auto find_row = [&](const Segment &s, int cell, int page) {
+            const bool good = page >= 0 && page < a.kv.npages;
+            const int slot = cell - divide(p.page, cell) * a.kv.page_size;
+            off = good ? (page * a.kv.page_stride + slot * a.kv.cell_stride + s.kvh * a.kv.head_stride) * (kInt8 ? 1 : 2) : 0;
+            row_mask = __ballot_sync(FULL_MASK, good);
+            if constexpr (kInt8) {
+                sc = 0;
+                if (good) {
+                    const long long so = page * a.kv.scale_page_stride + slot * a.kv.scale_cell_stride + s.kvh * a.kv.scale_head_stride;
+                    sc = ld_in_u16(a.kv.k_scale_f16 + so) | static_cast<uint32_t>(ld_in_u16(a.kv.v_scale_f16 + so)) << 16;
+                }
+            }
+        };
+        if constexpr (!kInt8) {
+            // The queries of a segment: 16-byte pieces, zeros where there is no sequence.
+            auto queries = [&](const Segment &s) {
+                const int n0 = min(p.seqs, s.count), tiles = s.count > p.seqs ? 2 : 1, c = lane & 15;
                 for (int i = 0; i < tiles; ++i) {
-                    const int rows = (i == 0 ? n0 : w.count - n0) * p.group, mine_row = 32 * quarter + lane;
-                    const int seq = mine_row / p.group;
-                    const long long at = 2 * ((w.first + i * p.seqs + seq) * a.q_seq_stride +
-                                              (w.kvh * p.group + mine_row - seq * p.group) * a.q_head_stride);
-                    const long long good = mine_row < rows ? at : -1;
-                    const int c = lane & 15;
+                    const int rows = (i == 0 ? n0 : s.count - n0) * p.group, row = 32 * quarter + lane, seq = row / p.group;
+                    const long long at = row >= rows ? -1 : 2 * ((s.first + i * p.seqs + seq) * a.q_seq_stride +
+                                                                 (s.kvh * p.group + row - seq * p.group) * a.q_head_stride);
 #pragma unroll 4
                     for (int e = 0; e < 16; ++e) {
                         const int r = 2 * e + (lane >> 4);
-                        const long long ro = __shfl_sync(FULL_MASK, good, r);
+                        const long long ro = __shfl_sync(FULL_MASK, at, r);
                         cp_async_16_or_zero(base + i * TILE_BYTES + tile_at(32 * quarter + r, c),
                                             static_cast<const char *>(a.q) + (ro < 0 ? 0 : ro) + 16 * c, ro >= 0);
                     }
                 }
-            } else {
-                // 16 lanes a row of 128 elements, 8 each; rounded to binary16 times a power of two.
+                cp_async_arrive(&bars->q_full);
+            };
+            uint32_t kv = 0, tile = 0;              // tiles of keys or values, of cells, so far
+            for (uint32_t k = 0; ok; ++k) {
+                ok = wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1);
+                if (!ok) break;
+                const Segment s = bars->seg[k % SEGS];
+                __syncwarp();
+                if (s.count == 0) break;
+                const bool two = s.count > p.seqs;
+                const int n = s.t1 - s.t0;
+                int page = page_of(s, s.t0 * ROWS + 32 * quarter + lane);
+                bool asked = ready_warp(&bars->q_empty, (k & 1) ^ 1);
+                if (asked) queries(s);
+                auto copy = [&](const void *what, long long row_off, uint32_t rows) {
+                    const uint32_t slot = kv % STAGES;
+                    if (!wait_warp(&bars->kv_empty[slot], ((kv / STAGES) & 1) ^ 1)) return false;
+                    const char *from = static_cast<const char *>(what) + 16 * (lane & 15);
+                    const uint32_t to = ring + slot * TILE_BYTES;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int r = 2 * e + (lane >> 4);
+                        const long long ro = __shfl_sync(FULL_MASK, row_off, r);
+                        cp_async_16_or_zero(to + tile_at(32 * quarter + r, lane & 15), from + ro, (rows >> r) & 1u);
+                    }
+                    if (!(p.stall != 0 && blockIdx.x == 0 && kv == 0)) cp_async_arrive(&bars->kv_full[slot]);
+                    ++kv;
+                    return true;
+                };
+                long long last_off = 0;
+                uint32_t last_mask = 0;
+                for (int j = 0; ok && j <= n; ++j) {
+                    // In the order of use (see key_item): with one row tile, keys of tile j go before the values of tile j - 1.
+                    if (j < n) {
+                        if (!two) {
+                            last_off = off;
+                            last_mask = row_mask;
+                        }
+                        const int cell = (s.t0 + j) * ROWS + 32 * quarter + lane;
+                        find_row(s, cell, page);
+                        page = j + 1 < n ? page_of(s, cell + ROWS) : -1;
+                        const uint32_t side = tile % SIDES;
+                        ok = wait_warp(&bars->side_empty[side], (tile / SIDES & 1) ^ 1);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            reinterpret_cast<uint32_t *>(&bars->mask[side])[quarter] = row_mask;
+                            mbar_arrive(&bars->side_full[side]);
+                        }
+                        ++tile;
+                        ok = copy(a.kv.k, off, row_mask);
+                    } else if (!two) {
+                        last_off = off;
+                        last_mask = row_mask;
+                    }
+                    if (ok && (two ? j < n : j > 0)) ok = copy(a.kv.v, two ? off : last_off, two ? row_mask : last_mask);
+                    if (ok && !asked) {
+                        ok = wait_warp(&bars->q_empty, (k & 1) ^ 1);
+                        if (ok) queries(s);
+                        asked = true;
+                    }
+                }
+                if (ok && lane == 0) mbar_arrive(&bars->seg_empty[k % SEGS]);
+            }
+        } else {
+            // Copies of int8 tiles run ahead of their conversion; every thread converts what it copied.
+            uint32_t issued = 0, done = 0;          // tiles of keys or values (even: keys)
+            uint32_t is = 0, fs = 0;                // segments begun, and finished with
+            int it = 0, in = 0, ft = 0, fn = 0;     // tiles issued of segment is - 1 and their number; done of fs - 1
+            bool ended = false;
+            Segment s = {}, f = {};                 // segments is - 1 and fs - 1
+            int next_page = -1;
+            uint32_t masks[2], scs[2];              // of tiles on their way
+            int ahead = 0;
+            // The queries of a segment: 16 lanes a row of 128 elements, 8 each, as binary16 numbers times a power of two.
+            auto queries = [&](const Segment &w) {
                 constexpr int STEPS = F::REAL / (2 * COPY_WARPS);
+                const int n0 = min(p.seqs, w.count), tiles = w.count > p.seqs ? 2 : 1;
                 const float c = a.scale * LOG2E;
                 for (int i = 0; i < tiles; ++i) {
                     const int rows = (i == 0 ? n0 : w.count - n0) * p.group;
@@ -438,121 +527,80 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                         }
                     }
                 }
-            }
-        };
-        auto can_issue = [&]() {
-            if (ended || issued - done >= F::FLIGHT) return false;
-            if (it == in) {                          // a new segment
-                if (!ready_warp(&bars->seg_full[is % SEGS], (is / SEGS) & 1)) return false;
-                s = bars->seg[is % SEGS];
                 __syncwarp();
-                ++is;
-                if (s.count == 0) {
-                    ended = true;
-                    return false;
-                }
-                it = 0;
-                in = 2 * (s.t1 - s.t0);
-                next_page = page_of(s.t0 * ROWS + 32 * quarter + lane);
-            }
-            return kInt8 || ready_warp(&bars->kv_empty[issued % STAGES], ((issued / STAGES) & 1) ^ 1);
-        };
-        auto issue = [&]() {
-            const bool values = it & 1;
-            if (!values) {
-                const int cell = (s.t0 + (it >> 1)) * ROWS + 32 * quarter + lane;
-                const int page = next_page;
-                next_page = page_of(it + 2 < in ? cell + ROWS : s.len);
-                const bool good = page >= 0 && page < a.kv.npages;
-                const int slot = cell - divide(p.page, cell) * a.kv.page_size;
-                off = good ? (page * a.kv.page_stride + slot * a.kv.cell_stride + s.kvh * a.kv.head_stride) * (kInt8 ? 1 : 2) : 0;
-                row_mask = __ballot_sync(FULL_MASK, good);
-                uint32_t sc = 0;
-                if constexpr (kInt8) {
-                    if (good) {
-                        const long long so = page * a.kv.scale_page_stride + slot * a.kv.scale_cell_stride + s.kvh * a.kv.scale_head_stride;
-                        sc = ld_in_u16(a.kv.k_scale_f16 + so) | static_cast<uint32_t>(ld_in_u16(a.kv.v_scale_f16 + so)) << 16;
+                if (lane == 0) mbar_arrive(&bars->q_full);
+            };
+            auto can_issue = [&]() {
+                if (ended || issued - done >= F::RAW) return false;
+                if (it == in) {                      // a new segment
+                    if (!ready_warp(&bars->seg_full[is % SEGS], (is / SEGS) & 1)) return false;
+                    s = bars->seg[is % SEGS];
+                    __syncwarp();
+                    ++is;
+                    if (s.count == 0) {
+                        ended = true;
+                        return false;
                     }
+                    it = 0;
+                    in = 2 * (s.t1 - s.t0);
+                    next_page = page_of(s, s.t0 * ROWS + 32 * quarter + lane);
                 }
-                if (tiles_in_flight == 0) {
-                    masks[0] = row_mask;
-                    pair_scale[0] = sc;
-                } else {
-                    masks[1] = row_mask;
-                    pair_scale[1] = sc;
+                return true;
+            };
+            auto issue = [&]() {
+                if (!(it & 1)) {
+                    const int cell = (s.t0 + (it >> 1)) * ROWS + 32 * quarter + lane;
+                    find_row(s, cell, next_page);
+                    next_page = it + 2 < in ? page_of(s, cell + ROWS) : -1;
+                    if (ahead == 0) {
+                        masks[0] = row_mask;
+                        scs[0] = sc;
+                    } else {
+                        masks[1] = row_mask;
+                        scs[1] = sc;
+                    }
+                    ++ahead;
                 }
-                ++tiles_in_flight;
-            }
-            const char *from = static_cast<const char *>(values ? a.kv.v : a.kv.k);
-            if constexpr (!kInt8) {
-                // The first queries come along with the first keys.
-                if (is == 1 && it == 0) {
-                    load_queries(s);
-                    q_here = true;
-                }
-                const uint32_t to = ring + (issued % STAGES) * TILE_BYTES;
-                const int c = lane & 15;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int r = 2 * e + (lane >> 4);
-                    const long long ro = __shfl_sync(FULL_MASK, off, r);
-                    cp_async_16_or_zero(to + tile_at(32 * quarter + r, c), from + ro + 16 * c, (row_mask >> r) & 1u);
-                }
-            } else {
+                const char *from = static_cast<const char *>((it & 1) ? a.kv.v : a.kv.k) + 16 * (lane & 7);
                 const uint32_t to = raws + (issued % F::RAW) * (TILE_BYTES / 2) + 16 * (32 * quarter * 8 + lane);
-                const int c = lane & 7;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int r = 4 * e + (lane >> 3);
                     const long long ro = __shfl_sync(FULL_MASK, off, r);
-                    cp_async_16_or_zero(to + 512 * e, from + ro + 16 * c, (row_mask >> r) & 1u);
+                    cp_async_16_or_zero(to + 512 * e, from + ro, (row_mask >> r) & 1u);
                 }
-            }
-            cp_async_commit();
-            ++issued;
-            ++it;
-        };
-        // The oldest tile on its way: waited for, made operands, and signalled.
-        auto finish = [&]() {
-            cp_async_wait_at_most(static_cast<int>(issued - done) - 1);
-            if (ft == fn) {                          // the first of its segment
-                f = bars->seg[fs % SEGS];
-                ++fs;
-                ft = 0;
-                fn = 2 * (f.t1 - f.t0);
-                if (!q_here) {
-                    if (!wait_warp(&bars->q_empty, (fs & 1))) return false;   // of segment fs - 2
-                    load_queries(f);
-                    if (!kInt8) {
-                        cp_async_commit();
-                        cp_async_wait<0>();
-                    }
+                cp_async_commit();
+                ++issued;
+                ++it;
+            };
+            // The oldest tile on its way: waited for, made operands, and signalled.
+            auto finish = [&]() {
+                if (ft == fn) {                      // the first of its segment
+                    f = bars->seg[fs % SEGS];
+                    if (!wait_warp(&bars->q_empty, (fs & 1) ^ 1)) return false;
+                    queries(f);
+                    ++fs;
+                    ft = 0;
+                    fn = 2 * (f.t1 - f.t0);
                 }
-                q_here = false;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->q_full);
-            }
-            const uint32_t tile = done >> 1;
-            if (!(done & 1u)) {
-                if (!wait_warp(&bars->side_empty[tile % SIDES], ((tile / SIDES) & 1) ^ 1)) return false;
-                if (lane == 0) reinterpret_cast<uint32_t *>(&bars->mask[tile % SIDES])[quarter] = masks[0];
-                if constexpr (kInt8) {
+                const uint32_t tile = done >> 1;
+                if (!(done & 1u)) {
+                    if (!wait_warp(&bars->side_empty[tile % SIDES], ((tile / SIDES) & 1) ^ 1)) return false;
+                    if (lane == 0) reinterpret_cast<uint32_t *>(&bars->mask[tile % SIDES])[quarter] = masks[0];
                     const int r = 32 * quarter + lane;
-                    const float vs = __half2float(__ushort_as_half(static_cast<uint16_t>(pair_scale[0] >> 16)));
-                    scales->key[tile % SIDES][r] = __half2float(__ushort_as_half(static_cast<uint16_t>(pair_scale[0] & 0xFFFFu)));
+                    const float vs = __half2float(__ushort_as_half(static_cast<uint16_t>(scs[0] >> 16)));
+                    scales->key[tile % SIDES][r] = __half2float(__ushort_as_half(static_cast<uint16_t>(scs[0] & 0xFFFFu)));
                     scales->value[tile % SIDES][r] = vs;
                     // The sums' reference has to be finite, whatever the scale: within binary16's numbers.
                     scales->log_value[tile % SIDES][r] = __log2f(fminf(fmaxf(fabsf(vs), 5.9604645e-8f), 65504.0f));
+                    masks[0] = masks[1];
+                    scs[0] = scs[1];
+                    --ahead;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->side_full[tile % SIDES]);
                 }
-                masks[0] = masks[1];
-                pair_scale[0] = pair_scale[1];
-                --tiles_in_flight;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->side_full[tile % SIDES]);
-            }
-            if constexpr (kInt8) {
                 if (!wait_warp(&bars->kv_empty[done % STAGES], ((done / STAGES) & 1) ^ 1)) return false;
+                cp_async_wait_at_most(static_cast<int>(issued - done) - 1);
                 const uint32_t from = raws + (done % F::RAW) * (TILE_BYTES / 2) + 16 * (32 * quarter * 8 + lane);
                 const uint32_t to = ring + (done % STAGES) * TILE_BYTES;
                 const int c = lane & 7;
@@ -566,25 +614,17 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                         st_shared_v4(to + tile_at(r, 2 * c + h), codes_to_half2(w[2 * h], 0x4140), codes_to_half2(w[2 * h], 0x4342),
                                      codes_to_half2(w[2 * h + 1], 0x4140), codes_to_half2(w[2 * h + 1], 0x4342));
                 }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && !(p.stall != 0 && blockIdx.x == 0 && done == 0)) mbar_arrive(&bars->kv_full[done % STAGES]);
-            ++done;
-            if (++ft == fn && lane == 0) mbar_arrive(&bars->seg_empty[(fs - 1) % SEGS]);
-            return true;
-        };
-        while (ok) {
-            if (can_issue()) {
-                issue();
-            } else if (issued != done) {
-                ok = finish();
-            } else if (ended) {
-                break;
-            } else if (it == in) {
-                ok = wait_warp(&bars->seg_full[is % SEGS], (is / SEGS) & 1);
-            } else {
-                ok = wait_warp(&bars->kv_empty[issued % STAGES], ((issued / STAGES) & 1) ^ 1);
+                __syncwarp();
+                if (lane == 0 && !(p.stall != 0 && blockIdx.x == 0 && done == 0)) mbar_arrive(&bars->kv_full[done % STAGES]);
+                ++done;
+                if (++ft == fn && lane == 0) mbar_arrive(&bars->seg_empty[(fs - 1) % SEGS]);
+                return true;
+            };
+            while (ok) {
+                if (can_issue()) issue();
+                else if (issued != done) ok = finish();
+                else if (ended) break;
+                else ok = wait_warp(&bars->seg_full[is % SEGS], (is / SEGS) & 1);
             }
         }
         cp_async_wait<0>();
@@ -607,6 +647,12 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             const bool two = s.count > p.seqs;
             const int n = s.t1 - s.t0;
             if (!wait_warp(&bars->q_full, k & 1)) break;
+            // Orders what the copy warps wrote (and waits have shown) before the tensor cores' reads.
+            auto landed = [&](uint32_t slot, uint32_t n) {
+                if (!wait_warp(&bars->kv_full[slot], n & 1)) return false;
+                fence_proxy_async_smem();
+                return true;
+            };
             auto scores = [&](auto which, uint32_t q_at, uint32_t slot) {
                 constexpr int i = decltype(which)::value;
                 const uint64_t qd = sw128_kmajor_desc(q_at), kd = sw128_kmajor_desc(ring + slot * TILE_BYTES);
@@ -638,12 +684,12 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             using I0 = std::integral_constant<int, 0>;
             using I1 = std::integral_constant<int, 1>;
             for (int j = 0; ok && j <= n; ++j) {
-                const uint32_t kn = kv + 2 * j, vn = kn - 1;        // keys of tile j, values of tile j - 1
+                const uint32_t kn = kv + key_item(two || kInt8, j), vn = kv + value_item(two || kInt8, j - 1, n);
                 const uint32_t ks = kn % STAGES, vs = vn % STAGES;
                 if (two) {
-                    if (j > 0) ok = wait_warp(&bars->kv_full[vs], (vn / STAGES) & 1) && outputs(I0(), vs, j == 1);
+                    if (j > 0) ok = landed(vs, vn / STAGES) && outputs(I0(), vs, j == 1);
                     if (ok && j < n) {
-                        ok = wait_warp(&bars->kv_full[ks], (kn / STAGES) & 1);
+                        ok = landed(ks, kn / STAGES);
                         if (ok) scores(I0(), base, ks);
                     }
                     if (ok && j > 0) ok = outputs(I1(), vs, j == 1);
@@ -655,14 +701,14 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 } else {
                     // Tile j goes to stream j % 2; the other's last weights are worked out meanwhile.
                     if (j < n) {
-                        ok = wait_warp(&bars->kv_full[ks], (kn / STAGES) & 1);
+                        ok = landed(ks, kn / STAGES);
                         if (!ok) break;
                         if (j & 1) scores(I1(), base, ks);
                         else scores(I0(), base, ks);
                         if (one) tc_commit(&bars->kv_empty[ks]);
                     }
                     if (j > 0) {
-                        ok = wait_warp(&bars->kv_full[vs], (vn / STAGES) & 1) &&
+                        ok = landed(vs, vn / STAGES) &&
                              ((j & 1) ? outputs(I0(), vs, j <= 2) : outputs(I1(), vs, j <= 2));
                         if (ok && one) tc_commit(&bars->kv_empty[vs]);
                     }
@@ -971,116 +1017,126 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
 }
 
 // Adds a row's partial sums: of the prefix, in the order of the CTAs that hold them, and of the
-// sequence's own cells, as paged attention left them. A CTA takes a sequence and a query head.
-constexpr int JOIN_WARPS = 8, JOIN_BATCH = 4;
-template <typename QT>
-__global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __grid_constant__ Params p, const PagedPartial own, int grid) {
+// sequence's own cells, as paged attention left them. A warp takes kRows query heads of a sequence
+// at once; `split` warps share them, each every split-th range, and are added in order.
+constexpr int JOIN_WARPS = 8;
+template <typename QT, int kRows, int kRanges>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __grid_constant__ Params p, const PagedPartial own, int grid, int split) {
     const PrefixAttnArgs &a = p.a;
-    const int s = blockIdx.x, h = blockIdx.y, kvh = h / p.group, in_group = h - kvh * p.group;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int s = blockIdx.x, set = warp / split, part = warp - set * split;
+    const int h0 = (blockIdx.y * (JOIN_WARPS / split) + set) * kRows;
+    // Before the wait: prefix_kernel let paged attention's kernel start, and that this grid, only after it
+    // had waited for its own predecessors, so groups and lengths are final.
     // The group that sequence s is of: the last that begins at or before it.
     int lo = -1, hi = a.ngroups + 1;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    const int own_len = ld_in(a.lens + s);
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32, g = lo + (lane + 1) * step;
         const int below = __popc(__ballot_sync(FULL_MASK, g < hi && min(max(ld_in(a.cu + g), 0), a.nseq) <= s));
         lo += below * step;
         hi = min(hi, lo + step);
     }
-    // Ranges of the prefix: slots c0 (and its part), then those of CTAs c0 + 1 .. c1.
-    int first = 0, n = 0;
-    const float *whole = nullptr;
-    int row = 0;
-    if (lo >= 0 && lo < a.ngroups) {
-        const Group x = group_of(p, lo);
-        if (x.tiles > 0 && s < x.first + x.count) {
-            const int b = (s - x.first) / (2 * p.seqs), in_block = s - x.first - b * 2 * p.seqs;
-            row = in_block < p.seqs ? in_block * p.group + in_group : ROWS + (in_block - p.seqs) * p.group + in_group;
-            const int2 at = __ldcg(p.meta + static_cast<size_t>(x.first / (2 * p.seqs) + lo + b) * a.kv.nkv + kvh);
-            if (at.x < 0) {
-                whole = p.whole + (static_cast<size_t>(s) * a.nheads + h) * SLOT_ROW;
-                n = 1;
-            } else {
-                // Nothing but numbers is taken from scratch: a CTA that gave up may have left anything.
-                first = min(at.x, 2 * grid - 1);
-                n = max(0, min(at.y, grid - 1) - (first >> 1) + 1);
-            }
+    Group x = {};
+    if (lo >= 0 && lo < a.ngroups) x = group_of(p, lo);
+    const bool shared = x.tiles > 0 && s < x.first + x.count;
+    const int b = (s - x.first) / (2 * p.seqs), in_block = s - x.first - b * 2 * p.seqs;
+    const int row0 = in_block < p.seqs ? in_block * p.group : ROWS + (in_block - p.seqs) * p.group;   // of the block's rows
+    const size_t block = static_cast<size_t>(x.first / (2 * p.seqs) + lo + b) * a.kv.nkv;
+    const bool mine = own_len > 0 && a.table_cols > 0;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // Where a row's ranges lie: number i of the prefix is at the first place, then every `next` bytes from the second.
+    const float *at0[kRows], *at1[kRows], *own0[kRows], *own1[kRows];
+    int n[kRows], all[kRows], most = 0;
+    const size_t slot_bytes = static_cast<size_t>(2 * ROWS) * SLOT_ROW, own_slot = static_cast<size_t>(own.heads_per_unit) * SLOT_ROW;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const int h = min(h0 + r, a.nheads - 1), kvh = h / p.group, in_group = h - kvh * p.group;
+        const size_t out_row = static_cast<size_t>(s) * a.nheads + h;
+        n[r] = 0;
+        if (shared) {
+            const int2 m = __ldcg(p.meta + block + kvh);
+            // Nothing but numbers is taken from scratch: a CTA that gave up may have left anything.
+            const int first = min(max(m.x, 0), 2 * grid - 1);
+            at0[r] = m.x < 0 ? p.whole + out_row * SLOT_ROW : p.slots + first * slot_bytes + static_cast<size_t>(row0 + in_group) * SLOT_ROW;
+            at1[r] = p.slots + (first & ~1) * slot_bytes + static_cast<size_t>(row0 + in_group) * SLOT_ROW;
+            n[r] = m.x < 0 ? 1 : max(0, min(m.y, grid - 1) - (first >> 1) + 1);
         }
-    }
-    // Ranges of the sequence's own cells.
-    const int unit = kvh * own.parts + in_group / own.heads_per_unit, unit_head = in_group % own.heads_per_unit;
-    int4 w = make_int4(-1, 0, 0, -1);
-    int own_n = 0;
-    const int own_len = ld_in(a.lens + s);
-    if (own_len > 0 && a.table_cols > 0) {
-        w = __ldcg(own.meta + static_cast<size_t>(s) * own.units + unit);
-        own_n = 1;
-        if (w.x >= 0) {
-            w.z = max(0, min(w.z, 2 * own.grid - 1));
-            own_n = max(0, min(w.w, own.grid - 1) - (w.z >> 1) + 1);
+        all[r] = n[r];
+        if (mine) {
+            const int part_of = in_group / own.heads_per_unit;
+            const int4 w = __ldcg(own.meta + static_cast<size_t>(s) * own.units + kvh * own.parts + part_of);
+            const int first = min(max(w.z, 0), 2 * own.grid - 1);
+            const size_t head = static_cast<size_t>(in_group - part_of * own.heads_per_unit) * SLOT_ROW;
+            own0[r] = w.x < 0 ? own.rows + out_row * SLOT_ROW : own.slots + first * own_slot + head;
+            own1[r] = own.slots + (first & ~1) * own_slot + head;
+            all[r] += w.x < 0 ? 1 : max(0, min(w.w, own.grid - 1) - (first >> 1) + 1);
         }
+        most = max(most, all[r]);
     }
-    const int all = n + own_n;
-    // Range i: its sums, reference and weights' sum.
-    auto place = [&](int i) {
-        if (i < n) return whole != nullptr ? whole : p.slots + (static_cast<size_t>(i == 0 ? first : 2 * ((first >> 1) + i)) * 2 * ROWS + row) * SLOT_ROW;
-        const int e = i - n;
-        if (w.x < 0) return own.rows + (static_cast<size_t>(s) * a.nheads + h) * SLOT_ROW;
-        return own.slots + (static_cast<size_t>(e == 0 ? w.z : 2 * ((w.z >> 1) + e)) * own.heads_per_unit + unit_head) * SLOT_ROW;
+    float top[kRows], l[kRows];
+    float4 y[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        top[r] = -INFINITY;
+        l[r] = 0.0f;
+        y[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    auto add = [&](int r, float2 ml, float4 v) {
+        const float t = fmaxf(top[r], ml.x), ref = t == -INFINITY ? 0.0f : t;
+        const float f = ex2(top[r] - ref), g = ex2(ml.x - ref);
+        top[r] = t;
+        l[r] = fmaf(ml.y, g, l[r] * f);
+        y[r].x = fmaf(v.x, g, y[r].x * f);
+        y[r].y = fmaf(v.y, g, y[r].y * f);
+        y[r].z = fmaf(v.z, g, y[r].z * f);
+        y[r].w = fmaf(v.w, g, y[r].w * f);
     };
-    float top = -INFINITY, l = 0.0f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = warp; i0 < all; i0 += warps * JOIN_BATCH) {
-        float2 ml[JOIN_BATCH];
-        float4 v[JOIN_BATCH];
+    for (int i0 = part; i0 < most; i0 += split * kRanges) {
+        float2 ml[kRanges][kRows];
+        float4 v[kRanges][kRows];
 #pragma unroll
-        for (int e = 0; e < JOIN_BATCH; ++e) {
-            const int i = i0 + warps * e;
-            ml[e] = make_float2(-INFINITY, 0.0f);
-            v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < all) {
-                const float *at = place(i);
-                ml[e] = __ldcg(reinterpret_cast<const float2 *>(at + 128));
-                v[e] = ld_in(reinterpret_cast<const float4 *>(at) + lane);
+        for (int e = 0; e < kRanges; ++e)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const int i = i0 + split * e, j = i - n[r];
+                ml[e][r] = make_float2(-INFINITY, 0.0f);
+                v[e][r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < all[r]) {
+                    const float *at = j < 0 ? (i == 0 ? at0[r] : at1[r] + 2 * i * slot_bytes) : (j == 0 ? own0[r] : own1[r] + 2 * j * own_slot);
+                    ml[e][r] = __ldcg(reinterpret_cast<const float2 *>(at + 128));
+                    v[e][r] = ld_in(reinterpret_cast<const float4 *>(at) + lane);
+                }
             }
-        }
 #pragma unroll
-        for (int e = 0; e < JOIN_BATCH; ++e) {
-            const float t = fmaxf(top, ml[e].x), b = t == -INFINITY ? 0.0f : t;
-            const float f = ex2(top - b), g = ex2(ml[e].x - b);
-            top = t;
-            l = fmaf(ml[e].y, g, l * f);
-            y.x = fmaf(v[e].x, g, y.x * f);
-            y.y = fmaf(v[e].y, g, y.y * f);
-            y.z = fmaf(v[e].z, g, y.z * f);
-            y.w = fmaf(v[e].w, g, y.w * f);
-        }
+        for (int e = 0; e < kRanges; ++e)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) add(r, ml[e][r], v[e][r]);
     }
-    __shared__ float4 sum[JOIN_WARPS][32];
-    __shared__ float2 weight[JOIN_WARPS];
-    if (warps > 1) {
-        sum[warp][lane] = y;
-        if (lane == 0) weight[warp] = make_float2(top, l);
+    __shared__ float4 sums[JOIN_WARPS][kRows][32];
+    __shared__ float2 weights[JOIN_WARPS][kRows];
+    if (split > 1) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            sums[warp][r][lane] = y[r];
+            if (lane == 0) weights[warp][r] = make_float2(top[r], l[r]);
+        }
         __syncthreads();
-        if (warp > 0) return;
-        for (int o = 1; o < warps; ++o) {
-            const float2 ml = weight[o];
-            const float4 v = sum[o][lane];
-            const float t = fmaxf(top, ml.x), b = t == -INFINITY ? 0.0f : t;
-            const float f = ex2(top - b), g = ex2(ml.x - b);
-            top = t;
-            l = fmaf(ml.y, g, l * f);
-            y.x = fmaf(v.x, g, y.x * f);
-            y.y = fmaf(v.y, g, y.y * f);
-            y.z = fmaf(v.z, g, y.z * f);
-            y.w = fmaf(v.w, g, y.w * f);
-        }
+        if (part > 0) return;
+        for (int o = 1; o < split; ++o)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) add(r, weights[warp + o][r], sums[warp + o][r][lane]);
     }
-    const size_t out_row = static_cast<size_t>(s) * a.nheads + h;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    store4(static_cast<QT *>(a.out) + out_row * 128 + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-    if (lane == 0 && a.lse != nullptr) a.lse[out_row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * LN2;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        if (h0 + r >= a.nheads) break;
+        const size_t out_row = static_cast<size_t>(s) * a.nheads + h0 + r;
+        const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
+        store4(static_cast<QT *>(a.out) + out_row * 128 + 4 * lane, make_float4(y[r].x * inv, y[r].y * inv, y[r].z * inv, y[r].w * inv));
+        if (lane == 0 && a.lse != nullptr) a.lse[out_row] = l[r] == 0.0f ? -INFINITY : (top[r] + log2f(l[r])) * LN2;
+    }
 }
 
 int seqs_of(int group, bool split) { return (split ? 64 : 128) / group; }
@@ -1138,14 +1194,21 @@ cudaError_t run(Params &p, const Layout &y, const PagedAttnArgs &own_args, cudaS
     }
     p.seqs = seqs_of(p.group, Form<kKv, QT>::kSplit);
     if (e == cudaSuccess) e = launch(kernel, dim3(y.grid), PTHREADS, smem, stream, p);
-    // Ranges of a block, on average.
-    const int ranges = y.grid / (p.a.kv.nkv * std::max(1, std::max(p.a.ngroups, p.a.nseq / (2 * p.seqs)))) + 1;
-    const int join_warps = ranges <= 4 ? 1 : ranges <= 16 ? 4 : JOIN_WARPS;
     PagedPartial own;
     if (e == cudaSuccess) e = launch_paged_partial(own_args, own, stream);
-    if (e == cudaSuccess)
-        e = launch(prefix_join_kernel<QT>, dim3(p.a.nseq, p.a.nheads), 32 * join_warps, 0, stream, p, own, y.grid);
-    return e;
+    if (e != cudaSuccess) return e;
+    // Ranges of a block, on average.
+    const int ranges = y.grid / (p.a.kv.nkv * std::max(1, std::max(p.a.ngroups, p.a.nseq / (2 * p.seqs)))) + 1;
+    // As many warps share rows as there are ranges for and the GPU has room for at once.
+    constexpr int ROWS_AT_ONCE = 2;
+    const long long warps = static_cast<long long>(p.a.nseq) * ((p.a.nheads + ROWS_AT_ONCE - 1) / ROWS_AT_ONCE);
+    int split = 1;
+    while (split < JOIN_WARPS && 2 * split <= ranges && 2 * split * warps <= 16LL * device_sm_count()) split *= 2;
+    auto join = [&](auto kernel, int rows) {
+        const int heads = rows * (JOIN_WARPS / split);   // of a CTA
+        return launch(kernel, dim3(p.a.nseq, (p.a.nheads + heads - 1) / heads), 32 * JOIN_WARPS, 0, stream, p, own, y.grid, split);
+    };
+    return join(prefix_join_kernel<QT, ROWS_AT_ONCE, 4>, ROWS_AT_ONCE);
 }
 
 }  // namespace
