@@ -54,7 +54,8 @@ constexpr int TILE_BYTES = 2 * HALF;
 constexpr int MMA_WARP = 8, WALK_WARP = 9, COPY_WARP = 12, COPY_WARPS = 4, PTHREADS = 512;
 // 128 registers a thread at launch: 8 softmax warps x 168 + 8 x 88 = 16 x 128.
 constexpr int MORE_REGISTERS = 168, FEW_REGISTERS = 88;
-constexpr int SLOT_ROW = 132;               // 128 sums, reference, weight sum, padding
+constexpr int BLOCK = 2 * ROWS;             // rows of a block at most
+constexpr int OWN_ROW = 132;                // paged attention's partial results: 128 sums, reference, weights' sum, padding
 constexpr float LAZY = 8.0f;                // log2 of how far the sums may run above their reference
 constexpr int SEGS = 4, SIDES = 4;
 constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
@@ -79,9 +80,12 @@ struct Params {
     Divider page;
     int group, seqs;          // query heads per KV head; sequences of a row tile
     int capacity;             // cells of a row of the prefix table
-    float *slots;             // [2 grid][256][SLOT_ROW]: a segment at a CTA's begin, and its last
-    float *whole;             // [nseq][nheads][SLOT_ROW]: of blocks that fall into one CTA
+    // Partial results: sums as sums_at() says, and reference and weights' sum of each row.
+    float4 *slots, *whole;    // [2 grid][BLOCK x 32]: a segment at a CTA's begin, and its last; [nkv][whole_rows x 32]
+    float2 *slot_refs, *whole_refs;
+    int whole_rows;           // of blocks that fall into one CTA, at whole_row()
     int2 *meta;               // [blocks][nkv]: first slot, last CTA; -1 where whole
+    int2 *places;             // [nseq]: a sequence's block and its first sequence; -1 without a prefix
     uint64_t wait_ns;
     int stall;                // diagnostics only: CTA 0 never signals its first key tile
 };
@@ -100,11 +104,20 @@ __device__ __forceinline__ Group group_of(const Params &p, int g) {
     return x;
 }
 
+// Block b of group g, among all.
+__device__ __forceinline__ int block_number(const Params &p, const Group &x, int g, int b) { return x.first / (2 * p.seqs) + g + b; }
+// First row of a whole block's partial results (of a KV head): a multiple of 8, and behind the rows of the blocks before it.
+__device__ __forceinline__ int whole_row(const Params &p, int block, int first) { return ((first * p.group + 7) / 8 + block) * 8; }
+// Columns 4 chunk .. + 3 of a row, in 16-byte pieces: 8 rows' pieces are a line, so that a warp whose lanes
+// have a row each and one that takes 8 rows by 4 pieces both move whole lines.
+__device__ __forceinline__ size_t sums_at(int row, int chunk) { return static_cast<size_t>(row >> 3) * 256 + chunk * 8 + (row & 7); }
+
 // A block's part in this CTA.
 struct Segment {
     int g, kvh, first, count;   // count: sequences of the block, 0 at the range's end
     int len, t0, t1;            // cells of the prefix; tiles of cells
     int slot;                   // of the partial results, -1: whole
+    int row;                    // of them, where whole
 };
 
 struct alignas(16) Bars {
@@ -192,6 +205,9 @@ __device__ __forceinline__ void cp_async_wait_at_most(int n) {
 __device__ __forceinline__ void arrive(uint64_t *bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
+__device__ __forceinline__ long long quotient(long long a, long long b) {   // neither is negative
+    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
 template <int N>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -216,8 +232,8 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
     constexpr int STAGES = F::STAGES;
     extern __shared__ unsigned char raw_smem[];
     __shared__ long long sh_scan[PTHREADS / 32];
-    __shared__ int sh_group;
-    __shared__ long long sh_inside;             // the range's first tile, counted in its group
+    __shared__ Group sh_at;                     // the group that the range begins in
+    __shared__ int sh_group, sh_kvh, sh_block, sh_tile;
     const PrefixAttnArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(FULL_MASK, tid >> 5, 0);   // the same for the warp, as the compiler now knows
@@ -264,7 +280,11 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
     const int g0 = min(tid * each, a.ngroups), g1 = min(g0 + each, a.ngroups);
     auto tiles_in = [&](const Group &x) { return static_cast<long long>(x.tiles) * x.blocks * a.kv.nkv; };
     long long mine = 0;
-    for (int g = g0; g < g1; ++g) mine += tiles_in(group_of(p, g));
+    Group own_group = {};                       // the last of this thread's, read once where it is the only one
+    for (int g = g0; g < g1; ++g) {
+        own_group = group_of(p, g);
+        mine += tiles_in(own_group);
+    }
     long long before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -282,17 +302,25 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         all += sh_scan[w];
     }
     before -= mine;
-    const long long per = (all + gridDim.x - 1) / gridDim.x;
+    const long long per = quotient(all + gridDim.x - 1, gridDim.x);
     const long long x0 = per * blockIdx.x, x1 = min(x0 + per, all);
     if (x0 < x1 && x0 >= before && x0 < before + mine) {
         long long b = before;
         int g = g0;
-        for (long long n = tiles_in(group_of(p, g)); x0 >= b + n; n = tiles_in(group_of(p, g))) {
-            b += n;
-            ++g;
+        Group x = own_group;
+        if (g1 - g0 > 1) {
+            x = group_of(p, g);
+            for (long long n = tiles_in(x); x0 >= b + n; n = tiles_in(x)) {
+                b += n;
+                x = group_of(p, ++g);
+            }
         }
+        const long long unit = quotient(x0 - b, x.tiles), kvh = quotient(unit, x.blocks);
+        sh_at = x;
         sh_group = g;
-        sh_inside = x0 - b;
+        sh_kvh = static_cast<int>(kvh);
+        sh_block = static_cast<int>(unit - kvh * x.blocks);
+        sh_tile = static_cast<int>(x0 - b - unit * x.tiles);
     }
     __syncthreads();
     const uint32_t tmem = bars->tmem;
@@ -316,16 +344,8 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         fewer_registers<FEW_REGISTERS>();
         // ---- the segments of the range ----------------------------------------------------
         long long left = sh_group < 0 ? 0 : x1 - x0;
-        int g = max(sh_group, 0);
-        Group x = {};
-        int kvh = 0, b = 0, t = 0;
-        if (left > 0) {
-            x = group_of(p, g);
-            const long long unit = sh_inside / x.tiles;
-            t = static_cast<int>(sh_inside - unit * x.tiles);
-            kvh = static_cast<int>(unit / x.blocks);
-            b = static_cast<int>(unit - static_cast<long long>(kvh) * x.blocks);
-        }
+        int g = sh_group, kvh = sh_kvh, b = sh_block, t = sh_tile;   // unused without a group
+        Group x = sh_at;
         for (uint32_t k = 0;; ++k) {
             Segment s = {};
             if (left > 0) {
@@ -339,11 +359,13 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 s.t1 = t + n;
                 const bool whole = n == x.tiles;
                 s.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (k == 0 ? 0 : 1);
+                const int block = block_number(p, x, g, b);
+                s.row = whole_row(p, block, s.first);
                 if (t == 0 && lane == 0) {
                     // Where the join finds the block: its first tile is tile `at` of the batch.
                     const long long at = x1 - left;
-                    p.meta[static_cast<size_t>(x.first / (2 * p.seqs) + g + b) * a.kv.nkv + kvh] =
-                        whole ? make_int2(-1, 0) : make_int2(s.slot, static_cast<int>((at + x.tiles - 1) / per));
+                    p.meta[static_cast<size_t>(block) * a.kv.nkv + kvh] =
+                        whole ? make_int2(-1, 0) : make_int2(s.slot, static_cast<int>(quotient(at + x.tiles - 1, per)));
                 }
                 left -= n;
                 t = 0;
@@ -382,7 +404,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         bool ok = true;
         long long off = 0;                          // of this lane's row, in bytes
         uint32_t row_mask = 0;                      // rows of the quarter that are there
-        uint32_t sc = 0;                            // key and value scale of this lane's row
+        uint16_t key_scale = 0, value_scale = 0;    // of this lane's row
         auto page_of = [&](const Segment &s, int cell) {
             return cell < s.len ? ld_in(a.prefix_table + s.g * a.prefix_stride + divide(p.page, cell)) : -1;
         };
@@ -393,10 +415,11 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             off = good ? (page * a.kv.page_stride + slot * a.kv.cell_stride + s.kvh * a.kv.head_stride) * (kInt8 ? 1 : 2) : 0;
             row_mask = __ballot_sync(FULL_MASK, good);
             if constexpr (kInt8) {
-                sc = 0;
+                key_scale = value_scale = 0;
                 if (good) {
                     const long long so = page * a.kv.scale_page_stride + slot * a.kv.scale_cell_stride + s.kvh * a.kv.scale_head_stride;
-                    sc = ld_in_u16(a.kv.k_scale_f16 + so) | static_cast<uint32_t>(ld_in_u16(a.kv.v_scale_f16 + so)) << 16;
+                    key_scale = ld_in_u16(a.kv.k_scale_f16 + so);
+                    value_scale = ld_in_u16(a.kv.v_scale_f16 + so);
                 }
             }
         };
@@ -487,7 +510,8 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             bool ended = false;
             Segment s = {}, f = {};                 // segments is - 1 and fs - 1
             int next_page = -1;
-            uint32_t masks[2], scs[2];              // of tiles on their way
+            uint32_t masks[2];                      // of tiles on their way
+            uint16_t key_scales[2] = {0, 0}, value_scales[2] = {0, 0};
             int ahead = 0;
             // The queries of a segment: 16 lanes a row of 128 elements, 8 each, as binary16 numbers times a power of two.
             auto queries = [&](const Segment &w) {
@@ -554,10 +578,12 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                     next_page = it + 2 < in ? page_of(s, cell + ROWS) : -1;
                     if (ahead == 0) {
                         masks[0] = row_mask;
-                        scs[0] = sc;
+                        key_scales[0] = key_scale;
+                        value_scales[0] = value_scale;
                     } else {
                         masks[1] = row_mask;
-                        scs[1] = sc;
+                        key_scales[1] = key_scale;
+                        value_scales[1] = value_scale;
                     }
                     ++ahead;
                 }
@@ -588,13 +614,14 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                     if (!wait_warp(&bars->side_empty[tile % SIDES], ((tile / SIDES) & 1) ^ 1)) return false;
                     if (lane == 0) reinterpret_cast<uint32_t *>(&bars->mask[tile % SIDES])[quarter] = masks[0];
                     const int r = 32 * quarter + lane;
-                    const float vs = __half2float(__ushort_as_half(static_cast<uint16_t>(scs[0] >> 16)));
-                    scales->key[tile % SIDES][r] = __half2float(__ushort_as_half(static_cast<uint16_t>(scs[0] & 0xFFFFu)));
+                    const float vs = __half2float(__ushort_as_half(value_scales[0]));
+                    scales->key[tile % SIDES][r] = __half2float(__ushort_as_half(key_scales[0]));
                     scales->value[tile % SIDES][r] = vs;
                     // The sums' reference has to be finite, whatever the scale: within binary16's numbers.
                     scales->log_value[tile % SIDES][r] = __log2f(fminf(fmaxf(fabsf(vs), 5.9604645e-8f), 65504.0f));
                     masks[0] = masks[1];
-                    scs[0] = scs[1];
+                    key_scales[0] = key_scales[1];
+                    value_scales[0] = value_scales[1];
                     --ahead;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->side_full[tile % SIDES]);
@@ -604,10 +631,13 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 const uint32_t from = raws + (done % F::RAW) * (TILE_BYTES / 2) + 16 * (32 * quarter * 8 + lane);
                 const uint32_t to = ring + (done % STAGES) * TILE_BYTES;
                 const int c = lane & 7;
-#pragma unroll 4
+                uint4 got[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) got[e] = ld_shared_v4(from + 512 * e);
+#pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int r = 32 * quarter + 4 * e + (lane >> 3);
-                    const uint4 v = ld_shared_v4(from + 512 * e);
+                    const uint4 v = got[e];
                     const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -724,7 +754,20 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         mbar_wait(&bars->drain, 0, p.wait_ns);
         __syncwarp();
     } else if (warp > WALK_WARP) {
-        fewer_registers<FEW_REGISTERS>();   // completes the group of four whose registers the softmax takes
+        fewer_registers<FEW_REGISTERS>();
+        // ---- two warps: where the join finds each sequence's block ------------------------------
+        const int step = 2 * gridDim.x, at = 2 * blockIdx.x + (warp - WALK_WARP - 1);
+        for (int g = at; g < a.ngroups; g += step) {
+            const Group x = group_of(p, g);
+            for (int i = lane; i < x.count; i += 32) {
+                const int b = i / (2 * p.seqs);
+                p.places[x.first + i] = x.tiles > 0 ? make_int2(block_number(p, x, g, b), x.first + b * 2 * p.seqs) : make_int2(-1, 0);
+            }
+        }
+        // Sequences of no group.
+        const int begin = min(max(ld_in(a.cu), 0), a.nseq), end = min(max(ld_in(a.cu + a.ngroups), 0), a.nseq);
+        for (int s = 32 * at + lane; s < a.nseq; s += 32 * step)
+            if (s < begin || s >= end) p.places[s] = make_int2(-1, 0);
     } else {
         more_registers<MORE_REGISTERS>();
         // ---- softmax of one stream, one row per thread --------------------------------------
@@ -949,19 +992,11 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             }
             tc_fence_after_sync();
             if (!idle) {
-                const int seq = real / p.group, head = real - seq * p.group;
                 const bool valid = real < rows && !(kSplit && high);
-                const long long out_row = static_cast<long long>(s.first + (two ? i * p.seqs : 0) + seq) * a.nheads + s.kvh * p.group + head;
-                float *to = s.slot < 0 ? p.whole + out_row * SLOT_ROW
-                                       : p.slots + (static_cast<size_t>(s.slot) * 2 * ROWS + (two ? i * ROWS : 0) + real) * SLOT_ROW;
-                const uint32_t live = __ballot_sync(FULL_MASK, valid);
-                // A piece of 32 columns is staged in this stream's query tile with its 16-byte chunks at
-                // chunk ^ (row % 8) and leaves as whole 128-byte rows.
-                const uint32_t stage = base + (two ? i * TILE_BYTES : 0) + (two ? quarter : warp) * 4096;
-                char *row_to[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    row_to[e] = reinterpret_cast<char *>(__shfl_sync(FULL_MASK, reinterpret_cast<unsigned long long>(to), 4 * e + (lane >> 3))) + 16 * (lane & 7);
+                const int block_row = (two ? i * p.seqs * p.group : 0) + real;
+                const int at = s.slot < 0 ? s.row + block_row : block_row;
+                const size_t from = s.slot < 0 ? static_cast<size_t>(s.kvh) * p.whole_rows : static_cast<size_t>(s.slot) * BLOCK;
+                float4 *to = (s.slot < 0 ? p.whole : p.slots) + from * 32;
                 const int piece0 = two ? 0 : 2 * i, piece1 = two ? 4 : 2 * i + 2;   // with the same rows, half of the columns each
 #pragma unroll 1
                 for (int piece = piece0; piece < piece1; ++piece) {
@@ -970,9 +1005,6 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                     if (two) {
                         tmem_ld32(tmem + lanes + O_COL + 128 * i + 32 * piece, o);
                         tmem_ld_wait();
-                        if (!any)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = 0u;
                     } else {
                         uint32_t u[32];
                         tmem_ld32(tmem + lanes + O_COL + 32 * piece, o);
@@ -986,22 +1018,13 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             o[e] = __float_as_uint(fmaf(__uint_as_float(__shfl_xor_sync(FULL_MASK, o[e], 16)), 1.0f / 2048.0f, __uint_as_float(o[e])));
+                    if (valid)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        st_shared_v4(stage + lane * 128 + ((e ^ (lane & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                    __syncwarp();
-                    uint4 v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = 4 * e + (lane >> 3);
-                        v[e] = ld_shared_v4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if ((live >> (4 * e + (lane >> 3))) & 1u) *reinterpret_cast<uint4 *>(row_to[e] + 128 * piece) = v[e];
-                    __syncwarp();
+                        for (int e = 0; e < 8; ++e)
+                            to[sums_at(at, 8 * piece + e)] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                                         __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
                 }
-                if (valid && (two || i == 0)) *reinterpret_cast<float2 *>(to + 128) = sum;
+                if (valid && (two || i == 0)) ((s.slot < 0 ? p.whole_refs : p.slot_refs) + from)[at] = sum;
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -1016,150 +1039,159 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
     }
 }
 
-// Adds a row's partial sums: of the prefix, in the order of the CTAs that hold them, and of the
-// sequence's own cells, as paged attention left them. A warp takes kRows query heads of a sequence
-// at once; `split` warps share them, each every split-th range, and are added in order.
-constexpr int JOIN_WARPS = 8;
-template <typename QT, int kRows, int kRanges>
-__global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __grid_constant__ Params p, const PagedPartial own, int grid, int split) {
+// Adds the rows' partial sums: of the prefix, in the order of the CTAs that hold them, and of the sequences'
+// own cells, as paged attention left them. Rows are a KV head's: sequence times query heads. A warp takes 8 rows by 32
+// columns, a lane the row lane % 8 and pieces lane / 8 and + 4; `split` warps share them, each every split-th
+// range, and are added in order.
+constexpr int JOIN_WARPS = 8, JOIN_RANGES = 4;
+template <typename QT>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __grid_constant__ Params p, const PagedPartial own, int grid, int split,
+                                                                      int blocks) {
     const PrefixAttnArgs &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int s = blockIdx.x, set = warp / split, part = warp - set * split;
-    const int h0 = (blockIdx.y * (JOIN_WARPS / split) + set) * kRows;
+    const int set = warp / split, part = warp - set * split;
+    const int unit = blockIdx.x * (JOIN_WARPS / split) + set, quarter = unit & 3;
+    const int all_rows = a.nseq * p.group, row = 8 * (unit >> 2) + (lane & 7), kvh = blockIdx.y;
+    const bool valid = row < all_rows;
+    const int s = valid ? row / p.group : 0, head = valid ? row - s * p.group : 0, h = kvh * p.group + head;
+    const size_t out_row = static_cast<size_t>(s) * a.nheads + h;
+    const int chunk = 8 * quarter + (lane >> 3);
     // Before the wait: prefix_kernel let paged attention's kernel start, and that this grid, only after it
-    // had waited for its own predecessors, so groups and lengths are final.
-    // The group that sequence s is of: the last that begins at or before it.
-    int lo = -1, hi = a.ngroups + 1;
-    const int own_len = ld_in(a.lens + s);
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, g = lo + (lane + 1) * step;
-        const int below = __popc(__ballot_sync(FULL_MASK, g < hi && min(max(ld_in(a.cu + g), 0), a.nseq) <= s));
-        lo += below * step;
-        hi = min(hi, lo + step);
-    }
-    Group x = {};
-    if (lo >= 0 && lo < a.ngroups) x = group_of(p, lo);
-    const bool shared = x.tiles > 0 && s < x.first + x.count;
-    const int b = (s - x.first) / (2 * p.seqs), in_block = s - x.first - b * 2 * p.seqs;
-    const int row0 = in_block < p.seqs ? in_block * p.group : ROWS + (in_block - p.seqs) * p.group;   // of the block's rows
-    const size_t block = static_cast<size_t>(x.first / (2 * p.seqs) + lo + b) * a.kv.nkv;
-    const bool mine = own_len > 0 && a.table_cols > 0;
+    // had waited for its own predecessors, so lengths are final.
+    const bool mine = valid && a.table_cols > 0 && ld_in(a.lens + s) > 0;
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // Where a row's ranges lie: number i of the prefix is at the first place, then every `next` bytes from the second.
-    const float *at0[kRows], *at1[kRows], *own0[kRows], *own1[kRows];
-    int n[kRows], all[kRows], most = 0;
-    const size_t slot_bytes = static_cast<size_t>(2 * ROWS) * SLOT_ROW, own_slot = static_cast<size_t>(own.heads_per_unit) * SLOT_ROW;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        const int h = min(h0 + r, a.nheads - 1), kvh = h / p.group, in_group = h - kvh * p.group;
-        const size_t out_row = static_cast<size_t>(s) * a.nheads + h;
-        n[r] = 0;
-        if (shared) {
-            const int2 m = __ldcg(p.meta + block + kvh);
-            // Nothing but numbers is taken from scratch: a CTA that gave up may have left anything.
-            const int first = min(max(m.x, 0), 2 * grid - 1);
-            at0[r] = m.x < 0 ? p.whole + out_row * SLOT_ROW : p.slots + first * slot_bytes + static_cast<size_t>(row0 + in_group) * SLOT_ROW;
-            at1[r] = p.slots + (first & ~1) * slot_bytes + static_cast<size_t>(row0 + in_group) * SLOT_ROW;
-            n[r] = m.x < 0 ? 1 : max(0, min(m.y, grid - 1) - (first >> 1) + 1);
+    // Where this lane's ranges lie: the first, then every second slot from the next CTA's on.
+    const float4 *sums0 = p.whole, *sums1 = p.slots;
+    const float2 *refs0 = p.whole_refs, *refs1 = p.slot_refs;
+    const float *own0 = own.rows, *own1 = own.slots;
+    int n = 0, most = 0;
+    const int2 place = valid ? __ldcg(p.places + s) : make_int2(-1, 0);
+    const int part_of = head / own.heads_per_unit;
+    const int4 w = mine ? __ldcg(own.meta + static_cast<size_t>(s) * own.units + kvh * own.parts + part_of) : make_int4(0, 0, 0, 0);
+    if (place.x >= 0) {
+        // Nothing but numbers is taken from scratch: a CTA that gave up may have left anything.
+        const int block = min(place.x, blocks - 1), first = min(max(place.y, max(0, s - 2 * p.seqs + 1)), s);
+        const int2 m = __ldcg(p.meta + static_cast<size_t>(block) * a.kv.nkv + kvh);
+        const int at = (s - first) * p.group + head;
+        if (m.x < 0) {
+            const size_t from = static_cast<size_t>(kvh) * p.whole_rows;
+            const int whole = min(whole_row(p, block, first) + at, p.whole_rows - 1);
+            sums0 += from * 32 + sums_at(whole, chunk);
+            refs0 += from + whole;
+            n = 1;
+        } else {
+            const int slot = min(m.x, 2 * grid - 1), c0 = slot >> 1;
+            sums0 = p.slots + static_cast<size_t>(slot) * (BLOCK * 32) + sums_at(at, chunk);
+            refs0 = p.slot_refs + slot * BLOCK + at;
+            sums1 += static_cast<size_t>(2 * c0) * (BLOCK * 32) + sums_at(at, chunk);
+            refs1 += 2 * c0 * BLOCK + at;
+            n = max(1, min(m.y, grid - 1) - c0 + 1);
         }
-        all[r] = n[r];
-        if (mine) {
-            const int part_of = in_group / own.heads_per_unit;
-            const int4 w = __ldcg(own.meta + static_cast<size_t>(s) * own.units + kvh * own.parts + part_of);
-            const int first = min(max(w.z, 0), 2 * own.grid - 1);
-            const size_t head = static_cast<size_t>(in_group - part_of * own.heads_per_unit) * SLOT_ROW;
-            own0[r] = w.x < 0 ? own.rows + out_row * SLOT_ROW : own.slots + first * own_slot + head;
-            own1[r] = own.slots + (first & ~1) * own_slot + head;
-            all[r] += w.x < 0 ? 1 : max(0, min(w.w, own.grid - 1) - (first >> 1) + 1);
+    }
+    int all = n;
+    if (mine) {
+        const size_t in_slot = static_cast<size_t>(head - part_of * own.heads_per_unit) * OWN_ROW + 4 * chunk;
+        const size_t own_slot = static_cast<size_t>(own.heads_per_unit) * OWN_ROW;
+        if (w.x < 0) {
+            own0 += out_row * OWN_ROW + 4 * chunk;
+            all += 1;
+        } else {
+            const int slot = min(max(w.z, 0), 2 * own.grid - 1), c0 = slot >> 1;
+            own0 = own.slots + slot * own_slot + in_slot;
+            own1 += 2 * c0 * own_slot + in_slot;
+            all += max(1, min(w.w, own.grid - 1) - c0 + 1);
         }
-        most = max(most, all[r]);
     }
-    float top[kRows], l[kRows];
-    float4 y[kRows];
+    most = __reduce_max_sync(FULL_MASK, all);
+    float top = -INFINITY, l = 0.0f;
+    float4 y[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    auto add = [&](float2 ml, const float4 (&v)[2]) {
+        const float t = fmaxf(top, ml.x), ref = t == -INFINITY ? 0.0f : t;
+        const float f = ex2(top - ref), g = ex2(ml.x - ref);
+        top = t;
+        l = fmaf(ml.y, g, l * f);
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        top[r] = -INFINITY;
-        l[r] = 0.0f;
-        y[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    auto add = [&](int r, float2 ml, float4 v) {
-        const float t = fmaxf(top[r], ml.x), ref = t == -INFINITY ? 0.0f : t;
-        const float f = ex2(top[r] - ref), g = ex2(ml.x - ref);
-        top[r] = t;
-        l[r] = fmaf(ml.y, g, l[r] * f);
-        y[r].x = fmaf(v.x, g, y[r].x * f);
-        y[r].y = fmaf(v.y, g, y[r].y * f);
-        y[r].z = fmaf(v.z, g, y[r].z * f);
-        y[r].w = fmaf(v.w, g, y[r].w * f);
+        for (int e = 0; e < 2; ++e) {
+            y[e].x = fmaf(v[e].x, g, y[e].x * f);
+            y[e].y = fmaf(v[e].y, g, y[e].y * f);
+            y[e].z = fmaf(v[e].z, g, y[e].z * f);
+            y[e].w = fmaf(v[e].w, g, y[e].w * f);
+        }
     };
-    for (int i0 = part; i0 < most; i0 += split * kRanges) {
-        float2 ml[kRanges][kRows];
-        float4 v[kRanges][kRows];
+    for (int i0 = part; i0 < most; i0 += split * JOIN_RANGES) {
+        float2 ml[JOIN_RANGES];
+        float4 v[JOIN_RANGES][2];
 #pragma unroll
-        for (int e = 0; e < kRanges; ++e)
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const int i = i0 + split * e, j = i - n[r];
-                ml[e][r] = make_float2(-INFINITY, 0.0f);
-                v[e][r] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < all[r]) {
-                    const float *at = j < 0 ? (i == 0 ? at0[r] : at1[r] + 2 * i * slot_bytes) : (j == 0 ? own0[r] : own1[r] + 2 * j * own_slot);
-                    ml[e][r] = __ldcg(reinterpret_cast<const float2 *>(at + 128));
-                    v[e][r] = ld_in(reinterpret_cast<const float4 *>(at) + lane);
-                }
+        for (int e = 0; e < JOIN_RANGES; ++e) {
+            const int i = i0 + split * e, j = i - n;
+            ml[e] = make_float2(-INFINITY, 0.0f);
+            v[e][0] = v[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < n) {
+                const float4 *at = i == 0 ? sums0 : sums1 + static_cast<size_t>(2 * i) * (BLOCK * 32);
+                ml[e] = __ldcg(i == 0 ? refs0 : refs1 + 2 * i * BLOCK);
+                v[e][0] = ld_in(at);
+                v[e][1] = ld_in(at + 4 * 8);
+            } else if (i < all) {
+                const float *at = j == 0 ? own0 : own1 + 2 * j * static_cast<size_t>(own.heads_per_unit) * OWN_ROW;
+                ml[e] = __ldcg(reinterpret_cast<const float2 *>(at - 4 * chunk + 128));
+                v[e][0] = ld_in(reinterpret_cast<const float4 *>(at));
+                v[e][1] = ld_in(reinterpret_cast<const float4 *>(at + 16));
             }
-#pragma unroll
-        for (int e = 0; e < kRanges; ++e)
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) add(r, ml[e][r], v[e][r]);
-    }
-    __shared__ float4 sums[JOIN_WARPS][kRows][32];
-    __shared__ float2 weights[JOIN_WARPS][kRows];
-    if (split > 1) {
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            sums[warp][r][lane] = y[r];
-            if (lane == 0) weights[warp][r] = make_float2(top[r], l[r]);
         }
+#pragma unroll
+        for (int e = 0; e < JOIN_RANGES; ++e) add(ml[e], v[e]);
+    }
+    __shared__ float4 sums[JOIN_WARPS][2][32];
+    __shared__ float2 refs[JOIN_WARPS][32];
+    if (split > 1) {
+        sums[warp][0][lane] = y[0];
+        sums[warp][1][lane] = y[1];
+        refs[warp][lane] = make_float2(top, l);
         __syncthreads();
         if (part > 0) return;
-        for (int o = 1; o < split; ++o)
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) add(r, weights[warp + o][r], sums[warp + o][r][lane]);
+        for (int o = 1; o < split; ++o) {
+            const float4 v[2] = {sums[warp + o][0][lane], sums[warp + o][1][lane]};
+            add(refs[warp + o][lane], v);
+        }
     }
+    if (!valid) return;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    QT *out = static_cast<QT *>(a.out) + out_row * 128 + 4 * chunk;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        if (h0 + r >= a.nheads) break;
-        const size_t out_row = static_cast<size_t>(s) * a.nheads + h0 + r;
-        const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
-        store4(static_cast<QT *>(a.out) + out_row * 128 + 4 * lane, make_float4(y[r].x * inv, y[r].y * inv, y[r].z * inv, y[r].w * inv));
-        if (lane == 0 && a.lse != nullptr) a.lse[out_row] = l[r] == 0.0f ? -INFINITY : (top[r] + log2f(l[r])) * LN2;
-    }
+    for (int e = 0; e < 2; ++e) store4(out + 16 * e, make_float4(y[e].x * inv, y[e].y * inv, y[e].z * inv, y[e].w * inv));
+    if (chunk == 0 && a.lse != nullptr) a.lse[out_row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * LN2;
 }
 
 int seqs_of(int group, bool split) { return (split ? 64 : 128) / group; }
 
 struct Layout {
-    size_t meta, whole, slots, own, bytes;
-    int grid;
+    size_t meta, places, whole, whole_refs, slots, slot_refs, own, bytes;
+    int grid, blocks, whole_rows;
 };
 // q_fp32 only changes how many sequences a row tile takes: the scratch is laid out for the smaller number.
 Layout layout(const PrefixAttnSizes &z) {
     Layout y;
     const int seqs = std::max(1, seqs_of(z.nheads / z.nkv, true));
-    const long long blocks = z.nseq / (2 * seqs) + z.ngroups + 1;
-    const long long tiles = (static_cast<long long>(z.prefix_capacity) + ROWS - 1) / ROWS * blocks * z.nkv;
+    y.blocks = z.nseq / (2 * seqs) + z.ngroups + 1;
+    y.whole_rows = (z.nseq * (z.nheads / z.nkv) + 7) / 8 * 8 + 8 * (y.blocks + 1);
+    const long long tiles = (static_cast<long long>(z.prefix_capacity) + ROWS - 1) / ROWS * y.blocks * z.nkv;
     y.grid = static_cast<int>(std::max(1LL, std::min<long long>(device_sm_count(), tiles)));
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     size_t at = 0;
     y.meta = at;
-    at += up(sizeof(int2) * blocks * z.nkv);
+    at += up(sizeof(int2) * y.blocks * z.nkv);
+    y.places = at;
+    at += up(sizeof(int2) * z.nseq);
     y.whole = at;
-    at += up(sizeof(float) * z.nseq * static_cast<size_t>(z.nheads) * SLOT_ROW);
+    at += up(sizeof(float4) * 32 * z.nkv * y.whole_rows);
+    y.whole_refs = at;
+    at += up(sizeof(float2) * z.nkv * y.whole_rows);
     y.slots = at;
-    at += up(sizeof(float) * 2 * y.grid * 2 * ROWS * SLOT_ROW);
+    at += up(sizeof(float4) * 32 * BLOCK * 2 * y.grid);
+    y.slot_refs = at;
+    at += up(sizeof(float2) * BLOCK * 2 * y.grid);
     y.own = at;
     at += paged_partial_bytes(z.nseq, z.nheads, z.nkv, z.capacity);
     y.bytes = at;
@@ -1200,15 +1232,12 @@ cudaError_t run(Params &p, const Layout &y, const PagedAttnArgs &own_args, cudaS
     // Ranges of a block, on average.
     const int ranges = y.grid / (p.a.kv.nkv * std::max(1, std::max(p.a.ngroups, p.a.nseq / (2 * p.seqs)))) + 1;
     // As many warps share rows as there are ranges for and the GPU has room for at once.
-    constexpr int ROWS_AT_ONCE = 2;
-    const long long warps = static_cast<long long>(p.a.nseq) * ((p.a.nheads + ROWS_AT_ONCE - 1) / ROWS_AT_ONCE);
+    const long long units = static_cast<long long>((p.a.nseq * p.group + 7) / 8) * 4;   // of a KV head
     int split = 1;
-    while (split < JOIN_WARPS && 2 * split <= ranges && 2 * split * warps <= 16LL * device_sm_count()) split *= 2;
-    auto join = [&](auto kernel, int rows) {
-        const int heads = rows * (JOIN_WARPS / split);   // of a CTA
-        return launch(kernel, dim3(p.a.nseq, (p.a.nheads + heads - 1) / heads), 32 * JOIN_WARPS, 0, stream, p, own, y.grid, split);
-    };
-    return join(prefix_join_kernel<QT, ROWS_AT_ONCE, 4>, ROWS_AT_ONCE);
+    while (split < JOIN_WARPS && 2 * split <= ranges && 2 * split * units * p.a.kv.nkv <= 16LL * device_sm_count()) split *= 2;
+    const int per = JOIN_WARPS / split;
+    return launch(prefix_join_kernel<QT>, dim3(static_cast<unsigned>((units + per - 1) / per), p.a.kv.nkv), 32 * JOIN_WARPS, 0, stream, p, own,
+                  y.grid, split, y.blocks);
 }
 
 }  // namespace
@@ -1224,8 +1253,12 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs &a, cudaStream_t stream) {
     const Layout y = layout({a.nseq, a.ngroups, a.nheads, a.kv.nkv, p.capacity, a.table_cols * a.kv.page_size});
     char *b = static_cast<char *>(a.scratch);
     p.meta = reinterpret_cast<int2 *>(b + y.meta);
-    p.whole = reinterpret_cast<float *>(b + y.whole);
-    p.slots = reinterpret_cast<float *>(b + y.slots);
+    p.places = reinterpret_cast<int2 *>(b + y.places);
+    p.whole = reinterpret_cast<float4 *>(b + y.whole);
+    p.whole_refs = reinterpret_cast<float2 *>(b + y.whole_refs);
+    p.slots = reinterpret_cast<float4 *>(b + y.slots);
+    p.slot_refs = reinterpret_cast<float2 *>(b + y.slot_refs);
+    p.whole_rows = y.whole_rows;
     // Waits last as long as a CTA's whole range may: some 2 us a tile.
     const long long tiles = (static_cast<long long>(p.capacity) + ROWS - 1) / ROWS * a.kv.nkv * (a.nseq + a.ngroups);
     p.wait_ns = wait_limit_ns() + 8192ull * static_cast<uint64_t>(std::min(tiles / y.grid + 1, 1LL << 24));
