@@ -104,6 +104,9 @@ __device__ __forceinline__ Group group_of(const Params &p, int g) {
     return x;
 }
 
+__device__ __forceinline__ long long tiles_in(const Params &p, const Group &x) {
+    return static_cast<long long>(x.tiles) * x.blocks * p.a.kv.nkv;
+}
 // Block b of group g, among all.
 __device__ __forceinline__ int block_number(const Params &p, const Group &x, int g, int b) { return x.first / (2 * p.seqs) + g + b; }
 // First row of a whole block's partial results (of a KV head): a multiple of 8, and behind the rows of the blocks before it.
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
     constexpr bool kInt8 = F::kInt8, kSplit = F::kSplit;
     constexpr int STAGES = F::STAGES;
     extern __shared__ unsigned char raw_smem[];
-    __shared__ long long sh_scan[PTHREADS / 32];
+    __shared__ long long sh_scan[PTHREADS / 32 - MMA_WARP];
     __shared__ Group sh_at;                     // the group that the range begins in
     __shared__ int sh_group, sh_kvh, sh_block, sh_tile;
     const PrefixAttnArgs &a = p.a;
@@ -269,61 +272,65 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         for (int i = 0; i < 4; ++i) mbar_init(&bars->pair[i], 2);
         mbar_init(&bars->drain, 1);
         bars->abort = 0;
-        sh_group = -1;
         fence_mbar_init();
     }
-    grid_dependency_wait();
-    grid_launch_dependents();
-
-    // ---- this CTA's range of tiles -------------------------------------------------
-    const int each = (a.ngroups + PTHREADS - 1) / PTHREADS;
-    const int g0 = min(tid * each, a.ngroups), g1 = min(g0 + each, a.ngroups);
-    auto tiles_in = [&](const Group &x) { return static_cast<long long>(x.tiles) * x.blocks * a.kv.nkv; };
-    long long mine = 0;
-    Group own_group = {};                       // the last of this thread's, read once where it is the only one
-    for (int g = g0; g < g1; ++g) {
-        own_group = group_of(p, g);
-        mine += tiles_in(own_group);
-    }
-    long long before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(FULL_MASK, before, o);
-        if (lane >= o) before += y;
-    }
-    if (lane == 31) sh_scan[warp] = before;
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    long long all = 0;
-#pragma unroll
-    for (int w = 0; w < PTHREADS / 32; ++w) {
-        if (w < warp) before += sh_scan[w];
-        all += sh_scan[w];
-    }
-    before -= mine;
-    const long long per = quotient(all + gridDim.x - 1, gridDim.x);
-    const long long x0 = per * blockIdx.x, x1 = min(x0 + per, all);
-    if (x0 < x1 && x0 >= before && x0 < before + mine) {
-        long long b = before;
-        int g = g0;
-        Group x = own_group;
-        if (g1 - g0 > 1) {
-            x = group_of(p, g);
-            for (long long n = tiles_in(x); x0 >= b + n; n = tiles_in(x)) {
-                b += n;
-                x = group_of(p, ++g);
-            }
-        }
-        const long long unit = quotient(x0 - b, x.tiles), kvh = quotient(unit, x.blocks);
-        sh_at = x;
-        sh_group = g;
-        sh_kvh = static_cast<int>(kvh);
-        sh_block = static_cast<int>(unit - kvh * x.blocks);
-        sh_tile = static_cast<int>(x0 - b - unit * x.tiles);
-    }
-    __syncthreads();
     const uint32_t tmem = bars->tmem;
+    long long per = 0, x1 = 0, range = 0;           // tiles of a CTA, the range's end and length (not in softmax warps)
+    if (warp >= MMA_WARP) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+        // ---- this CTA's range of tiles -------------------------------------------------
+        constexpr int FINDERS = PTHREADS - 32 * MMA_WARP;
+        const int me = tid - 32 * MMA_WARP, each = (a.ngroups + FINDERS - 1) / FINDERS;
+        const int g0 = min(me * each, a.ngroups), g1 = min(g0 + each, a.ngroups);
+        long long mine = 0;
+        Group own_group = {};                       // the last of this thread's, read once where it is the only one
+        for (int g = g0; g < g1; ++g) {
+            own_group = group_of(p, g);
+            mine += tiles_in(p, own_group);
+        }
+        long long before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(FULL_MASK, before, o);
+            if (lane >= o) before += y;
+        }
+        if (lane == 31) sh_scan[warp - MMA_WARP] = before;
+        named_bar_sync(1, FINDERS);
+        long long all = 0;
+#pragma unroll
+        for (int w = 0; w < FINDERS / 32; ++w) {
+            if (w < warp - MMA_WARP) before += sh_scan[w];
+            all += sh_scan[w];
+        }
+        before -= mine;
+        per = quotient(all + gridDim.x - 1, gridDim.x);
+        const long long x0 = per * blockIdx.x;
+        x1 = min(x0 + per, all);
+        range = max(0LL, x1 - x0);
+        if (range > 0 && x0 >= before && x0 < before + mine) {
+            long long b = before;
+            int g = g0;
+            Group x = own_group;
+            if (g1 - g0 > 1) {
+                x = group_of(p, g);
+                for (long long n = tiles_in(p, x); x0 >= b + n; n = tiles_in(p, x)) {
+                    b += n;
+                    x = group_of(p, ++g);
+                }
+            }
+            const long long unit = quotient(x0 - b, x.tiles), kvh = quotient(unit, x.blocks);
+            sh_at = x;
+            sh_group = g;
+            sh_kvh = static_cast<int>(kvh);
+            sh_block = static_cast<int>(unit - kvh * x.blocks);
+            sh_tile = static_cast<int>(x0 - b - unit * x.tiles);
+        }
+        named_bar_sync(1, FINDERS);
+    }
 
     // A wait of the pipeline: the first that runs out sets the error word, and
     // all later ones return at once.
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
     if (warp == WALK_WARP) {
         fewer_registers<FEW_REGISTERS>();
         // ---- the segments of the range ----------------------------------------------------
-        long long left = sh_group < 0 ? 0 : x1 - x0;
+        long long left = range;
         int g = sh_group, kvh = sh_kvh, b = sh_block, t = sh_tile;   // unused without a group
         Group x = sh_at;
         for (uint32_t k = 0;; ++k) {
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                         kvh = 0;
                         // The next group that has tiles: 32 at a time.
                         for (int from = g + 1; left > 0; from += 32) {
-                            const bool have = from + lane < a.ngroups && tiles_in(group_of(p, from + lane)) > 0;
+                            const bool have = from + lane < a.ngroups && tiles_in(p, group_of(p, from + lane)) > 0;
                             const uint32_t found = __ballot_sync(FULL_MASK, have);
                             if (found != 0u) {
                                 g = from + __ffs(found) - 1;
@@ -503,16 +510,10 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 if (ok && lane == 0) mbar_arrive(&bars->seg_empty[k % SEGS]);
             }
         } else {
-            // Copies of int8 tiles run ahead of their conversion; every thread converts what it copied.
-            uint32_t issued = 0, done = 0;          // tiles of keys or values (even: keys)
-            uint32_t is = 0, fs = 0;                // segments begun, and finished with
-            int it = 0, in = 0, ft = 0, fn = 0;     // tiles issued of segment is - 1 and their number; done of fs - 1
-            bool ended = false;
-            Segment s = {}, f = {};                 // segments is - 1 and fs - 1
-            int next_page = -1;
-            uint32_t masks[2];                      // of tiles on their way
-            uint16_t key_scales[2] = {0, 0}, value_scales[2] = {0, 0};
-            int ahead = 0;
+            // Copies of int8 tiles run ahead of their conversion: keys and values of one tile and the next
+            // one's keys are under way. Every thread converts what it copied.
+            uint32_t kv = 0, tile = 0;              // tiles of keys or values converted, of cells
+            uint32_t sent = 0;                      // of keys or values copied
             // The queries of a segment: 16 lanes a row of 128 elements, 8 each, as binary16 numbers times a power of two.
             auto queries = [&](const Segment &w) {
                 constexpr int STEPS = F::REAL / (2 * COPY_WARPS);
@@ -554,41 +555,9 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->q_full);
             };
-            auto can_issue = [&]() {
-                if (ended || issued - done >= F::RAW) return false;
-                if (it == in) {                      // a new segment
-                    if (!ready_warp(&bars->seg_full[is % SEGS], (is / SEGS) & 1)) return false;
-                    s = bars->seg[is % SEGS];
-                    __syncwarp();
-                    ++is;
-                    if (s.count == 0) {
-                        ended = true;
-                        return false;
-                    }
-                    it = 0;
-                    in = 2 * (s.t1 - s.t0);
-                    next_page = page_of(s, s.t0 * ROWS + 32 * quarter + lane);
-                }
-                return true;
-            };
-            auto issue = [&]() {
-                if (!(it & 1)) {
-                    const int cell = (s.t0 + (it >> 1)) * ROWS + 32 * quarter + lane;
-                    find_row(s, cell, next_page);
-                    next_page = it + 2 < in ? page_of(s, cell + ROWS) : -1;
-                    if (ahead == 0) {
-                        masks[0] = row_mask;
-                        key_scales[0] = key_scale;
-                        value_scales[0] = value_scale;
-                    } else {
-                        masks[1] = row_mask;
-                        key_scales[1] = key_scale;
-                        value_scales[1] = value_scale;
-                    }
-                    ++ahead;
-                }
-                const char *from = static_cast<const char *>((it & 1) ? a.kv.v : a.kv.k) + 16 * (lane & 7);
-                const uint32_t to = raws + (issued % F::RAW) * (TILE_BYTES / 2) + 16 * (32 * quarter * 8 + lane);
+            auto send = [&](const void *what) {
+                const char *from = static_cast<const char *>(what) + 16 * (lane & 7);
+                const uint32_t to = raws + (sent % F::RAW) * (TILE_BYTES / 2) + 16 * (32 * quarter * 8 + lane);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int r = 4 * e + (lane >> 3);
@@ -596,40 +565,14 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                     cp_async_16_or_zero(to + 512 * e, from + ro, (row_mask >> r) & 1u);
                 }
                 cp_async_commit();
-                ++issued;
-                ++it;
+                ++sent;
             };
-            // The oldest tile on its way: waited for, made operands, and signalled.
-            auto finish = [&]() {
-                if (ft == fn) {                      // the first of its segment
-                    f = bars->seg[fs % SEGS];
-                    if (!wait_warp(&bars->q_empty, (fs & 1) ^ 1)) return false;
-                    queries(f);
-                    ++fs;
-                    ft = 0;
-                    fn = 2 * (f.t1 - f.t0);
-                }
-                const uint32_t tile = done >> 1;
-                if (!(done & 1u)) {
-                    if (!wait_warp(&bars->side_empty[tile % SIDES], ((tile / SIDES) & 1) ^ 1)) return false;
-                    if (lane == 0) reinterpret_cast<uint32_t *>(&bars->mask[tile % SIDES])[quarter] = masks[0];
-                    const int r = 32 * quarter + lane;
-                    const float vs = __half2float(__ushort_as_half(value_scales[0]));
-                    scales->key[tile % SIDES][r] = __half2float(__ushort_as_half(key_scales[0]));
-                    scales->value[tile % SIDES][r] = vs;
-                    // The sums' reference has to be finite, whatever the scale: within binary16's numbers.
-                    scales->log_value[tile % SIDES][r] = __log2f(fminf(fmaxf(fabsf(vs), 5.9604645e-8f), 65504.0f));
-                    masks[0] = masks[1];
-                    key_scales[0] = key_scales[1];
-                    value_scales[0] = value_scales[1];
-                    --ahead;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->side_full[tile % SIDES]);
-                }
-                if (!wait_warp(&bars->kv_empty[done % STAGES], ((done / STAGES) & 1) ^ 1)) return false;
-                cp_async_wait_at_most(static_cast<int>(issued - done) - 1);
-                const uint32_t from = raws + (done % F::RAW) * (TILE_BYTES / 2) + 16 * (32 * quarter * 8 + lane);
-                const uint32_t to = ring + (done % STAGES) * TILE_BYTES;
+            // The oldest tile on its way, as binary16 operands. `under_way`: copies behind it.
+            auto convert = [&](int under_way) {
+                if (!wait_warp(&bars->kv_empty[kv % STAGES], ((kv / STAGES) & 1) ^ 1)) return false;
+                cp_async_wait_at_most(under_way);
+                const uint32_t from = raws + (kv % F::RAW) * (TILE_BYTES / 2) + 16 * (32 * quarter * 8 + lane);
+                const uint32_t to = ring + (kv % STAGES) * TILE_BYTES;
                 const int c = lane & 7;
                 uint4 got[8];
 #pragma unroll
@@ -637,24 +580,84 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int r = 32 * quarter + 4 * e + (lane >> 3);
-                    const uint4 v = got[e];
-                    const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+                    const uint32_t w[4] = {got[e].x ^ 0x80808080u, got[e].y ^ 0x80808080u, got[e].z ^ 0x80808080u, got[e].w ^ 0x80808080u};
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         st_shared_v4(to + tile_at(r, 2 * c + h), codes_to_half2(w[2 * h], 0x4140), codes_to_half2(w[2 * h], 0x4342),
                                      codes_to_half2(w[2 * h + 1], 0x4140), codes_to_half2(w[2 * h + 1], 0x4342));
                 }
                 __syncwarp();
-                if (lane == 0 && !(p.stall != 0 && blockIdx.x == 0 && done == 0)) mbar_arrive(&bars->kv_full[done % STAGES]);
-                ++done;
-                if (++ft == fn && lane == 0) mbar_arrive(&bars->seg_empty[(fs - 1) % SEGS]);
+                if (lane == 0 && !(p.stall != 0 && blockIdx.x == 0 && kv == 0)) mbar_arrive(&bars->kv_full[kv % STAGES]);
+                ++kv;
                 return true;
             };
-            while (ok) {
-                if (can_issue()) issue();
-                else if (issued != done) ok = finish();
-                else if (ended) break;
-                else ok = wait_warp(&bars->seg_full[is % SEGS], (is / SEGS) & 1);
+            Segment s = {}, next = {};              // of the tile that is converted, of the one that is copied
+            uint32_t k = 0;                         // segments begun with copies
+            int t = 0, t_next = 0, page = -1;       // page: of this lane's row of the tile to copy next
+            auto enter = [&]() {                    // the next segment's first tile is to be copied next
+                if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) return false;
+                next = bars->seg[k % SEGS];
+                __syncwarp();
+                ++k;
+                t_next = next.t0;
+                page = page_of(next, t_next * ROWS + 32 * quarter + lane);
+                return true;
+            };
+            uint32_t mask = 0;                      // of the tile that is converted, as its scales
+            uint16_t scale_k = 0, scale_v = 0;
+            auto row = [&]() {                      // the row of the tile to copy, and the page of the one behind it
+                const int cell = t_next * ROWS + 32 * quarter + lane;
+                find_row(next, cell, page);
+                page = t_next + 1 < next.t1 ? page_of(next, cell + ROWS) : -1;
+            };
+            ok = enter();
+            if (ok && next.count > 0) {
+                row();
+                send(a.kv.k);
+                send(a.kv.v);
+            }
+            uint32_t converted = 0;                 // segments begun with conversions
+            while (ok && next.count > 0) {
+                const bool first = t_next == next.t0;
+                s = next;
+                t = t_next;
+                mask = row_mask;
+                scale_k = key_scale;
+                scale_v = value_scale;
+                const uint32_t seg = k - 1;
+                bool more = ++t_next < next.t1;
+                if (!more) {
+                    ok = enter();
+                    if (!ok) break;
+                    more = next.count > 0;
+                }
+                if (more) {
+                    row();
+                    send(a.kv.k);
+                }
+                if (first) {
+                    ok = wait_warp(&bars->q_empty, (converted & 1) ^ 1);
+                    if (!ok) break;
+                    queries(s);
+                    ++converted;
+                }
+                const uint32_t side = tile % SIDES;
+                ok = wait_warp(&bars->side_empty[side], ((tile / SIDES) & 1) ^ 1);
+                if (!ok) break;
+                if (lane == 0) reinterpret_cast<uint32_t *>(&bars->mask[side])[quarter] = mask;
+                const float vs = __half2float(__ushort_as_half(scale_v));
+                scales->key[side][32 * quarter + lane] = __half2float(__ushort_as_half(scale_k));
+                scales->value[side][32 * quarter + lane] = vs;
+                // The sums' reference has to be finite, whatever the scale: within binary16's numbers.
+                scales->log_value[side][32 * quarter + lane] = __log2f(fminf(fmaxf(fabsf(vs), 5.9604645e-8f), 65504.0f));
+                ++tile;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->side_full[side]);
+                ok = convert(more ? 2 : 1);
+                if (!ok) break;
+                if (more) send(a.kv.v);
+                ok = convert(more ? 2 : 0);
+                if (ok && t + 1 == s.t1 && lane == 0) mbar_arrive(&bars->seg_empty[seg % SEGS]);
             }
         }
         cp_async_wait<0>();
@@ -717,11 +720,11 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 const uint32_t kn = kv + key_item(two || kInt8, j), vn = kv + value_item(two || kInt8, j - 1, n);
                 const uint32_t ks = kn % STAGES, vs = vn % STAGES;
                 if (two) {
-                    if (j > 0) ok = landed(vs, vn / STAGES) && outputs(I0(), vs, j == 1);
-                    if (ok && j < n) {
-                        ok = landed(ks, kn / STAGES);
-                        if (ok) scores(I0(), base, ks);
-                    }
+                    // Both copies are waited for before the weights, so that nothing stands between the products.
+                    if (j > 0) ok = landed(vs, vn / STAGES);
+                    if (ok && j < n) ok = landed(ks, kn / STAGES);
+                    if (ok && j > 0) ok = outputs(I0(), vs, j == 1);
+                    if (ok && j < n) scores(I0(), base, ks);
                     if (ok && j > 0) ok = outputs(I1(), vs, j == 1);
                     if (ok && j > 0 && one) tc_commit(&bars->kv_empty[vs]);
                     if (ok && j < n) {
@@ -776,21 +779,27 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         const uint32_t s_at = tmem + lanes + S_COL + 128 * i;
         const bool high = lane >= 16;       // fp32 queries: the remainders' rows
         uint32_t ns = 0, tiles = 0;
-        for (uint32_t k = 0;; ++k) {
-            if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
-            const Segment s = bars->seg[k % SEGS];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->seg_empty[k % SEGS]);
-            if (s.count == 0) break;
-            const bool two = s.count > p.seqs;
-            const int n = s.t1 - s.t0;
+        // Once through the code before there is anything to do, while the range is found and the first cells
+        // come: its instructions are then there. It waits for nothing, signals nothing and writes nothing.
+        bool dry = true;
+        for (uint32_t k = 0;; k += dry ? 0 : 1, dry = false) {
+            Segment s = {};
+            if (!dry) {
+                if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
+                s = bars->seg[k % SEGS];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->seg_empty[k % SEGS]);
+                if (s.count == 0) break;
+            }
+            const bool two = s.count > p.seqs || dry;
+            const int n = dry ? 1 : s.t1 - s.t0;
             const int count = !two ? s.count : i == 0 ? p.seqs : s.count - p.seqs;   // sequences of this stream's rows
             const int real = kSplit ? 16 * quarter + (lane & 15) : row;              // the row among the tile's
             const int rows = count * p.group;
-            const bool idle = (kSplit ? 16 : 32) * quarter >= rows;                  // a warp without rows
+            const bool idle = !dry && (kSplit ? 16 : 32) * quarter >= rows;          // a warp without rows
             float c = a.scale * LOG2E;
             if constexpr (kInt8) {
-                if (!wait_warp(&bars->q_full, k & 1)) break;
+                if (!dry && !wait_warp(&bars->q_full, k & 1)) break;
                 c = scales->row[(two ? i : 0) * ROWS + row];
             }
             float m = -INFINITY, l = 0.0f;   // m in base 2, LIFT not counted
@@ -798,9 +807,11 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             for (int j = 0; j < n; ++j) {
                 if (!two && (j & 1) != i) continue;
                 const uint32_t side = (tiles + j) % SIDES;
-                ok = wait_warp(&bars->s_full[i], ns & 1);
-                if (!ok) break;
-                ++ns;
+                if (!dry) {
+                    ok = wait_warp(&bars->s_full[i], ns & 1);
+                    if (!ok) break;
+                    ++ns;
+                }
                 if (idle) {
                     if (lane == 0) {
                         arrive(&bars->side_empty[side], two ? 1u : 2u);
@@ -809,7 +820,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                     }
                     continue;
                 }
-                ok = wait_warp(&bars->side_full[side], ((tiles + j) / SIDES) & 1);
+                if (!dry) ok = wait_warp(&bars->side_full[side], ((tiles + j) / SIDES) & 1);
                 if (!ok) break;
                 tc_fence_after_sync();
                 uint32_t sr[4][32];
@@ -940,16 +951,18 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                             first[e] = high ? got : pw[e];
                             second[e] = high ? pl[e] : got;
                         }
-                        tmem_st16(s_at + 16 * g, first);
-                        tmem_st16(s_at + 32 + 16 * g, second);
-                    } else {
+                        if (!dry) {
+                            tmem_st16(s_at + 16 * g, first);
+                            tmem_st16(s_at + 32 + 16 * g, second);
+                        }
+                    } else if (!dry) {
                         tmem_st16(s_at + 16 * g, pw);
                     }
                     if (g == CHUNKS - 1 || (!kSplit && g == 1)) {   // the products with half of the values can begin
                         tmem_st_wait();
                         tc_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (lane == 0 && !dry) {
                             if (kSplit || g == 1) mbar_arrive(&bars->p_half[i]);
                             if (g == CHUNKS - 1) {
                                 mbar_arrive(&bars->p_full[i]);
@@ -965,14 +978,19 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 }
                 any = true;
             }
-            tiles += n;
             if (!ok) break;
+            if (dry) {
+                grid_dependency_wait();   // results go to scratch that an earlier call may still read
+                grid_launch_dependents();
+            } else {
+                tiles += n;
+            }
             // ---- the segment's results ---------------------------------------------------------
             if constexpr (kSplit) l += __shfl_xor_sync(FULL_MASK, l, 16);
             float2 sum = make_float2(m == -INFINITY ? -INFINITY : m - F::LIFT, l);
             float f0 = 1.0f, f1 = 1.0f;
             bool any0 = any, any1 = any;
-            if (!(wait_warp(&bars->o_full[0], k & 1) && wait_warp(&bars->o_full[1], k & 1))) break;
+            if (!dry && !(wait_warp(&bars->o_full[0], k & 1) && wait_warp(&bars->o_full[1], k & 1))) break;
             if (!two) {
                 // Both streams have the same rows: their sums through the second query tile, which nothing uses.
                 float4 *shared = reinterpret_cast<float4 *>(raw_smem + (base + TILE_BYTES - smem_u32(raw_smem)));
@@ -987,12 +1005,12 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 any0 = o0.z != 0.0f;
                 any1 = o1.z != 0.0f;
                 sum = make_float2(top, fmaf(o0.y, f0, o1.y * f1));
-            } else if (lane == 0) {
+            } else if (lane == 0 && !dry) {
                 mbar_arrive(&bars->pair[quarter]);   // a phase of each segment
             }
             tc_fence_after_sync();
             if (!idle) {
-                const bool valid = real < rows && !(kSplit && high);
+                const bool valid = real < rows && !(kSplit && high) && !dry;
                 const int block_row = (two ? i * p.seqs * p.group : 0) + real;
                 const int at = s.slot < 0 ? s.row + block_row : block_row;
                 const size_t from = s.slot < 0 ? static_cast<size_t>(s.kvh) * p.whole_rows : static_cast<size_t>(s.slot) * BLOCK;
@@ -1028,7 +1046,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             }
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->q_empty);
+            if (lane == 0 && !dry) mbar_arrive(&bars->q_empty);
         }
     }
     tc_fence_before_sync();
