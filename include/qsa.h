@@ -570,8 +570,7 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
  * Sums and softmax statistics are fp32. The weights of prefix cells are rounded
  * once to the 16-bit operand type (the pages', binary16 for int8 cells), as in
  * qsa_window_attn; for fp32 queries they keep 22 bits.
- * Errors and limits as qsa_paged_attn; nheads / nkv above 128 (64 for fp32
- * queries), ngroups above 65,535 or prefix_cols * page_size above 2^30 returns
+ * Errors and limits as qsa_paged_attn; nheads / nkv above 128, ngroups above 65,535 or prefix_cols * page_size above 2^30 returns
  * QSA_ERR_UNSUPPORTED.
  */
 size_t qsa_prefix_attn_scratch_bytes(int nseq, int ngroups, int nheads, int nkv, int prefix_cols, int table_cols,

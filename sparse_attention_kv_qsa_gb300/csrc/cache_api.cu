@@ -182,7 +182,7 @@ qsa_status qsa_prefix_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_strid
     if (!good_stride(q_seq_stride, q_dtype) || !good_stride(q_head_stride, q_dtype)) return QSA_ERR_INVALID;
     if (nseq == 0) return QSA_OK;
     const int group = nheads / kv->nkv;
-    if (nseq > MAX_SEQS || ngroups > MAX_SEQS || nheads > MAX_HEADS || group > (q_dtype == QSA_F32 ? 64 : 128) ||
+    if (nseq > MAX_SEQS || ngroups > MAX_SEQS || nheads > MAX_HEADS || group > 128 ||
         static_cast<long long>(nseq) * nheads > MAX_CELLS ||
         static_cast<long long>(nseq) * nheads * ((static_cast<long long>(table_cols) * kv->page_size + 63) / 64) > MAX_TILES ||
         static_cast<long long>(nseq + ngroups) * nheads * ((static_cast<long long>(prefix_cols) * kv->page_size + 127) / 128) > MAX_TILES)

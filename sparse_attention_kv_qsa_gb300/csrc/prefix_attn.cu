@@ -32,9 +32,11 @@
 // tile's end and pages that are none; those rows arrive as zeros.
 //
 // fp32 queries (int8 cells): a row's query is scaled by a power of two and held as a
-// binary16 number and the remainder times 2^11, in two rows 16 lanes apart of the
-// tile (64 rows a tile), and so are its weights; lanes exchange halves of the
-// products, so that each finds the weights of 64 of the 128 cells.
+// binary16 number and what that left of it, another; so are its weights. Both
+// halves' products go to the same sums, the second halves being within binary16's
+// range as they are: the queries' largest is 2^13 at least, the weights' 2^7, and what
+// falls below its smallest number is 2^-32 of that or less. A block is one row tile then, its
+// two query tiles the halves.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -65,7 +67,7 @@ struct Form {
     static constexpr bool kInt8 = kKv == QSA_I8;
     static constexpr bool kSplit = std::is_same<QT, float>::value;
     using T = typename std::conditional<kKv == QSA_BF16, __nv_bfloat16, __half>::type;   // operands
-    static constexpr int REAL = kSplit ? 64 : ROWS;      // rows of a tile that are a query head
+    static constexpr int TILES = kSplit ? 1 : 2;         // row tiles of a block at most
     static constexpr int STAGES = kInt8 ? 3 : 5;         // tiles of keys or values
     static constexpr int RAW = kInt8 ? 3 : 0;            // int8 tiles on their way
     // Arrivals that make a tile complete: of every copying thread's copies, or of the warps that converted it.
@@ -78,7 +80,7 @@ struct Form {
 struct Params {
     PrefixAttnArgs a;
     Divider page;
-    int group, seqs;          // query heads per KV head; sequences of a row tile
+    int group, seqs, block;   // query heads per KV head; sequences of a row tile, and of a block
     int capacity;             // cells of a row of the prefix table
     // Partial results: sums as sums_at() says, and reference and weights' sum of each row.
     float4 *slots, *whole;    // [2 grid][BLOCK x 32]: a segment at a CTA's begin, and its last; [nkv][whole_rows x 32]
@@ -100,7 +102,7 @@ __device__ __forceinline__ Group group_of(const Params &p, int g) {
     x.count = min(max(ld_in(p.a.cu + g + 1), x.first), p.a.nseq) - x.first;
     x.len = min(max(ld_in(p.a.prefix_lens + g), 0), p.capacity);
     x.tiles = (x.len + ROWS - 1) / ROWS;
-    x.blocks = (x.count + 2 * p.seqs - 1) / (2 * p.seqs);
+    x.blocks = (x.count + p.block - 1) / p.block;
     return x;
 }
 
@@ -108,7 +110,7 @@ __device__ __forceinline__ long long tiles_in(const Params &p, const Group &x) {
     return static_cast<long long>(x.tiles) * x.blocks * p.a.kv.nkv;
 }
 // Block b of group g, among all.
-__device__ __forceinline__ int block_number(const Params &p, const Group &x, int g, int b) { return x.first / (2 * p.seqs) + g + b; }
+__device__ __forceinline__ int block_number(const Params &p, const Group &x, int g, int b) { return x.first / p.block + g + b; }
 // First row of a whole block's partial results (of a KV head): a multiple of 8, and behind the rows of the blocks before it.
 __device__ __forceinline__ int whole_row(const Params &p, int block, int first) { return ((first * p.group + 7) / 8 + block) * 8; }
 // Columns 4 chunk .. + 3 of a row, in 16-byte pieces: 8 rows' pieces are a line, so that a warp whose lanes
@@ -161,6 +163,11 @@ __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -178,11 +185,11 @@ __device__ __forceinline__ uint32_t pack<__half>(float a, float b) {
     const __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// a, b as binary16 numbers and what that left of them, times 2^11.
+// a, b as binary16 numbers, and what that left of them.
 __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
     hi = pack<__half>(a, b);
     const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    lo = pack<__half>((a - h.x) * 2048.0f, (b - h.y) * 2048.0f);
+    lo = pack<__half>(a - h.x, b - h.y);
 }
 // Bytes `sel` picks of a word of int8 codes xored with 0x80, as binary16: 0x64 above a byte u is 1024 + u.
 __device__ __forceinline__ uint32_t codes_to_half2(uint32_t w, uint32_t sel) {
@@ -218,6 +225,22 @@ __device__ __forceinline__ void more_registers() {
 template <int N>
 __device__ __forceinline__ void fewer_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// 32 consecutive fp32 columns of this thread's TMEM lane, there when it returns: load and wait are one
+// statement, because registers that a load is still to write may be copied between two.
+__device__ __forceinline__ void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
 }
 // 16-byte chunk c (of 16) of row r of a tile: two halves of 64 elements, 128-byte rows, chunks swizzled.
 __device__ __forceinline__ uint32_t tile_at(int r, int c) { return (c >> 3) * HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
@@ -359,8 +382,8 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 const int n = static_cast<int>(min(static_cast<long long>(x.tiles - t), left));
                 s.g = g;
                 s.kvh = kvh;
-                s.first = x.first + b * 2 * p.seqs;
-                s.count = min(2 * p.seqs, x.first + x.count - s.first);
+                s.first = x.first + b * p.block;
+                s.count = min(p.block, x.first + x.count - s.first);
                 s.len = x.len;
                 s.t0 = t;
                 s.t1 = t + n;
@@ -514,42 +537,43 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             // one's keys are under way. Every thread converts what it copied.
             uint32_t kv = 0, tile = 0;              // tiles of keys or values converted, of cells
             uint32_t sent = 0;                      // of keys or values copied
-            // The queries of a segment: 16 lanes a row of 128 elements, 8 each, as binary16 numbers times a power of two.
+            // The queries of a segment: 16 lanes a row of 128 elements, 8 each, times a power of two that brings
+            // the largest to 2^13 at least, as binary16 numbers (and the rest, into the second tile).
             auto queries = [&](const Segment &w) {
-                constexpr int STEPS = F::REAL / (2 * COPY_WARPS);
-                const int n0 = min(p.seqs, w.count), tiles = w.count > p.seqs ? 2 : 1;
+                constexpr int AT_ONCE = kSplit ? 2 : 4;
+                const int l = lane & 15, n0 = min(p.seqs, w.count), tiles = w.count > p.seqs ? 2 : 1;
                 const float c = a.scale * LOG2E;
-                for (int i = 0; i < tiles; ++i) {
-                    const int rows = (i == 0 ? n0 : w.count - n0) * p.group;
-                    for (int e = 0; e < STEPS; ++e) {
-                        const int r = STEPS * 2 * quarter + 2 * e + (lane >> 4), l = lane & 15;   // of the tile's real rows
-                        const bool have = r < rows;
-                        const int seq = r / p.group;
-                        const QT *qp = static_cast<const QT *>(a.q) + (have ? (w.first + i * p.seqs + seq) * a.q_seq_stride +
-                                                                                  (w.kvh * p.group + r - seq * p.group) * a.q_head_stride : 0) + 8 * l;
-                        float4 u = load4(qp), v = load4(qp + 4);
-                        if (!have) u = v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        float top = fmaxf(fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))),
-                                          fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+#pragma unroll 1
+                for (int e = 0; e < 16 * tiles; e += AT_ONCE) {
+                    const int i = e >> 4, rows = (i == 0 ? n0 : w.count - n0) * p.group;
+                    float4 u[AT_ONCE], v[AT_ONCE];
+#pragma unroll
+                    for (int q = 0; q < AT_ONCE; ++q) {
+                        const int r = 32 * quarter + 2 * (e - 16 * i + q) + (lane >> 4), seq = r / p.group;
+                        const QT *from = static_cast<const QT *>(a.q) + (w.first + i * p.seqs + seq) * a.q_seq_stride +
+                                         (w.kvh * p.group + r - seq * p.group) * a.q_head_stride + 8 * l;
+                        u[q] = r < rows ? load4(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        v[q] = r < rows ? load4(from + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int q = 0; q < AT_ONCE; ++q) {
+                        const int r = 32 * quarter + 2 * (e - 16 * i + q) + (lane >> 4);
+                        float top = fmaxf(fmaxf(fmaxf(fabsf(u[q].x), fabsf(u[q].y)), fmaxf(fabsf(u[q].z), fabsf(u[q].w))),
+                                          fmaxf(fmaxf(fabsf(v[q].x), fabsf(v[q].y)), fmaxf(fabsf(v[q].z), fabsf(v[q].w))));
 #pragma unroll
                         for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
                         int ex = 0;
                         if (top > 0.0f && top < INFINITY) frexpf(top, &ex);
-                        ex = max(-126, min(127, ex));   // both powers are fp32 numbers
-                        const float down = ldexpf(1.0f, -ex);
+                        ex = max(-113, ex);   // 2^(14 - ex) and 2^(ex - 14) are fp32 numbers
+                        const float up = ldexpf(1.0f, 14 - ex);
                         uint32_t hi[4], lo[4];
-                        split(u.x * down, u.y * down, hi[0], lo[0]);
-                        split(u.z * down, u.w * down, hi[1], lo[1]);
-                        split(v.x * down, v.y * down, hi[2], lo[2]);
-                        split(v.z * down, v.w * down, hi[3], lo[3]);
-                        // A real row r of 64 is rows 32 (r / 16) + r % 16 and 16 further.
-                        const int at = kSplit ? 32 * (r >> 4) + (r & 15) : r;
-                        st_shared_v4(base + i * TILE_BYTES + tile_at(at, l), hi[0], hi[1], hi[2], hi[3]);
-                        if (kSplit) st_shared_v4(base + i * TILE_BYTES + tile_at(at + 16, l), lo[0], lo[1], lo[2], lo[3]);
-                        if (l == 0) {
-                            scales->row[i * ROWS + at] = c * ldexpf(1.0f, ex);
-                            if (kSplit) scales->row[i * ROWS + at + 16] = c * ldexpf(1.0f, ex);
-                        }
+                        split(u[q].x * up, u[q].y * up, hi[0], lo[0]);
+                        split(u[q].z * up, u[q].w * up, hi[1], lo[1]);
+                        split(v[q].x * up, v[q].y * up, hi[2], lo[2]);
+                        split(v[q].z * up, v[q].w * up, hi[3], lo[3]);
+                        st_shared_v4(base + i * TILE_BYTES + tile_at(r, l), hi[0], hi[1], hi[2], hi[3]);
+                        if (kSplit) st_shared_v4(base + TILE_BYTES + tile_at(r, l), lo[0], lo[1], lo[2], lo[3]);
+                        if (l == 0) scales->row[i * ROWS + r] = c * ldexpf(1.0f, ex - 14);
                     }
                 }
                 __syncwarp();
@@ -670,7 +694,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         constexpr uint32_t idesc_v = idesc | (1u << 16);   // second operand contiguous in N
         bool ok = true;
         uint32_t kv = 0;                   // tiles of keys or values so far
-        uint32_t ns[2] = {0, 0};           // products S of each stream so far
+        uint32_t ns = 0;                   // products S of each stream so far, modulo 2^16
         for (uint32_t k = 0; ok; ++k) {
             if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
             const Segment s = bars->seg[k % SEGS];
@@ -686,63 +710,62 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 fence_proxy_async_smem();
                 return true;
             };
-            auto scores = [&](auto which, uint32_t q_at, uint32_t slot) {
-                constexpr int i = decltype(which)::value;
+            // Stream i's S of the keys in a slot with the queries at q_at (and the halves behind them).
+            auto scores = [&](int i, uint32_t q_at, uint32_t slot) {
                 const uint64_t qd = sw128_kmajor_desc(q_at), kd = sw128_kmajor_desc(ring + slot * TILE_BYTES);
                 tc_fence_after_sync();
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint64_t step = (kk >> 2) * (HALF >> 4) + 2 * (kk & 3);
-                    if (one) tc_mma_bf16(tmem + S_COL + 128 * i, qd + step, kd + step, idesc, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < (kSplit ? 16 : 8); ++kk) {
+                    const uint64_t step = ((kk >> 2) & 1) * (HALF >> 4) + 2 * (kk & 3);
+                    if (one) tc_mma_bf16(tmem + S_COL + 128 * i, qd + step + (kk >> 3) * (TILE_BYTES >> 4), kd + step, idesc, kk > 0 ? 1u : 0u);
                 }
                 if (one) tc_commit(&bars->s_full[i]);
-                ++ns[i];
+                ns += 1u << (16 * i);
             };
-            auto outputs = [&](auto which, uint32_t slot, bool first) {
-                constexpr int i = decltype(which)::value;
-                const uint32_t p_col = tmem + S_COL + 128 * i, o_col = tmem + O_COL + 128 * i;
+            // Stream i's last weights times the values in a slot.
+            auto outputs = [&](int i, uint32_t slot, bool first) {
+                const uint32_t p_col = tmem + S_COL + 128 * i, o_col = tmem + O_COL + 128 * i, parity = ((ns >> (16 * i)) - 1) & 1;
                 const uint64_t vd = sw128_mnmajor_desc(ring + slot * TILE_BYTES, HALF);
-                if (!wait_warp(&bars->p_half[i], (ns[i] - 1) & 1)) return false;
-                tc_fence_after_sync();
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    if (one) tc_mma_bf16_ta(o_col, p_col + 8 * kk, vd + 128 * kk, idesc_v, !first || kk > 0 ? 1u : 0u);
-                if (!wait_warp(&bars->p_full[i], (ns[i] - 1) & 1)) return false;
-                tc_fence_after_sync();
+                for (int half = 0; half < 2; ++half) {
+                    if (!wait_warp(half == 0 ? &bars->p_half[i] : &bars->p_full[i], parity)) return false;
+                    tc_fence_after_sync();
 #pragma unroll
-                for (int kk = 4; kk < 8; ++kk)
-                    if (one) tc_mma_bf16_ta(o_col, p_col + 8 * kk, vd + 128 * kk, idesc_v, 1u);
+                    for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
+                        // 16 cells' weights are 8 columns; with their remainders, 32 cells' are 16 and 16.
+                        const uint32_t at = p_col + (kSplit ? 32 * (kk >> 1) + 8 * (kk & 1) : 8 * kk);
+                        if (one) tc_mma_bf16_ta(o_col, at, vd + 128 * kk, idesc_v, !first || kk > 0 ? 1u : 0u);
+                        if (kSplit && one) tc_mma_bf16_ta(o_col, at + 16, vd + 128 * kk, idesc_v, 1u);
+                    }
+                }
                 return true;
             };
-            using I0 = std::integral_constant<int, 0>;
-            using I1 = std::integral_constant<int, 1>;
+#pragma unroll 1
             for (int j = 0; ok && j <= n; ++j) {
+                // keys of tile j, values of tile j - 1
                 const uint32_t kn = kv + key_item(two || kInt8, j), vn = kv + value_item(two || kInt8, j - 1, n);
                 const uint32_t ks = kn % STAGES, vs = vn % STAGES;
                 if (two) {
                     // Both copies are waited for before the weights, so that nothing stands between the products.
                     if (j > 0) ok = landed(vs, vn / STAGES);
                     if (ok && j < n) ok = landed(ks, kn / STAGES);
-                    if (ok && j > 0) ok = outputs(I0(), vs, j == 1);
-                    if (ok && j < n) scores(I0(), base, ks);
-                    if (ok && j > 0) ok = outputs(I1(), vs, j == 1);
-                    if (ok && j > 0 && one) tc_commit(&bars->kv_empty[vs]);
-                    if (ok && j < n) {
-                        scores(I1(), base + TILE_BYTES, ks);
-                        if (one) tc_commit(&bars->kv_empty[ks]);
+#pragma unroll 1
+                    for (int i = 0; ok && i < 2; ++i) {
+                        if (j > 0) ok = outputs(i, vs, j == 1);
+                        if (ok && i == 1 && j > 0 && one) tc_commit(&bars->kv_empty[vs]);
+                        if (ok && j < n) scores(i, base + i * TILE_BYTES, ks);
                     }
+                    if (ok && j < n && one) tc_commit(&bars->kv_empty[ks]);
                 } else {
                     // Tile j goes to stream j % 2; the other's last weights are worked out meanwhile.
                     if (j < n) {
                         ok = landed(ks, kn / STAGES);
                         if (!ok) break;
-                        if (j & 1) scores(I1(), base, ks);
-                        else scores(I0(), base, ks);
+                        scores(j & 1, base, ks);
                         if (one) tc_commit(&bars->kv_empty[ks]);
                     }
                     if (j > 0) {
-                        ok = landed(vs, vn / STAGES) &&
-                             ((j & 1) ? outputs(I0(), vs, j <= 2) : outputs(I1(), vs, j <= 2));
+                        ok = landed(vs, vn / STAGES) && outputs((j - 1) & 1, vs, j <= 2);
                         if (ok && one) tc_commit(&bars->kv_empty[vs]);
                     }
                 }
@@ -763,8 +786,8 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         for (int g = at; g < a.ngroups; g += step) {
             const Group x = group_of(p, g);
             for (int i = lane; i < x.count; i += 32) {
-                const int b = i / (2 * p.seqs);
-                p.places[x.first + i] = x.tiles > 0 ? make_int2(block_number(p, x, g, b), x.first + b * 2 * p.seqs) : make_int2(-1, 0);
+                const int b = i / p.block;
+                p.places[x.first + i] = x.tiles > 0 ? make_int2(block_number(p, x, g, b), x.first + b * p.block) : make_int2(-1, 0);
             }
         }
         // Sequences of no group.
@@ -777,7 +800,6 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         const int i = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
         const uint32_t s_at = tmem + lanes + S_COL + 128 * i;
-        const bool high = lane >= 16;       // fp32 queries: the remainders' rows
         uint32_t ns = 0, tiles = 0;
         // Once through the code before there is anything to do, while the range is found and the first cells
         // come: its instructions are then there. It waits for nothing, signals nothing and writes nothing.
@@ -794,9 +816,8 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             const bool two = s.count > p.seqs || dry;
             const int n = dry ? 1 : s.t1 - s.t0;
             const int count = !two ? s.count : i == 0 ? p.seqs : s.count - p.seqs;   // sequences of this stream's rows
-            const int real = kSplit ? 16 * quarter + (lane & 15) : row;              // the row among the tile's
             const int rows = count * p.group;
-            const bool idle = !dry && (kSplit ? 16 : 32) * quarter >= rows;          // a warp without rows
+            const bool idle = !dry && 32 * quarter >= rows;                          // a warp without rows
             float c = a.scale * LOG2E;
             if constexpr (kInt8) {
                 if (!dry && !wait_warp(&bars->q_full, k & 1)) break;
@@ -823,151 +844,113 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 if (!dry) ok = wait_warp(&bars->side_full[side], ((tiles + j) / SIDES) & 1);
                 if (!ok) break;
                 tc_fence_after_sync();
-                uint32_t sr[4][32];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) tmem_ld32(s_at + 32 * g, sr[g]);
-                tmem_ld_wait();
-                const uint4 mask = bars->mask[side];
-                const uint32_t bits[4] = {mask.x, mask.y, mask.z, mask.w};
-                constexpr int CHUNKS = kSplit ? 2 : 4;   // of 32 cells that this lane finds the weights of
-                if constexpr (kSplit) {
-                    // Lanes below 16 take cells 0 to 63 of their row, their partners 64 to 127.
-#pragma unroll
-                    for (int g = 0; g < 2; ++g)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const uint32_t give = high ? sr[g][e] : sr[2 + g][e], keep = high ? sr[2 + g][e] : sr[g][e];
-                            const uint32_t got = __shfl_xor_sync(FULL_MASK, give, 16);
-                            const float hi = __uint_as_float(high ? got : keep), lo = __uint_as_float(high ? keep : got);
-                            sr[g][e] = __float_as_uint(fmaf(lo, 1.0f / 2048.0f, hi));
-                        }
-                }
-                const int from = kSplit && high ? 64 : 0;   // this lane's first cell
-                if constexpr (kInt8) {
-#pragma unroll
-                    for (int g = 0; g < CHUNKS; ++g)
+                // The tile goes through 32 cells at a time, twice (largest, then weights), in loops that stay
+                // rolled: read out of TMEM once and worked on straight through, the code of a tile does not
+                // stay in the instruction cache (int8 and fp32 queries took 4 us a tile, 16-bit ones 1.0).
+                auto products = [&](int g, uint64_t (&x)[16]) {
+                    uint32_t r[32];
+                    const uint32_t there = reinterpret_cast<const uint32_t *>(&bars->mask[side])[g];
+                    tmem_read32(s_at + 32 * g, r);
+                    if constexpr (kInt8) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
-                            const float4 ks = *reinterpret_cast<const float4 *>(scales->key[side] + from + 32 * g + e);
-                            sr[g][e] = __float_as_uint(__uint_as_float(sr[g][e]) * ks.x);
-                            sr[g][e + 1] = __float_as_uint(__uint_as_float(sr[g][e + 1]) * ks.y);
-                            sr[g][e + 2] = __float_as_uint(__uint_as_float(sr[g][e + 2]) * ks.z);
-                            sr[g][e + 3] = __float_as_uint(__uint_as_float(sr[g][e + 3]) * ks.w);
-                        }
-                }
-                if ((bits[0] & bits[1] & bits[2] & bits[3]) != 0xFFFFFFFFu) {
+                            const float4 ks = *reinterpret_cast<const float4 *>(scales->key[side] + 32 * g + e);
+                            float y[4];
+                            unpair(mul_pair(pair(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), pair(ks.x, ks.y)), y[0], y[1]);
+                            unpair(mul_pair(pair(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), pair(ks.z, ks.w)), y[2], y[3]);
 #pragma unroll
-                    for (int g = 0; g < CHUNKS; ++g) {
-                        const uint32_t b = kSplit && high ? bits[2 + g % 2] : bits[g];
-                        if (b == 0xFFFFFFFFu) continue;
+                            for (int q = 0; q < 4; ++q) r[e + q] = __float_as_uint(y[q]);
+                        }
+                    }
+                    if (there != 0xFFFFFFFFu) {   // behind the scales: an absent cell's is 0
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (!((b >> e) & 1u)) sr[g][e] = 0xFF800000u;
+                            if (!((there >> e) & 1u)) r[e] = 0xFF800000u;
                     }
-                }
-                uint64_t sums[2];
-                uint32_t pw[16], pl[16];
-                // Weights of 32 cells against the reference as it stands, so that they need not wait
-                // for the maximum of this tile, which rarely moves it.
-                auto weights = [&](int g) {
-                    const float mc = m == -INFINITY ? 0.0f : m - F::LIFT;
-                    const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float x0, x1;
-                        unpair(fma_pair(pair(__uint_as_float(sr[g][2 * e]), __uint_as_float(sr[g][2 * e + 1])), c2, mc2), x0, x1);
-                        x0 = ex2(x0);
-                        x1 = ex2(x1);
-                        sums[e & 1] = g == 0 && e < 2 ? pair(x0, x1) : add_pair(sums[e & 1], pair(x0, x1));
-                        if constexpr (kInt8) {
-                            const float2 vs = *reinterpret_cast<const float2 *>(scales->value[side] + from + 32 * g + 2 * e);
-                            x0 *= vs.x;
-                            x1 *= vs.y;
-                        }
-                        if constexpr (kSplit) split(x0, x1, pw[e], pl[e]);
-                        else pw[e] = pack<T>(x0, x1);
-                    }
+                    for (int e = 0; e < 16; ++e) x[e] = pair(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
                 };
-                if (!kSplit && any) weights(0);
-                float tops[8];
-                if constexpr (kInt8) {
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) {
+                    uint64_t x[16];
+                    products(g, x);
+                    if constexpr (kInt8) {
+                        const uint64_t c2 = pair(c, c);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) tops[e] = -INFINITY;
+                        for (int e = 0; e < 16; e += 2) {
+                            const float4 lv = *reinterpret_cast<const float4 *>(scales->log_value[side] + 32 * g + 2 * e);
+                            float y[4];
+                            unpair(fma_pair(x[e], c2, pair(lv.x, lv.y)), y[0], y[1]);
+                            unpair(fma_pair(x[e + 1], c2, pair(lv.z, lv.w)), y[2], y[3]);
 #pragma unroll
-                    for (int g = 0; g < CHUNKS; ++g)
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 lv = *reinterpret_cast<const float4 *>(scales->log_value[side] + from + 32 * g + e);
-                            tops[e & 4] = fmaxf(tops[e & 4], fmaf(__uint_as_float(sr[g][e]), c, lv.x));
-                            tops[(e & 4) + 1] = fmaxf(tops[(e & 4) + 1], fmaf(__uint_as_float(sr[g][e + 1]), c, lv.y));
-                            tops[(e & 4) + 2] = fmaxf(tops[(e & 4) + 2], fmaf(__uint_as_float(sr[g][e + 2]), c, lv.z));
-                            tops[(e & 4) + 3] = fmaxf(tops[(e & 4) + 3], fmaf(__uint_as_float(sr[g][e + 3]), c, lv.w));
+                            for (int q = 0; q < 4; ++q) tops[q] = fmaxf(tops[q], y[q]);
                         }
-                } else {
-                    // 8 chains, so that the maximum of 128 is not a chain of 128.
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) tops[e] = __uint_as_float(sr[0][e]);
+                        for (int e = 0; e < 16; e += 4) {
+                            float y[8];
 #pragma unroll
-                    for (int e = 8; e < 128; e += 16)
+                            for (int q = 0; q < 4; ++q) unpair(x[e + q], y[2 * q], y[2 * q + 1]);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float y = __uint_as_float(sr[e >> 5][(e & 31) + q]);
-                            tops[q] = e + 8 < 128 ? fmaxf(fmaxf(tops[q], y), __uint_as_float(sr[(e + 8) >> 5][((e + 8) & 31) + q]))
-                                                  : fmaxf(tops[q], y);
+                            for (int q = 0; q < 4; ++q) tops[q] = fmaxf(fmaxf(tops[q], y[2 * q]), y[2 * q + 1]);
                         }
+                    }
                 }
-                float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
-                                  fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
+                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 if constexpr (!kInt8) top *= c;
-                if constexpr (kSplit) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 16));
                 const bool move = top - m > LAZY;   // also true from -infinity to a finite maximum
-                if (__any_sync(FULL_MASK, move) || !any) {
+                if (__any_sync(FULL_MASK, move)) {
                     const float f = move ? ex2(m - top) : 1.0f;
                     if (move) m = top;
                     l *= f;
                     if (any) {
                         const uint32_t o_at = tmem + lanes + O_COL + 128 * i;
 #pragma unroll 1
-                        for (int g = 0; g < 8; ++g) {
-                            uint32_t o[16];
-                            tmem_ld16(o_at + 16 * g, o);
-                            tmem_ld_wait();
+                        for (int g = 0; g < 4; ++g) {
+                            uint32_t o[32];
+                            tmem_read32(o_at + 32 * g, o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(o_at + 16 * g, o);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(o_at + 32 * g, o);
                         }
                     }
-                    if (!kSplit) weights(0);
                 }
+                const float mc = m == -INFINITY ? 0.0f : m - F::LIFT;
+                const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+                uint64_t sums[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) {
+                    uint64_t x[16];
+                    products(g, x);
+                    uint32_t pw[16], pl[16];
 #pragma unroll
-                for (int g = 0; g < CHUNKS; ++g) {
-                    if (kSplit || g > 0) weights(g);
-                    if constexpr (kSplit) {
-                        // The row of rounded weights gets the partner's for cells 64 on, the row of remainders those below.
-                        uint32_t first[16], second[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint32_t got = __shfl_xor_sync(FULL_MASK, high ? pw[e] : pl[e], 16);
-                            first[e] = high ? got : pw[e];
-                            second[e] = high ? pl[e] : got;
+                    for (int e = 0; e < 16; ++e) {
+                        float x0, x1;
+                        unpair(fma_pair(x[e], c2, mc2), x0, x1);
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        sums[e & 1] = add_pair(sums[e & 1], pair(x0, x1));
+                        if constexpr (kInt8) {
+                            const float2 vs = *reinterpret_cast<const float2 *>(scales->value[side] + 32 * g + 2 * e);
+                            x0 *= vs.x;
+                            x1 *= vs.y;
                         }
-                        if (!dry) {
-                            tmem_st16(s_at + 16 * g, first);
-                            tmem_st16(s_at + 32 + 16 * g, second);
-                        }
-                    } else if (!dry) {
-                        tmem_st16(s_at + 16 * g, pw);
+                        if constexpr (kSplit) split(x0, x1, pw[e], pl[e]);
+                        else pw[e] = pack<T>(x0, x1);
                     }
-                    if (g == CHUNKS - 1 || (!kSplit && g == 1)) {   // the products with half of the values can begin
+                    if (!dry) {
+                        // Weights of 32 cells over products that have been read.
+                        tmem_st16(s_at + (kSplit ? 32 : 16) * g, pw);
+                        if (kSplit) tmem_st16(s_at + 32 * g + 16, pl);
+                    }
+                    if (g & 1) {   // the products with half of the values can begin
                         tmem_st_wait();
                         tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0 && !dry) {
-                            if (kSplit || g == 1) mbar_arrive(&bars->p_half[i]);
-                            if (g == CHUNKS - 1) {
-                                mbar_arrive(&bars->p_full[i]);
-                                arrive(&bars->side_empty[side], two ? 1u : 2u);
-                            }
+                            mbar_arrive(g == 1 ? &bars->p_half[i] : &bars->p_full[i]);
+                            if (g == 3) arrive(&bars->side_empty[side], two ? 1u : 2u);
                         }
                     }
                 }
@@ -986,13 +969,12 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 tiles += n;
             }
             // ---- the segment's results ---------------------------------------------------------
-            if constexpr (kSplit) l += __shfl_xor_sync(FULL_MASK, l, 16);
             float2 sum = make_float2(m == -INFINITY ? -INFINITY : m - F::LIFT, l);
             float f0 = 1.0f, f1 = 1.0f;
             bool any0 = any, any1 = any;
             if (!dry && !(wait_warp(&bars->o_full[0], k & 1) && wait_warp(&bars->o_full[1], k & 1))) break;
             if (!two) {
-                // Both streams have the same rows: their sums through the second query tile, which nothing uses.
+                // Both streams have the same rows: their sums through the second query tile, which nothing reads any more.
                 float4 *shared = reinterpret_cast<float4 *>(raw_smem + (base + TILE_BYTES - smem_u32(raw_smem)));
                 shared[i * ROWS + row] = make_float4(sum.x, sum.y, any ? 1.0f : 0.0f, 0.0f);
                 __syncwarp();
@@ -1010,8 +992,8 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             }
             tc_fence_after_sync();
             if (!idle) {
-                const bool valid = real < rows && !(kSplit && high) && !dry;
-                const int block_row = (two ? i * p.seqs * p.group : 0) + real;
+                const bool valid = row < rows && !dry;
+                const int block_row = (two ? i * p.seqs * p.group : 0) + row;
                 const int at = s.slot < 0 ? s.row + block_row : block_row;
                 const size_t from = s.slot < 0 ? static_cast<size_t>(s.kvh) * p.whole_rows : static_cast<size_t>(s.slot) * BLOCK;
                 float4 *to = (s.slot < 0 ? p.whole : p.slots) + from * 32;
@@ -1019,23 +1001,14 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
 #pragma unroll 1
                 for (int piece = piece0; piece < piece1; ++piece) {
                     uint32_t o[32];
-                    __syncwarp();
-                    if (two) {
-                        tmem_ld32(tmem + lanes + O_COL + 128 * i + 32 * piece, o);
-                        tmem_ld_wait();
-                    } else {
+                    tmem_read32(tmem + lanes + O_COL + (two ? 128 * i : 0) + 32 * piece, o);
+                    if (!two) {
                         uint32_t u[32];
-                        tmem_ld32(tmem + lanes + O_COL + 32 * piece, o);
-                        tmem_ld32(tmem + lanes + O_COL + 128 + 32 * piece, u);
-                        tmem_ld_wait();
+                        tmem_read32(tmem + lanes + O_COL + 128 + 32 * piece, u);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             o[e] = __float_as_uint((any0 ? __uint_as_float(o[e]) * f0 : 0.0f) + (any1 ? __uint_as_float(u[e]) * f1 : 0.0f));
                     }
-                    if constexpr (kSplit)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(fmaf(__uint_as_float(__shfl_xor_sync(FULL_MASK, o[e], 16)), 1.0f / 2048.0f, __uint_as_float(o[e])));
                     if (valid)
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -1090,7 +1063,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __gr
     const int4 w = mine ? __ldcg(own.meta + static_cast<size_t>(s) * own.units + kvh * own.parts + part_of) : make_int4(0, 0, 0, 0);
     if (place.x >= 0) {
         // Nothing but numbers is taken from scratch: a CTA that gave up may have left anything.
-        const int block = min(place.x, blocks - 1), first = min(max(place.y, max(0, s - 2 * p.seqs + 1)), s);
+        const int block = min(place.x, blocks - 1), first = min(max(place.y, max(0, s - p.block + 1)), s);
         const int2 m = __ldcg(p.meta + static_cast<size_t>(block) * a.kv.nkv + kvh);
         const int at = (s - first) * p.group + head;
         if (m.x < 0) {
@@ -1182,17 +1155,14 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(const __gr
     if (chunk == 0 && a.lse != nullptr) a.lse[out_row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * LN2;
 }
 
-int seqs_of(int group, bool split) { return (split ? 64 : 128) / group; }
-
 struct Layout {
     size_t meta, places, whole, whole_refs, slots, slot_refs, own, bytes;
     int grid, blocks, whole_rows;
 };
-// q_fp32 only changes how many sequences a row tile takes: the scratch is laid out for the smaller number.
+// Blocks of fp32 queries are one row tile: the scratch is laid out for as many blocks, whatever the type.
 Layout layout(const PrefixAttnSizes &z) {
     Layout y;
-    const int seqs = std::max(1, seqs_of(z.nheads / z.nkv, true));
-    y.blocks = z.nseq / (2 * seqs) + z.ngroups + 1;
+    y.blocks = z.nseq / (ROWS / (z.nheads / z.nkv)) + z.ngroups + 1;
     y.whole_rows = (z.nseq * (z.nheads / z.nkv) + 7) / 8 * 8 + 8 * (y.blocks + 1);
     const long long tiles = (static_cast<long long>(z.prefix_capacity) + ROWS - 1) / ROWS * y.blocks * z.nkv;
     y.grid = static_cast<int>(std::max(1LL, std::min<long long>(device_sm_count(), tiles)));
@@ -1242,13 +1212,14 @@ cudaError_t run(Params &p, const Layout &y, const PagedAttnArgs &own_args, cudaS
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e == cudaSuccess) configured_device = dev;
     }
-    p.seqs = seqs_of(p.group, Form<kKv, QT>::kSplit);
+    p.seqs = ROWS / p.group;
+    p.block = Form<kKv, QT>::TILES * p.seqs;
     if (e == cudaSuccess) e = launch(kernel, dim3(y.grid), PTHREADS, smem, stream, p);
     PagedPartial own;
     if (e == cudaSuccess) e = launch_paged_partial(own_args, own, stream);
     if (e != cudaSuccess) return e;
     // Ranges of a block, on average.
-    const int ranges = y.grid / (p.a.kv.nkv * std::max(1, std::max(p.a.ngroups, p.a.nseq / (2 * p.seqs)))) + 1;
+    const int ranges = y.grid / (p.a.kv.nkv * std::max(1, std::max(p.a.ngroups, p.a.nseq / p.block))) + 1;
     // As many warps share rows as there are ranges for and the GPU has room for at once.
     const long long units = static_cast<long long>((p.a.nseq * p.group + 7) / 8) * 4;   // of a KV head
     int split = 1;

@@ -3,8 +3,8 @@ prefix's cells and the sequence's own. Tolerances: cache_ref.bounds; weights of 
 operand type (bfloat16 or binary16), or keep 22 bits for fp32 queries.
 
 Binary16 weights below its normal numbers are off by up to 2^-25, half its smallest step. Prefix weights (value scale
-included) are held so that a row's largest is at least 2^7, so that is 2^-32 of the largest, and 2^-43 where a remainder
-times 2^11 is kept; weights of own cells keep a remainder too and reach at least 1: 2^-36. For n cells a column is off by
+included) are held so that a row's largest is at least 2^7, so that is 2^-32 of the largest (the remainders that fp32
+queries keep too); weights of own cells keep a remainder times 2^11 and reach at least 1: 2^-36. For n cells a column is off by
 n times that, times the largest weight, scale and |code|; with codes of up to 128 whose largest in a cell is at least 64 that
 is at most twice the largest p_j |v_jd| of any column, which the largest column's sum of |p v| bounds. It counts in a column
 where the cell that has nearly all the weight has a value of 0: relative to that column's own sum it is not small."""
@@ -102,7 +102,7 @@ class Shared:
                 o, l, _, size, S = ref.attend(self.q[s, h * grp:(h + 1) * grp][:, None], k, v, ok[None], scale)
                 tol, ltol = ref.bounds(o, l, size, S, k.shape[0], qt, p_half)
                 if self.kv != BF16 and k.shape[0] > 0:
-                    tol = tol + 2 * k.shape[0] * (2.0 ** -36 if qt == F32 else 2.0 ** -32) * size.amax(-1, keepdim=True)
+                    tol = tol + 2 * k.shape[0] * 2.0 ** -32 * size.amax(-1, keepdim=True)
                 for name, got, want, t in (("out", out, o, tol), ("lse", lse, l, ltol)):
                     got = got[s, h * grp:(h + 1) * grp]
                     if bool(torch.isnan(want).all()):        # the formula's own NaN

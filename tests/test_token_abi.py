@@ -171,7 +171,7 @@ def test_prefix_limits(lib):
     assert prefix(lib, ngroups=65536) == UNSUPPORTED
     assert prefix(lib, nheads=65536) == UNSUPPORTED
     assert prefix(lib, nheads=258) == UNSUPPORTED
-    assert prefix(lib, pages(**INT8), q_dtype=qsa.F32, nheads=130) == UNSUPPORTED
+    assert prefix(lib, pages(**INT8), q_dtype=qsa.F32, nheads=258) == UNSUPPORTED
     assert prefix(lib, pcols=1 << 27, pstride=1 << 27) == UNSUPPORTED
     assert prefix(lib, cols=1 << 27, tstride=1 << 27) == UNSUPPORTED
     n = qsa.prefix_attn_scratch_bytes
