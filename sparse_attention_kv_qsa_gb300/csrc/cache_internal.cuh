@@ -57,8 +57,24 @@ struct PagedPartial {
     int parts, units, heads_per_unit, grid;
 };
 
+// What prefix_share.cuh's functions go by.
+struct PrefixShare {
+    const int32_t *cu, *prefix_lens;
+    int ngroups, nseq, capacity, nkv;
+    int seqs, block;          // sequences of a row tile, and of a block of rows
+    int sms, grid;            // SMs, CTAs of the prefix's kernel
+    int whole;                // nothing is divided: no block has two row tiles, or both kernels' grids have room
+    int one_tile_ns, two_tiles_ns;
+    float own_tile_ns, own_unit_ns;   // paged attention's tile of cells, and unit of a sequence and KV head
+    int own_units;
+};
+
 size_t paged_partial_bytes(int nseq, int nheads, int nkv, int capacity);
-cudaError_t launch_paged_partial(const PagedAttnArgs &a, PagedPartial &left, cudaStream_t stream);
+// The units and CTAs of a call, for PrefixShare.
+int paged_units(const PagedAttnArgs &a);
+int paged_ctas(const PagedAttnArgs &a);
+// Launched behind the shared prefix's kernel, with which it shares the GPU.
+cudaError_t launch_paged_partial(const PagedAttnArgs &a, const PrefixShare &share, PagedPartial &left, cudaStream_t stream);
 
 struct PrefixAttnArgs {
     const void *q;

@@ -53,6 +53,7 @@
 
 #include "attn_row.cuh"
 #include "cache_internal.cuh"
+#include "prefix_share.cuh"
 #include "qsa_internal.cuh"
 
 namespace qsa {
@@ -75,6 +76,7 @@ struct Params {
     int by_unit;      // no more units than ranges: a place in meta is a unit, else a range
     int4 *meta;       // sequence, unit, first range, last range of the unit to join there, or -1
     float *rows;      // [nseq][nheads][SLOT_ROW]: partial results of whole units (kPart)
+    PrefixShare share;   // the kernel before this one, which has the other SMs (kPart)
     float *lse2;      // [nseq][nheads], or null
     float *logits;    // [nseq][nheads][stride], or null
 };
@@ -84,12 +86,13 @@ struct Span {
     int n, sinks, shift;
     __device__ __forceinline__ int cell(int i) const { return i < sinks ? i : i + shift; }
 };
-__device__ __forceinline__ Span visible(const Params &p, int s) {
-    const int len = min(max(ld_in(p.a.lens + s), 0), p.capacity);
+__device__ __forceinline__ Span span_of(const Params &p, int length) {
+    const int len = min(max(length, 0), p.capacity);
     const int lo = p.a.window < 0 ? 0 : max(0, len - p.a.window);
     const int k = min(p.a.sinks, lo);
     return {k + len - lo, k, lo - k};
 }
+__device__ __forceinline__ Span visible(const Params &p, int s) { return span_of(p, ld_in(p.a.lens + s)); }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -190,11 +193,14 @@ __device__ __forceinline__ int tiles_of(const Span &v) {
 template <int kTile>
 struct Cursor {
     int s, u, t, nt;
+    int length;       // of the next sequence, which is on its way while this one is worked on
     Span v;
+    __device__ __forceinline__ void look_ahead(const Params &p) { length = s + 1 < p.a.nseq ? ld_in(p.a.lens + s + 1) : 0; }
     __device__ __forceinline__ void enter(const Params &p, int seq) {
         s = seq;
-        v = visible(p, s);
+        v = span_of(p, length);
         nt = tiles_of<kTile>(v);
+        look_ahead(p);
     }
     // The next tile, which exists.
     __device__ __forceinline__ void next(const Params &p) {
@@ -208,21 +214,27 @@ struct Cursor {
 };
 
 // kPart: the results stay partial sums (rows, slots), and meta has a place for every unit: another
-// kernel adds them to what it has. It is then launched behind a kernel that its results do not depend on, and
-// which let it start only after it had waited for its own predecessors: it waits for that one at its end alone.
+// kernel adds them to what it has. Every warp then has a range of its own, in tiles of one step, and nothing to
+// merge: own cells behind a prefix are few, and units of one or two tiles of 64 left warps idle and waiting (512
+// sequences of 72 cells, 2 KV heads: 3.7 us a unit and CTA). It is launched behind a kernel that its
+// results do not depend on, and which let it start only after it had waited for its own predecessors: it waits
+// for that one at its end alone.
 template <int kKv, typename QT, int kMT, bool kPart>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __grid_constant__ Params p) {
     using F = Form<kKv>;
     using O = typename F::O;
     constexpr bool kInt8 = F::kInt8;
-    constexpr int STEP = F::STEP, TILE = F::TILE, STAGES = F::STAGES, ELEM = kInt8 ? 1 : 2;
+    constexpr int STEP = F::STEP, TILE = kPart ? STEP : F::TILE, STAGES = F::STAGES, ELEM = kInt8 ? 1 : 2;
+    constexpr int RANGES = kPart ? WARPS : 1;      // of a CTA
     constexpr int HEADS_PER_UNIT = 8 * kMT;
     constexpr int GROUPS = STEP / 16;              // of 16 cells, whose weights are found together
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long sh_scan[WARPS];
-    __shared__ int sh_seq, sh_unit, sh_tile;
-    __shared__ Span sh_span;
+    __shared__ long long sh_tiles[kPart ? WARPS : 1], sh_work[kPart ? WARPS : 1];
+    __shared__ int sh_seq[RANGES], sh_unit[RANGES], sh_tile[RANGES];
+    __shared__ Span sh_span[RANGES];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int range = blockIdx.x * RANGES + (kPart ? warp : 0), in_cta = kPart ? warp : 0;
     const int r = lane >> 2, t = lane & 3;
     const PagedAttnArgs &a = p.a;
 
@@ -247,8 +259,25 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
         if (lane >= o) before += y;
     }
     if (lane == 31) sh_scan[warp] = before;
-    if (tid == 0) {
-        sh_seq = -1;
+    if constexpr (kPart) {
+        long long tiles = 0, work = 0;
+        for (int g = tid; g < p.share.ngroups && !p.share.whole; g += THREADS) {
+            const PrefixGroup x = prefix_group(p.share, g);
+            tiles += prefix_tiles(p.share, x);
+            work += prefix_work(p.share, x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            tiles += __shfl_xor_sync(FULL_MASK, tiles, o);
+            work += __shfl_xor_sync(FULL_MASK, work, o);
+        }
+        if (lane == 0) {
+            sh_tiles[warp] = tiles;
+            sh_work[warp] = work;
+        }
+    }
+    if (tid < RANGES) {
+        sh_seq[tid] = -1;
         if (!p.by_unit) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
@@ -261,24 +290,41 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     before -= mine;
     // Below 2^63: at most 65,535 sequences of 2^24 tiles times 65,535 units.
     const long long all = total * p.units;
-    const long long per = (all + gridDim.x - 1) / gridDim.x;
-    const long long x0 = per * blockIdx.x, x1 = min(x0 + per, all);
-    // The tile that x0 is.
-    if (x0 < x1 && x0 >= before * p.units && x0 < (before + mine) * p.units) {
-        int s = s0;
-        long long b = before;
-        Span v = first_span;
-        int n = tiles_of<TILE>(v);
-        while (x0 >= (b + n) * p.units) {
-            b += n;
-            v = visible(p, ++s);
-            n = tiles_of<TILE>(v);
+    int ctas = gridDim.x;
+    if constexpr (kPart) {
+        long long tiles = 0, work = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            tiles += sh_tiles[w];
+            work += sh_work[w];
         }
-        const long long in_seq = x0 - b * p.units;
-        sh_seq = s;
-        sh_span = v;
-        sh_unit = static_cast<int>(in_seq / n);
-        sh_tile = static_cast<int>(in_seq % n);
+        // Two on each SM that the prefix leaves.
+        if (!p.share.whole) {
+            const int taken = prefix_ctas(p.share, tiles, work, all);
+            if (taken < p.share.sms) ctas = min(ctas, CTAS_PER_SM * (p.share.sms - taken));
+        }
+    }
+    const long long per = (all + ctas * RANGES - 1) / (ctas * RANGES);
+    const long long x0 = per * range, x1 = min(x0 + per, all);
+    // The tile that a range begins with.
+    for (int w = 0; w < RANGES; ++w) {
+        const long long begin = kPart ? per * (blockIdx.x * RANGES + w) : x0;
+        if (begin < all && begin >= before * p.units && begin < (before + mine) * p.units) {
+            int s = s0;
+            long long b = before;
+            Span v = first_span;
+            int n = tiles_of<TILE>(v);
+            while (begin >= (b + n) * p.units) {
+                b += n;
+                v = visible(p, ++s);
+                n = tiles_of<TILE>(v);
+            }
+            const long long in_seq = begin - b * p.units;
+            sh_seq[w] = s;
+            sh_span[w] = v;
+            sh_unit[w] = static_cast<int>(in_seq / n);
+            sh_tile[w] = static_cast<int>(in_seq % n);
+        }
     }
     // Sequences without a visible cell have no tile: their rows are written here.
     for (int s = blockIdx.x; !kPart && s < a.nseq; s += gridDim.x) {
@@ -293,7 +339,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
             for (int u = tid; u < p.units; u += THREADS) p.meta[s * p.units + u] = make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
-    if (sh_seq < 0) {
+    if (sh_seq[in_cta] < 0) {
         if (kPart) grid_dependency_wait();
         return;
     }
@@ -309,11 +355,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     // ---- copies, which run ahead over the units without a stop ----------------------
     const int row = lane & (STEP - 1);             // the row whose address this lane finds
     Cursor<TILE> at;                               // the step whose page is fetched next
-    at.s = sh_seq;
-    at.v = sh_span;
+    at.s = sh_seq[in_cta];
+    at.v = sh_span[in_cta];
     at.nt = tiles_of<TILE>(at.v);
-    at.u = sh_unit;
-    at.t = sh_tile;
+    at.u = sh_unit[in_cta];
+    at.t = sh_tile[in_cta];
+    at.look_ahead(p);
     Cursor<TILE> here = at;                        // the step that is computed
     struct Place {                                 // of this lane's row: the page, and the rest of its address
         int page;
@@ -322,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
     auto fetch = [&](int step) {
         if (step >= steps) return;
         if (step > 0) at.next(p);
-        const int i = at.t * TILE + warp * STEP + row;
+        const int i = at.t * TILE + (kPart ? 0 : warp * STEP) + row;
         place.page = -1;
         if (i < at.v.n) {
             const int j = at.v.cell(i), pg = static_cast<int>(divide(p.page, j)), in_page = j - pg * a.kv.page_size;
@@ -626,6 +673,49 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
             }
         }
 
+        if constexpr (kPart) {
+            // ---- this warp's sums are the segment's ------------------------------------------
+            const bool whole = t0 == 0 && t1 == nt;
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) {
+                sum[m] += __shfl_xor_sync(FULL_MASK, sum[m], 1);
+                sum[m] += __shfl_xor_sync(FULL_MASK, sum[m], 2);
+                const int h = 8 * m + r;
+                if (h < nh) {
+                    float *sp = whole ? p.rows + (static_cast<size_t>(s) * a.nheads + h0 + h) * SLOT_ROW
+                                      : p.slots + (static_cast<size_t>(2 * range + (begins ? 0 : 1)) * HEADS_PER_UNIT + h) * SLOT_ROW;
+#pragma unroll
+                    for (int n = 0; n < 16; n += 2) {
+                        float y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = fmaf(o[m][n + (e >> 1)][2 + (e & 1)], 1.0f / O::LO, o[m][n + (e >> 1)][e & 1]);
+                        if constexpr (kInt8) {   // columns 32 t + n and 16 further
+                            *reinterpret_cast<float2 *>(sp + 32 * t + n) = make_float2(y[0], y[2]);
+                            *reinterpret_cast<float2 *>(sp + 32 * t + 16 + n) = make_float2(y[1], y[3]);
+                        } else {
+                            *reinterpret_cast<float2 *>(sp + 8 * n + 2 * t) = make_float2(y[0], y[1]);
+                            *reinterpret_cast<float2 *>(sp + 8 * n + 8 + 2 * t) = make_float2(y[2], y[3]);
+                        }
+                    }
+                    if (t == 0) *reinterpret_cast<float2 *>(sp + 128) = make_float2(ref[m], sum[m]);
+                }
+            }
+            if (lane == 0) {
+                int4 *at_unit = p.meta + static_cast<size_t>(s) * p.units + u;
+                const long long unit0 = x0 - t0;
+                if (whole) *at_unit = make_int4(-1, 0, 0, 0);
+                else if (begins && t0 > 0 && unit0 / per == range - 1)
+                    *at_unit = make_int4(s, u, static_cast<int>(unit0 / per) * 2 + (unit0 % per == 0 ? 0 : 1),
+                                         static_cast<int>((unit0 + nt - 1) / per));
+            }
+            if (step < steps) {
+                here.t = here.nt - 1;
+                here.next(p);
+                if (AHEAD) load_q();
+            }
+            __syncwarp();
+            continue;
+        }
         // ---- join the warps, in warp order, through the stage each has just used ----------
         __syncwarp();
         const int used = (step - 1) % STAGES;
@@ -675,7 +765,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                 y.z = fmaf(z.z, f, y.z);
                 y.w = fmaf(z.w, f, y.w);
             }
-            if (whole && !kPart) {
+            if (whole) {
                 const size_t out_row = static_cast<size_t>(s) * a.nheads + h0 + h;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 store4(static_cast<QT *>(a.out) + out_row * 128 + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
@@ -685,8 +775,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
                     if (p.lse2 != nullptr) p.lse2[out_row] = e;
                 }
             } else {
-                float *sp = kPart && whole ? p.rows + (static_cast<size_t>(s) * a.nheads + h0 + h) * SLOT_ROW
-                                           : p.slots + (static_cast<size_t>(slot) * HEADS_PER_UNIT + h) * SLOT_ROW;
+                float *sp = p.slots + (static_cast<size_t>(slot) * HEADS_PER_UNIT + h) * SLOT_ROW;
                 *reinterpret_cast<float4 *>(sp + 4 * lane) = y;
                 if (lane == 0) {
                     sp[128] = top;
@@ -965,12 +1054,23 @@ size_t partial_meta_bytes(int nseq, int nheads, int nkv) {
 }  // namespace
 
 size_t paged_partial_bytes(int nseq, int nheads, int nkv, int capacity) {
-    return partial_rows_bytes(nseq, nheads) + partial_meta_bytes(nseq, nheads, nkv) + layout(nseq, nheads, nkv, capacity, false).bytes;
+    const Layout y = layout(nseq, nheads, nkv, capacity, false);
+    return partial_rows_bytes(nseq, nheads) + partial_meta_bytes(nseq, nheads, nkv) +
+           sizeof(float) * 2 * WARPS * y.grid * y.heads_per_unit * SLOT_ROW;
 }
 
-cudaError_t launch_paged_partial(const PagedAttnArgs &a, PagedPartial &left, cudaStream_t stream) {
+int paged_ctas(const PagedAttnArgs &a) { return layout(a.nseq, a.nheads, a.kv.nkv, a.table_cols * a.kv.page_size, false).grid; }
+
+int paged_units(const PagedAttnArgs &a) {
+    Params p;
+    prepare(p, a);
+    return p.units * a.nseq;
+}
+
+cudaError_t launch_paged_partial(const PagedAttnArgs &a, const PrefixShare &share, PagedPartial &left, cudaStream_t stream) {
     Params p;
     const int heads = prepare(p, a);
+    p.share = share;
     const Layout y = layout(a.nseq, a.nheads, a.kv.nkv, p.capacity, false);
     p.by_unit = 1;
     char *b = static_cast<char *>(a.scratch);
@@ -978,8 +1078,8 @@ cudaError_t launch_paged_partial(const PagedAttnArgs &a, PagedPartial &left, cud
     b += partial_rows_bytes(a.nseq, a.nheads);
     p.meta = reinterpret_cast<int4 *>(b);
     b += partial_meta_bytes(a.nseq, a.nheads, a.kv.nkv);
-    p.slots = reinterpret_cast<float *>(b + y.slots);
-    left = {p.rows, p.slots, p.meta, p.parts, p.units, heads, y.grid};
+    p.slots = reinterpret_cast<float *>(b);
+    left = {p.rows, p.slots, p.meta, p.parts, p.units, heads, WARPS * y.grid};
     if (p.capacity == 0) return cudaSuccess;   // no sequence has a cell
     if (a.kv.dtype == QSA_BF16)
         return heads == 8 ? run_kernel<QSA_BF16, __nv_bfloat16, 1, true>(p, y.grid, stream)

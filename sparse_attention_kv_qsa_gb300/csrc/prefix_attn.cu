@@ -43,6 +43,7 @@
 
 #include "attn_row.cuh"
 #include "cache_internal.cuh"
+#include "prefix_share.cuh"
 #include "qsa_internal.cuh"
 
 namespace qsa {
@@ -80,8 +81,9 @@ struct Form {
 struct Params {
     PrefixAttnArgs a;
     Divider page;
+    PrefixShare share;
     int group, seqs, block;   // query heads per KV head; sequences of a row tile, and of a block
-    int capacity;             // cells of a row of the prefix table
+    int own_tile;             // cells of paged attention's tile
     // Partial results: sums as sums_at() says, and reference and weights' sum of each row.
     float4 *slots, *whole;    // [2 grid][BLOCK x 32]: a segment at a CTA's begin, and its last; [nkv][whole_rows x 32]
     float2 *slot_refs, *whole_refs;
@@ -92,23 +94,8 @@ struct Params {
     int stall;                // diagnostics only: CTA 0 never signals its first key tile
 };
 
-// A group of sequences.
-struct Group {
-    int first, count, len, tiles, blocks;
-};
-__device__ __forceinline__ Group group_of(const Params &p, int g) {
-    Group x;
-    x.first = min(max(ld_in(p.a.cu + g), 0), p.a.nseq);
-    x.count = min(max(ld_in(p.a.cu + g + 1), x.first), p.a.nseq) - x.first;
-    x.len = min(max(ld_in(p.a.prefix_lens + g), 0), p.capacity);
-    x.tiles = (x.len + ROWS - 1) / ROWS;
-    x.blocks = (x.count + p.block - 1) / p.block;
-    return x;
-}
-
-__device__ __forceinline__ long long tiles_in(const Params &p, const Group &x) {
-    return static_cast<long long>(x.tiles) * x.blocks * p.a.kv.nkv;
-}
+using Group = PrefixGroup;
+__device__ __forceinline__ Group group_of(const Params &p, int g) { return prefix_group(p.share, g); }
 // Block b of group g, among all.
 __device__ __forceinline__ int block_number(const Params &p, const Group &x, int g, int b) { return x.first / p.block + g + b; }
 // First row of a whole block's partial results (of a KV head): a multiple of 8, and behind the rows of the blocks before it.
@@ -218,6 +205,11 @@ __device__ __forceinline__ void arrive(uint64_t *bar, uint32_t n) {
 __device__ __forceinline__ long long quotient(long long a, long long b) {   // neither is negative
     return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
+__device__ __forceinline__ long long sum_of_warp(long long x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(FULL_MASK, x, o);
+    return x;
+}
 template <int N>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -257,7 +249,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
     constexpr bool kInt8 = F::kInt8, kSplit = F::kSplit;
     constexpr int STAGES = F::STAGES;
     extern __shared__ unsigned char raw_smem[];
-    __shared__ long long sh_scan[PTHREADS / 32 - MMA_WARP];
+    __shared__ long long sh_scan[PTHREADS / 32 - MMA_WARP], sh_work[PTHREADS / 32 - MMA_WARP], sh_own[PTHREADS / 32 - MMA_WARP];
     __shared__ Group sh_at;                     // the group that the range begins in
     __shared__ int sh_group, sh_kvh, sh_block, sh_tile;
     const PrefixAttnArgs &a = p.a;
@@ -302,35 +294,49 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
     tc_fence_after_sync();
     const uint32_t tmem = bars->tmem;
     long long per = 0, x1 = 0, range = 0;           // tiles of a CTA, the range's end and length (not in softmax warps)
+    grid_dependency_wait();
+    grid_launch_dependents();
     if (warp >= MMA_WARP) {
-        grid_dependency_wait();
-        grid_launch_dependents();
         // ---- this CTA's range of tiles -------------------------------------------------
         constexpr int FINDERS = PTHREADS - 32 * MMA_WARP;
         const int me = tid - 32 * MMA_WARP, each = (a.ngroups + FINDERS - 1) / FINDERS;
         const int g0 = min(me * each, a.ngroups), g1 = min(g0 + each, a.ngroups);
-        long long mine = 0;
+        long long mine = 0, work = 0, own = 0;
         Group own_group = {};                       // the last of this thread's, read once where it is the only one
         for (int g = g0; g < g1; ++g) {
             own_group = group_of(p, g);
-            mine += tiles_in(p, own_group);
+            mine += prefix_tiles(p.share, own_group);
+            work += prefix_work(p.share, own_group);
         }
+        const int capacity = a.table_cols * a.kv.page_size;
+        for (int s = me; s < a.nseq && !p.share.whole; s += FINDERS) own += (min(max(ld_in(a.lens + s), 0), capacity) + p.own_tile - 1) / p.own_tile;
         long long before = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(FULL_MASK, before, o);
             if (lane >= o) before += y;
         }
-        if (lane == 31) sh_scan[warp - MMA_WARP] = before;
+        work = sum_of_warp(work);
+        own = sum_of_warp(own);
+        if (lane == 31) {
+            sh_scan[warp - MMA_WARP] = before;
+            sh_work[warp - MMA_WARP] = work;
+            sh_own[warp - MMA_WARP] = own;
+        }
         named_bar_sync(1, FINDERS);
         long long all = 0;
+        work = own = 0;
 #pragma unroll
         for (int w = 0; w < FINDERS / 32; ++w) {
             if (w < warp - MMA_WARP) before += sh_scan[w];
             all += sh_scan[w];
+            work += sh_work[w];
+            own += sh_own[w];
         }
         before -= mine;
-        per = quotient(all + gridDim.x - 1, gridDim.x);
+        int ctas = gridDim.x;
+        if (!p.share.whole) ctas = max(1, min(ctas, prefix_ctas(p.share, all, work, own * (p.share.own_units / a.nseq))));
+        per = quotient(all + ctas - 1, ctas);
         const long long x0 = per * blockIdx.x;
         x1 = min(x0 + per, all);
         range = max(0LL, x1 - x0);
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             Group x = own_group;
             if (g1 - g0 > 1) {
                 x = group_of(p, g);
-                for (long long n = tiles_in(p, x); x0 >= b + n; n = tiles_in(p, x)) {
+                for (long long n = prefix_tiles(p.share, x); x0 >= b + n; n = prefix_tiles(p.share, x)) {
                     b += n;
                     x = group_of(p, ++g);
                 }
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                         kvh = 0;
                         // The next group that has tiles: 32 at a time.
                         for (int from = g + 1; left > 0; from += 32) {
-                            const bool have = from + lane < a.ngroups && tiles_in(p, group_of(p, from + lane)) > 0;
+                            const bool have = from + lane < a.ngroups && prefix_tiles(p.share, group_of(p, from + lane)) > 0;
                             const uint32_t found = __ballot_sync(FULL_MASK, have);
                             if (found != 0u) {
                                 g = from + __ffs(found) - 1;
@@ -801,23 +807,21 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
         const uint32_t s_at = tmem + lanes + S_COL + 128 * i;
         uint32_t ns = 0, tiles = 0;
-        // Once through the code before there is anything to do, while the range is found and the first cells
-        // come: its instructions are then there. It waits for nothing, signals nothing and writes nothing.
+        // Once through the code as soon as there is a segment, while its first cells come: its instructions are
+        // then there (the first tile took 3 to 5 us without it). It waits for nothing, signals nothing and
+        // writes nothing.
         bool dry = true;
         for (uint32_t k = 0;; k += dry ? 0 : 1, dry = false) {
-            Segment s = {};
-            if (!dry) {
-                if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
-                s = bars->seg[k % SEGS];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->seg_empty[k % SEGS]);
-                if (s.count == 0) break;
-            }
+            if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
+            const Segment s = bars->seg[k % SEGS];
+            __syncwarp();
+            if (lane == 0 && !dry) mbar_arrive(&bars->seg_empty[k % SEGS]);
+            if (s.count == 0) break;
             const bool two = s.count > p.seqs || dry;
             const int n = dry ? 1 : s.t1 - s.t0;
             const int count = !two ? s.count : i == 0 ? p.seqs : s.count - p.seqs;   // sequences of this stream's rows
             const int rows = count * p.group;
-            const bool idle = !dry && 32 * quarter >= rows;                          // a warp without rows
+            const bool idle = 32 * quarter >= rows && !dry;                          // a warp without rows
             float c = a.scale * LOG2E;
             if constexpr (kInt8) {
                 if (!dry && !wait_warp(&bars->q_full, k & 1)) break;
@@ -844,9 +848,9 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 if (!dry) ok = wait_warp(&bars->side_full[side], ((tiles + j) / SIDES) & 1);
                 if (!ok) break;
                 tc_fence_after_sync();
-                // The tile goes through 32 cells at a time, twice (largest, then weights), in loops that stay
-                // rolled: read out of TMEM once and worked on straight through, the code of a tile does not
-                // stay in the instruction cache (int8 and fp32 queries took 4 us a tile, 16-bit ones 1.0).
+                // 32 cells at a time, twice: for the largest, and for the weights. The loops stay rolled and read TMEM
+                // twice: straight through, the code of a tile did not stay in the instruction cache (fp32
+                // queries 4.2 us a tile, rolled 2.1; 16-bit cells, held in registers, were no faster).
                 auto products = [&](int g, uint64_t (&x)[16]) {
                     uint32_t r[32];
                     const uint32_t there = reinterpret_cast<const uint32_t *>(&bars->mask[side])[g];
@@ -872,7 +876,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 };
                 float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                for (int g = 0; g < 4; ++g) {
+                for (int g = dry ? 3 : 0; g < 4; ++g) {
                     uint64_t x[16];
                     products(g, x);
                     if constexpr (kInt8) {
@@ -920,7 +924,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
                 uint64_t sums[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll 1
-                for (int g = 0; g < 4; ++g) {
+                for (int g = dry ? 3 : 0; g < 4; ++g) {
                     uint64_t x[16];
                     products(g, x);
                     uint32_t pw[16], pl[16];
@@ -939,8 +943,8 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                         if constexpr (kSplit) split(x0, x1, pw[e], pl[e]);
                         else pw[e] = pack<T>(x0, x1);
                     }
+                    // Weights of 32 cells over products that have been read.
                     if (!dry) {
-                        // Weights of 32 cells over products that have been read.
                         tmem_st16(s_at + (kSplit ? 32 : 16) * g, pw);
                         if (kSplit) tmem_st16(s_at + 32 * g + 16, pl);
                     }
@@ -962,12 +966,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 any = true;
             }
             if (!ok) break;
-            if (dry) {
-                grid_dependency_wait();   // results go to scratch that an earlier call may still read
-                grid_launch_dependents();
-            } else {
-                tiles += n;
-            }
+            if (!dry) tiles += n;
             // ---- the segment's results ---------------------------------------------------------
             float2 sum = make_float2(m == -INFINITY ? -INFINITY : m - F::LIFT, l);
             float f0 = 1.0f, f1 = 1.0f;
@@ -999,7 +998,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 float4 *to = (s.slot < 0 ? p.whole : p.slots) + from * 32;
                 const int piece0 = two ? 0 : 2 * i, piece1 = two ? 4 : 2 * i + 2;   // with the same rows, half of the columns each
 #pragma unroll 1
-                for (int piece = piece0; piece < piece1; ++piece) {
+                for (int piece = dry ? 3 : piece0; piece < piece1; ++piece) {
                     uint32_t o[32];
                     tmem_read32(tmem + lanes + O_COL + (two ? 128 * i : 0) + 32 * piece, o);
                     if (!two) {
@@ -1214,9 +1213,17 @@ cudaError_t run(Params &p, const Layout &y, const PagedAttnArgs &own_args, cudaS
     }
     p.seqs = ROWS / p.group;
     p.block = Form<kKv, QT>::TILES * p.seqs;
+    // Measured, ns, side by side: a tile of 128 prefix cells for one row tile, for two; paged attention's tile of
+    // 16 cells (32 int8), a quarter of a CTA's time for one, and what a unit costs besides.
+    constexpr bool kInt8 = Form<kKv, QT>::kInt8;
+    p.share = {p.a.cu, p.a.prefix_lens, p.a.ngroups, p.a.nseq, p.a.prefix_cols * p.a.kv.page_size, p.a.kv.nkv, p.seqs, p.block,
+               device_sm_count(), y.grid,
+               p.block == p.seqs || p.a.nseq <= p.seqs || y.grid + (paged_ctas(own_args) + 1) / 2 <= device_sm_count(),
+               1500, kInt8 ? 3000 : 2300, kInt8 ? 550.0f : 400.0f, 400.0f, paged_units(own_args)};
+    p.own_tile = Form<kKv, QT>::kInt8 ? 32 : 16;
     if (e == cudaSuccess) e = launch(kernel, dim3(y.grid), PTHREADS, smem, stream, p);
     PagedPartial own;
-    if (e == cudaSuccess) e = launch_paged_partial(own_args, own, stream);
+    if (e == cudaSuccess) e = launch_paged_partial(own_args, p.share, own, stream);
     if (e != cudaSuccess) return e;
     // Ranges of a block, on average.
     const int ranges = y.grid / (p.a.kv.nkv * std::max(1, std::max(p.a.ngroups, p.a.nseq / p.block))) + 1;
@@ -1238,8 +1245,8 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs &a, cudaStream_t stream) {
     p.a = a;
     p.page = make_divider(a.kv.page_size);
     p.group = a.nheads / a.kv.nkv;
-    p.capacity = a.prefix_cols * a.kv.page_size;
-    const Layout y = layout({a.nseq, a.ngroups, a.nheads, a.kv.nkv, p.capacity, a.table_cols * a.kv.page_size});
+    const int capacity = a.prefix_cols * a.kv.page_size;
+    const Layout y = layout({a.nseq, a.ngroups, a.nheads, a.kv.nkv, capacity, a.table_cols * a.kv.page_size});
     char *b = static_cast<char *>(a.scratch);
     p.meta = reinterpret_cast<int2 *>(b + y.meta);
     p.places = reinterpret_cast<int2 *>(b + y.places);
@@ -1249,7 +1256,7 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs &a, cudaStream_t stream) {
     p.slot_refs = reinterpret_cast<float2 *>(b + y.slot_refs);
     p.whole_rows = y.whole_rows;
     // Waits last as long as a CTA's whole range may: some 2 us a tile.
-    const long long tiles = (static_cast<long long>(p.capacity) + ROWS - 1) / ROWS * a.kv.nkv * (a.nseq + a.ngroups);
+    const long long tiles = (static_cast<long long>(capacity) + ROWS - 1) / ROWS * a.kv.nkv * (a.nseq + a.ngroups);
     p.wait_ns = wait_limit_ns() + 8192ull * static_cast<uint64_t>(std::min(tiles / y.grid + 1, 1LL << 24));
     p.stall = (debug_inject() & 32u) != 0u;
     PagedAttnArgs own = {};
