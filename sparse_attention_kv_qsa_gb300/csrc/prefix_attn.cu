@@ -23,7 +23,8 @@
 //   1 MMA warp        all tcgen05.mma
 //   1 warp            walks the range and publishes its segments (a block's part in this CTA)
 //   4 copy warps      cells by 16-byte asynchronous copies, each row from its own page (any page
-//                     size), into 128-byte-swizzled tiles; int8 cells become binary16 on the way
+//                     size), into 128-byte-swizzled tiles; int8 cells become binary16 on the way (and
+//                     the queries beside them, by the softmax warps)
 //
 // Two streams of softmax keep the tensor cores fed: with more than 128 rows
 // each takes a tile of rows, and both use every tile of cells; with fewer, both have the
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             mbar_init(&bars->seg_full[i], 1);
             mbar_init(&bars->seg_empty[i], 1 + 8 + COPY_WARPS);
         }
-        mbar_init(&bars->q_full, F::COPIES);
+        mbar_init(&bars->q_full, kInt8 ? 8 : F::COPIES);
         mbar_init(&bars->q_empty, 8);
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&bars->kv_full[i], F::COPIES);
@@ -543,48 +544,6 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             // one's keys are under way. Every thread converts what it copied.
             uint32_t kv = 0, tile = 0;              // tiles of keys or values converted, of cells
             uint32_t sent = 0;                      // of keys or values copied
-            // The queries of a segment: 16 lanes a row of 128 elements, 8 each, times a power of two that brings
-            // the largest to 2^13 at least, as binary16 numbers (and the rest, into the second tile).
-            auto queries = [&](const Segment &w) {
-                constexpr int AT_ONCE = kSplit ? 2 : 4;
-                const int l = lane & 15, n0 = min(p.seqs, w.count), tiles = w.count > p.seqs ? 2 : 1;
-                const float c = a.scale * LOG2E;
-#pragma unroll 1
-                for (int e = 0; e < 16 * tiles; e += AT_ONCE) {
-                    const int i = e >> 4, rows = (i == 0 ? n0 : w.count - n0) * p.group;
-                    float4 u[AT_ONCE], v[AT_ONCE];
-#pragma unroll
-                    for (int q = 0; q < AT_ONCE; ++q) {
-                        const int r = 32 * quarter + 2 * (e - 16 * i + q) + (lane >> 4), seq = r / p.group;
-                        const QT *from = static_cast<const QT *>(a.q) + (w.first + i * p.seqs + seq) * a.q_seq_stride +
-                                         (w.kvh * p.group + r - seq * p.group) * a.q_head_stride + 8 * l;
-                        u[q] = r < rows ? load4(from) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        v[q] = r < rows ? load4(from + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-#pragma unroll
-                    for (int q = 0; q < AT_ONCE; ++q) {
-                        const int r = 32 * quarter + 2 * (e - 16 * i + q) + (lane >> 4);
-                        float top = fmaxf(fmaxf(fmaxf(fabsf(u[q].x), fabsf(u[q].y)), fmaxf(fabsf(u[q].z), fabsf(u[q].w))),
-                                          fmaxf(fmaxf(fabsf(v[q].x), fabsf(v[q].y)), fmaxf(fabsf(v[q].z), fabsf(v[q].w))));
-#pragma unroll
-                        for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
-                        int ex = 0;
-                        if (top > 0.0f && top < INFINITY) frexpf(top, &ex);
-                        ex = max(-113, ex);   // 2^(14 - ex) and 2^(ex - 14) are fp32 numbers
-                        const float up = ldexpf(1.0f, 14 - ex);
-                        uint32_t hi[4], lo[4];
-                        split(u[q].x * up, u[q].y * up, hi[0], lo[0]);
-                        split(u[q].z * up, u[q].w * up, hi[1], lo[1]);
-                        split(v[q].x * up, v[q].y * up, hi[2], lo[2]);
-                        split(v[q].z * up, v[q].w * up, hi[3], lo[3]);
-                        st_shared_v4(base + i * TILE_BYTES + tile_at(r, l), hi[0], hi[1], hi[2], hi[3]);
-                        if (kSplit) st_shared_v4(base + TILE_BYTES + tile_at(r, l), lo[0], lo[1], lo[2], lo[3]);
-                        if (l == 0) scales->row[i * ROWS + r] = c * ldexpf(1.0f, ex - 14);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->q_full);
-            };
             auto send = [&](const void *what) {
                 const char *from = static_cast<const char *>(what) + 16 * (lane & 7);
                 const uint32_t to = raws + (sent % F::RAW) * (TILE_BYTES / 2) + 16 * (32 * quarter * 8 + lane);
@@ -646,9 +605,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 send(a.kv.k);
                 send(a.kv.v);
             }
-            uint32_t converted = 0;                 // segments begun with conversions
             while (ok && next.count > 0) {
-                const bool first = t_next == next.t0;
                 s = next;
                 t = t_next;
                 mask = row_mask;
@@ -664,12 +621,6 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 if (more) {
                     row();
                     send(a.kv.k);
-                }
-                if (first) {
-                    ok = wait_warp(&bars->q_empty, (converted & 1) ^ 1);
-                    if (!ok) break;
-                    queries(s);
-                    ++converted;
                 }
                 const uint32_t side = tile % SIDES;
                 ok = wait_warp(&bars->side_empty[side], ((tile / SIDES) & 1) ^ 1);
@@ -810,13 +761,56 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         // Once through the code as soon as there is a segment, while its first cells come: its instructions are
         // then there (the first tile took 3 to 5 us without it). It waits for nothing, signals nothing and
         // writes nothing.
-        bool dry = true;
+        bool dry = !kInt8;   // their loops are longer than the wait for the first cells
         for (uint32_t k = 0;; k += dry ? 0 : 1, dry = false) {
             if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
             const Segment s = bars->seg[k % SEGS];
             __syncwarp();
             if (lane == 0 && !dry) mbar_arrive(&bars->seg_empty[k % SEGS]);
             if (s.count == 0) break;
+            if constexpr (kInt8) {
+                // The segment's queries: 16 lanes a row of 128 elements, 8 each, times a power of two that brings
+                // the largest to 2^13 at least, as binary16 numbers (and the rest, into the second tile).
+                if (!wait_warp(&bars->q_empty, (k & 1) ^ 1)) break;
+                const int l8 = lane & 15;
+                const float to_log2 = a.scale * LOG2E;
+#pragma unroll 1
+                for (int tile = 0; tile < (s.count > p.seqs ? 2 : 1); ++tile) {
+                    const int seqs = min(p.seqs, s.count - tile * p.seqs), r0 = 16 * warp + (lane >> 4);
+                    float4 u[8], v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = r0 + 2 * e, seq = r / p.group;
+                        const QT *from = static_cast<const QT *>(a.q) + (s.first + tile * p.seqs + seq) * a.q_seq_stride +
+                                         (s.kvh * p.group + r - seq * p.group) * a.q_head_stride + 8 * l8;
+                        const bool have = seq < seqs;
+                        u[e] = have ? load4(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        v[e] = have ? load4(from + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = r0 + 2 * e;
+                        float top = fmaxf(fmaxf(fmaxf(fabsf(u[e].x), fabsf(u[e].y)), fmaxf(fabsf(u[e].z), fabsf(u[e].w))),
+                                          fmaxf(fmaxf(fabsf(v[e].x), fabsf(v[e].y)), fmaxf(fabsf(v[e].z), fabsf(v[e].w))));
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+                        int ex = 0;
+                        if (top > 0.0f && top < INFINITY) frexpf(top, &ex);
+                        ex = max(-113, ex);   // 2^(14 - ex) and 2^(ex - 14) are fp32 numbers
+                        const float up = ldexpf(1.0f, 14 - ex);
+                        uint32_t hi[4], lo[4];
+                        split(u[e].x * up, u[e].y * up, hi[0], lo[0]);
+                        split(u[e].z * up, u[e].w * up, hi[1], lo[1]);
+                        split(v[e].x * up, v[e].y * up, hi[2], lo[2]);
+                        split(v[e].z * up, v[e].w * up, hi[3], lo[3]);
+                        st_shared_v4(base + tile * TILE_BYTES + tile_at(r, l8), hi[0], hi[1], hi[2], hi[3]);
+                        if (kSplit) st_shared_v4(base + TILE_BYTES + tile_at(r, l8), lo[0], lo[1], lo[2], lo[3]);
+                        if (l8 == 0) scales->row[tile * ROWS + r] = to_log2 * ldexpf(1.0f, ex - 14);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->q_full);
+            }
             const bool two = s.count > p.seqs || dry;
             const int n = dry ? 1 : s.t1 - s.t0;
             const int count = !two ? s.count : i == 0 ? p.seqs : s.count - p.seqs;   // sequences of this stream's rows
