@@ -13,9 +13,9 @@
 // cosine are of at most an eighth, in fp32.
 //
 // Work. A row is a token's head. 16 lanes (a team) take a row, 8 elements each;
-// a CTA has 16 teams and a power of two of tokens, every team rows of one token
+// a CTA has 8 or 16 teams and a power of two of tokens, every team rows of one token
 // alone, so that a lane's 8 sines and cosines stay in registers. They are found
-// once per token by 64 threads, through shared memory. Rows are read ahead, four
+// once per token by 64 threads, through shared memory. Rows are read ahead, three or four
 // per team, before anything that has to be looked up (the token's sequence by a
 // 32-way search in cu, its length, its page).
 #include <algorithm>
@@ -31,8 +31,9 @@
 namespace qsa {
 namespace {
 
-constexpr int THREADS = 256, LANES = 16, TEAMS = THREADS / LANES;
-constexpr int MAX_TOKENS = TEAMS, MAX_PAIRS = 64;
+constexpr int FEW_TOKENS_THREADS = 256, MANY_TOKENS_THREADS = 128;
+constexpr int LANES = 16;
+constexpr int MAX_PAIRS = 64;
 constexpr int NO_PAGES = -1;
 
 struct Params {
@@ -158,10 +159,11 @@ __device__ __forceinline__ int sequence_of(const Params &p, int t) {
 }
 
 // kPages: NO_PAGES (rotate), QSA_BF16, QSA_F16 or QSA_I8.
-template <typename T, int kPages>
+template <typename T, int kPages, int THREADS>
 __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ Params p) {
     constexpr bool kAppend = kPages != NO_PAGES;
-    constexpr int AHEAD = 4;
+    constexpr int AHEAD = kPages == QSA_I8 ? 3 : 4;
+    constexpr int TEAMS = THREADS / LANES, MAX_TOKENS = TEAMS;
     __shared__ __align__(16) float cosines[MAX_TOKENS][MAX_PAIRS], sines[MAX_TOKENS][MAX_PAIRS];
     __shared__ Place places[MAX_TOKENS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, team = tid / LANES, l = tid % LANES;
@@ -299,6 +301,7 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ P
                     store_row(static_cast<T *>(p.k_out) + t * p.k_out_tok + h * p.k_out_head + 8 * l, y);
             }
             if constexpr (kPages == QSA_I8) {
+                if (!__any_sync(FULL_MASK, k < 2)) continue;   // queries alone
                 // The team's largest magnitude; both teams take part.
                 float top = 0.0f, odd = 0.0f;
 #pragma unroll
@@ -313,12 +316,19 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ P
                     const __half scale = __float2half_rn(fminf(__fdiv_rn(top, 127.0f), 65504.0f));
                     const float f = __half2float(scale);
                     uint32_t w[2] = {0u, 0u};
-                    if (!bad && f > 0.0f)
+                    if (!bad && f > 0.0f) {
+                        // The quotient by the reciprocal is off by less than 2^-15 (of 127 at most, two roundings; near
+                        // zero it is cut off all the same): where that could change the nearest integer, divide.
+                        const float inv = __frcp_rn(f);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const int code = min(127, max(-127, __float2int_rn(__fdiv_rn(y[e], f))));
+                            float q = y[e] * inv;
+                            const float off = fabsf(q - rintf(q));
+                            if (!(off < 0.4999f)) q = __fdiv_rn(y[e], f);
+                            const int code = min(127, max(-127, __float2int_rn(q)));
                             w[e >> 2] |= (static_cast<uint32_t>(code) & 255u) << (8 * (e & 3));
                         }
+                    }
                     int8_t *to = static_cast<int8_t *>(k == 0 ? p.kv.k : p.kv.v) + places[mine].at + h * p.kv.head_stride + 8 * l;
                     *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
                     if (l == 0)
@@ -334,12 +344,13 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ P
     }
 }
 
-template <typename T, int kPages>
-cudaError_t launch(Params p, cudaStream_t stream) {
-    // A CTA has some 64 rows where there are CTAs enough for all SMs.
-    const int rows = 2 * p.nkv + p.nheads;
+template <typename T, int kPages, int THREADS>
+cudaError_t launch_threads(Params p, cudaStream_t stream) {
+    // A CTA has some 64 rows (32 of 32 bits) where there are CTAs enough for all SMs. Measured: 16,384 tokens of 24
+    // heads 34.9 us, with 32 rows 38.8, with 128 36.3; 4,097 of 16 heads in 32 bits 11.8 us, with 64 rows 13.0.
+    const int rows = 2 * p.nkv + p.nheads, wanted = 128 / static_cast<int>(sizeof(T));
     p.tokens = 1;
-    while (p.tokens < MAX_TOKENS && p.tokens * rows < 64 && p.ntok / p.tokens >= 2 * device_sm_count()) p.tokens *= 2;
+    while (p.tokens < THREADS / LANES && p.tokens * rows < wanted && p.ntok / p.tokens >= 2 * device_sm_count()) p.tokens *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((p.ntok + p.tokens - 1) / p.tokens);
     cfg.blockDim = dim3(THREADS);
@@ -349,7 +360,16 @@ cudaError_t launch(Params p, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rows_kernel<T, kPages>, p);
+    return cudaLaunchKernelEx(&cfg, rows_kernel<T, kPages, THREADS>, p);
+}
+
+// Few tokens' rows are spread over more threads each (one token of 48 rows 3.7 us, with 128 threads 4.3); many tokens'
+// CTAs are small, so that more of them are at different stages on an SM (ragged prompts of 48 rows a token 101 us, with 256
+// threads 138).
+template <typename T, int kPages>
+cudaError_t launch(const Params &p, cudaStream_t stream) {
+    return p.ntok <= 2 * device_sm_count() ? launch_threads<T, kPages, FEW_TOKENS_THREADS>(p, stream)
+                                           : launch_threads<T, kPages, MANY_TOKENS_THREADS>(p, stream);
 }
 
 template <typename T>
