@@ -4,7 +4,7 @@
 
 One attention layer with random projections stands for a model. The prompts'
 tokens attend with a sliding window and the first tokens always visible
-(``window_attn``), their keys and values go into pages, and each further token
+(``window_attn``), their keys and values go into pages (``cache_append``), and each further token
 attends its sequence's pages (``paged_attn``), which also adds the weight that
 every cell received to a running mass. When a cache has grown past its budget
 by a few pages, ``cache_evict`` keeps the first cells, the most recent ones and
@@ -54,11 +54,10 @@ class PagedCache:
         """New cells ``[n, nkv, 128]`` at the end of sequence ``s``."""
         n, at = k.shape[0], self.length[s]
         self._reserve(s, at + n)
-        j = torch.arange(at, at + n, device=self.device)
-        page, slot = self.table[s].long()[j // self.page], j % self.page
-        self.k[page, slot], self.v[page, slot] = k, v
         self.length[s] = at + n
         self.lens[s] = at + n
+        cu = None if n == 1 else torch.tensor([0, n], dtype=torch.int32, device=self.device)
+        qsa.cache_append(k, v, self.k, self.v, self.table[s:s + 1], self.lens[s:s + 1], cu=cu)
 
     def attend(self, q: torch.Tensor, window: int = -1, sinks: int = 0) -> torch.Tensor:
         """Each sequence's newest token ``q [sequences, heads, 128]`` over its cells; the mass grows."""

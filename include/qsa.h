@@ -318,7 +318,7 @@ qsa_status qsa_get_device_error(uint32_t *code, cudaStream_t stream);
  * no counterpart). For the kernels launched after the call: every spin-wait
  * gives up after wait_limit_ns (default 2,000,000,000; in the prompt attention
  * 8 us more for every 128 keys of the call, as items take that long, in the shared
- * prefix's for every 128 cells that a CTA may have), and
+ * prefix's for every 128 cells of the prefix table's width), and
  * `faults` plants a wait that cannot complete so that the time-out path runs:
  *   bit 0: the tensor-core scorer's CTA 0 never loads its first key piece
  *          (qsa_block_scores, _q8, _gmax and _select_static with nq > 4);
@@ -570,8 +570,8 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
  * Sums and softmax statistics are fp32. The weights of prefix cells are rounded
  * once to the 16-bit operand type (the pages', binary16 for int8 cells), as in
  * qsa_window_attn; for fp32 queries they keep 22 bits.
- * Errors and limits as qsa_paged_attn; nheads / nkv above 128, ngroups above 65,535 or prefix_cols * page_size above 2^30 returns
- * QSA_ERR_UNSUPPORTED.
+ * Errors and limits as qsa_paged_attn; nheads / nkv above 128, ngroups above 65,535
+ * or prefix_cols * page_size above 2^30 returns QSA_ERR_UNSUPPORTED.
  */
 size_t qsa_prefix_attn_scratch_bytes(int nseq, int ngroups, int nheads, int nkv, int prefix_cols, int table_cols,
                                      int page_size);

@@ -1249,9 +1249,9 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs &a, cudaStream_t stream) {
     p.slots = reinterpret_cast<float4 *>(b + y.slots);
     p.slot_refs = reinterpret_cast<float2 *>(b + y.slot_refs);
     p.whole_rows = y.whole_rows;
-    // Waits last as long as a CTA's whole range may: some 2 us a tile.
-    const long long tiles = (static_cast<long long>(capacity) + ROWS - 1) / ROWS * a.kv.nkv * (a.nseq + a.ngroups);
-    p.wait_ns = wait_limit_ns() + 8192ull * static_cast<uint64_t>(std::min(tiles / y.grid + 1, 1LL << 24));
+    // A wait may last as long as a CTA takes for a whole prefix: some 2 to 4 us a tile.
+    p.wait_ns = wait_limit_ns() + 8192ull * ((static_cast<uint64_t>(capacity) + ROWS - 1) / ROWS);
+    if (a.kv.npages == 0) p.a.kv.k = p.a.kv.v = const_cast<void *>(a.q);   // nothing is read, but addresses are formed
     p.stall = (debug_inject() & 32u) != 0u;
     PagedAttnArgs own = {};
     own.q = a.q;
