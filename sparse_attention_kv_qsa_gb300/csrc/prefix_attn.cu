@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         constexpr uint32_t idesc_v = idesc | (1u << 16);   // second operand contiguous in N
         bool ok = true;
         uint32_t kv = 0;                   // tiles of keys or values so far
-        uint32_t ns = 0;                   // products S of each stream so far, modulo 2^16
+        uint32_t odd = 0;                  // bit i: stream i has had an odd number of products S
         for (uint32_t k = 0; ok; ++k) {
             if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
             const Segment s = bars->seg[k % SEGS];
@@ -686,11 +686,11 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                     if (one) tc_mma_bf16(tmem + S_COL + 128 * i, qd + step + half, kd + step, idesc, kk > 0 ? 1u : 0u);
                 }
                 if (one) tc_commit(&bars->s_full[i]);
-                ns += 1u << (16 * i);
+                odd ^= 1u << i;
             };
             // Stream i's last weights times the values in a slot.
             auto outputs = [&](int i, uint32_t slot, bool first) {
-                const uint32_t p_col = tmem + S_COL + 128 * i, o_col = tmem + O_COL + 128 * i, parity = ((ns >> (16 * i)) - 1) & 1;
+                const uint32_t p_col = tmem + S_COL + 128 * i, o_col = tmem + O_COL + 128 * i, parity = ~(odd >> i) & 1u;
                 const uint64_t vd = sw128_mnmajor_desc(ring + slot * TILE_BYTES, HALF);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {

@@ -344,6 +344,26 @@ def test_past_32_bit_offsets(dev):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("nseq", [3, 40])
+def test_more_than_65536_tiles_a_cta(dev, nseq):
+    """The longest prefix, 2^30 cells, of which all pages are one: every wait of 110,000 tiles a CTA has its turn.
+    Keys of zeros weigh every cell 1, and values are -1, 0 or 1: a CTA's sums are integers below 110,400 x 128 < 2^24,
+    so exact. Joining rounds to 2^-24 some 80 times (5e-6, a share of lse's 20.8 2e-6): far from half a step of
+    bfloat16 beside the mean of 128 such values, which it holds exactly."""
+    g = torch.Generator(device=dev).manual_seed(0)
+    k = torch.zeros((1, 128, 2, 128), device=dev, dtype=BF16)
+    v = torch.randint(-1, 2, k.shape, generator=g, device=dev).to(BF16)
+    q = torch.randn((nseq, 8, 128), generator=g, device=dev, dtype=BF16)
+    table = torch.zeros((1, 2 ** 23), dtype=torch.int32, device=dev)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    own, none = torch.zeros((nseq, 0), dtype=torch.int32, device=dev), torch.zeros(nseq, dtype=torch.int32, device=dev)
+    out, lse = qsa.prefix_attn(q, k, v, table, ints(2 ** 30), ints(0, nseq), own, none)
+    assert qsa.device_error(dev) == 0
+    want = v[0].float().mean(0).to(BF16).repeat_interleave(4, 0)
+    assert torch.equal(out, want.expand_as(out))
+    assert float((lse - 30 * math.log(2)).abs().max()) <= 2e-5
+
+
 def test_binding_refusals(dev):
     b = Shared(dev, [(2, 50), (2, 20)], [5, 5, 5, 5], 2, 4, 16, BF16, BF16)
     base = dict(q=b.q, k=b.k, v=b.v, pt=b.ptable, pl=b.plens, cu=b.cu, t=b.table, ln=b.lens, ks=None)
