@@ -485,7 +485,8 @@ qsa_status qsa_cache_evict(const qsa_kv_pages *kv, int nseq, const int32_t *page
  * by -angle where `inverse` (which undoes it, and is its gradient). The
  * position of token t for pair p is positions[axis[p] * position_stride + t]:
  * one axis for text, several (time, height, width) for images and video, an
- * axis for each pair. A pair whose axis is outside [0, naxes) is not turned.
+ * axis for each pair. A pair whose axis is outside [0, naxes) is turned by 0. The
+ * formula holds for every angle: an infinity or NaN in a pair can make both NaN.
  * The angle is reduced exactly (fixed point, 2^-32 turns), whatever the
  * position; sine, cosine and products are fp32, the result is rounded once.
  * A frequency that is not finite gives NaN.
@@ -567,7 +568,8 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
  * scratch   at least qsa_prefix_attn_scratch_bytes(...) bytes, 16-byte aligned
  *           (0 for nseq = 0 and for arguments that are refused); no contents
  *           need survive.
- * Sums and softmax statistics are fp32. The weights of prefix cells are rounded
+ * Sums and softmax statistics are fp32, those of a prefix over 32,768 cells at
+ * most (4,096 for fp32 queries) before they are added to others. The weights of prefix cells are rounded
  * once to the 16-bit operand type (the pages', binary16 for int8 cells), as in
  * qsa_window_attn; for fp32 queries they keep 22 bits.
  * Errors and limits as qsa_paged_attn; nheads / nkv above 128, ngroups above 65,535

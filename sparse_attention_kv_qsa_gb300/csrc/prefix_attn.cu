@@ -40,11 +40,11 @@
 // two query tiles the halves.
 //
 // Measured (GB300, in a CUDA graph, all three launches): 32 sequences of 32 heads on 8 KV heads behind 65,536 bfloat16
-// cells 65 us, 46 of them streaming at 5.8 TB/s; 64 behind 4,096, up to 1,024 cells of their own, 46 us (floor 24.5,
-// mostly own cells); 512 of 16 heads on 2 behind 8,192 binary16 cells 59 us: a tile of cells for two row tiles takes
+// cells 66.5 us, 46 of them streaming at 5.8 TB/s; 64 behind 4,096, up to 1,024 cells of their own, 46.6 us (floor 24.5,
+// mostly own cells); 512 of 16 heads on 2 behind 8,192 binary16 cells 59.4 us: a tile of cells for two row tiles takes
 // 1.95 us, the tensor cores 1.1 of that, because a tile's weights (1.4 us), its products and the next scores
 // follow one another. 40 fp32 sequences of 8 heads on 2 behind 3 texts of up to 65,536 int8 cells 53 us, 2 us a
-// tile. 4 behind 600 cells 12.5 us: launches, and code that comes for the first time.
+// tile. 4 behind 600 cells 12.9 us: launches, and code that comes for the first time.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -84,6 +84,11 @@ struct Form {
     // Weights are kept 2^7 above their reference where the operand is binary16, whose smallest
     // numbers they would otherwise reach sooner: 2^(8 + 7) is within its range.
     static constexpr float LIFT = kKv == QSA_BF16 ? 0.0f : 7.0f;
+    // Tiles that one sum in tensor memory takes: the tensor cores cut a sum off at every step of 16 cells, always towards
+    // zero, so that its error grows with its length (262,144 cells around 1 in one CTA were 6e-4 too small, with two
+    // halves more). Longer segments are cut and their parts added as rounded fp32 numbers: 8e-5 then, a fraction of a
+    // rounding to 16 bits, and 7e-6 for fp32 results. 65,536 cells in one CTA take 1 % longer so (fp32 queries 8 %).
+    static constexpr int CHAIN = kSplit ? 32 : 256;
 };
 
 struct Params {
@@ -118,6 +123,7 @@ struct Segment {
     int len, t0, t1;            // cells of the prefix; tiles of cells
     int slot;                   // of the partial results, -1: whole
     int row;                    // of them, where whole
+    int behind;                 // whether its sums are added to those of the segment before it
 };
 
 struct alignas(16) Bars {
@@ -390,9 +396,14 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         long long left = range;
         int g = sh_group, kvh = sh_kvh, b = sh_block, t = sh_tile;   // unused without a group
         Group x = sh_at;
+        int uncut = 0;                              // tiles of the block's part that are to follow
+        bool begins = true;                         // the range
+        Segment s = {};
         for (uint32_t k = 0;; ++k) {
-            Segment s = {};
-            if (left > 0) {
+            if (uncut > 0) {
+                s.t0 = s.t1;
+                s.behind = 1;
+            } else if (left > 0) {
                 const int n = static_cast<int>(min(static_cast<long long>(x.tiles - t), left));
                 s.g = g;
                 s.kvh = kvh;
@@ -400,9 +411,11 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 s.count = min(p.block, x.first + x.count - s.first);
                 s.len = x.len;
                 s.t0 = t;
-                s.t1 = t + n;
+                s.behind = 0;
+                uncut = n;
                 const bool whole = n == x.tiles;
-                s.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (k == 0 ? 0 : 1);
+                s.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (begins ? 0 : 1);
+                begins = false;
                 const int block = block_number(p, x, g, b);
                 s.row = whole_row(p, block, s.first);
                 if (t == 0 && lane == 0) {
@@ -430,7 +443,12 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                         }
                     }
                 }
+            } else {
+                s = {};
             }
+            const int m = min(uncut, F::CHAIN);
+            s.t1 = s.t0 + m;
+            uncut -= m;
             if (!wait_warp(&bars->seg_empty[k % SEGS], ((k / SEGS) & 1) ^ 1)) break;
             if (lane == 0) {
                 bars->seg[k % SEGS] = s;
@@ -771,6 +789,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         // then there (the first tile took 3 to 5 us without it). It waits for nothing, signals nothing and
         // writes nothing.
         bool dry = !kInt8;   // their loops are longer than the wait for the first cells
+        float2 held = make_float2(-INFINITY, 0.0f);   // reference and weights' sum of the rows so far, where segments are cut
         for (uint32_t k = 0;; k += dry ? 0 : 1, dry = false) {
             if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
             const Segment s = bars->seg[k % SEGS];
@@ -1000,6 +1019,41 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 const size_t from = s.slot < 0 ? static_cast<size_t>(s.kvh) * p.whole_rows : static_cast<size_t>(s.slot) * BLOCK;
                 float4 *to = (s.slot < 0 ? p.whole : p.slots) + from * 32;
                 const int piece0 = two ? 0 : 2 * i, piece1 = two ? 4 : 2 * i + 2;   // with the same rows, half of the columns each
+                if (__builtin_expect(s.behind, 0)) {
+                    // The rows' sums so far, which this thread wrote, are added in tensor memory.
+                    const float top = fmaxf(held.x, sum.x), ref = top == -INFINITY ? 0.0f : top, f = ex2(sum.x - ref), f_held = ex2(held.x - ref);
+                    sum = make_float2(top, fmaf(sum.y, f, held.y * f_held));
+                    f0 = any0 ? f0 * f : 0.0f;
+                    f1 = any1 ? f1 * f : 0.0f;
+#pragma unroll 1
+                    for (int piece = piece0; piece < piece1; ++piece) {
+                        const uint32_t o_at = tmem + lanes + O_COL + (two ? 128 * i : 0) + 32 * piece;
+                        uint32_t o[32];
+                        tmem_read32(o_at, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(any0 ? __uint_as_float(o[e]) * f0 : 0.0f);
+                        if (!two) {
+                            uint32_t u[32];
+                            tmem_read32(tmem + lanes + O_COL + 128 + 32 * piece, u);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + (any1 ? __uint_as_float(u[e]) * f1 : 0.0f));
+                        }
+                        if (valid)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 was = ld_in(to + sums_at(at, 8 * piece + e));
+                                const float y[4] = {was.x, was.y, was.z, was.w};
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) o[4 * e + q] = __float_as_uint(fmaf(y[q], f_held, __uint_as_float(o[4 * e + q])));
+                            }
+                        tmem_st32(o_at, o);
+                    }
+                    tmem_st_wait();
+                    f0 = 1.0f;
+                    any0 = true;
+                    any1 = false;
+                }
+                held = sum;
 #pragma unroll 1
                 for (int piece = dry ? 3 : piece0; piece < piece1; ++piece) {
                     uint32_t o[32];

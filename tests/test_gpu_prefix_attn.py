@@ -364,6 +364,45 @@ def test_more_than_65536_tiles_a_cta(dev, nseq):
     assert float((lse - 30 * math.log(2)).abs().max()) <= 2e-5
 
 
+@pytest.mark.parametrize("kv,qt", KINDS)
+@pytest.mark.parametrize("members", [1, 3])
+def test_long_sums(dev, members, kv, qt):
+    """152 groups of 2^18 cells, so that a CTA holds all of one: 32 times the same 8,192, pages in an order of their own
+    each time, whose values lie around 1. Tensor cores cut a sum off, by 2^-23 of it at every step of 16 cells: always
+    towards zero, so that all results are off alike. The mean of their errors is bounded by 2^-23 of the sums of |p v| for
+    each step of 256 tiles (fp32 queries: 32, with two steps), and 2^-23 for each part that is added."""
+    groups, n, pages = 152, 2 ** 18, 64
+    g = torch.Generator(device=dev).manual_seed(members)
+    k, v = (torch.randn((pages, 128, 1, 128), generator=g, device=dev) for _ in range(2))
+    v += 1
+    ks = vs = None
+    if kv == I8:
+        ks, vs = ((x.abs().amax(-1) / 127).to(F16) for x in (k, v))
+        k, v = ((x / sc.float()[..., None]).round().clamp(-127, 127) for x, sc in ((k, ks), (v, vs)))
+    k, v = k.to(kv), v.to(kv)
+    q = (4 * torch.randn((groups * members, 64, 128), generator=g, device=dev)).to(qt)
+    table = torch.rand((groups, n // (128 * pages), pages), generator=g, device=dev).argsort(-1).to(torch.int32).reshape(groups, -1)
+    own, none = torch.zeros((len(q), 0), dtype=torch.int32, device=dev), torch.zeros(len(q), dtype=torch.int32, device=dev)
+    cu = torch.arange(0, len(q) + 1, members, dtype=torch.int32, device=dev)
+    lens = torch.full((groups,), n, dtype=torch.int32, device=dev)
+    out, lse = qsa.prefix_attn(q, k, v, table, lens, cu, own, none, k_scale_f16=ks, v_scale_f16=vs)
+    assert qsa.device_error(dev) == 0
+    (kd, seen), (vd, _) = (ref.paged_cells(x, sc, torch.arange(pages, device=dev), 128 * pages, 0, 128) for x, sc in ((k, ks), (v, vs)))
+    chain = 32 if qt == F32 else 256
+    steps, parts = chain * (16 if qt == F32 else 8), n // 128 // chain
+    p_half = 2.0 ** -22 if qt == F32 else ref.half_step(BF16 if kv == BF16 else F16)
+    off = total = 0.0
+    for s in range(0, len(q), 76):
+        o, l, _, size, S = ref.attend(q[s:s + 76].reshape(1, -1, 128), kd, vd, seen[None], 128 ** -0.5)
+        tol, ltol = ref.bounds(o, l, size, S, 128 * chain + parts, qt, p_half)
+        tol = tol + 2 * 128 * pages * 2.0 ** -32 * size.amax(-1, keepdim=True)
+        got = out[s:s + 76].reshape(1, -1, 128)
+        ref.check(got, o, tol, ("out", s))
+        ref.check(lse[s:s + 76].reshape(1, -1), l + math.log(n // (128 * pages)), ltol + 2.0 ** -20, ("lse", s))
+        off, total = off + float((got.double() - o).sum()), total + float(size.sum())
+    assert abs(off) <= (steps + parts) * 2.0 ** -23 * total
+
+
 def test_binding_refusals(dev):
     b = Shared(dev, [(2, 50), (2, 20)], [5, 5, 5, 5], 2, 4, 16, BF16, BF16)
     base = dict(q=b.q, k=b.k, v=b.v, pt=b.ptable, pl=b.plens, cu=b.cu, t=b.table, ln=b.lens, ks=None)
