@@ -61,6 +61,11 @@ bool good_rows(const int64_t *strides, int dtype, int ntok, int nheads, bool wri
     return !written || ((ntok == 1 || strides[0] >= 128) && (nheads == 1 || strides[1] >= 128));
 }
 
+// Whether rows are read and written at the same address with other strides: some would be read after others are written.
+bool entangled(const void *in, const int64_t *in_strides, const void *out, const int64_t *out_strides, int ntok, int nheads) {
+    return in == out && ((ntok > 1 && in_strides[0] != out_strides[0]) || (nheads > 1 && in_strides[1] != out_strides[1]));
+}
+
 bool row_type(int dtype) { return dtype == QSA_F32 || dtype == QSA_F16 || dtype == QSA_BF16; }
 
 }  // namespace
@@ -75,7 +80,7 @@ qsa_status qsa_rotate(const void *x, qsa_dtype dtype, const int64_t *strides, in
     if (!good_rows(strides, dtype, ntok, nheads, false) || !good_rows(strides + 2, dtype, ntok, nheads, true)) return QSA_ERR_INVALID;
     if (ntok == 0) return QSA_OK;
     if (nheads > MAX_HEADS) return QSA_ERR_UNSUPPORTED;
-    if (!aligned(x, 16) || !aligned(out, 16)) return QSA_ERR_INVALID;
+    if (!aligned(x, 16) || !aligned(out, 16) || entangled(x, strides, out, strides + 2, ntok, nheads)) return QSA_ERR_INVALID;
     return from_cuda(qsa::launch_rotate(x, dtype, strides, ntok, nheads, *rotation, out, stream));
 }
 
@@ -106,8 +111,9 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
     if (ntok == 0 || nseq == 0) return QSA_OK;
     if (nseq > MAX_SEQS || nheads > MAX_HEADS || nkv > MAX_HEADS) return QSA_ERR_UNSUPPORTED;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(lens, 4)) return QSA_ERR_INVALID;
-    if (nheads > 0 && (!aligned(q, 16) || !aligned(q_out, 16))) return QSA_ERR_INVALID;
-    if (k_out != nullptr && !aligned(k_out, 16)) return QSA_ERR_INVALID;
+    if (nheads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || entangled(q, strides + 4, q_out, strides + 6, ntok, nheads)))
+        return QSA_ERR_INVALID;
+    if (k_out != nullptr && (!aligned(k_out, 16) || entangled(k, strides, k_out, strides + 8, ntok, nkv))) return QSA_ERR_INVALID;
     if (cu != nullptr && !aligned(cu, 4)) return QSA_ERR_INVALID;
     if (table_cols > 0 && !aligned(page_table, 4)) return QSA_ERR_INVALID;
     const qsa::CacheAppendArgs a{k, v, q, dtype, strides, ntok, nheads, *kv, page_table, table_cols, table_stride,

@@ -97,6 +97,18 @@ def test_append_argument_errors(lib, bad):
     assert append(lib, **bad) == INVALID
 
 
+def test_in_place_with_other_strides(lib):
+    """Rows would be read after others have been written there."""
+    for st in ((0, 128, 1024, 128), (1024, 128, 2048, 128), (128, 640, 1024, 128)):
+        assert rotate(lib, strides=st, out=A) == INVALID
+        q, k = (256, 128, 256, 128) + st + (256, 128), (0, 128, 256, 128, 1024, 128, 1024, 128, 256, 128)
+        assert append(lib, strides=q, q_out=A) == INVALID and append(lib, strides=k, k_out=A) == INVALID
+    # a dimension of one element has no stride: these get as far as the device, which is not there
+    if not torch.cuda.is_available():
+        assert rotate(lib, ntok=1, strides=(0, 128, 1024, 128), out=A) not in (OK, INVALID)
+        assert rotate(lib, nheads=1, strides=(1024, 0, 1024, 128), out=A) not in (OK, INVALID)
+
+
 def test_append_limits(lib):
     assert append(lib, ntok=0, k=None, v=None, q=None, q_out=None, lens=None) == OK
     assert append(lib, nseq=0) == OK
