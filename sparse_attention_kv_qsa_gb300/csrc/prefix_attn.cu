@@ -46,6 +46,7 @@
 // follow one another. 40 fp32 sequences of 8 heads on 2 behind 3 texts of up to 65,536 int8 cells 53 us, 2 us a
 // tile. 4 behind 600 cells 12.9 us: launches, and code that comes for the first time.
 #include <algorithm>
+#include <cfloat>
 #include <cstring>
 #include <type_traits>
 
@@ -833,7 +834,9 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                         split(v[e].z * up, v[e].w * up, hi[3], lo[3]);
                         st_shared_v4(base + tile * TILE_BYTES + tile_at(r, l8), hi[0], hi[1], hi[2], hi[3]);
                         if (kSplit) st_shared_v4(base + TILE_BYTES + tile_at(r, l8), lo[0], lo[1], lo[2], lo[3]);
-                        if (l8 == 0) scales->row[tile * ROWS + r] = to_log2 * ldexpf(1.0f, ex - 14);
+                        // Not 0, which an absent cell's -infinity would make NaN: a smaller factor's logits (sums are below 2^44)
+                        // and this one's are 0 beside 1 all the same.
+                        if (l8 == 0) scales->row[tile * ROWS + r] = fmaxf(to_log2 * ldexpf(1.0f, ex - 14), FLT_MIN);
                     }
                 }
                 __syncwarp();

@@ -257,6 +257,15 @@ def test_queries_of_the_whole_range_over_int8_cells(dev, qmul, scale):
     b.check(*b.call(scale=scale), scale=scale)
 
 
+@pytest.mark.parametrize("qt,qmul,scale", [(F32, 1e-13, 1e-30), (F32, 1.0, 1e-42), (BF16, 1.0, 1e-42), (F16, 1e-3, 1e-42), (F32, 0.0, 1e-42)])
+def test_small_queries_and_scales_over_int8_cells(dev, qt, qmul, scale):
+    """Logits that vanish: the mean of the cells that are there, beside absent ones (a tile's end, a hole)."""
+    b = Shared(dev, [(5, 600), (3, 128), (30, 300), (2, 1)], lens_of(40), 2, 4, 16, I8, qt)
+    b.ptable[0, 4] = -1
+    b.q = b.q * qmul
+    b.check(*b.call(scale=scale), scale=scale)
+
+
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 @pytest.mark.parametrize("kv,qt", [(BF16, BF16), (F16, F16)])
 def test_odd_values_reach_who_sees_them_alone(dev, kv, qt, bad):
