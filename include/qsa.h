@@ -487,8 +487,8 @@ qsa_status qsa_cache_evict(const qsa_kv_pages *kv, int nseq, const int32_t *page
  * one axis for text, several (time, height, width) for images and video, an
  * axis for each pair. A pair whose axis is outside [0, naxes) is turned by 0. The
  * formula holds for every angle: an infinity or NaN in a pair can make both NaN.
- * The angle is reduced exactly (fixed point, 2^-32 turns), whatever the
- * position; sine, cosine and products are fp32, the result is rounded once.
+ * The angle is reduced exactly (fixed point, to 2^-32 turns), whatever the
+ * position and the frequency; sine, cosine and products are fp32, the result is rounded once.
  * A frequency that is not finite gives NaN.
  * freqs     fp32 [npairs]; npairs a multiple of 8, 8 .. 64.
  * axis      int32 [npairs], or NULL: axis 0 for every pair.

@@ -8,7 +8,7 @@
 //
 // Angles. freq / 2 pi is held in 64-bit fixed point (turns), and position times
 // that modulo 2^64 is the angle's fraction of a turn without any error but the
-// factor's own (2^-64 of the position): whole turns fall off by themselves at
+// factor's own (2^-64 of the position, for every frequency): whole turns fall off by themselves at
 // every position. The nearest quarter turn is split off, so that sine and
 // cosine are of at most an eighth, in fp32.
 //
@@ -126,15 +126,29 @@ __device__ __forceinline__ void store_row(T *p, const float (&x)[8]) {
         reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// |freq| / 2 pi in units of 2^-64 turns, modulo a turn; the sign goes to the product.
+// |freq| / 2 pi in units of 2^-64 turns, modulo a turn, at most 1.01 units too small; the sign goes to the product.
+// |freq| = m 2^e has 24 bits m; whole turns of the largest, e = 104, are gone from the 104th bit of 1 / (2 pi) on, and 96
+// bits from there give the product's fraction.
 __device__ __forceinline__ uint64_t turns_of(float freq) {
-    constexpr uint64_t INV_2PI = 2935890503282001226ull;   // 2^64 / (2 pi)
+    // 2^256 / (2 pi), 64 bits each
+    constexpr uint64_t W0 = 0x28be60db9391054aull, W1 = 0x7f09d5f47d4d3770ull, W2 = 0x36d8a5664f10e410ull, W3 = 0x7f9458eaf7aef158ull;
     const uint32_t bits = __float_as_uint(freq), field = (bits >> 23) & 255u;
-    const uint64_t m = (bits & 0x7FFFFFu) | (field > 0u ? 0x800000u : 0u);
+    const uint32_t m = (bits & 0x7FFFFFu) | (field > 0u ? 0x800000u : 0u);
     const int e = static_cast<int>(max(field, 1u)) - 150;   // |freq| = m 2^e
-    const uint64_t lo = m * INV_2PI, hi = __umul64hi(m, INV_2PI);
+    uint64_t a = W0, b = W1;                                 // from bit max(e, 0) on
+    if (e > 0) {                                             // |freq| of 2^24 at least
+        const bool far = e >= 64;
+        const int r = e & 63;
+        const uint64_t w0 = far ? W1 : W0, w1 = far ? W2 : W1, w2 = far ? W3 : W2;
+        a = r == 0 ? w0 : (w0 << r) | (w1 >> (64 - r));
+        b = r == 0 ? w1 : (w1 << r) | (w2 >> (64 - r));
+    }
+    // m (a + b / 2^64) with b's upper half, in 32-bit products: m x 2^-32 of a unit at most is left out.
+    const uint64_t p1 = static_cast<uint64_t>(m) * static_cast<uint32_t>(a >> 32);
+    const uint64_t p0 = static_cast<uint64_t>(m) * static_cast<uint32_t>(a) + __umulhi(m, static_cast<uint32_t>(b >> 32));
+    const uint64_t lo = p0 + (p1 << 32), hi = (p1 + (p0 >> 32)) >> 32;
     uint64_t t;
-    if (e >= 0) t = e < 64 ? lo << e : 0;
+    if (e >= 0) t = lo;
     else if (e > -64) t = (lo >> -e) | (hi << (64 + e));
     else t = e > -128 ? hi >> (-e - 64) : 0;
     return static_cast<int32_t>(bits) < 0 ? 0 - t : t;

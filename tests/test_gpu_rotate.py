@@ -72,6 +72,22 @@ def test_every_position(dev, freq):
     check(x, qsa.rotate(x, p, freqs), p, freqs)
 
 
+@pytest.mark.parametrize("freq", [1.0, 1e4, 16777216.0, 3.0e7, -1.2345e9, 9.2e18, 2.5e19, 1.5e20, -7.7e30, 3.4028234663852886e38])
+def test_every_frequency(dev, freq):
+    """Angles of the largest frequencies at positions of all of int32, to the same tolerance as others'."""
+    freqs = torch.full((64,), freq, device=dev)
+    freqs[1::2] *= 0.999
+    freqs[2::3] *= 0.7654321
+    p = torch.tensor([0, 1, -1, 3, 1000, -999999, 2 ** 24 + 1, 2 ** 30 + 12345, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device=dev)
+    g = torch.Generator(device=dev).manual_seed(4)
+    x = torch.randn((p.numel(), 2, 128), generator=g, device=dev)
+    angle = token_ref.far_angles(p, freqs)[:, None]
+    a, b = x.cpu().double().chunk(2, -1)
+    want = torch.cat((a * angle.cos() - b * angle.sin(), b * angle.cos() + a * angle.sin()), -1)
+    err = (qsa.rotate(x, p, freqs).cpu().double() - want).abs()
+    assert bool((err <= token_ref.rotate_tol(x, want, F32, 64)).all()), float(err.max())
+
+
 def test_odd_frequencies_and_axes(dev):
     x, positions, freqs, _ = inputs(dev, 9, 2, F32, axes=2)
     axis = torch.zeros(64, dtype=torch.int32, device=dev)

@@ -145,6 +145,20 @@ def test_reference_rotation_by_hand():
     assert abs(float(far[0, 0, 0]) - math.cos(2 ** 31 - 1)) < 1e-9
 
 
+def test_reference_far_angles_by_hand():
+    assert token_ref.inv_two_pi(48) == int(2 ** 48 / (2 * math.pi))
+    p, f = torch.tensor([7, -3, 2 ** 31 - 1], dtype=torch.int32), torch.tensor([0.5, 2.0, 1e4])
+    far = token_ref.far_angles(p, f)
+    # the product is below 2^45 and so exact in 64 bits; cos and sin of it are the C library's
+    for i, a in enumerate(p.tolist()):
+        for j, b in enumerate(f.tolist()):
+            assert abs(math.cos(far[i, j]) - math.cos(a * b)) < 1e-14 and abs(math.sin(far[i, j]) - math.sin(a * b)) < 1e-14
+    # 2^100 radians: its fraction of a turn from 1 / (2 pi) to 500 places
+    turns = (token_ref.inv_two_pi(500) << 100) % (1 << 500) / (1 << 500)
+    want = token_ref.far_angles(torch.tensor([1]), torch.tensor([2.0 ** 100]))
+    assert abs(float(want) - 2 * math.pi * (turns - round(turns))) < 1e-14
+
+
 def test_reference_codes_by_hand():
     x = torch.zeros((4, 128)); x[0, 0], x[0, 1], x[0, 2] = 127.0, -63.5, 0.5
     x[2, 3], x[3, 0] = 1e-9, math.inf

@@ -27,6 +27,34 @@ def rotate(x, positions, freqs, axis=None, interleaved=False, inverse=False):
     return y
 
 
+def inv_two_pi(bits):
+    """2^bits / (2 pi), cut off, by Machin's formula in whole numbers."""
+    unit = 1 << (bits + 64)
+
+    def arctan_of_one_over(n):
+        term, total, k = unit // n, 0, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term, k = term // (n * n), k + 2
+        return total
+
+    return (unit << bits) // (8 * (4 * arctan_of_one_over(5) - arctan_of_one_over(239)))
+
+
+def far_angles(positions, freqs):
+    """position x frequency less its whole turns [ntok, pairs], in 64 bits: worked out in whole numbers of 2^-400 turns."""
+    unit, inv = 1 << 400, inv_two_pi(400)
+    rows = []
+    for p in positions.tolist():
+        row = []
+        for f in freqs.tolist():
+            n, d = float(f).as_integer_ratio()
+            turns = p * n * inv // d % unit
+            row.append((turns - unit if 2 * turns > unit else turns) / unit * 2 * np.pi)
+        rows.append(row)
+    return torch.tensor(rows, dtype=torch.float64)
+
+
 def rotate_tol(x, want, dtype, pairs, interleaved=False):
     """sincospif is off by one unit in the last place (2^-24 below 1), its argument by 2^-24 of at most pi/4 and the
     angle by 2^-32 turns and 2^-33 of the factor's: below 1.9 x 2^-24 for each sine and cosine; a product and a fused
