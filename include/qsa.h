@@ -506,8 +506,9 @@ typedef struct {
  * out[t][h] = x[t][h] rotated by token t's position (see qsa_rotation).
  * x, out    [ntok][nheads][128] of dtype (QSA_F32, QSA_F16 or QSA_BF16),
  *           16-byte aligned; strides: element strides of x per token and head,
- *           then of out, multiples of 16 bytes, not negative, those of out at
- *           least 128 (a dimension of one element: any). out is x itself (same
+ *           then of out, multiples of 16 bytes, not negative; out's rows are
+ *           apart: its narrower stride is at least 128, its wider one past the last row of the
+ *           narrower dimension (a dimension of one element: any). out is x itself (same
  *           address and strides) or does not overlap it.
  * A missing rotation, frequency or position, a bad type, size, pointer or
  * stride returns QSA_ERR_INVALID; nheads or naxes above 65,535 QSA_ERR_UNSUPPORTED.
@@ -537,7 +538,8 @@ qsa_status qsa_rotate(const void *x, qsa_dtype dtype, const int64_t *strides, in
  * strides   of k, v, q, q_out, k_out per token and head (10 numbers, elements;
  *           rules as qsa_rotate's; those of missing tensors are not read).
  *           q_out may be q itself, k_out k itself; no other overlaps.
- * The pages' strides are at least 128 here (a dimension of one element: any).
+ * The pages' cells (and scales) are apart here: each stride of a dimension of
+ * more than one element is past all that the narrower ones span.
  * cu        int32 [nseq + 1], ascending (values are clamped to [0, ntok]), or
  *           NULL: one token per sequence, ntok == nseq.
  * page_table, lens as qsa_paged_attn. Errors and limits as qsa_paged_attn.

@@ -2,6 +2,7 @@
 // caller's stream. Declarations and the contract: include/qsa.h.
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "cache_internal.cuh"
 
@@ -55,10 +56,36 @@ qsa_status check_rotation(const qsa_rotation *r, bool own_positions) {
     return r->naxes > MAX_HEADS ? QSA_ERR_UNSUPPORTED : QSA_OK;
 }
 
+// A dimension of memory that is written: `count` pieces, `stride` elements apart.
+struct Dim {
+    int64_t stride, count;
+};
+// The dimensions of more than one piece, the widest stride last; returns how many there are.
+int by_stride(Dim *dims, int n) {
+    int kept = 0;
+    for (int i = 0; i < n; ++i)
+        if (dims[i].count > 1) dims[kept++] = dims[i];
+    for (int i = 1; i < kept; ++i)
+        for (int j = i; j > 0 && dims[j].stride < dims[j - 1].stride; --j) std::swap(dims[j], dims[j - 1]);
+    return kept;
+}
+// Whether no two pieces of `size` elements share any: each dimension steps over all that the narrower ones span.
+bool apart(Dim *dims, int n, int64_t size) {
+    n = by_stride(dims, n);
+    int64_t span = size;
+    for (int i = 0; i < n; ++i) {
+        if (dims[i].stride < span) return false;
+        // Past 2^62 elements there is no memory: nothing wider can be stepped over either way.
+        span = dims[i].stride > (int64_t{1} << 62) / dims[i].count ? int64_t{1} << 62 : dims[i].stride * (dims[i].count - 1) + span;
+    }
+    return true;
+}
+
 // Strides per token and head of [ntok][nheads][128] elements, which rows written must not share.
 bool good_rows(const int64_t *strides, int dtype, int ntok, int nheads, bool written) {
     if (!good_stride(strides[0], dtype) || !good_stride(strides[1], dtype)) return false;
-    return !written || ((ntok == 1 || strides[0] >= 128) && (nheads == 1 || strides[1] >= 128));
+    Dim dims[2] = {{strides[0], ntok}, {strides[1], nheads}};
+    return !written || nheads > MAX_HEADS || apart(dims, 2, QSA_D);   // so many are unsupported, whatever their strides
 }
 
 // Whether rows are read and written at the same address with other strides: some would be read after others are written.
@@ -102,12 +129,12 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
         return QSA_ERR_INVALID;
     if (k_out != nullptr && !good_rows(strides + 8, dtype, ntok, nkv, true)) return QSA_ERR_INVALID;
     // Cells are written: none may share its memory with another.
-    if ((kv->npages > 1 && kv->page_stride < 128) || (kv->page_size > 1 && kv->cell_stride < 128) ||
-        (nkv > 1 && kv->head_stride < 128))
-        return QSA_ERR_INVALID;
-    if (kv->dtype == QSA_I8 && ((kv->npages > 1 && kv->scale_page_stride < 1) || (kv->page_size > 1 && kv->scale_cell_stride < 1) ||
-                                (nkv > 1 && kv->scale_head_stride < 1)))
-        return QSA_ERR_INVALID;
+    Dim cells[3] = {{kv->page_stride, kv->npages}, {kv->cell_stride, kv->page_size}, {kv->head_stride, nkv}};
+    if (!apart(cells, 3, QSA_D)) return QSA_ERR_INVALID;
+    if (kv->dtype == QSA_I8) {
+        Dim scales[3] = {{kv->scale_page_stride, kv->npages}, {kv->scale_cell_stride, kv->page_size}, {kv->scale_head_stride, nkv}};
+        if (!apart(scales, 3, 1)) return QSA_ERR_INVALID;
+    }
     if (ntok == 0 || nseq == 0) return QSA_OK;
     if (nseq > MAX_SEQS || nheads > MAX_HEADS || nkv > MAX_HEADS) return QSA_ERR_UNSUPPORTED;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(lens, 4)) return QSA_ERR_INVALID;

@@ -109,6 +109,43 @@ def test_in_place_with_other_strides(lib):
         assert rotate(lib, nheads=1, strides=(1024, 0, 1024, 128), out=A) not in (OK, INVALID)
 
 
+OVER_ONE_ANOTHER = [(128, 128), (640, 128), (128, 512), (896, 128), (136, 128), (1024, 8)]      # of 5 tokens of 8 heads
+
+
+@pytest.mark.parametrize("st", OVER_ONE_ANOTHER)
+def test_rows_written_over_one_another(lib, st):
+    """Row [t][h] is also row [t + 1][h - i], or begins inside of it."""
+    assert rotate(lib, strides=(1024, 128) + st) == INVALID
+    assert append(lib, strides=(256, 128, 256, 128, 1024, 128) + st + (256, 128)) == INVALID
+    if st[1] == 128 and st[0] < 256 or st[1] < 128:                                             # 2 KV heads
+        assert append(lib, strides=(256, 128, 256, 128, 1024, 128, 1024, 128) + st) == INVALID
+
+
+@pytest.mark.parametrize("bad", [dict(page_stride=128), dict(page_stride=256), dict(page_stride=4096 - 8), dict(cell_stride=128),
+                                 dict(head_stride=256), dict(head_stride=2048, cell_stride=256),
+                                 dict(INT8, scale_page_stride=31), dict(INT8, scale_cell_stride=1), dict(INT8, scale_head_stride=2),
+                                 dict(INT8, scale_page_stride=1, scale_cell_stride=1, scale_head_stride=1)])
+def test_cells_written_over_one_another(lib, bad):
+    assert append(lib, pages(**bad)) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="gets as far as the device, which must not be there")
+@pytest.mark.parametrize("st", [(1024, 128), (128, 640), (1152, 144), (6144, 128), (1032, 128), (136, 1024), (1 << 40, 1 << 50), (1 << 55, 128)])
+def test_rows_apart_in_any_order(lib, st):
+    """Tokens outside heads, heads outside tokens, slices of something wider."""
+    assert rotate(lib, strides=(1024, 128) + st) not in (OK, INVALID)
+    assert append(lib, strides=(256, 128, 256, 128, 1024, 128) + st + (256, 128)) not in (OK, INVALID)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="gets as far as the device, which must not be there")
+@pytest.mark.parametrize("good", [dict(head_stride=16 * 128, cell_stride=128), dict(page_stride=8192), dict(cell_stride=512, page_stride=16 * 512),
+                                  dict(head_stride=256, cell_stride=512, page_stride=16 * 512), dict(npages=1, page_stride=0),
+                                  dict(page_size=1, cell_stride=0), dict(nkv=1, head_stride=0),
+                                  dict(INT8, scale_cell_stride=1, scale_head_stride=16), dict(page_stride=256, cell_stride=100 * 256)])
+def test_cells_apart_in_any_order(lib, good):
+    assert append(lib, pages(**good)) not in (OK, INVALID)
+
+
 def test_append_limits(lib):
     assert append(lib, ntok=0, k=None, v=None, q=None, q_out=None, lens=None) == OK
     assert append(lib, nseq=0) == OK
