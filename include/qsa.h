@@ -509,7 +509,8 @@ typedef struct {
  *           then of out, multiples of 16 bytes, not negative; out's rows are
  *           apart: its narrower stride is at least 128, its wider one past the last row of the
  *           narrower dimension (a dimension of one element: any). out is x itself (same
- *           address and strides) or does not overlap it.
+ *           address and strides) or does not overlap it: refused where the strides
+ *           are the same, or the address; other overlaps are the caller's to avoid.
  * A missing rotation, frequency or position, a bad type, size, pointer or
  * stride returns QSA_ERR_INVALID; nheads or naxes above 65,535 QSA_ERR_UNSUPPORTED.
  */
@@ -539,7 +540,8 @@ qsa_status qsa_rotate(const void *x, qsa_dtype dtype, const int64_t *strides, in
  *           rules as qsa_rotate's; those of missing tensors are not read).
  *           q_out may be q itself, k_out k itself; no other overlaps.
  * The pages' cells (and scales) are apart here: each stride of a dimension of
- * more than one element is past all that the narrower ones span.
+ * more than one element is past all that the narrower ones span,
+ * and keys' do not overlap values'.
  * cu        int32 [nseq + 1], ascending (values are clamped to [0, ntok]), or
  *           NULL: one token per sequence, ntok == nseq.
  * page_table, lens as qsa_paged_attn. Errors and limits as qsa_paged_attn.

@@ -88,9 +88,32 @@ bool good_rows(const int64_t *strides, int dtype, int ntok, int nheads, bool wri
     return !written || nheads > MAX_HEADS || apart(dims, 2, QSA_D);   // so many are unsupported, whatever their strides
 }
 
-// Whether rows are read and written at the same address with other strides: some would be read after others are written.
-bool entangled(const void *in, const int64_t *in_strides, const void *out, const int64_t *out_strides, int ntok, int nheads) {
-    return in == out && ((ntok > 1 && in_strides[0] != out_strides[0]) || (nheads > 1 && in_strides[1] != out_strides[1]));
+// Whether a piece at a, moved by `by`, meets one of dims' (which are apart, and ordered): of a dimension's steps only the two
+// beside `by` can bring it within what the narrower ones span.
+bool meets(int64_t by, const Dim *dims, int n, int64_t size) {
+    if (n == 0) return by > -size && by < size;
+    const int64_t stride = dims[n - 1].stride, count = dims[n - 1].count;
+    const int64_t below = by / stride - (by % stride < 0 ? 1 : 0);
+    for (int64_t step = below; step <= below + 1; ++step)
+        if (step > -count && step < count && meets(by - step * stride, dims, n - 1, size)) return true;
+    return false;
+}
+// Two sets of pieces of the same dimensions, at a and b: whether they share memory. Sizes and strides in elements of `bytes`.
+bool overlap(const void *a, const void *b, Dim *dims, int n, int64_t size, int bytes) {
+    n = by_stride(dims, n);
+    for (int i = 0; i < n; ++i) {
+        if (dims[i].stride > (int64_t{1} << 60) / bytes) return false;   // no memory is so wide
+        dims[i].stride *= bytes;
+    }
+    return meets(static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)), dims, n, size * bytes);
+}
+
+// Whether rows would be read after others are written there: out over in, but for the very same rows. Where the strides
+// differ, the same address alone is looked at.
+bool entangled(const void *in, const int64_t *in_strides, const void *out, const int64_t *out_strides, int dtype, int ntok, int nheads) {
+    if ((ntok > 1 && in_strides[0] != out_strides[0]) || (nheads > 1 && in_strides[1] != out_strides[1])) return in == out;
+    Dim dims[2] = {{out_strides[0], ntok}, {out_strides[1], nheads}};
+    return in != out && overlap(in, out, dims, 2, QSA_D, element_size(dtype));
 }
 
 bool row_type(int dtype) { return dtype == QSA_F32 || dtype == QSA_F16 || dtype == QSA_BF16; }
@@ -107,7 +130,7 @@ qsa_status qsa_rotate(const void *x, qsa_dtype dtype, const int64_t *strides, in
     if (!good_rows(strides, dtype, ntok, nheads, false) || !good_rows(strides + 2, dtype, ntok, nheads, true)) return QSA_ERR_INVALID;
     if (ntok == 0) return QSA_OK;
     if (nheads > MAX_HEADS) return QSA_ERR_UNSUPPORTED;
-    if (!aligned(x, 16) || !aligned(out, 16) || entangled(x, strides, out, strides + 2, ntok, nheads)) return QSA_ERR_INVALID;
+    if (!aligned(x, 16) || !aligned(out, 16) || entangled(x, strides, out, strides + 2, dtype, ntok, nheads)) return QSA_ERR_INVALID;
     return from_cuda(qsa::launch_rotate(x, dtype, strides, ntok, nheads, *rotation, out, stream));
 }
 
@@ -138,9 +161,15 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
     if (ntok == 0 || nseq == 0) return QSA_OK;
     if (nseq > MAX_SEQS || nheads > MAX_HEADS || nkv > MAX_HEADS) return QSA_ERR_UNSUPPORTED;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(lens, 4)) return QSA_ERR_INVALID;
-    if (nheads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || entangled(q, strides + 4, q_out, strides + 6, ntok, nheads)))
+    if (nheads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || entangled(q, strides + 4, q_out, strides + 6, dtype, ntok, nheads)))
         return QSA_ERR_INVALID;
-    if (k_out != nullptr && (!aligned(k_out, 16) || entangled(k, strides, k_out, strides + 8, ntok, nkv))) return QSA_ERR_INVALID;
+    if (k_out != nullptr && (!aligned(k_out, 16) || entangled(k, strides, k_out, strides + 8, dtype, ntok, nkv))) return QSA_ERR_INVALID;
+    if (kv->npages > 0) {
+        Dim both[3] = {{kv->page_stride, kv->npages}, {kv->cell_stride, kv->page_size}, {kv->head_stride, nkv}};
+        if (overlap(kv->k, kv->v, both, 3, QSA_D, element_size(kv->dtype))) return QSA_ERR_INVALID;
+        Dim scales[3] = {{kv->scale_page_stride, kv->npages}, {kv->scale_cell_stride, kv->page_size}, {kv->scale_head_stride, nkv}};
+        if (kv->dtype == QSA_I8 && overlap(kv->k_scale_f16, kv->v_scale_f16, scales, 3, 1, 2)) return QSA_ERR_INVALID;
+    }
     if (cu != nullptr && !aligned(cu, 4)) return QSA_ERR_INVALID;
     if (table_cols > 0 && !aligned(page_table, 4)) return QSA_ERR_INVALID;
     const qsa::CacheAppendArgs a{k, v, q, dtype, strides, ntok, nheads, *kv, page_table, table_cols, table_stride,

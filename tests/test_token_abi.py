@@ -109,6 +109,13 @@ def test_in_place_with_other_strides(lib):
         assert rotate(lib, nheads=1, strides=(1024, 0, 1024, 128), out=A) not in (OK, INVALID)
 
 
+def far(**kw):
+    """Pages whose values lie far from their keys."""
+    d = dict(v=A + (1 << 30), v_scale_f16=A + (1 << 31) if "k_scale_f16" in kw else None)
+    d.update({k: v for k, v in kw.items() if k != "v_scale_f16"})
+    return pages(**d)
+
+
 OVER_ONE_ANOTHER = [(128, 128), (640, 128), (128, 512), (896, 128), (136, 128), (1024, 8)]      # of 5 tokens of 8 heads
 
 
@@ -116,9 +123,9 @@ OVER_ONE_ANOTHER = [(128, 128), (640, 128), (128, 512), (896, 128), (136, 128), 
 def test_rows_written_over_one_another(lib, st):
     """Row [t][h] is also row [t + 1][h - i], or begins inside of it."""
     assert rotate(lib, strides=(1024, 128) + st) == INVALID
-    assert append(lib, strides=(256, 128, 256, 128, 1024, 128) + st + (256, 128)) == INVALID
+    assert append(lib, far(), strides=(256, 128, 256, 128, 1024, 128) + st + (256, 128)) == INVALID
     if st[1] == 128 and st[0] < 256 or st[1] < 128:                                             # 2 KV heads
-        assert append(lib, strides=(256, 128, 256, 128, 1024, 128, 1024, 128) + st) == INVALID
+        assert append(lib, far(), strides=(256, 128, 256, 128, 1024, 128, 1024, 128) + st) == INVALID
 
 
 @pytest.mark.parametrize("bad", [dict(page_stride=128), dict(page_stride=256), dict(page_stride=4096 - 8), dict(cell_stride=128),
@@ -126,7 +133,7 @@ def test_rows_written_over_one_another(lib, st):
                                  dict(INT8, scale_page_stride=31), dict(INT8, scale_cell_stride=1), dict(INT8, scale_head_stride=2),
                                  dict(INT8, scale_page_stride=1, scale_cell_stride=1, scale_head_stride=1)])
 def test_cells_written_over_one_another(lib, bad):
-    assert append(lib, pages(**bad)) == INVALID
+    assert append(lib, far(**bad)) == INVALID
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="gets as far as the device, which must not be there")
@@ -134,7 +141,7 @@ def test_cells_written_over_one_another(lib, bad):
 def test_rows_apart_in_any_order(lib, st):
     """Tokens outside heads, heads outside tokens, slices of something wider."""
     assert rotate(lib, strides=(1024, 128) + st) not in (OK, INVALID)
-    assert append(lib, strides=(256, 128, 256, 128, 1024, 128) + st + (256, 128)) not in (OK, INVALID)
+    assert append(lib, far(), strides=(256, 128, 256, 128, 1024, 128) + st + (256, 128)) not in (OK, INVALID)
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="gets as far as the device, which must not be there")
@@ -143,6 +150,44 @@ def test_rows_apart_in_any_order(lib, st):
                                   dict(page_size=1, cell_stride=0), dict(nkv=1, head_stride=0),
                                   dict(INT8, scale_cell_stride=1, scale_head_stride=16), dict(page_stride=256, cell_stride=100 * 256)])
 def test_cells_apart_in_any_order(lib, good):
+    assert append(lib, far(**good)) not in (OK, INVALID)
+
+
+def rows_of(at, strides, ntok, nheads, size=128):
+    """The bytes that rows of bfloat16 elements lie at, as a set of 16-byte pieces."""
+    return {(at + 2 * (t * strides[0] + h * strides[1])) // 16 + i for t in range(ntok) for h in range(nheads) for i in range(size // 8)}
+
+
+def test_rows_over_the_rows_that_are_read(lib):
+    """Whatever 16 bytes the output begins behind or before the input: refused where any row of it lies on one that is read,
+    but for the very same rows; what gets past is what a plain list of all pieces finds apart."""
+    at = 1 << 20
+    for st, ntok, nheads in (((1024, 128), 5, 8), ((128, 640), 5, 8), ((1152, 144), 3, 8), ((2048, 256), 4, 3), ((512, 128), 1, 3), ((264, 64), 4, 1)):
+        read = rows_of(at, st, ntok, nheads)
+        for off in [i for i in range(-700, 700)] + [5 * 1024 // 8, -5 * 1024 // 8, 1 << 20]:
+            out = at + 16 * off
+            meets = off != 0 and not read.isdisjoint(rows_of(out, st, ntok, nheads))
+            if meets or not torch.cuda.is_available():   # others get as far as the device, which must not be there
+                assert (rotate(lib, x=at, out=out, strides=st + st, ntok=ntok, nheads=nheads) == INVALID) == meets, (st, off)
+    st = (1024, 128)
+    for off in (2048, -2048, 256, 4096, 16):             # tokens, heads, and part of a row
+        assert append(lib, far(), q=at, q_out=at + off) == INVALID
+        if abs(off) < 4096:                              # k's tokens are 256 elements apart
+            assert append(lib, far(), k=at, k_out=at + off) == INVALID
+
+
+@pytest.mark.parametrize("bad", [dict(v=A), dict(v=A + 256), dict(k=A + 4096, v=A), dict(v=A + 16), dict(v=A + 2 * 4096 * 99),
+                                 dict(INT8, v=A + (1 << 30), v_scale_f16=A), dict(INT8, v=A + (1 << 30), v_scale_f16=A + 64 * 99),
+                                 dict(INT8, v=A + (1 << 30), k_scale_f16=A + 2, v_scale_f16=A)])
+def test_keys_cells_over_values_cells(lib, bad):
+    assert append(lib, pages(**bad)) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="gets as far as the device, which must not be there")
+@pytest.mark.parametrize("good", [dict(v=A + 2 * 4096, page_stride=8192), dict(k=A + 2 * 4096, v=A, page_stride=8192),
+                                  dict(v=A + 256, head_stride=256, cell_stride=512, page_stride=8192), dict(v=A + 2 * 4096 * 100),
+                                  dict(INT8, v=A + (1 << 30), v_scale_f16=A + 64, scale_page_stride=64), dict(v=A + 512, npages=1, page_stride=0, page_size=1)])
+def test_keys_cells_beside_values_cells(lib, good):
     assert append(lib, pages(**good)) not in (OK, INVALID)
 
 
