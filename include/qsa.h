@@ -512,7 +512,8 @@ typedef struct {
  *           address and strides) or does not overlap it: refused where the strides
  *           are the same, or the address; other overlaps are the caller's to avoid.
  * A missing rotation, frequency or position, a bad type, size, pointer or
- * stride returns QSA_ERR_INVALID; nheads or naxes above 65,535 QSA_ERR_UNSUPPORTED.
+ * stride returns QSA_ERR_INVALID; nheads or naxes above 65,535 or ntok above
+ * 2^31 - 64 QSA_ERR_UNSUPPORTED.
  */
 qsa_status qsa_rotate(const void *x, qsa_dtype dtype, const int64_t *strides, int ntok, int nheads,
                       const qsa_rotation *rotation, void *out, cudaStream_t stream);
@@ -544,7 +545,7 @@ qsa_status qsa_rotate(const void *x, qsa_dtype dtype, const int64_t *strides, in
  * and keys' do not overlap values'.
  * cu        int32 [nseq + 1], ascending (values are clamped to [0, ntok]), or
  *           NULL: one token per sequence, ntok == nseq.
- * page_table, lens as qsa_paged_attn. Errors and limits as qsa_paged_attn.
+ * page_table, lens as qsa_paged_attn. Errors and limits as qsa_paged_attn and qsa_rotate.
  */
 qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dtype dtype, const int64_t *strides,
                             int ntok, int nheads, const qsa_kv_pages *kv, const int32_t *page_table, int table_cols,

@@ -9,6 +9,7 @@
 namespace {
 
 constexpr long long MAX_SEQS = 65535, MAX_HEADS = 65535, MAX_CELLS = 1LL << 30, MAX_TILES = 1LL << 38;
+constexpr long long MAX_TOKENS = (1LL << 31) - 64;   // what a CTA adds to a token's number stays within 32 bits
 
 bool aligned(const void *p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -129,7 +130,7 @@ qsa_status qsa_rotate(const void *x, qsa_dtype dtype, const int64_t *strides, in
     if (s != QSA_OK) return s;
     if (!good_rows(strides, dtype, ntok, nheads, false) || !good_rows(strides + 2, dtype, ntok, nheads, true)) return QSA_ERR_INVALID;
     if (ntok == 0) return QSA_OK;
-    if (nheads > MAX_HEADS) return QSA_ERR_UNSUPPORTED;
+    if (nheads > MAX_HEADS || ntok > MAX_TOKENS) return QSA_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || !aligned(out, 16) || entangled(x, strides, out, strides + 2, dtype, ntok, nheads)) return QSA_ERR_INVALID;
     return from_cuda(qsa::launch_rotate(x, dtype, strides, ntok, nheads, *rotation, out, stream));
 }
@@ -159,7 +160,7 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
         if (!apart(scales, 3, 1)) return QSA_ERR_INVALID;
     }
     if (ntok == 0 || nseq == 0) return QSA_OK;
-    if (nseq > MAX_SEQS || nheads > MAX_HEADS || nkv > MAX_HEADS) return QSA_ERR_UNSUPPORTED;
+    if (nseq > MAX_SEQS || nheads > MAX_HEADS || nkv > MAX_HEADS || ntok > MAX_TOKENS) return QSA_ERR_UNSUPPORTED;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(lens, 4)) return QSA_ERR_INVALID;
     if (nheads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || entangled(q, strides + 4, q_out, strides + 6, dtype, ntok, nheads)))
         return QSA_ERR_INVALID;

@@ -153,6 +153,13 @@ def test_cells_apart_in_any_order(lib, good):
     assert append(lib, far(**good)) not in (OK, INVALID)
 
 
+@pytest.mark.parametrize("ntok", [2 ** 31 - 63, 2 ** 31 - 1])
+def test_more_tokens_than_numbers(lib, ntok):
+    """Their numbers, and those behind them in the last CTA, would pass 32 bits. Rows of stride 0 need no memory for that."""
+    assert rotate(lib, ntok=ntok, nheads=1, strides=(0, 0, 128, 128)) == UNSUPPORTED
+    assert append(lib, far(), ntok=ntok, nheads=2, strides=(0, 0, 0, 0, 0, 0, 256, 128, 256, 128)) == UNSUPPORTED
+
+
 def rows_of(at, strides, ntok, nheads, size=128):
     """The bytes that rows of bfloat16 elements lie at, as a set of 16-byte pieces."""
     return {(at + 2 * (t * strides[0] + h * strides[1])) // 16 + i for t in range(ntok) for h in range(nheads) for i in range(size // 8)}
