@@ -577,8 +577,9 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
  * most (4,096 for fp32 queries) before they are added to others. The weights of prefix cells are rounded
  * once to the 16-bit operand type (the pages', binary16 for int8 cells), as in
  * qsa_window_attn; for fp32 queries they keep 22 bits.
- * Errors and limits as qsa_paged_attn; nheads / nkv above 128, ngroups above 65,535
- * or prefix_cols * page_size above 2^30 returns QSA_ERR_UNSUPPORTED.
+ * Errors and limits as qsa_paged_attn; nheads / nkv above 128, ngroups above 65,535,
+ * prefix_cols * page_size above 2^30 or (nseq + ngroups) * nheads *
+ * ceil(prefix_cols * page_size / 128) above 2^38 returns QSA_ERR_UNSUPPORTED.
  */
 size_t qsa_prefix_attn_scratch_bytes(int nseq, int ngroups, int nheads, int nkv, int prefix_cols, int table_cols,
                                      int page_size);

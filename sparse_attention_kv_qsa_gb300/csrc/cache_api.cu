@@ -117,6 +117,14 @@ bool entangled(const void *in, const int64_t *in_strides, const void *out, const
     return in != out && overlap(in, out, dims, 2, QSA_D, element_size(dtype));
 }
 
+// The limits of the shared prefix's attention; the sizes are not negative, nkv divides nheads.
+bool prefix_fits(long long nseq, long long ngroups, long long nheads, int nkv, long long prefix_cols, long long table_cols, int page_size) {
+    const long long prefix = prefix_cols * page_size, capacity = table_cols * page_size;
+    return nseq <= MAX_SEQS && ngroups <= MAX_SEQS && nheads <= MAX_HEADS && nkv <= MAX_HEADS && nheads / nkv <= 128 &&
+           prefix <= MAX_CELLS && capacity <= MAX_CELLS && nseq * nheads <= MAX_CELLS && nseq * nheads * ((capacity + 63) / 64) <= MAX_TILES &&
+           (nseq + ngroups) * nheads * ((prefix + 127) / 128) <= MAX_TILES;
+}
+
 bool row_type(int dtype) { return dtype == QSA_F32 || dtype == QSA_F16 || dtype == QSA_BF16; }
 
 }  // namespace
@@ -222,8 +230,7 @@ qsa_status qsa_paged_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_stride
 size_t qsa_prefix_attn_scratch_bytes(int nseq, int ngroups, int nheads, int nkv, int prefix_cols, int table_cols,
                                      int page_size) {
     if (nseq < 1 || ngroups < 0 || nheads < 1 || nkv < 1 || nheads % nkv != 0 || prefix_cols < 0 || table_cols < 0 ||
-        page_size < 1 || nseq > MAX_SEQS || ngroups > MAX_SEQS || nheads > MAX_HEADS || nheads / nkv > 128 ||
-        static_cast<long long>(prefix_cols) * page_size > MAX_CELLS || static_cast<long long>(table_cols) * page_size > MAX_CELLS)
+        page_size < 1 || !prefix_fits(nseq, ngroups, nheads, nkv, prefix_cols, table_cols, page_size))
         return 0;
     return qsa::prefix_attn_scratch_bytes({nseq, ngroups, nheads, nkv, prefix_cols * page_size, table_cols * page_size});
 }
@@ -244,12 +251,7 @@ qsa_status qsa_prefix_attn(const void *q, qsa_dtype q_dtype, int64_t q_seq_strid
     if (s != QSA_OK) return s;
     if (!good_stride(q_seq_stride, q_dtype) || !good_stride(q_head_stride, q_dtype)) return QSA_ERR_INVALID;
     if (nseq == 0) return QSA_OK;
-    const int group = nheads / kv->nkv;
-    if (nseq > MAX_SEQS || ngroups > MAX_SEQS || nheads > MAX_HEADS || group > 128 ||
-        static_cast<long long>(nseq) * nheads > MAX_CELLS ||
-        static_cast<long long>(nseq) * nheads * ((static_cast<long long>(table_cols) * kv->page_size + 63) / 64) > MAX_TILES ||
-        static_cast<long long>(nseq + ngroups) * nheads * ((static_cast<long long>(prefix_cols) * kv->page_size + 127) / 128) > MAX_TILES)
-        return QSA_ERR_UNSUPPORTED;
+    if (!prefix_fits(nseq, ngroups, nheads, kv->nkv, prefix_cols, table_cols, kv->page_size)) return QSA_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lens, 4) || !aligned(cu_seqs, 4)) return QSA_ERR_INVALID;
     if (ngroups > 0 && (!aligned(prefix_lens, 4) || (prefix_cols > 0 && !aligned(prefix_table, 4)))) return QSA_ERR_INVALID;
     if (lse != nullptr && !aligned(lse, 4)) return QSA_ERR_INVALID;

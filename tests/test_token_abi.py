@@ -294,3 +294,16 @@ def test_prefix_limits(lib):
     assert n(64, 3, 32, 8, 4096, 64, 16) >= n(4, 1, 32, 8, 4096, 64, 16) > 0 and n(4, 0, 8, 2, 0, 0, 16) > 0
     # partial results do not grow with the lengths: bounded by the GPU, the sequences and the groups
     assert n(64, 1, 32, 8, 1 << 25, 1 << 25, 16) == n(64, 1, 32, 8, 1 << 20, 1 << 20, 16) <= 128 << 20
+
+
+# nseq, groups, heads, KV heads, prefix columns, columns, page size: each just past a limit, and just within
+@pytest.mark.parametrize("within,past", [((65535, 1, 16384, 16384, 1, 1, 16), (65535, 1, 16385, 16385, 1, 1, 16)),
+                                         ((2048, 2048, 64, 1, 1 << 20, 1, 128), (2048, 2049, 64, 1, 1 << 20, 1, 128)),
+                                         ((128, 1, 64, 1, 1, 1 << 26, 16), (512, 1, 64, 1, 1, 1 << 26, 16)),
+                                         ((4, 1, 128, 1, 1, 1, 16), (4, 1, 129, 1, 1, 1, 16)), ((4, 65535, 8, 8, 1, 1, 16), (4, 65536, 8, 8, 1, 1, 16))])
+def test_no_scratch_for_what_is_refused(lib, within, past):
+    assert qsa.prefix_attn_scratch_bytes(*within) > 0
+    assert qsa.prefix_attn_scratch_bytes(*past) == 0
+    nseq, ngroups, heads, nkv, pcols, cols, page = past
+    kv = pages(nkv=nkv, page_size=page, head_stride=128, cell_stride=128 * nkv, page_stride=128 * nkv * page)
+    assert prefix(lib, kv, nseq=nseq, ngroups=ngroups, nheads=heads, pcols=pcols, pstride=pcols, cols=cols, tstride=cols) == UNSUPPORTED
