@@ -87,6 +87,11 @@ float real(PyObject *o) {
     if (v == -1.0 && PyErr_Occurred()) throw PythonError();
     return static_cast<float>(v);
 }
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PythonError();
+    return v != 0;
+}
 int size32(int64_t n, const char *name) {
     if (n > INT_MAX) refuse("%s is too large", name);
     return static_cast<int>(n);
@@ -378,8 +383,8 @@ qsa_rotation rotation_of(PyObject *positions, PyObject *freqs, PyObject *axis, P
         r.naxes = p.dim() == 1 ? 1 : size32(p.size(0), "axes");
         r.position_stride = p.dim() == 1 ? 0 : stride(p, 0);
     }
-    r.interleaved = PyObject_IsTrue(interleaved) > 0;
-    r.inverse = PyObject_IsTrue(inverse) > 0;
+    r.interleaved = truth(interleaved);
+    r.inverse = truth(inverse);
     return r;
 }
 

@@ -1,6 +1,7 @@
 """Rotation by position on the GPU against its formula in 64 bits."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -190,3 +191,19 @@ def test_binding_refusals(dev):
     odd = torch.zeros((4 * 2 * 132,), device=dev, dtype=BF16).as_strided((4, 2, 128), (264, 132, 1))
     with pytest.raises(qsa.QSAError):                      # rows 264 bytes apart
         qsa.rotate(odd, positions, freqs)
+
+
+def test_what_is_neither_true_nor_false(dev):
+    """Its own error, and nothing has been launched."""
+    x, positions, freqs, _ = inputs(dev, 4, 2, BF16)
+    out = torch.full_like(x, 5)
+    for odd in (np.zeros(2), torch.zeros(2)):
+        for name in ("interleaved", "inverse"):
+            with pytest.raises((ValueError, RuntimeError), match="ambiguous"):
+                qsa.rotate(x, positions, freqs, out=out, **{name: odd})
+        k_pages, v_pages = (torch.full((1, 16, 2, 128), 5, device=dev, dtype=BF16) for _ in range(2))
+        with pytest.raises((ValueError, RuntimeError), match="ambiguous"):
+            qsa.cache_append(x, x, k_pages, v_pages, torch.zeros((4, 1), dtype=torch.int32, device=dev),
+                             torch.arange(1, 5, dtype=torch.int32, device=dev), freqs=freqs, interleaved=odd)
+        assert bool((k_pages == 5).all()) and bool((v_pages == 5).all())
+    assert bool((out == 5).all())
