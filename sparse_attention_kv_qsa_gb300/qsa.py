@@ -610,7 +610,8 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, axi
     or ``(2p, 2p + 1)`` where ``interleaved``, by the angle ``position *
     freqs[p]`` (by its negative where ``inverse``: the way back, and the
     gradient). ``positions`` int32 ``[ntok]``, or ``[axes, ntok]`` with the axis
-    of each pair in ``axis`` int32 ``[len(freqs)]`` (time, height, width);
+    of each pair in ``axis`` int32 ``[len(freqs)]`` (time, height, width; without it
+    the first for all);
     ``freqs`` float32, 8, 16, .. 64 of them. ``out`` may be ``x`` itself."""
     r = (_ops_module or _ops()).rotate(x, positions, freqs, axis, interleaved, inverse, out)
     if r.__class__ is int:
