@@ -29,7 +29,9 @@ D = 128
 def generate(texts: int = 2, readers: int = 24, text: int = 900, question: int = 40, steps: int = 60, heads: int = 8,
              nkv: int = 2, page: int = 16, int8: bool = False, seed: int = 0, each_step=None):
     """Returns the last step's outputs ``[texts * readers, heads, 128]``. ``each_step(state)`` is called after every step
-    with what it read and wrote."""
+    with what it read and wrote. The first text has ``text`` tokens, each further one 100 fewer, but one at least."""
+    if min(texts, readers, text, question, steps) < 1:
+        raise ValueError("texts, readers, text, question and steps are 1 at least")
     dev = torch.device("cuda")
     g = torch.Generator(device=dev).manual_seed(seed)
     width, nseq = heads * D, texts * readers
@@ -44,7 +46,7 @@ def generate(texts: int = 2, readers: int = 24, text: int = 900, question: int =
         return torch.tensor(values, dtype=torch.int32, device=dev)
 
     # One pool: pages of the texts, then of the readers.
-    text_lens = [text - 100 * t for t in range(texts)]
+    text_lens = [max(1, text - 100 * t) for t in range(texts)]
     columns, own_columns = -(-text // page), -(-(question + steps) // page)
     npages = texts * columns + nseq * own_columns
     kind = torch.int8 if int8 else torch.bfloat16

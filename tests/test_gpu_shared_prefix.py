@@ -49,3 +49,24 @@ def test_example_agrees_with_plain_attention(int8):
     out = ex.generate(texts=texts, readers=readers, text=300, question=question, steps=25, heads=nkv * group, nkv=nkv, page=page, int8=int8,
                       each_step=each_step)
     assert len(seen) == 25 and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("texts,text", [(4, 150), (3, 1)])
+def test_example_with_more_texts_than_hundreds_of_tokens(texts, text):
+    """Further texts are shorter, down to one token, whose value its readers weigh beside their own cells."""
+    import shared_prefix as ex
+    last = {}
+
+    def each_step(s):
+        last.update(s)
+
+    out = ex.generate(texts=texts, readers=2, text=text, question=3, steps=2, heads=4, nkv=1, each_step=each_step)
+    assert last["text_lens"] == [max(1, text - 100 * t) for t in range(texts)] and min(last["text_lens"]) == 1
+    for i in range(2 * texts):
+        m, n = last["text_lens"][i // 2], 5
+        assert int(last["lens"][i]) == n and int(last["at"][i]) == m + n - 1
+        k, v = (torch.cat((ref.paged_cells(last[x], None, last["text_table"][i // 2], m, 0, 16)[0],
+                           ref.paged_cells(last[x], None, last["own_table"][i], n, 0, 16)[0])) for x in ("k", "v"))
+        o, l, _, size, S = ref.attend(last["turned_q"][i][:, None], k, v, torch.ones((1, m + n), dtype=torch.bool, device=k.device), 128 ** -0.5)
+        bound, _ = ref.bounds(o, l, size, S, m + n, torch.bfloat16, 2.0 ** -8)
+        ref.check(out[i], o[:, 0], bound[:, 0], i)

@@ -2,6 +2,8 @@
 reaches a kernel), and the 64-bit forms that the GPU tests compare with are right where they can be written down by hand."""
 import ctypes
 import math
+import os
+import sys
 
 import pytest
 import torch
@@ -307,3 +309,11 @@ def test_no_scratch_for_what_is_refused(lib, within, past):
     nseq, ngroups, heads, nkv, pcols, cols, page = past
     kv = pages(nkv=nkv, page_size=page, head_stride=128, cell_stride=128 * nkv, page_stride=128 * nkv * page)
     assert prefix(lib, kv, nseq=nseq, ngroups=ngroups, nheads=heads, pcols=pcols, pstride=pcols, cols=cols, tstride=cols) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("bad", [dict(text=0), dict(text=-5), dict(texts=0), dict(readers=0), dict(question=0), dict(steps=0)])
+def test_example_refuses_what_it_cannot_run(bad):
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import shared_prefix as ex
+    with pytest.raises(ValueError, match="at least"):
+        ex.generate(**bad)
