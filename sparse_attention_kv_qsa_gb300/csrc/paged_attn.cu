@@ -190,15 +190,18 @@ __device__ __forceinline__ int tiles_of(const Span &v) {
 }
 
 // A place in the CTA's range of tiles: tile t of unit u of sequence s.
-template <int kTile>
+template <int kTile, bool kAhead>
 struct Cursor {
     int s, u, t, nt;
-    int length;       // of the next sequence, which is on its way while this one is worked on
+    int length;       // kAhead: of the next sequence, which is on its way while this one is worked on
     Span v;
-    __device__ __forceinline__ void look_ahead(const Params &p) { length = s + 1 < p.a.nseq ? ld_in(p.a.lens + s + 1) : 0; }
+    __device__ __forceinline__ void look_ahead(const Params &p) {
+        if constexpr (kAhead) length = s + 1 < p.a.nseq ? ld_in(p.a.lens + s + 1) : 0;
+    }
     __device__ __forceinline__ void enter(const Params &p, int seq) {
         s = seq;
-        v = span_of(p, length);
+        if constexpr (kAhead) v = span_of(p, length);
+        else v = visible(p, s);
         nt = tiles_of<kTile>(v);
         look_ahead(p);
     }
@@ -354,14 +357,16 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) paged_kernel(const __gri
 
     // ---- copies, which run ahead over the units without a stop ----------------------
     const int row = lane & (STEP - 1);             // the row whose address this lane finds
-    Cursor<TILE> at;                               // the step whose page is fetched next
+    // Lengths ahead for the partial form alone: in units of 16 heads, which spill, they cost 4 % (8 x 16,384 cells of 8 KV
+    // heads 102 us, with them 106).
+    Cursor<TILE, kPart> at;                               // the step whose page is fetched next
     at.s = sh_seq[in_cta];
     at.v = sh_span[in_cta];
     at.nt = tiles_of<TILE>(at.v);
     at.u = sh_unit[in_cta];
     at.t = sh_tile[in_cta];
     at.look_ahead(p);
-    Cursor<TILE> here = at;                        // the step that is computed
+    Cursor<TILE, kPart> here = at;                        // the step that is computed
     struct Place {                                 // of this lane's row: the page, and the rest of its address
         int page;
         long long rest, scale_rest;
