@@ -86,10 +86,13 @@ struct Form {
     // numbers they would otherwise reach sooner: 2^(8 + 7) is within its range.
     static constexpr float LIFT = kKv == QSA_BF16 ? 0.0f : 7.0f;
     // Tiles that one sum in tensor memory takes: the tensor cores cut a sum off at every step of 16 cells, always towards
-    // zero, so that its error grows with its length (262,144 cells around 1 in one CTA were 6e-4 too small, with two
-    // halves more). Longer segments are cut and their parts added as rounded fp32 numbers: 8e-5 then, a fraction of a
-    // rounding to 16 bits, and 7e-6 for fp32 results. 65,536 cells in one CTA take 1 % longer so (fp32 queries 8 %).
-    static constexpr int CHAIN = kSplit ? 32 : 256;
+    // zero, so that its error grows with its length. Then it is put aside in scratch, and added there as rounded fp32 numbers.
+    // 16 bits: 262,144 cells around 1 in one sum were 6e-4 too small, in sums of 32,768 8e-5, a fraction of the result's
+    // rounding. fp32 queries (two halves, 16 steps a tile; relative error against 64 bits, the plain form's in 32 bits in
+    // brackets): 512 sequences of 64 heads on 8 behind 4,096 cells 4.3e-6 in sums of 16 tiles, 1.6e-6 of 4, 1.3e-6 of 3,
+    // 1.1e-6 of 2 (1.5e-6); 500 behind 1,000, 4 tiles a sum as it is, 1.3e-6, of 3 1.1e-6 (0.95e-6). 40 sequences behind 3 texts
+    // took 54.8 us with sums of 16 tiles, 59.8 with 4, 60.2 with 3; 60 of 64 heads behind 30,000 148.6, 158.6, 163.9, with 2 172.6.
+    static constexpr int CHAIN = kSplit ? 3 : 256;
 };
 
 struct Params {
@@ -124,7 +127,6 @@ struct Segment {
     int len, t0, t1;            // cells of the prefix; tiles of cells
     int slot;                   // of the partial results, -1: whole
     int row;                    // of them, where whole
-    int behind;                 // whether its sums are added to those of the segment before it
 };
 
 struct alignas(16) Bars {
@@ -397,14 +399,9 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         long long left = range;
         int g = sh_group, kvh = sh_kvh, b = sh_block, t = sh_tile;   // unused without a group
         Group x = sh_at;
-        int uncut = 0;                              // tiles of the block's part that are to follow
-        bool begins = true;                         // the range
-        Segment s = {};
         for (uint32_t k = 0;; ++k) {
-            if (uncut > 0) {
-                s.t0 = s.t1;
-                s.behind = 1;
-            } else if (left > 0) {
+            Segment s = {};
+            if (left > 0) {
                 const int n = static_cast<int>(min(static_cast<long long>(x.tiles - t), left));
                 s.g = g;
                 s.kvh = kvh;
@@ -412,11 +409,9 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 s.count = min(p.block, x.first + x.count - s.first);
                 s.len = x.len;
                 s.t0 = t;
-                s.behind = 0;
-                uncut = n;
+                s.t1 = t + n;
                 const bool whole = n == x.tiles;
-                s.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (begins ? 0 : 1);
-                begins = false;
+                s.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (k == 0 ? 0 : 1);
                 const int block = block_number(p, x, g, b);
                 s.row = whole_row(p, block, s.first);
                 if (t == 0 && lane == 0) {
@@ -444,12 +439,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                         }
                     }
                 }
-            } else {
-                s = {};
             }
-            const int m = min(uncut, F::CHAIN);
-            s.t1 = s.t0 + m;
-            uncut -= m;
             if (!wait_warp(&bars->seg_empty[k % SEGS], ((k / SEGS) & 1) ^ 1)) break;
             if (lane == 0) {
                 bars->seg[k % SEGS] = s;
@@ -707,7 +697,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 if (one) tc_commit(&bars->s_full[i]);
                 odd ^= 1u << i;
             };
-            // Stream i's last weights times the values in a slot.
+            // Stream i's last weights times the values in a slot; `first`: the sums begin with them.
             auto outputs = [&](int i, uint32_t slot, bool first) {
                 const uint32_t p_col = tmem + S_COL + 128 * i, o_col = tmem + O_COL + 128 * i, parity = ~(odd >> i) & 1u;
                 const uint64_t vd = sw128_mnmajor_desc(ring + slot * TILE_BYTES, HALF);
@@ -736,7 +726,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                     if (ok && j < n) ok = landed(ks, kn / STAGES);
 #pragma unroll 1
                     for (int i = 0; ok && i < 2; ++i) {
-                        if (j > 0) ok = outputs(i, vs, j == 1);
+                        if (j > 0) ok = outputs(i, vs, (j - 1) % F::CHAIN == 0);
                         if (ok && i == 1 && j > 0 && one) tc_commit(&bars->kv_empty[vs]);
                         if (ok && j < n) scores(i, base + i * TILE_BYTES, ks);
                     }
@@ -750,7 +740,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                         if (one) tc_commit(&bars->kv_empty[ks]);
                     }
                     if (j > 0) {
-                        ok = landed(vs, vn / STAGES) && outputs((j - 1) & 1, vs, j <= 2);
+                        ok = landed(vs, vn / STAGES) && outputs((j - 1) & 1, vs, ((j - 1) >> 1) % F::CHAIN == 0);
                         if (ok && one) tc_commit(&bars->kv_empty[vs]);
                     }
                 }
@@ -790,7 +780,6 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
         // then there (the first tile took 3 to 5 us without it). It waits for nothing, signals nothing and
         // writes nothing.
         bool dry = !kInt8;   // their loops are longer than the wait for the first cells
-        float2 held = make_float2(-INFINITY, 0.0f);   // reference and weights' sum of the rows so far, where segments are cut
         for (uint32_t k = 0;; k += dry ? 0 : 1, dry = false) {
             if (!wait_warp(&bars->seg_full[k % SEGS], (k / SEGS) & 1)) break;
             const Segment s = bars->seg[k % SEGS];
@@ -854,6 +843,48 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             }
             float m = -INFINITY, l = 0.0f;   // m in base 2, LIFT not counted
             bool any = false, ok = true;
+            // Sums that have had CHAIN tiles are put aside in the place of the CTA's last segment, which no other has, and which has its
+            // own results there from its end on: those of two row tiles in their places there, those of two streams in a half each.
+            float m_aside = -INFINITY;
+            int summed = 0;                  // tiles in the sums in tensor memory
+            bool put = false;                // sums lie aside
+            const uint32_t o_mine = tmem + lanes + O_COL + 128 * i;
+            // The sums in tensor memory and those put aside, added: put aside, or `back` into tensor memory.
+            auto add_aside = [&](bool back) {
+                float4 *aside = p.slots + static_cast<size_t>(2 * blockIdx.x + 1) * (BLOCK * 32);
+                const int at = (two ? i * p.seqs * p.group : i * ROWS) + row;
+                const float f = ex2(m_aside - (m == -INFINITY ? 0.0f : m));
+                const bool add = put && row < rows;
+#pragma unroll 1
+                for (int piece = 0; piece < 4; ++piece) {
+                    float4 was[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        was[e] = add ? ld_in(aside + sums_at(at, 8 * piece + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    uint32_t o[32];
+                    tmem_read32(o_mine + 32 * piece, o);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float y[4] = {was[e].x, was[e].y, was[e].z, was[e].w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) o[4 * e + q] = __float_as_uint(fmaf(y[q], f, __uint_as_float(o[4 * e + q])));
+                    }
+                    if (back) {
+                        tmem_st32(o_mine + 32 * piece, o);
+                    } else if (row < rows) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            aside[sums_at(at, 8 * piece + e)] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                    }
+                }
+                if (back) {
+                    tmem_st_wait();
+                    tc_fence_before_sync();   // the other stream reads them
+                }
+                m_aside = m;
+                put = true;
+            };
             for (int j = 0; j < n; ++j) {
                 if (!two && (j & 1) != i) continue;
                 const uint32_t side = (tiles + j) % SIDES;
@@ -873,6 +904,11 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 if (!dry) ok = wait_warp(&bars->side_full[side], ((tiles + j) / SIDES) & 1);
                 if (!ok) break;
                 tc_fence_after_sync();
+                if (__builtin_expect(summed == F::CHAIN, 0)) {
+                    add_aside(false);
+                    any = false;             // the sums in tensor memory begin again
+                    summed = 0;
+                }
                 // 32 cells at a time, twice: for the largest, and for the weights. The loops stay rolled and read TMEM
                 // twice: straight through, the code of a tile did not stay in the instruction cache (fp32
                 // queries 4.2 us a tile, rolled 2.1; 16-bit cells, held in registers, were no faster).
@@ -934,14 +970,13 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                     if (move) m = top;
                     l *= f;
                     if (any) {
-                        const uint32_t o_at = tmem + lanes + O_COL + 128 * i;
 #pragma unroll 1
                         for (int g = 0; g < 4; ++g) {
                             uint32_t o[32];
-                            tmem_read32(o_at + 32 * g, o);
+                            tmem_read32(o_mine + 32 * g, o);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st32(o_at + 32 * g, o);
+                            tmem_st32(o_mine + 32 * g, o);
                         }
                     }
                 }
@@ -989,6 +1024,7 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                     l += y0 + y1;
                 }
                 any = true;
+                ++summed;
             }
             if (!ok) break;
             if (!dry) tiles += n;
@@ -997,6 +1033,10 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
             float f0 = 1.0f, f1 = 1.0f;
             bool any0 = any, any1 = any;
             if (!dry && !(wait_warp(&bars->o_full[0], k & 1) && wait_warp(&bars->o_full[1], k & 1))) break;
+            if (__builtin_expect(put, 0)) {
+                tc_fence_after_sync();
+                add_aside(true);
+            }
             if (!two) {
                 // Both streams have the same rows: their sums through the second query tile, which nothing reads any more.
                 float4 *shared = reinterpret_cast<float4 *>(raw_smem + (base + TILE_BYTES - smem_u32(raw_smem)));
@@ -1022,41 +1062,6 @@ __global__ void __launch_bounds__(PTHREADS, 1) prefix_kernel(const __grid_consta
                 const size_t from = s.slot < 0 ? static_cast<size_t>(s.kvh) * p.whole_rows : static_cast<size_t>(s.slot) * BLOCK;
                 float4 *to = (s.slot < 0 ? p.whole : p.slots) + from * 32;
                 const int piece0 = two ? 0 : 2 * i, piece1 = two ? 4 : 2 * i + 2;   // with the same rows, half of the columns each
-                if (__builtin_expect(s.behind, 0)) {
-                    // The rows' sums so far, which this thread wrote, are added in tensor memory.
-                    const float top = fmaxf(held.x, sum.x), ref = top == -INFINITY ? 0.0f : top, f = ex2(sum.x - ref), f_held = ex2(held.x - ref);
-                    sum = make_float2(top, fmaf(sum.y, f, held.y * f_held));
-                    f0 = any0 ? f0 * f : 0.0f;
-                    f1 = any1 ? f1 * f : 0.0f;
-#pragma unroll 1
-                    for (int piece = piece0; piece < piece1; ++piece) {
-                        const uint32_t o_at = tmem + lanes + O_COL + (two ? 128 * i : 0) + 32 * piece;
-                        uint32_t o[32];
-                        tmem_read32(o_at, o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(any0 ? __uint_as_float(o[e]) * f0 : 0.0f);
-                        if (!two) {
-                            uint32_t u[32];
-                            tmem_read32(tmem + lanes + O_COL + 128 + 32 * piece, u);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + (any1 ? __uint_as_float(u[e]) * f1 : 0.0f));
-                        }
-                        if (valid)
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 was = ld_in(to + sums_at(at, 8 * piece + e));
-                                const float y[4] = {was.x, was.y, was.z, was.w};
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) o[4 * e + q] = __float_as_uint(fmaf(y[q], f_held, __uint_as_float(o[4 * e + q])));
-                            }
-                        tmem_st32(o_at, o);
-                    }
-                    tmem_st_wait();
-                    f0 = 1.0f;
-                    any0 = true;
-                    any1 = false;
-                }
-                held = sum;
 #pragma unroll 1
                 for (int piece = dry ? 3 : piece0; piece < piece1; ++piece) {
                     uint32_t o[32];
