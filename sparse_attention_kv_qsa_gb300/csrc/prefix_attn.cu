@@ -1291,7 +1291,7 @@ cudaError_t run(Params &p, const Layout &y, const PagedAttnArgs &own_args, cudaS
     if (e == cudaSuccess) e = launch_paged_partial(own_args, p.share, own, stream);
     if (e != cudaSuccess) return e;
     // Ranges of a block, on average.
-    const int ranges = y.grid / (p.a.kv.nkv * std::max(1, std::max(p.a.ngroups, p.a.nseq / p.block))) + 1;
+    const int ranges = static_cast<int>(y.grid / (static_cast<long long>(p.a.kv.nkv) * std::max(1, std::max(p.a.ngroups, p.a.nseq / p.block)))) + 1;
     // As many warps share rows as there are ranges for and the GPU has room for at once.
     const long long units = static_cast<long long>((p.a.nseq * p.group + 7) / 8) * 4;   // of a KV head
     int split = 1;
