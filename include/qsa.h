@@ -556,7 +556,9 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
  * Attention of one new token per sequence where groups of sequences share a
  * long prefix: the result of qsa_paged_attn (without window and mass) over the
  * prefix's cells and then the sequence's own, with the prefix read once for
- * all sequences of its group.
+ * all sequences of its group, and with weights of fewer bits (below). It
+ * pays from some 60,000 to 130,000 prefix cells on, counted for every sequence and KV head
+ * (int8: 150,000 to 270,000); under that qsa_paged_attn over both, in one table, is faster.
  * Group g is sequences cu_seqs[g] .. cu_seqs[g+1]-1; its prefix is the first
  * prefix_lens[g] cells of the pages of row g of prefix_table. Sequence s has
  * lens[s] cells of its own in the pages of row s of page_table (its own token
@@ -577,7 +579,7 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
  * off towards zero at every 16 cells, are over 32,768 cells of a prefix at
  * most (384 for fp32 queries) before they are added to others, rounded. The weights of prefix cells are rounded
  * once to the 16-bit operand type (the pages', binary16 for int8 cells), as in
- * qsa_window_attn; for fp32 queries they keep 22 bits.
+ * qsa_window_attn, where qsa_paged_attn keeps 17 or 22 bits; for fp32 queries they keep 22 bits.
  * Errors and limits as qsa_paged_attn; nheads / nkv above 128, ngroups above 65,535,
  * prefix_cols * page_size above 2^30 or (nseq + ngroups) * nheads *
  * ceil(prefix_cols * page_size / 128) above 2^38 returns QSA_ERR_UNSUPPORTED.

@@ -40,11 +40,11 @@
 // two query tiles the halves.
 //
 // Measured (GB300, in a CUDA graph, all three launches): 32 sequences of 32 heads on 8 KV heads behind 65,536 bfloat16
-// cells 66.5 us, 46 of them streaming at 5.8 TB/s; 64 behind 4,096, up to 1,024 cells of their own, 46.6 us (floor 24.5,
-// mostly own cells); 512 of 16 heads on 2 behind 8,192 binary16 cells 59.4 us: a tile of cells for two row tiles takes
+// cells 65.5 us, 46 of them streaming at 5.8 TB/s; 64 behind 4,096, up to 1,024 cells of their own, 46.2 us (floor 24.5,
+// mostly own cells); 512 of 16 heads on 2 behind 8,192 binary16 cells 59.0 us: a tile of cells for two row tiles takes
 // 1.95 us, the tensor cores 1.1 of that, because a tile's weights (1.4 us), its products and the next scores
-// follow one another. 40 fp32 sequences of 8 heads on 2 behind 3 texts of up to 65,536 int8 cells 53 us, 2 us a
-// tile. 4 behind 600 cells 12.9 us: launches, and code that comes for the first time.
+// follow one another. 40 fp32 sequences of 8 heads on 2 behind 3 texts of up to 65,536 int8 cells 60 us, 2 us a
+// tile and 5 for sums put aside. 4 behind 600 cells 13.3 us: launches, and code that comes for the first time.
 #include <algorithm>
 #include <cfloat>
 #include <cstring>

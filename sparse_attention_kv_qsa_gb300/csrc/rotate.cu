@@ -19,10 +19,11 @@
 // per team, before anything that has to be looked up (the token's sequence by a
 // 32-way search in cu, its length, its page).
 //
-// Measured (GB300): 16,384 tokens of 24 bfloat16 heads on three axes 34.9 us, 5.8 TB/s (0.85 of the
-// measured copy rate); ragged prompts of 20,797 tokens appended, 32 query heads on 8, 100 us, 5.5 TB/s (0.81);
+// Measured (GB300): 16,384 tokens of 24 bfloat16 heads on three axes 35.2 us, 5.7 TB/s (0.84 of the
+// measured copy rate); ragged prompts of 20,797 tokens appended, 32 query heads on 8, 99 us, 5.6 TB/s (0.82);
 // 256 single tokens of 72 rows 5.8 us and one of 48 rows 3.3 us on the device, where the chain sequence - length -
-// page and one barrier are what counts; 4,192 tokens to int8 cells 34 us, three waves of CTAs of the same chain.
+// page and one barrier are what counts, and where a token has more rows than are ahead a second round of loads; 4,192 tokens
+// to int8 cells 33 us, three waves of CTAs of the same chain with four rounds of loads each.
 #include <algorithm>
 #include <cmath>
 #include <cuda_bf16.h>

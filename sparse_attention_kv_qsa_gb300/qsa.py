@@ -547,7 +547,8 @@ def prefix_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, p
     (group ``g``) share a prefix, the first ``prefix_lens[g]`` cells of the
     pages ``prefix_table[g]``, and each has ``lens[s]`` cells of its own in the
     pages ``page_table[s]``: what ``paged_attn`` gives over both, but the prefix
-    is read once for its group. Pages, types and ``scale`` as in
+    is read once for its group, and its weights have the pages' bits. It pays from some 60,000 to 130,000
+    prefix cells on, counted for every sequence and KV head (int8: 150,000 to 270,000). Pages, types and ``scale`` as in
     ``paged_attn``. ``scratch``: a uint8 tensor of
     ``prefix_attn_scratch_bytes`` bytes, allocated when not given."""
     r = (_ops_module or _ops()).prefix_attn(

@@ -317,3 +317,11 @@ def test_example_refuses_what_it_cannot_run(bad):
     import shared_prefix as ex
     with pytest.raises(ValueError, match="at least"):
         ex.generate(**bad)
+
+
+def test_scratch_of_many_groups(lib):
+    """What the GPU's CTAs leave (66 MB at most), 1.1 KB a sequence and head, and 4.2 KB a group and KV head."""
+    n = qsa.prefix_attn_scratch_bytes
+    for heads, nkv in ((8, 1), (8, 8), (32, 8), (128, 1), (64, 4)):
+        for nseq, ngroups in ((1, 1), (512, 1), (512, 64), (512, 512), (4096, 4096)):
+            assert n(nseq, ngroups, heads, nkv, 1 << 20, 1 << 20, 16) <= 66e6 + 1100 * nseq * heads + 4200 * ngroups * nkv
