@@ -542,7 +542,8 @@ qsa_status qsa_rotate(const void *x, qsa_dtype dtype, const int64_t *strides, in
  *           q_out may be q itself, k_out k itself; no other overlaps.
  * The pages' cells (and scales) are apart here: each stride of a dimension of
  * more than one element is past all that the narrower ones span,
- * and keys' do not overlap values'.
+ * and keys' do not overlap values' (without a rotation they may be the same, for
+ * k and v that are the same rows).
  * cu        int32 [nseq + 1], ascending (values are clamped to [0, ntok]), or
  *           NULL: one token per sequence, ntok == nseq.
  * page_table, lens as qsa_paged_attn. Errors and limits as qsa_paged_attn and qsa_rotate.

@@ -173,7 +173,10 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
     if (nheads > 0 && (!aligned(q, 16) || !aligned(q_out, 16) || entangled(q, strides + 4, q_out, strides + 6, dtype, ntok, nheads)))
         return QSA_ERR_INVALID;
     if (k_out != nullptr && (!aligned(k_out, 16) || entangled(k, strides, k_out, strides + 8, dtype, ntok, nkv))) return QSA_ERR_INVALID;
-    if (kv->npages > 0) {
+    // One pool for both holds what it is given where keys and values are the same rows.
+    const bool one_pool = kv->k == kv->v && kv->k_scale_f16 == kv->v_scale_f16 && k == v && rotation == nullptr &&
+                          (ntok == 1 || strides[0] == strides[2]) && (nkv == 1 || strides[1] == strides[3]);
+    if (kv->npages > 0 && !one_pool) {
         Dim both[3] = {{kv->page_stride, kv->npages}, {kv->cell_stride, kv->page_size}, {kv->head_stride, nkv}};
         if (overlap(kv->k, kv->v, both, 3, QSA_D, element_size(kv->dtype))) return QSA_ERR_INVALID;
         Dim scales[3] = {{kv->scale_page_stride, kv->npages}, {kv->scale_cell_stride, kv->page_size}, {kv->scale_head_stride, nkv}};

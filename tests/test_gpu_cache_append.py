@@ -285,3 +285,18 @@ def test_binding_refusals(dev):
     with pytest.raises(qsa.QSAError):                       # pages that are all one page
         qsa.cache_append(b.kx, b.vx, one, one, b.table, b.lens, cu=b.cu)
     assert bool((b.k == 5).all()) and bool((b.v == 5).all())
+
+
+@pytest.mark.parametrize("rows,kv", KINDS)
+def test_one_pool_for_keys_and_values(dev, rows, kv):
+    """Without a rotation the same rows may go to the same pages as keys and as values."""
+    b, one = (Batch(dev, [3, 1, 40], [5, 0, 9], 2, 1, 16, rows, kv) for _ in range(2))
+    qsa.cache_append(b.kx, b.kx, b.k, b.v, b.table, b.lens, cu=b.cu, k_scale_f16=b.ks, v_scale_f16=b.vs)
+    qsa.cache_append(b.kx, b.kx, one.k, one.k, b.table, b.lens, cu=b.cu, k_scale_f16=one.ks, v_scale_f16=one.ks)
+    assert torch.equal(b.k, b.v) and torch.equal(one.k, b.k)
+    if kv == I8:
+        assert torch.equal(one.ks, b.ks) and torch.equal(b.ks, b.vs)
+    with pytest.raises(qsa.QSAError):
+        qsa.cache_append(b.kx, b.vx, one.k, one.k, b.table, b.lens, cu=b.cu, k_scale_f16=one.ks, v_scale_f16=one.ks)
+    with pytest.raises(qsa.QSAError):
+        qsa.cache_append(b.kx, b.kx, one.k, one.k, b.table, b.lens, cu=b.cu, k_scale_f16=one.ks, v_scale_f16=one.ks, freqs=b.freqs)

@@ -192,6 +192,19 @@ def test_keys_cells_over_values_cells(lib, bad):
     assert append(lib, pages(**bad)) == INVALID
 
 
+def test_one_pool_for_keys_and_values(lib):
+    """The same rows to the same cells: refused where they would differ."""
+    plain = dict(rot="none", nheads=0, q=None, q_out=None, k_out=None)
+    int8 = dict(INT8, v=A, k_scale_f16=B, v_scale_f16=B)
+    for kv in (dict(v=A), int8):
+        assert append(lib, pages(**kv), **dict(plain, v=B)) == INVALID
+        assert append(lib, pages(**kv), **dict(plain, strides=strides(2, 512))) == INVALID
+        assert append(lib, pages(**kv)) == INVALID                                              # keys are turned
+        if not torch.cuda.is_available():
+            assert append(lib, pages(**kv), **plain) not in (OK, INVALID)
+    assert append(lib, pages(**dict(int8, v_scale_f16=B + 2)), **plain) == INVALID
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="gets as far as the device, which must not be there")
 @pytest.mark.parametrize("good", [dict(v=A + 2 * 4096, page_stride=8192), dict(k=A + 2 * 4096, v=A, page_stride=8192),
                                   dict(v=A + 256, head_stride=256, cell_stride=512, page_stride=8192), dict(v=A + 2 * 4096 * 100),
