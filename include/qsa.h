@@ -578,7 +578,7 @@ qsa_status qsa_cache_append(const void *k, const void *v, const void *q, qsa_dty
  *           need survive.
  * Sums and softmax statistics are fp32; the tensor cores' sums, which they cut
  * off towards zero at every 16 cells, are over 32,768 cells of a prefix at
- * most (384 for fp32 queries) before they are added to others, rounded. The weights of prefix cells are rounded
+ * most (256 for fp32 queries) before they are added to others, rounded. The weights of prefix cells are rounded
  * once to the 16-bit operand type (the pages', binary16 for int8 cells), as in
  * qsa_window_attn, where qsa_paged_attn keeps 17 or 22 bits; for fp32 queries they keep 22 bits.
  * Errors and limits as qsa_paged_attn; nheads / nkv above 128, ngroups above 65,535,

@@ -43,8 +43,8 @@
 // cells 65.5 us, 46 of them streaming at 5.8 TB/s; 64 behind 4,096, up to 1,024 cells of their own, 46.2 us (floor 24.5,
 // mostly own cells); 512 of 16 heads on 2 behind 8,192 binary16 cells 59.0 us: a tile of cells for two row tiles takes
 // 1.95 us, the tensor cores 1.1 of that, because a tile's weights (1.4 us), its products and the next scores
-// follow one another. 40 fp32 sequences of 8 heads on 2 behind 3 texts of up to 65,536 int8 cells 60 us, 2 us a
-// tile and 5 for sums put aside. 4 behind 600 cells 13.3 us: launches, and code that comes for the first time.
+// follow one another. 40 fp32 sequences of 8 heads on 2 behind 3 texts of up to 65,536 int8 cells 62 us, 2 us a
+// tile and 7 for sums put aside. 4 behind 600 cells 13.3 us: launches, and code that comes for the first time.
 #include <algorithm>
 #include <cfloat>
 #include <cstring>
@@ -90,9 +90,10 @@ struct Form {
     // 16 bits: 262,144 cells around 1 in one sum were 6e-4 too small, in sums of 32,768 8e-5, a fraction of the result's
     // rounding. fp32 queries (two halves, 16 steps a tile; relative error against 64 bits, the plain form's in 32 bits in
     // brackets): 512 sequences of 64 heads on 8 behind 4,096 cells 4.3e-6 in sums of 16 tiles, 1.6e-6 of 4, 1.3e-6 of 3,
-    // 1.1e-6 of 2 (1.5e-6); 500 behind 1,000, 4 tiles a sum as it is, 1.3e-6, of 3 1.1e-6 (0.95e-6). 40 sequences behind 3 texts
-    // took 54.8 us with sums of 16 tiles, 59.8 with 4, 60.2 with 3; 60 of 64 heads behind 30,000 148.6, 158.6, 163.9, with 2 172.6.
-    static constexpr int CHAIN = kSplit ? 3 : 256;
+    // 1.1e-6 of 2 (1.5e-6); 500 behind 1,000 1.3e-6 of 4, 1.1e-6 of 3, 0.92e-6 of 2 (0.95e-6); 2 of 20 heads on 4 behind 26,317
+    // 1.36e-6 of 3, 1.12e-6 of 2 (0.94e-6). 40 sequences behind 3 texts took 54.8 us with sums of 16 tiles, 59.8 with 4, 60.2 with 3
+    // and 62 with 2; 60 of 64 heads behind 30,000 148.6, 158.6, 163.9 and 172.6.
+    static constexpr int CHAIN = kSplit ? 2 : 256;
 };
 
 struct Params {

@@ -439,13 +439,13 @@ def repeated(dev, qt, kv, lens, members, spread, seed):
 @pytest.mark.parametrize("lens,members", [([300, 700, 123, 511, 402], [3, 1, 4, 2, 1]), ([7, 5, 9, 3, 8, 6, 7], [1, 1, 2, 1, 5, 1, 1])])
 def test_long_sums_of_several_blocks(dev, lens, members, kv, qt):
     """Ranges of some 860 tiles a CTA, and of 19 (of a row tile; fp32 queries' blocks are more): of two blocks, mostly, with
-    sums that end in each of them and go on. Sums of at most 256 tiles (3 for fp32 queries), and as many parts as there are."""
+    sums that end in each of them and go on. Sums of at most 256 tiles (2 for fp32 queries), and as many parts as there are."""
     q, out, lse, kd, vd, seen = repeated(dev, qt, kv, lens, members, 4, 5)
     p_half = 2.0 ** -22 if qt == F32 else ref.half_step(BF16 if kv == BF16 else F16)
     s = 0
     for n, m in zip(lens, members):
         o, l, _, size, S = ref.attend(q[s:s + m].reshape(1, -1, 128), kd, vd, seen[None], 128 ** -0.5)
-        chain = 3 if qt == F32 else 256
+        chain = 2 if qt == F32 else 256
         tol, ltol = ref.bounds(o, l, size, S, 128 * chain + 64 * n // chain + 152, qt, p_half)
         tol = tol + 2 * 8192 * 2.0 ** -32 * size.amax(-1, keepdim=True)
         ref.check(out[s:s + m].reshape(1, -1, 128), o, tol, ("out", s))
@@ -456,15 +456,15 @@ def test_long_sums_of_several_blocks(dev, lens, members, kv, qt):
 def test_sums_of_fp32_queries_end_early(dev):
     """A CTA has 64 tiles of one text here, 32 for either stream, and adds up weights that are nearly equal with values around
     1, so that sums grow evenly. Tensor cores cut them off at each of 16 steps a tile, by less than 2^-23 of the sum so far: over
-    the 48 steps of 3 tiles less than 24.5 x 2^-23 of the sum at the end, 25 as growth is not quite even. Putting 11 such sums
-    together, and the streams, rounds by 2^-24 a dozen times, to either side. (Sums of 16 tiles, 256 steps: 128.5 x 2^-23 at most,
+    the 32 steps of 2 tiles less than 16.5 x 2^-23 of the sum at the end, 17 as growth is not quite even. Putting 16 such sums
+    together, and the streams, rounds by 2^-24 some 16 times, to either side. (Sums of 16 tiles, 256 steps: 128.5 x 2^-23 at most,
     and 39 when they were so.)"""
     q, out, _, kd, vd, seen = repeated(dev, F32, I8, [1] * 152, [1] * 152, 0.25, 6)
     off = total = 0.0
     for s in range(0, 152, 19):
         o, _, _, size, _ = ref.attend(q[s:s + 19].reshape(1, -1, 128), kd, vd, seen[None], 128 ** -0.5)
         off, total = off + float((out[s:s + 19].reshape(1, -1, 128).double() - o).sum()), total + float(size.sum())
-    assert abs(off) <= (25 + 6) * 2.0 ** -23 * total, off / total * 2 ** 23
+    assert abs(off) <= (17 + 8) * 2.0 ** -23 * total, off / total * 2 ** 23
 
 
 def test_binding_refusals(dev):
